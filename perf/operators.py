@@ -192,8 +192,8 @@ def _prepare_adamw(c, seed):
             state.update(m_scale=views(s["ms"], d=32), v_scale=views(s["vs"], d=32))
         s["op"] = pkg.AdamW(views(s["p16"], 0, k) + p[k:], masters=p[:k] + [None] * (len(sizes) - k),
                             state_bits=c["bits"], lr=LR, betas=BETAS, eps=ADAM_EPS, weight_decay=s["decay"],
-                            lr_scale=s["share"], seed=SEED, **state)
-        s["grads"] = views(s["g16"], 0, k) + views(s["g32"], k, off=n_wide)
+                            lr_scale=s["share"], seed=SEED, grads=views(s["g16"], 0, k) + views(s["g32"], k, off=n_wide),
+                            **state)
     return s
 
 
@@ -404,9 +404,9 @@ def _own_norm(s):
 def _own_adamw(s):
     op, out, factor = s["op"], {}, None
     if s["case"]["clip"]:
-        out["norm"] = op.grad_norm(s["grads"], MAX_NORM)
+        out["norm"] = op.grad_norm(MAX_NORM)
         factor = out["norm"][1:]
-    op.step(s["grads"], STEP, grad_scale=factor)
+    op.step(STEP, grad_scale=factor)
     return {**out, **{k: s[k] for k in ("p", "p16", "m", "v", "ms", "vs") if k in s}}
 
 
