@@ -438,6 +438,188 @@ rlk_status rlk_attn_out_bias_gemm(const rlk_ja_shape* shape,
                                   const void* b_txt, const void* b_img,
                                   void* y_txt, void* y_img, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * What stands before and after the projections in the block: rows
+ * adaln_modulation (LayerNorm, eps 1e-6, times 1 + scale plus shift) and
+ * adaln_gate_residual (x + gate * sublayer) of the RFC's WS1 table, forward
+ * and backward, each one pass over its activations for both streams.
+ *
+ * Per stream, sample b, token row x of width C (sums over the row):
+ *   hat(x)   layer: (x - mean) * rstd, rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ *            rms:   x * rstd,          rstd = 1 / sqrt(mean(x^2) + eps)
+ *   adaln_modulation:     y = hat(x) * w * (1 + scale_b) + shift_b
+ *   adaln_gate_residual:  r = x + alpha * gate_b * u, rounded to x's type;
+ *            u = h, or with a norm after the sublayer u = hat(h) * w_post;
+ *            y = adaln_modulation of the rounded r (the next sublayer's input)
+ * A row's bytes depend on nothing but the row, its sample's modulation and the
+ * weights. Backward (gradients of sum(y * dy) + sum(r * dr)):
+ *   e = dy * (1 + scale_b) * w;  d = dr + rstd * (e - mean(e) - hat * mean(e * hat))
+ *            (no mean(e) for rms);  dx = d
+ *   dscale_b = w * A_b, dshift_b = S_b, dw = sum_b (1 + scale_b) * A_b with
+ *            A_b = sum_t dy * hat, S_b = sum_t dy
+ *   f = alpha * gate_b * d;  dh = f, or through the norm of h likewise;
+ *   dgate_b = alpha * w_post * G_b, dw_post = alpha * sum_b gate_b * G_b with
+ *            G_b = sum_t d * hat(h) (sum_t d * h without a norm after)
+ * Sums over tokens run in chunks whose length depends on the stream's T alone,
+ * chunks ascending, then b ascending, in fp32 and without atomics: a sample's
+ * gradients do not depend on its batch.
+ *
+ * Every row is processed, padded text rows too. Arithmetic is fp32 with IEEE
+ * division and square root; each output is rounded once. */
+#define RLK_NORM_NONE 0
+#define RLK_NORM_LAYER 1
+#define RLK_NORM_RMS 2
+#define RLK_BF16 0
+#define RLK_FP32 1
+
+/* Limits (otherwise RLK_ERR_INVALID_ARG): 1 <= B <= 65535, T_txt, T_img >= 0
+ * and not both 0, each <= 2^20, B * (T_txt + T_img) < 2^31; C a multiple of 8
+ * up to 8192; eps > 0; alpha finite. x_dtype bf16 with y_dtype fp32 returns
+ * RLK_ERR_UNSUPPORTED. The strides count elements, are at least C and keep
+ * every row 16-byte aligned (otherwise RLK_ERR_ALIGNMENT). */
+typedef struct rlk_adaln_shape {
+    int32_t B, T_txt, T_img, C;
+    int32_t norm;        /* of the modulation: RLK_NORM_LAYER or RLK_NORM_RMS */
+    int32_t post;        /* of h: RLK_NORM_NONE, RLK_NORM_LAYER or RLK_NORM_RMS */
+    int32_t x_dtype;     /* x, r, dr, dx: the residual stream */
+    int32_t y_dtype;     /* y, h, dy, dh: the sublayers' inputs and outputs */
+    int32_t mod_dtype;   /* gate, scale, shift */
+    float eps;           /* of both norms */
+    float alpha;         /* residual scale (1 in the model) */
+    int64_t mod_stride;  /* from sample to sample of gate, scale and shift: 6 * C
+                            for columns of one modulation projection */
+    int64_t dmod_stride; /* the same of dgate, dscale and dshift */
+} rlk_adaln_shape;
+
+/* One stream's buffers (T = its token count). All device memory, 16-byte
+ * aligned, dense but for the modulation's sample stride. */
+typedef struct rlk_adaln_io {
+    const void* x;      /* [B, T, C] */
+    const void* h;      /* [B, T, C], gate_residual only */
+    const void* gate;   /* [B, C] or NULL (1), gate_residual only */
+    const void* scale;  /* [B, C] or NULL (0) */
+    const void* shift;  /* [B, C] or NULL (0) */
+    const float* w;     /* [C] or NULL (1) */
+    const float* w_post; /* [C] or NULL (1), with a norm after the sublayer */
+    void* r;            /* [B, T, C]: written by gate_residual_fwd (may be x),
+                           read by gate_residual_bwd */
+    void* y;            /* [B, T, C], written; gate_residual_fwd takes NULL
+                           (r alone) */
+    float* stats;       /* [B, T, 2]: (mean, rstd) of x, or of r (mean 0 for
+                           rms); forward: written unless NULL; backward: read */
+    float* post_stats;  /* the same of h, with a norm after the sublayer */
+} rlk_adaln_io;
+
+/* One stream's gradients. dy NULL: y was not used (gate_residual only; then
+ * dscale, dshift, dw must be NULL); dr NULL: 0. dy and dr not both NULL. dx
+ * is required and may be dr; dh is required by gate_residual_bwd. The fp32
+ * sums may each be NULL (not wanted). */
+typedef struct rlk_adaln_grad {
+    const void* dy;    /* [B, T, C] */
+    const void* dr;    /* [B, T, C] */
+    void* dx;          /* [B, T, C] */
+    void* dh;          /* [B, T, C] */
+    float* dgate;      /* [B, C], rows dmod_stride apart */
+    float* dscale;     /* [B, C] */
+    float* dshift;     /* [B, C] */
+    float* dw;         /* [C] */
+    float* dw_post;    /* [C] */
+} rlk_adaln_grad;
+
+/* Bytes of the backward calls' workspace (column sums of token chunks); 0
+ * for an invalid shape. Calls that may overlap on the GPU need one each. */
+size_t rlk_adaln_workspace_bytes(const rlk_adaln_shape* shape);
+
+/* A stream's io (and grad) may be NULL only when its T is 0. */
+rlk_status rlk_adaln_modulation_fwd(const rlk_adaln_shape* shape, const rlk_adaln_io* txt, const rlk_adaln_io* img,
+                                    void* stream);
+rlk_status rlk_adaln_modulation_bwd(const rlk_adaln_shape* shape, const rlk_adaln_io* txt, const rlk_adaln_io* img,
+                                    const rlk_adaln_grad* gtxt, const rlk_adaln_grad* gimg, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+rlk_status rlk_adaln_gate_residual_fwd(const rlk_adaln_shape* shape, const rlk_adaln_io* txt,
+                                       const rlk_adaln_io* img, void* stream);
+rlk_status rlk_adaln_gate_residual_bwd(const rlk_adaln_shape* shape, const rlk_adaln_io* txt,
+                                       const rlk_adaln_io* img, const rlk_adaln_grad* gtxt,
+                                       const rlk_adaln_grad* gimg, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The optimiser step that consumes the gradients (the gains', the norm
+ * weights', the projections'): global gradient norm with the clip factor, and
+ * AdamW over a list of tensors, a few launches for the whole list.
+ *
+ * With g' = *grad_scale * g, t = step, rate = lr * lr_scale:
+ *   m = beta1 * m + (1 - beta1) * g';   v = beta2 * v + (1 - beta2) * g'^2
+ *   p -= rate * weight_decay * p
+ *        + rate / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32 with IEEE division and square root; m and v take each product and
+ * sum rounded by itself.
+ *
+ * Parameters: fp32 (p, master NULL), or bf16 with an fp32 master: the master
+ * is updated and p receives its bf16 rounding.
+ * States in 32 bits: fp32 m and v. States in 8 bits: blocks of 32 consecutive
+ * elements hold e4m3 codes and one power-of-two scale (biased exponent byte:
+ * value = code * 2^(scale - 127), the block's largest magnitude's code in
+ * 224 .. 448), all zero at the start. The update of p takes the new m and v
+ * before they are rounded. They are rounded up with the probability of the
+ * remainder: to nearest, a second moment whose step (1 - beta2) is below half
+ * a code would neither grow nor fall. The random bits are a hash of (seed,
+ * step, key, element index modulo 2^32), so a run repeats byte for byte and a
+ * tensor's result does not depend on its place in the list. A positive v keeps
+ * at least the smallest code (1/229376 of the largest in its block), so that
+ * no denominator falls to eps alone. Blocks whose largest magnitude is below
+ * 2^-95 keep that scale and lose what it cannot hold. A block with an infinity or
+ * NaN gets the scale 255, which reads as NaN. */
+typedef struct rlk_adamw_tensor {
+    void* p;               /* [n] fp32, or bf16 when master is given */
+    float* master;         /* [n] or NULL */
+    const void* g;         /* [n], read only */
+    void* m;               /* [n] fp32 or e4m3 */
+    void* v;               /* [n] fp32 or e4m3 */
+    uint8_t* m_scale;      /* [ceil(n / 32)], 8-bit states only */
+    uint8_t* v_scale;      /* [ceil(n / 32)], 8-bit states only */
+    int64_t n;             /* 0 .. 2^40; a tensor of 0 is skipped */
+    double lr_scale;       /* >= 0 */
+    double weight_decay;   /* >= 0 */
+    int32_t g_dtype;       /* RLK_BF16 or RLK_FP32 */
+    int32_t state_bits;    /* 32 or 8 */
+    uint32_t key;          /* of the random bits; distinct per tensor */
+    uint32_t reserved;     /* 0 */
+} rlk_adamw_tensor;
+
+typedef struct rlk_adamw_args {
+    double lr, beta1, beta2, eps;  /* lr >= 0, 0 <= beta < 1, eps > 0 */
+    int64_t step;          /* 1 .. 2^31 - 1: this step's number */
+    const float* lr_dev;   /* device, or NULL: read instead of lr */
+    const int64_t* step_dev; /* device, or NULL: read instead of step (same range),
+                              so that a captured step follows its counter */
+    const float* grad_scale; /* device, or NULL (1). Not finite: every tensor is
+                              left as it was */
+    uint32_t seed;         /* of the 8-bit states' rounding */
+    uint32_t reserved;     /* 0 */
+} rlk_adamw_args;
+
+/* The tensors' buffers must not overlap (a written range that overlaps another
+ * buffer of the list: RLK_ERR_INVALID_ARG). tensors is host memory, read
+ * before return; 0 tensors launch nothing. lr_dev and grad_scale need 4-byte
+ * alignment, step_dev 8, everything else 16. */
+rlk_status rlk_adamw_step(const rlk_adamw_tensor* tensors, int32_t n_tensors, const rlk_adamw_args* args, void* stream);
+
+/* Global L2 norm of the list's gradients (g, n and g_dtype are read, nothing
+ * else) and the factor that clips it:
+ *   out[0] = pre_scale * sqrt(sum g^2)
+ *   out[1] = pre_scale * min(1, max_norm / (out[0] + 1e-6)), NaN if out[0] is
+ *            not finite (AdamW then leaves its tensors as they were)
+ * pre_scale > 0 undoes a loss scale or averages accumulated gradients;
+ * max_norm > 0, or INFINITY for no clipping. Squares are fp32: magnitudes
+ * below 2^-63 vanish, and a norm above 2^63 counts as infinite. Sums run in a
+ * fixed order per tensor, tensors in list order (fp64), without atomics.
+ * workspace: rlk_grad_norm_workspace_bytes() bytes; out: fp32 [2], 4-byte
+ * aligned. */
+size_t rlk_grad_norm_workspace_bytes(const rlk_adamw_tensor* tensors, int32_t n_tensors);
+rlk_status rlk_grad_norm(const rlk_adamw_tensor* tensors, int32_t n_tensors, float pre_scale, float max_norm, float* out,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, then reads and clears the device-side error word
  * that bounded waits in the kernels set when they give up. Returns RLK_OK,
  * RLK_ERR_DEVICE_TIMEOUT, or RLK_ERR_CUDA if the stream reported an error. */
@@ -542,7 +724,8 @@ rlk_status rlk_joint_attn_fwd_shard(const rlk_ja_shape* shape, const void* ctx, 
  * While tracing is on, every entry point that can launch work (the fused
  * forward and backward with concatenated or separate streams, the
  * allocation-free forward, the key-shard and from-context forwards, the
- * QKV and output projections and the standalone operators) appends one
+ * QKV and output projections, the standalone operators, the adaln operators,
+ * the gradient norm and the optimiser step) appends one
  * record when it returns, including calls refused
  * during validation (status != RLK_OK, no kernel listed, actual backend
  * "none"). The kernels listed are the ones the call enqueued, in launch
@@ -569,7 +752,8 @@ typedef struct rlk_op_record {
     char accumulator[16];          /* "fp32" */
     char arithmetic_policy[192];   /* operand/accumulate/cast/transcendental policy */
     char reduction_order[160];
-    int32_t B, H, T_txt, grid_h, grid_w;  /* the call's geometry (0 if the shape was null) */
+    int32_t B, H, T_txt, grid_h, grid_w;  /* the call's geometry (0 if the shape was null; the adaln
+                                             operators: H 0, grid 1 x T_img; the optimiser: all 0) */
 } rlk_op_record;
 
 /* Turns the operator trace on (1) or off (0); either way clears the log. */
@@ -587,7 +771,9 @@ const char* rlk_strerror(int status);
  * 2 attention forward, 3 backward preprocess, 4 dK/dV, 5 dQ,
  * 6 RoPE/RMSNorm backward of the keys (the queries' runs inside dQ),
  * 7 gain-gradient fold, 8 qk_gemm, 9 softmax,
- * 10 av_gemm, 11 forward key shard, 12 qkv_bias_gemm, 13 attn_out_bias_gemm.
+ * 10 av_gemm, 11 forward key shard, 12 qkv_bias_gemm, 13 attn_out_bias_gemm,
+ * 19 adaln forward, 20 adaln backward, 21 its folds, 22 gradient norm, 23 its
+ * fold, 24 AdamW (14 .. 18: the standalone backward operators).
  * rlk_kernel_timing(1) makes later calls record a CUDA event pair around
  * every launch (up to 4096 launches per kernel id); rlk_kernel_timing(0)
  * stops and clears. rlk_kernel_timing_read() waits for the recorded events

@@ -31,6 +31,9 @@ __all__ = [
     "rlk_attn_out_bias_gemm", "rlk_selftest_wait_timeout", "rlk_fwd_tile_schedule", "FWD_TILES",
     "rlk_joint_attn_bwd_stats", "rlk_joint_attn_softmax_bwd", "rlk_joint_attn_av_gemm_bwd",
     "rlk_joint_attn_qk_gemm_bwd", "rlk_qk_norm_rope_bwd",
+    "AdalnShape", "AdalnIo", "AdalnGrad", "rlk_adaln_workspace_bytes", "rlk_adaln_modulation_fwd",
+    "rlk_adaln_modulation_bwd", "rlk_adaln_gate_residual_fwd", "rlk_adaln_gate_residual_bwd", "AdaLN", "NORMS",
+    "AdamwTensor", "AdamwArgs", "rlk_adamw_step", "rlk_grad_norm", "rlk_grad_norm_workspace_bytes", "AdamW",
     "EXPORTED_SYMBOLS", "KERNEL_IDS",
 ]
 
@@ -50,6 +53,7 @@ KERNEL_IDS = {
     "bwd_dkdv": 4, "bwd_dq": 5, "norm_rope_bwd_k": 6, "dg_fold": 7,
     "qk_gemm": 8, "softmax": 9, "av_gemm": 10, "attn_fwd_shard": 11, "qkv_gemm": 12, "out_gemm": 13,
     "dp_gemm": 14, "softmax_bwd": 15, "key_gemm": 16, "query_gemm": 17, "norm_rope_bwd_q": 18,
+    "adaln_fwd": 19, "adaln_bwd": 20, "adaln_fold": 21, "grad_norm": 22, "grad_norm_fold": 23, "adamw": 24,
 }
 # which intermediate rlk_joint_attn_unfused_bytes() sizes
 UNFUSED = {"scores": 0, "p": 1, "alpha": 2, "rows": 3, "dp": 4, "ds": 5, "stats": 6, "dhat": 7, "gain_tiles": 8}
@@ -68,6 +72,9 @@ EXPORTED_SYMBOLS = (
     "rlk_fwd_tile_schedule",
     "rlk_joint_attn_bwd_stats", "rlk_joint_attn_softmax_bwd", "rlk_joint_attn_av_gemm_bwd",
     "rlk_joint_attn_qk_gemm_bwd", "rlk_qk_norm_rope_bwd",
+    "rlk_adaln_workspace_bytes", "rlk_adaln_modulation_fwd", "rlk_adaln_modulation_bwd",
+    "rlk_adaln_gate_residual_fwd", "rlk_adaln_gate_residual_bwd",
+    "rlk_adamw_step", "rlk_grad_norm", "rlk_grad_norm_workspace_bytes",
 )
 OP_TRACE_CAP = 256
 OP_TRACE_MAX_KERNELS = 8
@@ -92,6 +99,49 @@ class Shape(ctypes.Structure):
     @property
     def S(self) -> int:
         return self.T_txt + self.grid_h * self.grid_w
+
+
+NORMS = {"none": 0, "layer": 1, "rms": 2}
+
+
+class AdalnShape(ctypes.Structure):
+    """rlk_adaln_shape."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T_txt", "T_img", "C", "norm", "post", "x_dtype", "y_dtype",
+                                              "mod_dtype")] + \
+               [("eps", ctypes.c_float), ("alpha", ctypes.c_float), ("mod_stride", ctypes.c_int64),
+                ("dmod_stride", ctypes.c_int64)]
+
+    @classmethod
+    def make(cls, B, T_txt, T_img, C, norm="layer", post="none", x_fp32=False, y_fp32=False, mod_fp32=False, eps=1e-6,
+             alpha=1.0, mod_stride=None, dmod_stride=None):
+        return cls(B, T_txt, T_img, C, NORMS[norm], NORMS[post], int(x_fp32), int(y_fp32), int(mod_fp32), eps, alpha,
+                   C if mod_stride is None else mod_stride, C if dmod_stride is None else dmod_stride)
+
+
+class AdalnIo(ctypes.Structure):
+    """rlk_adaln_io: one stream's buffers (device pointers)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "h", "gate", "scale", "shift", "w", "w_post", "r", "y", "stats",
+                                               "post_stats")]
+
+
+class AdalnGrad(ctypes.Structure):
+    """rlk_adaln_grad: one stream's gradients (device pointers)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dy", "dr", "dx", "dh", "dgate", "dscale", "dshift", "dw", "dw_post")]
+
+
+class AdamwTensor(ctypes.Structure):
+    """rlk_adamw_tensor."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("p", "master", "g", "m", "v", "m_scale", "v_scale")] + \
+               [("n", ctypes.c_int64), ("lr_scale", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("g_dtype", ctypes.c_int32), ("state_bits", ctypes.c_int32), ("key", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
+
+
+class AdamwArgs(ctypes.Structure):
+    """rlk_adamw_args."""
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps")] + \
+               [("step", ctypes.c_int64), ("lr_dev", ctypes.c_void_p), ("step_dev", ctypes.c_void_p),
+                ("grad_scale", ctypes.c_void_p), ("seed", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
 
 
 class Trace(ctypes.Structure):
@@ -220,6 +270,20 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     L.rlk_joint_attn_fwd_ctx.restype = i32
     L.rlk_attn_out_bias_gemm.argtypes = [shp] + [vp] * 9
     L.rlk_attn_out_bias_gemm.restype = i32
+    ash, aio, agr = ctypes.POINTER(AdalnShape), ctypes.POINTER(AdalnIo), ctypes.POINTER(AdalnGrad)
+    L.rlk_adaln_workspace_bytes.argtypes = [ash]
+    L.rlk_adaln_workspace_bytes.restype = sz
+    for name in ("modulation", "gate_residual"):
+        fwd, bwd = getattr(L, f"rlk_adaln_{name}_fwd"), getattr(L, f"rlk_adaln_{name}_bwd")
+        fwd.argtypes, fwd.restype = [ash, aio, aio, vp], i32
+        bwd.argtypes, bwd.restype = [ash, aio, aio, agr, agr, vp, sz, vp], i32
+    adt = ctypes.POINTER(AdamwTensor)
+    L.rlk_adamw_step.argtypes = [adt, ctypes.c_int32, ctypes.POINTER(AdamwArgs), vp]
+    L.rlk_adamw_step.restype = i32
+    L.rlk_grad_norm_workspace_bytes.argtypes = [adt, ctypes.c_int32]
+    L.rlk_grad_norm_workspace_bytes.restype = sz
+    L.rlk_grad_norm.argtypes = [adt, ctypes.c_int32, ctypes.c_float, ctypes.c_float, vp, vp, sz, vp]
+    L.rlk_grad_norm.restype = i32
     L.rlk_op_trace_enable.argtypes = [i32]
     L.rlk_op_trace_enable.restype = i32
     L.rlk_op_trace_count.argtypes = []
@@ -446,6 +510,62 @@ def rlk_attn_out_bias_gemm(shape, o, w, b, y, stream=None) -> None:
     rc = lib().rlk_attn_out_bias_gemm(ctypes.byref(shape), _ptr(o[0]), _ptr(o[1]), _ptr(w[0]), _ptr(w[1]),
                                       _ptr(b[0]), _ptr(b[1]), _ptr(y[0]), _ptr(y[1]), _stream_handle(stream))
     _check(rc, "rlk_attn_out_bias_gemm")
+
+
+def rlk_adaln_workspace_bytes(shape: AdalnShape) -> int:
+    return int(lib().rlk_adaln_workspace_bytes(ctypes.byref(shape)))
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def rlk_adaln_modulation_fwd(shape, io, stream=None) -> None:
+    """Enqueue adaln_modulation; io is a (text, image) pair of AdalnIo (None
+    for a stream without tokens)."""
+    _check(lib().rlk_adaln_modulation_fwd(_ref(shape), _ref(io[0]), _ref(io[1]), _stream_handle(stream)),
+           "rlk_adaln_modulation_fwd")
+
+
+def rlk_adaln_gate_residual_fwd(shape, io, stream=None) -> None:
+    """Enqueue adaln_gate_residual with the next adaln_modulation."""
+    _check(lib().rlk_adaln_gate_residual_fwd(_ref(shape), _ref(io[0]), _ref(io[1]), _stream_handle(stream)),
+           "rlk_adaln_gate_residual_fwd")
+
+
+def rlk_adaln_modulation_bwd(shape, io, grad, workspace, workspace_bytes=None, stream=None) -> None:
+    """Enqueue the modulation's backward; io and grad are (text, image) pairs."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().rlk_adaln_modulation_bwd(_ref(shape), _ref(io[0]), _ref(io[1]), _ref(grad[0]), _ref(grad[1]),
+                                          _ptr(workspace), int(workspace_bytes), _stream_handle(stream)),
+           "rlk_adaln_modulation_bwd")
+
+
+def rlk_adaln_gate_residual_bwd(shape, io, grad, workspace, workspace_bytes=None, stream=None) -> None:
+    """Enqueue the gate-residual's backward; io and grad are (text, image) pairs."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().rlk_adaln_gate_residual_bwd(_ref(shape), _ref(io[0]), _ref(io[1]), _ref(grad[0]), _ref(grad[1]),
+                                             _ptr(workspace), int(workspace_bytes), _stream_handle(stream)),
+           "rlk_adaln_gate_residual_bwd")
+
+
+def rlk_adamw_step(tensors, n_tensors, args, stream=None) -> None:
+    """Enqueue one AdamW step over an array of AdamwTensor."""
+    _check(lib().rlk_adamw_step(tensors, int(n_tensors), _ref(args), _stream_handle(stream)), "rlk_adamw_step")
+
+
+def rlk_grad_norm_workspace_bytes(tensors, n_tensors) -> int:
+    return int(lib().rlk_grad_norm_workspace_bytes(tensors, int(n_tensors)))
+
+
+def rlk_grad_norm(tensors, n_tensors, pre_scale, max_norm, out, workspace, workspace_bytes=None, stream=None) -> None:
+    """Enqueue the list's gradient norm and clip factor into out [2]."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().rlk_grad_norm(tensors, int(n_tensors), float(pre_scale), float(max_norm), _ptr(out), _ptr(workspace),
+                               int(workspace_bytes), _stream_handle(stream)), "rlk_grad_norm")
 
 
 def rlk_op_trace_enable(enable: bool) -> None:
@@ -749,3 +869,383 @@ class JointAttention:
         rq = c[o_rq:o_rq + rows * 4].view(torch.float32).view(sh.B, sh.H, sh.S)
         rk = c[o_rk:o_rk + rows * 4].view(torch.float32).view(sh.B, sh.H, sh.S)
         return qh, kh, rq, rk
+
+
+def _require_current(device) -> None:
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"the buffers are on {device}: the library computes on CUDA devices only")
+    if torch.cuda.current_device() != device.index:
+        raise ValueError(f"the current device is cuda:{torch.cuda.current_device()}, the buffers are on {device}")
+
+
+class AdaLN:
+    """Buffers + calls of the block's norms, modulation, gate and residual for
+    one geometry: adaln_modulation before a sublayer's projections,
+    adaln_gate_residual (with the next modulation) after them.
+
+    Activations are (text, image) pairs, [B, T_txt, C] and [B, T_img, C], a
+    pair's text None if T_txt is 0 and its image None if T_img is 0.
+    ``scale``, ``shift`` and ``gate`` are pairs of [B, C] views (columns of the
+    modulation projection's output, all with one sample stride) or None (0, 0
+    and 1). ``w`` and ``w_post`` are pairs of float32 [C] norm weights or None.
+    x, r and their gradients have ``x_dtype``; y, h and theirs ``y_dtype``.
+
+    Every call returns its outputs as a dict of pairs; passing that dict back
+    as ``out`` reuses its buffers."""
+
+    def __init__(self, B: int, T_txt: int, T_img: int, C: int, norm: str = "layer", post: str | None = None,
+                 x_dtype=None, y_dtype=None, mod_dtype=None, eps: float = 1e-6, alpha: float = 1.0, device="cuda"):
+        import torch
+        bf16, f32 = torch.bfloat16, torch.float32
+        self.x_dtype, self.y_dtype, self.mod_dtype = x_dtype or bf16, y_dtype or bf16, mod_dtype or bf16
+        if not {self.x_dtype, self.y_dtype, self.mod_dtype} <= {bf16, f32}:
+            raise ValueError("types are bfloat16 or float32")
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.shape = AdalnShape.make(B, T_txt, T_img, C, norm, post or "none", self.x_dtype == f32, self.y_dtype == f32,
+                                     self.mod_dtype == f32, eps, alpha)
+        self.tokens = (T_txt, T_img)
+        n_ws = rlk_adaln_workspace_bytes(self.shape)
+        if n_ws == 0:
+            raise RlkError(1, "AdaLN: invalid shape")
+        self._ws_bytes = n_ws
+        self.workspace = None  # of the backward, allocated at its first call
+
+    # ---- checks
+    def _bad(self, name, t, want, dtype):
+        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(want)} tensor on {self.device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+
+    def _need(self, name, pair, dtype, tail):
+        """A pair of required dense tensors [B, T, *tail] (None for a stream without tokens)."""
+        if len(pair) != 2:
+            raise ValueError(f"{name} must be a (text, image) pair")
+        for i in (0, 1):
+            T = self.tokens[i]
+            if T == 0:
+                if pair[i] is not None:
+                    raise ValueError(f"{name}[{i}] must be None: the stream has no tokens")
+                continue
+            t = pair[i]
+            if t is None:
+                raise ValueError(f"{name}[{i}] is missing")
+            if t.dtype != dtype or t.shape != (self.shape.B, T, tail) or not t.is_contiguous() or \
+                    t.device != self.device:
+                self._bad(f"{name}[{i}]", t, (self.shape.B, T, tail), dtype)
+        return pair
+
+    def _weights(self, name, pair):
+        import torch
+        if pair is None:
+            return (None, None)
+        for i in (0, 1):
+            t = pair[i]
+            if t is not None and (t.dtype != torch.float32 or t.shape != (self.shape.C,) or not t.is_contiguous()
+                                  or t.device != self.device):
+                self._bad(f"{name}[{i}]", t, (self.shape.C,), torch.float32)
+        return pair
+
+    def _mods(self, *named):
+        """Pairs of [B, C] views with one sample stride (set in the shape)."""
+        sh, stride, got = self.shape, None, []
+        for name, pair in named:
+            pair = (None, None) if pair is None else pair
+            for i in (0, 1):
+                t = pair[i]
+                if t is None:
+                    continue
+                if t.dtype != self.mod_dtype or t.shape != (sh.B, sh.C) or t.stride(1) != 1 or t.device != self.device:
+                    raise ValueError(f"{name}[{i}] must be a {self.mod_dtype} [{sh.B}, {sh.C}] view with unit column "
+                                     f"stride on {self.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+                if sh.B > 1:
+                    if stride is not None and t.stride(0) != stride:
+                        raise ValueError(f"scale, shift and gate must have one sample stride: got {stride} and "
+                                         f"{t.stride(0)} ({name}[{i}])")
+                    stride = t.stride(0)
+            got.append(pair)
+        sh.mod_stride = sh.C if stride is None else stride
+        return got
+
+    def _alloc(self, pair_like, dtype=None, tail=None):
+        import torch
+        res = []
+        for i in (0, 1):
+            T = self.tokens[i]
+            if T == 0:
+                res.append(None)
+            elif tail is not None:
+                res.append(torch.empty((self.shape.B, T, tail), dtype=dtype, device=self.device))
+            else:
+                res.append(torch.empty(pair_like, dtype=dtype, device=self.device))
+        return tuple(res)
+
+    def _outputs(self, out, want):
+        """The outputs `want` = {name: (shape or None for [B, T, tail], dtype, tail)}, new or taken from `out`."""
+        if out is None:
+            return {k: self._alloc(s, d, t) for k, (s, d, t) in want.items()}
+        if out.keys() != want.keys():
+            raise ValueError(f"out must hold {sorted(want)}, got {sorted(out)}")
+        for k, (s, d, t) in want.items():
+            if t is not None:
+                self._need(f"out[{k!r}]", out[k], d, t)
+                continue
+            for i in (0, 1):
+                v = out[k][i]
+                if self.tokens[i] and (v is None or v.dtype != d or v.shape != s or not v.is_contiguous()
+                                       or v.device != self.device):
+                    raise ValueError(f"out[{k!r}][{i}] must be a contiguous {d} {tuple(s)} tensor on {self.device}")
+        return out
+
+    def _fill(self, cls, **pairs):
+        """One struct of pointers per stream (None for a stream without tokens)."""
+        res = []
+        for i in (0, 1):
+            if self.tokens[i] == 0:
+                res.append(None)
+                continue
+            res.append(cls(**{k: v[i].data_ptr() for k, v in pairs.items() if v[i] is not None}))
+        return res
+
+    def _on_device(self):
+        """The library launches on the current device: it must be the tensors' one."""
+        _require_current(self.device)
+
+    def _workspace(self):
+        import torch
+        if self.workspace is None:
+            self.workspace = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
+        return self.workspace
+
+    # ---- calls
+    def modulation(self, x, scale, shift, w=None, out=None, stream=None):
+        """y = hat(x) * w * (1 + scale) + shift. Returns y and stats."""
+        import torch
+        self._need("x", x, self.x_dtype, self.shape.C)
+        scale, shift = self._mods(("scale", scale), ("shift", shift))
+        w = self._weights("w", w)
+        out = self._outputs(out, {"y": (None, self.y_dtype, self.shape.C), "stats": (None, torch.float32, 2)})
+        self._on_device()
+        rlk_adaln_modulation_fwd(self.shape, self._fill(AdalnIo, x=x, scale=scale, shift=shift, w=w, y=out["y"],
+                                                        stats=out["stats"]), stream)
+        return out
+
+    def gate_residual(self, x, h, gate, scale, shift, w=None, w_post=None, want_y=True, out=None, stream=None):
+        """r = x + alpha * gate * u (u = h, or hat(h) * w_post with a norm
+        after the sublayer), y = modulation of r. Returns r, and with want_y y
+        and stats, and with a norm after the sublayer post_stats. ``out`` may
+        hold x itself as r."""
+        import torch
+        sh, post = self.shape, self.shape.post != 0
+        self._need("x", x, self.x_dtype, sh.C)
+        self._need("h", h, self.y_dtype, sh.C)
+        gate, scale, shift = self._mods(("gate", gate), ("scale", scale), ("shift", shift))
+        w, w_post = self._weights("w", w), self._weights("w_post", w_post)
+        want = {"r": (None, self.x_dtype, sh.C)}
+        if want_y:
+            want.update(y=(None, self.y_dtype, sh.C), stats=(None, torch.float32, 2))
+        if post:
+            want["post_stats"] = (None, torch.float32, 2)
+        out = self._outputs(out, want)
+        self._on_device()
+        rlk_adaln_gate_residual_fwd(sh, self._fill(AdalnIo, x=x, h=h, gate=gate, scale=scale, shift=shift, w=w,
+                                                   w_post=w_post, **out), stream)
+        return out
+
+    def modulation_bwd(self, x, scale, stats, dy, dr=None, w=None, out=None, stream=None):
+        """Gradients of the modulation: dx (with dr, the gradient that reaches
+        x by the residual path, added), dscale and dshift [B, C] and, with w,
+        dw [C], all sums float32. ``out`` may hold dr itself as dx."""
+        import torch
+        sh, f32 = self.shape, torch.float32
+        self._need("x", x, self.x_dtype, sh.C)
+        self._need("stats", stats, f32, 2)
+        self._need("dy", dy, self.y_dtype, sh.C)
+        dr = (None, None) if dr is None else self._need("dr", dr, self.x_dtype, sh.C)
+        (scale,) = self._mods(("scale", scale))
+        w = self._weights("w", w)
+        want = {"dx": (None, self.x_dtype, sh.C), "dscale": ((sh.B, sh.C), f32, None), "dshift": ((sh.B, sh.C), f32, None)}
+        if w[0] is not None or w[1] is not None:
+            want["dw"] = ((sh.C,), f32, None)
+        out = self._outputs(out, want)
+        self._on_device()
+        rlk_adaln_modulation_bwd(sh, self._fill(AdalnIo, x=x, scale=scale, w=w, stats=stats),
+                                 self._fill(AdalnGrad, dy=dy, dr=dr, **out), self._workspace(), self._ws_bytes, stream)
+        return out
+
+    def gate_residual_bwd(self, r, h, gate, scale, stats, dy, dr=None, w=None, w_post=None, post_stats=None, out=None,
+                          stream=None):
+        """Gradients of gate_residual from r and the statistics it left: dx,
+        dh, dgate, with dy (None: y was not used) dscale and dshift, with w
+        dw, with w_post dw_post. dr is the gradient that reaches r by the
+        residual path. ``out`` may hold dr itself as dx."""
+        import torch
+        sh, f32 = self.shape, torch.float32
+        self._need("r", r, self.x_dtype, sh.C)
+        self._need("h", h, self.y_dtype, sh.C)
+        if dy is None and dr is None:
+            raise ValueError("dy and dr cannot both be None")
+        dr = (None, None) if dr is None else self._need("dr", dr, self.x_dtype, sh.C)
+        gate, scale = self._mods(("gate", gate), ("scale", scale))
+        w, w_post = self._weights("w", w), self._weights("w_post", w_post)
+        want = {"dx": (None, self.x_dtype, sh.C), "dh": (None, self.y_dtype, sh.C), "dgate": ((sh.B, sh.C), f32, None)}
+        if dy is not None:
+            self._need("dy", dy, self.y_dtype, sh.C)
+            self._need("stats", stats, f32, 2)
+            want.update(dscale=((sh.B, sh.C), f32, None), dshift=((sh.B, sh.C), f32, None))
+            if w[0] is not None or w[1] is not None:
+                want["dw"] = ((sh.C,), f32, None)
+        else:
+            dy = stats = (None, None)
+        if sh.post:
+            self._need("post_stats", post_stats, f32, 2)
+            if w_post[0] is not None or w_post[1] is not None:
+                want["dw_post"] = ((sh.C,), f32, None)
+        else:
+            post_stats = (None, None)
+        out = self._outputs(out, want)
+        self._on_device()
+        rlk_adaln_gate_residual_bwd(sh, self._fill(AdalnIo, r=r, h=h, gate=gate, scale=scale, w=w, w_post=w_post,
+                                                   stats=stats, post_stats=post_stats),
+                                    self._fill(AdalnGrad, dy=dy, dr=dr, **out), self._workspace(), self._ws_bytes, stream)
+        return out
+
+
+class AdamW:
+    """AdamW over a list of parameters (see rlk_adamw_step in the header).
+
+    ``params`` are contiguous CUDA tensors, float32, or bfloat16 with a float32
+    master copy (taken from ``masters``, or made from the parameter). States
+    are zero unless given: ``m`` and ``v`` float32 (state_bits 32) or
+    float8_e4m3fn with uint8 ``m_scale`` and ``v_scale`` per 32 elements
+    (state_bits 8). ``weight_decay`` and ``lr_scale`` are one number or one per
+    parameter. ``keys`` (default 0, 1, ...) name the parameters to the 8-bit
+    states' rounding. ``grads``, bfloat16 or float32, may be held here (buffers
+    that a backward pass writes anew for every step) or given to each call."""
+
+    def __init__(self, params, masters=None, state_bits: int = 32, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay=0.01, lr_scale=1.0, seed: int = 0, keys=None, grads=None, m=None, v=None, m_scale=None,
+                 v_scale=None):
+        import torch
+        f32, bf16 = torch.float32, torch.bfloat16
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        n = len(params)
+        if n == 0:
+            raise ValueError("no parameters given")
+        self.params, self.state_bits = list(params), state_bits
+        self.lr, self.betas, self.eps, self.seed = float(lr), betas, float(eps), int(seed)
+        self.device = self.params[0].device
+        each = lambda x: list(x) if isinstance(x, (list, tuple)) else [x] * n  # noqa: E731
+        decay, share, keys = each(weight_decay), each(lr_scale), list(range(n)) if keys is None else list(keys)
+        masters = [None] * n if masters is None else list(masters)
+        code = torch.float8_e4m3fn if state_bits == 8 else f32
+        blocks = [-(-p.numel() // 32) for p in self.params]
+
+        def states(given, dtype, sizes):
+            if given is None:
+                return [torch.zeros(k, dtype=dtype, device=self.device) for k in sizes]
+            return list(given)
+        sizes = [p.numel() for p in self.params]
+        self.m, self.v = states(m, code, sizes), states(v, code, sizes)
+        self.m_scale = states(m_scale, torch.uint8, blocks) if state_bits == 8 else [None] * n
+        self.v_scale = states(v_scale, torch.uint8, blocks) if state_bits == 8 else [None] * n
+        if not len(decay) == len(share) == len(keys) == len(masters) == len(self.m) == len(self.v) == len(self.m_scale) \
+                == len(self.v_scale) == n:
+            raise ValueError(f"expected one entry for each of the {n} parameters")
+        self.masters = []
+        self._list = (AdamwTensor * n)()
+        for i, p in enumerate(self.params):
+            if p.dtype not in (f32, bf16):
+                raise ValueError(f"parameter {i} must be float32 or bfloat16, got {p.dtype}")
+            if p.dtype == f32 and masters[i] is not None:
+                raise ValueError(f"parameter {i} is float32 and takes no master")
+            if p.dtype == bf16 and masters[i] is None:
+                masters[i] = p.detach().float().contiguous()
+            self.masters.append(masters[i])
+            for name, t, dtype, k in (("parameter", p, p.dtype, sizes[i]), ("master", masters[i], f32, sizes[i]),
+                                      ("m", self.m[i], code, sizes[i]), ("v", self.v[i], code, sizes[i]),
+                                      ("m_scale", self.m_scale[i], torch.uint8, blocks[i]),
+                                      ("v_scale", self.v_scale[i], torch.uint8, blocks[i])):
+                if t is not None:
+                    self._dense(f"{name} {i}", t, (dtype,), k)
+            e = self._list[i]
+            e.p, e.master, e.m, e.v = _ptr(p), _ptr(masters[i]), _ptr(self.m[i]), _ptr(self.v[i])
+            e.m_scale, e.v_scale, e.n = _ptr(self.m_scale[i]), _ptr(self.v_scale[i]), sizes[i]
+            e.lr_scale, e.weight_decay, e.state_bits, e.key = float(share[i]), float(decay[i]), state_bits, int(keys[i])
+        self.grads = None
+        if grads is not None:
+            self._take(grads)
+        self._args = AdamwArgs(lr=self.lr, beta1=float(betas[0]), beta2=float(betas[1]), eps=self.eps, seed=self.seed)
+        self.workspace = None  # of grad_norm, allocated at its first call
+
+    def _dense(self, name, t, dtypes, n):
+        if t.dtype not in dtypes or t.numel() != n or not t.is_contiguous() or t.device != self.device:
+            raise ValueError(f"{name} must be a contiguous tensor of {n} elements ({dtypes}) on {self.device}, got "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+    def _take(self, grads):
+        """The list's gradient buffers from now on."""
+        import torch
+        grads = list(grads)
+        if len(grads) != len(self.params):
+            raise ValueError(f"expected {len(self.params)} gradients, got {len(grads)}")
+        for i, (g, p) in enumerate(zip(grads, self.params)):
+            self._dense(f"gradient {i}", g, (torch.float32, torch.bfloat16), p.numel())
+        for e, g in zip(self._list, grads):
+            e.g, e.g_dtype = g.data_ptr(), int(g.dtype == torch.float32)
+        self.grads = grads
+
+    def _ready(self, grads):
+        if grads is not None:
+            self._take(grads)
+        if self.grads is None:
+            raise ValueError("no gradients given")
+        _require_current(self.device)
+
+    def _scalar(self, name, t, dtype):
+        if t is None:
+            return None
+        if t.dtype != dtype or t.numel() != 1 or t.device != self.device:
+            raise ValueError(f"{name} must be one {dtype} value on {self.device}")
+        return t.data_ptr()
+
+    def grad_norm(self, max_norm: float = float("inf"), pre_scale: float = 1.0, grads=None, out=None, stream=None):
+        """float32 [2] on the device: the gradients' global norm (times
+        pre_scale) and the factor (pre_scale included) that clips it to
+        max_norm, NaN if the norm is not finite."""
+        import torch
+        self._ready(grads)
+        n = len(self.params)
+        if out is None:
+            out = torch.empty(2, dtype=torch.float32, device=self.device)
+        else:
+            self._dense("out", out, (torch.float32,), 2)
+        if self.workspace is None:
+            self.workspace = torch.empty(rlk_grad_norm_workspace_bytes(self._list, n), dtype=torch.uint8,
+                                         device=self.device)
+        rlk_grad_norm(self._list, n, pre_scale, max_norm, out, self.workspace, stream=stream)
+        return out
+
+    def step(self, step, lr=None, grad_scale=None, grads=None, stream=None):
+        """One update, in place. ``step`` is this step's number from 1 on, and
+        ``lr`` the rate if not the constructor's; each an ordinary number, or a
+        device tensor of one value (int64, float32) that is read when the
+        kernels run, as a captured step needs. ``grad_scale`` is one float32
+        value on the device, such as grad_norm(...)[1:]; if it is not finite
+        nothing is changed."""
+        import torch
+        self._ready(grads)
+        a = self._args
+        a.step_dev = a.lr_dev = None
+        if isinstance(step, torch.Tensor):
+            a.step_dev, a.step = self._scalar("step", step, torch.int64), 1
+        else:
+            a.step = int(step)
+        if isinstance(lr, torch.Tensor):
+            a.lr_dev, a.lr = self._scalar("lr", lr, torch.float32), 0.0
+        else:
+            a.lr = self.lr if lr is None else float(lr)
+        a.grad_scale = self._scalar("grad_scale", grad_scale, torch.float32)
+        rlk_adamw_step(self._list, len(self.params), a, stream)

@@ -11,8 +11,10 @@
 #include <cstdio>
 #include <cstring>
 #include <initializer_list>
-#include <utility>
+#include <memory>
 #include <mutex>
+#include <new>
+#include <utility>
 #include <vector>
 
 #include "rlk_device.cuh"
@@ -133,8 +135,8 @@ std::mutex g_dev_mu;
 int g_dev_state[kMaxDevices];  // 0 unknown, 1 ok, 2 wrong arch, 3 fast math, 4 cuda error
 
 int strict_all_units() {
-    const int r[7] = {probe_host_tu(), probe_prologue_tu(), probe_fwd_tu(), probe_bwd_tu(), probe_unfused_tu(),
-                      probe_qkv_tu(), probe_unfused_bwd_tu()};
+    const int r[9] = {probe_host_tu(), probe_prologue_tu(), probe_fwd_tu(), probe_bwd_tu(), probe_unfused_tu(),
+                      probe_qkv_tu(), probe_unfused_bwd_tu(), probe_adaln_tu(), probe_adamw_tu()};
     for (int v : r)
         if (v < 0) return -1;
     for (int v : r)
@@ -271,6 +273,12 @@ constexpr const char* kFwdPolicy =
 constexpr const char* kFwdOrder =
     "key tiles of 128: text tiles with a valid key, then image tiles, ascending; row sums: 8 partials "
     "by column mod 8, fixed tree";
+constexpr const char* kAdalnPolicy =
+    "fp32 math on bf16 or fp32 rows, variance about the row's mean, IEEE sqrt and division, one rounding per output; "
+    "the norm reads the rounded residual";
+constexpr const char* kAdalnRowOrder = "row sums: 8 columns per thread, xor 16..1, warps ascending";
+constexpr const char* kAdalnSumOrder =
+    "row sums as in the forward; column sums: token chunks (by T), their runs in order, then b ascending";
 const OpInfo kOps[] = {
     {"qk_rmsnorm+multi_axis_rope+joint_attention_fused", "rlk_joint_attn_fwd", kFwdPolicy, kFwdOrder},
     {"joint_attention_fused backward", "rlk_joint_attn_bwd",
@@ -323,13 +331,24 @@ const OpInfo kOps[] = {
      "fp32 inverse rotation and RMSNorm backward, one bf16 cast of dQ dK",
      "row dot products: 4 products per lane then xor 16..1; gain partials per 32-row quarter, then tiles, h, b "
      "ascending"},
+    {"adaln_modulation", "rlk_adaln_modulation_fwd", kAdalnPolicy, kAdalnRowOrder},
+    {"adaln_modulation backward", "rlk_adaln_modulation_bwd", kAdalnPolicy, kAdalnSumOrder},
+    {"adaln_gate_residual+adaln_modulation", "rlk_adaln_gate_residual_fwd", kAdalnPolicy, kAdalnRowOrder},
+    {"adaln_gate_residual+adaln_modulation backward", "rlk_adaln_gate_residual_bwd", kAdalnPolicy, kAdalnSumOrder},
+    {"adamw", "rlk_adamw_step",
+     "fp32 update, moments rounded product by product, IEEE div/sqrt; 8-bit moments: e4m3 times 2^k per 32 elements, "
+     "stochastic rounding by a counter hash; p from the unrounded moments",
+     "elementwise"},
+    {"gradient norm and clip factor", "rlk_grad_norm", "fp32 squares, fp64 sum of the chunks, IEEE div/sqrt",
+     "chunks of a tensor: a thread's squares in order, xor 16..1, warps ascending; chunks in a fixed tree"},
 };
 const char* const kKernelNames[kNumKernelIds] = {
     "rope_table_kernel", "prologue_kernel", "attn_fwd_tc_kernel", "bwd_pre_kernel",
     "attn_bwd_dkdv_tc_kernel", "attn_bwd_dq_tc_kernel", "norm_rope_bwd_k_kernel", "dg_fold_kernels",
     "qk_gemm_kernel", "softmax_kernel", "av_gemm_kernel", "attn_fwd_tc_kernel<shard>", "qkv_gemm_kernel",
     "qkv_gemm_kernel<out_proj>", "qk_gemm_kernel<dp>", "softmax_bwd_kernel", "acc_gemm_kernel<key>",
-    "acc_gemm_kernel<query>", "norm_rope_bwd_q_kernel"};
+    "acc_gemm_kernel<query>", "norm_rope_bwd_q_kernel", "adaln_fwd_kernel", "adaln_bwd_kernel", "adaln_fold_kernel",
+    "grad_norm_kernel", "grad_norm_fold_kernel", "adamw_kernel"};
 
 struct OpLog {
     std::mutex mu;
@@ -1067,6 +1086,301 @@ rlk_status rlk_joint_attn_fwd_shard(const rlk_ja_shape* shape, const void* ctx, 
     OpScope sc(kOpFwdShard, shape);
     return sc.finish(rlk_joint_attn_fwd_shard_impl(shape, ctx, v, txt_valid_len, blk_begin, blk_end, state_in,
                                                    state_out, out, lse, stream));
+}
+
+// ---- adaln_modulation, adaln_gate_residual ----
+static bool adaln_shape_ok(const rlk_adaln_shape* sh, rlk_status* why) {
+    *why = RLK_ERR_INVALID_ARG;
+    if (sh == nullptr) return false;
+    auto known = [](int32_t dtype) { return dtype == RLK_BF16 || dtype == RLK_FP32; };
+    if (sh->B < 1 || sh->B > 65535 || sh->T_txt < 0 || sh->T_img < 0 || sh->T_txt > kMaxTokens ||
+        sh->T_img > kMaxTokens || sh->T_txt + sh->T_img == 0 ||
+        (long long)sh->B * ((long long)sh->T_txt + sh->T_img) >= (1LL << 31) || sh->C < 8 || sh->C > 8192 ||
+        sh->C % 8 != 0 || (sh->norm != RLK_NORM_LAYER && sh->norm != RLK_NORM_RMS) || sh->post < RLK_NORM_NONE ||
+        sh->post > RLK_NORM_RMS || !known(sh->x_dtype) || !known(sh->y_dtype) || !known(sh->mod_dtype) ||
+        !(sh->eps > 0.0f) || !std::isfinite(sh->eps) || !std::isfinite(sh->alpha) || sh->mod_stride < sh->C ||
+        sh->dmod_stride < sh->C)
+        return false;
+    if (sh->x_dtype == RLK_BF16 && sh->y_dtype == RLK_FP32) {
+        *why = RLK_ERR_UNSUPPORTED;
+        return false;
+    }
+    if (sh->mod_stride % (sh->mod_dtype == RLK_FP32 ? 4 : 8) != 0 || sh->dmod_stride % 4 != 0) {
+        *why = RLK_ERR_ALIGNMENT;
+        return false;
+    }
+    return true;
+}
+
+static AdalnArgs adaln_args(const rlk_adaln_shape* sh) {
+    AdalnArgs a{};
+    a.mod_stride = sh->mod_stride;
+    a.dmod_stride = sh->dmod_stride;
+    a.B = sh->B;
+    a.C = sh->C;
+    a.norm = sh->norm;
+    a.post = sh->post;
+    a.x_fp32 = sh->x_dtype == RLK_FP32;
+    a.y_fp32 = sh->y_dtype == RLK_FP32;
+    a.mod_fp32 = sh->mod_dtype == RLK_FP32;
+    a.eps = sh->eps;
+    a.alpha = sh->alpha;
+    for (int i = 0; i < 2; ++i) {
+        AdalnStream& s = a.s[i];
+        s.T = i == 0 ? sh->T_txt : sh->T_img;
+        s.chunk_rows = adaln_chunk_rows(s.T);
+        s.chunks = (s.T + s.chunk_rows - 1) / s.chunk_rows;
+    }
+    return a;
+}
+
+static size_t adaln_workspace(const AdalnArgs& a) {
+    return (size_t)a.B * ((size_t)a.s[0].chunks + a.s[1].chunks) * 3 * a.C * sizeof(float);
+}
+
+// Null and alignment checks of one call; fills the streams of a.
+static rlk_status adaln_fill(AdalnArgs* a, bool gate, bool bwd, const rlk_adaln_io* const io[2],
+                             const rlk_adaln_grad* const gr[2]) {
+    const bool post = gate && a->post != RLK_NORM_NONE;
+    for (int i = 0; i < 2; ++i) {
+        AdalnStream& s = a->s[i];
+        if (s.T == 0) continue;
+        if (io[i] == nullptr || (bwd && gr[i] == nullptr)) return RLK_ERR_INVALID_ARG;
+        const rlk_adaln_io& d = *io[i];
+        rlk_status st;
+        s.scale = d.scale;
+        s.w = d.w;
+        if (gate) {
+            if (a->post == RLK_NORM_NONE && d.w_post != nullptr) return RLK_ERR_INVALID_ARG;
+            s.h = d.h;
+            s.gate = d.gate;
+            s.w_post = d.w_post;
+            if (post) s.post_stats = d.post_stats;
+        }
+        if (!bwd) {
+            s.x = d.x;
+            s.shift = d.shift;
+            s.y = d.y;
+            s.stats = d.stats;
+            if (gate) s.r = d.r;
+            st = gate ? check_ptrs({s.x, s.h, s.r}, {s.y, s.gate, s.scale, s.shift, s.w, s.w_post, s.stats, s.post_stats})
+                      : check_ptrs({s.x, s.y}, {s.scale, s.shift, s.w, s.stats});
+            if (st != RLK_OK) return st;
+            continue;
+        }
+        const rlk_adaln_grad& q = *gr[i];
+        s.x = gate ? d.r : d.x;
+        s.stats = d.stats;
+        s.dy = q.dy;
+        s.dr = q.dr;
+        s.dx = q.dx;
+        s.dscale = q.dscale;
+        s.dshift = q.dshift;
+        s.dw = q.dw;
+        if (gate) {
+            s.dh = q.dh;
+            s.dgate = q.dgate;
+            s.dw_post = q.dw_post;
+        }
+        if (s.dy == nullptr && (!gate || s.dr == nullptr || s.dscale != nullptr || s.dshift != nullptr || s.dw != nullptr))
+            return RLK_ERR_INVALID_ARG;
+        if (s.dw_post != nullptr && !post) return RLK_ERR_INVALID_ARG;
+        if ((s.dy != nullptr && s.stats == nullptr) || (post && s.post_stats == nullptr)) return RLK_ERR_INVALID_ARG;
+        st = gate ? check_ptrs({s.x, s.h, s.dx, s.dh}, {}) : check_ptrs({s.x, s.dx}, {});
+        if (st == RLK_OK)
+            st = check_ptrs({}, {s.dy, s.dr, s.gate, s.scale, s.w, s.w_post, s.stats, s.post_stats, s.dgate, s.dscale,
+                                 s.dshift, s.dw, s.dw_post});
+        if (st != RLK_OK) return st;
+    }
+    return RLK_OK;
+}
+
+static rlk_status adaln_call(const rlk_adaln_shape* shape, bool gate, bool bwd, const rlk_adaln_io* txt,
+                             const rlk_adaln_io* img, const rlk_adaln_grad* gtxt, const rlk_adaln_grad* gimg,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+    rlk_status st = RLK_OK;
+    if (!adaln_shape_ok(shape, &st)) return st;
+    AdalnArgs a = adaln_args(shape);
+    const rlk_adaln_io* const io[2] = {txt, img};
+    const rlk_adaln_grad* const gr[2] = {gtxt, gimg};
+    st = adaln_fill(&a, gate, bwd, io, gr);
+    if (st != RLK_OK) return st;
+    if (bwd) {
+        st = check_ptrs({workspace}, {});
+        if (st != RLK_OK) return st;
+        if (workspace_bytes < adaln_workspace(a)) return RLK_ERR_WORKSPACE;
+        a.part = static_cast<float*>(workspace);
+    }
+    st = device_ok(stream);
+    if (st != RLK_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return (bwd ? launch_adaln_bwd(a, gate, s) : launch_adaln_fwd(a, gate, s)) == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
+}
+
+// The geometry an operator-trace record shows for an adaln call.
+struct AdalnTraceShape {
+    rlk_ja_shape s{};
+    const rlk_ja_shape* p = nullptr;
+    explicit AdalnTraceShape(const rlk_adaln_shape* sh) {
+        if (sh == nullptr) return;
+        s.B = sh->B;
+        s.T_txt = sh->T_txt;
+        s.grid_h = 1;
+        s.grid_w = sh->T_img;
+        p = &s;
+    }
+};
+
+size_t rlk_adaln_workspace_bytes(const rlk_adaln_shape* shape) {
+    rlk_status why;
+    if (!adaln_shape_ok(shape, &why)) return 0;
+    return adaln_workspace(adaln_args(shape));
+}
+
+rlk_status rlk_adaln_modulation_fwd(const rlk_adaln_shape* shape, const rlk_adaln_io* txt, const rlk_adaln_io* img,
+                                    void* stream) {
+    OpScope sc(kOpAdalnModFwd, AdalnTraceShape(shape).p);
+    return sc.finish(adaln_call(shape, false, false, txt, img, nullptr, nullptr, nullptr, 0, stream));
+}
+
+rlk_status rlk_adaln_modulation_bwd(const rlk_adaln_shape* shape, const rlk_adaln_io* txt, const rlk_adaln_io* img,
+                                    const rlk_adaln_grad* gtxt, const rlk_adaln_grad* gimg, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+    OpScope sc(kOpAdalnModBwd, AdalnTraceShape(shape).p);
+    return sc.finish(adaln_call(shape, false, true, txt, img, gtxt, gimg, workspace, workspace_bytes, stream));
+}
+
+rlk_status rlk_adaln_gate_residual_fwd(const rlk_adaln_shape* shape, const rlk_adaln_io* txt,
+                                       const rlk_adaln_io* img, void* stream) {
+    OpScope sc(kOpAdalnGateFwd, AdalnTraceShape(shape).p);
+    return sc.finish(adaln_call(shape, true, false, txt, img, nullptr, nullptr, nullptr, 0, stream));
+}
+
+rlk_status rlk_adaln_gate_residual_bwd(const rlk_adaln_shape* shape, const rlk_adaln_io* txt,
+                                       const rlk_adaln_io* img, const rlk_adaln_grad* gtxt,
+                                       const rlk_adaln_grad* gimg, void* workspace, size_t workspace_bytes,
+                                       void* stream) {
+    OpScope sc(kOpAdalnGateBwd, AdalnTraceShape(shape).p);
+    return sc.finish(adaln_call(shape, true, true, txt, img, gtxt, gimg, workspace, workspace_bytes, stream));
+}
+
+// ---- gradient norm, AdamW ----
+constexpr int kMaxListTensors = 1 << 20;
+constexpr long long kMaxListElements = 1LL << 40;
+
+// What both calls read of a list: n, g and its type.
+static rlk_status grads_ok(const rlk_adamw_tensor* t, int32_t n) {
+    if (n < 0 || n > kMaxListTensors || (n > 0 && t == nullptr)) return RLK_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i) {
+        if (t[i].n < 0 || t[i].n > kMaxListElements || (t[i].g_dtype != RLK_BF16 && t[i].g_dtype != RLK_FP32))
+            return RLK_ERR_INVALID_ARG;
+        if (t[i].n == 0) continue;
+        if (t[i].g == nullptr) return RLK_ERR_INVALID_ARG;
+        if (!aligned16(t[i].g)) return RLK_ERR_ALIGNMENT;
+    }
+    return RLK_OK;
+}
+
+// No written range of the list may overlap another one of its ranges: sorted
+// by their starts, each is held against the furthest ends before it.
+static rlk_status list_disjoint(const rlk_adamw_tensor* t, int32_t n) {
+    struct Range {
+        uintptr_t lo, hi;
+        bool written;
+    };
+    std::unique_ptr<Range[]> r(new (std::nothrow) Range[(size_t)n * 7]);
+    if (!r) return RLK_ERR_CUDA;
+    size_t k = 0;
+    auto add = [&](const void* p, uint64_t bytes, bool written) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+        r[k++] = Range{lo, lo + bytes, written};
+    };
+    for (int i = 0; i < n; ++i) {
+        const rlk_adamw_tensor& e = t[i];
+        const uint64_t c = (uint64_t)e.n;
+        if (c == 0) continue;
+        add(e.p, c * (e.master != nullptr ? 2 : 4), true);
+        if (e.master != nullptr) add(e.master, c * 4, true);
+        add(e.g, c * (e.g_dtype == RLK_FP32 ? 4 : 2), false);
+        add(e.m, c * (e.state_bits / 8), true);
+        add(e.v, c * (e.state_bits / 8), true);
+        if (e.state_bits == 8) {
+            add(e.m_scale, (c + 31) / 32, true);
+            add(e.v_scale, (c + 31) / 32, true);
+        }
+    }
+    std::sort(r.get(), r.get() + k, [](const Range& a, const Range& b) { return a.lo < b.lo; });
+    uintptr_t any = 0, written = 0;
+    for (size_t i = 0; i < k; ++i) {
+        if (r[i].lo < (r[i].written ? any : written)) return RLK_ERR_INVALID_ARG;
+        any = std::max(any, r[i].hi);
+        if (r[i].written) written = std::max(written, r[i].hi);
+    }
+    return RLK_OK;
+}
+
+static rlk_status adamw_impl(const rlk_adamw_tensor* t, int32_t n, const rlk_adamw_args* a, void* stream) {
+    if (a == nullptr) return RLK_ERR_INVALID_ARG;
+    rlk_status st = grads_ok(t, n);
+    if (st != RLK_OK) return st;
+    auto below_one = [](double b) { return b >= 0.0 && b < 1.0; };
+    auto rate_ok = [](double x) { return x >= 0.0 && std::isfinite(x); };
+    if (!rate_ok(a->lr) || !below_one(a->beta1) || !below_one(a->beta2) || !(a->eps > 0.0) || !std::isfinite(a->eps) ||
+        (a->step_dev == nullptr && (a->step < 1 || a->step > 0x7fffffffLL)) || a->reserved != 0)
+        return RLK_ERR_INVALID_ARG;
+    auto aligned_to = [](const void* p, uintptr_t k) { return (reinterpret_cast<uintptr_t>(p) & (k - 1)) == 0; };
+    if (!aligned_to(a->lr_dev, 4) || !aligned_to(a->grad_scale, 4) || !aligned_to(a->step_dev, 8))
+        return RLK_ERR_ALIGNMENT;
+    for (int i = 0; i < n; ++i) {
+        const rlk_adamw_tensor& e = t[i];
+        if ((e.state_bits != 32 && e.state_bits != 8) || e.reserved != 0 || !rate_ok(e.lr_scale) ||
+            !rate_ok(e.weight_decay))
+            return RLK_ERR_INVALID_ARG;
+        if (e.n == 0) continue;
+        st = e.state_bits == 8 ? check_ptrs({e.p, e.m, e.v, e.m_scale, e.v_scale}, {e.master})
+                               : check_ptrs({e.p, e.m, e.v}, {e.master});
+        if (st != RLK_OK) return st;
+    }
+    st = list_disjoint(t, n);
+    if (st != RLK_OK) return st;
+    st = device_ok(stream);
+    if (st != RLK_OK) return st;
+    return launch_adamw(t, n, *a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
+}
+
+rlk_status rlk_adamw_step(const rlk_adamw_tensor* tensors, int32_t n_tensors, const rlk_adamw_args* args,
+                          void* stream) {
+    OpScope sc(kOpAdamw, nullptr);
+    return sc.finish(adamw_impl(tensors, n_tensors, args, stream));
+}
+
+size_t rlk_grad_norm_workspace_bytes(const rlk_adamw_tensor* tensors, int32_t n_tensors) {
+    if (grads_ok(tensors, n_tensors) != RLK_OK) return 0;
+    return std::max<size_t>(1, grad_norm_partials(tensors, n_tensors)) * sizeof(float);
+}
+
+static rlk_status grad_norm_impl(const rlk_adamw_tensor* t, int32_t n, float pre_scale, float max_norm, float* out,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+    rlk_status st = grads_ok(t, n);
+    if (st != RLK_OK) return st;
+    if (!(pre_scale > 0.0f) || !std::isfinite(pre_scale) || !(max_norm > 0.0f) || out == nullptr)
+        return RLK_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(out) & 3u) != 0) return RLK_ERR_ALIGNMENT;
+    st = check_ptrs({workspace}, {});
+    if (st != RLK_OK) return st;
+    if (workspace_bytes < rlk_grad_norm_workspace_bytes(t, n)) return RLK_ERR_WORKSPACE;
+    st = device_ok(stream);
+    if (st != RLK_OK) return st;
+    return launch_grad_norm(t, n, pre_scale, max_norm, out, static_cast<float*>(workspace),
+                            static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? RLK_OK
+               : RLK_ERR_CUDA;
+}
+
+rlk_status rlk_grad_norm(const rlk_adamw_tensor* tensors, int32_t n_tensors, float pre_scale, float max_norm, float* out,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+    OpScope sc(kOpGradNorm, nullptr);
+    return sc.finish(grad_norm_impl(tensors, n_tensors, pre_scale, max_norm, out, workspace, workspace_bytes, stream));
 }
 
 rlk_status rlk_joint_attn_check_status(void* stream) {

@@ -92,7 +92,9 @@ enum KernelId {
     kKRopeTable = 0, kKPrologue = 1, kKAttnFwd = 2, kKBwdPre = 3,
     kKBwdDkDv = 4, kKBwdDq = 5, kKNormRopeBwd = 6, kKDgFold = 7,
     kKQkGemm = 8, kKSoftmax = 9, kKAvGemm = 10, kKAttnFwdShard = 11, kKQkvGemm = 12, kKOutGemm = 13,
-    kKDpGemm = 14, kKSoftmaxBwd = 15, kKKeyGemm = 16, kKQueryGemm = 17, kKNormRopeBwdQ = 18, kNumKernelIds = 19
+    kKDpGemm = 14, kKSoftmaxBwd = 15, kKKeyGemm = 16, kKQueryGemm = 17, kKNormRopeBwdQ = 18,
+    kKAdalnFwd = 19, kKAdalnBwd = 20, kKAdalnFold = 21, kKGradNorm = 22, kKGradNormFold = 23, kKAdamw = 24,
+    kNumKernelIds = 25
 };
 
 // Launch timing hooks (rlk_host.cu): bracket one launch with events.
@@ -106,7 +108,8 @@ void timing_end(int kernel_id, cudaStream_t s);
 enum OpKind {
     kOpFwd = 0, kOpBwd, kOpFwdNoalloc, kOpNormRope, kOpQkGemm, kOpSoftmax, kOpAvGemm, kOpFwdShard,
     kOpFwdStreams, kOpBwdStreams, kOpQkvGemm, kOpFwdCtx, kOpOutGemm,
-    kOpBwdStats, kOpSoftmaxBwd, kOpAvGemmBwd, kOpQkGemmBwd, kOpNormRopeBwd
+    kOpBwdStats, kOpSoftmaxBwd, kOpAvGemmBwd, kOpQkGemmBwd, kOpNormRopeBwd,
+    kOpAdalnModFwd, kOpAdalnModBwd, kOpAdalnGateFwd, kOpAdalnGateBwd, kOpAdamw, kOpGradNorm
 };
 class OpScope {
    public:
@@ -244,6 +247,40 @@ cudaError_t launch_proj_gemm(const Geom& g, bool out_proj, const uint16_t* const
                              const SegBf16& k, const SegBf16& v, bool store_q, bool store_k, cudaStream_t s);
 int probe_qkv_tu(void);
 int read_and_clear_status_qkv(cudaStream_t s);
+
+// k_adaln.cu: adaln_modulation and adaln_gate_residual over both streams
+// (s[0] text, s[1] image; T = 0: absent). The backward's column sums of token
+// chunks (A, S, G per chunk, fp32 [3, C]) go through part: text chunks (b, j),
+// then image chunks.
+struct AdalnStream {
+    const void *x, *h, *gate, *scale, *shift;  // backward: x is the normalised rows (r for gate_residual)
+    const float *w, *w_post;
+    void *r, *y;
+    float *stats, *post_stats;
+    const void *dy, *dr;
+    void *dx, *dh;
+    float *dgate, *dscale, *dshift, *dw, *dw_post;
+    int T, chunks, chunk_rows;  // chunks of a sample, rows of a chunk
+};
+struct AdalnArgs {
+    AdalnStream s[2];
+    long long mod_stride, dmod_stride;
+    float* part;
+    int B, C, norm, post;
+    bool x_fp32, y_fp32, mod_fp32;
+    float eps, alpha;
+};
+int adaln_chunk_rows(int T);
+cudaError_t launch_adaln_fwd(const AdalnArgs& a, bool gate, cudaStream_t s);
+cudaError_t launch_adaln_bwd(const AdalnArgs& a, bool gate, cudaStream_t s);
+int probe_adaln_tu(void);
+
+// k_adamw.cu: the optimiser step (checked arguments)
+size_t grad_norm_partials(const rlk_adamw_tensor* t, int n);  // fp32 values of the norm's workspace
+cudaError_t launch_grad_norm(const rlk_adamw_tensor* t, int n, float pre, float max_norm, float* out, float* part,
+                             cudaStream_t s);
+cudaError_t launch_adamw(const rlk_adamw_tensor* t, int n, const rlk_adamw_args& a, cudaStream_t s);
+int probe_adamw_tu(void);
 
 // Tile geometry of the attention kernels (reported by the trace record).
 extern const int kFwdBlockQ, kFwdBlockKV;

@@ -1,0 +1,381 @@
+"""adaln_modulation and adaln_gate_residual on the GPU against their 64-bit
+definitions, forward and backward, within each value's own error bound: the
+fp32 bound that comes with the definition, plus half a step of the output's
+type (bf16 2^-8, fp32 2^-24, relative)."""
+
+import numpy as np
+import pytest
+
+import invariant_mmdit_joint_gb300 as pkg
+from oracle import block_ops as O
+from tests import _helpers as Hh
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module")
+def dev():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    d = torch.device("cuda:0")
+    torch.cuda.set_device(d)
+    return d
+
+
+def types(name):
+    import torch
+    return {"bf16": torch.bfloat16, "fp32": torch.float32}[name]
+
+
+def half_step(t):
+    import torch
+    return torch.finfo(t.dtype).eps / 2
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def assert_near(got, ref, where):
+    """|got - value| <= bound + half a step of got's type."""
+    value, bound = ref
+    g = f64(got)
+    assert g.shape == value.shape, where
+    err = np.abs(g - value)
+    tol = bound * (1 + 1e-6) + half_step(got) * (np.abs(value) + bound) + 1e-37
+    assert np.all(err <= tol), (where, float(np.max(err / tol)), np.unravel_index(np.argmax(err / tol), err.shape))
+
+
+class Case:
+    """Inputs of one call, (text, image) pairs on the device."""
+
+    def __init__(self, dev, B, txt, img, C, norm="layer", post="none", x="bf16", y="bf16", mod="bf16", weights=True,
+                 alpha=0.75, seed=1, offset=0.5, pack=6):
+        import torch
+        self.__dict__.update(B=B, T=(txt, img), C=C, norm=norm, post=post, alpha=alpha, dev=dev, weights=weights)
+        g = torch.Generator(device=dev)
+        g.manual_seed(seed)
+        self.op = pkg.AdaLN(B, txt, img, C, norm=norm, post=post, x_dtype=types(x), y_dtype=types(y),
+                            mod_dtype=types(mod), eps=EPS, alpha=alpha, device=dev)
+
+        def r(*shape):
+            return torch.randn(shape, generator=g, device=dev)
+
+        def pair(f):
+            return tuple(f(T) if T else None for T in self.T)
+        spread = torch.exp(r(C))
+        self.x = pair(lambda T: ((r(B, T, C) + offset) * spread).to(types(x)))
+        self.h = pair(lambda T: (r(B, T, C) + offset).to(types(y)))
+        self.dy = pair(lambda T: r(B, T, C).to(types(y)))
+        self.dr = pair(lambda T: r(B, T, C).to(types(x)))
+        mods = pair(lambda T: (0.4 * r(B, pack * C)).to(types(mod)))
+        self.scale, self.shift, self.gate = (tuple(None if m is None else m[:, i * C:(i + 1) * C] for m in mods)
+                                             for i in range(3))
+        self.w = pair(lambda T: 0.5 + torch.rand(C, generator=g, device=dev)) if weights else None
+        self.w_post = pair(lambda T: 0.5 + torch.rand(C, generator=g, device=dev)) if weights and post != "none" else None
+
+    def np(self, name, i, absent=None):
+        pair = getattr(self, name)
+        if pair is None or pair[i] is None:
+            return np.full(self.C, absent) if name.startswith("w") else np.full((self.B, self.C), absent)
+        return f64(pair[i])
+
+
+SHAPES = [
+    # B, text, image tokens, C: one token, one column group, odd counts, a warp's edge, two passes of columns
+    (1, 0, 1, 8), (2, 1, 0, 8), (3, 1, 2, 264), (1, 16, 64, 256), (2, 5, 131, 1160), (5, 9, 33, 136),
+    (1, 3, 17, 4096), (2, 2, 5, 4104), (1, 1, 3, 8192), (2, 31, 1037, 200),
+]
+KINDS = [
+    dict(norm="layer", post="none", x="bf16", y="bf16", mod="bf16", weights=False, alpha=1.0),
+    dict(norm="rms", post="rms", x="bf16", y="bf16", mod="fp32"),
+    dict(norm="layer", post="layer", x="fp32", y="bf16", mod="bf16"),
+    dict(norm="rms", post="layer", x="fp32", y="fp32", mod="fp32", alpha=-1.25),
+    dict(norm="layer", post="rms", x="fp32", y="fp32", mod="bf16", weights=False),
+]
+
+
+def check_stats(got, x, kind, where):
+    mean, rstd, me, re = O.stats(x, kind, EPS)
+    g = f64(got)
+    assert np.all(np.abs(g[..., 0] - mean) <= me + 2 * O.U * np.abs(mean)), where
+    assert np.all(np.abs(g[..., 1] - rstd) <= re + 2 * O.U * rstd), where
+
+
+def check_modulation(c, out, x, i, where):
+    y, err, _, _ = O.modulation(x, c.np("scale", i), c.np("shift", i), c.np("w", i, 1.0), c.norm, EPS)
+    assert_near(out["y"][i], (y, err), (where, "y"))
+    check_stats(out["stats"][i], x, c.norm, where)
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=lambda k: "-".join(str(v) for v in k.values()))
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_forward_and_backward(dev, shape, kind):
+    c = Case(dev, *shape, **kind)
+    # modulation
+    m = c.op.modulation(c.x, c.scale, c.shift, w=c.w)
+    b = c.op.modulation_bwd(c.x, c.scale, m["stats"], c.dy, c.dr, w=c.w)
+    nodr = c.op.modulation_bwd(c.x, c.scale, m["stats"], c.dy, None, w=c.w)
+    # gate, residual and the next modulation
+    f = c.op.gate_residual(c.x, c.h, c.gate, c.scale, c.shift, w=c.w, w_post=c.w_post)
+    q = c.op.gate_residual_bwd(f["r"], c.h, c.gate, c.scale, f["stats"], c.dy, c.dr, w=c.w, w_post=c.w_post,
+                               post_stats=f.get("post_stats"))
+    plain = c.op.gate_residual(c.x, c.h, c.gate, None, None, w_post=c.w_post, want_y=False)
+    last = c.op.gate_residual_bwd(f["r"], c.h, c.gate, None, None, None, c.dr, w_post=c.w_post,
+                                  post_stats=f.get("post_stats"))
+    for i in (0, 1):
+        if c.T[i] == 0:
+            assert all(v[i] is None for o in (m, b, f, q) for k, v in o.items() if k in ("y", "r", "dx", "dscale"))
+            continue
+        where = (shape, kind, i)
+        x, h, dy, dr = (f64(getattr(c, k)[i]) for k in ("x", "h", "dy", "dr"))
+        check_modulation(c, m, x, i, where)
+        sc, w, wp, gt = c.np("scale", i), c.np("w", i, 1.0), c.np("w_post", i, 1.0), c.np("gate", i)
+        st = f64(m["stats"][i])
+        for got, res in ((b, dr), (nodr, 0.0 * dr)):
+            ref = O.modulation_backward(x, sc, w, st[..., 0], st[..., 1], dy, res, c.norm)
+            assert set(got) == {"dx", "dscale", "dshift"} | ({"dw"} if c.weights else set())
+            for k in got:
+                assert_near(got[k][i], ref[k], (where, "modulation", k))
+        r, err, post = O.residual(x, h, gt, wp, c.post, c.alpha, EPS)
+        assert_near(f["r"][i], (r, err), (where, "r"))
+        assert Hh.bits_equal(plain["r"][i], f["r"][i])
+        r = f64(f["r"][i])
+        check_modulation(c, f, r, i, where)
+        ps = None
+        if c.post != "none":
+            check_stats(f["post_stats"][i], h, c.post, where)
+            g = f64(f["post_stats"][i])
+            ps = (g[..., 0], g[..., 1])
+        st = f64(f["stats"][i])
+        ref = O.gate_residual_backward(r, h, gt, sc, w, wp, st[..., 0], st[..., 1], ps, dy, dr, c.norm, c.post, c.alpha)
+        for k in q:
+            assert_near(q[k][i], ref[k], (where, "gate", k))
+        ref = O.gate_residual_backward(r, h, gt, sc, w, wp, None, None, ps, None, dr, c.norm, c.post, c.alpha)
+        assert set(last) == {"dx", "dh", "dgate"} | ({"dw_post"} if c.w_post else set())
+        for k in last:
+            assert_near(last[k][i], ref[k], (where, "residual alone", k))
+
+
+def test_large_mean_and_tiny_variance(dev):
+    """Rows far from zero: the variance is taken about the mean, so nothing cancels; constant rows stay finite."""
+    import torch
+    C = 1024
+    c = Case(dev, 1, 0, 4, C, x="fp32", y="fp32", mod="fp32", weights=False)
+    x = torch.full((1, 4, C), 1000.0, device=dev)
+    x[0, 1] += torch.randn(C, device=dev) * 0.01
+    x[0, 2] = 0.0
+    x[0, 3, ::2] = -1000.0
+    got = c.op.modulation((None, x), c.scale, c.shift)
+    xs = f64(x)
+    check_modulation(c, got, xs, 1, "offset rows")
+    # a constant row is its shift exactly
+    for row in (0, 2):
+        assert torch.equal(got["y"][1][0, row], c.shift[1][0])
+
+
+def test_non_finite_rows_stay_in_their_row(dev):
+    import torch
+    c = Case(dev, 2, 3, 5, 264, post="rms")
+    clean = c.op.gate_residual(c.x, c.h, c.gate, c.scale, c.shift, w=c.w, w_post=c.w_post)
+    x = tuple(t.clone() for t in c.x)
+    x[0][1, 2, 7], x[1][0, 0, 0] = float("inf"), float("nan")
+    got = c.op.gate_residual(x, c.h, c.gate, c.scale, c.shift, w=c.w, w_post=c.w_post)
+    for i, bad in ((0, (1, 2)), (1, (0, 0))):
+        assert torch.isnan(got["y"][i][bad]).any()
+        keep = torch.ones(got["y"][i].shape[:2], dtype=torch.bool)
+        keep[bad] = False
+        assert Hh.bits_equal(got["y"][i][keep.to(dev)], clean["y"][i][keep.to(dev)])
+
+
+@pytest.mark.parametrize("T", [1, 3, 40, 700, 2100])
+def test_a_sample_does_not_depend_on_its_batch(dev, T):
+    """Rows, statistics and per-sample gradients of a sample alone, first and last in a batch: the same bytes."""
+    B = 5
+    c = Case(dev, B, 0, T, 520, post="rms")
+    f = c.op.gate_residual(c.x, c.h, c.gate, c.scale, c.shift, w=c.w, w_post=c.w_post)
+    q = c.op.gate_residual_bwd(f["r"], c.h, c.gate, c.scale, f["stats"], c.dy, c.dr, w=c.w, w_post=c.w_post,
+                               post_stats=f["post_stats"])
+    one = pkg.AdaLN(1, 0, T, 520, post="rms", eps=EPS, alpha=c.alpha, device=dev)
+
+    def only(pair, b):
+        return (None, pair[1][b:b + 1].contiguous())
+    for b in (0, B - 1):
+        g = one.gate_residual(*(only(p, b) for p in (c.x, c.h, c.gate, c.scale, c.shift)), w=c.w, w_post=c.w_post)
+        for k in f:
+            assert Hh.bits_equal(g[k][1][0], f[k][1][b]), k
+        p = one.gate_residual_bwd(g["r"], only(c.h, b), only(c.gate, b), only(c.scale, b), g["stats"], only(c.dy, b),
+                                  only(c.dr, b), w=c.w, w_post=c.w_post, post_stats=g["post_stats"])
+        for k in ("dx", "dh", "dgate", "dscale", "dshift"):
+            assert Hh.bits_equal(p[k][1][0], q[k][1][b]), k
+
+
+def test_streams_are_independent_and_runs_repeat(dev):
+    """Text and image in one call give the bytes of each alone, and a second run the first's."""
+    c = Case(dev, 2, 77, 300, 640, post="layer")
+    both = c.op.gate_residual(c.x, c.h, c.gate, c.scale, c.shift, w=c.w, w_post=c.w_post)
+    args = dict(w=c.w, w_post=c.w_post)
+    grads = [c.op.gate_residual_bwd(both["r"], c.h, c.gate, c.scale, both["stats"], c.dy, c.dr,
+                                    post_stats=both["post_stats"], **args) for _ in range(2)]
+    for k in grads[0]:
+        for i in (0, 1):
+            assert Hh.bits_equal(grads[0][k][i], grads[1][k][i]), k
+    for i in (0, 1):
+        T = [0, 0]
+        T[i] = c.T[i]
+        one = pkg.AdaLN(2, *T, 640, post="layer", eps=EPS, alpha=c.alpha, device=dev)
+
+        def only(pair):
+            return (pair[0], None) if i == 0 else (None, pair[1])
+        got = one.gate_residual(*(only(p) for p in (c.x, c.h, c.gate, c.scale, c.shift)), w=only(c.w),
+                                w_post=only(c.w_post))
+        for k in both:
+            assert Hh.bits_equal(got[k][i], both[k][i]), k
+        back = one.gate_residual_bwd(got["r"], only(c.h), only(c.gate), only(c.scale), got["stats"], only(c.dy),
+                                     only(c.dr), w=only(c.w), w_post=only(c.w_post), post_stats=got["post_stats"])
+        for k in back:
+            assert Hh.bits_equal(back[k][i], grads[0][k][i]), k
+
+
+def test_in_place_residual_and_gradient(dev):
+    """r may be x and dx may be dr."""
+    c = Case(dev, 3, 9, 130, 1160, post="rms")
+    a = (c.x, c.h, c.gate, c.scale, c.shift)
+    want = c.op.gate_residual(*a, w=c.w, w_post=c.w_post)
+    wantb = c.op.gate_residual_bwd(want["r"], c.h, c.gate, c.scale, want["stats"], c.dy, c.dr, w=c.w, w_post=c.w_post,
+                                   post_stats=want["post_stats"])
+    out = {k: tuple(t.clone() for t in v) for k, v in want.items()}
+    out["r"] = c.x
+    got = c.op.gate_residual(*a, w=c.w, w_post=c.w_post, out=out)
+    assert got["r"][1].data_ptr() == c.x[1].data_ptr()
+    outb = {k: tuple(t.clone().zero_() for t in v) for k, v in wantb.items()}
+    outb["dx"] = c.dr
+    gotb = c.op.gate_residual_bwd(got["r"], c.h, c.gate, c.scale, got["stats"], c.dy, c.dr, w=c.w, w_post=c.w_post,
+                                  post_stats=got["post_stats"], out=outb)
+    for a, b in ((got, want), (gotb, wantb)):
+        for k in b:
+            for i in (0, 1):
+                assert Hh.bits_equal(a[k][i], b[k][i]), k
+
+
+def test_absent_modulation_is_the_plain_norm(dev):
+    import torch
+    c = Case(dev, 2, 4, 21, 136, x="fp32", y="fp32", mod="fp32", weights=False)
+    zeros = tuple(torch.zeros_like(s) for s in c.scale)
+    ones = tuple(torch.ones_like(s) for s in c.scale)
+    a = c.op.gate_residual(c.x, c.h, None, None, None)
+    b = c.op.gate_residual(c.x, c.h, ones, zeros, zeros)
+    for k in a:
+        for i in (0, 1):
+            assert torch.equal(a[k][i], b[k][i]), k
+    a = c.op.gate_residual_bwd(a["r"], c.h, None, None, a["stats"], c.dy, c.dr)
+    b = c.op.gate_residual_bwd(b["r"], c.h, ones, zeros, b["stats"], c.dy, c.dr)
+    for k in a:
+        for i in (0, 1):
+            assert torch.equal(a[k][i], b[k][i]), k
+
+
+def test_rows_behind_the_tensors_stay(dev):
+    """Outputs inside larger buffers: nothing before or behind them is written."""
+    import torch
+    c = Case(dev, 2, 3, 11, 264, post="rms")
+    f = c.op.gate_residual(c.x, c.h, c.gate, c.scale, c.shift, w=c.w, w_post=c.w_post)
+    q = c.op.gate_residual_bwd(f["r"], c.h, c.gate, c.scale, f["stats"], c.dy, c.dr, w=c.w, w_post=c.w_post,
+                               post_stats=f["post_stats"])
+    guards = []
+
+    def guarded(t):
+        pad = 64
+        buf = torch.full((t.numel() + 2 * pad,), -7.5, dtype=t.dtype, device=dev)
+        guards.append((buf, pad, t.numel()))
+        return buf[pad:pad + t.numel()].view(t.shape)
+    out = {k: tuple(guarded(t) for t in v) for k, v in f.items()}
+    c.op.gate_residual(c.x, c.h, c.gate, c.scale, c.shift, w=c.w, w_post=c.w_post, out=out)
+    outb = {k: tuple(guarded(t) for t in v) for k, v in q.items()}
+    c.op.gate_residual_bwd(f["r"], c.h, c.gate, c.scale, f["stats"], c.dy, c.dr, w=c.w, w_post=c.w_post,
+                           post_stats=f["post_stats"], out=outb)
+    for got, want in ((out, f), (outb, q)):
+        for k in want:
+            for i in (0, 1):
+                assert Hh.bits_equal(got[k][i], want[k][i]), k
+    for buf, pad, n in guards:
+        assert bool((buf[:pad] == -7.5).all()) and bool((buf[pad + n:] == -7.5).all())
+
+
+def test_graph_replay_and_other_streams(dev):
+    import torch
+    c, d = (Case(dev, 2, 40, 300, 640, post="rms", seed=s) for s in (3, 4))
+    names = ("x", "h", "gate", "scale", "shift", "dy", "dr")
+
+    def step(k, out=None):
+        f = c.op.gate_residual(k["x"], k["h"], k["gate"], k["scale"], k["shift"], w=c.w, w_post=c.w_post,
+                               out=None if out is None else out[0])
+        q = c.op.gate_residual_bwd(f["r"], k["h"], k["gate"], k["scale"], f["stats"], k["dy"], k["dr"], w=c.w,
+                                   w_post=c.w_post, post_stats=f["post_stats"], out=None if out is None else out[1])
+        return f, q
+    ins = [{n: getattr(k, n) for n in names} for k in (c, d)]
+    want = [step(k) for k in ins]
+    cap = {n: tuple(t.clone() if t.is_contiguous() else t.clone(memory_format=torch.contiguous_format)
+                    for t in ins[0][n]) for n in names}
+    outs = step(cap)
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(g, stream=s):
+            step(cap, outs)
+    torch.cuda.current_stream().wait_stream(s)
+    for which in (1, 0, 1):
+        for n in names:
+            for i in (0, 1):
+                cap[n][i].copy_(ins[which][n][i])
+        g.replay()
+        torch.cuda.synchronize()
+        for got, ref in zip(outs, want[which]):
+            for k in ref:
+                for i in (0, 1):
+                    assert Hh.bits_equal(got[k][i], ref[k][i]), (which, k)
+    # a stream given by hand, with nothing on the current one to order it
+    torch.cuda.synchronize()
+    f = c.op.gate_residual(*(ins[0][n] for n in names[:5]), w=c.w, w_post=c.w_post, stream=s)
+    s.synchronize()
+    for k in f:
+        assert Hh.bits_equal(f[k][1], want[0][0][k][1]), k
+
+
+def test_offsets_past_32_bits(dev):
+    """An activation of more than 2^32 bytes and 2^31 elements: the last rows are computed like the first."""
+    import torch
+    B, T, C = 3, 180_000, 4096
+    op = pkg.AdaLN(B, 0, T, C, device=dev)
+    g = torch.Generator(device=dev)
+    g.manual_seed(9)
+    x = torch.empty((B, T, C), dtype=torch.bfloat16, device=dev)
+    assert x.numel() > 2 ** 31
+    tile = torch.randn((1, 1000, C), generator=g, device=dev).bfloat16()
+    for b in range(B):
+        for t in range(0, T, 1000):
+            x[b, t:t + 1000] = tile[0]
+    mod = torch.randn((1, 2 * C), generator=g, device=dev).bfloat16().expand(B, 2 * C).contiguous()
+    scale, shift = (None, mod[:, :C]), (None, mod[:, C:])
+    out = op.modulation((None, x), scale, shift)
+    small = pkg.AdaLN(1, 0, 1000, C, device=dev).modulation((None, tile), (None, mod[:1, :C].contiguous()),
+                                                          (None, mod[:1, C:].contiguous()))
+    for b, t in ((0, 0), (1, 90_000), (2, T - 1000)):
+        assert Hh.bits_equal(out["y"][1][b, t:t + 1000], small["y"][1][0])
+    back = op.modulation_bwd((None, x), scale, out["stats"], (None, x), None, out=None)
+    sb = pkg.AdaLN(1, 0, 1000, C, device=dev)
+    sbk = sb.modulation_bwd((None, tile), (None, mod[:1, :C].contiguous()), small["stats"], (None, tile), None)
+    for b, t in ((0, 0), (2, T - 1000)):
+        assert Hh.bits_equal(back["dx"][1][b, t:t + 1000], sbk["dx"][1][0])
+
+
+def test_the_trace_names_the_kernels(dev):
+    c = Case(dev, 1, 3, 5, 64)
+    with pkg.op_trace() as t:
+        m = c.op.modulation(c.x, c.scale, c.shift)
+        c.op.modulation_bwd(c.x, c.scale, m["stats"], c.dy, c.dr)
+    assert [(r["op"], r["status"], r["kernels"]) for r in t.records] == [
+        ("adaln_modulation", 0, ["adaln_fwd_kernel"]),
+        ("adaln_modulation backward", 0, ["adaln_bwd_kernel", "adaln_fold_kernel"])]

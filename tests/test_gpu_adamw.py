@@ -1,0 +1,284 @@
+"""The gradient norm and AdamW on the GPU against their 64-bit definitions,
+within the bounds that come with these, and the 8-bit states bit by bit."""
+
+import numpy as np
+import pytest
+
+import invariant_mmdit_joint_gb300 as pkg
+from oracle import block_ops as O
+from tests import _helpers as Hh
+
+pytestmark = pytest.mark.gpu
+HYPER = dict(lr=3e-3, beta1=0.9, beta2=0.95, eps=1e-8)
+SIZES = [1, 7, 8, 31, 32, 33, 255, 2048, 2049, 4096, 4100, 12345, 100_003]
+
+
+@pytest.fixture(scope="module")
+def dev():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    d = torch.device("cuda:0")
+    torch.cuda.set_device(d)
+    return d
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def make(dev, sizes, bits, seed=1, **kw):
+    """Parameters (every second one bf16 with a master), gradients of both types, and the optimiser."""
+    import torch
+    g = torch.Generator(device=dev)
+    g.manual_seed(seed)
+
+    def r(n, s=1.0):
+        return torch.randn(n, generator=g, device=dev) * s
+    masters = [r(n, 0.05) if i % 2 else None for i, n in enumerate(sizes)]
+    params = [m.bfloat16() if m is not None else r(n, 0.05) for m, n in zip(masters, sizes)]
+    grads = [r(n, 10.0 ** ((i % 7) - 5)).to(torch.bfloat16 if i % 3 else torch.float32) for i, n in enumerate(sizes)]
+    kw = {**dict(lr=HYPER["lr"], betas=(HYPER["beta1"], HYPER["beta2"]), eps=HYPER["eps"],
+                 weight_decay=[0.1 * (i % 2) for i in range(len(sizes))],
+                 lr_scale=[1.0 + 0.5 * (i % 3) for i in range(len(sizes))], seed=77), **kw}
+    return pkg.AdamW(params, masters=masters, state_bits=bits, grads=grads, **kw), grads
+
+
+def truth(opt, i):
+    return opt.params[i] if opt.masters[i] is None else opt.masters[i]
+
+
+def state(opt, i):
+    """m and v of a parameter in 64 bits."""
+    import torch
+    if opt.state_bits == 32:
+        return f64(opt.m[i]), f64(opt.v[i])
+    u = lambda t: t.view(torch.uint8).cpu().numpy()  # noqa: E731
+    return O.decode(u(opt.m[i]), u(opt.m_scale[i])), O.decode(u(opt.v[i]), u(opt.v_scale[i]))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_steps_against_the_definition(dev, bits):
+    import torch
+    opt, grads = make(dev, SIZES, bits)
+    for step in (1, 2, 3, 500):
+        before = [(f64(truth(opt, i)), *state(opt, i)) for i in range(len(SIZES))]
+        opt.step(step)
+        for i, (p, m, v) in enumerate(before):
+            (p1, m1, v1), (pe, me, ve) = O.adamw(
+                p, f64(grads[i]), m, v, **{**HYPER, "lr": HYPER["lr"] * (1.0 + 0.5 * (i % 3))},
+                weight_decay=0.1 * (i % 2), step=step)
+            got = f64(truth(opt, i))
+            assert np.all(np.abs(got - p1) <= pe + 1e-37), (bits, step, i, np.max(np.abs(got - p1) / (pe + 1e-37)))
+            if opt.masters[i] is not None:
+                assert Hh.bits_equal(opt.params[i], opt.masters[i].bfloat16())
+            gm, gv = state(opt, i)
+            if bits == 32:
+                assert np.all(np.abs(gm - m1) <= me + 1e-37) and np.all(np.abs(gv - v1) <= ve + 1e-37), (step, i)
+                continue
+            # 8 bits: less than a step (2^-3 of the value's power of two, 2^-9 of the scale) around the fp32 value
+            for got, value, err, s in ((gm, m1, me, opt.m_scale[i]), (gv, v1, ve, opt.v_scale[i])):
+                scale = np.repeat(2.0 ** (s.cpu().numpy().astype(float) - 127), 32)[:value.size]
+                gap = np.maximum(np.abs(value) * 2.0 ** -3, scale * 2.0 ** -9) + err
+                assert np.all(np.abs(got - value) <= gap), (step, i)
+    assert all(bool(torch.isfinite(truth(opt, i)).all()) for i in range(len(SIZES)))
+
+
+def test_eight_bit_states_bit_by_bit(dev):
+    """The codes and scales follow from the fp32 moments (each product and sum
+    rounded by itself, as numpy's float32 does) and the hash's random bits."""
+    import torch
+    keys = [3 * i + 5 for i in range(len(SIZES))]
+    opt, grads = make(dev, SIZES, 8, keys=keys)
+    f, b1, b2 = np.float32, np.float32(0.9), np.float32(0.95)
+    o1, o2 = f(1 - 0.9), f(1 - 0.95)
+    scale = torch.tensor([0.37], device=dev)
+    for step in (1, 2, 9):
+        before = [state(opt, i) for i in range(len(SIZES))]
+        opt.step(step, grad_scale=scale)
+        for i, (m, v) in enumerate(before):
+            g = grads[i].float().cpu().numpy() * f(0.37)
+            m1 = b1 * m.astype(f) + o1 * g
+            v1 = b2 * v.astype(f) + (o2 * g) * g
+            assert m1.dtype == f and v1.dtype == f
+            rnd = O.random_bits(77, step, keys[i], m.size)
+            for name, value, part, positive in (("m", m1, rnd & 0xFFFF, False), ("v", v1, rnd >> 16, True)):
+                q, s = O.encode(value, part, positive)
+                got = getattr(opt, name)[i].view(torch.uint8).cpu().numpy()
+                np.testing.assert_array_equal(getattr(opt, name + "_scale")[i].cpu().numpy(), s)
+                np.testing.assert_array_equal(got, q)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_tensor_does_not_depend_on_its_list(dev, bits):
+    """One list, and each tensor by itself under the same key: the same bytes; a list past one launch's entries too."""
+    sizes = (SIZES * 45)[:560]
+    opt, grads = make(dev, sizes, bits, weight_decay=0.01, lr_scale=1.0)
+    copies = [(truth(opt, i).clone(), grads[i]) for i in range(len(sizes))]
+    for step in (1, 2):
+        opt.step(step)
+    for i in (0, 5, 12, 254, 255, 256, 257, 511, 512, 559):
+        p, g = copies[i]
+        one = pkg.AdamW([p], state_bits=bits, lr=HYPER["lr"], betas=(0.9, 0.95), weight_decay=0.01, seed=77, keys=[i],
+                        grads=[g])
+        for step in (1, 2):
+            one.step(step)
+        assert Hh.bits_equal(p, truth(opt, i)), i
+        for a, b in ((one.m[0], opt.m[i]), (one.v[0], opt.v[i])):
+            import torch
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
+
+
+@pytest.mark.parametrize("sizes", [[1], [5, 0, 4097], SIZES, [3_000_001]], ids=str)
+def test_gradient_norm(dev, sizes):
+    import torch
+    opt, grads = make(dev, sizes, 32)
+    want = np.sqrt(sum((f64(g) ** 2).sum() for g in grads))
+    # a chunk's squares: 16 in a thread, 5 shuffles, 8 warps, in fp32; half of that in the root; three roundings
+    tol = (0.5 * (16 + 5 + 8 + 2) + 3) * O.U
+    for pre, most in ((1.0, float("inf")), (0.25, want / 10), (1.0, 2 * want)):
+        got = f64(opt.grad_norm(most, pre_scale=pre))
+        assert abs(got[0] - pre * want) <= tol * pre * want
+        factor = pre * min(1.0, most / (pre * want + 1e-6))
+        assert abs(got[1] - factor) <= 2 * tol * factor
+    again = opt.grad_norm(2.0)
+    assert Hh.bits_equal(again, opt.grad_norm(2.0))
+
+
+def test_a_norm_that_is_not_finite_leaves_everything(dev):
+    import torch
+    for bits in (32, 8):
+        opt, grads = make(dev, SIZES, bits)
+        opt.step(1)
+        keep = [t.clone() for t in opt.params + [m for m in opt.masters if m is not None] + opt.m + opt.v]
+        for bad in (float("nan"), float("inf"), 3e30):  # the last one's square is not finite
+            grads[-1][17] = bad
+            n = opt.grad_norm(1.0)
+            assert not bool(torch.isfinite(n[0])) and bool(torch.isnan(n[1]))
+            opt.step(2, grad_scale=n[1:])
+            now = opt.params + [m for m in opt.masters if m is not None] + opt.m + opt.v
+            assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(now, keep))
+
+
+def test_non_finite_gradients_without_a_norm(dev):
+    """A NaN stays in its element with 32-bit states; with 8-bit ones its block of 32 reads as NaN from then on."""
+    import torch
+    for bits in (32, 8):
+        p = torch.zeros(100, device=dev)
+        g = torch.ones(100, device=dev)
+        g[40] = float("nan")
+        opt = pkg.AdamW([p], state_bits=bits, grads=[g])
+        opt.step(1)
+        assert torch.isnan(p).nonzero().flatten().tolist() == [40]
+        if bits == 8:
+            assert opt.m_scale[0].tolist()[1] == 255 and opt.v_scale[0].tolist()[1] == 255
+            opt.step(2)
+            assert torch.isnan(p).nonzero().flatten().tolist() == list(range(32, 64))
+
+
+def test_extreme_values_in_eight_bits(dev):
+    import torch
+    n = 64
+    g = torch.zeros(n, device=dev)
+    g[0], g[1], g[2] = 1e-18, -1e-30, 1e-38     # squares that vanish, a subnormal
+    g[32], g[33], g[34] = 1e18, 1.0, -1e-4      # a block of one giant
+    p = torch.zeros(n, device=dev)
+    opt = pkg.AdamW([p], state_bits=8, grads=[g], lr=1e-3, weight_decay=0.0, seed=5)
+    opt.step(1)
+    assert bool(torch.isfinite(p).all())
+    rnd = O.random_bits(5, 1, 0, n)
+    x = g.cpu().numpy()
+    f = np.float32
+    m1, v1 = f(1 - 0.9) * x, (f(1 - 0.999) * x) * x
+    for name, value, part, positive in (("m", m1, rnd & 0xFFFF, False), ("v", v1, rnd >> 16, True)):
+        q, s = O.encode(value, part, positive)
+        np.testing.assert_array_equal(getattr(opt, name + "_scale")[0].cpu().numpy(), s)
+        np.testing.assert_array_equal(getattr(opt, name)[0].view(torch.uint8).cpu().numpy(), q)
+
+
+def test_the_rounding_keeps_slow_moments_moving(dev):
+    """With beta2 = 0.999 a second moment moves by a thousandth a step, far
+    below half a code. Its mean over many elements still follows the running
+    average: 4096 elements from 0 toward g^2 = 1 over 200 steps."""
+    import torch
+    n = 4096
+    g = torch.ones(n, device=dev)
+    opt = pkg.AdamW([torch.zeros(n, device=dev)], state_bits=8, grads=[g], betas=(0.9, 0.999), lr=0.0, seed=11)
+    for step in range(1, 201):
+        opt.step(step)
+    _, v = state(opt, 0)
+    want = 1 - 0.999 ** 200
+    # a step's rounding has a variance of at most (change) * (code step = v / 8): relative standard deviation of one
+    # element below sqrt(sum of 0.001 / (8 v_t)) < 0.5, of the mean over 4096 below 0.008; four of those
+    assert abs(v.mean() / want - 1) < 0.032, v.mean() / want
+
+
+def test_captured_steps_follow_their_counter(dev):
+    import torch
+    for bits in (32, 8):
+        a, grads = make(dev, SIZES, bits)
+        b, _ = make(dev, SIZES, bits)
+        lr = torch.tensor([1e-3], device=dev)
+        count = torch.zeros(1, dtype=torch.int64, device=dev)
+        out, s, graph = torch.empty(2, device=dev), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        b.grad_norm(1.0, out=out)  # allocates the workspace
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            with torch.cuda.graph(graph, stream=s):
+                count.add_(1)
+                b.grad_norm(1.0, out=out)
+                b.step(count, lr=lr, grad_scale=out[1:])
+        torch.cuda.current_stream().wait_stream(s)
+        for step in range(1, 6):
+            rate = 1e-3 / step
+            lr.fill_(rate)
+            n = a.grad_norm(1.0)
+            a.step(step, lr=float(np.float32(rate)), grad_scale=n[1:])
+            graph.replay()
+            torch.cuda.synchronize()
+            assert Hh.bits_equal(n, out)
+            for x, y in zip(a.params + a.m + a.v, b.params + b.m + b.v):
+                assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), (bits, step)
+
+
+def test_elements_behind_the_tensors_stay(dev):
+    import torch
+    for bits in (32, 8):
+        for n in (1, 9, 33, 2047, 4099):
+            bufs = {}
+
+            def view(name, dtype, size, fill=0):
+                bufs[name] = torch.full((size + 256,), 1, dtype=torch.float32, device=dev).to(dtype)
+                t = bufs[name][:size]
+                t.copy_(torch.full((size,), fill, dtype=torch.float32, device=dev).to(dtype))
+                return t
+            code = torch.float8_e4m3fn if bits == 8 else torch.float32
+            kw = dict(m=[view("m", code, n)], v=[view("v", code, n)])
+            if bits == 8:
+                kw.update(m_scale=[view("ms", torch.uint8, -(-n // 32))], v_scale=[view("vs", torch.uint8, -(-n // 32))])
+            opt = pkg.AdamW([view("p", torch.bfloat16, n, 0.5)], masters=[view("w", torch.float32, n, 0.5)],
+                            state_bits=bits, grads=[view("g", torch.bfloat16, n, 0.25)], **kw)
+            opt.step(1, grad_scale=opt.grad_norm(1.0)[1:])
+            torch.cuda.synchronize()
+            for name, b in bufs.items():
+                size = -(-n // 32) if name in ("ms", "vs") else n
+                assert bool((b[size:].float() == 1).all()), (bits, n, name)
+
+
+def test_a_tensor_past_32_bits(dev):
+    """More than 2^32 elements with 8-bit states: the last ones are updated like the first."""
+    import torch
+    n = 2 ** 32 + 4097
+    p = torch.zeros(n, device=dev)
+    g = torch.full((n,), 0.5, dtype=torch.bfloat16, device=dev)
+    g[-1] = -2.0
+    opt = pkg.AdamW([p], state_bits=8, grads=[g], lr=1e-2, weight_decay=0.0)
+    norm = f64(opt.grad_norm(float("inf")))[0]
+    assert abs(norm / np.sqrt((n - 1) * 0.25 + 4.0) - 1) < 40 * O.U
+    opt.step(1)
+    assert torch.equal(p[:4096], p[2 ** 32:2 ** 32 + 4096])
+    # the first step is lr * |g| / (|g| + eps): 1 - 2e-8 of lr for |g| = 0.5, 1 - 5e-9 for |g| = 2, each with the
+    # definition's 8u of roundings, so the two sizes are not equal but at most 1.5e-8 + 16u apart
+    assert float(p[0]) < 0 and abs(float(p[-1]) / -float(p[0]) - 1) <= 1.5e-8 + 16 * O.U
+    # the hash repeats after 2^32 elements
+    assert torch.equal(opt.m[0].view(torch.uint8)[:4096], opt.m[0].view(torch.uint8)[2 ** 32:2 ** 32 + 4096])
