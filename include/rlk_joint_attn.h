@@ -519,7 +519,7 @@ typedef struct rlk_adaln_grad {
     const void* dr;    /* [B, T, C] */
     void* dx;          /* [B, T, C] */
     void* dh;          /* [B, T, C] */
-    float* dgate;      /* [B, C], rows dmod_stride apart */
+    float* dgate;      /* [B, C], rows dmod_stride apart (a multiple of 4) */
     float* dscale;     /* [B, C] */
     float* dshift;     /* [B, C] */
     float* dw;         /* [C] */

@@ -892,7 +892,9 @@ class AdaLN:
     x, r and their gradients have ``x_dtype``; y, h and theirs ``y_dtype``.
 
     Every call returns its outputs as a dict of pairs; passing that dict back
-    as ``out`` reuses its buffers."""
+    as ``out`` reuses its buffers. The backward calls share one workspace:
+    calls that may overlap on the GPU (other streams, graphs replayed at the
+    same time) need an object each."""
 
     def __init__(self, B: int, T_txt: int, T_img: int, C: int, norm: str = "layer", post: str | None = None,
                  x_dtype=None, y_dtype=None, mod_dtype=None, eps: float = 1e-6, alpha: float = 1.0, device="cuda"):
@@ -906,129 +908,121 @@ class AdaLN:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self.shape = AdalnShape.make(B, T_txt, T_img, C, norm, post or "none", self.x_dtype == f32, self.y_dtype == f32,
                                      self.mod_dtype == f32, eps, alpha)
-        self.tokens = (T_txt, T_img)
-        n_ws = rlk_adaln_workspace_bytes(self.shape)
-        if n_ws == 0:
+        self._ws_bytes = rlk_adaln_workspace_bytes(self.shape)
+        if self._ws_bytes == 0:
             raise RlkError(1, "AdaLN: invalid shape")
-        self._ws_bytes = n_ws
+        self._f32, self._index = f32, -1 if self.device.index is None else self.device.index
+        # expected sizes of each stream's tensors, None where it has no tokens
+        self._rows = tuple(torch.Size((B, T, C)) if T else None for T in (T_txt, T_img))
+        self._stats = tuple(torch.Size((B, T, 2)) if T else None for T in (T_txt, T_img))
+        self._sums = tuple(torch.Size((B, C)) if T else None for T in (T_txt, T_img))
+        self._vector = tuple(torch.Size((C,)) if T else None for T in (T_txt, T_img))
+        self._shapes = {}  # the call's shape struct by the modulation's sample stride
         self.workspace = None  # of the backward, allocated at its first call
 
     # ---- checks
-    def _bad(self, name, t, want, dtype):
-        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(want)} tensor on {self.device}, got {t.dtype} "
+    def _bad(self, name, i, t, want, dtype):
+        if want is None:
+            raise ValueError(f"{name}[{i}] must be None: the stream has no tokens")
+        if t is None:
+            raise ValueError(f"{name}[{i}] is missing")
+        raise ValueError(f"{name}[{i}] must be a contiguous {dtype} {tuple(want)} tensor on {self.device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
 
-    def _need(self, name, pair, dtype, tail):
-        """A pair of required dense tensors [B, T, *tail] (None for a stream without tokens)."""
+    def _need(self, name, pair, dtype, sizes):
+        """Pointers of a pair of required dense tensors."""
         if len(pair) != 2:
             raise ValueError(f"{name} must be a (text, image) pair")
+        got = [None, None]
         for i in (0, 1):
-            T = self.tokens[i]
-            if T == 0:
-                if pair[i] is not None:
-                    raise ValueError(f"{name}[{i}] must be None: the stream has no tokens")
+            t, want = pair[i], sizes[i]
+            if want is None and t is None:
                 continue
-            t = pair[i]
-            if t is None:
-                raise ValueError(f"{name}[{i}] is missing")
-            if t.dtype != dtype or t.shape != (self.shape.B, T, tail) or not t.is_contiguous() or \
-                    t.device != self.device:
-                self._bad(f"{name}[{i}]", t, (self.shape.B, T, tail), dtype)
-        return pair
-
-    def _weights(self, name, pair):
-        import torch
-        if pair is None:
-            return (None, None)
-        for i in (0, 1):
-            t = pair[i]
-            if t is not None and (t.dtype != torch.float32 or t.shape != (self.shape.C,) or not t.is_contiguous()
-                                  or t.device != self.device):
-                self._bad(f"{name}[{i}]", t, (self.shape.C,), torch.float32)
-        return pair
-
-    def _mods(self, *named):
-        """Pairs of [B, C] views with one sample stride (set in the shape)."""
-        sh, stride, got = self.shape, None, []
-        for name, pair in named:
-            pair = (None, None) if pair is None else pair
-            for i in (0, 1):
-                t = pair[i]
-                if t is None:
-                    continue
-                if t.dtype != self.mod_dtype or t.shape != (sh.B, sh.C) or t.stride(1) != 1 or t.device != self.device:
-                    raise ValueError(f"{name}[{i}] must be a {self.mod_dtype} [{sh.B}, {sh.C}] view with unit column "
-                                     f"stride on {self.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-                if sh.B > 1:
-                    if stride is not None and t.stride(0) != stride:
-                        raise ValueError(f"scale, shift and gate must have one sample stride: got {stride} and "
-                                         f"{t.stride(0)} ({name}[{i}])")
-                    stride = t.stride(0)
-            got.append(pair)
-        sh.mod_stride = sh.C if stride is None else stride
+            if want is None or t is None or t.dtype is not dtype or t.shape != want or not t.is_contiguous() \
+                    or t.get_device() != self._index:
+                self._bad(name, i, t, want, dtype)
+            got[i] = t.data_ptr()
         return got
 
-    def _alloc(self, pair_like, dtype=None, tail=None):
-        import torch
-        res = []
+    def _weights(self, name, pair):
+        """Pointers of a pair of optional [C] weights."""
+        if pair is None:
+            return (None, None)
+        sizes = tuple(None if t is None else w for t, w in zip(pair, self._vector))
         for i in (0, 1):
-            T = self.tokens[i]
-            if T == 0:
-                res.append(None)
-            elif tail is not None:
-                res.append(torch.empty((self.shape.B, T, tail), dtype=dtype, device=self.device))
-            else:
-                res.append(torch.empty(pair_like, dtype=dtype, device=self.device))
-        return tuple(res)
+            if pair[i] is not None and self._vector[i] is None:
+                self._bad(name, i, pair[i], None, None)
+        return self._need(name, pair, self._f32, sizes)
+
+    def _mods(self, *named):
+        """The call's shape (with the views' sample stride) and the pointers of pairs of [B, C] views."""
+        sh, stride, res = self.shape, None, []
+        many = sh.B > 1
+        for name, pair in named:
+            got = [None, None]
+            if pair is not None:
+                if len(pair) != 2:
+                    raise ValueError(f"{name} must be a (text, image) pair")
+                for i in (0, 1):
+                    t, want = pair[i], self._sums[i]
+                    if t is None:
+                        continue
+                    if want is None or t.dtype is not self.mod_dtype or t.shape != want or t.stride(1) != 1 \
+                            or t.get_device() != self._index:
+                        raise ValueError(f"{name}[{i}] must be a {self.mod_dtype} [{sh.B}, {sh.C}] view with unit column "
+                                         f"stride on {self.device} (None without tokens), got {t.dtype} "
+                                         f"{tuple(t.shape)} on {t.device}")
+                    if many:
+                        s = t.stride(0)
+                        if stride is None:
+                            stride = s
+                        elif s != stride:
+                            raise ValueError(f"scale, shift and gate must have one sample stride: got {stride} and {s} "
+                                             f"({name}[{i}])")
+                    got[i] = t.data_ptr()
+            res.append(got)
+        if stride is None:
+            stride = sh.C
+        call = self._shapes.get(stride)
+        if call is None:
+            call = AdalnShape.from_buffer_copy(sh)
+            call.mod_stride = stride
+            self._shapes[stride] = call
+        return [call] + res
 
     def _outputs(self, out, want):
-        """The outputs `want` = {name: (shape or None for [B, T, tail], dtype, tail)}, new or taken from `out`."""
+        """The outputs {name: (sizes, dtype)}, new or taken from `out`, and their pointers."""
+        import torch
         if out is None:
-            return {k: self._alloc(s, d, t) for k, (s, d, t) in want.items()}
-        if out.keys() != want.keys():
+            out = {k: tuple(None if s is None else torch.empty(s, dtype=d, device=self.device) for s in sizes)
+                   for k, (sizes, d) in want.items()}
+        elif out.keys() != want.keys():
             raise ValueError(f"out must hold {sorted(want)}, got {sorted(out)}")
-        for k, (s, d, t) in want.items():
-            if t is not None:
-                self._need(f"out[{k!r}]", out[k], d, t)
-                continue
-            for i in (0, 1):
-                v = out[k][i]
-                if self.tokens[i] and (v is None or v.dtype != d or v.shape != s or not v.is_contiguous()
-                                       or v.device != self.device):
-                    raise ValueError(f"out[{k!r}][{i}] must be a contiguous {d} {tuple(s)} tensor on {self.device}")
-        return out
+        return out, {k: self._need(k, out[k], d, sizes) for k, (sizes, d) in want.items()}
 
-    def _fill(self, cls, **pairs):
-        """One struct of pointers per stream (None for a stream without tokens)."""
-        res = []
-        for i in (0, 1):
-            if self.tokens[i] == 0:
-                res.append(None)
-                continue
-            res.append(cls(**{k: v[i].data_ptr() for k, v in pairs.items() if v[i] is not None}))
-        return res
-
-    def _on_device(self):
-        """The library launches on the current device: it must be the tensors' one."""
+    def _launch(self, name, call, io, grad=None, stream=None):
+        """The C call on one struct of pointers per stream ({field: pointers})."""
         _require_current(self.device)
-
-    def _workspace(self):
+        on = [s is not None for s in self._rows]
+        ios = [AdalnIo(**{k: v[i] for k, v in io.items()}) if on[i] else None for i in (0, 1)]
+        if grad is None:
+            (rlk_adaln_modulation_fwd if name == "modulation" else rlk_adaln_gate_residual_fwd)(call, ios, stream)
+            return
         import torch
         if self.workspace is None:
             self.workspace = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
-        return self.workspace
+        grads = [AdalnGrad(**{k: v[i] for k, v in grad.items()}) if on[i] else None for i in (0, 1)]
+        f = rlk_adaln_modulation_bwd if name == "modulation" else rlk_adaln_gate_residual_bwd
+        f(call, ios, grads, self.workspace, self._ws_bytes, stream)
 
     # ---- calls
     def modulation(self, x, scale, shift, w=None, out=None, stream=None):
         """y = hat(x) * w * (1 + scale) + shift. Returns y and stats."""
-        import torch
-        self._need("x", x, self.x_dtype, self.shape.C)
-        scale, shift = self._mods(("scale", scale), ("shift", shift))
-        w = self._weights("w", w)
-        out = self._outputs(out, {"y": (None, self.y_dtype, self.shape.C), "stats": (None, torch.float32, 2)})
-        self._on_device()
-        rlk_adaln_modulation_fwd(self.shape, self._fill(AdalnIo, x=x, scale=scale, shift=shift, w=w, y=out["y"],
-                                                        stats=out["stats"]), stream)
+        px = self._need("x", x, self.x_dtype, self._rows)
+        call, pscale, pshift = self._mods(("scale", scale), ("shift", shift))
+        pw = self._weights("w", w)
+        out, p = self._outputs(out, {"y": (self._rows, self.y_dtype), "stats": (self._stats, self._f32)})
+        self._launch("modulation", call, dict(x=px, scale=pscale, shift=pshift, w=pw, **p), stream=stream)
         return out
 
     def gate_residual(self, x, h, gate, scale, shift, w=None, w_post=None, want_y=True, out=None, stream=None):
@@ -1036,42 +1030,35 @@ class AdaLN:
         after the sublayer), y = modulation of r. Returns r, and with want_y y
         and stats, and with a norm after the sublayer post_stats. ``out`` may
         hold x itself as r."""
-        import torch
-        sh, post = self.shape, self.shape.post != 0
-        self._need("x", x, self.x_dtype, sh.C)
-        self._need("h", h, self.y_dtype, sh.C)
-        gate, scale, shift = self._mods(("gate", gate), ("scale", scale), ("shift", shift))
-        w, w_post = self._weights("w", w), self._weights("w_post", w_post)
-        want = {"r": (None, self.x_dtype, sh.C)}
+        px = self._need("x", x, self.x_dtype, self._rows)
+        ph = self._need("h", h, self.y_dtype, self._rows)
+        call, pgate, pscale, pshift = self._mods(("gate", gate), ("scale", scale), ("shift", shift))
+        pw, pwp = self._weights("w", w), self._weights("w_post", w_post)
+        want = {"r": (self._rows, self.x_dtype)}
         if want_y:
-            want.update(y=(None, self.y_dtype, sh.C), stats=(None, torch.float32, 2))
-        if post:
-            want["post_stats"] = (None, torch.float32, 2)
-        out = self._outputs(out, want)
-        self._on_device()
-        rlk_adaln_gate_residual_fwd(sh, self._fill(AdalnIo, x=x, h=h, gate=gate, scale=scale, shift=shift, w=w,
-                                                   w_post=w_post, **out), stream)
+            want.update(y=(self._rows, self.y_dtype), stats=(self._stats, self._f32))
+        if call.post:
+            want["post_stats"] = (self._stats, self._f32)
+        out, p = self._outputs(out, want)
+        self._launch("gate_residual", call, dict(x=px, h=ph, gate=pgate, scale=pscale, shift=pshift, w=pw, w_post=pwp,
+                                                 **p), stream=stream)
         return out
 
     def modulation_bwd(self, x, scale, stats, dy, dr=None, w=None, out=None, stream=None):
         """Gradients of the modulation: dx (with dr, the gradient that reaches
         x by the residual path, added), dscale and dshift [B, C] and, with w,
         dw [C], all sums float32. ``out`` may hold dr itself as dx."""
-        import torch
-        sh, f32 = self.shape, torch.float32
-        self._need("x", x, self.x_dtype, sh.C)
-        self._need("stats", stats, f32, 2)
-        self._need("dy", dy, self.y_dtype, sh.C)
-        dr = (None, None) if dr is None else self._need("dr", dr, self.x_dtype, sh.C)
-        (scale,) = self._mods(("scale", scale))
-        w = self._weights("w", w)
-        want = {"dx": (None, self.x_dtype, sh.C), "dscale": ((sh.B, sh.C), f32, None), "dshift": ((sh.B, sh.C), f32, None)}
-        if w[0] is not None or w[1] is not None:
-            want["dw"] = ((sh.C,), f32, None)
-        out = self._outputs(out, want)
-        self._on_device()
-        rlk_adaln_modulation_bwd(sh, self._fill(AdalnIo, x=x, scale=scale, w=w, stats=stats),
-                                 self._fill(AdalnGrad, dy=dy, dr=dr, **out), self._workspace(), self._ws_bytes, stream)
+        px = self._need("x", x, self.x_dtype, self._rows)
+        pst = self._need("stats", stats, self._f32, self._stats)
+        pdy = self._need("dy", dy, self.y_dtype, self._rows)
+        pdr = (None, None) if dr is None else self._need("dr", dr, self.x_dtype, self._rows)
+        call, pscale = self._mods(("scale", scale))
+        pw = self._weights("w", w)
+        want = {"dx": (self._rows, self.x_dtype), "dscale": (self._sums, self._f32), "dshift": (self._sums, self._f32)}
+        if pw[0] or pw[1]:
+            want["dw"] = (self._vector, self._f32)
+        out, p = self._outputs(out, want)
+        self._launch("modulation", call, dict(x=px, scale=pscale, w=pw, stats=pst), dict(dy=pdy, dr=pdr, **p), stream)
         return out
 
     def gate_residual_bwd(self, r, h, gate, scale, stats, dy, dr=None, w=None, w_post=None, post_stats=None, out=None,
@@ -1080,35 +1067,30 @@ class AdaLN:
         dh, dgate, with dy (None: y was not used) dscale and dshift, with w
         dw, with w_post dw_post. dr is the gradient that reaches r by the
         residual path. ``out`` may hold dr itself as dx."""
-        import torch
-        sh, f32 = self.shape, torch.float32
-        self._need("r", r, self.x_dtype, sh.C)
-        self._need("h", h, self.y_dtype, sh.C)
+        f32 = self._f32
+        pr = self._need("r", r, self.x_dtype, self._rows)
+        ph = self._need("h", h, self.y_dtype, self._rows)
         if dy is None and dr is None:
             raise ValueError("dy and dr cannot both be None")
-        dr = (None, None) if dr is None else self._need("dr", dr, self.x_dtype, sh.C)
-        gate, scale = self._mods(("gate", gate), ("scale", scale))
-        w, w_post = self._weights("w", w), self._weights("w_post", w_post)
-        want = {"dx": (None, self.x_dtype, sh.C), "dh": (None, self.y_dtype, sh.C), "dgate": ((sh.B, sh.C), f32, None)}
+        none = (None, None)
+        pdr = none if dr is None else self._need("dr", dr, self.x_dtype, self._rows)
+        call, pgate, pscale = self._mods(("gate", gate), ("scale", scale))
+        pw, pwp = self._weights("w", w), self._weights("w_post", w_post)
+        want = {"dx": (self._rows, self.x_dtype), "dh": (self._rows, self.y_dtype), "dgate": (self._sums, f32)}
+        pdy = pst = pps = none
         if dy is not None:
-            self._need("dy", dy, self.y_dtype, sh.C)
-            self._need("stats", stats, f32, 2)
-            want.update(dscale=((sh.B, sh.C), f32, None), dshift=((sh.B, sh.C), f32, None))
-            if w[0] is not None or w[1] is not None:
-                want["dw"] = ((sh.C,), f32, None)
-        else:
-            dy = stats = (None, None)
-        if sh.post:
-            self._need("post_stats", post_stats, f32, 2)
-            if w_post[0] is not None or w_post[1] is not None:
-                want["dw_post"] = ((sh.C,), f32, None)
-        else:
-            post_stats = (None, None)
-        out = self._outputs(out, want)
-        self._on_device()
-        rlk_adaln_gate_residual_bwd(sh, self._fill(AdalnIo, r=r, h=h, gate=gate, scale=scale, w=w, w_post=w_post,
-                                                   stats=stats, post_stats=post_stats),
-                                    self._fill(AdalnGrad, dy=dy, dr=dr, **out), self._workspace(), self._ws_bytes, stream)
+            pdy = self._need("dy", dy, self.y_dtype, self._rows)
+            pst = self._need("stats", stats, f32, self._stats)
+            want.update(dscale=(self._sums, f32), dshift=(self._sums, f32))
+            if pw[0] or pw[1]:
+                want["dw"] = (self._vector, f32)
+        if call.post:
+            pps = self._need("post_stats", post_stats, f32, self._stats)
+            if pwp[0] or pwp[1]:
+                want["dw_post"] = (self._vector, f32)
+        out, p = self._outputs(out, want)
+        self._launch("gate_residual", call, dict(r=pr, h=ph, gate=pgate, scale=pscale, w=pw, w_post=pwp, stats=pst,
+                                                 post_stats=pps), dict(dy=pdy, dr=pdr, **p), stream)
         return out
 
 

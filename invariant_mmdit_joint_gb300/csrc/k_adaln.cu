@@ -4,50 +4,124 @@
 //   r = x + alpha * gate_b * u,  u = h or hat(h) * w_post,  then y from r
 // (the formulas and the gradients' are in include/rlk_joint_attn.h).
 //
-// Every kernel here is bound by HBM: a row is read once, stays in registers
-// between its reductions and is written once.
+// Each activation is read once and written once: the floor is HBM (1024^2, C =
+// 2560: 13.2 us forward, 26.3 us backward; 1328^2 with the gate: 65 and 130
+// us). What it takes to come near it is to have few instructions and many rows
+// under way: rows are copied ahead by cp.async, a CTA's threads keep the same
+// columns for every row, and what a sample's rows share stays in registers.
+// Measured: forward 19.2 us (4.6 TB/s) and 81 us (5.4 TB/s), backward with its
+// folds 42 us (4.2 TB/s) and 165 us (5.3 TB/s); the rest is the latency of a
+// row's sums (shuffles and one barrier each), which the warps of an SM cover
+// only in part.
 #include "rlk_device.cuh"
 #include "rlk_internal.h"
-
+#include "rlk_sm100.cuh"
 RLK_DEFINE_STRICT_PROBE(probe_adaln_tu)
 
 namespace rlk {
 namespace {
 
-constexpr int kMaxThreads = 512;  // 8 columns a thread and pass: C <= 4096 in one, <= 8192 in two
-constexpr int kMaxWarps = kMaxThreads / 32;
+using namespace sm100;
+
+// ------------------------------------------------------------ row ring
+// Rows come through a ring of shared-memory stages filled by cp.async. A
+// thread copies and reads only its own 16-byte pieces, so the ring needs no
+// barrier, and rows ahead are in flight without holding registers.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
 
 // ------------------------------------------------------------ 8 columns
-__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    v[0] = bf16_lo(q.x), v[1] = bf16_hi(q.x), v[2] = bf16_lo(q.y), v[3] = bf16_hi(q.y);
-    v[4] = bf16_lo(q.z), v[5] = bf16_hi(q.z), v[6] = bf16_lo(q.w), v[7] = bf16_hi(q.w);
+// Eight consecutive columns of a row as four pairs of fp32 values: the packed
+// instructions take half the issue slots of the scalar ones, which these
+// kernels would otherwise run out of before HBM does.
+struct V8 {
+    uint64_t p[4];
+};
+__device__ __forceinline__ V8 v8_all(float x) {
+    const uint64_t q = f2_pack(x, x);
+    return V8{{q, q, q, q}};
 }
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+__device__ __forceinline__ uint64_t bf16_pair(uint32_t w) { return f2_pack(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ uint32_t pair_bf16(uint64_t v) {
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    return pack_bf16(lo, hi);
 }
-// stores 8 values and leaves in v what was stored
-__device__ __forceinline__ void store8(uint16_t* p, float (&v)[8]) {
-    uint4 q = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-    *reinterpret_cast<uint4*>(p) = q;
-    v[0] = bf16_lo(q.x), v[1] = bf16_hi(q.x), v[2] = bf16_lo(q.y), v[3] = bf16_hi(q.y);
-    v[4] = bf16_lo(q.z), v[5] = bf16_hi(q.z), v[6] = bf16_lo(q.w), v[7] = bf16_hi(q.w);
+__device__ __forceinline__ V8 v8_of(uint4 q) {
+    return V8{{bf16_pair(q.x), bf16_pair(q.y), bf16_pair(q.z), bf16_pair(q.w)}};
 }
-__device__ __forceinline__ void store8(float* p, float (&v)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ V8 v8_of(float4 a, float4 b) {
+    return V8{{f2_pack(a.x, a.y), f2_pack(a.z, a.w), f2_pack(b.x, b.y), f2_pack(b.z, b.w)}};
 }
-// 8 values of a modulation row (or `absent` in each)
-__device__ __forceinline__ void load8_mod(const void* base, bool fp32, long long at, float absent, float (&v)[8]) {
-    if (base == nullptr) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = absent;
-    } else if (fp32) {
-        load8(static_cast<const float*>(base) + at, v);
-    } else {
-        load8(static_cast<const uint16_t*>(base) + at, v);
+__device__ __forceinline__ V8 load8(const uint16_t* p) { return v8_of(*reinterpret_cast<const uint4*>(p)); }
+__device__ __forceinline__ V8 load8(const float* p) {
+    return v8_of(reinterpret_cast<const float4*>(p)[0], reinterpret_cast<const float4*>(p)[1]);
+}
+__device__ __forceinline__ float4 half_of(const V8& v, int k) {
+    float4 f;
+    f2_unpack(v.p[2 * k], f.x, f.y);
+    f2_unpack(v.p[2 * k + 1], f.z, f.w);
+    return f;
+}
+// Stores the values, rounded to the type, and returns what was stored.
+__device__ __forceinline__ V8 store8(uint16_t* p, const V8& v, bool write = true) {
+    const uint4 q = make_uint4(pair_bf16(v.p[0]), pair_bf16(v.p[1]), pair_bf16(v.p[2]), pair_bf16(v.p[3]));
+    if (write) *reinterpret_cast<uint4*>(p) = q;
+    return v8_of(q);
+}
+__device__ __forceinline__ V8 store8(float* p, const V8& v, bool write = true) {
+    if (write) {
+        reinterpret_cast<float4*>(p)[0] = half_of(v, 0);
+        reinterpret_cast<float4*>(p)[1] = half_of(v, 1);
     }
+    return v;
+}
+// 8 values of a modulation row (or `absent` in each).
+__device__ __forceinline__ V8 load8_mod(const void* base, bool fp32, long long at, float absent) {
+    if (base == nullptr) return v8_all(absent);
+    return fp32 ? load8(static_cast<const float*>(base) + at) : load8(static_cast<const uint16_t*>(base) + at);
+}
+__device__ __forceinline__ V8 operator*(const V8& a, const V8& b) {
+    return V8{{mul_f2(a.p[0], b.p[0]), mul_f2(a.p[1], b.p[1]), mul_f2(a.p[2], b.p[2]), mul_f2(a.p[3], b.p[3])}};
+}
+__device__ __forceinline__ V8 operator+(const V8& a, const V8& b) {
+    return V8{{add_f2(a.p[0], b.p[0]), add_f2(a.p[1], b.p[1]), add_f2(a.p[2], b.p[2]), add_f2(a.p[3], b.p[3])}};
+}
+__device__ __forceinline__ V8 operator-(const V8& a, const V8& b) {
+    return V8{{sub_f2(a.p[0], b.p[0]), sub_f2(a.p[1], b.p[1]), sub_f2(a.p[2], b.p[2]), sub_f2(a.p[3], b.p[3])}};
+}
+__device__ __forceinline__ V8 fma8(const V8& a, const V8& b, const V8& c) {
+    return V8{{fma_f2(a.p[0], b.p[0], c.p[0]), fma_f2(a.p[1], b.p[1], c.p[1]), fma_f2(a.p[2], b.p[2], c.p[2]),
+               fma_f2(a.p[3], b.p[3], c.p[3])}};
+}
+// Adds the eight values (or their products) to a pair of running sums.
+__device__ __forceinline__ void sum8(uint64_t& s, const V8& v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = add_f2(s, v.p[i]);
+}
+__device__ __forceinline__ void dot8(uint64_t& s, const V8& a, const V8& b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = fma_f2(a.p[i], b.p[i], s);
+}
+__device__ __forceinline__ float pair_sum(uint64_t s) {
+    float lo, hi;
+    f2_unpack(s, lo, hi);
+    return lo + hi;
+}
+
+// A value that the compiler keeps in a register: it would rather read special
+// registers and kernel arguments anew at every use, which here cost more
+// instructions a row than the sums.
+template <typename T>
+__device__ __forceinline__ T kept(T x) {
+    asm volatile("" : "+r"(x));
+    return x;
 }
 
 __device__ __forceinline__ float warp_sum(float x) {
@@ -56,363 +130,567 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
-// Elements of a row that warp w holds.
-template <int NV>
-__device__ __forceinline__ int warp_count(int w, int groups) {
-    int n = 0;
+// The 16-byte pieces of 8 columns: one of bf16, two of fp32. Piece k of all
+// threads is consecutive in a stage (PITCH = 16 bytes for each of the most
+// threads the kernel is built for, so that a piece is at a fixed offset), as
+// the copies want it: with a thread's own pieces together instead, each
+// 16-byte copy of a warp went to another line and the 1328^2 backward took
+// 229 us for 175.
+template <typename T>
+constexpr int kPieces = sizeof(T) / 2;
+template <int PITCH, typename T>
+__device__ __forceinline__ void ring_fill(uint32_t to, const T* src) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) n += min(max(groups - (j * (int)blockDim.x + 32 * w), 0), 32);
-    return 8 * n;
+    for (int p = 0; p < kPieces<T>; ++p) copy16(to + p * PITCH, reinterpret_cast<const char*>(src) + 16 * p);
+}
+template <int PITCH>
+__device__ __forceinline__ V8 ring_read(const uint8_t* at, const uint16_t*) {
+    return v8_of(*reinterpret_cast<const uint4*>(at));
+}
+template <int PITCH>
+__device__ __forceinline__ V8 ring_read(const uint8_t* at, const float*) {
+    return v8_of(*reinterpret_cast<const float4*>(at), *reinterpret_cast<const float4*>(at + PITCH));
 }
 
-// Mean (0 for rms) and 1 / deviation of a row held NV * 8 values a thread,
-// inactive ones 0. Each warp takes its own mean and its squares about that,
-// the warps are then joined about the row's mean (a large mean cancels in
-// neither step), so one block barrier a row is enough. buf: kMaxWarps slots
-// that the previous call must not have used.
-template <int NV>
-__device__ __forceinline__ float2 row_stats(const float (&v)[NV][8], const bool (&act)[NV], bool rms, int C, float eps,
-                                            float2* buf) {
-    const int warp = threadIdx.x / 32, n_warps = blockDim.x / 32, groups = C / 8;
-    float s = 0.0f, q = 0.0f, mean_w = 0.0f;
-    if (!rms) {
+// ------------------------------------------------------------ sums of a row
+// A CTA owns a row at a time, a thread the same NV * 8 of its columns in every
+// row (the last 8 may lie past it). Sums run within a warp, then over the
+// warps, both by exchanges in one order that depends on C alone.
+constexpr int kMaxThreads = 512;
+
+// Sum over each half of a warp.
+__device__ __forceinline__ float half_sum(float v) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s += v[j][i];
-        s = warp_sum(s);
-        mean_w = s / (float)max(warp_count<NV>(warp, groups), 1);
-    }
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-        if (act[j])
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float z = v[j][i] - mean_w;
-                q = fmaf(z, z, q);
-            }
-    q = warp_sum(q);
-    if (threadIdx.x % 32 == 0) buf[warp] = make_float2(s, q);
-    __syncthreads();
-    float mean = 0.0f, m2 = 0.0f;
-    if (!rms) {
-        for (int w = 0; w < n_warps; ++w) mean += buf[w].x;
-        mean /= (float)C;
-    }
-    for (int w = 0; w < n_warps; ++w) {
-        const float2 p = buf[w];
-        if (!rms) {
-            const float n = (float)warp_count<NV>(w, groups);
-            const float z = n > 0.0f ? p.x / n - mean : 0.0f;
-            m2 = fmaf(n * z, z, m2);
-        }
-        m2 += p.y;
-    }
-    return make_float2(mean, 1.0f / sqrtf(m2 / (float)C + eps));
+    for (int m = 8; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
 }
 
-// Sums of two values over the block; buf as above.
-__device__ __forceinline__ float2 block_sum2(float x, float y, float2* buf) {
-    const int warp = threadIdx.x / 32, n_warps = blockDim.x / 32;
-    x = warp_sum(x);
-    y = warp_sum(y);
-    if (threadIdx.x % 32 == 0) buf[warp] = make_float2(x, y);
-    __syncthreads();
-    float2 r = make_float2(0.0f, 0.0f);
-    for (int w = 0; w < n_warps; ++w) {
-        r.x += buf[w].x;
-        r.y += buf[w].y;
+// Values of a row that a warp holds (0 for one past the CTA's).
+template <int NV>
+__device__ __forceinline__ float held_by(int warp, int groups) {
+    if (warp >= (int)blockDim.x / 32) return 0.0f;
+    int held = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) held += min(max(groups - (j * (int)blockDim.x + 32 * warp), 0), 32);
+    return 8.0f * (float)held;
+}
+
+// A thread whose last 8 columns lie past the row takes the row's last 8 once
+// more, so that its loads need no branch; `last` (whether they exist) keeps
+// them out of the sums and the results.
+struct RowSums {
+    float mine, joined;  // values of a row that this warp and warp lane % 16 hold
+    float inv_mine, inv_c, eps;
+    bool last;
+    int tid, warps;
+};
+
+// The sum over a thread's columns of what f(pair sum, j) adds up.
+template <int NV, typename F>
+__device__ __forceinline__ float thread_sum(bool last, F f) {
+    uint64_t s = 0, e = 0;
+#pragma unroll
+    for (int j = 0; j + 1 < NV; ++j) f(s, j);
+    f(e, NV - 1);
+    const float end = last ? pair_sum(e) : 0.0f;
+    return NV == 1 ? end : pair_sum(s) + end;
+}
+
+// Mean (0 for rms) and 1 / deviation of a row. Each warp takes its own mean
+// and its squares about that; the warps are then joined about the row's mean
+// (a large mean cancels in neither step), so one barrier is enough. buf: 16
+// slots, zero where there is no warp, that the previous call has not used.
+template <int NV>
+__device__ __forceinline__ float2 row_stats(const V8 (&v)[NV], bool rms, const RowSums& g, float2* buf) {
+    float mean = 0.0f;
+    if (!rms) mean = warp_sum(thread_sum<NV>(g.last, [&](uint64_t& s, int j) { sum8(s, v[j]); })) * g.inv_mine;
+    const V8 m = v8_all(mean);
+    float m2 = warp_sum(thread_sum<NV>(g.last, [&](uint64_t& s, int j) {
+        const V8 z = v[j] - m;
+        dot8(s, z, z);
+    }));
+    if (g.warps > 1) {
+        if (g.tid % 32 == 0) buf[g.tid / 32] = make_float2(mean, m2);
+        __syncthreads();
+        const float2 p = buf[g.tid % 16];
+        mean = rms ? 0.0f : half_sum(p.x * g.joined) * g.inv_c;
+        const float z = p.x - mean;  // 0 for rms
+        m2 = half_sum(fmaf(g.joined * z, z, p.y));
     }
-    return r;
+    return make_float2(mean, 1.0f / sqrtf(fmaf(m2, g.inv_c, g.eps)));
+}
+
+// Sums of two values over the CTA. The halves of a warp take one value each
+// (one exchange, then four steps on one value instead of five on two), and
+// the warps' sums are joined the same way. buf: [2][16] as above.
+__device__ __forceinline__ float2 block_sum2(float x, float y, int tid, int warps, float* buf) {
+    const int lane = tid % 32;
+    const bool upper = lane >= 16;
+    float v = half_sum((upper ? y : x) + __shfl_xor_sync(0xffffffffu, upper ? x : y, 16));
+    if (warps > 1) {
+        if (lane % 16 == 0) buf[(lane & 16) + tid / 32] = v;
+        __syncthreads();
+        v = half_sum(buf[lane]);
+    }
+    const float other = __shfl_xor_sync(0xffffffffu, v, 16);
+    return upper ? make_float2(other, v) : make_float2(v, other);
 }
 
 // ------------------------------------------------------------ forward
-// One CTA per row.
-template <typename X, typename Y, int NV, bool GATE, bool POST>
-__global__ void __launch_bounds__(kMaxThreads) adaln_fwd_kernel(const __grid_constant__ AdalnArgs a) {
-    __shared__ float2 buf[2][kMaxWarps];
-    const long long rows_txt = (long long)a.B * a.s[0].T;
-    const int img = blockIdx.x >= rows_txt;
-    const AdalnStream& st = a.s[img];
-    const long long row = (long long)blockIdx.x - (img ? rows_txt : 0);
-    const int b = (int)(row / st.T), C = a.C;
-    const X* x = static_cast<const X*>(st.x) + row * C;
-    float v[NV][8];
-    bool act[NV];
+// CTA i takes the rows [i, i + 1) / grid of all. What is the same for every
+// row of a sample (w * (1 + scale), shift, alpha * gate * w_post) stays in a
+// thread's registers until the CTA comes to the next sample.
+constexpr int kFwdStages = 3;
+
+template <typename X, typename Y, int NV, int THREADS, bool GATE, bool POST>
+__global__ void __launch_bounds__(THREADS) adaln_fwd_kernel(const __grid_constant__ AdalnArgs a) {
+    constexpr int PITCH = 16 * THREADS;
+    constexpr int kX = NV * kPieces<X>, kRow = kX + (GATE ? NV * kPieces<Y> : 0);  // a row's pieces: x, h
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float2 buf[2][16];
+    const int tid = kept((int)threadIdx.x), threads = blockDim.x, C = kept(a.C), warps = kept(threads / 32);
+    const int col = 8 * tid;
+    const bool rms = a.norm == RLK_NORM_RMS, post_rms = a.post == RLK_NORM_RMS;
+    RowSums g;
+    g.mine = held_by<NV>(tid / 32, C / 8);
+    g.joined = held_by<NV>(tid % 16, C / 8);
+    g.inv_mine = 1.0f / fmaxf(g.mine, 1.0f);
+    g.inv_c = 1.0f / (float)C;
+    g.eps = a.eps;
+    g.tid = tid;
+    g.warps = warps;
+    const bool last = g.last = 8 * (NV - 1) * threads + col < C;
+    // a thread's columns: c0 and, of NV = 2, c0 + step
+    const int c0 = min(col, C - 8), step = min(8 * threads + col, C - 8) - c0;
+    const int rows_txt = a.B * a.s[0].T, rows = rows_txt + a.B * a.s[1].T;
+    const int lo = (int)((long long)rows * blockIdx.x / gridDim.x);
+    const int hi = (int)((long long)rows * (blockIdx.x + 1) / gridDim.x);
+    constexpr uint32_t stage_bytes = kRow * PITCH;
+    const uint32_t ring = smem_u32(smem) + 16 * tid;
+    // the next row to copy: text rows of all samples, then image rows
+    int fill_row = lo;
+    const bool in_img = lo >= rows_txt;
+    const long long at0 = (long long)(lo - (in_img ? rows_txt : 0)) * C + c0;
+    const X* fx = static_cast<const X*>(a.s[in_img].x) + at0;
+    const Y* fh = static_cast<const Y*>(a.s[in_img].h) + at0;
+    auto fill = [&](uint32_t to) {
+        if (fill_row < hi) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = 8 * (j * blockDim.x + threadIdx.x);
-        act[j] = c < C;
-        if (act[j]) {
-            load8(x + c, v[j]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
-        }
-    }
-    if (GATE) {
-        float u[NV][8];
-        const Y* h = static_cast<const Y*>(st.h) + row * C;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = 8 * (j * blockDim.x + threadIdx.x);
-            if (act[j]) {
-                load8(h + c, u[j]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) u[j][i] = 0.0f;
+            for (int j = 0; j < NV; ++j) {
+                ring_fill<PITCH>(to + PITCH * (j * kPieces<X>), fx + j * step);
+                if (GATE) ring_fill<PITCH>(to + PITCH * (kX + j * kPieces<Y>), fh + j * step);
+            }
+            fx += C;
+            if (GATE) fh += C;
+            if (++fill_row == rows_txt) {
+                fx = static_cast<const X*>(a.s[1].x) + c0;
+                fh = static_cast<const Y*>(a.s[1].h) + c0;
             }
         }
-        float2 ps = make_float2(0.0f, 1.0f);
-        if (POST) {
-            ps = row_stats<NV>(u, act, a.post == RLK_NORM_RMS, C, a.eps, buf[1]);
-            if (threadIdx.x == 0 && st.post_stats != nullptr) reinterpret_cast<float2*>(st.post_stats)[row] = ps;
-        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < kFwdStages - 1; ++k) fill(ring + k * stage_bytes);
+    if (tid < 32) buf[tid / 16][tid % 16] = make_float2(0.0f, 0.0f);
+    __syncthreads();
+    uint32_t stage = 0, filled = (kFwdStages - 1) * stage_bytes;  // to read, to fill
+    int parity = 0;
+    for (int row = lo; row < hi;) {
+        const int img = row >= rows_txt, off = img ? rows_txt : 0;
+        const AdalnStream& st = a.s[img];
+        const int b = (row - off) / st.T, end = min(off + (b + 1) * st.T, hi);
+        V8 k[NV], sh[NV], ga[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = 8 * (j * blockDim.x + threadIdx.x);
-            if (!act[j]) continue;
-            float g[8], w[8];
-            load8_mod(st.gate, a.mod_fp32, b * a.mod_stride + c, 1.0f, g);
-            if (POST) load8_mod(st.w_post, true, c, 1.0f, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float t = u[j][i];
-                if (POST) t = (t - ps.x) * ps.y * w[i];
-                v[j][i] = fmaf(a.alpha * g[i], t, v[j][i]);
+            const int c = c0 + j * step;
+            const long long mod = b * a.mod_stride + c;
+            k[j] = load8_mod(st.w, true, c, 1.0f) * (v8_all(1.0f) + load8_mod(st.scale, a.mod_fp32, mod, 0.0f));
+            sh[j] = load8_mod(st.shift, a.mod_fp32, mod, 0.0f);
+            if (GATE) {
+                ga[j] = v8_all(a.alpha) * load8_mod(st.gate, a.mod_fp32, mod, 1.0f);
+                if (POST) ga[j] = ga[j] * load8_mod(st.w_post, true, c, 1.0f);
             }
-            store8(static_cast<X*>(st.r) + row * C + c, v[j]);
         }
-        if (st.y == nullptr) return;
-    }
-    const float2 ms = row_stats<NV>(v, act, a.norm == RLK_NORM_RMS, C, a.eps, buf[0]);
-    if (threadIdx.x == 0 && st.stats != nullptr) reinterpret_cast<float2*>(st.stats)[row] = ms;
+        const long long first = (long long)(row - off) * C + c0;
+        X* rp = static_cast<X*>(st.r) + first;
+        Y* yp = static_cast<Y*>(st.y) + first;
+        float2* stats = reinterpret_cast<float2*>(st.stats) + (row - off);
+        float2* post_stats = reinterpret_cast<float2*>(st.post_stats) + (row - off);
+        const bool want_y = !GATE || st.y != nullptr;
+        const bool want_stats = tid == 0 && st.stats != nullptr;
+        const bool want_post = POST && tid == 0 && st.post_stats != nullptr;
+        for (; row < end; ++row, rp += C, yp += C, ++stats, ++post_stats) {
+            fill(ring + filled);
+            filled = stage;
+            copies_wait<kFwdStages - 1>();
+            const uint8_t* const at = smem + 16 * tid + stage;
+            stage = stage == (kFwdStages - 1) * stage_bytes ? 0 : stage + stage_bytes;
+            V8 v[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = 8 * (j * blockDim.x + threadIdx.x);
-        if (!act[j]) continue;
-        float w[8], sc[8], sh[8];
-        load8_mod(st.w, true, c, 1.0f, w);
-        load8_mod(st.scale, a.mod_fp32, b * a.mod_stride + c, 0.0f, sc);
-        load8_mod(st.shift, a.mod_fp32, b * a.mod_stride + c, 0.0f, sh);
+            for (int j = 0; j < NV; ++j) v[j] = ring_read<PITCH>(at + PITCH * (j * kPieces<X>), (const X*)nullptr);
+            if (GATE) {
+                V8 u[NV];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = fmaf((v[j][i] - ms.x) * ms.y, w[i] * (1.0f + sc[i]), sh[i]);
-        store8(static_cast<Y*>(st.y) + row * C + c, v[j]);
+                for (int j = 0; j < NV; ++j)
+                    u[j] = ring_read<PITCH>(at + PITCH * (kX + j * kPieces<Y>), (const Y*)nullptr);
+                if (POST) {
+                    const float2 ps = row_stats<NV>(u, post_rms, g, buf[parity]);
+                    parity ^= 1;
+                    if (want_post) *post_stats = ps;
+                    const V8 m = v8_all(ps.x), s = v8_all(ps.y);
+#pragma unroll
+                    for (int j = 0; j < NV; ++j) u[j] = (u[j] - m) * s;
+                }
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    v[j] = store8(rp + j * step, fma8(u[j], ga[j], v[j]), j + 1 < NV || last);
+                if (!want_y) continue;
+            }
+            const float2 ms = row_stats<NV>(v, rms, g, buf[parity]);
+            parity ^= 1;
+            if (want_stats) *stats = ms;
+            const V8 m = v8_all(ms.x), s = v8_all(ms.y);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) store8(yp + j * step, fma8((v[j] - m) * s, k[j], sh[j]), j + 1 < NV || last);
+        }
     }
+    copies_wait<0>();
 }
 
 // ------------------------------------------------------------ backward
-// One CTA per chunk of one (stream, sample)'s token rows, rows ascending. A
-// thread owns its columns through the chunk and adds up A = sum dy * hat,
-// S = sum dy and G = sum d * hat(h) (or d * h) in registers; the chunk's sums
-// go to the workspace, where adaln_fold_kernel adds the chunks in order.
-template <typename X, typename Y, int NV, bool GATE, bool POST>
-__global__ void __launch_bounds__(kMaxThreads) adaln_bwd_kernel(const __grid_constant__ AdalnArgs a) {
-    __shared__ float2 buf[4][kMaxWarps];
-    const int chunks_txt = a.B * a.s[0].chunks;
-    const int img = (int)blockIdx.x >= chunks_txt;
-    const AdalnStream& st = a.s[img];
-    const int chunk = (int)blockIdx.x - (img ? chunks_txt : 0);
-    const int b = chunk / st.chunks, t0 = (chunk - b * st.chunks) * st.chunk_rows;
-    const int t1 = min(t0 + st.chunk_rows, st.T), C = a.C;
+// The rows of each (stream, sample) come in chunks; CTA i takes the chunks that
+// begin in the rows [i, i + 1) / grid of all. Their rows follow one another, so
+// the ring runs on from chunk to chunk. A thread owns its columns and adds up A = sum
+// dy * hat, S = sum dy and G = sum d * hat(h) (or d * h) in registers; a
+// chunk's sums go to the workspace, where adaln_fold_kernel adds the chunks in
+// order.
+template <typename X, typename Y, bool GATE>
+constexpr int kBwdRow = 2 * kPieces<X> + (GATE ? 2 : 1) * kPieces<Y>;  // pieces of 8 columns: x, dr, dy, h
+// CTAs of an SM that the registers are held to (96 a thread up to 320 of
+// them; 64 and three CTAs left the 1024^2 modulation as it was, 42 us).
+template <int NV, int THREADS>
+constexpr int kBwdCtas = NV == 2 ? 1 : 680 / THREADS;
+// Stages: four, or as many as let that many CTAs share the shared memory.
+template <typename X, typename Y, int NV, int THREADS, bool GATE>
+constexpr int kBwdFit = 220 * 1024 / kBwdCtas<NV, THREADS> / (16 * THREADS * NV * kBwdRow<X, Y, GATE>);
+template <typename X, typename Y, int NV, int THREADS, bool GATE>
+constexpr int kBwdStages = kBwdFit<X, Y, NV, THREADS, GATE> >= 4
+                               ? 4
+                               : (kBwdFit<X, Y, NV, THREADS, GATE> >= 1 ? kBwdFit<X, Y, NV, THREADS, GATE> : 1);
+
+template <typename X, typename Y, int NV, int THREADS, bool GATE, bool POST>
+__global__ void __launch_bounds__(THREADS, kBwdCtas<NV, THREADS>) adaln_bwd_kernel(const __grid_constant__ AdalnArgs a) {
+    constexpr int STAGES = kBwdStages<X, Y, NV, THREADS, GATE>, PITCH = 16 * THREADS;
+    constexpr int kX = NV * kPieces<X>, kY = NV * kPieces<Y>;
+    constexpr int kDr = kX, kDy = 2 * kX, kH = 2 * kX + kY;  // a row's pieces: x, dr, dy, h
+    constexpr int kRow = 2 * kX + kY + (GATE ? kY : 0);
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float buf[2][32];
+    const int tid = kept((int)threadIdx.x), threads = blockDim.x, C = kept(a.C), warps = kept(threads / 32);
+    const int col = 8 * tid;
+    const int units_txt = a.B * a.s[0].chunks, units = units_txt + a.B * a.s[1].chunks;
+    const int rows_txt = a.B * a.s[0].T, rows = rows_txt + a.B * a.s[1].T;
+    // the first chunk that begins at row i / grid of all rows or after it, and that chunk's first row
+    auto share = [&](unsigned i, int& unit, int& row) {
+        const int at = (int)((long long)rows * i / gridDim.x), img = at >= rows_txt, off = img ? rows_txt : 0;
+        const AdalnStream& st = a.s[img];
+        const int T = max(st.T, 1), b = (at - off) / T, j = (at - off - b * T + st.chunk_rows - 1) / st.chunk_rows;
+        unit = (img ? units_txt : 0) + b * st.chunks + j;
+        row = off + b * T + min(j * st.chunk_rows, T);
+    };
+    int lo, hi, row_lo, row_hi;
+    share(blockIdx.x, lo, row_lo);
+    share(blockIdx.x + 1, hi, row_hi);
+    if (blockIdx.x + 1 == gridDim.x) hi = units, row_hi = rows;
     const float inv_c = 1.0f / (float)C;
-    bool act[NV];
-    float sum_a[NV][8], sum_s[NV][8], sum_g[NV][8], k[NV][8], kg[NV][8], wp[NV][8];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = 8 * (j * blockDim.x + threadIdx.x);
-        act[j] = c < C;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum_a[j][i] = sum_s[j][i] = sum_g[j][i] = k[j][i] = kg[j][i] = wp[j][i] = 0.0f;
-        if (!act[j]) continue;
-        float w[8], sc[8];
-        load8_mod(st.w, true, c, 1.0f, w);
-        load8_mod(st.scale, a.mod_fp32, b * a.mod_stride + c, 0.0f, sc);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) k[j][i] = w[i] * (1.0f + sc[i]);
-        if (GATE) {
-            load8_mod(st.gate, a.mod_fp32, b * a.mod_stride + c, 1.0f, kg[j]);
-            if (POST) load8_mod(st.w_post, true, c, 1.0f, wp[j]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) kg[j][i] *= a.alpha;
-        }
-    }
-    for (int t = t0; t < t1; ++t) {
-        const long long row = (long long)b * st.T + t, at = row * C;
-        const int par = (t & 1) * 2;
-        float d[NV][8], hat[NV][8], e[NV][8];
-        float rstd = 0.0f;
-        if (st.dy != nullptr) {
-            const float2 ms = reinterpret_cast<const float2*>(st.stats)[row];
-            rstd = ms.y;
-            float s1 = 0.0f, s2 = 0.0f;
+    const bool rms = a.norm == RLK_NORM_RMS, post_rms = a.post == RLK_NORM_RMS;
+    const bool last = 8 * (NV - 1) * threads + col < C;
+    // a thread's columns: c0 and, of NV = 2, c0 + step
+    const int c0 = min(col, C - 8), step = min(8 * threads + col, C - 8) - c0;
+    constexpr uint32_t stage_bytes = kRow * PITCH;
+    const uint32_t ring = smem_u32(smem) + 16 * tid;
+    // the next row to copy
+    int fill_row = row_lo;
+    const X *fx, *fdr;
+    const Y *fdy, *fh;
+    bool copy_dy, copy_dr;
+    auto fill_from = [&](const AdalnStream& st, long long at) {
+        fx = static_cast<const X*>(st.x) + at;
+        fdr = static_cast<const X*>(st.dr) + at;
+        fdy = static_cast<const Y*>(st.dy) + at;
+        fh = static_cast<const Y*>(st.h) + at;
+        copy_dy = st.dy != nullptr;
+        copy_dr = st.dr != nullptr;
+    };
+    fill_from(a.s[row_lo >= rows_txt], (long long)(row_lo - (row_lo >= rows_txt ? rows_txt : 0)) * C + c0);
+    auto fill = [&](uint32_t to) {
+        if (fill_row < row_hi) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int c = 8 * (j * blockDim.x + threadIdx.x);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) hat[j][i] = e[j][i] = 0.0f;
-                if (!act[j]) continue;
-                load8(static_cast<const X*>(st.x) + at + c, hat[j]);
-                load8(static_cast<const Y*>(st.dy) + at + c, e[j]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float z = (hat[j][i] - ms.x) * ms.y, dy = e[j][i];
-                    sum_a[j][i] = fmaf(dy, z, sum_a[j][i]);
-                    sum_s[j][i] += dy;
-                    hat[j][i] = z;
-                    e[j][i] = dy * k[j][i];
-                    s1 += e[j][i];
-                    s2 = fmaf(e[j][i], z, s2);
+                if (copy_dy) {
+                    ring_fill<PITCH>(to + PITCH * (j * kPieces<X>), fx + j * step);
+                    ring_fill<PITCH>(to + PITCH * (kDy + j * kPieces<Y>), fdy + j * step);
                 }
+                if (copy_dr) ring_fill<PITCH>(to + PITCH * (kDr + j * kPieces<X>), fdr + j * step);
+                if (GATE) ring_fill<PITCH>(to + PITCH * (kH + j * kPieces<Y>), fh + j * step);
             }
-            float2 c12 = block_sum2(s1, s2, buf[par]);
-            const float c1 = a.norm == RLK_NORM_RMS ? 0.0f : c12.x * inv_c, c2 = c12.y * inv_c;
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) d[j][i] = rstd * (e[j][i] - c1 - hat[j][i] * c2);
-        } else {
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) d[j][i] = 0.0f;
+            fx += C;
+            fdr += C;
+            fdy += C;
+            if (GATE) fh += C;
+            if (++fill_row == rows_txt) fill_from(a.s[1], c0);
         }
+        copies_commit();
+    };
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = 8 * (j * blockDim.x + threadIdx.x);
-            if (!act[j]) continue;
-            if (st.dr != nullptr) {
-                float dr[8];
-                load8(static_cast<const X*>(st.dr) + at + c, dr);
+    for (int k = 0; k < STAGES - 1; ++k) fill(ring + k * stage_bytes);
+    if (tid < 32) buf[0][tid] = buf[1][tid] = 0.0f;
+    __syncthreads();
+    V8 sum_a[NV], sum_s[NV], sum_g[NV], k[NV], kg[NV];
+    uint32_t stage = 0, filled = (STAGES - 1) * stage_bytes;  // to read, to fill
+    int parity = 0, row = row_lo, sample = -1;
+    for (int unit = lo; unit < hi; ++unit) {  // (none, if the CTA's rows lie inside one chunk)
+        const int img = unit >= units_txt, v = unit - (img ? units_txt : 0);
+        const AdalnStream& st = a.s[img];
+        const bool has_dy = st.dy != nullptr, has_dr = st.dr != nullptr;
+        const int b = v / st.chunks, t0 = (v - b * st.chunks) * st.chunk_rows;
+        if (sample != img * a.B + b) {
+            sample = img * a.B + b;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) d[j][i] += dr[i];
-            }
-            float o[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = d[j][i];
-            store8(static_cast<X*>(st.dx) + at + c, o);
-        }
-        if (!GATE) continue;
-        float2 ps = make_float2(0.0f, 1.0f);
-        if (POST) ps = reinterpret_cast<const float2*>(st.post_stats)[row];
-        float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = 8 * (j * blockDim.x + threadIdx.x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) hat[j][i] = e[j][i] = 0.0f;
-            if (!act[j]) continue;
-            load8(static_cast<const Y*>(st.h) + at + c, hat[j]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float z = POST ? (hat[j][i] - ps.x) * ps.y : hat[j][i];
-                sum_g[j][i] = fmaf(d[j][i], z, sum_g[j][i]);
-                hat[j][i] = z;
-                e[j][i] = d[j][i] * kg[j][i];
-                if (POST) {
-                    e[j][i] *= wp[j][i];
-                    s1 += e[j][i];
-                    s2 = fmaf(e[j][i], z, s2);
+            for (int j = 0; j < NV; ++j) {
+                const int c = c0 + j * step;
+                const long long mod = b * a.mod_stride + c;
+                k[j] = load8_mod(st.w, true, c, 1.0f) * (v8_all(1.0f) + load8_mod(st.scale, a.mod_fp32, mod, 0.0f));
+                if (GATE) {
+                    kg[j] = v8_all(a.alpha) * load8_mod(st.gate, a.mod_fp32, mod, 1.0f);
+                    if (POST) kg[j] = kg[j] * load8_mod(st.w_post, true, c, 1.0f);
                 }
             }
         }
-        if (POST) {
-            const float2 c12 = block_sum2(s1, s2, buf[par + 1]);
-            const float c1 = a.post == RLK_NORM_RMS ? 0.0f : c12.x * inv_c, c2 = c12.y * inv_c;
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) sum_a[j] = sum_s[j] = sum_g[j] = v8_all(0.0f);
+        const int n = min(st.chunk_rows, st.T - t0), local = row - (img ? rows_txt : 0);
+        X* dx = static_cast<X*>(st.dx) + (long long)local * C + c0;
+        Y* dh = static_cast<Y*>(st.dh) + (long long)local * C + c0;
+        // statistics are read a row ahead
+        const float2* stats = reinterpret_cast<const float2*>(st.stats) + local;
+        const float2* post_stats = reinterpret_cast<const float2*>(st.post_stats) + local;
+        float2 next_ms = make_float2(0.0f, 0.0f), next_ps = next_ms;
+        if (has_dy) next_ms = *stats;
+        if (POST) next_ps = *post_stats;
+        for (int t = 0; t < n; ++t, dx += C, dh += C) {
+            fill(ring + filled);
+            filled = stage;
+            const float2 ms = next_ms, ps = next_ps;
+            if (t + 1 < n) {
+                if (has_dy) next_ms = *++stats;
+                if (POST) next_ps = *++post_stats;
+            }
+            copies_wait<STAGES - 1>();
+            const uint8_t* const at = smem + 16 * tid + stage;
+            stage = stage == (STAGES - 1) * stage_bytes ? 0 : stage + stage_bytes;
+            V8 d[NV], hat[NV];
+            if (has_dy) {
+                const V8 m = v8_all(ms.x), s = v8_all(ms.y);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) e[j][i] = ps.y * (e[j][i] - c1 - hat[j][i] * c2);
+                for (int j = 0; j < NV; ++j) {
+                    const V8 dy = ring_read<PITCH>(at + PITCH * (kDy + j * kPieces<Y>), (const Y*)nullptr);
+                    hat[j] = (ring_read<PITCH>(at + PITCH * (j * kPieces<X>), (const X*)nullptr) - m) * s;
+                    sum_a[j] = fma8(dy, hat[j], sum_a[j]);
+                    sum_s[j] = sum_s[j] + dy;
+                    d[j] = dy * k[j];
+                }
+                const float s1 = thread_sum<NV>(last, [&](uint64_t& q, int j) { sum8(q, d[j]); });
+                const float s2 = thread_sum<NV>(last, [&](uint64_t& q, int j) { dot8(q, d[j], hat[j]); });
+                const float2 c12 = block_sum2(s1, s2, tid, warps, buf[parity]);
+                parity ^= 1;
+                // d = dr + rstd * (e - mean(e) - hat * mean(e * hat))
+                const V8 c1 = v8_all(rms ? 0.0f : -ms.y * (c12.x * inv_c)), c2 = v8_all(-ms.y * (c12.y * inv_c));
+#pragma unroll
+                for (int j = 0; j < NV; ++j) d[j] = fma8(d[j], s, fma8(hat[j], c2, c1));
+            } else {
+#pragma unroll
+                for (int j = 0; j < NV; ++j) d[j] = v8_all(0.0f);
+            }
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                if (has_dr) d[j] = d[j] + ring_read<PITCH>(at + PITCH * (kDr + j * kPieces<X>), (const X*)nullptr);
+                store8(dx + j * step, d[j], j + 1 < NV || last);
+            }
+            if (!GATE) continue;
+            const V8 m = v8_all(ps.x), s = v8_all(ps.y);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                hat[j] = ring_read<PITCH>(at + PITCH * (kH + j * kPieces<Y>), (const Y*)nullptr);
+                if (POST) hat[j] = (hat[j] - m) * s;
+                sum_g[j] = fma8(d[j], hat[j], sum_g[j]);
+                d[j] = d[j] * kg[j];
+                if (!POST) store8(dh + j * step, d[j], j + 1 < NV || last);
+            }
+            if (POST) {
+                const float s1 = thread_sum<NV>(last, [&](uint64_t& q, int j) { sum8(q, d[j]); });
+                const float s2 = thread_sum<NV>(last, [&](uint64_t& q, int j) { dot8(q, d[j], hat[j]); });
+                const float2 c12 = block_sum2(s1, s2, tid, warps, buf[parity]);
+                parity ^= 1;
+                const V8 c1 = v8_all(post_rms ? 0.0f : -ps.y * (c12.x * inv_c)), c2 = v8_all(-ps.y * (c12.y * inv_c));
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    store8(dh + j * step, fma8(d[j], s, fma8(hat[j], c2, c1)), j + 1 < NV || last);
+            }
         }
+        row += n;
+        float* const part = a.part + (long long)unit * 3 * C + c0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = 8 * (j * blockDim.x + threadIdx.x);
-            if (act[j]) store8(static_cast<Y*>(st.dh) + at + c, e[j]);
+            if (j + 1 == NV && !last) break;
+            store8(part + j * step, sum_a[j]);
+            store8(part + C + j * step, sum_s[j]);
+            if (GATE) store8(part + 2 * C + j * step, sum_g[j]);
         }
     }
-    float* part = a.part + (long long)blockIdx.x * 3 * C;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = 8 * (j * blockDim.x + threadIdx.x);
-        if (!act[j]) continue;
-        store8(part + c, sum_a[j]);
-        store8(part + C + c, sum_s[j]);
-        if (GATE) store8(part + 2 * C + c, sum_g[j]);
-    }
+    copies_wait<0>();
 }
 
-// Adds the chunks' column sums: 8 interleaved runs over a sample's chunks,
-// each ascending, then the runs in order; weights' gradients over the samples
-// ascending. blockIdx.y: (stream, which of A, S, G).
-constexpr int kFoldRuns = 8;
-__global__ void __launch_bounds__(32 * kFoldRuns) adaln_fold_kernel(const __grid_constant__ AdalnArgs a) {
-    __shared__ float run[kFoldRuns][32];
-    const int img = blockIdx.y / 3, which = blockIdx.y % 3;
+// Adds the chunks' column sums of one sample, stream and quantity (A, S or G;
+// blockIdx.y = 3 * stream + which, z = sample): a thread takes four columns of
+// every kFoldRuns-th chunk, the runs are added in order. Weights' gradients
+// need every sample's sum: it replaces the sample's first chunk's, which only
+// this CTA reads, for adaln_weight_kernel.
+constexpr int kFoldRuns = 16;
+constexpr int kFoldColumns = 64;  // of a CTA: 16 threads
+__global__ void __launch_bounds__(kFoldColumns / 4 * kFoldRuns) adaln_fold_kernel(const __grid_constant__ AdalnArgs a) {
+    __shared__ float4 run[kFoldRuns][kFoldColumns / 4];
+    const int img = blockIdx.y / 3, which = blockIdx.y % 3, b = blockIdx.z;
     const AdalnStream& st = a.s[img];
-    float* per_sample = which == 0 ? st.dscale : (which == 1 ? st.dshift : st.dgate);
-    float* total = which == 0 ? st.dw : (which == 1 ? nullptr : st.dw_post);
+    float* const per_sample = which == 0 ? st.dscale : (which == 1 ? st.dshift : st.dgate);
+    const float* const total = which == 0 ? st.dw : (which == 1 ? nullptr : st.dw_post);
     if (st.T == 0 || (per_sample == nullptr && total == nullptr)) return;
-    const int lane = threadIdx.x % 32, slice = threadIdx.x / 32;
-    const int c = blockIdx.x * 32 + lane, C = a.C;
-    const long long first = img ? (long long)a.B * a.s[0].chunks : 0;
-    const float* w = which == 0 ? st.w : (which == 1 ? nullptr : (a.post != RLK_NORM_NONE ? st.w_post : nullptr));
-    const float share = (w != nullptr && c < C ? w[c] : 1.0f) * (which == 2 ? a.alpha : 1.0f);
-    float sum = 0.0f;
-    for (int b = 0; b < a.B; ++b) {
-        float s = 0.0f;
-        if (c < C)
-            for (int j = slice; j < st.chunks; j += kFoldRuns)
-                s += a.part[((first + (long long)b * st.chunks + j) * 3 + which) * C + c];
-        run[slice][lane] = s;
-        __syncthreads();
-        if (slice == 0 && c < C) {
-            s = run[0][lane];
-            for (int k = 1; k < kFoldRuns; ++k) s += run[k][lane];
-            if (per_sample != nullptr) per_sample[b * a.dmod_stride + c] = share * s;
-            if (total != nullptr) {
-                float coef = which == 0 ? 1.0f : a.alpha;
-                const void* mod = which == 0 ? st.scale : st.gate;
-                const long long at = b * a.mod_stride + c;
-                float m = which == 0 ? 0.0f : 1.0f;
-                if (mod != nullptr)
-                    m = a.mod_fp32 ? static_cast<const float*>(mod)[at]
-                                   : bf16_lo(static_cast<const uint16_t*>(mod)[at]);
-                coef = which == 0 ? 1.0f + m : coef * m;
-                sum = fmaf(coef, s, sum);
-            }
+    const int lane = threadIdx.x % (kFoldColumns / 4), slice = threadIdx.x / (kFoldColumns / 4);
+    const int c = blockIdx.x * kFoldColumns + 4 * lane, C = a.C;
+    const long long first = (img ? (long long)a.B * a.s[0].chunks : 0) + (long long)b * st.chunks;
+    float* const part = a.part + (first * 3 + which) * C + c;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c < C)
+#pragma unroll 8
+        for (int j = slice; j < st.chunks; j += kFoldRuns) {
+            const float4 p = *reinterpret_cast<const float4*>(part + (long long)j * 3 * C);
+            s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
         }
-        __syncthreads();
+    run[slice][lane] = s;
+    __syncthreads();
+    if (slice > 0 || c >= C) return;
+#pragma unroll
+    for (int k = 1; k < kFoldRuns; ++k) {
+        const float4 p = run[k][lane];
+        s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
     }
-    if (slice == 0 && c < C && total != nullptr) total[c] = sum;
+    if (total != nullptr) *reinterpret_cast<float4*>(part) = s;
+    if (per_sample == nullptr) return;
+    float4 w = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    if (which == 0 && st.w != nullptr) w = *reinterpret_cast<const float4*>(st.w + c);
+    if (which == 2) {
+        if (a.post != RLK_NORM_NONE && st.w_post != nullptr) w = *reinterpret_cast<const float4*>(st.w_post + c);
+        w.x *= a.alpha, w.y *= a.alpha, w.z *= a.alpha, w.w *= a.alpha;
+    }
+    *reinterpret_cast<float4*>(per_sample + b * a.dmod_stride + c) =
+        make_float4(w.x * s.x, w.y * s.y, w.z * s.z, w.w * s.w);
 }
 
-int threads_of(int C, int* nv) {
-    const int groups = C / 8;
-    *nv = groups <= kMaxThreads ? 1 : 2;
-    return ((groups + *nv - 1) / *nv + 31) / 32 * 32;
+// dw = sum_b (1 + scale_b) * A_b and dw_post = alpha * sum_b gate_b * G_b, b
+// ascending. blockIdx.y = 2 * stream + (0: dw, 1: dw_post).
+__global__ void __launch_bounds__(128) adaln_weight_kernel(const __grid_constant__ AdalnArgs a) {
+    const int img = blockIdx.y / 2, post = blockIdx.y % 2;
+    const AdalnStream& st = a.s[img];
+    float* const total = post ? st.dw_post : st.dw;
+    const int c = blockIdx.x * 128 + threadIdx.x, C = a.C;
+    if (st.T == 0 || total == nullptr || c >= C) return;
+    const void* const mod = post ? st.gate : st.scale;
+    const float* part = a.part + ((img ? (long long)a.B * a.s[0].chunks : 0) * 3 + (post ? 2 : 0)) * C + c;
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int b = 0; b < a.B; ++b) {
+        const long long at = b * a.mod_stride + c;
+        float m = post ? 1.0f : 0.0f;
+        if (mod != nullptr)
+            m = a.mod_fp32 ? static_cast<const float*>(mod)[at] : bf16_lo(static_cast<const uint16_t*>(mod)[at]);
+        sum = fmaf(post ? a.alpha * m : 1.0f + m, part[(long long)b * st.chunks * 3 * C], sum);
+    }
+    total[c] = sum;
 }
 
+// CTAs of a kernel that the current GPU holds at once, with its dynamic
+// shared memory allowed; the last answer is kept, since one program's calls
+// mostly repeat a launch shape.
+struct Fit {
+    const void* kernel = nullptr;
+    int device = -1, threads = 0, smem = 0, ctas = 0;
+};
+cudaError_t fit(const void* kernel, int threads, int smem, int* ctas) {
+    static thread_local Fit last;
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (last.kernel != kernel || last.device != device || last.threads != threads || last.smem != smem) {
+        int sms = 0, per_sm = 0;
+        last.kernel = nullptr;
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
+        if (e != cudaSuccess) return e;
+        last = Fit{kernel, device, threads, smem, sms * (per_sm > 0 ? per_sm : 1)};
+    }
+    *ctas = last.ctas;
+    return cudaSuccess;
+}
+
+int threads_of(int C, int nv) { return ((C / 8 + nv - 1) / nv + 31) / 32 * 32; }
+
+template <typename X, typename Y, int NV, int THREADS, bool GATE, bool POST>
+cudaError_t fwd_launch(const AdalnArgs& a, cudaStream_t s) {
+    constexpr int kSmem = kFwdStages * 16 * NV * (kPieces<X> + (GATE ? kPieces<Y> : 0)) * THREADS;
+    const int threads = threads_of(a.C, NV);
+    const auto kernel = adaln_fwd_kernel<X, Y, NV, THREADS, GATE, POST>;
+    int ctas = 0;
+    const cudaError_t e = fit(reinterpret_cast<const void*>(kernel), threads, kSmem, &ctas);
+    if (e != cudaSuccess) return e;
+    const long long rows = (long long)a.B * ((long long)a.s[0].T + a.s[1].T);
+    kernel<<<(unsigned)(rows < ctas ? rows : ctas), threads, kSmem, s>>>(a);
+    return cudaGetLastError();
+}
+// 8 columns a thread up to C = 1024, else 16: half the warps join a row, and
+// more rows are under way on an SM (1024^2 modulation 21.2 us, 25.6 with 8).
 template <typename X, typename Y, bool GATE, bool POST>
 cudaError_t fwd_nv(const AdalnArgs& a, cudaStream_t s) {
-    int nv;
-    const int threads = threads_of(a.C, &nv);
-    const long long rows = (long long)a.B * ((long long)a.s[0].T + a.s[1].T);
-    if (nv == 1)
-        adaln_fwd_kernel<X, Y, 1, GATE, POST><<<(unsigned)rows, threads, 0, s>>>(a);
-    else
-        adaln_fwd_kernel<X, Y, 2, GATE, POST><<<(unsigned)rows, threads, 0, s>>>(a);
+    if (a.C <= 1024) return fwd_launch<X, Y, 1, 128, GATE, POST>(a, s);
+    if (a.C <= 2560) return fwd_launch<X, Y, 2, 160, GATE, POST>(a, s);
+    if (a.C <= 4096) return fwd_launch<X, Y, 2, 256, GATE, POST>(a, s);
+    return fwd_launch<X, Y, 2, 512, GATE, POST>(a, s);
+}
+
+template <typename X, typename Y, int NV, int THREADS, bool GATE, bool POST>
+cudaError_t bwd_launch(const AdalnArgs& a, cudaStream_t s) {
+    constexpr int kSmem =
+        kBwdStages<X, Y, NV, THREADS, GATE> * 16 * THREADS * NV * kBwdRow<X, Y, GATE>;
+    const auto kernel = adaln_bwd_kernel<X, Y, NV, THREADS, GATE, POST>;
+    const int threads = threads_of(a.C, NV);
+    int ctas = 0;
+    const cudaError_t e = fit(reinterpret_cast<const void*>(kernel), threads, kSmem, &ctas);
+    if (e != cudaSuccess) return e;
+    const long long units = (long long)a.B * (a.s[0].chunks + a.s[1].chunks);
+    kernel<<<(unsigned)(units < ctas ? units : ctas), threads, kSmem, s>>>(a);
     return cudaGetLastError();
 }
+// 8 columns a thread up to C = 4096: with 16 the sums and factors leave room
+// for one CTA an SM (1024^2 modulation 47 us for 51, the 1328^2 gate 175 for
+// 220). Built for three numbers of threads, which fix the registers' limit
+// and the ring's layout.
 template <typename X, typename Y, bool GATE, bool POST>
 cudaError_t bwd_nv(const AdalnArgs& a, cudaStream_t s) {
-    int nv;
-    const int threads = threads_of(a.C, &nv);
-    const long long chunks = (long long)a.B * (a.s[0].chunks + a.s[1].chunks);
-    if (nv == 1)
-        adaln_bwd_kernel<X, Y, 1, GATE, POST><<<(unsigned)chunks, threads, 0, s>>>(a);
-    else
-        adaln_bwd_kernel<X, Y, 2, GATE, POST><<<(unsigned)chunks, threads, 0, s>>>(a);
-    return cudaGetLastError();
+    if (a.C <= 1280) return bwd_launch<X, Y, 1, 160, GATE, POST>(a, s);
+    if (a.C <= 2560) return bwd_launch<X, Y, 1, 320, GATE, POST>(a, s);
+    if (a.C <= 4096) return bwd_launch<X, Y, 1, 512, GATE, POST>(a, s);
+    return bwd_launch<X, Y, 2, 512, GATE, POST>(a, s);
 }
 
 template <typename X, typename Y>
@@ -428,7 +706,11 @@ cudaError_t bwd_xy(const AdalnArgs& a, bool gate, cudaStream_t s) {
 
 }  // namespace
 
-int adaln_chunk_rows(int T) { return T >= 1024 ? 16 : (T >= 128 ? 8 : 4); }
+// Rows of a chunk, from T alone: long ones write and fold fewer sums (1328^2
+// gate, T = 6889: 160 us with 32 rows, 165 with 16, 180 with 8), short ones
+// spread few rows over the SMs (1024^2 modulation, T = 4096: 49, 42, 46 us; T =
+// 513: 16.3 us with 4 rows for 18.6 with 8).
+int adaln_chunk_rows(int T) { return T >= 4096 ? 16 : 4; }
 
 cudaError_t launch_adaln_fwd(const AdalnArgs& a, bool gate, cudaStream_t s) {
     timing_begin(kKAdalnFwd, s);
@@ -450,13 +732,21 @@ cudaError_t launch_adaln_bwd(const AdalnArgs& a, bool gate, cudaStream_t s) {
         e = a.y_fp32 ? bwd_xy<float, float>(a, gate, s) : bwd_xy<float, uint16_t>(a, gate, s);
     timing_end(kKAdalnBwd, s);
     if (e != cudaSuccess) return e;
-    bool any = false;
-    for (const AdalnStream& t : a.s) any = any || t.dgate || t.dscale || t.dshift || t.dw || t.dw_post;
-    if (!any) return cudaSuccess;
+    bool any = false, weights = false;
+    for (const AdalnStream& t : a.s) {
+        weights = weights || t.dw != nullptr || t.dw_post != nullptr;
+        any = any || t.dgate != nullptr || t.dscale != nullptr || t.dshift != nullptr;
+    }
+    if (!any && !weights) return cudaSuccess;
     timing_begin(kKAdalnFold, s);
-    adaln_fold_kernel<<<dim3((a.C + 31) / 32, 6), 32 * kFoldRuns, 0, s>>>(a);
+    adaln_fold_kernel<<<dim3((a.C + kFoldColumns - 1) / kFoldColumns, 6, a.B), kFoldColumns / 4 * kFoldRuns, 0, s>>>(a);
+    e = cudaGetLastError();
+    if (e == cudaSuccess && weights) {
+        adaln_weight_kernel<<<dim3((a.C + 127) / 128, 4), 128, 0, s>>>(a);
+        e = cudaGetLastError();
+    }
     timing_end(kKAdalnFold, s);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace rlk

@@ -260,7 +260,7 @@ struct AdalnStream {
     const void *dy, *dr;
     void *dx, *dh;
     float *dgate, *dscale, *dshift, *dw, *dw_post;
-    int T, chunks, chunk_rows;  // chunks of a sample, rows of a chunk
+    int T, chunks, chunk_rows;  // chunks of a sample in the backward, rows of a chunk
 };
 struct AdalnArgs {
     AdalnStream s[2];
