@@ -552,8 +552,8 @@ rlk_status rlk_adaln_gate_residual_bwd(const rlk_adaln_shape* shape, const rlk_a
  *   m = beta1 * m + (1 - beta1) * g';   v = beta2 * v + (1 - beta2) * g'^2
  *   p -= rate * weight_decay * p
  *        + rate / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
- * in fp32 with IEEE division and square root; m and v take each product and
- * sum rounded by itself.
+ * in fp32, quotient and square root within one unit in the last place; m and v
+ * take each product and sum rounded by itself.
  *
  * Parameters: fp32 (p, master NULL), or bf16 with an fp32 master: the master
  * is updated and p receives its bf16 rounding.
@@ -588,7 +588,7 @@ typedef struct rlk_adamw_tensor {
 } rlk_adamw_tensor;
 
 typedef struct rlk_adamw_args {
-    double lr, beta1, beta2, eps;  /* lr >= 0, 0 <= beta < 1, eps > 0 */
+    double lr, beta1, beta2, eps;  /* lr >= 0, 0 <= beta < 1, 2^-50 <= eps <= 1 */
     int64_t step;          /* 1 .. 2^31 - 1: this step's number */
     const float* lr_dev;   /* device, or NULL: read instead of lr */
     const int64_t* step_dev; /* device, or NULL: read instead of step (same range),

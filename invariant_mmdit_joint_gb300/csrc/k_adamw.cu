@@ -1,12 +1,17 @@
 // The optimiser step over a list of tensors: the gradients' global norm with
 // its clip factor, and AdamW with fp32 or blockwise 8-bit states (formulas and
-// the states' format: include/rlk_joint_attn.h). Elementwise and bound by HBM:
+// the states' format: include/rlk_joint_attn.h). Elementwise: the floor is HBM,
 // 28 bytes an element with fp32 states (p, g, m, v read; p, m, v written), 16
-// with 8-bit ones and bf16 gradients.
+// with 8-bit ones and bf16 gradients. Measured: 45 million elements, fp32
+// states, 193 us (6.5 TB/s, 0.96 of the copy bandwidth); 166 million, 8-bit
+// states, 483 us (5.5 TB/s, 0.81), there bound by the arithmetic pipes: 82
+// instructions an element (105 and 600 us with one element at a time, sqrtf
+// and the division, and nothing fetched ahead).
 //
 // The list travels as a kernel argument (up to kMaxTensors entries), so a call
 // copies nothing to the device and a captured graph holds its own list. A CTA
-// takes one chunk of one tensor, found by bisection in the chunk counts.
+// takes one chunk of one tensor, found by bisection in the chunk counts: 16384
+// elements (8-bit states: 530 us with 4096, 493 with 32768).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -15,19 +20,23 @@
 
 #include "rlk_device.cuh"
 #include "rlk_internal.h"
+#include "rlk_sm100.cuh"
 
 RLK_DEFINE_STRICT_PROBE(probe_adamw_tu)
 
 namespace rlk {
 namespace {
 
+using namespace sm100;
+
 constexpr int kMaxTensors = 256;
 constexpr int kThreads = 256;
 constexpr int kPerThread = 8;
 constexpr int kPass = kThreads * kPerThread;  // elements a CTA covers at once
-constexpr int kChunk = 2 * kPass;
+constexpr int kChunk = 8 * kPass;
+constexpr int kNormChunk = 8 * kPass;
 
-enum : uint32_t { kGradFp32 = 1, kMaster = 2, kEightBit = 4 };
+enum : uint32_t { kGradFp32 = 1, kHasMaster = 2, kEightBit = 4 };
 
 struct Entry {
     void* p;
@@ -43,12 +52,17 @@ struct Entry {
     uint32_t chunk0;  // chunks of the entries before this one
     uint32_t pad;
 };
+template <int N>
 struct List {
     int count;
-    Entry e[kMaxTensors];
+    Entry e[N];
 };
+// Lists of at most kFewTensors travel as a small argument (1.4 KB for 22: the
+// norm and step of twelve small tensors take 9.3 us for 10.7).
+constexpr int kFewTensors = 16;
 
-__device__ __forceinline__ int entry_of(const List& l, uint32_t chunk) {
+template <int N>
+__device__ __forceinline__ int entry_of(const List<N>& l, uint32_t chunk) {
     int lo = 0, hi = l.count;  // the last entry whose chunk0 <= chunk
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
@@ -61,8 +75,37 @@ __device__ __forceinline__ int entry_of(const List& l, uint32_t chunk) {
 }
 
 // ------------------------------------------------------------ 8 elements
-// `left` elements remain from p on; missing ones read as 0 and are not written.
-__device__ __forceinline__ void load8(const float* p, int left, float (&v)[8]) {
+// Eight elements as four pairs for the packed fp32 instructions. `left`
+// elements remain from p on; missing ones read as 0 and are not written.
+struct V8 {
+    uint64_t p[4];
+};
+__device__ __forceinline__ V8 pairs(const float (&v)[8]) {
+    return V8{{f2_pack(v[0], v[1]), f2_pack(v[2], v[3]), f2_pack(v[4], v[5]), f2_pack(v[6], v[7])}};
+}
+__device__ __forceinline__ void singles(const V8& q, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f2_unpack(q.p[i], v[2 * i], v[2 * i + 1]);
+}
+__device__ __forceinline__ V8 all8(float x) {
+    const uint64_t q = f2_pack(x, x);
+    return V8{{q, q, q, q}};
+}
+__device__ __forceinline__ V8 operator*(const V8& a, const V8& b) {
+    return V8{{mul_f2(a.p[0], b.p[0]), mul_f2(a.p[1], b.p[1]), mul_f2(a.p[2], b.p[2]), mul_f2(a.p[3], b.p[3])}};
+}
+__device__ __forceinline__ V8 operator+(const V8& a, const V8& b) {
+    return V8{{add_f2(a.p[0], b.p[0]), add_f2(a.p[1], b.p[1]), add_f2(a.p[2], b.p[2]), add_f2(a.p[3], b.p[3])}};
+}
+__device__ __forceinline__ V8 operator-(const V8& a, const V8& b) {
+    return V8{{sub_f2(a.p[0], b.p[0]), sub_f2(a.p[1], b.p[1]), sub_f2(a.p[2], b.p[2]), sub_f2(a.p[3], b.p[3])}};
+}
+__device__ __forceinline__ V8 fma8(const V8& a, const V8& b, const V8& c) {
+    return V8{{fma_f2(a.p[0], b.p[0], c.p[0]), fma_f2(a.p[1], b.p[1], c.p[1]), fma_f2(a.p[2], b.p[2], c.p[2]),
+               fma_f2(a.p[3], b.p[3], c.p[3])}};
+}
+__device__ __forceinline__ V8 load8(const float* p, int left) {
+    float v[8];
     if (left >= 8) {
         const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
@@ -70,8 +113,10 @@ __device__ __forceinline__ void load8(const float* p, int left, float (&v)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.0f;
     }
+    return pairs(v);
 }
-__device__ __forceinline__ void load8(const uint16_t* p, int left, float (&v)[8]) {
+__device__ __forceinline__ V8 load8(const uint16_t* p, int left) {
+    float v[8];
     if (left >= 8) {
         const uint4 q = *reinterpret_cast<const uint4*>(p);
         v[0] = bf16_lo(q.x), v[1] = bf16_hi(q.x), v[2] = bf16_lo(q.y), v[3] = bf16_hi(q.y);
@@ -80,8 +125,11 @@ __device__ __forceinline__ void load8(const uint16_t* p, int left, float (&v)[8]
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = i < left ? bf16_lo(p[i]) : 0.0f;
     }
+    return pairs(v);
 }
-__device__ __forceinline__ void store8(float* p, int left, const float (&v)[8]) {
+__device__ __forceinline__ void store8(float* p, int left, const V8& q) {
+    float v[8];
+    singles(q, v);
     if (left >= 8) {
         reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
         reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -91,7 +139,9 @@ __device__ __forceinline__ void store8(float* p, int left, const float (&v)[8]) 
             if (i < left) p[i] = v[i];
     }
 }
-__device__ __forceinline__ void store8(uint16_t* p, int left, const float (&v)[8]) {
+__device__ __forceinline__ void store8(uint16_t* p, int left, const V8& f) {
+    float v[8];
+    singles(f, v);
     const uint4 q =
         make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
     if (left >= 8) {
@@ -125,61 +175,84 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int left, uint2 q) {
 // ------------------------------------------------------------ 8-bit states
 // e4m3 codes times 2^(scale - 127); scale 0 (a fresh state) reads as 0 and
 // 255 as NaN, both by the multiplication itself.
-__device__ __forceinline__ void decode8(uint2 q, uint8_t scale, float (&v)[8]) {
-    const float f = __uint_as_float((uint32_t)scale << 23);
+__device__ __forceinline__ V8 decode8(uint2 q, uint32_t scale) {
     const uint32_t w[2] = {q.x, q.y};
+    V8 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const __half2_raw h =
             __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i % 2))), __NV_E4M3);
         const float2 t = __half22float2(__half2(h));
-        v[2 * i] = t.x * f;
-        v[2 * i + 1] = t.y * f;
+        v.p[i] = f2_pack(t.x, t.y);
     }
+    return v * all8(__uint_as_float(scale << 23));
 }
-// The 32-bit hash with the least bias of Wellons' prospector search.
-__device__ __forceinline__ uint32_t hash32(uint32_t x) {
+// The 32-bit hash "lowbias32" of Wellons' prospector search, but for its last
+// step: of x, the hash is x ^ (x >> 16), its upper half x >> 16.
+__device__ __forceinline__ uint32_t hash_open(uint32_t x) {
     x ^= x >> 16;
     x *= 0x7feb352du;
     x ^= x >> 15;
-    x *= 0x846ca68bu;
+    return x * 0x846ca68bu;
+}
+__device__ __forceinline__ uint32_t hash32(uint32_t x) {
+    x = hash_open(x);
     return x ^ (x >> 16);
+}
+// max(|a|, |b|, |c|) that keeps a NaN, and that of eight values
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float top8(const V8& q) {
+    float v[8];
+    singles(q, v);
+    return max_abs(max_abs(v[0], v[1], v[2]), max_abs(v[3], v[4], v[5]), max_abs(v[6], v[7], 0.0f));
 }
 // Four threads hold a block of 32. Its scale 2^(e - 8 - 127): e is the biased
 // exponent of the largest magnitude, one more where that is above 1.75 * 2^..
-// so that the largest code is at most 448. Below the smallest normal code
-// (2^-6) codes are 2^-9 apart, as the values of [2^-6, 2^-5) are: adding 2^-6
-// puts both ranges under one integer rounding. Adding the random bits below
-// the code's last bit and truncating rounds up with the remainder's share.
+// so that the largest code is at most 448. Adding random bits (rnd, 16 of
+// them in bits 4 .. 19 and half a unit below) under a code's last bit and
+// clearing what lies under it rounds up with the remainder's share. Below the
+// smallest normal code (2^-6) codes are 2^-9 apart, as the values of [2^-6,
+// 2^-5) are: 2^-6 is added before and taken off after. What is left is a value
+// that has a code, so that the conversion does not round again.
 template <bool POSITIVE>
-__device__ __forceinline__ uint2 encode8(const float (&v)[8], const uint32_t (&rnd)[8], uint8_t& scale) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    if (top >= 0x7f800000u) {
-        scale = 255;
-        return make_uint2(0, 0);
-    }
+__device__ __forceinline__ uint2 encode8(const V8& q, float t, const uint32_t (&rnd)[8], uint32_t& scale) {
+    float v[8];
+    singles(q, v);
+    t = max_abs(t, __shfl_xor_sync(0xffffffffu, t, 1), 0.0f);
+    t = max_abs(t, __shfl_xor_sync(0xffffffffu, t, 2), 0.0f);
+    const uint32_t top = __float_as_uint(t);
     const uint32_t e = max((top + 0x1fffffu) >> 23, 32u);
-    scale = (uint8_t)(e - 8);
-    const float f = __uint_as_float((262u - e) << 23);
-    uint32_t w[2] = {0, 0};
+    const bool finite = top < 0x7f800000u;
+    scale = finite ? e - 8 : 255u;
+    float y[8], c[8];
+    singles(q * all8(__uint_as_float((262u - e) << 23)), y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = fabsf(y[i]) < 0.015625f ? 0.015625f : 0.0f;
+    if (!POSITIVE)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = fabsf(y[i]);
+    float s[8];
+    singles(pairs(y) + pairs(c), s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = __uint_as_float((__float_as_uint(s[i]) + rnd[i]) & 0xfff00000u);
+    singles(pairs(s) - pairs(c), s);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float y = fabsf(v[i]) * f;
-        const bool small = y < 0.015625f;
-        const uint32_t bits = __float_as_uint(small ? y + 0.015625f : y);
-        uint32_t code = ((bits + ((rnd[i] << 4) | 8u)) >> 20) - (small ? 968u : 960u);
-        if (POSITIVE) {
-            if (v[i] > 0.0f) code = max(code, 1u);
-        } else {
-            code |= (__float_as_uint(v[i]) >> 24) & 0x80u;
-        }
-        w[i / 4] |= code << (8 * (i % 4));
+        if (POSITIVE)
+            s[i] = v[i] > 0.0f ? fmaxf(s[i], 0.001953125f) : s[i];
+        else
+            s[i] = __uint_as_float(__float_as_uint(s[i]) | (__float_as_uint(v[i]) & 0x80000000u));
     }
-    return make_uint2(w[0], w[1]);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(s[2 * i], s[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+    const uint2 codes = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+    return finite ? codes : make_uint2(0, 0);
 }
 
 // ------------------------------------------------------------ AdamW
@@ -187,60 +260,191 @@ struct Scalars {
     float s, b1, b2, o1, o2, inv_c2, eps, step, decay;  // step = rate / (1 - beta1^t); decay = rate * weight decay
 };
 
-template <bool G32, bool MASTER, bool Q8>
-__device__ __forceinline__ void adamw_chunk(const Entry& e, const Scalars& k, long long i0, uint32_t base) {
+// m / (sqrt(v) * c + eps), each of the two within one unit in the last place:
+// for eight elements at once, Newton's step for the square root from the
+// hardware's estimate of 1 / sqrt, and Markstein's for the quotient (q + r /
+// d, r = m - d q by one fma) from its estimate of 1 / d. Written out, because
+// the compiler's square root and division each carry a branch an element for
+// operands that cannot occur here (they were a quarter of the 8-bit step's
+// instructions). v is scaled by 2^40, so that subnormal values become normal
+// ones, and kept from 0 by 2^-124, which is 2^-82 in sqrt(v): at most 2^-27 of
+// eps >= 2^-50 for c <= 32. v >= 2^86 and NaN (top, the largest) take sqrtf
+// and the division.
+__device__ __forceinline__ V8 quotient8(const V8& m, const V8& v, float top, float c, float eps) {
+    if (!(top < 7.7371252e25f)) {
+        float mi[8], u[8];
+        singles(m, mi);
+        singles(v, u);
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) u[i] = mi[i] / fmaf(sqrtf(u[i]), c, eps);
+        return pairs(u);
+    }
+    const V8 x = fma8(v, all8(1099511627776.0f), all8(4.7019774e-38f));
+    float t[8];
+    singles(x, t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(t[i]));
+    const V8 r = pairs(t), s = x * r, ns = x * (r * all8(-1.0f));
+    const V8 root = fma8(fma8(ns, s, x), r * all8(0.5f), s);
+    const float c20 = c * 9.5367431640625e-7f;  // 2^-20
+    const V8 d = fma8(root, all8(c20), all8(eps)), nd = fma8(root, all8(-c20), all8(-eps));
+    singles(d, t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(t[i]));
+    const V8 y = pairs(t), q = m * y;
+    return fma8(fma8(nd, q, m), y, q);
+}
+
+// New m, v and p of 8 elements from g (unscaled), and the largest v (NaN if
+// one is). m and v take each product and sum rounded by itself: the 8-bit
+// codes follow from these bits.
+__device__ __forceinline__ float update8(const Scalars& k, const V8& grad, V8& m, V8& v, V8& p) {
+    const V8 g = grad * all8(k.s);
+    m = all8(k.b1) * m + all8(k.o1) * g;
+    v = all8(k.b2) * v + (all8(k.o2) * g) * g;
+    const float top = top8(v);
+    p = p - fma8(all8(k.decay), p, all8(k.step) * quotient8(m, v, top, k.inv_c2, k.eps));
+    return top;
+}
+template <bool G32>
+__device__ __forceinline__ V8 load_grad(const Entry& e, long long at, int left) {
+    return G32 ? load8(static_cast<const float*>(e.g) + at, left) : load8(static_cast<const uint16_t*>(e.g) + at, left);
+}
+
+// One chunk with fp32 states: 28 bytes an element, and enough loads of a
+// thread at once that nothing need be fetched ahead.
+template <bool G32, bool MASTER>
+__device__ __forceinline__ void adamw_chunk32(const Entry& e, const Scalars& k, long long i0) {
+    float* const master = MASTER ? e.master : static_cast<float*>(e.p);
 #pragma unroll 1
     for (int j = 0; j < kChunk / kPass; ++j) {
         const long long at = i0 + j * kPass + threadIdx.x * kPerThread;
-        if (i0 + j * kPass >= e.n) return;  // the same for the whole CTA
         const int left = (int)min(max(e.n - at, 0LL), 8LL);
-        float g[8], p[8], m[8], v[8];
-        float* const master = MASTER ? e.master : static_cast<float*>(e.p);
-        if (G32)
-            load8(static_cast<const float*>(e.g) + at, left, g);
-        else
-            load8(static_cast<const uint16_t*>(e.g) + at, left, g);
-        load8(master + at, left, p);
-        if (Q8) {
-            const uint2 mq = load_codes(static_cast<const uint8_t*>(e.m) + at, left);
-            const uint2 vq = load_codes(static_cast<const uint8_t*>(e.v) + at, left);
-            decode8(mq, left > 0 ? e.ms[at / 32] : 0, m);
-            decode8(vq, left > 0 ? e.vs[at / 32] : 0, v);
-        } else {
-            load8(static_cast<const float*>(e.m) + at, left, m);
-            load8(static_cast<const float*>(e.v) + at, left, v);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float gs = __fmul_rn(g[i], k.s);
-            m[i] = __fadd_rn(__fmul_rn(k.b1, m[i]), __fmul_rn(k.o1, gs));
-            v[i] = __fadd_rn(__fmul_rn(k.b2, v[i]), __fmul_rn(__fmul_rn(k.o2, gs), gs));
-            const float u = m[i] / fmaf(sqrtf(v[i]), k.inv_c2, k.eps);
-            p[i] -= fmaf(k.decay, p[i], k.step * u);
-        }
+        if (left == 0) return;
+        const V8 g = load_grad<G32>(e, at, left);
+        V8 p = load8(master + at, left), m = load8(static_cast<const float*>(e.m) + at, left),
+           v = load8(static_cast<const float*>(e.v) + at, left);
+        update8(k, g, m, v, p);
         store8(master + at, left, p);
         if (MASTER) store8(static_cast<uint16_t*>(e.p) + at, left, p);
-        if (Q8) {
-            uint32_t lo[8], hi[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t r = hash32((uint32_t)(at + i) * 0x9e3779b9u + base);
-                lo[i] = r & 0xffffu;
-                hi[i] = r >> 16;
-            }  // (past the end m and v are 0)
-            uint8_t ms, vs;
-            const uint2 mq = encode8<false>(m, lo, ms), vq = encode8<true>(v, hi, vs);
-            store_codes(static_cast<uint8_t*>(e.m) + at, left, mq);
-            store_codes(static_cast<uint8_t*>(e.v) + at, left, vq);
-            if (threadIdx.x % 4 == 0 && left > 0) {
-                e.ms[at / 32] = ms;
-                e.vs[at / 32] = vs;
+        store8(static_cast<float*>(e.m) + at, left, m);
+        store8(static_cast<float*>(e.v) + at, left, v);
+    }
+}
+
+// One chunk with 8-bit states. Its work an element is several times that of
+// fp32 states, so the next passes' elements are copied ahead into shared
+// memory meanwhile; a thread copies and reads its own bytes only, which needs
+// no barrier. Piece k of all threads is consecutive in a stage.
+constexpr int kRingBytes = 48 * 1024;  // four CTAs an SM
+template <bool G32>
+constexpr int kStageBytes = kThreads * (16 * (G32 ? 4 : 3) + 16);  // g and master in 16 bytes, the codes in 8 each
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(to), "l"(from) : "memory");
+}
+template <bool G32, bool MASTER>
+__device__ __forceinline__ void adamw_chunk8(const Entry& e, const Scalars& k, long long i0, uint32_t base,
+                                             uint8_t* smem) {
+    constexpr int kMaster = G32 ? 2 : 1, kCodes = kMaster + 2;  // pieces before the master and the codes
+    constexpr int kPasses = kChunk / kPass, kStep = 16 * kThreads, kStages = kRingBytes / kStageBytes<G32>;  // 3, or 2
+    float* const master = MASTER ? e.master : static_cast<float*>(e.p);
+    const uint8_t* const mc = static_cast<const uint8_t*>(e.m);
+    const uint8_t* const vc = static_cast<const uint8_t*>(e.v);
+    const uint32_t ring = smem_u32(smem);
+    long long at = i0 + threadIdx.x * kPerThread;
+    auto fill = [&](int j, uint32_t stage) {
+        const long long i = at + (long long)j * kPass;
+        if (j < kPasses && i + 8 <= e.n) {  // (the last elements of a tensor are loaded one by one when their turn comes)
+            const uint32_t to = ring + stage + 16 * threadIdx.x;
+            if (G32) {
+                copy16(to, static_cast<const float*>(e.g) + i);
+                copy16(to + kStep, static_cast<const float*>(e.g) + i + 4);
+            } else {
+                copy16(to, static_cast<const uint16_t*>(e.g) + i);
             }
+            copy16(to + kMaster * kStep, master + i);
+            copy16(to + (kMaster + 1) * kStep, master + i + 4);
+            const uint32_t codes = ring + stage + kCodes * kStep + 8 * threadIdx.x;
+            copy8(codes, mc + i);
+            copy8(codes + 8 * kThreads, vc + i);
+        }
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
+    };
+    uint32_t next_ms = 0, next_vs = 0;
+    auto read_scales = [&](int j) {
+        const long long i = at + (long long)j * kPass;
+        if (j < kPasses && i < e.n) {
+            next_ms = e.ms[i / 32];
+            next_vs = e.vs[i / 32];
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < kStages - 1; ++j) fill(j, j * kStageBytes<G32>);
+    read_scales(0);
+    uint32_t stage = 0, filled = (kStages - 1) * kStageBytes<G32>;  // to read, to fill
+#pragma unroll 1
+    for (int j = 0; j < kPasses; ++j) {
+        if (i0 + j * kPass >= e.n) break;  // the same for the whole CTA
+        fill(j + kStages - 1, filled);
+        const uint8_t* const ready = smem + stage;
+        filled = stage;
+        stage = stage == (kStages - 1) * kStageBytes<G32> ? 0 : stage + kStageBytes<G32>;
+        const uint32_t old_ms = next_ms, old_vs = next_vs;
+        read_scales(j + 1);
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 1) : "memory");
+        const long long i = at + (long long)j * kPass;
+        const int left = (int)min(max(e.n - i, 0LL), 8LL);
+        V8 g, p;
+        uint2 mq, vq;
+        if (left == 8) {
+            const uint8_t* const from = ready + 16 * threadIdx.x;
+            float t[8];
+            if (G32) {
+                *reinterpret_cast<float4*>(t) = *reinterpret_cast<const float4*>(from);
+                *reinterpret_cast<float4*>(t + 4) = *reinterpret_cast<const float4*>(from + kStep);
+                g = pairs(t);
+            } else {
+                g = load8(reinterpret_cast<const uint16_t*>(from), 8);
+            }
+            *reinterpret_cast<float4*>(t) = *reinterpret_cast<const float4*>(from + kMaster * kStep);
+            *reinterpret_cast<float4*>(t + 4) = *reinterpret_cast<const float4*>(from + (kMaster + 1) * kStep);
+            p = pairs(t);
+            const uint8_t* const codes = ready + kCodes * kStep + 8 * threadIdx.x;
+            mq = *reinterpret_cast<const uint2*>(codes);
+            vq = *reinterpret_cast<const uint2*>(codes + 8 * kThreads);
         } else {
-            store8(static_cast<float*>(e.m) + at, left, m);
-            store8(static_cast<float*>(e.v) + at, left, v);
+            g = load_grad<G32>(e, i, left);
+            p = load8(master + i, left);
+            mq = load_codes(mc + i, left);
+            vq = load_codes(vc + i, left);
+        }
+        V8 m = decode8(mq, old_ms), v = decode8(vq, old_vs);
+        const float top = update8(k, g, m, v, p);
+        store8(master + i, left, p);
+        if (MASTER) store8(static_cast<uint16_t*>(e.p) + i, left, p);
+        uint32_t lo[8], hi[8];
+        const uint32_t x0 = (uint32_t)i * 0x9e3779b9u + base;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            // (past the end m and v are 0)
+            const uint32_t x = hash_open(x0 + (uint32_t)q * 0x9e3779b9u);
+            lo[q] = ((x ^ (x >> 16)) << 4 & 0xffff0u) | 8u;
+            hi[q] = (x >> 12 & 0xffff0u) | 8u;
+        }
+        uint32_t ms, vs;
+        mq = encode8<false>(m, top8(m), lo, ms);
+        vq = encode8<true>(v, top, hi, vs);
+        store_codes(static_cast<uint8_t*>(e.m) + i, left, mq);
+        store_codes(static_cast<uint8_t*>(e.v) + i, left, vq);
+        if (threadIdx.x % 4 == 0 && left > 0) {
+            e.ms[i / 32] = (uint8_t)ms;
+            e.vs[i / 32] = (uint8_t)vs;
         }
     }
+    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
 }
 
 struct StepArgs {
@@ -253,8 +457,11 @@ struct StepArgs {
     uint32_t seed, step;
 };
 
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ List l,
-                                                         const __grid_constant__ StepArgs a) {
+// ANY8: whether some tensor of the list has 8-bit states (fp32 ones alone need
+// less code and other registers).
+template <int N, bool ANY8>
+__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ List<N> l,
+                                                            const __grid_constant__ StepArgs a) {
     Scalars k;
     k.s = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
     if (!isfinite(k.s)) return;
@@ -278,52 +485,64 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     k.step = rate / c1;
     k.decay = rate * e.decay;
     const long long i0 = (long long)(blockIdx.x - e.chunk0) * kChunk;
-    const uint32_t base = hash32(hash32(hash32(a.seed) ^ step) ^ e.key);
-    switch (e.kind) {
-        case 0: adamw_chunk<false, false, false>(e, k, i0, base); break;
-        case kGradFp32: adamw_chunk<true, false, false>(e, k, i0, base); break;
-        case kMaster: adamw_chunk<false, true, false>(e, k, i0, base); break;
-        case kMaster | kGradFp32: adamw_chunk<true, true, false>(e, k, i0, base); break;
-        case kEightBit: adamw_chunk<false, false, true>(e, k, i0, base); break;
-        case kEightBit | kGradFp32: adamw_chunk<true, false, true>(e, k, i0, base); break;
-        case kEightBit | kMaster: adamw_chunk<false, true, true>(e, k, i0, base); break;
-        default: adamw_chunk<true, true, true>(e, k, i0, base); break;
+    extern __shared__ __align__(16) uint8_t smem[];  // the ring of 8-bit states
+    switch (ANY8 ? e.kind : e.kind & ~kEightBit) {
+        case 0: adamw_chunk32<false, false>(e, k, i0); break;
+        case kGradFp32: adamw_chunk32<true, false>(e, k, i0); break;
+        case kHasMaster: adamw_chunk32<false, true>(e, k, i0); break;
+        case kHasMaster | kGradFp32: adamw_chunk32<true, true>(e, k, i0); break;
+        default:
+            if (ANY8) {
+                const uint32_t base = hash32(hash32(hash32(a.seed) ^ step) ^ e.key);
+                switch (e.kind & ~kEightBit) {
+                    case 0: adamw_chunk8<false, false>(e, k, i0, base, smem); break;
+                    case kGradFp32: adamw_chunk8<true, false>(e, k, i0, base, smem); break;
+                    case kHasMaster: adamw_chunk8<false, true>(e, k, i0, base, smem); break;
+                    default: adamw_chunk8<true, true>(e, k, i0, base, smem); break;
+                }
+            }
     }
 }
 
 // ------------------------------------------------------------ gradient norm
-// One partial per chunk: a thread's squares in order, then a fixed tree.
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ List l, float* part) {
-    __shared__ float ws[kThreads / 32];
-    const Entry& e = l.e[entry_of(l, blockIdx.x)];
-    const long long i0 = (long long)(blockIdx.x - e.chunk0) * kChunk;
+// A chunk's squares: a thread's in order, then its warp's by exchanges, then
+// the eight warps ascending.
+__device__ __forceinline__ float warp_squares(const Entry& e, long long i0, int tid) {
     float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kChunk / kPass; ++j) {
-        const long long at = i0 + j * kPass + threadIdx.x * kPerThread;
+    const int passes = (int)min((e.n - i0 + kPass - 1) / kPass, (long long)(kNormChunk / kPass));
+#pragma unroll 4
+    for (int j = 0; j < passes; ++j) {
+        const long long at = i0 + j * kPass + tid * kPerThread;
         const int left = (int)min(max(e.n - at, 0LL), 8LL);
         float g[8];
-        if (e.kind & kGradFp32)
-            load8(static_cast<const float*>(e.g) + at, left, g);
-        else
-            load8(static_cast<const uint16_t*>(e.g) + at, left, g);
+        singles((e.kind & kGradFp32) ? load_grad<true>(e, at, left) : load_grad<false>(e, at, left), g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) s = fmaf(g[i], g[i], s);
     }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-    if (threadIdx.x % 32 == 0) ws[threadIdx.x / 32] = s;
+    return s;
+}
+template <int N>
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ List<N> l, float* part) {
+    __shared__ float sums[kThreads / 32];
+    const Entry& e = l.e[entry_of(l, blockIdx.x)];
+    const float s = warp_squares(e, (long long)(blockIdx.x - e.chunk0) * kNormChunk, threadIdx.x);
+    if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = s;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 1; w < kThreads / 32; ++w) s += ws[w];
-        part[blockIdx.x] = s;
+        float sum = sums[0];
+        for (int w = 1; w < kThreads / 32; ++w) sum += sums[w];
+        part[blockIdx.x] = sum;
     }
 }
 
+// The list's sum from its chunks', and what follows from it.
 __global__ void __launch_bounds__(1024) grad_norm_fold_kernel(const float* part, long long n, float pre, float max_norm,
                                                               float* out) {
     __shared__ double ws[32];
     double s = 0.0;
+#pragma unroll 8
     for (long long i = threadIdx.x; i < n; i += 1024) s += (double)part[i];
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
@@ -339,19 +558,20 @@ __global__ void __launch_bounds__(1024) grad_norm_fold_kernel(const float* part,
     }
 }
 
-long long chunks_of(long long n) { return (n + kChunk - 1) / kChunk; }
+// ------------------------------------------------------------ lists
+long long chunks_of(long long n, int chunk) { return (n + chunk - 1) / chunk; }
 
 // Calls f(list, first chunk, chunks) for runs of at most kMaxTensors tensors
-// and max_chunks chunks (a tensor's chunks stay together: n <= 2^40 elements
-// are 2^28 chunks).
+// and 2^30 chunks (a tensor's chunks stay together: n <= 2^40 elements are
+// at most 2^28 chunks).
 template <typename F>
-cudaError_t for_lists(const rlk_adamw_tensor* t, int n, F f) {
+cudaError_t for_lists(const rlk_adamw_tensor* t, int n, int chunk, F f) {
     constexpr long long kMaxChunks = 1LL << 30;
-    List l;
+    List<kMaxTensors> l;
     l.count = 0;
     long long chunks = 0, first = 0;
     for (int i = 0; i <= n; ++i) {
-        const long long c = i < n ? chunks_of(t[i].n) : 0;
+        const long long c = i < n ? chunks_of(t[i].n, chunk) : 0;
         if (i == n || l.count == kMaxTensors || chunks + c > kMaxChunks) {
             if (l.count > 0) {
                 const cudaError_t e = f(l, first, chunks);
@@ -374,7 +594,7 @@ cudaError_t for_lists(const rlk_adamw_tensor* t, int n, F f) {
         d.lr_scale = (float)t[i].lr_scale;
         d.decay = (float)t[i].weight_decay;
         d.key = t[i].key;
-        d.kind = (t[i].g_dtype == RLK_FP32 ? kGradFp32 : 0u) | (t[i].master != nullptr ? kMaster : 0u) |
+        d.kind = (t[i].g_dtype == RLK_FP32 ? kGradFp32 : 0u) | (t[i].master != nullptr ? kHasMaster : 0u) |
                  (t[i].state_bits == 8 ? kEightBit : 0u);
         d.chunk0 = (uint32_t)chunks;
         d.pad = 0;
@@ -382,20 +602,29 @@ cudaError_t for_lists(const rlk_adamw_tensor* t, int n, F f) {
     }
     return cudaSuccess;
 }
+List<kFewTensors> few(const List<kMaxTensors>& l) {
+    List<kFewTensors> s;
+    s.count = l.count;
+    std::copy(l.e, l.e + l.count, s.e);
+    return s;
+}
 
 }  // namespace
 
 size_t grad_norm_partials(const rlk_adamw_tensor* t, int n) {
     size_t c = 0;
-    for (int i = 0; i < n; ++i) c += (size_t)chunks_of(t[i].n);
+    for (int i = 0; i < n; ++i) c += (size_t)chunks_of(t[i].n, kNormChunk);
     return c;
 }
 
 cudaError_t launch_grad_norm(const rlk_adamw_tensor* t, int n, float pre, float max_norm, float* out, float* part,
                              cudaStream_t s) {
-    const cudaError_t e = for_lists(t, n, [&](const List& l, long long first, long long chunks) {
+    const cudaError_t e = for_lists(t, n, kNormChunk, [&](const List<kMaxTensors>& l, long long first, long long chunks) {
         timing_begin(kKGradNorm, s);
-        grad_norm_kernel<<<(unsigned)chunks, kThreads, 0, s>>>(l, part + first);
+        if (l.count <= kFewTensors)
+            grad_norm_kernel<<<(unsigned)chunks, kThreads, 0, s>>>(few(l), part + first);
+        else
+            grad_norm_kernel<<<(unsigned)chunks, kThreads, 0, s>>>(l, part + first);
         timing_end(kKGradNorm, s);
         return cudaGetLastError();
     });
@@ -421,9 +650,19 @@ cudaError_t launch_adamw(const rlk_adamw_tensor* t, int n, const rlk_adamw_args&
     a.grad_scale = r.grad_scale;
     a.seed = r.seed;
     a.step = (uint32_t)r.step;
-    return for_lists(t, n, [&](const List& l, long long, long long chunks) {
+    return for_lists(t, n, kChunk, [&](const List<kMaxTensors>& l, long long, long long chunks) {
+        int smem = 0;
+        for (int i = 0; i < l.count; ++i)
+            if (l.e[i].kind & kEightBit)
+                smem = kRingBytes;
+        auto launch = [&](auto kernel, const auto& list) {
+            kernel<<<(unsigned)chunks, kThreads, smem, s>>>(list, a);
+        };
         timing_begin(kKAdamw, s);
-        adamw_kernel<<<(unsigned)chunks, kThreads, 0, s>>>(l, a);
+        if (l.count <= kFewTensors)
+            smem > 0 ? launch(adamw_kernel<kFewTensors, true>, few(l)) : launch(adamw_kernel<kFewTensors, false>, few(l));
+        else
+            smem > 0 ? launch(adamw_kernel<kMaxTensors, true>, l) : launch(adamw_kernel<kMaxTensors, false>, l);
         timing_end(kKAdamw, s);
         return cudaGetLastError();
     });

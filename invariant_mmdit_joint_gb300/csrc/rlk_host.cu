@@ -336,7 +336,7 @@ const OpInfo kOps[] = {
     {"adaln_gate_residual+adaln_modulation", "rlk_adaln_gate_residual_fwd", kAdalnPolicy, kAdalnRowOrder},
     {"adaln_gate_residual+adaln_modulation backward", "rlk_adaln_gate_residual_bwd", kAdalnPolicy, kAdalnSumOrder},
     {"adamw", "rlk_adamw_step",
-     "fp32 update, moments rounded product by product, IEEE div/sqrt; 8-bit moments: e4m3 times 2^k per 32 elements, "
+     "fp32 update, moments rounded product by product, div/sqrt within 1 ulp; 8-bit moments: e4m3 times 2^k per 32 elements, "
      "stochastic rounding by a counter hash; p from the unrounded moments",
      "elementwise"},
     {"gradient norm and clip factor", "rlk_grad_norm", "fp32 squares, fp64 sum of the chunks, IEEE div/sqrt",
@@ -1325,7 +1325,7 @@ static rlk_status adamw_impl(const rlk_adamw_tensor* t, int32_t n, const rlk_ada
     if (st != RLK_OK) return st;
     auto below_one = [](double b) { return b >= 0.0 && b < 1.0; };
     auto rate_ok = [](double x) { return x >= 0.0 && std::isfinite(x); };
-    if (!rate_ok(a->lr) || !below_one(a->beta1) || !below_one(a->beta2) || !(a->eps > 0.0) || !std::isfinite(a->eps) ||
+    if (!rate_ok(a->lr) || !below_one(a->beta1) || !below_one(a->beta2) || !(a->eps >= 0x1p-50) || !(a->eps <= 1.0) ||
         (a->step_dev == nullptr && (a->step < 1 || a->step > 0x7fffffffLL)) || a->reserved != 0)
         return RLK_ERR_INVALID_ARG;
     auto aligned_to = [](const void* p, uintptr_t k) { return (reinterpret_cast<uintptr_t>(p) & (k - 1)) == 0; };

@@ -175,6 +175,7 @@ def test_adamw_tensors_fail_closed(L, over, code):
 
 @pytest.mark.parametrize("over, code", [
     (dict(lr=-1.0), 1), (dict(lr=float("nan")), 1), (dict(beta1=1.0), 1), (dict(beta2=-0.1), 1), (dict(eps=0.0), 1),
+    (dict(eps=1e-16), 1), (dict(eps=2.0), 1),
     (dict(step=0), 1), (dict(step=1 << 31), 1), (dict(reserved=3), 1), (dict(lr_dev=P + 2), 3), (dict(step_dev=P + 4), 3),
     (dict(grad_scale=P + 1), 3)])
 def test_adamw_arguments_fail_closed(L, over, code):
