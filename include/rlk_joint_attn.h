@@ -511,9 +511,10 @@ typedef struct rlk_adaln_io {
 } rlk_adaln_io;
 
 /* One stream's gradients. dy NULL: y was not used (gate_residual only; then
- * dscale, dshift, dw must be NULL); dr NULL: 0. dy and dr not both NULL. dx
- * is required and may be dr; dh is required by gate_residual_bwd. The fp32
- * sums may each be NULL (not wanted). */
+ * dscale, dshift, dw must be NULL); dr NULL: 0. One of the two is required,
+ * and each is given for both streams or for neither (otherwise
+ * RLK_ERR_INVALID_ARG). dx is required and may be dr; dh is required by
+ * gate_residual_bwd. The fp32 sums may each be NULL (not wanted). */
 typedef struct rlk_adaln_grad {
     const void* dy;    /* [B, T, C] */
     const void* dr;    /* [B, T, C] */

@@ -872,11 +872,24 @@ class JointAttention:
 
 
 def _require_current(device) -> None:
+    """The library launches on the current device: it must be the tensors' one."""
     import torch
     if device.type != "cuda":
         raise ValueError(f"the buffers are on {device}: the library computes on CUDA devices only")
-    if torch.cuda.current_device() != device.index:
+    if torch._C._cuda_getDevice() != device.index:
         raise ValueError(f"the current device is cuda:{torch.cuda.current_device()}, the buffers are on {device}")
+
+
+def _raw_stream(stream, index) -> int:
+    """The handle of `stream`, or of device `index`'s current one without
+    making a torch.cuda.Stream of it (3 us a call)."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+_NONE = (None, None)
 
 
 class AdaLN:
@@ -913,10 +926,12 @@ class AdaLN:
             raise RlkError(1, "AdaLN: invalid shape")
         self._f32, self._index = f32, -1 if self.device.index is None else self.device.index
         # expected sizes of each stream's tensors, None where it has no tokens
+        live = (T_txt > 0, T_img > 0)
+        self._live = live
         self._rows = tuple(torch.Size((B, T, C)) if T else None for T in (T_txt, T_img))
         self._stats = tuple(torch.Size((B, T, 2)) if T else None for T in (T_txt, T_img))
-        self._sums = tuple(torch.Size((B, C)) if T else None for T in (T_txt, T_img))
-        self._vector = tuple(torch.Size((C,)) if T else None for T in (T_txt, T_img))
+        self._sums = tuple(torch.Size((B, C)) if on else None for on in live)
+        self._vector = tuple(torch.Size((C,)) if on else None for on in live)
         self._shapes = {}  # the call's shape struct by the modulation's sample stride
         self.workspace = None  # of the backward, allocated at its first call
 
@@ -930,99 +945,101 @@ class AdaLN:
                          f"{tuple(t.shape)} on {t.device}")
 
     def _need(self, name, pair, dtype, sizes):
-        """Pointers of a pair of required dense tensors."""
+        """Pointers of a pair of required dense tensors (None without tokens)."""
         if len(pair) != 2:
             raise ValueError(f"{name} must be a (text, image) pair")
-        got = [None, None]
-        for i in (0, 1):
-            t, want = pair[i], sizes[i]
-            if want is None and t is None:
-                continue
-            if want is None or t is None or t.dtype is not dtype or t.shape != want or not t.is_contiguous() \
-                    or t.get_device() != self._index:
-                self._bad(name, i, t, want, dtype)
-            got[i] = t.data_ptr()
-        return got
+        index = self._index
+        t, want = pair[0], sizes[0]
+        p = q = None
+        if t is not None:
+            if want is None or t.dtype is not dtype or t.shape != want or not t.is_contiguous() or t.get_device() != index:
+                self._bad(name, 0, t, want, dtype)
+            p = t.data_ptr()
+        elif want is not None:
+            self._bad(name, 0, t, want, dtype)
+        t, want = pair[1], sizes[1]
+        if t is not None:
+            if want is None or t.dtype is not dtype or t.shape != want or not t.is_contiguous() or t.get_device() != index:
+                self._bad(name, 1, t, want, dtype)
+            q = t.data_ptr()
+        elif want is not None:
+            self._bad(name, 1, t, want, dtype)
+        return p, q
 
     def _weights(self, name, pair):
         """Pointers of a pair of optional [C] weights."""
-        if pair is None:
-            return (None, None)
-        sizes = tuple(None if t is None else w for t, w in zip(pair, self._vector))
+        if pair is None or (pair[0] is None and pair[1] is None):
+            return _NONE
         for i in (0, 1):
             if pair[i] is not None and self._vector[i] is None:
                 self._bad(name, i, pair[i], None, None)
-        return self._need(name, pair, self._f32, sizes)
+        return self._need(name, pair, self._f32, tuple(None if t is None else w for t, w in zip(pair, self._vector)))
+
+    def _view(self, name, i, t, strides):
+        """Pointer of a stream's [B, C] modulation view; its sample stride goes to `strides`."""
+        if t is None:
+            return None
+        want = self._sums[i]
+        s = t.stride()
+        if want is None or t.dtype is not self.mod_dtype or t.shape != want or s[1] != 1 or t.get_device() != self._index:
+            sh = self.shape
+            raise ValueError(f"{name}[{i}] must be a {self.mod_dtype} [{sh.B}, {sh.C}] view with unit column stride on "
+                             f"{self.device} (None without tokens), got {t.dtype} {tuple(t.shape)} on {t.device}")
+        strides.add(s[0])
+        return t.data_ptr()
 
     def _mods(self, *named):
         """The call's shape (with the views' sample stride) and the pointers of pairs of [B, C] views."""
-        sh, stride, res = self.shape, None, []
-        many = sh.B > 1
+        strides, res = set(), []
         for name, pair in named:
-            got = [None, None]
-            if pair is not None:
-                if len(pair) != 2:
-                    raise ValueError(f"{name} must be a (text, image) pair")
-                for i in (0, 1):
-                    t, want = pair[i], self._sums[i]
-                    if t is None:
-                        continue
-                    if want is None or t.dtype is not self.mod_dtype or t.shape != want or t.stride(1) != 1 \
-                            or t.get_device() != self._index:
-                        raise ValueError(f"{name}[{i}] must be a {self.mod_dtype} [{sh.B}, {sh.C}] view with unit column "
-                                         f"stride on {self.device} (None without tokens), got {t.dtype} "
-                                         f"{tuple(t.shape)} on {t.device}")
-                    if many:
-                        s = t.stride(0)
-                        if stride is None:
-                            stride = s
-                        elif s != stride:
-                            raise ValueError(f"scale, shift and gate must have one sample stride: got {stride} and {s} "
-                                             f"({name}[{i}])")
-                    got[i] = t.data_ptr()
-            res.append(got)
-        if stride is None:
-            stride = sh.C
+            if pair is None:
+                res.append(_NONE)
+                continue
+            if len(pair) != 2:
+                raise ValueError(f"{name} must be a (text, image) pair")
+            res.append((self._view(name, 0, pair[0], strides), self._view(name, 1, pair[1], strides)))
+        stride = self.shape.C
+        if strides and self.shape.B > 1:  # (a single sample's stride says nothing)
+            if len(strides) > 1:
+                raise ValueError(f"scale, shift and gate must have one sample stride, got {sorted(strides)}")
+            stride = strides.pop()
         call = self._shapes.get(stride)
         if call is None:
-            call = AdalnShape.from_buffer_copy(sh)
+            call = AdalnShape.from_buffer_copy(self.shape)
             call.mod_stride = stride
             self._shapes[stride] = call
-        return [call] + res
+        return call, res
 
     def _outputs(self, out, want):
-        """The outputs {name: (sizes, dtype)}, new or taken from `out`, and their pointers."""
-        import torch
+        """The outputs ((name, sizes, dtype), ...), new or taken from `out`, and their pointers."""
         if out is None:
+            import torch
             out = {k: tuple(None if s is None else torch.empty(s, dtype=d, device=self.device) for s in sizes)
-                   for k, (sizes, d) in want.items()}
-        elif out.keys() != want.keys():
-            raise ValueError(f"out must hold {sorted(want)}, got {sorted(out)}")
-        return out, {k: self._need(k, out[k], d, sizes) for k, (sizes, d) in want.items()}
+                   for k, sizes, d in want}
+        elif len(out) != len(want) or any(k not in out for k, _, _ in want):
+            raise ValueError(f"out must hold {sorted(k for k, _, _ in want)}, got {sorted(out)}")
+        return out, {k: self._need(k, out[k], d, sizes) for k, sizes, d in want}
 
-    def _launch(self, name, call, io, grad=None, stream=None):
-        """The C call on one struct of pointers per stream ({field: pointers})."""
-        _require_current(self.device)
-        on = [s is not None for s in self._rows]
-        ios = [AdalnIo(**{k: v[i] for k, v in io.items()}) if on[i] else None for i in (0, 1)]
-        if grad is None:
-            (rlk_adaln_modulation_fwd if name == "modulation" else rlk_adaln_gate_residual_fwd)(call, ios, stream)
-            return
-        import torch
+    def _structs(self, cls, *pairs):
+        """One struct of pointers per stream, its fields in order (None for a stream without tokens)."""
+        return [cls(*[p[i] for p in pairs]) if self._live[i] else None for i in (0, 1)]
+
+    def _scratch(self):
         if self.workspace is None:
+            import torch
             self.workspace = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
-        grads = [AdalnGrad(**{k: v[i] for k, v in grad.items()}) if on[i] else None for i in (0, 1)]
-        f = rlk_adaln_modulation_bwd if name == "modulation" else rlk_adaln_gate_residual_bwd
-        f(call, ios, grads, self.workspace, self._ws_bytes, stream)
+        return self.workspace
 
     # ---- calls
     def modulation(self, x, scale, shift, w=None, out=None, stream=None):
         """y = hat(x) * w * (1 + scale) + shift. Returns y and stats."""
         px = self._need("x", x, self.x_dtype, self._rows)
-        call, pscale, pshift = self._mods(("scale", scale), ("shift", shift))
+        call, (pscale, pshift) = self._mods(("scale", scale), ("shift", shift))
         pw = self._weights("w", w)
-        out, p = self._outputs(out, {"y": (self._rows, self.y_dtype), "stats": (self._stats, self._f32)})
-        self._launch("modulation", call, dict(x=px, scale=pscale, shift=pshift, w=pw, **p), stream=stream)
+        out, p = self._outputs(out, (("y", self._rows, self.y_dtype), ("stats", self._stats, self._f32)))
+        _require_current(self.device)
+        io = self._structs(AdalnIo, px, _NONE, _NONE, pscale, pshift, pw, _NONE, _NONE, p["y"], p["stats"])
+        rlk_adaln_modulation_fwd(call, io, _raw_stream(stream, self._index))
         return out
 
     def gate_residual(self, x, h, gate, scale, shift, w=None, w_post=None, want_y=True, out=None, stream=None):
@@ -1032,16 +1049,18 @@ class AdaLN:
         hold x itself as r."""
         px = self._need("x", x, self.x_dtype, self._rows)
         ph = self._need("h", h, self.y_dtype, self._rows)
-        call, pgate, pscale, pshift = self._mods(("gate", gate), ("scale", scale), ("shift", shift))
+        call, (pgate, pscale, pshift) = self._mods(("gate", gate), ("scale", scale), ("shift", shift))
         pw, pwp = self._weights("w", w), self._weights("w_post", w_post)
-        want = {"r": (self._rows, self.x_dtype)}
+        want = [("r", self._rows, self.x_dtype)]
         if want_y:
-            want.update(y=(self._rows, self.y_dtype), stats=(self._stats, self._f32))
+            want += (("y", self._rows, self.y_dtype), ("stats", self._stats, self._f32))
         if call.post:
-            want["post_stats"] = (self._stats, self._f32)
+            want.append(("post_stats", self._stats, self._f32))
         out, p = self._outputs(out, want)
-        self._launch("gate_residual", call, dict(x=px, h=ph, gate=pgate, scale=pscale, shift=pshift, w=pw, w_post=pwp,
-                                                 **p), stream=stream)
+        _require_current(self.device)
+        io = self._structs(AdalnIo, px, ph, pgate, pscale, pshift, pw, pwp, p["r"], p.get("y", _NONE),
+                           p.get("stats", _NONE), p.get("post_stats", _NONE))
+        rlk_adaln_gate_residual_fwd(call, io, _raw_stream(stream, self._index))
         return out
 
     def modulation_bwd(self, x, scale, stats, dy, dr=None, w=None, out=None, stream=None):
@@ -1051,14 +1070,17 @@ class AdaLN:
         px = self._need("x", x, self.x_dtype, self._rows)
         pst = self._need("stats", stats, self._f32, self._stats)
         pdy = self._need("dy", dy, self.y_dtype, self._rows)
-        pdr = (None, None) if dr is None else self._need("dr", dr, self.x_dtype, self._rows)
-        call, pscale = self._mods(("scale", scale))
+        pdr = _NONE if dr is None else self._need("dr", dr, self.x_dtype, self._rows)
+        call, (pscale,) = self._mods(("scale", scale))
         pw = self._weights("w", w)
-        want = {"dx": (self._rows, self.x_dtype), "dscale": (self._sums, self._f32), "dshift": (self._sums, self._f32)}
-        if pw[0] or pw[1]:
-            want["dw"] = (self._vector, self._f32)
+        want = [("dx", self._rows, self.x_dtype), ("dscale", self._sums, self._f32), ("dshift", self._sums, self._f32)]
+        if pw is not _NONE:
+            want.append(("dw", self._vector, self._f32))
         out, p = self._outputs(out, want)
-        self._launch("modulation", call, dict(x=px, scale=pscale, w=pw, stats=pst), dict(dy=pdy, dr=pdr, **p), stream)
+        _require_current(self.device)
+        io = self._structs(AdalnIo, px, _NONE, _NONE, pscale, _NONE, pw, _NONE, _NONE, _NONE, pst)
+        grad = self._structs(AdalnGrad, pdy, pdr, p["dx"], _NONE, _NONE, p["dscale"], p["dshift"], p.get("dw", _NONE))
+        rlk_adaln_modulation_bwd(call, io, grad, self._scratch(), self._ws_bytes, _raw_stream(stream, self._index))
         return out
 
     def gate_residual_bwd(self, r, h, gate, scale, stats, dy, dr=None, w=None, w_post=None, post_stats=None, out=None,
@@ -1067,30 +1089,32 @@ class AdaLN:
         dh, dgate, with dy (None: y was not used) dscale and dshift, with w
         dw, with w_post dw_post. dr is the gradient that reaches r by the
         residual path. ``out`` may hold dr itself as dx."""
-        f32 = self._f32
-        pr = self._need("r", r, self.x_dtype, self._rows)
-        ph = self._need("h", h, self.y_dtype, self._rows)
+        f32, rows, sums = self._f32, self._rows, self._sums
+        pr = self._need("r", r, self.x_dtype, rows)
+        ph = self._need("h", h, self.y_dtype, rows)
         if dy is None and dr is None:
             raise ValueError("dy and dr cannot both be None")
-        none = (None, None)
-        pdr = none if dr is None else self._need("dr", dr, self.x_dtype, self._rows)
-        call, pgate, pscale = self._mods(("gate", gate), ("scale", scale))
+        pdr = _NONE if dr is None else self._need("dr", dr, self.x_dtype, rows)
+        call, (pgate, pscale) = self._mods(("gate", gate), ("scale", scale))
         pw, pwp = self._weights("w", w), self._weights("w_post", w_post)
-        want = {"dx": (self._rows, self.x_dtype), "dh": (self._rows, self.y_dtype), "dgate": (self._sums, f32)}
-        pdy = pst = pps = none
+        want = [("dx", rows, self.x_dtype), ("dh", rows, self.y_dtype), ("dgate", sums, f32)]
+        pdy = pst = pps = _NONE
         if dy is not None:
-            pdy = self._need("dy", dy, self.y_dtype, self._rows)
+            pdy = self._need("dy", dy, self.y_dtype, rows)
             pst = self._need("stats", stats, f32, self._stats)
-            want.update(dscale=(self._sums, f32), dshift=(self._sums, f32))
-            if pw[0] or pw[1]:
-                want["dw"] = (self._vector, f32)
+            want += (("dscale", sums, f32), ("dshift", sums, f32))
+            if pw is not _NONE:
+                want.append(("dw", self._vector, f32))
         if call.post:
             pps = self._need("post_stats", post_stats, f32, self._stats)
-            if pwp[0] or pwp[1]:
-                want["dw_post"] = (self._vector, f32)
+            if pwp is not _NONE:
+                want.append(("dw_post", self._vector, f32))
         out, p = self._outputs(out, want)
-        self._launch("gate_residual", call, dict(r=pr, h=ph, gate=pgate, scale=pscale, w=pw, w_post=pwp, stats=pst,
-                                                 post_stats=pps), dict(dy=pdy, dr=pdr, **p), stream)
+        _require_current(self.device)
+        io = self._structs(AdalnIo, _NONE, ph, pgate, pscale, _NONE, pw, pwp, pr, _NONE, pst, pps)
+        grad = self._structs(AdalnGrad, pdy, pdr, p["dx"], p["dh"], p["dgate"], p.get("dscale", _NONE),
+                             p.get("dshift", _NONE), p.get("dw", _NONE), p.get("dw_post", _NONE))
+        rlk_adaln_gate_residual_bwd(call, io, grad, self._scratch(), self._ws_bytes, _raw_stream(stream, self._index))
         return out
 
 
@@ -1207,7 +1231,8 @@ class AdamW:
         if self.workspace is None:
             self.workspace = torch.empty(rlk_grad_norm_workspace_bytes(self._list, n), dtype=torch.uint8,
                                          device=self.device)
-        rlk_grad_norm(self._list, n, pre_scale, max_norm, out, self.workspace, stream=stream)
+        rlk_grad_norm(self._list, n, pre_scale, max_norm, out, self.workspace, self.workspace.numel(),
+                      _raw_stream(stream, self.device.index))
         return out
 
     def step(self, step, lr=None, grad_scale=None, grads=None, stream=None):
@@ -1230,4 +1255,4 @@ class AdamW:
         else:
             a.lr = self.lr if lr is None else float(lr)
         a.grad_scale = self._scalar("grad_scale", grad_scale, torch.float32)
-        rlk_adamw_step(self._list, len(self.params), a, stream)
+        rlk_adamw_step(self._list, len(self.params), a, _raw_stream(stream, self.device.index))

@@ -413,25 +413,28 @@ __global__ void __launch_bounds__(THREADS, kBwdCtas<NV, THREADS>) adaln_bwd_kern
     int fill_row = row_lo;
     const X *fx, *fdr;
     const Y *fdy, *fh;
-    bool copy_dy, copy_dr;
+    // (dy and dr are given for both streams or for neither)
+    const bool has_dy = a.s[row_lo >= rows_txt].dy != nullptr, has_dr = a.s[row_lo >= rows_txt].dr != nullptr;
     auto fill_from = [&](const AdalnStream& st, long long at) {
         fx = static_cast<const X*>(st.x) + at;
         fdr = static_cast<const X*>(st.dr) + at;
         fdy = static_cast<const Y*>(st.dy) + at;
         fh = static_cast<const Y*>(st.h) + at;
-        copy_dy = st.dy != nullptr;
-        copy_dr = st.dr != nullptr;
     };
     fill_from(a.s[row_lo >= rows_txt], (long long)(row_lo - (row_lo >= rows_txt ? rows_txt : 0)) * C + c0);
+    // what is absent reads as zeros: of the ring here, of the statistics below
+    if (!has_dy || !has_dr)
+        for (uint32_t i = 0; i < STAGES * kRow; ++i)
+            *reinterpret_cast<uint4*>(smem + 16 * tid + PITCH * i) = make_uint4(0, 0, 0, 0);
     auto fill = [&](uint32_t to) {
         if (fill_row < row_hi) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                if (copy_dy) {
+                if (has_dy) {
                     ring_fill<PITCH>(to + PITCH * (j * kPieces<X>), fx + j * step);
                     ring_fill<PITCH>(to + PITCH * (kDy + j * kPieces<Y>), fdy + j * step);
                 }
-                if (copy_dr) ring_fill<PITCH>(to + PITCH * (kDr + j * kPieces<X>), fdr + j * step);
+                if (has_dr) ring_fill<PITCH>(to + PITCH * (kDr + j * kPieces<X>), fdr + j * step);
                 if (GATE) ring_fill<PITCH>(to + PITCH * (kH + j * kPieces<Y>), fh + j * step);
             }
             fx += C;
@@ -452,7 +455,6 @@ __global__ void __launch_bounds__(THREADS, kBwdCtas<NV, THREADS>) adaln_bwd_kern
     for (int unit = lo; unit < hi; ++unit) {  // (none, if the CTA's rows lie inside one chunk)
         const int img = unit >= units_txt, v = unit - (img ? units_txt : 0);
         const AdalnStream& st = a.s[img];
-        const bool has_dy = st.dy != nullptr, has_dr = st.dr != nullptr;
         const int b = v / st.chunks, t0 = (v - b * st.chunks) * st.chunk_rows;
         if (sample != img * a.B + b) {
             sample = img * a.B + b;
@@ -490,7 +492,7 @@ __global__ void __launch_bounds__(THREADS, kBwdCtas<NV, THREADS>) adaln_bwd_kern
             const uint8_t* const at = smem + 16 * tid + stage;
             stage = stage == (STAGES - 1) * stage_bytes ? 0 : stage + stage_bytes;
             V8 d[NV], hat[NV];
-            if (has_dy) {
+            {
                 const V8 m = v8_all(ms.x), s = v8_all(ms.y);
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
@@ -507,15 +509,11 @@ __global__ void __launch_bounds__(THREADS, kBwdCtas<NV, THREADS>) adaln_bwd_kern
                 // d = dr + rstd * (e - mean(e) - hat * mean(e * hat))
                 const V8 c1 = v8_all(rms ? 0.0f : -ms.y * (c12.x * inv_c)), c2 = v8_all(-ms.y * (c12.y * inv_c));
 #pragma unroll
-                for (int j = 0; j < NV; ++j) d[j] = fma8(d[j], s, fma8(hat[j], c2, c1));
-            } else {
-#pragma unroll
-                for (int j = 0; j < NV; ++j) d[j] = v8_all(0.0f);
-            }
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                if (has_dr) d[j] = d[j] + ring_read<PITCH>(at + PITCH * (kDr + j * kPieces<X>), (const X*)nullptr);
-                store8(dx + j * step, d[j], j + 1 < NV || last);
+                for (int j = 0; j < NV; ++j) {
+                    const V8 dr = ring_read<PITCH>(at + PITCH * (kDr + j * kPieces<X>), (const X*)nullptr);
+                    d[j] = dr + fma8(d[j], s, fma8(hat[j], c2, c1));
+                    store8(dx + j * step, d[j], j + 1 < NV || last);
+                }
             }
             if (!GATE) continue;
             const V8 m = v8_all(ps.x), s = v8_all(ps.y);

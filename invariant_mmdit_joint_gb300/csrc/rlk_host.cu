@@ -1169,6 +1169,8 @@ static rlk_status adaln_fill(AdalnArgs* a, bool gate, bool bwd, const rlk_adaln_
             continue;
         }
         const rlk_adaln_grad& q = *gr[i];
+        if (i == 1 && a->s[0].T > 0 && ((gr[0]->dy == nullptr) != (q.dy == nullptr) || (gr[0]->dr == nullptr) != (q.dr == nullptr)))
+            return RLK_ERR_INVALID_ARG;
         s.x = gate ? d.r : d.x;
         s.stats = d.stats;
         s.dy = q.dy;

@@ -99,9 +99,12 @@ def test_adaln_pointers_fail_closed(L):
     assert bwd("modulation_bwd", dx=None) == 1
     assert bwd("modulation_bwd", i=dict(stats=None)) == 1
     assert bwd("modulation_bwd", i=dict(x=None)) == 1
-    assert bwd("gate_residual_bwd", dy=None, dr=None, dscale=None, dshift=None, dw=None) == 1
-    assert bwd("gate_residual_bwd", dy=None) == 1                      # sums that dy feeds
+    nothing = grad(dy=None, dr=None, dscale=None, dshift=None, dw=None)
+    assert call(L, "gate_residual_bwd", sh, (io(), io()), (nothing, nothing)) == 1
+    assert call(L, "gate_residual_bwd", sh, (io(), io()), (grad(dy=None), grad(dy=None))) == 1  # sums that dy feeds
     assert bwd("gate_residual_bwd", dh=None) == 1
+    assert bwd("gate_residual_bwd", dr=None) == 1                      # for one stream alone
+    assert bwd("modulation_bwd", dr=None) == 1
     assert bwd("gate_residual_bwd", i=dict(r=None)) == 1
     assert bwd("gate_residual_bwd", i=dict(post_stats=None)) == 1
     assert bwd("gate_residual_bwd", dgate=P + 4) == 3
@@ -121,7 +124,8 @@ def test_adaln_pointers_fail_closed(L):
         assert call(L, "modulation_bwd", sh, (io(), io()), gg, ws_bytes=need) == 5
         assert fwd("modulation_fwd", scale=None, shift=None, w=None, stats=None) == 5
         assert fwd("gate_residual_fwd", y=None, gate=None) == 5
-        assert bwd("gate_residual_bwd", dy=None, dscale=None, dshift=None, dw=None) == 5
+        alone = tuple(grad(dy=None, dscale=None, dshift=None, dw=None) for _ in range(2))
+        assert call(L, "gate_residual_bwd", sh, (io(), io()), alone) == 5
         only = pkg.AdalnShape.make(2, 0, 5, 64)
         assert call(L, "modulation_fwd", only, (None, io())) == 5
 

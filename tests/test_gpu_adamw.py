@@ -109,6 +109,36 @@ def test_eight_bit_states_bit_by_bit(dev):
                 np.testing.assert_array_equal(got, q)
 
 
+def test_the_quotient_over_the_whole_range(dev):
+    """p = -m / (sqrt(v) + eps), from v = 0 and subnormal v to v near the type's
+    end, for several eps: with beta 0.5 and no gradient m and v halve exactly,
+    at step 60 the corrections are 1, and p starts from 0 with a rate of 1.
+    Square root and quotient are within one unit in the last place (2u each),
+    their operand d = sqrt(v) + eps is rounded once, v below 2^-100 is moved
+    by 2^-124 - 40 (at most 2^-82 in its root)."""
+    import torch
+    rng = np.random.default_rng(8)
+    v = np.concatenate([[0.0, 2.0 ** -149, 2.0 ** -148, 2.0 ** -126, 2.0 ** 85, 2.0 ** 86, 2.0 ** 87, 3e38],
+                        2.0 ** rng.uniform(-149, 128, 40_000), 2.0 ** rng.uniform(-60, 0, 40_000)])
+    v = np.minimum(v, 3e38).astype(np.float32)
+    m = (rng.standard_normal(v.size) * np.maximum(np.sqrt(v.astype(np.float64)), 1e-25)).astype(np.float32)
+    # halves that are exact: no subnormal operand may lose its last bit
+    v, m = np.where(v < 2.0 ** -125, 0.0, v).astype(np.float32), np.where(np.abs(m) < 2.0 ** -125, 0.0, m).astype(np.float32)
+    tiny = 2.0 ** -149 * rng.integers(0, 1 << 20, 4096) * 2
+    v, m = np.concatenate([v, tiny.astype(np.float32)]), np.concatenate([m, np.full(4096, 1e-25, np.float32)])
+    for eps in (2.0 ** -50, 1e-15, 1e-8, 1.0):
+        p = torch.zeros(v.size, device=dev)
+        opt = pkg.AdamW([p], grads=[torch.zeros(v.size, device=dev)], m=[torch.from_numpy(m).to(dev)],
+                        v=[torch.from_numpy(v).to(dev)], lr=1.0, betas=(0.5, 0.5), eps=eps, weight_decay=0.0)
+        opt.step(60)
+        root = np.sqrt(v.astype(np.float64) / 2)
+        eps32 = float(np.float32(eps))
+        d = root + eps32
+        want = -(m.astype(np.float64) / 2) / d
+        bound = np.abs(want) * (2 * O.U * root / d + 2.0 ** -82 / d + 3 * O.U) * 1.001 + 2.0 ** -149
+        assert np.all(np.abs(f64(p) - want) <= bound), (eps, np.max(np.abs(f64(p) - want) / bound))
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_a_tensor_does_not_depend_on_its_list(dev, bits):
     """One list, and each tensor by itself under the same key: the same bytes; a list past one launch's entries too."""
