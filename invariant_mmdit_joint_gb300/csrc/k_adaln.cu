@@ -30,6 +30,9 @@ using namespace sm100;
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() {
@@ -59,9 +62,19 @@ __device__ __forceinline__ V8 v8_of(uint4 q) {
 __device__ __forceinline__ V8 v8_of(float4 a, float4 b) {
     return V8{{f2_pack(a.x, a.y), f2_pack(a.z, a.w), f2_pack(b.x, b.y), f2_pack(b.z, b.w)}};
 }
-__device__ __forceinline__ V8 load8(const uint16_t* p) { return v8_of(*reinterpret_cast<const uint4*>(p)); }
-__device__ __forceinline__ V8 load8(const float* p) {
-    return v8_of(reinterpret_cast<const float4*>(p)[0], reinterpret_cast<const float4*>(p)[1]);
+// With fp32 rows (SPLIT) a thread's eight columns are two groups of four, `half`
+// apart: as one run, each 16-byte access of a warp left out every other 16
+// bytes, so that a 32-byte sector went twice (fp32 modulation backward of 7 x
+// 3212 rows of 1128 columns: 127 us, 91 in two groups).
+template <bool SPLIT>
+__device__ __forceinline__ V8 load8(const uint16_t* p, int half) {
+    if (!SPLIT) return v8_of(*reinterpret_cast<const uint4*>(p));
+    const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(p + half);
+    return v8_of(make_uint4(a.x, a.y, b.x, b.y));
+}
+template <bool SPLIT>
+__device__ __forceinline__ V8 load8(const float* p, int half) {
+    return v8_of(*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + (SPLIT ? half : 4)));
 }
 __device__ __forceinline__ float4 half_of(const V8& v, int k) {
     float4 f;
@@ -70,22 +83,30 @@ __device__ __forceinline__ float4 half_of(const V8& v, int k) {
     return f;
 }
 // Stores the values, rounded to the type, and returns what was stored.
-__device__ __forceinline__ V8 store8(uint16_t* p, const V8& v, bool write = true) {
+template <bool SPLIT>
+__device__ __forceinline__ V8 store8(uint16_t* p, int half, const V8& v, bool write = true) {
     const uint4 q = make_uint4(pair_bf16(v.p[0]), pair_bf16(v.p[1]), pair_bf16(v.p[2]), pair_bf16(v.p[3]));
-    if (write) *reinterpret_cast<uint4*>(p) = q;
+    if (write && !SPLIT) *reinterpret_cast<uint4*>(p) = q;
+    if (write && SPLIT) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(q.x, q.y);
+        *reinterpret_cast<uint2*>(p + half) = make_uint2(q.z, q.w);
+    }
     return v8_of(q);
 }
-__device__ __forceinline__ V8 store8(float* p, const V8& v, bool write = true) {
+template <bool SPLIT>
+__device__ __forceinline__ V8 store8(float* p, int half, const V8& v, bool write = true) {
     if (write) {
-        reinterpret_cast<float4*>(p)[0] = half_of(v, 0);
-        reinterpret_cast<float4*>(p)[1] = half_of(v, 1);
+        *reinterpret_cast<float4*>(p) = half_of(v, 0);
+        *reinterpret_cast<float4*>(p + (SPLIT ? half : 4)) = half_of(v, 1);
     }
     return v;
 }
 // 8 values of a modulation row (or `absent` in each).
-__device__ __forceinline__ V8 load8_mod(const void* base, bool fp32, long long at, float absent) {
+template <bool SPLIT>
+__device__ __forceinline__ V8 load8_mod(const void* base, bool fp32, long long at, int half, float absent) {
     if (base == nullptr) return v8_all(absent);
-    return fp32 ? load8(static_cast<const float*>(base) + at) : load8(static_cast<const uint16_t*>(base) + at);
+    return fp32 ? load8<SPLIT>(static_cast<const float*>(base) + at, half)
+                : load8<SPLIT>(static_cast<const uint16_t*>(base) + at, half);
 }
 __device__ __forceinline__ V8 operator*(const V8& a, const V8& b) {
     return V8{{mul_f2(a.p[0], b.p[0]), mul_f2(a.p[1], b.p[1]), mul_f2(a.p[2], b.p[2]), mul_f2(a.p[3], b.p[3])}};
@@ -138,10 +159,19 @@ __device__ __forceinline__ float warp_sum(float x) {
 // 229 us for 175.
 template <typename T>
 constexpr int kPieces = sizeof(T) / 2;
-template <int PITCH, typename T>
-__device__ __forceinline__ void ring_fill(uint32_t to, const T* src) {
-#pragma unroll
-    for (int p = 0; p < kPieces<T>; ++p) copy16(to + p * PITCH, reinterpret_cast<const char*>(src) + 16 * p);
+template <int PITCH, bool SPLIT>
+__device__ __forceinline__ void ring_fill(uint32_t to, const uint16_t* src, int half) {
+    if (SPLIT) {
+        copy8(to, src);
+        copy8(to + 8, src + half);
+    } else {
+        copy16(to, src);
+    }
+}
+template <int PITCH, bool SPLIT>
+__device__ __forceinline__ void ring_fill(uint32_t to, const float* src, int half) {
+    copy16(to, src);
+    copy16(to + PITCH, src + (SPLIT ? half : 4));
 }
 template <int PITCH>
 __device__ __forceinline__ V8 ring_read(const uint8_t* at, const uint16_t*) {
@@ -180,7 +210,7 @@ __device__ __forceinline__ float held_by(int warp, int groups) {
 // them out of the sums and the results.
 struct RowSums {
     float mine, joined;  // values of a row that this warp and warp lane % 16 hold
-    float inv_mine, inv_c, eps;
+    float inv_mine, inv_c, inv_c_low, eps;
     bool last;
     int tid, warps;
 };
@@ -195,6 +225,10 @@ __device__ __forceinline__ float thread_sum(bool last, F f) {
     const float end = last ? pair_sum(e) : 0.0f;
     return NV == 1 ? end : pair_sum(s) + end;
 }
+
+// s / C as s times 1 / C in two parts: one rounding of 1 / C alone would shift
+// every row's statistics the same way.
+__device__ __forceinline__ float per_column(float s, const RowSums& g) { return fmaf(s, g.inv_c, s * g.inv_c_low); }
 
 // Mean (0 for rms) and 1 / deviation of a row. Each warp takes its own mean
 // and its squares about that; the warps are then joined about the row's mean
@@ -213,11 +247,11 @@ __device__ __forceinline__ float2 row_stats(const V8 (&v)[NV], bool rms, const R
         if (g.tid % 32 == 0) buf[g.tid / 32] = make_float2(mean, m2);
         __syncthreads();
         const float2 p = buf[g.tid % 16];
-        mean = rms ? 0.0f : half_sum(p.x * g.joined) * g.inv_c;
+        mean = rms ? 0.0f : per_column(half_sum(p.x * g.joined), g);
         const float z = p.x - mean;  // 0 for rms
         m2 = half_sum(fmaf(g.joined * z, z, p.y));
     }
-    return make_float2(mean, 1.0f / sqrtf(fmaf(m2, g.inv_c, g.eps)));
+    return make_float2(mean, 1.0f / sqrtf(per_column(m2, g) + g.eps));
 }
 
 // Sums of two values over the CTA. The halves of a warp take one value each
@@ -256,12 +290,15 @@ __global__ void __launch_bounds__(THREADS) adaln_fwd_kernel(const __grid_constan
     g.joined = held_by<NV>(tid % 16, C / 8);
     g.inv_mine = 1.0f / fmaxf(g.mine, 1.0f);
     g.inv_c = 1.0f / (float)C;
+    g.inv_c_low = fmaf(-(float)C, g.inv_c, 1.0f) / (float)C;
     g.eps = a.eps;
     g.tid = tid;
     g.warps = warps;
     const bool last = g.last = 8 * (NV - 1) * threads + col < C;
-    // a thread's columns: c0 and, of NV = 2, c0 + step
-    const int c0 = min(col, C - 8), step = min(8 * threads + col, C - 8) - c0;
+    // a thread's columns: from c0 and, of NV = 2, from c0 + step
+    constexpr bool S = sizeof(X) == 4;
+    const int c0 = (S ? 4 : 8) * min(tid, C / 8 - 1), half = S ? C / 2 : 4;
+    const int step = (S ? 4 : 8) * min(threads + tid, C / 8 - 1) - c0;
     const int rows_txt = a.B * a.s[0].T, rows = rows_txt + a.B * a.s[1].T;
     const int lo = (int)((long long)rows * blockIdx.x / gridDim.x);
     const int hi = (int)((long long)rows * (blockIdx.x + 1) / gridDim.x);
@@ -277,8 +314,8 @@ __global__ void __launch_bounds__(THREADS) adaln_fwd_kernel(const __grid_constan
         if (fill_row < hi) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                ring_fill<PITCH>(to + PITCH * (j * kPieces<X>), fx + j * step);
-                if (GATE) ring_fill<PITCH>(to + PITCH * (kX + j * kPieces<Y>), fh + j * step);
+                ring_fill<PITCH, S>(to + PITCH * (j * kPieces<X>), fx + j * step, half);
+                if (GATE) ring_fill<PITCH, S>(to + PITCH * (kX + j * kPieces<Y>), fh + j * step, half);
             }
             fx += C;
             if (GATE) fh += C;
@@ -304,11 +341,11 @@ __global__ void __launch_bounds__(THREADS) adaln_fwd_kernel(const __grid_constan
         for (int j = 0; j < NV; ++j) {
             const int c = c0 + j * step;
             const long long mod = b * a.mod_stride + c;
-            k[j] = load8_mod(st.w, true, c, 1.0f) * (v8_all(1.0f) + load8_mod(st.scale, a.mod_fp32, mod, 0.0f));
-            sh[j] = load8_mod(st.shift, a.mod_fp32, mod, 0.0f);
+            k[j] = load8_mod<S>(st.w, true, c, half, 1.0f) * (v8_all(1.0f) + load8_mod<S>(st.scale, a.mod_fp32, mod, half, 0.0f));
+            sh[j] = load8_mod<S>(st.shift, a.mod_fp32, mod, half, 0.0f);
             if (GATE) {
-                ga[j] = v8_all(a.alpha) * load8_mod(st.gate, a.mod_fp32, mod, 1.0f);
-                if (POST) ga[j] = ga[j] * load8_mod(st.w_post, true, c, 1.0f);
+                ga[j] = v8_all(a.alpha) * load8_mod<S>(st.gate, a.mod_fp32, mod, half, 1.0f);
+                if (POST) ga[j] = ga[j] * load8_mod<S>(st.w_post, true, c, half, 1.0f);
             }
         }
         const long long first = (long long)(row - off) * C + c0;
@@ -343,7 +380,7 @@ __global__ void __launch_bounds__(THREADS) adaln_fwd_kernel(const __grid_constan
                 }
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
-                    v[j] = store8(rp + j * step, fma8(u[j], ga[j], v[j]), j + 1 < NV || last);
+                    v[j] = store8<S>(rp + j * step, half, fma8(u[j], ga[j], v[j]), j + 1 < NV || last);
                 if (!want_y) continue;
             }
             const float2 ms = row_stats<NV>(v, rms, g, buf[parity]);
@@ -351,7 +388,7 @@ __global__ void __launch_bounds__(THREADS) adaln_fwd_kernel(const __grid_constan
             if (want_stats) *stats = ms;
             const V8 m = v8_all(ms.x), s = v8_all(ms.y);
 #pragma unroll
-            for (int j = 0; j < NV; ++j) store8(yp + j * step, fma8((v[j] - m) * s, k[j], sh[j]), j + 1 < NV || last);
+            for (int j = 0; j < NV; ++j) store8<S>(yp + j * step, half, fma8((v[j] - m) * s, k[j], sh[j]), j + 1 < NV || last);
         }
     }
     copies_wait<0>();
@@ -405,8 +442,10 @@ __global__ void __launch_bounds__(THREADS, kBwdCtas<NV, THREADS>) adaln_bwd_kern
     const float inv_c = 1.0f / (float)C;
     const bool rms = a.norm == RLK_NORM_RMS, post_rms = a.post == RLK_NORM_RMS;
     const bool last = 8 * (NV - 1) * threads + col < C;
-    // a thread's columns: c0 and, of NV = 2, c0 + step
-    const int c0 = min(col, C - 8), step = min(8 * threads + col, C - 8) - c0;
+    // a thread's columns: from c0 and, of NV = 2, from c0 + step
+    constexpr bool S = sizeof(X) == 4;
+    const int c0 = (S ? 4 : 8) * min(tid, C / 8 - 1), half = S ? C / 2 : 4;
+    const int step = (S ? 4 : 8) * min(threads + tid, C / 8 - 1) - c0;
     constexpr uint32_t stage_bytes = kRow * PITCH;
     const uint32_t ring = smem_u32(smem) + 16 * tid;
     // the next row to copy
@@ -431,11 +470,11 @@ __global__ void __launch_bounds__(THREADS, kBwdCtas<NV, THREADS>) adaln_bwd_kern
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 if (has_dy) {
-                    ring_fill<PITCH>(to + PITCH * (j * kPieces<X>), fx + j * step);
-                    ring_fill<PITCH>(to + PITCH * (kDy + j * kPieces<Y>), fdy + j * step);
+                    ring_fill<PITCH, S>(to + PITCH * (j * kPieces<X>), fx + j * step, half);
+                    ring_fill<PITCH, S>(to + PITCH * (kDy + j * kPieces<Y>), fdy + j * step, half);
                 }
-                if (has_dr) ring_fill<PITCH>(to + PITCH * (kDr + j * kPieces<X>), fdr + j * step);
-                if (GATE) ring_fill<PITCH>(to + PITCH * (kH + j * kPieces<Y>), fh + j * step);
+                if (has_dr) ring_fill<PITCH, S>(to + PITCH * (kDr + j * kPieces<X>), fdr + j * step, half);
+                if (GATE) ring_fill<PITCH, S>(to + PITCH * (kH + j * kPieces<Y>), fh + j * step, half);
             }
             fx += C;
             fdr += C;
@@ -462,10 +501,10 @@ __global__ void __launch_bounds__(THREADS, kBwdCtas<NV, THREADS>) adaln_bwd_kern
             for (int j = 0; j < NV; ++j) {
                 const int c = c0 + j * step;
                 const long long mod = b * a.mod_stride + c;
-                k[j] = load8_mod(st.w, true, c, 1.0f) * (v8_all(1.0f) + load8_mod(st.scale, a.mod_fp32, mod, 0.0f));
+                k[j] = load8_mod<S>(st.w, true, c, half, 1.0f) * (v8_all(1.0f) + load8_mod<S>(st.scale, a.mod_fp32, mod, half, 0.0f));
                 if (GATE) {
-                    kg[j] = v8_all(a.alpha) * load8_mod(st.gate, a.mod_fp32, mod, 1.0f);
-                    if (POST) kg[j] = kg[j] * load8_mod(st.w_post, true, c, 1.0f);
+                    kg[j] = v8_all(a.alpha) * load8_mod<S>(st.gate, a.mod_fp32, mod, half, 1.0f);
+                    if (POST) kg[j] = kg[j] * load8_mod<S>(st.w_post, true, c, half, 1.0f);
                 }
             }
         }
@@ -512,7 +551,7 @@ __global__ void __launch_bounds__(THREADS, kBwdCtas<NV, THREADS>) adaln_bwd_kern
                 for (int j = 0; j < NV; ++j) {
                     const V8 dr = ring_read<PITCH>(at + PITCH * (kDr + j * kPieces<X>), (const X*)nullptr);
                     d[j] = dr + fma8(d[j], s, fma8(hat[j], c2, c1));
-                    store8(dx + j * step, d[j], j + 1 < NV || last);
+                    store8<S>(dx + j * step, half, d[j], j + 1 < NV || last);
                 }
             }
             if (!GATE) continue;
@@ -523,7 +562,7 @@ __global__ void __launch_bounds__(THREADS, kBwdCtas<NV, THREADS>) adaln_bwd_kern
                 if (POST) hat[j] = (hat[j] - m) * s;
                 sum_g[j] = fma8(d[j], hat[j], sum_g[j]);
                 d[j] = d[j] * kg[j];
-                if (!POST) store8(dh + j * step, d[j], j + 1 < NV || last);
+                if (!POST) store8<S>(dh + j * step, half, d[j], j + 1 < NV || last);
             }
             if (POST) {
                 const float s1 = thread_sum<NV>(last, [&](uint64_t& q, int j) { sum8(q, d[j]); });
@@ -533,7 +572,7 @@ __global__ void __launch_bounds__(THREADS, kBwdCtas<NV, THREADS>) adaln_bwd_kern
                 const V8 c1 = v8_all(post_rms ? 0.0f : -ps.y * (c12.x * inv_c)), c2 = v8_all(-ps.y * (c12.y * inv_c));
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
-                    store8(dh + j * step, fma8(d[j], s, fma8(hat[j], c2, c1)), j + 1 < NV || last);
+                    store8<S>(dh + j * step, half, fma8(d[j], s, fma8(hat[j], c2, c1)), j + 1 < NV || last);
             }
         }
         row += n;
@@ -541,9 +580,9 @@ __global__ void __launch_bounds__(THREADS, kBwdCtas<NV, THREADS>) adaln_bwd_kern
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             if (j + 1 == NV && !last) break;
-            store8(part + j * step, sum_a[j]);
-            store8(part + C + j * step, sum_s[j]);
-            if (GATE) store8(part + 2 * C + j * step, sum_g[j]);
+            store8<S>(part + j * step, half, sum_a[j]);
+            store8<S>(part + C + j * step, half, sum_s[j]);
+            if (GATE) store8<S>(part + 2 * C + j * step, half, sum_g[j]);
         }
     }
     copies_wait<0>();
@@ -681,10 +720,11 @@ cudaError_t bwd_launch(const AdalnArgs& a, cudaStream_t s) {
 }
 // 8 columns a thread up to C = 4096: with 16 the sums and factors leave room
 // for one CTA an SM (1024^2 modulation 47 us for 51, the 1328^2 gate 175 for
-// 220). Built for three numbers of threads, which fix the registers' limit
-// and the ring's layout.
+// 220). Built for four numbers of threads, which fix the registers' limit and the
+// ring's layout.
 template <typename X, typename Y, bool GATE, bool POST>
 cudaError_t bwd_nv(const AdalnArgs& a, cudaStream_t s) {
+    if (a.C <= 512) return bwd_launch<X, Y, 1, 64, GATE, POST>(a, s);
     if (a.C <= 1280) return bwd_launch<X, Y, 1, 160, GATE, POST>(a, s);
     if (a.C <= 2560) return bwd_launch<X, Y, 1, 320, GATE, POST>(a, s);
     if (a.C <= 4096) return bwd_launch<X, Y, 1, 512, GATE, POST>(a, s);
@@ -708,7 +748,7 @@ cudaError_t bwd_xy(const AdalnArgs& a, bool gate, cudaStream_t s) {
 // gate, T = 6889: 160 us with 32 rows, 165 with 16, 180 with 8), short ones
 // spread few rows over the SMs (1024^2 modulation, T = 4096: 49, 42, 46 us; T =
 // 513: 16.3 us with 4 rows for 18.6 with 8).
-int adaln_chunk_rows(int T) { return T >= 4096 ? 16 : 4; }
+int adaln_chunk_rows(int T) { return T >= 4096 ? 16 : (T >= 2048 ? 8 : (T >= 128 ? 4 : (T > 32 ? 2 : 1))); }
 
 cudaError_t launch_adaln_fwd(const AdalnArgs& a, bool gate, cudaStream_t s) {
     timing_begin(kKAdalnFwd, s);

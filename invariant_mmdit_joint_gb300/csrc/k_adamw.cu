@@ -340,7 +340,7 @@ constexpr int kRingBytes = 48 * 1024;  // four CTAs an SM
 template <bool G32>
 constexpr int kStageBytes = kThreads * (16 * (G32 ? 4 : 3) + 16);  // g and master in 16 bytes, the codes in 8 each
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(from) : "memory");
+    asm volatile("cp.async.CACHE.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copy8(uint32_t to, const void* from) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(to), "l"(from) : "memory");
