@@ -464,8 +464,9 @@ rlk_status rlk_attn_out_bias_gemm(const rlk_ja_shape* shape,
  * chunks ascending, then b ascending, in fp32 and without atomics: a sample's
  * gradients do not depend on its batch.
  *
- * Every row is processed, padded text rows too. Arithmetic is fp32 with IEEE
- * division and square root; each output is rounded once. */
+ * Every row is processed, padded text rows too: theirs must hold finite values
+ * in the backward, with zero gradients if they are to add nothing. Arithmetic
+ * is fp32 with IEEE division and square root; each output is rounded once. */
 #define RLK_NORM_NONE 0
 #define RLK_NORM_LAYER 1
 #define RLK_NORM_RMS 2
@@ -615,8 +616,8 @@ rlk_status rlk_adamw_step(const rlk_adamw_tensor* tensors, int32_t n_tensors, co
  * max_norm > 0, or INFINITY for no clipping. Squares are fp32: magnitudes
  * below 2^-63 vanish, and a norm above 2^63 counts as infinite. Sums run in a
  * fixed order per tensor, tensors in list order (fp64), without atomics.
- * workspace: rlk_grad_norm_workspace_bytes() bytes; out: fp32 [2], 4-byte
- * aligned. */
+ * workspace: rlk_grad_norm_workspace_bytes() bytes, one for each of the calls
+ * that may overlap on the GPU; out: fp32 [2], 4-byte aligned. */
 size_t rlk_grad_norm_workspace_bytes(const rlk_adamw_tensor* tensors, int32_t n_tensors);
 rlk_status rlk_grad_norm(const rlk_adamw_tensor* tensors, int32_t n_tensors, float pre_scale, float max_norm, float* out,
                          void* workspace, size_t workspace_bytes, void* stream);

@@ -1128,7 +1128,11 @@ class AdamW:
     (state_bits 8). ``weight_decay`` and ``lr_scale`` are one number or one per
     parameter. ``keys`` (default 0, 1, ...) name the parameters to the 8-bit
     states' rounding. ``grads``, bfloat16 or float32, may be held here (buffers
-    that a backward pass writes anew for every step) or given to each call."""
+    that a backward pass writes anew for every step) or given to each call.
+    ``params``, ``masters``, ``m``, ``v``, ``m_scale`` and ``v_scale`` are lists
+    of the tensors in use: what a checkpoint keeps, and what the constructor
+    takes to go on from one. grad_norm's calls share one workspace: calls that
+    may overlap on the GPU need an object each."""
 
     def __init__(self, params, masters=None, state_bits: int = 32, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay=0.01, lr_scale=1.0, seed: int = 0, keys=None, grads=None, m=None, v=None, m_scale=None,

@@ -4,14 +4,17 @@
 // 28 bytes an element with fp32 states (p, g, m, v read; p, m, v written), 16
 // with 8-bit ones and bf16 gradients. Measured: 45 million elements, fp32
 // states, 193 us (6.5 TB/s, 0.96 of the copy bandwidth); 166 million, 8-bit
-// states, 483 us (5.5 TB/s, 0.81), there bound by the arithmetic pipes: 82
+// states, 448 us (6.0 TB/s, 0.88), there near the issue limit too: 82
 // instructions an element (105 and 600 us with one element at a time, sqrtf
 // and the division, and nothing fetched ahead).
 //
 // The list travels as a kernel argument (up to kMaxTensors entries), so a call
 // copies nothing to the device and a captured graph holds its own list. A CTA
-// takes one chunk of one tensor, found by bisection in the chunk counts: 16384
-// elements (8-bit states: 530 us with 4096, 493 with 32768).
+// takes one chunk of one tensor, found by bisection in the chunk counts. AdamW's
+// chunks are as long as still gives every SM eight (16384 elements at most:
+// 166 million with 8-bit states took 530 us with 4096, 493 with 32768, 483
+// with 16384; 12 tensors of 5 to 40 thousand DRAWN in chunks of 2048); the
+// norm's are always 16384, since its sums follow them.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -33,7 +36,7 @@ constexpr int kMaxTensors = 256;
 constexpr int kThreads = 256;
 constexpr int kPerThread = 8;
 constexpr int kPass = kThreads * kPerThread;  // elements a CTA covers at once
-constexpr int kChunk = 8 * kPass;
+constexpr int kMaxPasses = 8;  // of an AdamW chunk
 constexpr int kNormChunk = 8 * kPass;
 
 enum : uint32_t { kGradFp32 = 1, kHasMaster = 2, kEightBit = 4 };
@@ -314,10 +317,10 @@ __device__ __forceinline__ V8 load_grad(const Entry& e, long long at, int left) 
 // One chunk with fp32 states: 28 bytes an element, and enough loads of a
 // thread at once that nothing need be fetched ahead.
 template <bool G32, bool MASTER>
-__device__ __forceinline__ void adamw_chunk32(const Entry& e, const Scalars& k, long long i0) {
+__device__ __forceinline__ void adamw_chunk32(const Entry& e, const Scalars& k, long long i0, int passes) {
     float* const master = MASTER ? e.master : static_cast<float*>(e.p);
 #pragma unroll 1
-    for (int j = 0; j < kChunk / kPass; ++j) {
+    for (int j = 0; j < passes; ++j) {
         const long long at = i0 + j * kPass + threadIdx.x * kPerThread;
         const int left = (int)min(max(e.n - at, 0LL), 8LL);
         if (left == 0) return;
@@ -339,17 +342,20 @@ __device__ __forceinline__ void adamw_chunk32(const Entry& e, const Scalars& k, 
 constexpr int kRingBytes = 48 * 1024;  // four CTAs an SM
 template <bool G32>
 constexpr int kStageBytes = kThreads * (16 * (G32 ? 4 : 3) + 16);  // g and master in 16 bytes, the codes in 8 each
+// Through L1: a thread's two 16-byte copies of its fp32 elements share sectors
+// with no other thread's, and past L1 (.cg) each fetched them anew (166 million
+// elements 488 us, 448 through it).
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
-    asm volatile("cp.async.CACHE.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(from) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copy8(uint32_t to, const void* from) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(to), "l"(from) : "memory");
 }
 template <bool G32, bool MASTER>
-__device__ __forceinline__ void adamw_chunk8(const Entry& e, const Scalars& k, long long i0, uint32_t base,
+__device__ __forceinline__ void adamw_chunk8(const Entry& e, const Scalars& k, long long i0, int passes, uint32_t base,
                                              uint8_t* smem) {
     constexpr int kMaster = G32 ? 2 : 1, kCodes = kMaster + 2;  // pieces before the master and the codes
-    constexpr int kPasses = kChunk / kPass, kStep = 16 * kThreads, kStages = kRingBytes / kStageBytes<G32>;  // 3, or 2
+    constexpr int kStep = 16 * kThreads, kStages = kRingBytes / kStageBytes<G32>;  // 3, or 2
     float* const master = MASTER ? e.master : static_cast<float*>(e.p);
     const uint8_t* const mc = static_cast<const uint8_t*>(e.m);
     const uint8_t* const vc = static_cast<const uint8_t*>(e.v);
@@ -357,7 +363,7 @@ __device__ __forceinline__ void adamw_chunk8(const Entry& e, const Scalars& k, l
     long long at = i0 + threadIdx.x * kPerThread;
     auto fill = [&](int j, uint32_t stage) {
         const long long i = at + (long long)j * kPass;
-        if (j < kPasses && i + 8 <= e.n) {  // (the last elements of a tensor are loaded one by one when their turn comes)
+        if (j < passes && i + 8 <= e.n) {  // (the last elements of a tensor are loaded one by one when their turn comes)
             const uint32_t to = ring + stage + 16 * threadIdx.x;
             if (G32) {
                 copy16(to, static_cast<const float*>(e.g) + i);
@@ -376,7 +382,7 @@ __device__ __forceinline__ void adamw_chunk8(const Entry& e, const Scalars& k, l
     uint32_t next_ms = 0, next_vs = 0;
     auto read_scales = [&](int j) {
         const long long i = at + (long long)j * kPass;
-        if (j < kPasses && i < e.n) {
+        if (j < passes && i < e.n) {
             next_ms = e.ms[i / 32];
             next_vs = e.vs[i / 32];
         }
@@ -386,7 +392,7 @@ __device__ __forceinline__ void adamw_chunk8(const Entry& e, const Scalars& k, l
     read_scales(0);
     uint32_t stage = 0, filled = (kStages - 1) * kStageBytes<G32>;  // to read, to fill
 #pragma unroll 1
-    for (int j = 0; j < kPasses; ++j) {
+    for (int j = 0; j < passes; ++j) {
         if (i0 + j * kPass >= e.n) break;  // the same for the whole CTA
         fill(j + kStages - 1, filled);
         const uint8_t* const ready = smem + stage;
@@ -455,6 +461,7 @@ struct StepArgs {
     const long long* step_dev;
     const float* grad_scale;
     uint32_t seed, step;
+    int passes;  // of a chunk
 };
 
 // ANY8: whether some tensor of the list has 8-bit states (fp32 ones alone need
@@ -484,21 +491,21 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
     k.eps = a.eps;
     k.step = rate / c1;
     k.decay = rate * e.decay;
-    const long long i0 = (long long)(blockIdx.x - e.chunk0) * kChunk;
+    const long long i0 = (long long)(blockIdx.x - e.chunk0) * a.passes * kPass;
     extern __shared__ __align__(16) uint8_t smem[];  // the ring of 8-bit states
     switch (ANY8 ? e.kind : e.kind & ~kEightBit) {
-        case 0: adamw_chunk32<false, false>(e, k, i0); break;
-        case kGradFp32: adamw_chunk32<true, false>(e, k, i0); break;
-        case kHasMaster: adamw_chunk32<false, true>(e, k, i0); break;
-        case kHasMaster | kGradFp32: adamw_chunk32<true, true>(e, k, i0); break;
+        case 0: adamw_chunk32<false, false>(e, k, i0, a.passes); break;
+        case kGradFp32: adamw_chunk32<true, false>(e, k, i0, a.passes); break;
+        case kHasMaster: adamw_chunk32<false, true>(e, k, i0, a.passes); break;
+        case kHasMaster | kGradFp32: adamw_chunk32<true, true>(e, k, i0, a.passes); break;
         default:
             if (ANY8) {
                 const uint32_t base = hash32(hash32(hash32(a.seed) ^ step) ^ e.key);
                 switch (e.kind & ~kEightBit) {
-                    case 0: adamw_chunk8<false, false>(e, k, i0, base, smem); break;
-                    case kGradFp32: adamw_chunk8<true, false>(e, k, i0, base, smem); break;
-                    case kHasMaster: adamw_chunk8<false, true>(e, k, i0, base, smem); break;
-                    default: adamw_chunk8<true, true>(e, k, i0, base, smem); break;
+                    case 0: adamw_chunk8<false, false>(e, k, i0, a.passes, base, smem); break;
+                    case kGradFp32: adamw_chunk8<true, false>(e, k, i0, a.passes, base, smem); break;
+                    case kHasMaster: adamw_chunk8<false, true>(e, k, i0, a.passes, base, smem); break;
+                    default: adamw_chunk8<true, true>(e, k, i0, a.passes, base, smem); break;
                 }
             }
     }
@@ -650,7 +657,17 @@ cudaError_t launch_adamw(const rlk_adamw_tensor* t, int n, const rlk_adamw_args&
     a.grad_scale = r.grad_scale;
     a.seed = r.seed;
     a.step = (uint32_t)r.step;
-    return for_lists(t, n, kChunk, [&](const List<kMaxTensors>& l, long long, long long chunks) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    // (elementwise: the chunks change no byte)
+    for (a.passes = kMaxPasses; a.passes > 1; a.passes /= 2) {
+        long long chunks = 0;
+        for (int i = 0; i < n; ++i) chunks += chunks_of(t[i].n, a.passes * kPass);
+        if (chunks >= 8LL * sms) break;
+    }
+    return for_lists(t, n, a.passes * kPass, [&](const List<kMaxTensors>& l, long long, long long chunks) {
         int smem = 0;
         for (int i = 0; i < l.count; ++i)
             if (l.e[i].kind & kEightBit)

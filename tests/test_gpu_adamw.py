@@ -159,6 +159,45 @@ def test_a_tensor_does_not_depend_on_its_list(dev, bits):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
 
 
+def test_a_run_resumes_from_its_tensors(dev):
+    """Stopped after two steps and taken up by a new object from copies of the tensors: the same bytes."""
+    import torch
+    for bits in (32, 8):
+        a, grads = make(dev, SIZES, bits)
+        for step in (1, 2):
+            a.step(step)
+        copy = lambda ts: [None if t is None else t.clone() for t in ts]  # noqa: E731
+        state = dict(m=copy(a.m), v=copy(a.v))
+        if bits == 8:
+            state.update(m_scale=copy(a.m_scale), v_scale=copy(a.v_scale))
+        b = pkg.AdamW(copy(a.params), masters=copy(a.masters), state_bits=bits, lr=HYPER["lr"], betas=(0.9, 0.95),
+                      weight_decay=[0.1 * (i % 2) for i in range(len(SIZES))],
+                      lr_scale=[1.0 + 0.5 * (i % 3) for i in range(len(SIZES))], seed=77, grads=grads, **state)
+        for opt in (a, b):
+            opt.step(3)
+        for x, y in zip(a.params + a.m + a.v, b.params + b.m + b.v):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), bits
+
+
+@pytest.mark.parametrize("count", [4, 30])
+def test_one_list_of_both_kinds_of_state(dev, count):
+    """Tensors with 32-bit and 8-bit states in one call, in short and long lists: the bytes of two calls."""
+    import torch
+    sizes = (SIZES * 4)[:count]
+    pair = [[make(dev, sizes, bits, seed=4)[0] for bits in (32, 8)] for _ in range(2)]
+    for opt in pair[0]:
+        opt.step(1)
+    both = (pkg.AdamwTensor * (2 * count))()
+    for i in range(count):  # alternating
+        both[2 * i], both[2 * i + 1] = pair[1][0]._list[i], pair[1][1]._list[i]
+    args = pkg.AdamwArgs.from_buffer_copy(pair[1][0]._args)
+    args.step, args.lr = 1, HYPER["lr"]
+    pkg.rlk_adamw_step(both, 2 * count, args)
+    for a, b in zip(*pair):
+        for x, y in zip(a.params + a.m + a.v, b.params + b.m + b.v):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
 @pytest.mark.parametrize("sizes", [[1], [5, 0, 4097], SIZES, [3_000_001]], ids=str)
 def test_gradient_norm(dev, sizes):
     import torch
