@@ -3,7 +3,7 @@
 // the states' format: include/rlk_joint_attn.h). Elementwise: the floor is HBM,
 // 28 bytes an element with fp32 states (p, g, m, v read; p, m, v written), 16
 // with 8-bit ones and bf16 gradients. Measured: 45 million elements, fp32
-// states, 193 us (6.5 TB/s, 0.96 of the copy bandwidth); 166 million, 8-bit
+// states, 185.5 us (6.8 TB/s, the copy bandwidth); 166 million, 8-bit
 // states, 448 us (6.0 TB/s, 0.88), there near the issue limit too: 82
 // instructions an element (105 and 600 us with one element at a time, sqrtf
 // and the division, and nothing fetched ahead).
@@ -36,7 +36,9 @@ constexpr int kMaxTensors = 256;
 constexpr int kThreads = 256;
 constexpr int kPerThread = 8;
 constexpr int kPass = kThreads * kPerThread;  // elements a CTA covers at once
-constexpr int kMaxPasses = 8;  // of an AdamW chunk
+// Of an AdamW chunk; with fp32 states alone a chunk gains nothing by more than
+// two (185.5 us; 186.5 with one, 196 with eight).
+constexpr int kMaxPasses = 8, kMaxPasses32 = 2;
 constexpr int kNormChunk = 8 * kPass;
 
 enum : uint32_t { kGradFp32 = 1, kHasMaster = 2, kEightBit = 4 };
@@ -464,10 +466,11 @@ struct StepArgs {
     int passes;  // of a chunk
 };
 
-// ANY8: whether some tensor of the list has 8-bit states (fp32 ones alone need
-// less code and other registers).
+// ANY8: whether some tensor of the list has 8-bit states. fp32 ones alone take
+// three CTAs an SM: with the registers of four the compiler no longer has all
+// loads of a thread under way at once (45 million elements 185.5 us, 204).
 template <int N, bool ANY8>
-__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ List<N> l,
+__global__ void __launch_bounds__(kThreads, ANY8 ? 4 : 3) adamw_kernel(const __grid_constant__ List<N> l,
                                                             const __grid_constant__ StepArgs a) {
     Scalars k;
     k.s = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
@@ -662,7 +665,9 @@ cudaError_t launch_adamw(const rlk_adamw_tensor* t, int n, const rlk_adamw_args&
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     // (elementwise: the chunks change no byte)
-    for (a.passes = kMaxPasses; a.passes > 1; a.passes /= 2) {
+    bool any8 = false;
+    for (int i = 0; i < n; ++i) any8 = any8 || t[i].state_bits == 8;
+    for (a.passes = any8 ? kMaxPasses : kMaxPasses32; a.passes > 1; a.passes /= 2) {
         long long chunks = 0;
         for (int i = 0; i < n; ++i) chunks += chunks_of(t[i].n, a.passes * kPass);
         if (chunks >= 8LL * sms) break;
