@@ -4,15 +4,16 @@
 //   r = x + alpha * gate_b * u,  u = h or hat(h) * w_post,  then y from r
 // (the formulas and the gradients' are in include/rlk_joint_attn.h).
 //
-// Each activation is read once and written once: the floor is HBM (1024^2, C =
-// 2560: 13.2 us forward, 26.3 us backward; 1328^2 with the gate: 65 and 130
-// us). What it takes to come near it is to have few instructions and many rows
-// under way: rows are copied ahead by cp.async, a CTA's threads keep the same
-// columns for every row, and what a sample's rows share stays in registers.
-// Measured: forward 19.2 us (4.6 TB/s) and 81 us (5.4 TB/s), backward with its
-// folds 42 us (4.2 TB/s) and 165 us (5.3 TB/s); the rest is the latency of a
-// row's sums (shuffles and one barrier each), which the warps of an SM cover
-// only in part.
+// Each activation is read once and written once: the floor is HBM (bf16, 1024^2
+// guidance pair, C = 2560: 13.2 us forward, 26.3 us backward; four samples at
+// 1328^2: 65 us forward with norms on both sides, 130 us backward). What it
+// takes to come near it is many rows under way and few instructions: rows are
+// copied ahead by cp.async, a CTA's threads keep the same columns for every
+// row, and what a sample's rows share stays in registers. Measured: forward
+// 18.7 us (4.8 TB/s) and 78 us (5.6 TB/s), backward with its folds 43.6 us (4.1
+// TB/s) and 161 us (5.5 TB/s). The rest is the chain of a row's sums (about
+// 1100 cycles of shuffles and one barrier), which the 20 warps that an SM's
+// registers hold cover only in part, and the start and end of short launches.
 #include "rlk_device.cuh"
 #include "rlk_internal.h"
 #include "rlk_sm100.cuh"
@@ -186,7 +187,6 @@ __device__ __forceinline__ V8 ring_read(const uint8_t* at, const float*) {
 // A CTA owns a row at a time, a thread the same NV * 8 of its columns in every
 // row (the last 8 may lie past it). Sums run within a warp, then over the
 // warps, both by exchanges in one order that depends on C alone.
-constexpr int kMaxThreads = 512;
 
 // Sum over each half of a warp.
 __device__ __forceinline__ float half_sum(float v) {
@@ -275,9 +275,15 @@ __device__ __forceinline__ float2 block_sum2(float x, float y, int tid, int warp
 // row of a sample (w * (1 + scale), shift, alpha * gate * w_post) stays in a
 // thread's registers until the CTA comes to the next sample.
 constexpr int kFwdStages = 3;
+// CTAs of an SM that the registers are held to. A modulation's 83 a thread
+// leave room for four CTAs of 160 threads; 72 and five of them are faster
+// (1024^2, 19.3 -> 18.7 us). With a gate the same spills (78 -> 81 us at four
+// CTAs of 121 registers held to 96).
+template <int NV, int THREADS, bool GATE>
+constexpr int kFwdCtas = GATE || 820 / THREADS < 1 ? 1 : 820 / THREADS;
 
 template <typename X, typename Y, int NV, int THREADS, bool GATE, bool POST>
-__global__ void __launch_bounds__(THREADS) adaln_fwd_kernel(const __grid_constant__ AdalnArgs a) {
+__global__ void __launch_bounds__(THREADS, kFwdCtas<NV, THREADS, GATE>) adaln_fwd_kernel(const __grid_constant__ AdalnArgs a) {
     constexpr int PITCH = 16 * THREADS;
     constexpr int kX = NV * kPieces<X>, kRow = kX + (GATE ? NV * kPieces<Y> : 0);  // a row's pieces: x, h
     extern __shared__ __align__(16) uint8_t smem[];
