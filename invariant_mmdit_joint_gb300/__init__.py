@@ -1129,10 +1129,13 @@ class AdamW:
     parameter. ``keys`` (default 0, 1, ...) name the parameters to the 8-bit
     states' rounding. ``grads``, bfloat16 or float32, may be held here (buffers
     that a backward pass writes anew for every step) or given to each call.
-    ``params``, ``masters``, ``m``, ``v``, ``m_scale`` and ``v_scale`` are lists
-    of the tensors in use: what a checkpoint keeps, and what the constructor
-    takes to go on from one. grad_norm's calls share one workspace: calls that
-    may overlap on the GPU need an object each."""
+    ``params``, ``masters``, ``m``, ``v``, ``m_scale`` and ``v_scale`` hold the
+    tensors in use, one entry a parameter: what a checkpoint keeps, and what the
+    constructor takes to go on from one. They stay the same tensors for the
+    object's life: load values into them with ``copy_``; a parameter whose
+    ``data`` was replaced is refused. ``lr`` may be set at any time. grad_norm's
+    calls share one workspace: calls that may overlap on the GPU need an object
+    each."""
 
     def __init__(self, params, masters=None, state_bits: int = 32, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay=0.01, lr_scale=1.0, seed: int = 0, keys=None, grads=None, m=None, v=None, m_scale=None,
@@ -1144,8 +1147,7 @@ class AdamW:
         n = len(params)
         if n == 0:
             raise ValueError("no parameters given")
-        self.params, self.state_bits = list(params), state_bits
-        self.lr, self.betas, self.eps, self.seed = float(lr), betas, float(eps), int(seed)
+        self.params, self.state_bits, self.lr = tuple(params), state_bits, float(lr)
         self.device = self.params[0].device
         each = lambda x: list(x) if isinstance(x, (list, tuple)) else [x] * n  # noqa: E731
         decay, share, keys = each(weight_decay), each(lr_scale), list(range(n)) if keys is None else list(keys)
@@ -1155,16 +1157,17 @@ class AdamW:
 
         def states(given, dtype, sizes):
             if given is None:
-                return [torch.zeros(k, dtype=dtype, device=self.device) for k in sizes]
-            return list(given)
+                return tuple(torch.zeros(k, dtype=dtype, device=self.device) for k in sizes)
+            return tuple(given)
         sizes = [p.numel() for p in self.params]
         self.m, self.v = states(m, code, sizes), states(v, code, sizes)
-        self.m_scale = states(m_scale, torch.uint8, blocks) if state_bits == 8 else [None] * n
-        self.v_scale = states(v_scale, torch.uint8, blocks) if state_bits == 8 else [None] * n
+        self.m_scale = states(m_scale, torch.uint8, blocks) if state_bits == 8 else (None,) * n
+        self.v_scale = states(v_scale, torch.uint8, blocks) if state_bits == 8 else (None,) * n
         if not len(decay) == len(share) == len(keys) == len(masters) == len(self.m) == len(self.v) == len(self.m_scale) \
                 == len(self.v_scale) == n:
             raise ValueError(f"expected one entry for each of the {n} parameters")
-        self.masters = []
+        if not all(0 <= int(k) < 2 ** 32 for k in [seed, *keys]):
+            raise ValueError("seed and keys must be in 0 .. 2^32 - 1")
         self._list = (AdamwTensor * n)()
         for i, p in enumerate(self.params):
             if p.dtype not in (f32, bf16):
@@ -1173,7 +1176,6 @@ class AdamW:
                 raise ValueError(f"parameter {i} is float32 and takes no master")
             if p.dtype == bf16 and masters[i] is None:
                 masters[i] = p.detach().float().contiguous()
-            self.masters.append(masters[i])
             for name, t, dtype, k in (("parameter", p, p.dtype, sizes[i]), ("master", masters[i], f32, sizes[i]),
                                       ("m", self.m[i], code, sizes[i]), ("v", self.v[i], code, sizes[i]),
                                       ("m_scale", self.m_scale[i], torch.uint8, blocks[i]),
@@ -1184,10 +1186,12 @@ class AdamW:
             e.p, e.master, e.m, e.v = _ptr(p), _ptr(masters[i]), _ptr(self.m[i]), _ptr(self.v[i])
             e.m_scale, e.v_scale, e.n = _ptr(self.m_scale[i]), _ptr(self.v_scale[i]), sizes[i]
             e.lr_scale, e.weight_decay, e.state_bits, e.key = float(share[i]), float(decay[i]), state_bits, int(keys[i])
+        self.masters = tuple(masters)
+        self._pointers = [p.data_ptr() for p in self.params]
         self.grads = None
         if grads is not None:
             self._take(grads)
-        self._args = AdamwArgs(lr=self.lr, beta1=float(betas[0]), beta2=float(betas[1]), eps=self.eps, seed=self.seed)
+        self._args = AdamwArgs(lr=self.lr, beta1=float(betas[0]), beta2=float(betas[1]), eps=float(eps), seed=int(seed))
         self.workspace = None  # of grad_norm, allocated at its first call
 
     def _dense(self, name, t, dtypes, n):
@@ -1203,6 +1207,8 @@ class AdamW:
             raise ValueError(f"expected {len(self.params)} gradients, got {len(grads)}")
         for i, (g, p) in enumerate(zip(grads, self.params)):
             self._dense(f"gradient {i}", g, (torch.float32, torch.bfloat16), p.numel())
+            if g.dim() != 1 and g.shape != p.shape:
+                raise ValueError(f"gradient {i} must be {tuple(p.shape)} or flat, got {tuple(g.shape)}")
         for e, g in zip(self._list, grads):
             e.g, e.g_dtype = g.data_ptr(), int(g.dtype == torch.float32)
         self.grads = grads
@@ -1212,6 +1218,8 @@ class AdamW:
             self._take(grads)
         if self.grads is None:
             raise ValueError("no gradients given")
+        if [p.data_ptr() for p in self.params] != self._pointers:
+            raise ValueError("a parameter's data was replaced: copy_ into it, or make a new object")
         _require_current(self.device)
 
     def _scalar(self, name, t, dtype):

@@ -269,7 +269,8 @@ def test_adamw_binding_refuses_unfit_tensors(L):
     assert opt.masters[0] is None and opt.masters[1].dtype == torch.float32
     assert [m.dtype for m in opt.m] == [torch.float8_e4m3fn] * 2 and [s.numel() for s in opt.m_scale] == [2, 2]
     g = [torch.zeros(5, 7), torch.zeros(33)]
-    for bad in ([g[0]], [g[0], torch.zeros(32)], [g[0].half(), g[1]], [torch.zeros(7, 5).t(), g[1]]):
+    for bad in ([g[0]], [g[0], torch.zeros(32)], [g[0].half(), g[1]], [torch.zeros(7, 5).t(), g[1]],
+                [torch.zeros(7, 5), g[1]]):
         with pytest.raises(ValueError):
             opt.step(1, grads=bad)
     with pytest.raises(ValueError):
@@ -280,9 +281,24 @@ def test_adamw_binding_refuses_unfit_tensors(L):
         opt.grad_norm(1.0)
     for bad in (dict(params=[]), dict(params=[p[0].half()]), dict(params=p, state_bits=4), dict(params=p, m=[p[0]]),
                 dict(params=p, masters=[p[0], None]), dict(params=p, weight_decay=[0.1]), dict(params=[p[0].t()]),
-                dict(params=p, v=[torch.zeros(35), torch.zeros(34)]), dict(params=p, keys=[1])):
+                dict(params=p, v=[torch.zeros(35), torch.zeros(34)]), dict(params=p, keys=[1]),
+                dict(params=p, keys=[0, 2 ** 32]), dict(params=p, seed=-1)):
         with pytest.raises(ValueError):
             pkg.AdamW(**bad)
+
+
+def test_adamw_keeps_to_its_tensors(L):
+    torch = pytest.importorskip("torch")
+    p = [torch.zeros(5, 7), torch.zeros(33, dtype=torch.bfloat16)]
+    opt = pkg.AdamW(p, state_bits=8, grads=[torch.zeros(35), torch.zeros(33)])
+    for held in (opt.params, opt.masters, opt.m, opt.v, opt.m_scale, opt.v_scale):
+        with pytest.raises(TypeError):  # the call's list holds the addresses of those that are there
+            held[0] = torch.zeros(35)
+    p[0].data = torch.zeros(5, 7)
+    with pytest.raises(ValueError, match="replaced"):
+        opt.step(1)
+    with pytest.raises(ValueError, match="replaced"):
+        opt.grad_norm(1.0)
 
 
 # ------------------------------------------------------------------ definitions

@@ -219,13 +219,13 @@ def test_a_norm_that_is_not_finite_leaves_everything(dev):
     for bits in (32, 8):
         opt, grads = make(dev, SIZES, bits)
         opt.step(1)
-        keep = [t.clone() for t in opt.params + [m for m in opt.masters if m is not None] + opt.m + opt.v]
+        keep = [t.clone() for t in opt.params + opt.masters + opt.m + opt.v if t is not None]
         for bad in (float("nan"), float("inf"), 3e30):  # the last one's square is not finite
             grads[-1][17] = bad
             n = opt.grad_norm(1.0)
             assert not bool(torch.isfinite(n[0])) and bool(torch.isnan(n[1]))
             opt.step(2, grad_scale=n[1:])
-            now = opt.params + [m for m in opt.masters if m is not None] + opt.m + opt.v
+            now = [t for t in opt.params + opt.masters + opt.m + opt.v if t is not None]
             assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(now, keep))
 
 
