@@ -465,7 +465,8 @@ rlk_status rlk_attn_out_bias_gemm(const rlk_ja_shape* shape,
  * gradients do not depend on its batch.
  *
  * Every row is processed, padded text rows too: theirs must hold finite values
- * in the backward, with zero gradients if they are to add nothing. Arithmetic
+ * in the backward, with zero gradients if they are to add nothing. But for r = x
+ * and dx = dr, a written buffer must not overlap any other of the call. Arithmetic
  * is fp32 with IEEE division and square root; each output is rounded once. */
 #define RLK_NORM_NONE 0
 #define RLK_NORM_LAYER 1

@@ -10,8 +10,8 @@
 // takes to come near it is many rows under way and few instructions: rows are
 // copied ahead by cp.async, a CTA's threads keep the same columns for every
 // row, and what a sample's rows share stays in registers. Measured: forward
-// 18.7 us (4.8 TB/s) and 78 us (5.6 TB/s), backward with its folds 43.6 us (4.1
-// TB/s) and 161 us (5.5 TB/s). The rest is the chain of a row's sums (about
+// 18.7 us (4.8 TB/s) and 78 us (5.6 TB/s), backward with its folds 42 us (4.3
+// TB/s) and 163 us (5.4 TB/s). The rest is the chain of a row's sums (about
 // 1100 cycles of shuffles and one barrier), which the 20 warps that an SM's
 // registers hold cover only in part, and the start and end of short launches.
 #include "rlk_device.cuh"
@@ -598,8 +598,11 @@ __global__ void __launch_bounds__(THREADS, kBwdCtas<NV, THREADS>) adaln_bwd_kern
 // blockIdx.y = 3 * stream + which, z = sample): a thread takes four columns of
 // every kFoldRuns-th chunk, the runs are added in order. Weights' gradients
 // need every sample's sum: it replaces the sample's first chunk's, which only
-// this CTA reads, for adaln_weight_kernel.
-constexpr int kFoldRuns = 16;
+// this CTA reads, for adaln_weight_kernel. 32 runs: the 256 chunks of a 4096
+// token sample are eight loads a thread, all under way at once (1024^2
+// modulation 42.8 -> 41.9 us with its fold, 5 samples of 1365 fp32 rows with
+// the gate 42.9 -> 41.2; 64 runs of 16 columns 43.2 and 43.7).
+constexpr int kFoldRuns = 32;
 constexpr int kFoldColumns = 64;  // of a CTA: 16 threads
 __global__ void __launch_bounds__(kFoldColumns / 4 * kFoldRuns) adaln_fold_kernel(const __grid_constant__ AdalnArgs a) {
     __shared__ float4 run[kFoldRuns][kFoldColumns / 4];
