@@ -517,28 +517,40 @@ __global__ void __launch_bounds__(kThreads, ANY8 ? 4 : 3) adamw_kernel(const __g
 
 // ------------------------------------------------------------ gradient norm
 // A chunk's squares: a thread's in order, then its warp's by exchanges, then
-// the eight warps ascending.
-__device__ __forceinline__ float warp_squares(const Entry& e, long long i0, int tid) {
+// the eight warps ascending. 45 million bf16 gradients are 90 MB, 13 us at the
+// copy bandwidth; norm, fold and the step that follows take 207 us, 22 of them
+// for the first two (26 with a check of the bounds at each load).
+template <bool G32>
+__device__ __forceinline__ float thread_squares(const Entry& e, long long i0, int tid) {
     float s = 0.0f;
-    const int passes = (int)min((e.n - i0 + kPass - 1) / kPass, (long long)(kNormChunk / kPass));
-#pragma unroll 4
-    for (int j = 0; j < passes; ++j) {
-        const long long at = i0 + j * kPass + tid * kPerThread;
-        const int left = (int)min(max(e.n - at, 0LL), 8LL);
+    auto add = [&](const V8& v) {
         float g[8];
-        singles((e.kind & kGradFp32) ? load_grad<true>(e, at, left) : load_grad<false>(e, at, left), g);
+        singles(v, g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) s = fmaf(g[i], g[i], s);
-    }
+    };
+    constexpr int kPasses = kNormChunk / kPass;
+    const long long at = i0 + tid * kPerThread;
+    if (e.n - i0 >= kNormChunk) {  // no bounds to look at: all loads are under way at once
+        V8 v[kPasses];
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+        for (int j = 0; j < kPasses; ++j) v[j] = load_grad<G32>(e, at + j * kPass, 8);
+#pragma unroll
+        for (int j = 0; j < kPasses; ++j) add(v[j]);
+    } else {
+#pragma unroll 1
+        for (int j = 0; j < kPasses; ++j) add(load_grad<G32>(e, at + j * kPass, (int)min(max(e.n - at - j * kPass, 0LL), 8LL)));
+    }
     return s;
 }
 template <int N>
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ List<N> l, float* part) {
     __shared__ float sums[kThreads / 32];
     const Entry& e = l.e[entry_of(l, blockIdx.x)];
-    const float s = warp_squares(e, (long long)(blockIdx.x - e.chunk0) * kNormChunk, threadIdx.x);
+    const long long i0 = (long long)(blockIdx.x - e.chunk0) * kNormChunk;
+    float s = (e.kind & kGradFp32) ? thread_squares<true>(e, i0, threadIdx.x) : thread_squares<false>(e, i0, threadIdx.x);
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
     if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = s;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -548,7 +560,9 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
     }
 }
 
-// The list's sum from its chunks', and what follows from it.
+// The list's sum from its chunks', and what follows from it. One CTA, bound by
+// latency: only the sum is in fp64 (the root too, and 32 warps' sums added one
+// by one, took 1 us longer).
 __global__ void __launch_bounds__(1024) grad_norm_fold_kernel(const float* part, long long n, float pre, float max_norm,
                                                               float* out) {
     __shared__ double ws[32];
@@ -559,9 +573,12 @@ __global__ void __launch_bounds__(1024) grad_norm_fold_kernel(const float* part,
     for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
     if (threadIdx.x % 32 == 0) ws[threadIdx.x / 32] = s;
     __syncthreads();
+    if (threadIdx.x >= 32) return;
+    s = ws[threadIdx.x];
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
     if (threadIdx.x == 0) {
-        for (int w = 1; w < 32; ++w) s += ws[w];
-        const float norm = (float)((double)pre * sqrt(s));
+        const float norm = pre * sqrtf((float)s);
         out[0] = norm;
         float f = pre;
         if (max_norm < norm + 1e-6f) f = pre * (max_norm / (norm + 1e-6f));
