@@ -302,12 +302,13 @@ __device__ __forceinline__ V8 quotient8(const V8& m, const V8& v, float top, flo
 }
 
 // New m, v and p of 8 elements from g (unscaled), and the largest v (NaN if
-// one is). m and v take each product and sum rounded by itself: the 8-bit
-// codes follow from these bits.
+// one is). The 8-bit codes follow from the bits of m and v, so their rounding is
+// written out: the gradient's product, then one fma (left as a product and a
+// sum the compiler would choose one).
 __device__ __forceinline__ float update8(const Scalars& k, const V8& grad, V8& m, V8& v, V8& p) {
     const V8 g = grad * all8(k.s);
-    m = all8(k.b1) * m + all8(k.o1) * g;
-    v = all8(k.b2) * v + (all8(k.o2) * g) * g;
+    m = fma8(all8(k.b1), m, all8(k.o1) * g);
+    v = fma8(all8(k.b2), v, (all8(k.o2) * g) * g);
     const float top = top8(v);
     p = p - fma8(all8(k.decay), p, all8(k.step) * quotient8(m, v, top, k.inv_c2, k.eps));
     return top;
