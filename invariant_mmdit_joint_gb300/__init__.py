@@ -889,6 +889,16 @@ def _raw_stream(stream, index) -> int:
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _on(stream, device):
+    """Context in which memory is allocated for a call on `stream`: what the
+    allocator hands out is free there, and maybe not yet on another stream."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream)
+
+
 _NONE = (None, None)
 
 
@@ -1010,10 +1020,13 @@ class AdaLN:
             self._shapes[stride] = call
         return call, res
 
-    def _outputs(self, out, want):
+    def _outputs(self, out, want, stream):
         """The outputs ((name, sizes, dtype), ...), new or taken from `out`, and their pointers."""
         if out is None:
             import torch
+            if stream is not None:
+                with _on(stream, self.device):
+                    return self._outputs(None, want, None)
             out = {k: tuple(None if s is None else torch.empty(s, dtype=d, device=self.device) for s in sizes)
                    for k, sizes, d in want}
         elif len(out) != len(want) or any(k not in out for k, _, _ in want):
@@ -1024,10 +1037,11 @@ class AdaLN:
         """One struct of pointers per stream, its fields in order (None for a stream without tokens)."""
         return [cls(*[p[i] for p in pairs]) if self._live[i] else None for i in (0, 1)]
 
-    def _scratch(self):
+    def _scratch(self, stream):
         if self.workspace is None:
             import torch
-            self.workspace = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
+            with _on(stream, self.device):
+                self.workspace = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
         return self.workspace
 
     # ---- calls
@@ -1036,7 +1050,7 @@ class AdaLN:
         px = self._need("x", x, self.x_dtype, self._rows)
         call, (pscale, pshift) = self._mods(("scale", scale), ("shift", shift))
         pw = self._weights("w", w)
-        out, p = self._outputs(out, (("y", self._rows, self.y_dtype), ("stats", self._stats, self._f32)))
+        out, p = self._outputs(out, (("y", self._rows, self.y_dtype), ("stats", self._stats, self._f32)), stream)
         _require_current(self.device)
         io = self._structs(AdalnIo, px, _NONE, _NONE, pscale, pshift, pw, _NONE, _NONE, p["y"], p["stats"])
         rlk_adaln_modulation_fwd(call, io, _raw_stream(stream, self._index))
@@ -1056,7 +1070,7 @@ class AdaLN:
             want += (("y", self._rows, self.y_dtype), ("stats", self._stats, self._f32))
         if call.post:
             want.append(("post_stats", self._stats, self._f32))
-        out, p = self._outputs(out, want)
+        out, p = self._outputs(out, want, stream)
         _require_current(self.device)
         io = self._structs(AdalnIo, px, ph, pgate, pscale, pshift, pw, pwp, p["r"], p.get("y", _NONE),
                            p.get("stats", _NONE), p.get("post_stats", _NONE))
@@ -1076,11 +1090,11 @@ class AdaLN:
         want = [("dx", self._rows, self.x_dtype), ("dscale", self._sums, self._f32), ("dshift", self._sums, self._f32)]
         if pw is not _NONE:
             want.append(("dw", self._vector, self._f32))
-        out, p = self._outputs(out, want)
+        out, p = self._outputs(out, want, stream)
         _require_current(self.device)
         io = self._structs(AdalnIo, px, _NONE, _NONE, pscale, _NONE, pw, _NONE, _NONE, _NONE, pst)
         grad = self._structs(AdalnGrad, pdy, pdr, p["dx"], _NONE, _NONE, p["dscale"], p["dshift"], p.get("dw", _NONE))
-        rlk_adaln_modulation_bwd(call, io, grad, self._scratch(), self._ws_bytes, _raw_stream(stream, self._index))
+        rlk_adaln_modulation_bwd(call, io, grad, self._scratch(stream), self._ws_bytes, _raw_stream(stream, self._index))
         return out
 
     def gate_residual_bwd(self, r, h, gate, scale, stats, dy, dr=None, w=None, w_post=None, post_stats=None, out=None,
@@ -1109,12 +1123,12 @@ class AdaLN:
             pps = self._need("post_stats", post_stats, f32, self._stats)
             if pwp is not _NONE:
                 want.append(("dw_post", self._vector, f32))
-        out, p = self._outputs(out, want)
+        out, p = self._outputs(out, want, stream)
         _require_current(self.device)
         io = self._structs(AdalnIo, _NONE, ph, pgate, pscale, _NONE, pw, pwp, pr, _NONE, pst, pps)
         grad = self._structs(AdalnGrad, pdy, pdr, p["dx"], p["dh"], p["dgate"], p.get("dscale", _NONE),
                              p.get("dshift", _NONE), p.get("dw", _NONE), p.get("dw_post", _NONE))
-        rlk_adaln_gate_residual_bwd(call, io, grad, self._scratch(), self._ws_bytes, _raw_stream(stream, self._index))
+        rlk_adaln_gate_residual_bwd(call, io, grad, self._scratch(stream), self._ws_bytes, _raw_stream(stream, self._index))
         return out
 
 
@@ -1236,13 +1250,15 @@ class AdamW:
         import torch
         self._ready(grads)
         n = len(self.params)
-        if out is None:
-            out = torch.empty(2, dtype=torch.float32, device=self.device)
-        else:
+        if out is not None:
             self._dense("out", out, (torch.float32,), 2)
-        if self.workspace is None:
-            self.workspace = torch.empty(rlk_grad_norm_workspace_bytes(self._list, n), dtype=torch.uint8,
-                                         device=self.device)
+        if out is None or self.workspace is None:
+            with _on(stream, self.device):
+                if out is None:
+                    out = torch.empty(2, dtype=torch.float32, device=self.device)
+                if self.workspace is None:
+                    self.workspace = torch.empty(rlk_grad_norm_workspace_bytes(self._list, n), dtype=torch.uint8,
+                                                 device=self.device)
         rlk_grad_norm(self._list, n, pre_scale, max_norm, out, self.workspace, self.workspace.numel(),
                       _raw_stream(stream, self.device.index))
         return out

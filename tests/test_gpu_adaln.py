@@ -344,6 +344,41 @@ def test_graph_replay_and_other_streams(dev):
         assert Hh.bits_equal(f[k][1], want[0][0][k][1]), k
 
 
+def test_a_bf16_residual_rounds_its_product(dev):
+    """r = bf16(x + round(round(alpha * gate) * h)), so that ties stay ties."""
+    import torch
+    g = torch.Generator(device=dev).manual_seed(3)
+    x, h = (torch.randn(1, 300, 1096, generator=g, device=dev).bfloat16() for _ in range(2))
+    gate = (0.4 * torch.randn(1, 1096, generator=g, device=dev)).bfloat16()
+    op = pkg.AdaLN(1, 0, 300, 1096, alpha=0.7, device=dev)
+    r = op.gate_residual((None, x), (None, h), (None, gate), None, None, want_y=False)["r"][1]
+    share = torch.tensor(0.7, device=dev) * gate.float()
+    assert Hh.bits_equal(r, (x.float() + share[:, None] * h.float()).bfloat16())
+
+
+def test_results_on_a_stream_given_by_hand(dev):
+    """Buffers the call allocates must not be memory that the current stream still writes."""
+    import torch
+    c = Case(dev, 2, 40, 900, 1280, seed=5)
+    want = c.op.modulation(c.x, c.scale, c.shift)
+    grads = c.op.modulation_bwd(c.x, c.scale, want["stats"], c.dy, c.dr)
+    again = Case(dev, 2, 40, 900, 1280, seed=5)  # whose workspace does not exist yet
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for run, ref in ((lambda: again.op.modulation(c.x, c.scale, c.shift, stream=s), want),
+                     (lambda: again.op.modulation_bwd(c.x, c.scale, want["stats"], c.dy, c.dr, stream=s.cuda_stream), grads)):
+        junk = [torch.empty(n, dtype=torch.uint8, device=dev) for n in (2 ** 26, 2 ** 22, 2 ** 22, 2 ** 18, 2 ** 18, 2 ** 14)]
+        for _ in range(50):
+            for j in junk:
+                j.fill_(0x55)
+        del j, junk
+        got = run()
+        torch.cuda.synchronize()
+        for k in ref:
+            for i in (0, 1):
+                assert Hh.bits_equal(got[k][i], ref[k][i]), (k, i)
+
+
 def test_offsets_past_32_bits(dev):
     """An activation of more than 2^32 bytes and 2^31 elements: the last rows are computed like the first."""
     import torch
