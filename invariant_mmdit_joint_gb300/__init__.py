@@ -14,6 +14,7 @@ PyTorch is used only for device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from typing import Sequence
 
@@ -902,6 +903,22 @@ def _on(stream, device):
 _NONE = (None, None)
 
 
+class _Results(dict):
+    """What a call returned, with its pointers: passed back as ``out`` of the
+    same kind of call, it is looked at only for holding the same memory still
+    (checking seven pairs anew takes longer than the smallest kernels)."""
+
+    def __init__(self, kinds, names, pairs, pointers):
+        super().__init__(pairs)
+        self.kinds, self.names, self.pairs, self.pointers = kinds, names, list(pairs.values()), pointers
+        self.tensors = [t for pair in self.pairs for t in pair if t is not None]
+        self.addresses = [t.data_ptr() for t in self.tensors]
+
+    def fits(self, kinds, names):
+        return self.kinds is kinds and self.names == names and len(self) == len(self.pairs) and \
+            all(map(operator.is_, self.values(), self.pairs)) and [t.data_ptr() for t in self.tensors] == self.addresses
+
+
 class AdaLN:
     """Buffers + calls of the block's norms, modulation, gate and residual for
     one geometry: adaln_modulation before a sublayer's projections,
@@ -942,6 +959,11 @@ class AdaLN:
         self._stats = tuple(torch.Size((B, T, 2)) if T else None for T in (T_txt, T_img))
         self._sums = tuple(torch.Size((B, C)) if on else None for on in live)
         self._vector = tuple(torch.Size((C,)) if on else None for on in live)
+        # sizes and type of each output
+        x, y, f = self.x_dtype, self.y_dtype, self._f32
+        self._kinds = {"y": (self._rows, y), "r": (self._rows, x), "stats": (self._stats, f), "post_stats": (self._stats, f),
+                       "dx": (self._rows, x), "dh": (self._rows, y), "dgate": (self._sums, f), "dscale": (self._sums, f),
+                       "dshift": (self._sums, f), "dw": (self._vector, f), "dw_post": (self._vector, f)}
         self._shapes = {}  # the call's shape struct by the modulation's sample stride
         self.workspace = None  # of the backward, allocated at its first call
 
@@ -995,12 +1017,12 @@ class AdaLN:
             sh = self.shape
             raise ValueError(f"{name}[{i}] must be a {self.mod_dtype} [{sh.B}, {sh.C}] view with unit column stride on "
                              f"{self.device} (None without tokens), got {t.dtype} {tuple(t.shape)} on {t.device}")
-        strides.add(s[0])
+        strides.append(s[0])
         return t.data_ptr()
 
     def _mods(self, *named):
         """The call's shape (with the views' sample stride) and the pointers of pairs of [B, C] views."""
-        strides, res = set(), []
+        strides, res = [], []
         for name, pair in named:
             if pair is None:
                 res.append(_NONE)
@@ -1010,9 +1032,9 @@ class AdaLN:
             res.append((self._view(name, 0, pair[0], strides), self._view(name, 1, pair[1], strides)))
         stride = self.shape.C
         if strides and self.shape.B > 1:  # (a single sample's stride says nothing)
-            if len(strides) > 1:
-                raise ValueError(f"scale, shift and gate must have one sample stride, got {sorted(strides)}")
-            stride = strides.pop()
+            stride = strides[0]
+            if strides.count(stride) != len(strides):
+                raise ValueError(f"scale, shift and gate must have one sample stride, got {sorted(set(strides))}")
         call = self._shapes.get(stride)
         if call is None:
             call = AdalnShape.from_buffer_copy(self.shape)
@@ -1020,18 +1042,21 @@ class AdaLN:
             self._shapes[stride] = call
         return call, res
 
-    def _outputs(self, out, want, stream):
-        """The outputs ((name, sizes, dtype), ...), new or taken from `out`, and their pointers."""
+    def _outputs(self, out, names, stream):
+        """The outputs of these names, new or taken from `out`, and their pointers."""
+        of = self._kinds
+        if type(out) is _Results and out.fits(of, names):
+            return out, out.pointers
         if out is None:
             import torch
-            if stream is not None:
-                with _on(stream, self.device):
-                    return self._outputs(None, want, None)
-            out = {k: tuple(None if s is None else torch.empty(s, dtype=d, device=self.device) for s in sizes)
-                   for k, sizes, d in want}
-        elif len(out) != len(want) or any(k not in out for k, _, _ in want):
-            raise ValueError(f"out must hold {sorted(k for k, _, _ in want)}, got {sorted(out)}")
-        return out, {k: self._need(k, out[k], d, sizes) for k, sizes, d in want}
+            with _on(stream, self.device):
+                pairs = {k: tuple(None if s is None else torch.empty(s, dtype=of[k][1], device=self.device)
+                                  for s in of[k][0]) for k in names}
+            out = _Results(of, names, pairs, {k: self._need(k, pairs[k], of[k][1], of[k][0]) for k in names})
+            return out, out.pointers
+        if len(out) != len(names) or any(k not in out for k in names):
+            raise ValueError(f"out must hold {sorted(names)}, got {sorted(out)}")
+        return out, {k: self._need(k, out[k], of[k][1], of[k][0]) for k in names}
 
     def _structs(self, cls, *pairs):
         """One struct of pointers per stream, its fields in order (None for a stream without tokens)."""
@@ -1050,7 +1075,7 @@ class AdaLN:
         px = self._need("x", x, self.x_dtype, self._rows)
         call, (pscale, pshift) = self._mods(("scale", scale), ("shift", shift))
         pw = self._weights("w", w)
-        out, p = self._outputs(out, (("y", self._rows, self.y_dtype), ("stats", self._stats, self._f32)), stream)
+        out, p = self._outputs(out, ("y", "stats"), stream)
         _require_current(self.device)
         io = self._structs(AdalnIo, px, _NONE, _NONE, pscale, pshift, pw, _NONE, _NONE, p["y"], p["stats"])
         rlk_adaln_modulation_fwd(call, io, _raw_stream(stream, self._index))
@@ -1065,11 +1090,9 @@ class AdaLN:
         ph = self._need("h", h, self.y_dtype, self._rows)
         call, (pgate, pscale, pshift) = self._mods(("gate", gate), ("scale", scale), ("shift", shift))
         pw, pwp = self._weights("w", w), self._weights("w_post", w_post)
-        want = [("r", self._rows, self.x_dtype)]
-        if want_y:
-            want += (("y", self._rows, self.y_dtype), ("stats", self._stats, self._f32))
+        want = ("r", "y", "stats") if want_y else ("r",)
         if call.post:
-            want.append(("post_stats", self._stats, self._f32))
+            want += ("post_stats",)
         out, p = self._outputs(out, want, stream)
         _require_current(self.device)
         io = self._structs(AdalnIo, px, ph, pgate, pscale, pshift, pw, pwp, p["r"], p.get("y", _NONE),
@@ -1087,9 +1110,7 @@ class AdaLN:
         pdr = _NONE if dr is None else self._need("dr", dr, self.x_dtype, self._rows)
         call, (pscale,) = self._mods(("scale", scale))
         pw = self._weights("w", w)
-        want = [("dx", self._rows, self.x_dtype), ("dscale", self._sums, self._f32), ("dshift", self._sums, self._f32)]
-        if pw is not _NONE:
-            want.append(("dw", self._vector, self._f32))
+        want = ("dx", "dscale", "dshift") if pw is _NONE else ("dx", "dscale", "dshift", "dw")
         out, p = self._outputs(out, want, stream)
         _require_current(self.device)
         io = self._structs(AdalnIo, px, _NONE, _NONE, pscale, _NONE, pw, _NONE, _NONE, _NONE, pst)
@@ -1103,7 +1124,7 @@ class AdaLN:
         dh, dgate, with dy (None: y was not used) dscale and dshift, with w
         dw, with w_post dw_post. dr is the gradient that reaches r by the
         residual path. ``out`` may hold dr itself as dx."""
-        f32, rows, sums = self._f32, self._rows, self._sums
+        f32, rows = self._f32, self._rows
         pr = self._need("r", r, self.x_dtype, rows)
         ph = self._need("h", h, self.y_dtype, rows)
         if dy is None and dr is None:
@@ -1111,18 +1132,16 @@ class AdaLN:
         pdr = _NONE if dr is None else self._need("dr", dr, self.x_dtype, rows)
         call, (pgate, pscale) = self._mods(("gate", gate), ("scale", scale))
         pw, pwp = self._weights("w", w), self._weights("w_post", w_post)
-        want = [("dx", rows, self.x_dtype), ("dh", rows, self.y_dtype), ("dgate", sums, f32)]
+        want = ("dx", "dh", "dgate")
         pdy = pst = pps = _NONE
         if dy is not None:
             pdy = self._need("dy", dy, self.y_dtype, rows)
             pst = self._need("stats", stats, f32, self._stats)
-            want += (("dscale", sums, f32), ("dshift", sums, f32))
-            if pw is not _NONE:
-                want.append(("dw", self._vector, f32))
+            want += ("dscale", "dshift") if pw is _NONE else ("dscale", "dshift", "dw")
         if call.post:
             pps = self._need("post_stats", post_stats, f32, self._stats)
             if pwp is not _NONE:
-                want.append(("dw_post", self._vector, f32))
+                want += ("dw_post",)
         out, p = self._outputs(out, want, stream)
         _require_current(self.device)
         io = self._structs(AdalnIo, _NONE, ph, pgate, pscale, _NONE, pw, pwp, pr, _NONE, pst, pps)

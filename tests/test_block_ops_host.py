@@ -262,6 +262,31 @@ def test_adaln_binding_refuses_unfit_tensors(L):
         one.modulation((x[0], x[1]), s, s)  # a text without tokens
 
 
+def test_adaln_results_passed_back_are_looked_at(L):
+    torch = pytest.importorskip("torch")
+    op, names = pkg.AdaLN(2, 3, 5, 64, device="cpu"), ("y", "stats")
+    out, p = op._outputs(None, names, None)
+    assert op._outputs(out, names, None) == (out, p) and out["y"][1].data_ptr() == p["y"][1]
+    held = out["y"]
+    out["y"] = (held[0], torch.zeros_like(held[1]))  # another buffer: taken as such
+    assert op._outputs(out, names, None)[1]["y"] == tuple(t.data_ptr() for t in out["y"])
+    out["y"] = held
+    held[1].data = torch.zeros_like(held[1])  # the same tensor over other memory
+    assert op._outputs(out, names, None)[1]["y"][1] == held[1].data_ptr()
+    held[1].data = torch.zeros(5, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="y.1."):
+        op._outputs(out, names, None)
+    held[1].data = torch.zeros(2, 5, 64, dtype=torch.bfloat16)
+    for other in (pkg.AdaLN(2, 3, 4, 64, device="cpu"), pkg.AdaLN(2, 3, 5, 64, y_dtype=torch.float32, x_dtype=torch.float32, device="cpu")):
+        with pytest.raises(ValueError):
+            other._outputs(out, names, None)
+    with pytest.raises(ValueError, match="must hold"):
+        op._outputs(out, ("y", "stats", "r"), None)
+    out.pop("stats")
+    with pytest.raises(ValueError, match="must hold"):
+        op._outputs(out, names, None)
+
+
 def test_adamw_binding_refuses_unfit_tensors(L):
     torch = pytest.importorskip("torch")
     p = [torch.zeros(5, 7), torch.zeros(33, dtype=torch.bfloat16)]
