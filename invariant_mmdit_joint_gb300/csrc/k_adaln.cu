@@ -256,15 +256,18 @@ __device__ __forceinline__ float2 row_stats(const V8 (&v)[NV], bool rms, const R
 
 // Sums of two values over the CTA. The halves of a warp take one value each
 // (one exchange, then four steps on one value instead of five on two), and
-// the warps' sums are joined the same way. buf: [2][16] as above.
+// the warps' sums are joined the same way. buf: 16 slots for each value, zero
+// as above, and 16 more for each behind them if there can be more warps.
+template <bool MANY>
 __device__ __forceinline__ float2 block_sum2(float x, float y, int tid, int warps, float* buf) {
     const int lane = tid % 32;
     const bool upper = lane >= 16;
     float v = half_sum((upper ? y : x) + __shfl_xor_sync(0xffffffffu, upper ? x : y, 16));
     if (warps > 1) {
-        if (lane % 16 == 0) buf[(lane & 16) + tid / 32] = v;
+        const int warp = tid / 32;
+        if (lane % 16 == 0) buf[(lane & 16) + (MANY ? warp % 16 + warp / 16 * 32 : warp)] = v;
         __syncthreads();
-        v = half_sum(buf[lane]);
+        v = half_sum(MANY ? buf[lane] + buf[lane + 32] : buf[lane]);
     }
     const float other = __shfl_xor_sync(0xffffffffu, v, 16);
     return upper ? make_float2(other, v) : make_float2(v, other);
@@ -418,26 +421,29 @@ __global__ void __launch_bounds__(THREADS, kFwdCtas<NV, THREADS, GATE>) adaln_fw
 // order.
 template <typename X, typename Y, bool GATE>
 constexpr int kBwdRow = 2 * kPieces<X> + (GATE ? 2 : 1) * kPieces<Y>;  // pieces of 8 columns: x, dr, dy, h
-// CTAs of an SM that the registers are held to (96 a thread up to 320 of
-// them; 64 and three CTAs left the 1024^2 modulation as it was, 42 us).
-template <int NV, int THREADS>
-constexpr int kBwdCtas = NV == 2 ? 1 : 680 / THREADS;
+// CTAs of an SM that the registers are held to: 96 a thread up to 320 of them
+// (64 and three CTAs left the 1024^2 modulation as it was, 42 us). Of 512
+// threads two CTAs of 64 without a gate (1024^2 pair at C = 4096: 64 us, 75 with
+// one CTA of 101), one with it (two spill: 97 us, 125).
+template <int NV, int THREADS, bool GATE>
+constexpr int kBwdCtas = NV == 2 || THREADS > 512 ? 1 : (THREADS == 512 && !GATE ? 2 : 680 / THREADS);
 // Stages: four, or as many as let that many CTAs share the shared memory.
 template <typename X, typename Y, int NV, int THREADS, bool GATE>
-constexpr int kBwdFit = 220 * 1024 / kBwdCtas<NV, THREADS> / (16 * THREADS * NV * kBwdRow<X, Y, GATE>);
+constexpr int kBwdFit = 220 * 1024 / kBwdCtas<NV, THREADS, GATE> / (16 * THREADS * NV * kBwdRow<X, Y, GATE>);
 template <typename X, typename Y, int NV, int THREADS, bool GATE>
 constexpr int kBwdStages = kBwdFit<X, Y, NV, THREADS, GATE> >= 4
                                ? 4
                                : (kBwdFit<X, Y, NV, THREADS, GATE> >= 1 ? kBwdFit<X, Y, NV, THREADS, GATE> : 1);
 
 template <typename X, typename Y, int NV, int THREADS, bool GATE, bool POST>
-__global__ void __launch_bounds__(THREADS, kBwdCtas<NV, THREADS>) adaln_bwd_kernel(const __grid_constant__ AdalnArgs a) {
+__global__ void __launch_bounds__(THREADS, kBwdCtas<NV, THREADS, GATE>) adaln_bwd_kernel(const __grid_constant__ AdalnArgs a) {
     constexpr int STAGES = kBwdStages<X, Y, NV, THREADS, GATE>, PITCH = 16 * THREADS;
     constexpr int kX = NV * kPieces<X>, kY = NV * kPieces<Y>;
     constexpr int kDr = kX, kDy = 2 * kX, kH = 2 * kX + kY;  // a row's pieces: x, dr, dy, h
     constexpr int kRow = 2 * kX + kY + (GATE ? kY : 0);
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float buf[2][32];
+    constexpr bool MANY = THREADS > 512;
+    __shared__ float buf[2][MANY ? 64 : 32];
     const int tid = kept((int)threadIdx.x), threads = blockDim.x, C = kept(a.C), warps = kept(threads / 32);
     const int col = 8 * tid;
     const int units_txt = a.B * a.s[0].chunks, units = units_txt + a.B * a.s[1].chunks;
@@ -501,7 +507,9 @@ __global__ void __launch_bounds__(THREADS, kBwdCtas<NV, THREADS>) adaln_bwd_kern
     };
 #pragma unroll
     for (int k = 0; k < STAGES - 1; ++k) fill(ring + k * stage_bytes);
-    if (tid < 32) buf[0][tid] = buf[1][tid] = 0.0f;
+    if (tid < 32)
+#pragma unroll
+        for (int i = 0; i < (MANY ? 64 : 32); i += 32) buf[0][i + tid] = buf[1][i + tid] = 0.0f;
     __syncthreads();
     V8 sum_a[NV], sum_s[NV], sum_g[NV], k[NV], kg[NV];
     uint32_t stage = 0, filled = (STAGES - 1) * stage_bytes;  // to read, to fill
@@ -558,7 +566,7 @@ __global__ void __launch_bounds__(THREADS, kBwdCtas<NV, THREADS>) adaln_bwd_kern
                 }
                 const float s1 = thread_sum<NV>(last, [&](uint64_t& q, int j) { sum8(q, d[j]); });
                 const float s2 = thread_sum<NV>(last, [&](uint64_t& q, int j) { dot8(q, d[j], hat[j]); });
-                const float2 c12 = block_sum2(s1, s2, tid, warps, buf[parity]);
+                const float2 c12 = block_sum2<MANY>(s1, s2, tid, warps, buf[parity]);
                 parity ^= 1;
                 // d = dr + rstd * (e - mean(e) - hat * mean(e * hat))
                 const V8 c1 = v8_all(rms ? 0.0f : -ms.y * (c12.x * inv_c)), c2 = v8_all(-ms.y * (c12.y * inv_c));
@@ -582,7 +590,7 @@ __global__ void __launch_bounds__(THREADS, kBwdCtas<NV, THREADS>) adaln_bwd_kern
             if (POST) {
                 const float s1 = thread_sum<NV>(last, [&](uint64_t& q, int j) { sum8(q, d[j]); });
                 const float s2 = thread_sum<NV>(last, [&](uint64_t& q, int j) { dot8(q, d[j], hat[j]); });
-                const float2 c12 = block_sum2(s1, s2, tid, warps, buf[parity]);
+                const float2 c12 = block_sum2<MANY>(s1, s2, tid, warps, buf[parity]);
                 parity ^= 1;
                 const V8 c1 = v8_all(post_rms ? 0.0f : -ps.y * (c12.x * inv_c)), c2 = v8_all(-ps.y * (c12.y * inv_c));
 #pragma unroll
@@ -736,16 +744,23 @@ cudaError_t bwd_launch(const AdalnArgs& a, cudaStream_t s) {
     kernel<<<(unsigned)(units < ctas ? units : ctas), threads, kSmem, s>>>(a);
     return cudaGetLastError();
 }
-// 8 columns a thread up to C = 4096: with 16 the sums and factors leave room
-// for one CTA an SM (1024^2 modulation 47 us for 51, the 1328^2 gate 175 for
-// 220). Built for four numbers of threads, which fix the registers' limit and the
-// ring's layout.
+// 8 columns a thread up to C = 4096, with a gate up to 6144: with 16 the sums
+// and factors leave room for one CTA an SM (1024^2 modulation 47 us for 51, the
+// 1328^2 gate 175 for 220), and 512 threads of 128 registers spill those of a
+// gate (1024^2 pair, C = 5120: 158 us, 118 with 640 threads; C = 6144: 189 and
+// 143 with 768; C = 8192 would leave 64 a thread: 232, 269 with 1024). A
+// modulation at C = 6144 takes 104 us, 110 with 768. Built for these numbers
+// of threads, which fix the registers' limit and the ring's layout.
 template <typename X, typename Y, bool GATE, bool POST>
 cudaError_t bwd_nv(const AdalnArgs& a, cudaStream_t s) {
     if (a.C <= 512) return bwd_launch<X, Y, 1, 64, GATE, POST>(a, s);
     if (a.C <= 1280) return bwd_launch<X, Y, 1, 160, GATE, POST>(a, s);
     if (a.C <= 2560) return bwd_launch<X, Y, 1, 320, GATE, POST>(a, s);
     if (a.C <= 4096) return bwd_launch<X, Y, 1, 512, GATE, POST>(a, s);
+    if constexpr (GATE) {
+        if (a.C <= 5120) return bwd_launch<X, Y, 1, 640, GATE, POST>(a, s);
+        if (a.C <= 6144) return bwd_launch<X, Y, 1, 768, GATE, POST>(a, s);
+    }
     return bwd_launch<X, Y, 2, 512, GATE, POST>(a, s);
 }
 
