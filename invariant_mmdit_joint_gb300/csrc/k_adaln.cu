@@ -723,8 +723,12 @@ cudaError_t fwd_launch(const AdalnArgs& a, cudaStream_t s) {
 }
 // 8 columns a thread up to C = 1024, else 16: half the warps join a row, and
 // more rows are under way on an SM (1024^2 modulation 21.2 us, 25.6 with 8).
+// A gate's ring of one warp is laid out for one, or it bounds the CTAs of an SM
+// (8 x 3114 fp32 rows of 136 columns 18.5 us in the ring of four, 15.1).
 template <typename X, typename Y, bool GATE, bool POST>
 cudaError_t fwd_nv(const AdalnArgs& a, cudaStream_t s) {
+    if constexpr (GATE)
+        if (a.C <= 256) return fwd_launch<X, Y, 1, 32, GATE, POST>(a, s);
     if (a.C <= 1024) return fwd_launch<X, Y, 1, 128, GATE, POST>(a, s);
     if (a.C <= 2560) return fwd_launch<X, Y, 2, 160, GATE, POST>(a, s);
     if (a.C <= 4096) return fwd_launch<X, Y, 2, 256, GATE, POST>(a, s);
