@@ -1235,7 +1235,7 @@ class AdamW:
     def _take(self, grads):
         """The list's gradient buffers from now on."""
         import torch
-        grads = list(grads)
+        grads = tuple(grads)
         if len(grads) != len(self.params):
             raise ValueError(f"expected {len(self.params)} gradients, got {len(grads)}")
         for i, (g, p) in enumerate(zip(grads, self.params)):
@@ -1251,8 +1251,6 @@ class AdamW:
             self._take(grads)
         if self.grads is None:
             raise ValueError("no gradients given")
-        if [p.data_ptr() for p in self.params] != self._pointers:
-            raise ValueError("a parameter's data was replaced: copy_ into it, or make a new object")
         _require_current(self.device)
 
     def _scalar(self, name, t, dtype):
@@ -1290,6 +1288,8 @@ class AdamW:
         value on the device, such as grad_norm(...)[1:]; if it is not finite
         nothing is changed."""
         import torch
+        if list(map(torch.Tensor.data_ptr, self.params)) != self._pointers:
+            raise ValueError("a parameter's data was replaced: copy_ into it, or make a new object")
         self._ready(grads)
         a = self._args
         a.step_dev = a.lr_dev = None
