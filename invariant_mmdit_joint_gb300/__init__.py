@@ -890,14 +890,14 @@ def _raw_stream(stream, index) -> int:
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _on(stream, device):
-    """Context in which memory is allocated for a call on `stream`: what the
-    allocator hands out is free there, and maybe not yet on another stream."""
-    import contextlib
+def _empty(size, dtype, device, stream):
+    """Memory for a call on `stream`: what the allocator hands out for a stream
+    is free there, and maybe not yet on another one."""
     import torch
     if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream)
+        return torch.empty(size, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream):
+        return torch.empty(size, dtype=dtype, device=device)
 
 
 _NONE = (None, None)
@@ -1048,10 +1048,8 @@ class AdaLN:
         if type(out) is _Results and out.fits(of, names):
             return out, out.pointers
         if out is None:
-            import torch
-            with _on(stream, self.device):
-                pairs = {k: tuple(None if s is None else torch.empty(s, dtype=of[k][1], device=self.device)
-                                  for s in of[k][0]) for k in names}
+            pairs = {k: tuple(None if s is None else _empty(s, of[k][1], self.device, stream) for s in of[k][0])
+                     for k in names}
             out = _Results(of, names, pairs, {k: self._need(k, pairs[k], of[k][1], of[k][0]) for k in names})
             return out, out.pointers
         if len(out) != len(names) or any(k not in out for k in names):
@@ -1065,8 +1063,7 @@ class AdaLN:
     def _scratch(self, stream):
         if self.workspace is None:
             import torch
-            with _on(stream, self.device):
-                self.workspace = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
+            self.workspace = _empty(self._ws_bytes, torch.uint8, self.device, stream)
         return self.workspace
 
     # ---- calls
@@ -1267,15 +1264,12 @@ class AdamW:
         import torch
         self._ready(grads)
         n = len(self.params)
-        if out is not None:
+        if out is None:
+            out = _empty(2, torch.float32, self.device, stream)
+        else:
             self._dense("out", out, (torch.float32,), 2)
-        if out is None or self.workspace is None:
-            with _on(stream, self.device):
-                if out is None:
-                    out = torch.empty(2, dtype=torch.float32, device=self.device)
-                if self.workspace is None:
-                    self.workspace = torch.empty(rlk_grad_norm_workspace_bytes(self._list, n), dtype=torch.uint8,
-                                                 device=self.device)
+        if self.workspace is None:
+            self.workspace = _empty(rlk_grad_norm_workspace_bytes(self._list, n), torch.uint8, self.device, stream)
         rlk_grad_norm(self._list, n, pre_scale, max_norm, out, self.workspace, self.workspace.numel(),
                       _raw_stream(stream, self.device.index))
         return out
