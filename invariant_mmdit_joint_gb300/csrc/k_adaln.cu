@@ -280,10 +280,12 @@ __device__ __forceinline__ float2 block_sum2(float x, float y, int tid, int warp
 constexpr int kFwdStages = 3;
 // CTAs of an SM that the registers are held to. A modulation's 83 a thread
 // leave room for four CTAs of 160 threads; 72 and five of them are faster
-// (1024^2, 19.3 -> 18.7 us). With a gate the same spills (78 -> 81 us at four
-// CTAs of 121 registers held to 96).
+// (1024^2, 19.3 -> 18.7 us). A gate with a norm after spills in more than its
+// own three (78 us, 81 with four), but not with two CTAs of 256 or 320 threads,
+// of which its 131 would leave one (1024^2 pair, C = 4096: 77 -> 53 us, C = 5120:
+// 87 -> 63; two of 384 gained nothing, and without a norm after lost 74 -> 89).
 template <int NV, int THREADS, bool GATE>
-constexpr int kFwdCtas = GATE || 820 / THREADS < 1 ? 1 : 820 / THREADS;
+constexpr int kFwdCtas = GATE ? (THREADS == 256 || THREADS == 320 ? 2 : 1) : (THREADS >= 512 ? 1 : 820 / THREADS);
 
 template <typename X, typename Y, int NV, int THREADS, bool GATE, bool POST>
 __global__ void __launch_bounds__(THREADS, kFwdCtas<NV, THREADS, GATE>) adaln_fwd_kernel(const __grid_constant__ AdalnArgs a) {
@@ -732,6 +734,9 @@ cudaError_t fwd_nv(const AdalnArgs& a, cudaStream_t s) {
     if (a.C <= 1024) return fwd_launch<X, Y, 1, 128, GATE, POST>(a, s);
     if (a.C <= 2560) return fwd_launch<X, Y, 2, 160, GATE, POST>(a, s);
     if (a.C <= 4096) return fwd_launch<X, Y, 2, 256, GATE, POST>(a, s);
+    if (a.C <= 5120) return fwd_launch<X, Y, 2, 320, GATE, POST>(a, s);
+    if constexpr (!GATE)  // (55 -> 40 us at 6144 columns with two CTAs)
+        if (a.C <= 6144) return fwd_launch<X, Y, 2, 384, GATE, POST>(a, s);
     return fwd_launch<X, Y, 2, 512, GATE, POST>(a, s);
 }
 
