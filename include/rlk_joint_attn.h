@@ -460,7 +460,7 @@ rlk_status rlk_attn_out_bias_gemm(const rlk_ja_shape* shape,
  *   f = alpha * gate_b * d;  dh = f, or through the norm of h likewise;
  *   dgate_b = alpha * w_post * G_b, dw_post = alpha * sum_b gate_b * G_b with
  *            G_b = sum_t d * hat(h) (sum_t d * h without a norm after)
- * Sums over tokens run in chunks whose length depends on the stream's T alone,
+ * Sums over tokens run in chunks whose length depends on the stream's T and on C,
  * chunks ascending, then b ascending, in fp32 and without atomics: a sample's
  * gradients do not depend on its batch.
  *

@@ -786,11 +786,19 @@ cudaError_t bwd_xy(const AdalnArgs& a, bool gate, cudaStream_t s) {
 
 }  // namespace
 
-// Rows of a chunk, from T alone: long ones write and fold fewer sums (1328^2
-// gate, T = 6889: 160 us with 32 rows, 165 with 16, 180 with 8), short ones
-// spread few rows over the SMs (1024^2 modulation, T = 4096: 49, 42, 46 us; T =
-// 513: 16.3 us with 4 rows for 18.6 with 8).
-int adaln_chunk_rows(int T) { return T >= 4096 ? 16 : (T >= 2048 ? 8 : (T >= 128 ? 4 : (T > 32 ? 2 : 1))); }
+// Rows of a chunk, from T and C alone: long ones write and fold fewer sums
+// (1328^2 gate, T = 6889: 160 us with 32 rows, 165 with 16, 180 with 8), short
+// ones spread few rows over the SMs (1024^2 modulation, T = 4096: 49, 42, 46 us;
+// T = 513: 16.3 us with 4 rows for 18.6 with 8). Narrow rows leave room for more
+// CTAs, which 16-row chunks do not fill: 8 for 16 took 0.72 to 0.94 of the
+// time at T = 4096 and C <= 512 and as long with 8 samples of T = 6889, at
+// C = 768 .. 1280 0.76 to 0.94 with one or two samples and up to 1.04 with
+// four, but 1.05 to 1.10 with those of T = 6889. (4 rows there, and 2 below T =
+// 2048, gain up to a quarter with one sample and lose as much with four.)
+int adaln_chunk_rows(int T, int C) {
+    if (T >= 4096) return C <= 512 || (C <= 1280 && T < 6144) ? 8 : 16;
+    return T >= 2048 ? 8 : (T >= 128 ? 4 : (T > 32 ? 2 : 1));
+}
 
 cudaError_t launch_adaln_fwd(const AdalnArgs& a, bool gate, cudaStream_t s) {
     timing_begin(kKAdalnFwd, s);

@@ -278,7 +278,7 @@ constexpr const char* kAdalnPolicy =
     "the norm reads the rounded residual";
 constexpr const char* kAdalnRowOrder = "row sums: 8 columns per thread, xor 16..1, warps ascending";
 constexpr const char* kAdalnSumOrder =
-    "row sums as in the forward; column sums: token chunks (by T), their runs in order, then b ascending";
+    "row sums as in the forward; column sums: token chunks (by T, C), their runs in order, then b ascending";
 const OpInfo kOps[] = {
     {"qk_rmsnorm+multi_axis_rope+joint_attention_fused", "rlk_joint_attn_fwd", kFwdPolicy, kFwdOrder},
     {"joint_attention_fused backward", "rlk_joint_attn_bwd",
@@ -1128,7 +1128,7 @@ static AdalnArgs adaln_args(const rlk_adaln_shape* sh) {
     for (int i = 0; i < 2; ++i) {
         AdalnStream& s = a.s[i];
         s.T = i == 0 ? sh->T_txt : sh->T_img;
-        s.chunk_rows = adaln_chunk_rows(s.T);
+        s.chunk_rows = adaln_chunk_rows(s.T, sh->C);
         s.chunks = (s.T + s.chunk_rows - 1) / s.chunk_rows;
     }
     return a;

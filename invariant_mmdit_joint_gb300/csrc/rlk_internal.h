@@ -270,7 +270,7 @@ struct AdalnArgs {
     bool x_fp32, y_fp32, mod_fp32;
     float eps, alpha;
 };
-int adaln_chunk_rows(int T);
+int adaln_chunk_rows(int T, int C);
 cudaError_t launch_adaln_fwd(const AdalnArgs& a, bool gate, cudaStream_t s);
 cudaError_t launch_adaln_bwd(const AdalnArgs& a, bool gate, cudaStream_t s);
 int probe_adaln_tu(void);

@@ -192,7 +192,7 @@ def test_non_finite_rows_stay_in_their_row(dev):
         assert Hh.bits_equal(got["y"][i][keep.to(dev)], clean["y"][i][keep.to(dev)])
 
 
-@pytest.mark.parametrize("T", [1, 3, 40, 700, 2100])
+@pytest.mark.parametrize("T", [1, 3, 40, 700, 2100, 4100, 6200])
 def test_a_sample_does_not_depend_on_its_batch(dev, T):
     """Rows, statistics and per-sample gradients of a sample alone, first and last in a batch: the same bytes."""
     B = 5
