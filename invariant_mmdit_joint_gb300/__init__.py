@@ -1035,6 +1035,8 @@ class AdaLN:
             stride = strides[0]
             if strides.count(stride) != len(strides):
                 raise ValueError(f"scale, shift and gate must have one sample stride, got {sorted(set(strides))}")
+            if stride < self.shape.C:
+                raise ValueError(f"scale, shift and gate need rows of their own for every sample, got the stride {stride}")
         call = self._shapes.get(stride)
         if call is None:
             call = AdalnShape.from_buffer_copy(self.shape)

@@ -249,6 +249,9 @@ def test_adaln_binding_refuses_unfit_tensors(L):
     for over in bad:
         with pytest.raises(ValueError):
             op.modulation(**{**good, **over})
+    one_row = (mod[:1, :64].expand(2, 64),) * 2
+    with pytest.raises(ValueError, match="every sample"):
+        op.modulation(x=x, scale=one_row, shift=one_row)
     with pytest.raises(ValueError, match="CUDA"):
         op.modulation(**good)
     with pytest.raises(ValueError):

@@ -116,3 +116,43 @@ def test_block_step(dev):
             (ref, _, _), (pe, _, _) = O.adamw(f64(p0), f64(t), 0.0, 0.0, lr=1e-2, beta1=0.9, beta2=0.95, eps=1e-8,
                                               weight_decay=0.0, step=1, scale=f64(n)[1])
             assert np.all(np.abs(f64(p1) - ref) <= pe)
+
+
+def test_calls_on_two_streams_at_once(dev):
+    """Objects of their own on two streams, their kernels in flight together: the bytes of one stream alone."""
+    import torch
+    g = torch.Generator(device=dev).manual_seed(5)
+
+    def r(*shape):
+        return torch.randn(shape, generator=g, device=dev).bfloat16()
+    B, T, C = 2, (40, 1500), 1280
+    x, h, dy, dr = (tuple(r(B, t, C) for t in T) for _ in range(4))
+    mods = tuple(r(B, 3 * C) for _ in T)
+    scale, shift, gate = (tuple(m[:, i * C:(i + 1) * C] for m in mods) for i in range(3))
+    grads = [torch.randn(n, generator=g, device=dev) for n in (300_001, 70_000, 33)]
+
+    def job():
+        op = pkg.AdaLN(B, *T, C, device=dev)
+        opt = pkg.AdamW([torch.zeros_like(d) for d in grads], state_bits=8, grads=grads)
+
+        def run(t):
+            f = op.gate_residual(x, h, gate, scale, shift)
+            q = op.gate_residual_bwd(f["r"], h, gate, scale, f["stats"], dy, dr)
+            n = opt.grad_norm(1.0)
+            opt.step(t, grad_scale=n[1:])
+            return [t for d in (f, q) for k in sorted(d) for t in d[k]] + [n]
+        return run, opt
+    results = []
+    for streams in ([torch.cuda.current_stream()], [torch.cuda.Stream(), torch.cuda.Stream()]):
+        jobs = [job() for _ in streams]
+        torch.cuda.synchronize()
+        outs = [[] for _ in streams]
+        for t in range(1, 9):
+            for (run, _), s, o in zip(jobs, streams, outs):
+                with torch.cuda.stream(s):
+                    o += run(t)
+        torch.cuda.synchronize()
+        results += [o + list(opt.params + opt.m + opt.v) for o, (_, opt) in zip(outs, jobs)]
+    for other in results[1:]:
+        for a, b in zip(results[0], other):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
