@@ -425,12 +425,18 @@ __global__ void __launch_bounds__(THREADS, kFwdCtas<NV, THREADS, GATE>) adaln_fw
 // order.
 template <typename X, typename Y, bool GATE>
 constexpr int kBwdRow = 2 * kPieces<X> + (GATE ? 2 : 1) * kPieces<Y>;  // pieces of 8 columns: x, dr, dy, h
-// CTAs of an SM that the registers are held to: 96 a thread up to 320 of them
-// (64 and three CTAs left the 1024^2 modulation as it was, 42 us). Of 512
-// threads two CTAs of 64 without a gate (1024^2 pair at C = 4096: 64 us, 75 with
-// one CTA of 101), one with it (two spill: 97 us, 125).
+// CTAs of an SM that the registers are held to. Without a gate 96 registers a
+// thread (64 and three CTAs left the 1024^2 modulation as it was, 42 us), of
+// 512 threads 64 and two CTAs (1024^2 pair at C = 4096: 64 us, 75 with one CTA
+// of 101). A gate uses up to 128, and fewer CTAs that have them are faster
+// (four samples at 1328^2 with a norm after: C = 768 81 -> 67 us, C = 1920 with
+// 256 threads for 320 168 -> 151; the worst, 1024^2 at C = 1280 without it, 32
+// -> 34), but not one of 320 threads for two, nor two of 512 of 64 registers
+// (C = 4096 97 us, 125).
 template <int NV, int THREADS, bool GATE>
-constexpr int kBwdCtas = NV == 2 || THREADS > 512 ? 1 : (THREADS == 512 && !GATE ? 2 : 680 / THREADS);
+constexpr int kBwdCtas = NV == 2 || THREADS > 512 ? 1
+                         : GATE ? (THREADS == 320 ? 2 : 512 / THREADS)
+                                : (THREADS == 512 ? 2 : 680 / THREADS);
 // Stages: four, or as many as let that many CTAs share the shared memory.
 template <typename X, typename Y, int NV, int THREADS, bool GATE>
 constexpr int kBwdFit = 220 * 1024 / kBwdCtas<NV, THREADS, GATE> / (16 * THREADS * NV * kBwdRow<X, Y, GATE>);
@@ -769,6 +775,8 @@ template <typename X, typename Y, bool GATE, bool POST>
 cudaError_t bwd_nv(const AdalnArgs& a, cudaStream_t s) {
     if (a.C <= 512) return bwd_launch<X, Y, 1, 64, GATE, POST>(a, s);
     if (a.C <= 1280) return bwd_launch<X, Y, 1, 160, GATE, POST>(a, s);
+    if constexpr (GATE)
+        if (a.C <= 2048) return bwd_launch<X, Y, 1, 256, GATE, POST>(a, s);
     if (a.C <= 2560) return bwd_launch<X, Y, 1, 320, GATE, POST>(a, s);
     if (a.C <= 4096) return bwd_launch<X, Y, 1, 512, GATE, POST>(a, s);
     if constexpr (GATE) {

@@ -88,7 +88,8 @@ SHAPES = [
     (1, 0, 1, 8), (2, 1, 0, 8), (3, 1, 2, 264), (1, 16, 64, 256), (2, 5, 131, 1160), (5, 9, 33, 136),
     (1, 3, 17, 4096), (2, 2, 5, 4104), (1, 1, 3, 8192), (2, 31, 1037, 200),
     # each number of threads at its edges
-    (2, 3, 9, 2568), (1, 2, 7, 5120), (2, 5, 3, 5128), (1, 3, 6, 6144), (2, 2, 3, 6152),
+    (1, 2, 5, 512), (2, 3, 4, 1288), (1, 5, 6, 2048), (2, 1, 3, 2056), (2, 3, 9, 2568),
+    (1, 2, 7, 5120), (2, 5, 3, 5128), (1, 3, 6, 6144), (2, 2, 3, 6152),
 ]
 KINDS = [
     dict(norm="layer", post="none", x="bf16", y="bf16", mod="bf16", weights=False, alpha=1.0),
