@@ -556,7 +556,7 @@ rlk_status rlk_adaln_gate_residual_bwd(const rlk_adaln_shape* shape, const rlk_a
  *   p -= rate * weight_decay * p
  *        + rate / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  * in fp32, quotient and square root within one unit in the last place; m and v
- * as fma(beta, state, (1 - beta) * g') and fma(beta, state, ((1 - beta) * g') * g').
+ * take each product and sum rounded by itself, the last one ((1 - beta2) g') g'.
  *
  * Parameters: fp32 (p, master NULL), or bf16 with an fp32 master: the master
  * is updated and p receives its bf16 rounding.

@@ -4,7 +4,7 @@
 // 28 bytes an element with fp32 states (p, g, m, v read; p, m, v written), 16
 // with 8-bit ones and bf16 gradients. Measured: 45 million elements, fp32
 // states, 185.5 us (6.8 TB/s, the copy bandwidth); 166 million, 8-bit
-// states, 448 us (6.0 TB/s, 0.88), there near the issue limit too: 82
+// states, 455 us (5.9 TB/s, 0.86), there near the issue limit too: 83
 // instructions an element (105 and 600 us with one element at a time, sqrtf
 // and the division, and nothing fetched ahead).
 //
@@ -263,7 +263,7 @@ __device__ __forceinline__ uint2 encode8(const V8& q, float t, const uint32_t (&
 
 // ------------------------------------------------------------ AdamW
 struct Scalars {
-    float s, b1, b2, o1, o2, inv_c2, eps, step, decay;  // step = rate / (1 - beta1^t); decay = rate * weight decay
+    float s, b1, b2, o1, o2, inv_c2, eps, none, step, decay;  // step = rate / (1 - beta1^t); decay = rate * weight decay
 };
 
 // m / (sqrt(v) * c + eps), each of the two within one unit in the last place:
@@ -302,13 +302,16 @@ __device__ __forceinline__ V8 quotient8(const V8& m, const V8& v, float top, flo
 }
 
 // New m, v and p of 8 elements from g (unscaled), and the largest v (NaN if
-// one is). The 8-bit codes follow from the bits of m and v, so their rounding is
-// written out: the gradient's product, then one fma (left as a product and a
-// sum the compiler would choose one).
+// one is). m and v take each product and sum rounded by itself, as plain
+// arithmetic does: the 8-bit codes and their blocks' scales follow from these
+// bits, and one last place moves a scale in some five million. The products that
+// enter the sums are fmas with -0 (k.none, not known to the compiler), since a
+// packed product followed by a packed sum is made one fma otherwise.
 __device__ __forceinline__ float update8(const Scalars& k, const V8& grad, V8& m, V8& v, V8& p) {
     const V8 g = grad * all8(k.s);
-    m = fma8(all8(k.b1), m, all8(k.o1) * g);
-    v = fma8(all8(k.b2), v, (all8(k.o2) * g) * g);
+    const V8 none = all8(k.none);
+    m = fma8(all8(k.b1), m, none) + fma8(all8(k.o1), g, none);
+    v = fma8(all8(k.b2), v, none) + fma8(all8(k.o2) * g, g, none);
     const float top = top8(v);
     p = p - fma8(all8(k.decay), p, all8(k.step) * quotient8(m, v, top, k.inv_c2, k.eps));
     return top;
@@ -494,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, ANY8 ? 4 : 3) adamw_kernel(const __g
     k.o1 = a.o1;
     k.o2 = a.o2;
     k.eps = a.eps;
+    k.none = -0.0f * a.eps;
     k.step = rate / c1;
     k.decay = rate * e.decay;
     const long long i0 = (long long)(blockIdx.x - e.chunk0) * a.passes * kPass;

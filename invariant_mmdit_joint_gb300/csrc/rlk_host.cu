@@ -336,7 +336,7 @@ const OpInfo kOps[] = {
     {"adaln_gate_residual+adaln_modulation", "rlk_adaln_gate_residual_fwd", kAdalnPolicy, kAdalnRowOrder},
     {"adaln_gate_residual+adaln_modulation backward", "rlk_adaln_gate_residual_bwd", kAdalnPolicy, kAdalnSumOrder},
     {"adamw", "rlk_adamw_step",
-     "fp32 update, moments by one fma of the rounded g term, div/sqrt within 1 ulp; 8-bit moments: e4m3 times 2^k per 32 elements, "
+     "fp32 update, moments rounded product by product, div/sqrt within 1 ulp; 8-bit moments: e4m3 times 2^k per 32 elements, "
      "stochastic rounding by a counter hash; p from the unrounded moments",
      "elementwise"},
     {"gradient norm and clip factor", "rlk_grad_norm", "fp32 squares, fp64 sum of the chunks, IEEE div/sqrt",

@@ -84,13 +84,8 @@ def test_steps_against_the_definition(dev, bits):
     assert all(bool(torch.isfinite(truth(opt, i)).all()) for i in range(len(SIZES)))
 
 
-def fma(a, b, c):
-    """a * b + c of float32 rounded once: the product is exact in 64 bits, and
-    the sum's own rounding there decides one value in 2^29."""
-    return (np.float64(a) * b.astype(np.float64) + c.astype(np.float64)).astype(np.float32)
-
-
 def test_moments_bit_by_bit(dev):
+    """Each product and sum rounded by itself, as numpy's float32 does."""
     import torch
     n, f = 1_000_003, np.float32
     g = torch.Generator(device=dev).manual_seed(8)
@@ -99,8 +94,8 @@ def test_moments_bit_by_bit(dev):
     m0, v0, d0 = (t.cpu().numpy() for t in (m, v, d))
     pkg.AdamW([p], betas=(0.9, 0.95), m=[m], v=[v], grads=[d]).step(3)
     o1, o2 = f(1 - 0.9), f(1 - 0.95)
-    np.testing.assert_array_equal(m.cpu().numpy(), fma(f(0.9), m0, o1 * d0))
-    np.testing.assert_array_equal(v.cpu().numpy(), fma(f(0.95), v0, (o2 * d0) * d0))
+    np.testing.assert_array_equal(m.cpu().numpy(), f(0.9) * m0 + o1 * d0)
+    np.testing.assert_array_equal(v.cpu().numpy(), f(0.95) * v0 + (o2 * d0) * d0)
 
 
 def test_eight_bit_states_bit_by_bit(dev):
@@ -116,7 +111,7 @@ def test_eight_bit_states_bit_by_bit(dev):
         opt.step(step, grad_scale=scale)
         for i, (m, v) in enumerate(before):
             g = grads[i].float().cpu().numpy() * f(0.37)
-            m1, v1 = fma(b1, m.astype(f), o1 * g), fma(b2, v.astype(f), (o2 * g) * g)
+            m1, v1 = b1 * m.astype(f) + o1 * g, b2 * v.astype(f) + (o2 * g) * g
             assert m1.dtype == f and v1.dtype == f
             rnd = O.random_bits(77, step, keys[i], m.size)
             for name, value, part, positive in (("m", m1, rnd & 0xFFFF, False), ("v", v1, rnd >> 16, True)):
