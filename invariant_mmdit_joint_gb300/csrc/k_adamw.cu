@@ -386,13 +386,15 @@ __device__ __forceinline__ void adamw_chunk8(const Entry& e, const Scalars& k, l
         }
         asm volatile("cp.async.commit_group;\n" ::: "memory");
     };
-    uint32_t next_ms = 0, next_vs = 0;
+    // Past the end a scale is 0, and m and v with it: the threads there take part
+    // in the exchanges of a last block, which another scale kept from the pass
+    // before could turn into NaN (0 * infinity).
+    uint32_t next_ms, next_vs;
     auto read_scales = [&](int j) {
         const long long i = at + (long long)j * kPass;
-        if (j < passes && i < e.n) {
-            next_ms = e.ms[i / 32];
-            next_vs = e.vs[i / 32];
-        }
+        const bool inside = j < passes && i < e.n;
+        next_ms = inside ? e.ms[i / 32] : 0u;
+        next_vs = inside ? e.vs[i / 32] : 0u;
     };
 #pragma unroll
     for (int j = 0; j < kStages - 1; ++j) fill(j, j * kStageBytes<G32>);

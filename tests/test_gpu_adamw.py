@@ -363,3 +363,25 @@ def test_a_tensor_past_32_bits(dev):
     assert float(p[0]) < 0 and abs(float(p[-1]) / -float(p[0]) - 1) <= 1.5e-8 + 16 * O.U
     # the hash repeats after 2^32 elements
     assert torch.equal(opt.m[0].view(torch.uint8)[:4096], opt.m[0].view(torch.uint8)[2 ** 32:2 ** 32 + 4096])
+
+
+def test_a_nan_stays_in_its_block_in_long_chunks(dev):
+    """A block that reads as NaN must not reach the tensor's last block, 2048
+    elements on: a list long enough for chunks of two passes, a last block of
+    less than 25 elements (threads past the end share its exchanges), and the
+    bytes of the tensor stepped alone, in chunks of one pass."""
+    import torch
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    g = torch.Generator(device=dev).manual_seed(6)
+    for n in (2048 + 32 + 1, 2048 + 32 + 8, 2048 + 64 + 24, 4096 + 13):
+        grad = torch.randn(n, generator=g, device=dev)
+        grad[n - n % 32 - 2048 + 9] = float("nan")
+        grads = [grad, torch.randn(8 * sms * 4096 + 5, generator=g, device=dev)]
+        opts = [pkg.AdamW([torch.zeros_like(t) for t in grads[:k]], state_bits=8, grads=grads[:k], seed=3) for k in (1, 2)]
+        for step in (1, 2, 3):
+            for opt in opts:
+                opt.step(step)
+        for name in ("params", "m", "v", "m_scale", "v_scale"):
+            a, b = (getattr(opt, name)[0] for opt in opts)
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), (n, name)
+        assert opts[1].m_scale[0][-1] != 255 and bool(torch.isfinite(opts[1].params[0][-(n % 32):]).all()), n
