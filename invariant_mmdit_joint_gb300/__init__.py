@@ -1164,8 +1164,11 @@ class AdamW:
     ``params``, ``masters``, ``m``, ``v``, ``m_scale`` and ``v_scale`` hold the
     tensors in use, one entry a parameter: what a checkpoint keeps, and what the
     constructor takes to go on from one. They stay the same tensors for the
-    object's life: load values into them with ``copy_``; a parameter whose
-    ``data`` was replaced is refused. ``lr`` may be set at any time. grad_norm's
+    object's life, those of the masters and states its own over the memory of the
+    ones given: load values into them with ``copy_``. The calls refuse a list
+    with a tensor whose ``data`` was replaced since (by whoever holds it: the
+    parameters, the gradients, and what was read from the other lists), and its
+    old memory stays allocated. ``lr`` may be set at any time. grad_norm's
     calls share one workspace: calls that may overlap on the GPU need an object
     each."""
 
@@ -1179,24 +1182,23 @@ class AdamW:
         n = len(params)
         if n == 0:
             raise ValueError("no parameters given")
-        self.params, self.state_bits, self.lr = tuple(params), state_bits, float(lr)
+        self._params, self.state_bits, self.lr = tuple(params), state_bits, float(lr)
         self.device = self.params[0].device
         each = lambda x: list(x) if isinstance(x, (list, tuple)) else [x] * n  # noqa: E731
         decay, share, keys = each(weight_decay), each(lr_scale), list(range(n)) if keys is None else list(keys)
-        masters = [None] * n if masters is None else list(masters)
+        masters = [None] * n if masters is None else [None if t is None else t.detach() for t in masters]
         code = torch.float8_e4m3fn if state_bits == 8 else f32
         blocks = [-(-p.numel() // 32) for p in self.params]
 
         def states(given, dtype, sizes):
             if given is None:
                 return tuple(torch.zeros(k, dtype=dtype, device=self.device) for k in sizes)
-            return tuple(given)
+            return tuple(t.detach() for t in given)
         sizes = [p.numel() for p in self.params]
-        self.m, self.v = states(m, code, sizes), states(v, code, sizes)
-        self.m_scale = states(m_scale, torch.uint8, blocks) if state_bits == 8 else (None,) * n
-        self.v_scale = states(v_scale, torch.uint8, blocks) if state_bits == 8 else (None,) * n
-        if not len(decay) == len(share) == len(keys) == len(masters) == len(self.m) == len(self.v) == len(self.m_scale) \
-                == len(self.v_scale) == n:
+        m, v = states(m, code, sizes), states(v, code, sizes)
+        m_scale = states(m_scale, torch.uint8, blocks) if state_bits == 8 else (None,) * n
+        v_scale = states(v_scale, torch.uint8, blocks) if state_bits == 8 else (None,) * n
+        if not len(decay) == len(share) == len(keys) == len(masters) == len(m) == len(v) == len(m_scale) == len(v_scale) == n:
             raise ValueError(f"expected one entry for each of the {n} parameters")
         if not all(0 <= int(k) < 2 ** 32 for k in [seed, *keys]):
             raise ValueError("seed and keys must be in 0 .. 2^32 - 1")
@@ -1209,22 +1211,52 @@ class AdamW:
             if p.dtype == bf16 and masters[i] is None:
                 masters[i] = p.detach().float().contiguous()
             for name, t, dtype, k in (("parameter", p, p.dtype, sizes[i]), ("master", masters[i], f32, sizes[i]),
-                                      ("m", self.m[i], code, sizes[i]), ("v", self.v[i], code, sizes[i]),
-                                      ("m_scale", self.m_scale[i], torch.uint8, blocks[i]),
-                                      ("v_scale", self.v_scale[i], torch.uint8, blocks[i])):
+                                      ("m", m[i], code, sizes[i]), ("v", v[i], code, sizes[i]),
+                                      ("m_scale", m_scale[i], torch.uint8, blocks[i]),
+                                      ("v_scale", v_scale[i], torch.uint8, blocks[i])):
                 if t is not None:
                     self._dense(f"{name} {i}", t, (dtype,), k)
             e = self._list[i]
-            e.p, e.master, e.m, e.v = _ptr(p), _ptr(masters[i]), _ptr(self.m[i]), _ptr(self.v[i])
-            e.m_scale, e.v_scale, e.n = _ptr(self.m_scale[i]), _ptr(self.v_scale[i]), sizes[i]
+            e.p, e.master, e.m, e.v = _ptr(p), _ptr(masters[i]), _ptr(m[i]), _ptr(v[i])
+            e.m_scale, e.v_scale, e.n = _ptr(m_scale[i]), _ptr(v_scale[i]), sizes[i]
             e.lr_scale, e.weight_decay, e.state_bits, e.key = float(share[i]), float(decay[i]), state_bits, int(keys[i])
-        self.masters = tuple(masters)
-        self._pointers = [p.data_ptr() for p in self.params]
-        self.grads = None
+        self._lists = {"masters": tuple(masters), "m": m, "v": v, "m_scale": m_scale, "v_scale": v_scale}
+        # The call's list holds addresses. The storages behind them are held here, so that they stay allocated, and
+        # the tensors that someone else holds too are looked at for still being over them: parameters and gradients,
+        # and a list of states once it was read (180 tensors with 8-bit states and masters are 1200 addresses, 70 us a
+        # call; parameters and gradients are 21).
+        self._storages = list(map(torch.Tensor.untyped_storage, self._params))
+        self._data_ptr = torch.Tensor.data_ptr
+        self._params_at = list(map(self._data_ptr, self._params))
+        self._handed, self._others, self._others_at = set(), [], []
+        self._grads = None
         if grads is not None:
             self._take(grads)
         self._args = AdamwArgs(lr=self.lr, beta1=float(betas[0]), beta2=float(betas[1]), eps=float(eps), seed=int(seed))
         self.workspace = None  # of grad_norm, allocated at its first call
+
+    def _hand_out(self, name):
+        held = self._lists[name]
+        if name not in self._handed:
+            self._handed.add(name)
+            for t in held:
+                if t is not None:
+                    self._others.append(t)
+                    self._others_at.append(t.data_ptr())
+                    self._storages.append(t.untyped_storage())
+        return held
+
+    params = property(lambda self: self._params)
+    grads = property(lambda self: self._grads)
+    masters = property(lambda self: self._hand_out("masters"))
+    m = property(lambda self: self._hand_out("m"))
+    v = property(lambda self: self._hand_out("v"))
+    m_scale = property(lambda self: self._hand_out("m_scale"))
+    v_scale = property(lambda self: self._hand_out("v_scale"))
+
+    def _same(self, tensors, addresses):
+        if list(map(self._data_ptr, tensors)) != addresses:
+            raise ValueError("a tensor's data was replaced: copy_ into it, or make a new object (gradients: give them anew)")
 
     def _dense(self, name, t, dtypes, n):
         if t.dtype not in dtypes or t.numel() != n or not t.is_contiguous() or t.device != self.device:
@@ -1237,19 +1269,23 @@ class AdamW:
         grads = tuple(grads)
         if len(grads) != len(self.params):
             raise ValueError(f"expected {len(self.params)} gradients, got {len(grads)}")
-        for i, (g, p) in enumerate(zip(grads, self.params)):
-            self._dense(f"gradient {i}", g, (torch.float32, torch.bfloat16), p.numel())
+        f32, types, device = torch.float32, (torch.float32, torch.bfloat16), self.device
+        for i, (g, p, e) in enumerate(zip(grads, self.params, self._list)):
+            if g.dtype not in types or g.numel() != e.n or not g.is_contiguous() or g.device != device:
+                self._dense(f"gradient {i}", g, types, e.n)
             if g.dim() != 1 and g.shape != p.shape:
                 raise ValueError(f"gradient {i} must be {tuple(p.shape)} or flat, got {tuple(g.shape)}")
-        for e, g in zip(self._list, grads):
-            e.g, e.g_dtype = g.data_ptr(), int(g.dtype == torch.float32)
-        self.grads = grads
+        self._grads_at = list(map(self._data_ptr, grads))
+        for e, g, at in zip(self._list, grads, self._grads_at):
+            e.g, e.g_dtype = at, int(g.dtype is f32)
+        self._grads, self._grad_storages = grads, list(map(torch.Tensor.untyped_storage, grads))
 
     def _ready(self, grads):
         if grads is not None:
             self._take(grads)
-        if self.grads is None:
+        if self._grads is None:
             raise ValueError("no gradients given")
+        self._same(self._grads, self._grads_at)
         _require_current(self.device)
 
     def _scalar(self, name, t, dtype):
@@ -1284,8 +1320,9 @@ class AdamW:
         value on the device, such as grad_norm(...)[1:]; if it is not finite
         nothing is changed."""
         import torch
-        if list(map(torch.Tensor.data_ptr, self.params)) != self._pointers:
-            raise ValueError("a parameter's data was replaced: copy_ into it, or make a new object")
+        self._same(self._params, self._params_at)
+        if self._others:
+            self._same(self._others, self._others_at)
         self._ready(grads)
         a = self._args
         a.step_dev = a.lr_dev = None

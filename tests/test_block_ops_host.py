@@ -327,6 +327,54 @@ def test_adamw_keeps_to_its_tensors(L):
         opt.step(1)
 
 
+def test_adamw_looks_at_the_memory_its_list_points_to(L):
+    """Every tensor that someone else can hold: one whose data was replaced is
+    refused by the calls that would read or write its old memory, and that stays
+    allocated, so that no other tensor can come to its address."""
+    torch = pytest.importorskip("torch")
+    names = {"params": "p", "grads": "g", "masters": "master", "m": "m", "v": "v", "m_scale": "m_scale",
+             "v_scale": "v_scale"}
+
+    def make(given):
+        p = [torch.zeros(5, 7), torch.zeros(33, dtype=torch.bfloat16)]
+        state = dict(masters=[None, torch.zeros(33)])
+        for k in ("m", "v"):
+            state[k] = [torch.zeros(n, dtype=torch.float8_e4m3fn) for n in (35, 33)]
+            state[k + "_scale"] = [torch.zeros(2, dtype=torch.uint8) for _ in p]
+        return pkg.AdamW(p, state_bits=8, grads=[torch.zeros(35), torch.zeros(33)], **(state if given else {})), state
+    for given in (False, True):
+        for name, field in names.items():
+            opt, _ = make(given)
+            t, old = getattr(opt, name)[1], getattr(opt._list[1], field)
+            assert t.data_ptr() == old
+            t.data = torch.empty(0, dtype=t.dtype)
+            fresh = [torch.zeros(n, dtype=t.dtype) for n in (2, 33, 33) for _ in range(40)]
+            assert all(f.data_ptr() != old for f in fresh), name
+            for t.data in (fresh[0], fresh[50]):
+                with pytest.raises(ValueError, match="replaced"):
+                    opt.step(1)
+                if name == "grads":
+                    with pytest.raises(ValueError, match="replaced"):
+                        opt.grad_norm(1.0)
+                    with pytest.raises(ValueError, match="CUDA"):  # given anew they are taken
+                        opt.step(1, grads=[torch.zeros(35), torch.zeros(33)])
+                    opt, _ = make(given)
+                    t = opt.grads[1]
+        opt, _ = make(given)
+        opt.m[0].untyped_storage().resize_(0)
+        with pytest.raises(ValueError, match="replaced"):
+            opt.step(1)
+        for name in names:
+            with pytest.raises(AttributeError):
+                setattr(opt, name, getattr(opt, name))
+    # what a caller gave stays the object's memory, whatever the caller's own tensor is over
+    opt, state = make(True)
+    state["m"][0].data = torch.zeros(35, dtype=torch.float8_e4m3fn)
+    assert opt.m[0].data_ptr() == opt._list[0].m != state["m"][0].data_ptr()
+    with pytest.raises(ValueError, match="CUDA"):
+        opt.step(1)
+
+
 # ------------------------------------------------------------------ definitions
 def _loss(d, c):
     r = d["x"]
