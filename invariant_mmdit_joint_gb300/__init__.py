@@ -1184,6 +1184,7 @@ class AdamW:
             raise ValueError("no parameters given")
         self._params, self.state_bits, self.lr = tuple(params), state_bits, float(lr)
         self.device = self.params[0].device
+        self._index = self.device.index
         each = lambda x: list(x) if isinstance(x, (list, tuple)) else [x] * n  # noqa: E731
         decay, share, keys = each(weight_decay), each(lr_scale), list(range(n)) if keys is None else list(keys)
         masters = [None] * n if masters is None else [None if t is None else t.detach() for t in masters]
@@ -1233,6 +1234,7 @@ class AdamW:
         if grads is not None:
             self._take(grads)
         self._args = AdamwArgs(lr=self.lr, beta1=float(betas[0]), beta2=float(betas[1]), eps=float(eps), seed=int(seed))
+        self._args_ref = ctypes.byref(self._args)
         self.workspace = None  # of grad_norm, allocated at its first call
 
     def _hand_out(self, name):
@@ -1301,15 +1303,17 @@ class AdamW:
         max_norm, NaN if the norm is not finite."""
         import torch
         self._ready(grads)
-        n = len(self.params)
+        n = len(self._params)
         if out is None:
             out = _empty(2, torch.float32, self.device, stream)
         else:
             self._dense("out", out, (torch.float32,), 2)
         if self.workspace is None:
             self.workspace = _empty(rlk_grad_norm_workspace_bytes(self._list, n), torch.uint8, self.device, stream)
-        rlk_grad_norm(self._list, n, pre_scale, max_norm, out, self.workspace, self.workspace.numel(),
-                      _raw_stream(stream, self.device.index))
+        rc = lib().rlk_grad_norm(self._list, n, float(pre_scale), float(max_norm), out.data_ptr(), self.workspace.data_ptr(),
+                                 self.workspace.numel(), _raw_stream(stream, self._index))
+        if rc:
+            _check(rc, "rlk_grad_norm")
         return out
 
     def step(self, step, lr=None, grad_scale=None, grads=None, stream=None):
@@ -1335,4 +1339,6 @@ class AdamW:
         else:
             a.lr = self.lr if lr is None else float(lr)
         a.grad_scale = self._scalar("grad_scale", grad_scale, torch.float32)
-        rlk_adamw_step(self._list, len(self.params), a, _raw_stream(stream, self.device.index))
+        rc = lib().rlk_adamw_step(self._list, len(self._params), self._args_ref, _raw_stream(stream, self._index))
+        if rc:
+            _check(rc, "rlk_adamw_step")

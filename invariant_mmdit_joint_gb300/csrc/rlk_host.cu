@@ -1287,15 +1287,14 @@ static rlk_status grads_ok(const rlk_adamw_tensor* t, int32_t n) {
 // by their starts, each is held against the furthest ends before it.
 static rlk_status list_disjoint(const rlk_adamw_tensor* t, int32_t n) {
     struct Range {
-        uintptr_t lo, hi;
-        bool written;
+        uintptr_t lo, hi;  // lo is 16-byte aligned: its last bit says whether the range is written
     };
     std::unique_ptr<Range[]> r(new (std::nothrow) Range[(size_t)n * 7]);
     if (!r) return RLK_ERR_CUDA;
     size_t k = 0;
     auto add = [&](const void* p, uint64_t bytes, bool written) {
         const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-        r[k++] = Range{lo, lo + bytes, written};
+        r[k++] = Range{lo | (written ? 1u : 0u), lo + bytes};
     };
     for (int i = 0; i < n; ++i) {
         const rlk_adamw_tensor& e = t[i];
@@ -1314,9 +1313,10 @@ static rlk_status list_disjoint(const rlk_adamw_tensor* t, int32_t n) {
     std::sort(r.get(), r.get() + k, [](const Range& a, const Range& b) { return a.lo < b.lo; });
     uintptr_t any = 0, written = 0;
     for (size_t i = 0; i < k; ++i) {
-        if (r[i].lo < (r[i].written ? any : written)) return RLK_ERR_INVALID_ARG;
+        const bool writes = (r[i].lo & 1u) != 0;
+        if ((r[i].lo & ~(uintptr_t)15) < (writes ? any : written)) return RLK_ERR_INVALID_ARG;
         any = std::max(any, r[i].hi);
-        if (r[i].written) written = std::max(written, r[i].hi);
+        if (writes) written = std::max(written, r[i].hi);
     }
     return RLK_OK;
 }

@@ -197,6 +197,44 @@ def test_adamw_list_limits(L):
         assert L.rlk_adamw_step(entries(n=0, p=None, g=None, m=None, v=None), 2, ref(args()), None) == 5
 
 
+def test_overlaps_are_found_in_any_order(L):
+    """Lists of buffers in random places and orders against the rule itself: no
+    written range meets another one; read ones (gradients) may meet."""
+    if not no_gpu():
+        pytest.skip("addresses of no memory: for machines without a GPU")
+    rng = np.random.default_rng(12)
+    seen = set()
+    for trial in range(300):
+        count = int(rng.integers(1, 40))
+        t = (pkg.AdamwTensor * count)()
+        # distinct slots, in order, shuffled, or with a collision
+        slots = np.arange(7 * count)
+        if trial % 3:
+            rng.shuffle(slots)
+        ranges = []
+        for i in range(count):
+            bits, copy, n = int(rng.choice([8, 32])), bool(rng.integers(2)), int(rng.integers(0, 4096))
+            fields = {"g": (4, False), "p": (2 if copy else 4, True), "m": (bits // 8, True), "v": (bits // 8, True)}
+            if copy:
+                fields["master"] = (4, True)
+            if bits == 8:
+                fields.update(m_scale=(1 / 32, True), v_scale=(1 / 32, True))
+            t[i].n, t[i].state_bits, t[i].g_dtype, t[i].lr_scale = n, bits, 1, 1.0
+            for j, (k, (size, written)) in enumerate(fields.items()):
+                at = P + 16384 * int(slots[7 * i + j])
+                if trial % 2 and rng.random() < 0.02:
+                    at += int(rng.integers(-8192, 8192)) // 16 * 16  # perhaps into a neighbour
+                if k == "g" and rng.random() < 0.2:
+                    at = P + 16384 * 7 * count  # one shared by several
+                setattr(t[i], k, at)
+                if n:
+                    ranges.append((at, at + int(np.ceil(n * size)), written))
+        bad = any((a[2] or b[2]) and a[0] < b[1] and b[0] < a[1] for i, a in enumerate(ranges) for b in ranges[:i])
+        assert L.rlk_adamw_step(t, count, ref(args()), None) == (1 if bad else 5), trial
+        seen.add(bad)
+    assert seen == {False, True}
+
+
 def test_grad_norm_fails_closed(L):
     t = entries()
     need = pkg.rlk_grad_norm_workspace_bytes(t, 2)
