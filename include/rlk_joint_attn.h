@@ -594,8 +594,9 @@ typedef struct rlk_adamw_args {
     double lr, beta1, beta2, eps;  /* lr >= 0, 0 <= beta < 1, 2^-50 <= eps <= 1 */
     int64_t step;          /* 1 .. 2^31 - 1: this step's number */
     const float* lr_dev;   /* device, or NULL: read instead of lr */
-    const int64_t* step_dev; /* device, or NULL: read instead of step (same range),
-                              so that a captured step follows its counter */
+    const int64_t* step_dev; /* device, or NULL: read instead of step, so that a
+                              captured step follows its counter. Out of step's
+                              range: every tensor is left as it was */
     const float* grad_scale; /* device, or NULL (1). Not finite: every tensor is
                               left as it was */
     uint32_t seed;         /* of the 8-bit states' rounding */

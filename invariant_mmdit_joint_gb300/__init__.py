@@ -1321,8 +1321,8 @@ class AdamW:
         ``lr`` the rate if not the constructor's; each an ordinary number, or a
         device tensor of one value (int64, float32) that is read when the
         kernels run, as a captured step needs. ``grad_scale`` is one float32
-        value on the device, such as grad_norm(...)[1:]; if it is not finite
-        nothing is changed."""
+        value on the device, such as grad_norm(...)[1:]. If it is not finite, or
+        a device ``step`` is not in 1 .. 2^31 - 1, nothing is changed."""
         import torch
         self._same(self._params, self._params_at)
         if self._others:

@@ -488,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, ANY8 ? 4 : 3) adamw_kernel(const __g
     uint32_t step = a.step;
     if (a.step_dev != nullptr) {
         const long long t = *a.step_dev;
+        if (t < 1 || t > 0x7fffffffLL) return;  // 1 - beta^0 would make every element infinite or NaN
         step = (uint32_t)t;
         c1 = (float)(1.0 - pow(a.b1, (double)t));
         k.inv_c2 = (float)(1.0 / sqrt(1.0 - pow(a.b2, (double)t)));

@@ -385,3 +385,18 @@ def test_a_nan_stays_in_its_block_in_long_chunks(dev):
             a, b = (getattr(opt, name)[0] for opt in opts)
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), (n, name)
         assert opts[1].m_scale[0][-1] != 255 and bool(torch.isfinite(opts[1].params[0][-(n % 32):]).all()), n
+
+
+def test_a_counter_out_of_range_leaves_everything(dev):
+    """A device counter that was not advanced before the first step, or has run over."""
+    import torch
+    for bits in (32, 8):
+        opt, _ = make(dev, SIZES, bits)
+        opt.step(1)
+        tensors = [t for t in opt.params + opt.masters + opt.m + opt.v + opt.m_scale + opt.v_scale if t is not None]
+        keep = [t.clone() for t in tensors]
+        for t in (0, -1, 2 ** 31, -2 ** 63, 2 ** 32 + 5):
+            opt.step(torch.tensor([t], device=dev))
+            assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(tensors, keep)), t
+        opt.step(torch.tensor([2 ** 31 - 1], device=dev))
+        assert not torch.equal(opt.params[-1], keep[len(SIZES) - 1])
