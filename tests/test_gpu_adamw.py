@@ -400,3 +400,24 @@ def test_a_counter_out_of_range_leaves_everything(dev):
             assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(tensors, keep)), t
         opt.step(torch.tensor([2 ** 31 - 1], device=dev))
         assert not torch.equal(opt.params[-1], keep[len(SIZES) - 1])
+
+
+@pytest.mark.parametrize("betas", [(0.9, 0.999), (0.5, 0.99999), (1 - 2.0 ** -12, 1 - 2.0 ** -20), (0.0, 0.3)], ids=str)
+def test_a_step_number_on_the_device_gives_the_bytes_of_an_ordinary_one(dev, betas):
+    """The corrections 1 - beta^t are the same numbers wherever they are computed."""
+    import torch
+    rng = np.random.default_rng(2)
+    steps = [*range(1, 1500), *(int(t) for t in np.unique((2 ** rng.uniform(11, 31, 1500)).astype(np.int64))), 2 ** 31 - 1]
+    steps = [t for t in steps if t < 2 ** 31]
+    grads = [torch.tensor([1.0, -0.3], device=dev)]
+    opts = [pkg.AdamW([torch.zeros(2, device=dev)], grads=grads, betas=betas, lr=1e-2) for _ in range(2)]
+    device = torch.tensor(steps, device=dev)
+    out = torch.empty(2, len(steps), 2, device=dev)
+    for i, t in enumerate(steps):
+        for k, opt in enumerate(opts):
+            for s in (opt.params[0], opt.m[0], opt.v[0]):
+                s.zero_()
+            opt.step(device[i] if k else t)
+            out[k, i] = opt.params[0]
+    same = (out[0].view(torch.int32) == out[1].view(torch.int32)).all(1)
+    assert bool(same.all()), [steps[i] for i in (~same).nonzero().flatten().tolist()][:10]
