@@ -555,8 +555,9 @@ rlk_status rlk_adaln_gate_residual_bwd(const rlk_adaln_shape* shape, const rlk_a
  *   m = beta1 * m + (1 - beta1) * g';   v = beta2 * v + (1 - beta2) * g'^2
  *   p -= rate * weight_decay * p
  *        + rate / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
- * in fp32, quotient and square root within one unit in the last place; m and v
- * take each product and sum rounded by itself, the last one ((1 - beta2) g') g'.
+ * in fp32, quotient and square root within one unit in the last place (the
+ * quotient of a subnormal m within two; one past the type's range is not finite);
+ * m and v take each product and sum rounded by itself, the last one ((1 - beta2) g') g'.
  *
  * Parameters: fp32 (p, master NULL), or bf16 with an fp32 master: the master
  * is updated and p receives its bf16 rounding.

@@ -263,7 +263,7 @@ __device__ __forceinline__ uint2 encode8(const V8& q, float t, const uint32_t (&
 
 // ------------------------------------------------------------ AdamW
 struct Scalars {
-    float s, b1, b2, o1, o2, inv_c2, eps, none, step, decay;  // step = rate / (1 - beta1^t); decay = rate * weight decay
+    float s, b1, b2, o1, o2, inv_c2, eps, most, none, step, decay;  // step = rate / (1 - beta1^t); decay = rate * weight decay
 };
 
 // m / (sqrt(v) * c + eps), each of the two within one unit in the last place:
@@ -274,10 +274,11 @@ struct Scalars {
 // operands that cannot occur here (they were a quarter of the 8-bit step's
 // instructions). v is scaled by 2^40, so that subnormal values become normal
 // ones, and kept from 0 by 2^-124, which is 2^-82 in sqrt(v): at most 2^-27 of
-// eps >= 2^-50 for c <= 32. v >= 2^86 and NaN (top, the largest) take sqrtf
-// and the division.
-__device__ __forceinline__ V8 quotient8(const V8& m, const V8& v, float top, float c, float eps) {
-    if (!(top < 7.7371252e25f)) {
+// eps for c <= 2^55 eps (32 for the smallest eps, 2^-50). v >= 2^86, NaN (top, the
+// largest) and a c above that (the first steps with a beta2 next to 1) take sqrtf
+// and the division: `most` is 2^86, or 0 for such a c.
+__device__ __forceinline__ V8 quotient8(const V8& m, const V8& v, float top, float most, float c, float eps) {
+    if (!(top < most)) {
         float mi[8], u[8];
         singles(m, mi);
         singles(v, u);
@@ -313,7 +314,7 @@ __device__ __forceinline__ float update8(const Scalars& k, const V8& grad, V8& m
     m = fma8(all8(k.b1), m, none) + fma8(all8(k.o1), g, none);
     v = fma8(all8(k.b2), v, none) + fma8(all8(k.o2) * g, g, none);
     const float top = top8(v);
-    p = p - fma8(all8(k.decay), p, all8(k.step) * quotient8(m, v, top, k.inv_c2, k.eps));
+    p = p - fma8(all8(k.decay), p, all8(k.step) * quotient8(m, v, top, k.most, k.inv_c2, k.eps));
     return top;
 }
 template <bool G32>
@@ -468,9 +469,9 @@ __device__ __forceinline__ void adamw_chunk8(const Entry& e, const Scalars& k, l
 // units of 2^-64, cut off; relative to 1 - beta^t they are off by some 2^-64 / (1 -
 // beta)), and the rest is fp32 operations that no compiler may join or split. The
 // powers' table comes from the host, so that a thread multiplies as often as t
-// has bits set. (With two fp64 powers in every thread, 45 million elements with
-// fp32 states took 1027 us captured with a counter, 184 without; 166 million with
-// 8-bit states 1017 and 453.)
+// has bits set. Captured with a counter, 45 million elements with fp32 states take
+// 186 us, 184 without; 166 million with 8-bit states 465 and 453 (two fp64
+// powers in every thread: 1027 and 1017).
 struct Powers {
     uint64_t of[31];  // beta^(2^k) * 2^64
 };
@@ -551,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, ANY8 ? 4 : 3) adamw_kernel(const __g
     k.o1 = a.o1;
     k.o2 = a.o2;
     k.eps = a.eps;
+    k.most = k.inv_c2 <= 0x1p55f * a.eps ? 0x1p86f : 0.0f;
     k.none = -0.0f * a.eps;
     k.step = rate / c1;
     k.decay = rate * e.decay;

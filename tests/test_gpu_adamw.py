@@ -421,3 +421,50 @@ def test_a_step_number_on_the_device_gives_the_bytes_of_an_ordinary_one(dev, bet
             out[k, i] = opt.params[0]
     same = (out[0].view(torch.int32) == out[1].view(torch.int32)).all(1)
     assert bool(same.all()), [steps[i] for i in (~same).nonzero().flatten().tolist()][:10]
+
+
+@pytest.mark.parametrize("t, bit", [(1, 24), (3, 20), (7, 15), (1, 10)])
+def test_the_quotient_under_large_corrections(dev, t, bit):
+    """beta2 = 1 - 2^-bit in its first steps: 1 / sqrt(1 - beta2^t) far above 1,
+    second moments of 0 and near it, the smallest eps."""
+    import torch
+    beta2 = 1 - 2.0 ** -bit
+    rng = np.random.default_rng(9)
+    v = np.concatenate([np.zeros(512), 2.0 ** rng.uniform(-125, -60, 4096)]).astype(np.float32)
+    m = (rng.standard_normal(v.size) * 1e-20).astype(np.float32)
+    for eps in (2.0 ** -50, 2.0 ** -40, 1e-8):
+        p, mm, vv = (torch.from_numpy(a).to(dev) for a in (np.zeros_like(m), m, v))
+        pkg.AdamW([p], grads=[torch.zeros_like(p)], m=[mm], v=[vv], lr=1.0, betas=(0.5, beta2), eps=eps,
+                  weight_decay=0.0).step(t)
+        c1, c = 1 - 0.5 ** t, 1 / np.sqrt(-np.expm1(t * np.log1p(-2.0 ** -bit)))
+        root = np.sqrt(f64(vv)) * c  # of the moments that the step left
+        d = root + float(np.float32(eps))
+        want = -f64(mm) / c1 / d
+        # root 2u, c and d u, the quotient 2u, rate / c1 (c1 is exact) and its product u each
+        bound = np.abs(want) * (3 * O.U * root / d + 2.0 ** -27 + 5 * O.U) * 1.001 + 2.0 ** -149
+        assert np.all(np.abs(f64(p) - want) <= bound), (eps, np.max(np.abs(f64(p) - want) / bound))
+
+
+def test_the_quotient_of_the_smallest_moments(dev):
+    """|m| about the smallest normal value, where the residual m - d q of the
+    quotient's correction falls below the type's last bit. With an estimate of
+    1 / d within 2u, q is within 3u and the residual at most 3u |m|; its rounding
+    adds 2^-150, at most u |m| of a normal m, so the quotient is within 2u; of a
+    subnormal m it adds at most the residual itself, 4u in all."""
+    import torch
+    rng = np.random.default_rng(10)
+    normal = 2.0 ** rng.uniform(-124.9, -95, 20_000)
+    tiny = 2.0 ** -148 * rng.integers(1, 1 << 22, 20_000)  # halves that are exact
+    m = (np.concatenate([normal, tiny]) * rng.choice([-1, 1], 40_000)).astype(np.float32)
+    v = (2.0 ** rng.uniform(-100, 10, m.size)).astype(np.float32)
+    p = torch.zeros(m.size, device=dev)
+    pkg.AdamW([p], grads=[torch.zeros_like(p)], m=[torch.from_numpy(m).to(dev)], v=[torch.from_numpy(v).to(dev)],
+              lr=2.0 ** 40, betas=(0.5, 0.5), eps=2.0 ** -50, weight_decay=0.0).step(60)
+    half = m.astype(np.float64) / 2
+    root = np.sqrt(v.astype(np.float64) / 2)
+    d = root + 2.0 ** -50
+    want = -half / d * 2.0 ** 40
+    # d is rounded once; two roundings of q below the type's last bit, 2^40 of rate times
+    units = np.where(np.abs(half) >= 2.0 ** -126, 2, 4) + 1
+    bound = np.abs(want) * (2 * O.U * root / d + units * O.U) * 1.001 + 2.0 ** -109
+    assert np.all(np.abs(f64(p) - want) <= bound), np.max(np.abs(f64(p) - want) / bound)
