@@ -592,7 +592,8 @@ typedef struct rlk_adamw_tensor {
 } rlk_adamw_tensor;
 
 typedef struct rlk_adamw_args {
-    double lr, beta1, beta2, eps;  /* lr >= 0, 0 <= beta < 1, 2^-50 <= eps <= 1 */
+    double lr, beta1, beta2, eps;  /* lr >= 0, 0 <= beta < 1, 2^-50 <= eps <= 1; lr * lr_scale
+                              and that times weight_decay in fp32's range */
     int64_t step;          /* 1 .. 2^31 - 1: this step's number */
     const float* lr_dev;   /* device, or NULL: read instead of lr */
     const int64_t* step_dev; /* device, or NULL: read instead of step, so that a

@@ -186,6 +186,16 @@ def test_adamw_arguments_fail_closed(L, over, code):
     assert L.rlk_adamw_step(entries(), 2, ref(args(**over)), None) == code
 
 
+@pytest.mark.parametrize("a, e, code", [
+    (dict(lr=1e39), {}, 1), ({}, dict(lr_scale=1e39), 1), ({}, dict(weight_decay=1e39), 1),
+    (dict(lr=1e20), dict(lr_scale=1e20), 1), (dict(lr=1e20), dict(weight_decay=1e20), 1),
+    (dict(lr=1e20), dict(lr_scale=1e10, weight_decay=1e5), 5)])
+def test_adamw_rates_past_fp32_are_refused(L, a, e, code):
+    """The kernel holds them in fp32: an infinite rate makes NaN of elements without an update."""
+    if code == 1 or no_gpu():
+        assert L.rlk_adamw_step(entries(**e), 2, ref(args(**a)), None) == code
+
+
 def test_adamw_list_limits(L):
     assert L.rlk_adamw_step(entries(), -1, ref(args()), None) == 1
     assert L.rlk_adamw_step(None, 2, ref(args()), None) == 1
