@@ -1326,8 +1326,8 @@ static rlk_status adamw_impl(const rlk_adamw_tensor* t, int32_t n, const rlk_ada
     rlk_status st = grads_ok(t, n);
     if (st != RLK_OK) return st;
     auto below_one = [](double b) { return b >= 0.0 && b < 1.0; };
-    // (the kernel holds rates in fp32: one that is infinite there would be 0 * infinity = NaN in elements of no update)
-    auto rate_ok = [](double x) { return x >= 0.0 && std::isfinite((float)x); };
+    // (the kernel holds rates in fp32, where one past 3.4e38 would be infinite, and NaN in elements of no update)
+    auto rate_ok = [](double x) { return x >= 0.0 && x < 3.4e38; };
     if (!rate_ok(a->lr) || !below_one(a->beta1) || !below_one(a->beta2) || !(a->eps >= 0x1p-50) || !(a->eps <= 1.0) ||
         (a->step_dev == nullptr && (a->step < 1 || a->step > 0x7fffffffLL)) || a->reserved != 0)
         return RLK_ERR_INVALID_ARG;
@@ -1339,8 +1339,8 @@ static rlk_status adamw_impl(const rlk_adamw_tensor* t, int32_t n, const rlk_ada
         if ((e.state_bits != 32 && e.state_bits != 8) || e.reserved != 0 || !rate_ok(e.lr_scale) ||
             !rate_ok(e.weight_decay))
             return RLK_ERR_INVALID_ARG;
-        const float rate = (float)a->lr * (float)e.lr_scale;
-        if (a->lr_dev == nullptr && !rate_ok(rate * (float)e.weight_decay + rate)) return RLK_ERR_INVALID_ARG;
+        const double rate = a->lr * e.lr_scale;
+        if (a->lr_dev == nullptr && !rate_ok(std::max(rate, rate * e.weight_decay))) return RLK_ERR_INVALID_ARG;
         if (e.n == 0) continue;
         st = e.state_bits == 8 ? check_ptrs({e.p, e.m, e.v, e.m_scale, e.v_scale}, {e.master})
                                : check_ptrs({e.p, e.m, e.v}, {e.master});
