@@ -778,8 +778,9 @@ const char* rlk_strerror(int status);
  * 6 RoPE/RMSNorm backward of the keys (the queries' runs inside dQ),
  * 7 gain-gradient fold, 8 qk_gemm, 9 softmax,
  * 10 av_gemm, 11 forward key shard, 12 qkv_bias_gemm, 13 attn_out_bias_gemm,
- * 19 adaln forward, 20 adaln backward, 21 its folds, 22 gradient norm, 23 its
- * fold, 24 AdamW (14 .. 18: the standalone backward operators).
+ * 19 adaln forward, 20 adaln backward, 21 its fold, 22 gradient norm, 23 its
+ * fold, 24 AdamW, 25 adaln's weight gradients (14 .. 18: the standalone
+ * backward operators).
  * rlk_kernel_timing(1) makes later calls record a CUDA event pair around
  * every launch (up to 4096 launches per kernel id); rlk_kernel_timing(0)
  * stops and clears. rlk_kernel_timing_read() waits for the recorded events

@@ -55,6 +55,7 @@ KERNEL_IDS = {
     "qk_gemm": 8, "softmax": 9, "av_gemm": 10, "attn_fwd_shard": 11, "qkv_gemm": 12, "out_gemm": 13,
     "dp_gemm": 14, "softmax_bwd": 15, "key_gemm": 16, "query_gemm": 17, "norm_rope_bwd_q": 18,
     "adaln_fwd": 19, "adaln_bwd": 20, "adaln_fold": 21, "grad_norm": 22, "grad_norm_fold": 23, "adamw": 24,
+    "adaln_weight": 25,
 }
 # which intermediate rlk_joint_attn_unfused_bytes() sizes
 UNFUSED = {"scores": 0, "p": 1, "alpha": 2, "rows": 3, "dp": 4, "ds": 5, "stats": 6, "dhat": 7, "gain_tiles": 8}

@@ -844,11 +844,12 @@ cudaError_t launch_adaln_bwd(const AdalnArgs& a, bool gate, cudaStream_t s) {
     const int runs = std::min((std::max(a.s[0].chunks, a.s[1].chunks) + 1) / 2 * 2, kFoldRuns);  // (whole warps)
     adaln_fold_kernel<<<dim3((a.C + kFoldColumns - 1) / kFoldColumns, 6, a.B), kFoldColumns / 4 * runs, 0, s>>>(a);
     e = cudaGetLastError();
-    if (e == cudaSuccess && weights) {
-        adaln_weight_kernel<<<dim3((a.C + 127) / 128, 4), 128, 0, s>>>(a);
-        e = cudaGetLastError();
-    }
     timing_end(kKAdalnFold, s);
+    if (e != cudaSuccess || !weights) return e;
+    timing_begin(kKAdalnWeight, s);
+    adaln_weight_kernel<<<dim3((a.C + 127) / 128, 4), 128, 0, s>>>(a);
+    e = cudaGetLastError();
+    timing_end(kKAdalnWeight, s);
     return e;
 }
 

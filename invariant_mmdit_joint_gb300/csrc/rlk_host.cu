@@ -348,7 +348,7 @@ const char* const kKernelNames[kNumKernelIds] = {
     "qk_gemm_kernel", "softmax_kernel", "av_gemm_kernel", "attn_fwd_tc_kernel<shard>", "qkv_gemm_kernel",
     "qkv_gemm_kernel<out_proj>", "qk_gemm_kernel<dp>", "softmax_bwd_kernel", "acc_gemm_kernel<key>",
     "acc_gemm_kernel<query>", "norm_rope_bwd_q_kernel", "adaln_fwd_kernel", "adaln_bwd_kernel", "adaln_fold_kernel",
-    "grad_norm_kernel", "grad_norm_fold_kernel", "adamw_kernel"};
+    "grad_norm_kernel", "grad_norm_fold_kernel", "adamw_kernel", "adaln_weight_kernel"};
 
 struct OpLog {
     std::mutex mu;

@@ -94,7 +94,7 @@ enum KernelId {
     kKQkGemm = 8, kKSoftmax = 9, kKAvGemm = 10, kKAttnFwdShard = 11, kKQkvGemm = 12, kKOutGemm = 13,
     kKDpGemm = 14, kKSoftmaxBwd = 15, kKKeyGemm = 16, kKQueryGemm = 17, kKNormRopeBwdQ = 18,
     kKAdalnFwd = 19, kKAdalnBwd = 20, kKAdalnFold = 21, kKGradNorm = 22, kKGradNormFold = 23, kKAdamw = 24,
-    kNumKernelIds = 25
+    kKAdalnWeight = 25, kNumKernelIds = 26
 };
 
 // Launch timing hooks (rlk_host.cu): bracket one launch with events.

@@ -417,3 +417,21 @@ def test_the_trace_names_the_kernels(dev):
     assert [(r["op"], r["status"], r["kernels"]) for r in t.records] == [
         ("adaln_modulation", 0, ["adaln_fwd_kernel"]),
         ("adaln_modulation backward", 0, ["adaln_bwd_kernel", "adaln_fold_kernel"])]
+
+
+def test_the_trace_and_the_timing_name_the_weights_kernel(dev):
+    """A backward that writes a weight's gradient launches a third kernel, with or without another sum."""
+    c = Case(dev, 2, 3, 5, 64, post="rms")
+    m = c.op.modulation(c.x, c.scale, c.shift, w=c.w)
+    f = c.op.gate_residual(c.x, c.h, c.gate, c.scale, c.shift, w_post=c.w_post)
+    three = ["adaln_bwd_kernel", "adaln_fold_kernel", "adaln_weight_kernel"]
+    pkg.rlk_kernel_timing(True)
+    with pkg.op_trace() as t:
+        c.op.modulation_bwd(c.x, c.scale, m["stats"], c.dy, c.dr, w=c.w)
+        c.op.modulation_bwd(c.x, c.scale, m["stats"], c.dy, c.dr)
+        c.op.gate_residual_bwd(f["r"], c.h, c.gate, c.scale, f["stats"], c.dy, c.dr, w_post=c.w_post,
+                               post_stats=f["post_stats"])
+    counts = {k: pkg.rlk_kernel_timing_read(k)[1] for k in ("adaln_fwd", "adaln_bwd", "adaln_fold", "adaln_weight")}
+    pkg.rlk_kernel_timing(False)
+    assert [r["kernels"] for r in t.records] == [three, three[:2], three]
+    assert counts == {"adaln_fwd": 0, "adaln_bwd": 3, "adaln_fold": 3, "adaln_weight": 2}
