@@ -460,8 +460,9 @@ rlk_status rlk_attn_out_bias_gemm(const rlk_ja_shape* shape,
  *   f = alpha * gate_b * d;  dh = f, or through the norm of h likewise;
  *   dgate_b = alpha * w_post * G_b, dw_post = alpha * sum_b gate_b * G_b with
  *            G_b = sum_t d * hat(h) (sum_t d * h without a norm after)
- * Sums over tokens run in chunks whose length depends on the stream's T and on C,
- * chunks ascending, then b ascending, in fp32 and without atomics: a sample's
+ * Sums over tokens run in chunks whose length depends on the stream's T and on C:
+ * the rows of a chunk in order, every 32nd chunk in order, these 32 runs
+ * ascending, then (weights) b ascending, in fp32 and without atomics: a sample's
  * gradients do not depend on its batch.
  *
  * Every row is processed, padded text rows too: theirs must hold finite values
@@ -619,7 +620,8 @@ rlk_status rlk_adamw_step(const rlk_adamw_tensor* tensors, int32_t n_tensors, co
  * pre_scale > 0 undoes a loss scale or averages accumulated gradients;
  * max_norm > 0, or INFINITY for no clipping. Squares are fp32: magnitudes
  * below 2^-63 vanish, and a norm above 2^63 counts as infinite. Sums run in a
- * fixed order per tensor, tensors in list order (fp64), without atomics.
+ * fixed order without atomics: in fp32 over 16384 elements of a tensor, in fp64
+ * over these chunks of the whole list (every 1024th in order, then a tree).
  * workspace: rlk_grad_norm_workspace_bytes() bytes, one for each of the calls
  * that may overlap on the GPU; out: fp32 [2], 4-byte aligned. */
 size_t rlk_grad_norm_workspace_bytes(const rlk_adamw_tensor* tensors, int32_t n_tensors);

@@ -421,8 +421,7 @@ __global__ void __launch_bounds__(THREADS, kFwdCtas<NV, THREADS, GATE>) adaln_fw
 // begin in the rows [i, i + 1) / grid of all. Their rows follow one another, so
 // the ring runs on from chunk to chunk. A thread owns its columns and adds up A = sum
 // dy * hat, S = sum dy and G = sum d * hat(h) (or d * h) in registers; a
-// chunk's sums go to the workspace, where adaln_fold_kernel adds the chunks in
-// order.
+// chunk's sums go to the workspace, where adaln_fold_kernel adds the chunks.
 template <typename X, typename Y, bool GATE>
 constexpr int kBwdRow = 2 * kPieces<X> + (GATE ? 2 : 1) * kPieces<Y>;  // pieces of 8 columns: x, dr, dy, h
 // CTAs of an SM that the registers are held to. Without a gate 96 registers a

@@ -276,9 +276,12 @@ constexpr const char* kFwdOrder =
 constexpr const char* kAdalnPolicy =
     "fp32 math on bf16 or fp32 rows, variance about the row's mean, IEEE sqrt and division, one rounding per output; "
     "the norm reads the rounded residual";
-constexpr const char* kAdalnRowOrder = "row sums: 8 columns per thread, xor 16..1, warps ascending";
+constexpr const char* kAdalnRowOrder =
+    "row sums: 8 columns a thread (16 above C = 1024) in pairs, xor 16..1; means and squares of the warps joined by xor "
+    "8..1";
 constexpr const char* kAdalnSumOrder =
-    "row sums as in the forward; column sums: token chunks (by T, C), their runs in order, then b ascending";
+    "row sums: a thread's columns in pairs, xor 16..1, warps xor 8..1; column sums: rows of a chunk, each 32nd chunk, "
+    "those runs ascending, weights b ascending";
 const OpInfo kOps[] = {
     {"qk_rmsnorm+multi_axis_rope+joint_attention_fused", "rlk_joint_attn_fwd", kFwdPolicy, kFwdOrder},
     {"joint_attention_fused backward", "rlk_joint_attn_bwd",
@@ -340,7 +343,8 @@ const OpInfo kOps[] = {
      "stochastic rounding by a counter hash; p from the unrounded moments",
      "elementwise"},
     {"gradient norm and clip factor", "rlk_grad_norm", "fp32 squares, fp64 sum of the chunks, IEEE div/sqrt",
-     "chunks of a tensor: a thread's squares in order, xor 16..1, warps ascending; chunks in a fixed tree"},
+     "16384 elements of a tensor: a thread's squares in order, xor 16..1, warps ascending; the list's chunks: each "
+     "1024th in order, xor 16..1 twice"},
 };
 const char* const kKernelNames[kNumKernelIds] = {
     "rope_table_kernel", "prologue_kernel", "attn_fwd_tc_kernel", "bwd_pre_kernel",

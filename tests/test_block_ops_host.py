@@ -146,6 +146,20 @@ def test_adaln_calls_are_traced(L):
                for r in t.records)
 
 
+def test_the_trace_states_the_orders_of_the_sums_in_full(L):
+    """The trees that the GPU tests follow bit by bit, none of them cut off."""
+    sh = pkg.AdalnShape.make(2, 3, 5, 64)
+    with pkg.op_trace() as t:
+        call(L, "modulation_fwd", sh, (None, io()))
+        call(L, "modulation_bwd", sh, (None, io()), (grad(), grad()))
+        L.rlk_grad_norm(None, 1, 1.0, 1.0, P, P, 64, None)
+    for r, words in zip(t.records, (("16 above C = 1024", "xor 16..1", "warps", "xor 8..1"),
+                                    ("warps xor 8..1", "rows of a chunk", "32nd chunk", "runs ascending", "b ascending"),
+                                    ("16384 elements", "warps ascending", "1024th", "xor 16..1 twice"))):
+        assert all(w in r["reduction_order"] for w in words), r["reduction_order"]
+        assert len(r["reduction_order"]) < 159
+
+
 # ------------------------------------------------------------------ optimiser
 def entries(count=2, **over):
     base = dict(p=P, master=None, g=P, m=P, v=P, m_scale=None, v_scale=None, n=64, lr_scale=1.0, weight_decay=0.0,

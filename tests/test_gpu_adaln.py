@@ -435,3 +435,73 @@ def test_the_trace_and_the_timing_name_the_weights_kernel(dev):
     pkg.rlk_kernel_timing(False)
     assert [r["kernels"] for r in t.records] == [three, three[:2], three]
     assert counts == {"adaln_fwd": 0, "adaln_bwd": 3, "adaln_fold": 3, "adaln_weight": 2}
+
+
+def butterfly(x, first):
+    """What a sum by exchanges with lanes xor first .. 1 leaves in a lane, fp32."""
+    while first:
+        x = x + x[..., np.arange(x.shape[-1]) ^ first]
+        first //= 2
+    return x[..., 0]
+
+
+@pytest.mark.parametrize("T, rows", [(20, 1), (300, 4), (2500, 8), (4200, 8)])
+def test_token_sums_run_in_the_stated_order(dev, T, rows):
+    """dshift = sum_t dy bit by bit: rows of a chunk, every 32nd chunk, the runs."""
+    f = np.float32
+    c = Case(dev, 2, 0, T, 264, x="fp32", y="fp32")
+    m = c.op.modulation(c.x, c.scale, c.shift, w=c.w)
+    got = c.op.modulation_bwd(c.x, c.scale, m["stats"], c.dy, None, w=c.w)["dshift"][1].cpu().numpy()
+    dy = c.dy[1].cpu().numpy()
+    chunks = -(-T // rows)
+    part = np.zeros((2, chunks, 264), f)
+    for t in range(T):
+        part[:, t // rows] += dy[:, t]
+    runs = np.zeros((2, 32, 264), f)
+    for j in range(chunks):
+        runs[:, j % 32] += part[:, j]
+    want = runs[:, 0]
+    for k in range(1, 32):
+        want = want + runs[:, k]
+    assert want.dtype == f
+    np.testing.assert_array_equal(got, want)
+
+
+@pytest.mark.parametrize("C", [64, 520, 1024, 1032, 2568, 8192])
+def test_row_sums_run_in_the_stated_order(dev, C):
+    """A LayerNorm row's mean bit by bit: a thread's columns in pairs, its warp's
+    mean, the warps' means (times their columns) by exchanges, 1 / C in two parts."""
+    f, n = np.float32, 7
+    c = Case(dev, 1, 0, n, C, weights=False)
+    got = c.op.modulation(c.x, c.scale, c.shift)["stats"][1][0, :, 0].cpu().numpy()
+    x = c.x[1][0].float().cpu().numpy()
+    groups, per = C // 8, 1 if C <= 1024 else 2
+    threads = -(-(-(-groups // per)) // 32) * 32
+    held = np.zeros((threads * per, 8), f)
+    sums = np.zeros((n, threads), f)
+    for j in range(per):
+        for t in range(threads):
+            at = j * threads + t
+            if at >= groups:
+                continue
+            held[at] = 1
+            p = np.zeros((n, 2), f)
+            for i in range(4):
+                p = p + x[:, 8 * at + 2 * i:8 * at + 2 * i + 2]
+            pair = p[:, 0] + p[:, 1]
+            sums[:, t] = pair if j == 0 else sums[:, t] + pair
+    warps = threads // 32
+    width = held.reshape(per, warps, 32 * 8).sum((0, 2))  # columns of a warp
+    mean = butterfly(sums.reshape(n, warps, 32), 16) * (f(1) / np.maximum(width, f(1)))
+    if warps > 1:
+        slots = np.zeros((n, 16), f)
+        slots[:, :warps] = mean * width
+        s = butterfly(slots, 8)
+        inv = f(1) / f(C)
+        exact = np.longdouble  # (more bits than a product of two fp32 values has)
+        low = f(f(exact(1) - exact(f(C)) * exact(inv))) / f(C)
+        mean = (exact(s) * exact(inv) + exact(s * low)).astype(f)
+    else:
+        mean = mean[:, 0]
+    assert mean.dtype == f
+    np.testing.assert_array_equal(got, mean)

@@ -468,3 +468,43 @@ def test_the_quotient_of_the_smallest_moments(dev):
     units = np.where(np.abs(half) >= 2.0 ** -126, 2, 4) + 1
     bound = np.abs(want) * (2 * O.U * root / d + units * O.U) * 1.001 + 2.0 ** -109
     assert np.all(np.abs(f64(p) - want) <= bound), np.max(np.abs(f64(p) - want) / bound)
+
+
+def test_the_norm_sums_in_the_stated_order(dev):
+    """out[0] bit by bit, of bfloat16 gradients (whose squares fp32 holds): the
+    squares of a thread's eight elements of each pass in order, exchanges, warps
+    ascending; in 64 bits every 1024th chunk of the list, exchanges twice."""
+    import torch
+    f = np.float32
+    sizes = [5, 16384, 16385, 40_000, 1040 * 16384 + 77]
+    g = torch.Generator(device=dev).manual_seed(13)
+    grads = [(torch.randn(n, generator=g, device=dev) * 10.0 ** -i).bfloat16() for i, n in enumerate(sizes)]
+    opt = pkg.AdamW([torch.zeros(n, device=dev) for n in sizes], grads=grads)
+    got = opt.grad_norm(1.0).cpu().numpy()[0]
+
+    def fold(x, lanes):
+        while lanes > 1:
+            lanes //= 2
+            x = x + x[..., np.arange(x.shape[-1]) ^ lanes]
+        return x[..., 0]
+    chunks = []
+    for d in grads:
+        x = d.float().cpu().numpy()
+        x = np.pad(x, (0, -x.size % 16384)).reshape(-1, 8, 256, 8)  # chunk, pass, thread, element
+        s = np.zeros((x.shape[0], 256), f)
+        for j in range(8):
+            for i in range(8):
+                s = s + x[:, j, :, i] ** 2
+        s = fold(s.reshape(-1, 8, 32), 32)
+        total = s[:, 0]
+        for w in range(1, 8):
+            total = total + s[:, w]
+        assert total.dtype == f
+        chunks.append(total)
+    part = np.concatenate(chunks).astype(np.float64)
+    lanes = np.zeros(1024)
+    for i in range(0, part.size, 1024):
+        row = part[i:i + 1024]
+        lanes[:row.size] = lanes[:row.size] + row
+    total = fold(fold(lanes.reshape(32, 32), 32)[None], 32)[0]
+    assert got == np.sqrt(f(total))
