@@ -914,6 +914,8 @@ class _Results(dict):
         self.kinds, self.names, self.pairs, self.pointers = kinds, names, list(pairs.values()), pointers
         self.tensors = [t for pair in self.pairs for t in pair if t is not None]
         self.addresses = [t.data_ptr() for t in self.tensors]
+        # (held, so that no other memory can come to these addresses)
+        self.storages = [t.untyped_storage() for t in self.tensors]
 
     def fits(self, kinds, names):
         return self.kinds is kinds and self.names == names and len(self) == len(self.pairs) and \

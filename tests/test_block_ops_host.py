@@ -352,6 +352,20 @@ def test_adaln_results_passed_back_are_looked_at(L):
         op._outputs(out, names, None)
 
 
+def test_adaln_results_hold_their_memory(L):
+    """A result whose data was replaced twice must not come to its old address with fewer elements behind it."""
+    torch = pytest.importorskip("torch")
+    op, names = pkg.AdaLN(2, 3, 5, 64, device="cpu"), ("y", "stats")
+    for _ in range(40):
+        out, p = op._outputs(None, names, None)
+        t, old = out["y"][1], out["y"][1].data_ptr()
+        t.data = torch.empty(0, dtype=t.dtype)
+        t.data = torch.zeros(2, 5, 63, dtype=t.dtype)
+        assert t.data_ptr() != old
+        with pytest.raises(ValueError, match="y.1."):
+            op._outputs(out, names, None)
+
+
 def test_adamw_binding_refuses_unfit_tensors(L):
     torch = pytest.importorskip("torch")
     p = [torch.zeros(5, 7), torch.zeros(33, dtype=torch.bfloat16)]
