@@ -1117,7 +1117,7 @@ class AdaLN:
         _require_current(self.device)
         io = self._structs(AdalnIo, px, _NONE, _NONE, pscale, _NONE, pw, _NONE, _NONE, _NONE, pst)
         grad = self._structs(AdalnGrad, pdy, pdr, p["dx"], _NONE, _NONE, p["dscale"], p["dshift"], p.get("dw", _NONE))
-        rlk_adaln_modulation_bwd(call, io, grad, self._scratch(stream), self._ws_bytes, _raw_stream(stream, self._index))
+        rlk_adaln_modulation_bwd(call, io, grad, self._scratch(stream), None, _raw_stream(stream, self._index))
         return out
 
     def gate_residual_bwd(self, r, h, gate, scale, stats, dy, dr=None, w=None, w_post=None, post_stats=None, out=None,
@@ -1149,7 +1149,7 @@ class AdaLN:
         io = self._structs(AdalnIo, _NONE, ph, pgate, pscale, _NONE, pw, pwp, pr, _NONE, pst, pps)
         grad = self._structs(AdalnGrad, pdy, pdr, p["dx"], p["dh"], p["dgate"], p.get("dscale", _NONE),
                              p.get("dshift", _NONE), p.get("dw", _NONE), p.get("dw_post", _NONE))
-        rlk_adaln_gate_residual_bwd(call, io, grad, self._scratch(stream), self._ws_bytes, _raw_stream(stream, self._index))
+        rlk_adaln_gate_residual_bwd(call, io, grad, self._scratch(stream), None, _raw_stream(stream, self._index))
         return out
 
 

@@ -366,6 +366,21 @@ def test_adaln_results_hold_their_memory(L):
             op._outputs(out, names, None)
 
 
+def test_adaln_workspace_is_taken_for_what_it_is(L, monkeypatch):
+    """A workspace that someone put in place of the object's own: its own size goes to the library, not the needed one."""
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(pkg, "_require_current", lambda device: None)
+    op = pkg.AdaLN(2, 3, 5, 64, device="cpu")
+    x = (torch.zeros(2, 3, 64, dtype=torch.bfloat16), torch.zeros(2, 5, 64, dtype=torch.bfloat16))
+    stats = (torch.zeros(2, 3, 2), torch.zeros(2, 5, 2))
+    op.workspace = torch.zeros(pkg.rlk_adaln_workspace_bytes(op.shape) - 1, dtype=torch.uint8)
+    for call in (lambda: op.modulation_bwd(x, None, stats, x, stream=0),
+                 lambda: op.gate_residual_bwd(x, x, None, None, stats, x, stream=0)):
+        with pytest.raises(pkg.RlkError) as e:
+            call()
+        assert e.value.code == 4
+
+
 def test_adamw_binding_refuses_unfit_tensors(L):
     torch = pytest.importorskip("torch")
     p = [torch.zeros(5, 7), torch.zeros(33, dtype=torch.bfloat16)]
