@@ -370,12 +370,13 @@ def test_adaln_workspace_is_taken_for_what_it_is(L, monkeypatch):
     """A workspace that someone put in place of the object's own: its own size goes to the library, not the needed one."""
     torch = pytest.importorskip("torch")
     monkeypatch.setattr(pkg, "_require_current", lambda device: None)
+    monkeypatch.setattr(pkg, "_raw_stream", lambda stream, index: 0)
     op = pkg.AdaLN(2, 3, 5, 64, device="cpu")
     x = (torch.zeros(2, 3, 64, dtype=torch.bfloat16), torch.zeros(2, 5, 64, dtype=torch.bfloat16))
     stats = (torch.zeros(2, 3, 2), torch.zeros(2, 5, 2))
     op.workspace = torch.zeros(pkg.rlk_adaln_workspace_bytes(op.shape) - 1, dtype=torch.uint8)
-    for call in (lambda: op.modulation_bwd(x, None, stats, x, stream=0),
-                 lambda: op.gate_residual_bwd(x, x, None, None, stats, x, stream=0)):
+    for call in (lambda: op.modulation_bwd(x, None, stats, x),
+                 lambda: op.gate_residual_bwd(x, x, None, None, stats, x)):
         with pytest.raises(pkg.RlkError) as e:
             call()
         assert e.value.code == 4
