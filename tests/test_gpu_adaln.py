@@ -505,3 +505,137 @@ def test_row_sums_run_in_the_stated_order(dev, C):
         mean = mean[:, 0]
     assert mean.dtype == f
     np.testing.assert_array_equal(got, mean)
+
+
+WIDE = [
+    # the last width of each number of columns a thread and threads a CTA, and the first of the next
+    1024, 1032, 1288, 2048, 2056, 2560, 2568, 4096, 4104, 5120, 5128, 6144, 6152, 8192]
+WIDE_KINDS = [
+    dict(norm="layer", post="none", x="bf16", y="bf16", mod="bf16", weights=False, alpha=1.0),
+    dict(norm="layer", post="rms", x="bf16", y="bf16", mod="bf16"),
+    dict(norm="rms", post="layer", x="fp32", y="bf16", mod="bf16"),
+    dict(norm="layer", post="none", x="fp32", y="fp32", mod="fp32", alpha=-1.25),
+]
+
+
+def column_sum(got, terms, shares, where):
+    """A sum over tokens in 64 bits on the device: each term has at most six roundings, the sum T + 8, its factor two."""
+    import torch
+    value = shares * terms.sum(1)
+    tol = (terms.shape[1] + 16) * O.U * shares.abs() * terms.abs().sum(1)
+    bad = (got.double() - value).abs() > tol + 1e-37
+    assert not bool(bad.any()), (where, int(bad.sum()))
+
+
+@pytest.mark.parametrize("kind", WIDE_KINDS, ids=lambda k: "-".join(str(v) for v in k.values()))
+@pytest.mark.parametrize("C", WIDE)
+def test_many_rows_of_wide_columns(dev, C, kind):
+    """More rows than CTAs, so that each goes through its ring and its exchange
+    buffers several times and from sample to sample and stream to stream: every
+    row has the bytes of calls of a few rows (one a CTA, which are held against the
+    definition above), the column sums are held against 64 bits on the device."""
+    import torch
+    B, T = 3, (90, 1250 if C <= 2560 else 610)
+    c = Case(dev, B, *T, C, **kind)
+    m = c.op.modulation(c.x, c.scale, c.shift, w=c.w)
+    b = c.op.modulation_bwd(c.x, c.scale, m["stats"], c.dy, c.dr, w=c.w)
+    f = c.op.gate_residual(c.x, c.h, c.gate, c.scale, c.shift, w=c.w, w_post=c.w_post)
+    post = dict(w_post=c.w_post, post_stats=f.get("post_stats"))
+    q = c.op.gate_residual_bwd(f["r"], c.h, c.gate, c.scale, f["stats"], c.dy, c.dr, w=c.w, **post)
+    last = c.op.gate_residual_bwd(f["r"], c.h, c.gate, None, None, None, c.dr, **post)
+    n = 25  # tokens of a sample in a call of few rows
+    few = pkg.AdaLN(B, 0, n, C, norm=c.norm, post=c.post, x_dtype=c.op.x_dtype, y_dtype=c.op.y_dtype,
+                    mod_dtype=c.op.mod_dtype, eps=EPS, alpha=c.alpha, device=dev)
+    for i in (0, 1):
+        side = lambda pair: None if pair is None else (None, pair[i])  # noqa: E731
+        for t in {0, 17, T[i] // 2, T[i] - n}:
+            def some(pair):
+                return None if pair is None else (None, pair[i][:, t:t + n].contiguous())
+            x, h, dy, dr = (some(p) for p in (c.x, c.h, c.dy, c.dr))
+            mods = [side(p) for p in (c.gate, c.scale, c.shift)]
+            m1 = few.modulation(x, *mods[1:], w=side(c.w))
+            b1 = few.modulation_bwd(x, mods[1], m1["stats"], dy, dr, w=side(c.w))
+            f1 = few.gate_residual(x, h, *mods, w=side(c.w), w_post=side(c.w_post))
+            p1 = dict(w_post=side(c.w_post), post_stats=f1.get("post_stats"))
+            q1 = few.gate_residual_bwd(f1["r"], h, *mods[:2], f1["stats"], dy, dr, w=side(c.w), **p1)
+            l1 = few.gate_residual_bwd(f1["r"], h, mods[0], None, None, None, dr, **p1)
+            for got, ref, names in ((m, m1, ("y", "stats")), (b, b1, ("dx",)), (f, f1, list(f1)), (q, q1, ("dx", "dh")),
+                                    (last, l1, ("dx", "dh"))):
+                for k in names:
+                    assert Hh.bits_equal(got[k][i][:, t:t + n].contiguous(), ref[k][1]), (i, t, k)
+        row = lambda pair, absent: torch.full((B, C), absent, dtype=torch.float64, device=dev) if pair is None \
+            else pair[i].double().expand(B, C)  # noqa: E731
+
+        def hat(v, stats):
+            s = stats[i].double()
+            return (v[i].double() - s[..., :1]) * s[..., 1:]
+        w, wp, gate = row(c.w, 1.0), row(c.w_post, 1.0), row(c.gate, 1.0)
+        for got, rows, stats in ((b, c.x, m["stats"]), (q, f["r"], f["stats"])):
+            z = c.dy[i].double() * hat(rows, stats)
+            column_sum(got["dscale"][i], z, w, (i, "dscale"))
+            column_sum(got["dshift"][i], c.dy[i].double(), torch.ones_like(w), (i, "dshift"))
+            if c.w is not None:
+                column_sum(got["dw"][i][None], z.reshape(1, -1, C) * (1 + row(c.scale, 0.0)).repeat_interleave(T[i], 0)[None],
+                           w[:1] * 0 + 1, (i, "dw"))
+        hh = c.h[i].double() if c.post == "none" else hat(c.h, f["post_stats"])
+        # the residual's gradient alone is d itself, and with fp32 rows dx is
+        for got, d in ((last, c.dr[i]), (q, q["dx"][i])) if c.op.x_dtype == torch.float32 else ((last, c.dr[i]),):
+            z = d.double() * hh
+            column_sum(got["dgate"][i], z, c.alpha * wp, (i, "dgate"))
+            if c.w_post is not None:
+                column_sum(got["dw_post"][i][None], z.reshape(1, -1, C) * gate.repeat_interleave(T[i], 0)[None],
+                           w[:1] * 0 + c.alpha, (i, "dw_post"))
+
+
+def test_forms_that_only_the_c_entries_take(dev):
+    """Gradients' rows further apart than C, a backward that wants dw but neither
+    dscale nor dshift, dgate alone, weights of one stream alone: the bytes of the class."""
+    import torch
+    c = Case(dev, 3, 20, 150, 520, post="rms")
+    B, C = c.B, c.C
+    f = c.op.gate_residual(c.x, c.h, c.gate, c.scale, c.shift, w=c.w, w_post=c.w_post)
+    want = c.op.gate_residual_bwd(f["r"], c.h, c.gate, c.scale, f["stats"], c.dy, c.dr, w=c.w, w_post=c.w_post,
+                                  post_stats=f["post_stats"])
+    sums = {"dgate": B, "dscale": B, "dshift": B, "dw": 1, "dw_post": 1}
+    stride = 3 * C + 4
+    sh = pkg.AdalnShape.from_buffer_copy(c.op.shape)
+    sh.mod_stride, sh.dmod_stride = c.scale[0].stride(0), stride
+    ws = torch.empty(pkg.rlk_adaln_workspace_bytes(sh), dtype=torch.uint8, device=dev)
+    ptr = lambda t: t.data_ptr()  # noqa: E731
+    for names in (tuple(sums), ("dw",), ("dw_post",), ("dgate",), ("dshift", "dw_post"), ()):
+        io, grad, got = [], [], []
+        for i in (0, 1):
+            # the three rows of a sample side by side in one buffer
+            rows = torch.full((B, stride), -3.0, device=dev)
+            outs = {k: rows[:, j * C:(j + 1) * C] for j, k in enumerate(("dgate", "dscale", "dshift"))}
+            outs.update(dw=torch.empty(C, device=dev), dw_post=torch.empty(C, device=dev),
+                        dx=torch.empty_like(c.x[i]), dh=torch.empty_like(c.h[i]))
+            got.append((rows, outs))
+            io.append(pkg.AdalnIo(h=ptr(c.h[i]), gate=ptr(c.gate[i]), scale=ptr(c.scale[i]), w=ptr(c.w[i]),
+                                  w_post=ptr(c.w_post[i]), r=ptr(f["r"][i]), stats=ptr(f["stats"][i]),
+                                  post_stats=ptr(f["post_stats"][i])))
+            grad.append(pkg.AdalnGrad(dy=ptr(c.dy[i]), dr=ptr(c.dr[i]), dx=ptr(outs["dx"]), dh=ptr(outs["dh"]),
+                                      **{k: ptr(outs[k]) for k in names}))
+        pkg.rlk_adaln_gate_residual_bwd(sh, io, grad, ws)
+        torch.cuda.synchronize()
+        for i, (rows, outs) in enumerate(got):
+            for k in ("dx", "dh", *names):
+                assert Hh.bits_equal(outs[k].contiguous(), want[k][i]), (names, i, k)
+            for k in {"dgate", "dscale", "dshift"} - set(names):
+                assert bool((outs[k] == -3.0).all()), (names, i, k)
+            assert bool((rows[:, 3 * C:] == -3.0).all())
+    # weights of one stream alone: of the other they are 1
+    ones = torch.ones(C, device=dev)
+    for i in (0, 1):
+        alone = lambda pair: tuple(t if j == i else None for j, t in enumerate(pair))  # noqa: E731
+        full = lambda pair: tuple(t if j == i else ones for j, t in enumerate(pair))  # noqa: E731
+        res = []
+        for pick in (alone, full):
+            g = c.op.gate_residual(c.x, c.h, c.gate, c.scale, c.shift, w=pick(c.w), w_post=pick(c.w_post))
+            res.append((g, c.op.gate_residual_bwd(g["r"], c.h, c.gate, c.scale, g["stats"], c.dy, c.dr, w=pick(c.w),
+                                                  w_post=pick(c.w_post), post_stats=g["post_stats"])))
+        for a, b in zip(*res):
+            assert set(a) == set(b)
+            for k in a:
+                for j in (0, 1):
+                    assert Hh.bits_equal(a[k][j], b[k][j]), (i, k, j)

@@ -508,3 +508,31 @@ def test_the_norm_sums_in_the_stated_order(dev):
         lanes[:row.size] = lanes[:row.size] + row
     total = fold(fold(lanes.reshape(32, 32), 32)[None], 32)[0]
     assert got == np.sqrt(f(total))
+
+
+def test_long_chunks_step_like_short_ones(dev):
+    """Chunks of two, four and eight passes, whose copies ahead go round their
+    stages several times: the bytes of each tensor stepped alone in chunks of
+    one pass, from states of a step before, gradients and parameters of both types."""
+    import torch
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    for passes in (2, 4, 8):
+        count = 6
+        share = 8 * sms * 2048 * passes // count
+        sizes = [share + 16385 * passes + 321 * i for i in range(count)]  # chunks that do not come out even
+        if passes == 8:  # each still below the length from which a tensor alone takes two passes
+            sizes = [min(n, 8 * sms * 4096 - 4097 + 31 * i) for i, n in enumerate(sizes)]
+        assert sum(n // (2048 * passes) for n in sizes) >= 8 * sms and all(-(-n // 4096) < 8 * sms for n in sizes)
+        opt, grads = make(dev, sizes, 8, weight_decay=0.01, lr_scale=1.0)
+        copies = [truth(opt, i).clone() for i in range(count)]
+        for step in (1, 2):
+            opt.step(step)
+        for i in range(count):
+            p = copies[i].bfloat16() if opt.masters[i] is not None else copies[i]
+            one = pkg.AdamW([p], masters=[copies[i]] if opt.masters[i] is not None else None, state_bits=8,
+                            lr=HYPER["lr"], betas=(0.9, 0.95), weight_decay=0.01, seed=77, keys=[i], grads=[grads[i]])
+            for step in (1, 2):
+                one.step(step)
+            for a, b in ((truth(one, 0), truth(opt, i)), (p, opt.params[i]), (one.m[0], opt.m[i]), (one.v[0], opt.v[i]),
+                         (one.m_scale[0], opt.m_scale[i]), (one.v_scale[0], opt.v_scale[i])):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), (passes, i)
