@@ -803,12 +803,14 @@ cudaError_t bwd_xy(const AdalnArgs& a, bool gate, cudaStream_t s) {
 // ones spread few rows over the SMs (1024^2 modulation, T = 4096: 49, 42, 46 us;
 // T = 513: 16.3 us with 4 rows for 18.6 with 8). Narrow rows leave room for more
 // CTAs, which 16-row chunks do not fill: 8 for 16 took 0.72 to 0.94 of the
-// time at T = 4096 and C <= 512 and as long with 8 samples of T = 6889, at
-// C = 768 .. 1280 0.76 to 0.94 with one or two samples and up to 1.04 with
-// four, but 1.05 to 1.10 with those of T = 6889. (4 rows there, and 2 below T =
+// time at T = 4096 and C <= 512 and as long with 8 samples of T = 6889. At
+// C = 520 .. 1280, one, two and four samples with and without a gate, it took
+// 0.88 of the time in the mean at T = 4096 (0.66 to 1.10), 0.97 at 4608, 0.95 at
+// 4800, 1.01 at 5200, 1.04 at 6032 (0.89 to 1.11; one sample 1.03, four 1.07) and
+// 0.99 at 6889 (one sample 0.94, four 1.05). (4 rows there, and 2 below T =
 // 2048, gain up to a quarter with one sample and lose as much with four.)
 int adaln_chunk_rows(int T, int C) {
-    if (T >= 4096) return C <= 512 || (C <= 1280 && T < 6144) ? 8 : 16;
+    if (T >= 4096) return C <= 512 || (C <= 1280 && T < 5120) ? 8 : 16;
     return T >= 2048 ? 8 : (T >= 128 ? 4 : (T > 32 ? 2 : 1));
 }
 

@@ -639,3 +639,23 @@ def test_forms_that_only_the_c_entries_take(dev):
             for k in a:
                 for j in (0, 1):
                     assert Hh.bits_equal(a[k][j], b[k][j]), (i, k, j)
+
+
+@pytest.mark.parametrize("T, C, rows", [(5119, 520, 8), (6032, 520, 16), (6032, 512, 8), (4096, 1288, 16)])
+def test_chunks_of_long_streams_by_their_rule(dev, T, C, rows):
+    """dshift bit by bit on both sides of the rule for narrow rows."""
+    f = np.float32
+    g = Case(dev, 1, 0, T, C, x="fp32", y="fp32", weights=False)
+    m = g.op.modulation(g.x, g.scale, g.shift)
+    got = g.op.modulation_bwd(g.x, g.scale, m["stats"], g.dy, None)["dshift"][1][0].cpu().numpy()
+    dy = g.dy[1][0].cpu().numpy()
+    part = np.zeros((-(-T // rows), C), f)
+    for t in range(T):
+        part[t // rows] += dy[t]
+    runs = np.zeros((32, C), f)
+    for j, p in enumerate(part):
+        runs[j % 32] += p
+    want = runs[0]
+    for r in runs[1:]:
+        want = want + r
+    np.testing.assert_array_equal(got, want)
