@@ -229,7 +229,10 @@ __device__ __forceinline__ float thread_sum(bool last, F f) {
 }
 
 // s / C as s times 1 / C in two parts: one rounding of 1 / C alone would shift
-// every row's statistics the same way.
+// every row's statistics the same way. (A warp's own mean takes 1 / its columns
+// rounded once: exact for a whole warp's 256 or 512, and a last bit of the mean
+// for a row of one warp, C <= 256, unless C is a power of two. The backward's
+// two means take the rounded 1 / C: they are small next to the row's values.)
 __device__ __forceinline__ float per_column(float s, const RowSums& g) { return fmaf(s, g.inv_c, s * g.inv_c_low); }
 
 // Mean (0 for rms) and 1 / deviation of a row. Each warp takes its own mean

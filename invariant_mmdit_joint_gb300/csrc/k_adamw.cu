@@ -266,8 +266,9 @@ struct Scalars {
     float s, b1, b2, o1, o2, inv_c2, eps, most, none, step, decay;  // step = rate / (1 - beta1^t); decay = rate * weight decay
 };
 
-// m / (sqrt(v) * c + eps), each of the two within one unit in the last place:
-// for eight elements at once, Newton's step for the square root from the
+// m / (sqrt(v) * c + eps), each of the two within one unit in the last place
+// (the quotient of a subnormal m within two, whose residual r is below the type's
+// last bit): for eight elements at once, Newton's step for the square root from the
 // hardware's estimate of 1 / sqrt, and Markstein's for the quotient (q + r /
 // d, r = m - d q by one fma) from its estimate of 1 / d. Written out, because
 // the compiler's square root and division each carry a branch an element for
@@ -578,7 +579,10 @@ __global__ void __launch_bounds__(kThreads, ANY8 ? 4 : 3) adamw_kernel(const __g
 
 // ------------------------------------------------------------ gradient norm
 // A chunk's squares: a thread's in order, then its warp's by exchanges, then
-// the eight warps ascending. 45 million bf16 gradients are 90 MB, 13 us at the
+// the eight warps ascending, in fp32: 76 roundings in a row at most, 2^-18 of
+// the chunk's sum and half that of the norm (a few 2^-24 as roundings fall), and
+// the range that the header states. An SM does two fp64 fmas a cycle: 45 million
+// squares in fp64 would take 70 us. 45 million bf16 gradients are 90 MB, 13 us at the
 // copy bandwidth; norm, fold and the step that follows take 207 us, 22 of them
 // for the first two (26 with a check of the bounds at each load).
 template <bool G32>
@@ -592,7 +596,7 @@ __device__ __forceinline__ float thread_squares(const Entry& e, long long i0, in
     };
     constexpr int kPasses = kNormChunk / kPass;
     const long long at = i0 + tid * kPerThread;
-    if (e.n - i0 >= kNormChunk) {  // no bounds to look at: all loads are under way at once
+    if (e.n - i0 >= kNormChunk) {  // no bounds to look at between the loads
         V8 v[kPasses];
 #pragma unroll
         for (int j = 0; j < kPasses; ++j) v[j] = load_grad<G32>(e, at + j * kPass, 8);
@@ -622,8 +626,9 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
 }
 
 // The list's sum from its chunks', and what follows from it. One CTA, bound by
-// latency: only the sum is in fp64 (the root too, and 32 warps' sums added one
-// by one, took 1 us longer).
+// latency: only the sum over the list is in fp64, which is what grows long. Its
+// root in fp32 is two roundings more of a value that the chunks leave some units
+// off anyway (in fp64, and with 32 warps' sums added one by one, 1 us longer).
 __global__ void __launch_bounds__(1024) grad_norm_fold_kernel(const float* part, long long n, float pre, float max_norm,
                                                               float* out) {
     __shared__ double ws[32];
