@@ -388,15 +388,13 @@ __device__ __forceinline__ void adamw_chunk8(const Entry& e, const Scalars& k, l
         }
         asm volatile("cp.async.commit_group;\n" ::: "memory");
     };
-    // Past the end a scale is 0, and m and v with it: the threads there take part
-    // in the exchanges of a last block, which another scale kept from the pass
-    // before could turn into NaN (0 * infinity).
-    uint32_t next_ms, next_vs;
+    uint32_t next_ms = 0, next_vs = 0;
     auto read_scales = [&](int j) {
         const long long i = at + (long long)j * kPass;
-        const bool inside = j < passes && i < e.n;
-        next_ms = inside ? e.ms[i / 32] : 0u;
-        next_vs = inside ? e.vs[i / 32] : 0u;
+        if (j < passes && i < e.n) {
+            next_ms = e.ms[i / 32];
+            next_vs = e.vs[i / 32];
+        }
     };
 #pragma unroll
     for (int j = 0; j < kStages - 1; ++j) fill(j, j * kStageBytes<G32>);
@@ -409,7 +407,7 @@ __device__ __forceinline__ void adamw_chunk8(const Entry& e, const Scalars& k, l
         const uint8_t* const ready = smem + stage;
         filled = stage;
         stage = stage == (kStages - 1) * kStageBytes<G32> ? 0 : stage + kStageBytes<G32>;
-        const uint32_t old_ms = next_ms, old_vs = next_vs;
+        uint32_t old_ms = next_ms, old_vs = next_vs;
         read_scales(j + 1);
         asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 1) : "memory");
         const long long i = at + (long long)j * kPass;
@@ -437,6 +435,9 @@ __device__ __forceinline__ void adamw_chunk8(const Entry& e, const Scalars& k, l
             p = load8(master + i, left);
             mq = load_codes(mc + i, left);
             vq = load_codes(vc + i, left);
+            // Past the end m and v are 0, and so is their scale: the threads there take part in the exchanges of a
+            // last block, which the scale kept from the pass before could turn into NaN (0 * infinity).
+            if (left == 0) old_ms = old_vs = 0;
         }
         V8 m = decode8(mq, old_ms), v = decode8(vq, old_vs);
         const float top = update8(k, g, m, v, p);
