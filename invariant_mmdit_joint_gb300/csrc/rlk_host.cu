@@ -1287,33 +1287,55 @@ static rlk_status grads_ok(const rlk_adamw_tensor* t, int32_t n) {
     return RLK_OK;
 }
 
-// No written range of the list may overlap another one of its ranges: sorted
-// by their starts, each is held against the furthest ends before it.
+// No written range of the list may overlap another one of its ranges. The
+// ranges of one kind (all m, all bf16 parameters, ...) are mostly views of one
+// buffer in order, or allocated in order: if each kind is, and no kind's span
+// meets another one's, nothing overlaps. Otherwise all ranges are sorted by their
+// starts and each is held against the furthest ends before it (180 tensors of
+// 1200 ranges: 9 us).
 static rlk_status list_disjoint(const rlk_adamw_tensor* t, int32_t n) {
+    enum Kind { kG16, kG32, kP16, kP32, kMaster, kM, kV, kMs, kVs, kKinds };
+    auto each = [&](auto&& add) {
+        for (int i = 0; i < n; ++i) {
+            const rlk_adamw_tensor& e = t[i];
+            const uint64_t c = (uint64_t)e.n;
+            if (c == 0) continue;
+            e.g_dtype == RLK_FP32 ? add(kG32, e.g, c * 4) : add(kG16, e.g, c * 2);
+            e.master != nullptr ? add(kP16, e.p, c * 2) : add(kP32, e.p, c * 4);
+            if (e.master != nullptr) add(kMaster, e.master, c * 4);
+            add(kM, e.m, c * (e.state_bits / 8));
+            add(kV, e.v, c * (e.state_bits / 8));
+            if (e.state_bits == 8) {
+                add(kMs, e.m_scale, (c + 31) / 32);
+                add(kVs, e.v_scale, (c + 31) / 32);
+            }
+        }
+    };
+    struct Span {
+        uintptr_t lo = 0, hi = 0;  // hi 0: empty
+    } span[kKinds];
+    bool ordered = true;
+    each([&](int kind, const void* p, uint64_t bytes) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+        Span& s = span[kind];
+        if (s.hi == 0) s.lo = lo;
+        ordered = ordered && lo >= s.hi;
+        s.hi = lo + bytes;
+    });
+    for (int a = 0; a < kKinds; ++a)
+        for (int b = std::max(a + 1, (int)kP16); b < kKinds; ++b)  // (gradients may meet gradients)
+            ordered = ordered && (span[a].hi <= span[b].lo || span[b].hi <= span[a].lo);
+    if (ordered) return RLK_OK;
     struct Range {
         uintptr_t lo, hi;  // lo is 16-byte aligned: its last bit says whether the range is written
     };
     std::unique_ptr<Range[]> r(new (std::nothrow) Range[(size_t)n * 7]);
     if (!r) return RLK_ERR_CUDA;
     size_t k = 0;
-    auto add = [&](const void* p, uint64_t bytes, bool written) {
+    each([&](int kind, const void* p, uint64_t bytes) {
         const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-        r[k++] = Range{lo | (written ? 1u : 0u), lo + bytes};
-    };
-    for (int i = 0; i < n; ++i) {
-        const rlk_adamw_tensor& e = t[i];
-        const uint64_t c = (uint64_t)e.n;
-        if (c == 0) continue;
-        add(e.p, c * (e.master != nullptr ? 2 : 4), true);
-        if (e.master != nullptr) add(e.master, c * 4, true);
-        add(e.g, c * (e.g_dtype == RLK_FP32 ? 4 : 2), false);
-        add(e.m, c * (e.state_bits / 8), true);
-        add(e.v, c * (e.state_bits / 8), true);
-        if (e.state_bits == 8) {
-            add(e.m_scale, (c + 31) / 32, true);
-            add(e.v_scale, (c + 31) / 32, true);
-        }
-    }
+        r[k++] = Range{lo | (kind >= kP16 ? 1u : 0u), lo + bytes};
+    });
     std::sort(r.get(), r.get() + k, [](const Range& a, const Range& b) { return a.lo < b.lo; });
     uintptr_t any = 0, written = 0;
     for (size_t i = 0; i < k; ++i) {

@@ -228,25 +228,29 @@ def test_overlaps_are_found_in_any_order(L):
         pytest.skip("addresses of no memory: for machines without a GPU")
     rng = np.random.default_rng(12)
     seen = set()
-    for trial in range(300):
+    for trial in range(600):
         count = int(rng.integers(1, 40))
         t = (pkg.AdamwTensor * count)()
-        # distinct slots, in order, shuffled, or with a collision
+        # distinct slots: each kind's buffers in a run, tensor by tensor, or shuffled; some with a collision
         slots = np.arange(7 * count)
-        if trial % 3:
+        flat = trial % 3 == 0
+        if flat:
+            slots = slots.reshape(7, count).T.reshape(-1)
+        elif trial % 3 == 1:
             rng.shuffle(slots)
         ranges = []
         for i in range(count):
             bits, copy, n = int(rng.choice([8, 32])), bool(rng.integers(2)), int(rng.integers(0, 4096))
+            copy = copy if not flat else trial % 2 == 0 or i < count // 2
             fields = {"g": (4, False), "p": (2 if copy else 4, True), "m": (bits // 8, True), "v": (bits // 8, True)}
             if copy:
                 fields["master"] = (4, True)
             if bits == 8:
                 fields.update(m_scale=(1 / 32, True), v_scale=(1 / 32, True))
             t[i].n, t[i].state_bits, t[i].g_dtype, t[i].lr_scale = n, bits, 1, 1.0
-            for j, (k, (size, written)) in enumerate(fields.items()):
-                at = P + 16384 * int(slots[7 * i + j])
-                if trial % 2 and rng.random() < 0.02:
+            for k, (size, written) in fields.items():
+                at = P + 16384 * int(slots[7 * i + ("g", "p", "master", "m", "v", "m_scale", "v_scale").index(k)])
+                if trial % 4 > 1 and rng.random() < 0.02:
                     at += int(rng.integers(-8192, 8192)) // 16 * 16  # perhaps into a neighbour
                 if k == "g" and rng.random() < 0.2:
                     at = P + 16384 * 7 * count  # one shared by several
@@ -255,8 +259,8 @@ def test_overlaps_are_found_in_any_order(L):
                     ranges.append((at, at + int(np.ceil(n * size)), written))
         bad = any((a[2] or b[2]) and a[0] < b[1] and b[0] < a[1] for i, a in enumerate(ranges) for b in ranges[:i])
         assert L.rlk_adamw_step(t, count, ref(args()), None) == (1 if bad else 5), trial
-        seen.add(bad)
-    assert seen == {False, True}
+        seen.add((flat, bad))
+    assert len(seen) == 4
 
 
 def test_grad_norm_fails_closed(L):
