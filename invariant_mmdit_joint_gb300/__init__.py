@@ -901,6 +901,23 @@ def _empty(size, dtype, device, stream):
         return torch.empty(size, dtype=dtype, device=device)
 
 
+def _workspace(owner, size, stream, handle):
+    """The workspace of an object's calls, allocated at the first one. Its memory
+    goes back to the stream it was allocated for when the object does, perhaps
+    while another stream's call still works in it: a torch stream that uses it is
+    recorded, so that the memory waits for it."""
+    import torch
+    if owner.workspace is None:
+        owner.workspace = _empty(size, torch.uint8, owner.device, stream)
+        owner._streams.add(handle)
+    elif handle not in owner._streams and owner.workspace.is_cuda:
+        s = torch.cuda.current_stream(owner.device) if stream is None else stream
+        if not isinstance(s, int):
+            owner.workspace.record_stream(s)
+        owner._streams.add(handle)
+    return owner.workspace
+
+
 _NONE = (None, None)
 
 
@@ -937,7 +954,8 @@ class AdaLN:
     Every call returns its outputs as a dict of pairs; passing that dict back
     as ``out`` reuses its buffers. The backward calls share one workspace:
     calls that may overlap on the GPU (other streams, graphs replayed at the
-    same time) need an object each."""
+    same time) need an object each. An object outlives the graphs that captured
+    its calls, and its calls on a stream that is given as an address."""
 
     def __init__(self, B: int, T_txt: int, T_img: int, C: int, norm: str = "layer", post: str | None = None,
                  x_dtype=None, y_dtype=None, mod_dtype=None, eps: float = 1e-6, alpha: float = 1.0, device="cuda"):
@@ -968,7 +986,7 @@ class AdaLN:
                        "dx": (self._rows, x), "dh": (self._rows, y), "dgate": (self._sums, f), "dscale": (self._sums, f),
                        "dshift": (self._sums, f), "dw": (self._vector, f), "dw_post": (self._vector, f)}
         self._shapes = {}  # the call's shape struct by the modulation's sample stride
-        self.workspace = None  # of the backward, allocated at its first call
+        self.workspace, self._streams = None, set()  # of the backward, allocated at its first call; used by
 
     # ---- checks
     def _bad(self, name, i, t, want, dtype):
@@ -1065,12 +1083,6 @@ class AdaLN:
         """One struct of pointers per stream, its fields in order (None for a stream without tokens)."""
         return [cls(*[p[i] for p in pairs]) if self._live[i] else None for i in (0, 1)]
 
-    def _scratch(self, stream):
-        if self.workspace is None:
-            import torch
-            self.workspace = _empty(self._ws_bytes, torch.uint8, self.device, stream)
-        return self.workspace
-
     # ---- calls
     def modulation(self, x, scale, shift, w=None, out=None, stream=None):
         """y = hat(x) * w * (1 + scale) + shift. Returns y and stats."""
@@ -1117,7 +1129,8 @@ class AdaLN:
         _require_current(self.device)
         io = self._structs(AdalnIo, px, _NONE, _NONE, pscale, _NONE, pw, _NONE, _NONE, _NONE, pst)
         grad = self._structs(AdalnGrad, pdy, pdr, p["dx"], _NONE, _NONE, p["dscale"], p["dshift"], p.get("dw", _NONE))
-        rlk_adaln_modulation_bwd(call, io, grad, self._scratch(stream), None, _raw_stream(stream, self._index))
+        handle = _raw_stream(stream, self._index)
+        rlk_adaln_modulation_bwd(call, io, grad, _workspace(self, self._ws_bytes, stream, handle), None, handle)
         return out
 
     def gate_residual_bwd(self, r, h, gate, scale, stats, dy, dr=None, w=None, w_post=None, post_stats=None, out=None,
@@ -1149,7 +1162,8 @@ class AdaLN:
         io = self._structs(AdalnIo, _NONE, ph, pgate, pscale, _NONE, pw, pwp, pr, _NONE, pst, pps)
         grad = self._structs(AdalnGrad, pdy, pdr, p["dx"], p["dh"], p["dgate"], p.get("dscale", _NONE),
                              p.get("dshift", _NONE), p.get("dw", _NONE), p.get("dw_post", _NONE))
-        rlk_adaln_gate_residual_bwd(call, io, grad, self._scratch(stream), None, _raw_stream(stream, self._index))
+        handle = _raw_stream(stream, self._index)
+        rlk_adaln_gate_residual_bwd(call, io, grad, _workspace(self, self._ws_bytes, stream, handle), None, handle)
         return out
 
 
@@ -1173,7 +1187,9 @@ class AdamW:
     parameters, the gradients, and what was read from the other lists), and its
     old memory stays allocated. ``lr`` may be set at any time. grad_norm's
     calls share one workspace: calls that may overlap on the GPU need an object
-    each."""
+    each. An object outlives the graphs that captured its calls, and its calls on
+    a stream that is given as an address. States and masters that are made here
+    are written on the current stream."""
 
     def __init__(self, params, masters=None, state_bits: int = 32, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay=0.01, lr_scale=1.0, seed: int = 0, keys=None, grads=None, m=None, v=None, m_scale=None,
@@ -1238,7 +1254,7 @@ class AdamW:
             self._take(grads)
         self._args = AdamwArgs(lr=self.lr, beta1=float(betas[0]), beta2=float(betas[1]), eps=float(eps), seed=int(seed))
         self._args_ref = ctypes.byref(self._args)
-        self.workspace = None  # of grad_norm, allocated at its first call
+        self.workspace, self._streams = None, set()  # of grad_norm, allocated at its first call; used by
 
     def _hand_out(self, name):
         held = self._lists[name]
@@ -1311,10 +1327,12 @@ class AdamW:
             out = _empty(2, torch.float32, self.device, stream)
         else:
             self._dense("out", out, (torch.float32,), 2)
-        if self.workspace is None:
-            self.workspace = _empty(rlk_grad_norm_workspace_bytes(self._list, n), torch.uint8, self.device, stream)
-        rc = lib().rlk_grad_norm(self._list, n, float(pre_scale), float(max_norm), out.data_ptr(), self.workspace.data_ptr(),
-                                 self.workspace.numel(), _raw_stream(stream, self._index))
+        handle = _raw_stream(stream, self._index)
+        ws = self.workspace
+        if ws is None or handle not in self._streams:
+            ws = _workspace(self, rlk_grad_norm_workspace_bytes(self._list, n), stream, handle)
+        rc = lib().rlk_grad_norm(self._list, n, float(pre_scale), float(max_norm), out.data_ptr(), ws.data_ptr(), ws.numel(),
+                                 handle)
         if rc:
             _check(rc, "rlk_grad_norm")
         return out

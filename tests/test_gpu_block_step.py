@@ -156,3 +156,45 @@ def test_calls_on_two_streams_at_once(dev):
     for other in results[1:]:
         for a, b in zip(results[0], other):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_a_workspace_waits_for_the_streams_that_use_it(dev):
+    """Objects that go while a call on another stream than their workspace's own
+    has not run yet: its memory may not come to a tensor of the first stream
+    before that."""
+    import torch
+    g = torch.Generator(device=dev).manual_seed(6)
+
+    def r(*shape):
+        return torch.randn(shape, generator=g, device=dev).bfloat16()
+    B, T, C = 2, (40, 3000), 1024
+    x, dy = (tuple(r(B, t, C) for t in T) for _ in range(2))
+    grads = [torch.randn(n, generator=g, device=dev) for n in (3_000_001, 70_000)]
+    other = torch.cuda.Stream()
+    for by_hand in (False, True):
+        op = pkg.AdaLN(B, *T, C, device=dev)
+        opt = pkg.AdamW([torch.zeros_like(d) for d in grads], grads=grads)
+        stats = op.modulation(x, None, None)["stats"]
+        out, norm = op.modulation_bwd(x, None, stats, dy), opt.grad_norm(1.0)
+        want = [t.clone() for k in sorted(out) for t in out[k]] + [norm.clone()]
+        for t in (*(t for p in out.values() for t in p), norm):
+            t.zero_()
+        sizes = [op.workspace.numel(), opt.workspace.numel()]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(other):
+            torch.cuda._sleep(40_000_000)  # 20 ms ahead of the calls
+            if not by_hand:
+                op.modulation_bwd(x, None, stats, dy, out=out)
+                opt.grad_norm(1.0, out=norm)
+        if by_hand:
+            op.modulation_bwd(x, None, stats, dy, out=out, stream=other)
+            opt.grad_norm(1.0, out=norm, stream=other)
+        assert not other.query()
+        del op, opt
+        junk = [torch.full((n // 4,), float("nan"), device=dev) for n in sizes for _ in range(4)]
+        other.synchronize()
+        torch.cuda.synchronize()
+        got = [t for k in sorted(out) for t in out[k]] + [norm]
+        for a, b in zip(got, want):
+            assert Hh.bits_equal(a, b)
+        del junk
