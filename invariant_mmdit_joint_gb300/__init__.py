@@ -1206,14 +1206,14 @@ class AdamW:
         self._index = self.device.index
         each = lambda x: list(x) if isinstance(x, (list, tuple)) else [x] * n  # noqa: E731
         decay, share, keys = each(weight_decay), each(lr_scale), list(range(n)) if keys is None else list(keys)
-        masters = [None] * n if masters is None else [None if t is None else t.detach() for t in masters]
+        masters = [None] * n if masters is None else list(masters)
         code = torch.float8_e4m3fn if state_bits == 8 else f32
         blocks = [-(-p.numel() // 32) for p in self.params]
 
         def states(given, dtype, sizes):
             if given is None:
                 return tuple(torch.zeros(k, dtype=dtype, device=self.device) for k in sizes)
-            return tuple(t.detach() for t in given)
+            return tuple(given)
         sizes = [p.numel() for p in self.params]
         m, v = states(m, code, sizes), states(v, code, sizes)
         m_scale = states(m_scale, torch.uint8, blocks) if state_bits == 8 else (None,) * n
@@ -1245,7 +1245,8 @@ class AdamW:
         # the tensors that someone else holds too are looked at for still being over them: parameters and gradients,
         # and a list of states once it was read (180 tensors with 8-bit states and masters are 1200 addresses, 70 us a
         # call; parameters and gradients are 21).
-        self._storages = list(map(torch.Tensor.untyped_storage, self._params))
+        self._storages = {name: [None if t is None else t.untyped_storage() for t in held]
+                          for name, held in [("params", self._params), *self._lists.items()]}
         self._data_ptr = torch.Tensor.data_ptr
         self._params_at = list(map(self._data_ptr, self._params))
         self._handed, self._others, self._others_at = set(), [], []
@@ -1257,15 +1258,25 @@ class AdamW:
         self.workspace, self._streams = None, set()  # of grad_norm, allocated at its first call; used by
 
     def _hand_out(self, name):
-        held = self._lists[name]
+        """One of the lists, for someone to read: tensors of the object's own, looked at from now on."""
         if name not in self._handed:
+            import torch
             self._handed.add(name)
-            for t in held:
+            held, field = [], "master" if name == "masters" else name
+            for t, storage, e in zip(self._lists[name], self._storages[name], self._list):
                 if t is not None:
+                    at = getattr(e, field) or 0
+                    if t.data_ptr() == at:
+                        t = t.detach()
+                    else:  # whoever gave it has replaced its data
+                        n = t.element_size()
+                        size = -(-e.n // 32) if field.endswith("scale") else e.n
+                        t = torch.empty(0, dtype=t.dtype, device=self.device).set_(storage, (at - storage.data_ptr()) // n, (size,))
                     self._others.append(t)
-                    self._others_at.append(t.data_ptr())
-                    self._storages.append(t.untyped_storage())
-        return held
+                    self._others_at.append(at)
+                held.append(t)
+            self._lists[name] = tuple(held)
+        return self._lists[name]
 
     params = property(lambda self: self._params)
     grads = property(lambda self: self._grads)
