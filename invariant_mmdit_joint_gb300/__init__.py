@@ -909,7 +909,7 @@ def _workspace(owner, size, stream, handle):
     import torch
     if owner.workspace is None:
         owner.workspace = _empty(size, torch.uint8, owner.device, stream)
-        owner._streams.add(handle)
+        owner._streams = {handle}
     elif handle not in owner._streams and owner.workspace.is_cuda:
         s = torch.cuda.current_stream(owner.device) if stream is None else stream
         if not isinstance(s, int):
@@ -1261,7 +1261,6 @@ class AdamW:
         """One of the lists, for someone to read: tensors of the object's own, looked at from now on."""
         if name not in self._handed:
             import torch
-            self._handed.add(name)
             held, field = [], "master" if name == "masters" else name
             for t, storage, e in zip(self._lists[name], self._storages[name], self._list):
                 if t is not None:
@@ -1276,6 +1275,7 @@ class AdamW:
                     self._others_at.append(at)
                 held.append(t)
             self._lists[name] = tuple(held)
+            self._handed.add(name)
         return self._lists[name]
 
     params = property(lambda self: self._params)

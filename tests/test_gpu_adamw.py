@@ -536,3 +536,24 @@ def test_long_chunks_step_like_short_ones(dev):
             for a, b in ((truth(one, 0), truth(opt, i)), (p, opt.params[i]), (one.m[0], opt.m[i]), (one.v[0], opt.v[i]),
                          (one.m_scale[0], opt.m_scale[i]), (one.v_scale[0], opt.v_scale[i])):
                 assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), (passes, i)
+
+
+def test_the_functions_give_the_bytes_of_the_class(dev):
+    """rlk_grad_norm and rlk_adamw_step on a list of the caller's own, tensors and sizes in hand."""
+    import torch
+    (a, _), (b, _) = (make(dev, SIZES, 8, seed=6) for _ in range(2))
+    n = len(SIZES)
+    ws = torch.empty(pkg.rlk_grad_norm_workspace_bytes(b._list, n), dtype=torch.uint8, device=dev)
+    out = torch.empty(2, device=dev)
+    args = pkg.AdamwArgs.from_buffer_copy(b._args)
+    args.step, args.grad_scale, args.lr = 4, out[1:].data_ptr(), HYPER["lr"]
+    pkg.rlk_grad_norm(b._list, n, 0.5, 3.0, out, ws)
+    pkg.rlk_adamw_step(b._list, n, args)
+    want = a.grad_norm(3.0, pre_scale=0.5)
+    a.step(4, grad_scale=want[1:])
+    assert Hh.bits_equal(out, want)
+    for name in ("params", "m", "v", "m_scale", "v_scale"):
+        for x, y in zip(getattr(a, name), getattr(b, name)):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), name
+    with pytest.raises(pkg.RlkError):
+        pkg.rlk_grad_norm(b._list, n, 0.5, 3.0, out, ws[:-1])
