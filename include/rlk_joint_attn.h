@@ -628,6 +628,137 @@ size_t rlk_grad_norm_workspace_bytes(const rlk_adamw_tensor* tensors, int32_t n_
 rlk_status rlk_grad_norm(const rlk_adamw_tensor* tensors, int32_t n_tensors, float pre_scale, float max_norm, float* out,
                          void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Projections in 8-bit floating point. A row of K values is held as K codes
+ * (e4m3, or e5m2 with the wider range) and one power-of-two scale for each
+ * block of 128 of them (the last block may be shorter):
+ *   scale = 2^e, e the smallest, at least -126, with max |x| <= 448 * 2^e
+ *           (e5m2: 57344 * 2^e); one byte, e + 127;
+ *   code  = x * 2^-e, rounded to nearest, ties to even.
+ * An infinity or NaN takes the code of NaN and no part in its block's scale.
+ * Layout: row r's codes start at r * rlk_fp8_row_bytes(K) (K rounded up to a
+ * multiple of 16), its scales at r * rlk_fp8_scale_row_bytes(K) (the number of
+ * blocks rounded up to a multiple of 4). What lies behind a row's last scale
+ * is neither read nor written; codes behind a row's end are not read, and in
+ * qt they may be written as zeros.
+ *
+ * The three products of a projection y = x W^T + b sum over different axes, so
+ * their operands take blocks along different axes:
+ *   y  = x  (blocks along its columns)  times W (blocks of 128 x 128)
+ *   dx = dy (along its columns)         times W^T (the same codes, turned)
+ *   dW = dy^T, x^T (both turned, blocks along the tokens)
+ * rlk_fp8_quantize reads a matrix once and writes it as it is (q), turned (qt),
+ * or both, and its column sums (a bias gradient).
+ *
+ * rlk_fp8_gemm: d[t, f] = sum_k a[t, k] b[f, k] + bias[f], rounded once. K runs
+ * in chunks of 512 in ascending order: the products of a chunk in an fp32
+ * accumulator, the chunks' sums added in fp32. No atomics, and a row's bytes
+ * depend on its own operands alone, not on the number of rows or their place.
+ * Several products share a launch (both streams; Q, K and V): the arrays are
+ * host memory, read before return. */
+#define RLK_E4M3 0
+#define RLK_E5M2 1
+#define RLK_FP8_MAX_ITEMS 8
+
+size_t rlk_fp8_row_bytes(int64_t k);        /* 0 for k < 1 */
+size_t rlk_fp8_scale_row_bytes(int64_t k);  /* 0 for k < 1 */
+
+/* Limits: 0 <= rows < 2^31 - 128, 1 <= cols <= 2^20 a multiple of 8, x_stride
+ * >= cols (elements) with every row 16-byte aligned (else RLK_ERR_ALIGNMENT).
+ * Written buffers must not overlap another of the call. rows 0 writes nothing
+ * (but zeros to col_sum). */
+typedef struct rlk_fp8_quant {
+    const void* x;      /* [rows, cols] */
+    void* q;            /* [rows, cols] codes, or NULL */
+    uint8_t* q_scale;   /* [rows, ceil(cols / 128)], NULL with q */
+    void* qt;           /* [cols, rows] codes, or NULL (one of q and qt is required) */
+    uint8_t* qt_scale;  /* [cols, ceil(rows / 128)], NULL with qt */
+    float* col_sum;     /* [cols] or NULL: sums over the rows, 128 rows' sums in ascending order */
+    void* workspace;    /* rlk_fp8_quant_workspace_bytes() bytes with col_sum, else NULL */
+    int64_t rows, cols, x_stride;
+    int32_t x_dtype;    /* RLK_BF16 or RLK_FP32 */
+    int32_t format;     /* RLK_E4M3 or RLK_E5M2 */
+    int32_t square;     /* 1: blocks of 128 x 128 (weights): q and qt hold the same codes */
+    int32_t reserved;   /* 0 */
+} rlk_fp8_quant;
+
+/* Limits: 0 <= m, n < 2^31 - 256, n a multiple of 8, 1 <= k < 2^31 - 128,
+ * d_stride >= n a multiple of 8 elements. m or n 0 computes nothing. d must
+ * not overlap another buffer of the call. */
+typedef struct rlk_fp8_product {
+    const void* a;          /* [m, k] codes */
+    const uint8_t* a_scale; /* [m, ceil(k / 128)] */
+    const void* b;          /* [n, k] codes */
+    const uint8_t* b_scale; /* [n, ceil(k / 128)] */
+    const void* bias;       /* bf16 [n] or NULL */
+    void* d;                /* [m, n], rows d_stride elements apart */
+    int64_t m, n, k, d_stride;
+    int32_t a_format, b_format; /* RLK_E4M3 or RLK_E5M2 */
+    int32_t d_dtype;        /* RLK_BF16 or RLK_FP32 */
+    int32_t accumulate;     /* 1: d += the product (fp32 d only) */
+} rlk_fp8_product;
+
+/* Bytes of the column sums' workspace (128 rows' sums); 0 for an invalid size.
+ * Calls that may overlap on the GPU need one each. */
+size_t rlk_fp8_quant_workspace_bytes(int64_t rows, int64_t cols);
+/* 1 .. RLK_FP8_MAX_ITEMS items. Device pointers need 16-byte alignment, the
+ * scales 4. */
+rlk_status rlk_fp8_quantize(const rlk_fp8_quant* items, int32_t n_items, void* stream);
+rlk_status rlk_fp8_gemm(const rlk_fp8_product* items, int32_t n_items, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Muon for the projections' matrices: momentum, an update made orthogonal by
+ * Newton-Schulz products, and the weights' step, over a list of matrices.
+ *   m = momentum * m + g',  g' = *grad_scale * g
+ *   u = g' + momentum * m (nesterov), or m
+ *   X = u / (||u||_F + eps), turned over if it has more rows than columns
+ *   iterations times:  A = X X^T;  B = b A + c A A;  X = a X + B X
+ *   p -= rate * weight_decay * p + rate * update_rms * sqrt(max(rows, cols)) * X,
+ *        rate = lr * lr_scale   (X's entries have the mean square 1 / max(rows, cols)
+ *        at full rank: update_rms is then the update's root mean square)
+ * rlk_orthogonalize stops at X: x in, its X out in bf16.
+ *
+ * X, A and B are held in fp16 (X is within 2^-9 of the formula's in the mean
+ * square) with fp32 accumulators; the norm's squares are fp32 (magnitudes
+ * below 2^-63 vanish, a norm above 2^63 is infinite and gives X = 0), its sum
+ * fp64; m and p are fp32. Sums have a fixed order without atomics: a matrix's
+ * result does not depend on the list or its place in it. Matrices with an
+ * infinity or NaN become NaN, as their formulas do. */
+typedef struct rlk_muon_matrix {
+    void* p;            /* [rows, cols] fp32, or bf16 when master is given; rlk_orthogonalize: bf16, written */
+    float* master;      /* [rows, cols] or NULL; rlk_orthogonalize: NULL */
+    const void* g;      /* [rows, cols], read only */
+    float* m;           /* [rows, cols]; rlk_orthogonalize: NULL */
+    int64_t rows, cols; /* 0 .. 65536 each, rows * cols < 2^31; an empty matrix is skipped */
+    double lr_scale;    /* >= 0 */
+    double weight_decay; /* >= 0 */
+    int32_t g_dtype;    /* RLK_BF16 or RLK_FP32 */
+    int32_t reserved;   /* 0 */
+} rlk_muon_matrix;
+
+typedef struct rlk_muon_args {
+    double lr, momentum, update_rms; /* >= 0, momentum < 1; the rates' products in fp32's range */
+    double a, b, c;          /* the polynomial: finite */
+    double eps;              /* 2^-126 .. 1 */
+    const float* lr_dev;     /* device, or NULL: read instead of lr */
+    const float* grad_scale; /* device, or NULL (1). Not finite: every tensor is left as it was */
+    int32_t iterations;      /* 1 .. 32 */
+    int32_t nesterov;
+} rlk_muon_args;
+
+/* workspace: rlk_muon_workspace_bytes() bytes (about 4 bytes an element and 4
+ * for each pair of its shorter side; 0 for an invalid list), one for each of
+ * the calls that may overlap on the GPU. rlk_orthogonalize reads iterations,
+ * a, b, c and eps of args. The tensors' buffers must not overlap (a written
+ * range that overlaps another buffer of the list: RLK_ERR_INVALID_ARG). The
+ * list is host memory, read before return; 0 matrices launch nothing. lr_dev
+ * and grad_scale need 4-byte alignment, everything else 16. */
+size_t rlk_muon_workspace_bytes(const rlk_muon_matrix* matrices, int32_t n_matrices);
+rlk_status rlk_muon_step(const rlk_muon_matrix* matrices, int32_t n_matrices, const rlk_muon_args* args, void* workspace,
+                         size_t workspace_bytes, void* stream);
+rlk_status rlk_orthogonalize(const rlk_muon_matrix* matrices, int32_t n_matrices, const rlk_muon_args* args,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, then reads and clears the device-side error word
  * that bounded waits in the kernels set when they give up. Returns RLK_OK,
  * RLK_ERR_DEVICE_TIMEOUT, or RLK_ERR_CUDA if the stream reported an error. */
@@ -733,7 +864,7 @@ rlk_status rlk_joint_attn_fwd_shard(const rlk_ja_shape* shape, const void* ctx, 
  * forward and backward with concatenated or separate streams, the
  * allocation-free forward, the key-shard and from-context forwards, the
  * QKV and output projections, the standalone operators, the adaln operators,
- * the gradient norm and the optimiser step) appends one
+ * the 8-bit projections, the gradient norm and the optimiser steps) appends one
  * record when it returns, including calls refused
  * during validation (status != RLK_OK, no kernel listed, actual backend
  * "none"). The kernels listed are the ones the call enqueued, in launch
@@ -761,7 +892,8 @@ typedef struct rlk_op_record {
     char arithmetic_policy[192];   /* operand/accumulate/cast/transcendental policy */
     char reduction_order[160];
     int32_t B, H, T_txt, grid_h, grid_w;  /* the call's geometry (0 if the shape was null; the adaln
-                                             operators: H 0, grid 1 x T_img; the optimiser: all 0) */
+                                             operators: H 0, grid 1 x T_img; the 8-bit projections and
+                                             the optimisers: all 0) */
 } rlk_op_record;
 
 /* Turns the operator trace on (1) or off (0); either way clears the log. */
@@ -781,8 +913,10 @@ const char* rlk_strerror(int status);
  * 7 gain-gradient fold, 8 qk_gemm, 9 softmax,
  * 10 av_gemm, 11 forward key shard, 12 qkv_bias_gemm, 13 attn_out_bias_gemm,
  * 19 adaln forward, 20 adaln backward, 21 its fold, 22 gradient norm, 23 its
- * fold, 24 AdamW, 25 adaln's weight gradients (14 .. 18: the standalone
- * backward operators).
+ * fold, 24 AdamW, 25 adaln's weight gradients, 26 fp8 quantise, 27 its column
+ * sums' fold, 28 fp8 product, 29 Muon momentum, 30 its start, 31 .. 33 its products
+ * (X X^T, the polynomial, B X), 34 its update (14 .. 18: the standalone backward
+ * operators).
  * rlk_kernel_timing(1) makes later calls record a CUDA event pair around
  * every launch (up to 4096 launches per kernel id); rlk_kernel_timing(0)
  * stops and clears. rlk_kernel_timing_read() waits for the recorded events

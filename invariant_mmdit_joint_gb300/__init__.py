@@ -35,6 +35,9 @@ __all__ = [
     "AdalnShape", "AdalnIo", "AdalnGrad", "rlk_adaln_workspace_bytes", "rlk_adaln_modulation_fwd",
     "rlk_adaln_modulation_bwd", "rlk_adaln_gate_residual_fwd", "rlk_adaln_gate_residual_bwd", "AdaLN", "NORMS",
     "AdamwTensor", "AdamwArgs", "rlk_adamw_step", "rlk_grad_norm", "rlk_grad_norm_workspace_bytes", "AdamW",
+    "Fp8Quant", "Fp8Product", "rlk_fp8_row_bytes", "rlk_fp8_scale_row_bytes", "rlk_fp8_quant_workspace_bytes",
+    "rlk_fp8_quantize", "rlk_fp8_gemm", "FP8_FORMATS", "FP8_MAX_ITEMS", "Fp8Projection",
+    "MuonMatrix", "MuonArgs", "rlk_muon_workspace_bytes", "rlk_muon_step", "rlk_orthogonalize", "Muon", "orthogonalize",
     "EXPORTED_SYMBOLS", "KERNEL_IDS",
 ]
 
@@ -55,7 +58,8 @@ KERNEL_IDS = {
     "qk_gemm": 8, "softmax": 9, "av_gemm": 10, "attn_fwd_shard": 11, "qkv_gemm": 12, "out_gemm": 13,
     "dp_gemm": 14, "softmax_bwd": 15, "key_gemm": 16, "query_gemm": 17, "norm_rope_bwd_q": 18,
     "adaln_fwd": 19, "adaln_bwd": 20, "adaln_fold": 21, "grad_norm": 22, "grad_norm_fold": 23, "adamw": 24,
-    "adaln_weight": 25,
+    "adaln_weight": 25, "fp8_quant": 26, "fp8_fold": 27, "fp8_gemm": 28, "muon_momentum": 29, "muon_start": 30,
+    "muon_gram": 31, "muon_poly": 32, "muon_apply": 33, "muon_update": 34,
 }
 # which intermediate rlk_joint_attn_unfused_bytes() sizes
 UNFUSED = {"scores": 0, "p": 1, "alpha": 2, "rows": 3, "dp": 4, "ds": 5, "stats": 6, "dhat": 7, "gain_tiles": 8}
@@ -77,6 +81,8 @@ EXPORTED_SYMBOLS = (
     "rlk_adaln_workspace_bytes", "rlk_adaln_modulation_fwd", "rlk_adaln_modulation_bwd",
     "rlk_adaln_gate_residual_fwd", "rlk_adaln_gate_residual_bwd",
     "rlk_adamw_step", "rlk_grad_norm", "rlk_grad_norm_workspace_bytes",
+    "rlk_fp8_row_bytes", "rlk_fp8_scale_row_bytes", "rlk_fp8_quant_workspace_bytes", "rlk_fp8_quantize", "rlk_fp8_gemm",
+    "rlk_muon_workspace_bytes", "rlk_muon_step", "rlk_orthogonalize",
 )
 OP_TRACE_CAP = 256
 OP_TRACE_MAX_KERNELS = 8
@@ -144,6 +150,38 @@ class AdamwArgs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps")] + \
                [("step", ctypes.c_int64), ("lr_dev", ctypes.c_void_p), ("step_dev", ctypes.c_void_p),
                 ("grad_scale", ctypes.c_void_p), ("seed", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+FP8_FORMATS = {"e4m3": 0, "e5m2": 1}
+FP8_MAX_ITEMS = 8
+
+
+class Fp8Quant(ctypes.Structure):
+    """rlk_fp8_quant: one matrix to be rounded to codes."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "q", "q_scale", "qt", "qt_scale", "col_sum", "workspace")] + \
+               [(n, ctypes.c_int64) for n in ("rows", "cols", "x_stride")] + \
+               [(n, ctypes.c_int32) for n in ("x_dtype", "format", "square", "reserved")]
+
+
+class Fp8Product(ctypes.Structure):
+    """rlk_fp8_product: one product of two operands in codes."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("a", "a_scale", "b", "b_scale", "bias", "d")] + \
+               [(n, ctypes.c_int64) for n in ("m", "n", "k", "d_stride")] + \
+               [(n, ctypes.c_int32) for n in ("a_format", "b_format", "d_dtype", "accumulate")]
+
+
+class MuonMatrix(ctypes.Structure):
+    """rlk_muon_matrix."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("p", "master", "g", "m")] + \
+               [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("lr_scale", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("g_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class MuonArgs(ctypes.Structure):
+    """rlk_muon_args."""
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "momentum", "update_rms", "a", "b", "c", "eps")] + \
+               [("lr_dev", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p), ("iterations", ctypes.c_int32),
+                ("nesterov", ctypes.c_int32)]
 
 
 class Trace(ctypes.Structure):
@@ -286,6 +324,17 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     L.rlk_grad_norm_workspace_bytes.restype = sz
     L.rlk_grad_norm.argtypes = [adt, ctypes.c_int32, ctypes.c_float, ctypes.c_float, vp, vp, sz, vp]
     L.rlk_grad_norm.restype = i32
+    i64 = ctypes.c_int64
+    for name, args in (("row_bytes", [i64]), ("scale_row_bytes", [i64]), ("quant_workspace_bytes", [i64, i64])):
+        f = getattr(L, "rlk_fp8_" + name)
+        f.argtypes, f.restype = args, sz
+    L.rlk_fp8_quantize.argtypes, L.rlk_fp8_quantize.restype = [ctypes.POINTER(Fp8Quant), ctypes.c_int32, vp], i32
+    L.rlk_fp8_gemm.argtypes, L.rlk_fp8_gemm.restype = [ctypes.POINTER(Fp8Product), ctypes.c_int32, vp], i32
+    mat = ctypes.POINTER(MuonMatrix)
+    L.rlk_muon_workspace_bytes.argtypes, L.rlk_muon_workspace_bytes.restype = [mat, ctypes.c_int32], sz
+    for name in ("rlk_muon_step", "rlk_orthogonalize"):
+        f = getattr(L, name)
+        f.argtypes, f.restype = [mat, ctypes.c_int32, ctypes.POINTER(MuonArgs), vp, sz, vp], i32
     L.rlk_op_trace_enable.argtypes = [i32]
     L.rlk_op_trace_enable.restype = i32
     L.rlk_op_trace_count.argtypes = []
@@ -639,6 +688,43 @@ def rlk_fwd_tile_schedule(policy: str) -> str:
     return {v: k for k, v in FWD_TILES.items()}[prev]
 
 
+def rlk_fp8_row_bytes(k: int) -> int:
+    return lib().rlk_fp8_row_bytes(k)
+
+
+def rlk_fp8_scale_row_bytes(k: int) -> int:
+    return lib().rlk_fp8_scale_row_bytes(k)
+
+
+def rlk_fp8_quant_workspace_bytes(rows: int, cols: int) -> int:
+    return lib().rlk_fp8_quant_workspace_bytes(rows, cols)
+
+
+def rlk_fp8_quantize(items, stream=None) -> None:
+    """items: a ctypes array of Fp8Quant."""
+    _check(lib().rlk_fp8_quantize(items, len(items), _stream_handle(stream)), "rlk_fp8_quantize")
+
+
+def rlk_fp8_gemm(items, stream=None) -> None:
+    """items: a ctypes array of Fp8Product."""
+    _check(lib().rlk_fp8_gemm(items, len(items), _stream_handle(stream)), "rlk_fp8_gemm")
+
+
+def rlk_muon_workspace_bytes(matrices) -> int:
+    """matrices: a ctypes array of MuonMatrix."""
+    return lib().rlk_muon_workspace_bytes(matrices, len(matrices))
+
+
+def rlk_muon_step(matrices, args: MuonArgs, workspace, stream=None) -> None:
+    _check(lib().rlk_muon_step(matrices, len(matrices), ctypes.byref(args), _ptr(workspace), workspace.numel(),
+                               _stream_handle(stream)), "rlk_muon_step")
+
+
+def rlk_orthogonalize(matrices, args: MuonArgs, workspace, stream=None) -> None:
+    _check(lib().rlk_orthogonalize(matrices, len(matrices), ctypes.byref(args), _ptr(workspace), workspace.numel(),
+                                   _stream_handle(stream)), "rlk_orthogonalize")
+
+
 def rlk_strerror(code: int) -> str:
     return _strerror(code)
 
@@ -939,7 +1025,56 @@ class _Results(dict):
             all(map(operator.is_, self.values(), self.pairs)) and [t.data_ptr() for t in self.tensors] == self.addresses
 
 
-class AdaLN:
+class _Pairs:
+    """Checks and outputs of calls on (text, image) pairs of tensors: a subclass has ``device``, ``_index`` and, for
+    each output, ``_kinds``: its sizes (None where a stream has no tokens) and type."""
+
+    def _bad(self, name, i, t, want, dtype):
+        if want is None:
+            raise ValueError(f"{name}[{i}] must be None: the stream has no tokens")
+        if t is None:
+            raise ValueError(f"{name}[{i}] is missing")
+        raise ValueError(f"{name}[{i}] must be a contiguous {dtype} {tuple(want)} tensor on {self.device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+
+    def _need(self, name, pair, dtype, sizes):
+        """Pointers of a pair of required dense tensors (None without tokens)."""
+        if len(pair) != 2:
+            raise ValueError(f"{name} must be a (text, image) pair")
+        index = self._index
+        t, want = pair[0], sizes[0]
+        p = q = None
+        if t is not None:
+            if want is None or t.dtype is not dtype or t.shape != want or not t.is_contiguous() or t.get_device() != index:
+                self._bad(name, 0, t, want, dtype)
+            p = t.data_ptr()
+        elif want is not None:
+            self._bad(name, 0, t, want, dtype)
+        t, want = pair[1], sizes[1]
+        if t is not None:
+            if want is None or t.dtype is not dtype or t.shape != want or not t.is_contiguous() or t.get_device() != index:
+                self._bad(name, 1, t, want, dtype)
+            q = t.data_ptr()
+        elif want is not None:
+            self._bad(name, 1, t, want, dtype)
+        return p, q
+
+    def _outputs(self, out, names, stream):
+        """The outputs of these names, new or taken from `out`, and their pointers."""
+        of = self._kinds
+        if type(out) is _Results and out.fits(of, names):
+            return out, out.pointers
+        if out is None:
+            pairs = {k: tuple(None if s is None else _empty(s, of[k][1], self.device, stream) for s in of[k][0])
+                     for k in names}
+            out = _Results(of, names, pairs, {k: self._need(k, pairs[k], of[k][1], of[k][0]) for k in names})
+            return out, out.pointers
+        if len(out) != len(names) or any(k not in out for k in names):
+            raise ValueError(f"out must hold {sorted(names)}, got {sorted(out)}")
+        return out, {k: self._need(k, out[k], of[k][1], of[k][0]) for k in names}
+
+
+class AdaLN(_Pairs):
     """Buffers + calls of the block's norms, modulation, gate and residual for
     one geometry: adaln_modulation before a sublayer's projections,
     adaln_gate_residual (with the next modulation) after them.
@@ -989,36 +1124,6 @@ class AdaLN:
         self.workspace, self._streams = None, set()  # of the backward, allocated at its first call; used by
 
     # ---- checks
-    def _bad(self, name, i, t, want, dtype):
-        if want is None:
-            raise ValueError(f"{name}[{i}] must be None: the stream has no tokens")
-        if t is None:
-            raise ValueError(f"{name}[{i}] is missing")
-        raise ValueError(f"{name}[{i}] must be a contiguous {dtype} {tuple(want)} tensor on {self.device}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
-
-    def _need(self, name, pair, dtype, sizes):
-        """Pointers of a pair of required dense tensors (None without tokens)."""
-        if len(pair) != 2:
-            raise ValueError(f"{name} must be a (text, image) pair")
-        index = self._index
-        t, want = pair[0], sizes[0]
-        p = q = None
-        if t is not None:
-            if want is None or t.dtype is not dtype or t.shape != want or not t.is_contiguous() or t.get_device() != index:
-                self._bad(name, 0, t, want, dtype)
-            p = t.data_ptr()
-        elif want is not None:
-            self._bad(name, 0, t, want, dtype)
-        t, want = pair[1], sizes[1]
-        if t is not None:
-            if want is None or t.dtype is not dtype or t.shape != want or not t.is_contiguous() or t.get_device() != index:
-                self._bad(name, 1, t, want, dtype)
-            q = t.data_ptr()
-        elif want is not None:
-            self._bad(name, 1, t, want, dtype)
-        return p, q
-
     def _weights(self, name, pair):
         """Pointers of a pair of optional [C] weights."""
         if pair is None or (pair[0] is None and pair[1] is None):
@@ -1064,20 +1169,6 @@ class AdaLN:
             call.mod_stride = stride
             self._shapes[stride] = call
         return call, res
-
-    def _outputs(self, out, names, stream):
-        """The outputs of these names, new or taken from `out`, and their pointers."""
-        of = self._kinds
-        if type(out) is _Results and out.fits(of, names):
-            return out, out.pointers
-        if out is None:
-            pairs = {k: tuple(None if s is None else _empty(s, of[k][1], self.device, stream) for s in of[k][0])
-                     for k in names}
-            out = _Results(of, names, pairs, {k: self._need(k, pairs[k], of[k][1], of[k][0]) for k in names})
-            return out, out.pointers
-        if len(out) != len(names) or any(k not in out for k in names):
-            raise ValueError(f"out must hold {sorted(names)}, got {sorted(out)}")
-        return out, {k: self._need(k, out[k], of[k][1], of[k][0]) for k in names}
 
     def _structs(self, cls, *pairs):
         """One struct of pointers per stream, its fields in order (None for a stream without tokens)."""
@@ -1374,3 +1465,323 @@ class AdamW:
         rc = lib().rlk_adamw_step(self._list, len(self._params), self._args_ref, _raw_stream(stream, self._index))
         if rc:
             _check(rc, "rlk_adamw_step")
+
+
+def _cuda_device(device):
+    import torch
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
+
+
+class Fp8Projection(_Pairs):
+    """Buffers + calls of one projection y = x W^T + b of both streams in 8-bit floating point (rlk_fp8_quantize,
+    rlk_fp8_gemm), each stream with weights of its own.
+
+    x and dx are (text, image) pairs, bf16 [B, T_txt, n_in] and [B, T_img, n_in], y and dy likewise with n_out; a pair's
+    text is None if T_txt is 0 and its image None if T_img is 0. ``set_weights`` rounds the weights to codes that the
+    object holds until the next call of it. Values are rounded to e4m3 with a power-of-two scale for each 128 of them,
+    gradients to ``grad_format`` (e4m3 or e5m2). n_in and n_out are multiples of 8.
+
+    Every call returns its outputs as a dict of pairs; passing that dict back as ``out`` reuses its buffers. The calls
+    share one workspace and the weights' codes: calls that may overlap on the GPU (other streams, graphs replayed at
+    the same time) need an object each. An object outlives the graphs that captured its calls, and its calls on a stream
+    that is given as an address."""
+
+    def __init__(self, B: int, T_txt: int, T_img: int, n_in: int, n_out: int, out_dtype=None, dw_dtype=None,
+                 grad_format: str = "e4m3", device="cuda"):
+        import torch
+        bf16, f32 = torch.bfloat16, torch.float32
+        self.out_dtype, self.dw_dtype = out_dtype or bf16, dw_dtype or f32
+        if not {self.out_dtype, self.dw_dtype} <= {bf16, f32}:
+            raise ValueError("types are bfloat16 or float32")
+        if grad_format not in FP8_FORMATS:
+            raise ValueError(f"grad_format must be one of {sorted(FP8_FORMATS)}")
+        if B < 1 or T_txt < 0 or T_img < 0 or T_txt + T_img == 0 or not all(
+                8 <= k <= 1 << 20 and k % 8 == 0 for k in (n_in, n_out)) or B * max(T_txt, T_img) >= 1 << 31:
+            raise RlkError(1, "Fp8Projection: invalid shape")
+        self.device = _cuda_device(device)
+        self._index = -1 if self.device.index is None else self.device.index
+        self.B, self.T, self.n_in, self.n_out = B, (T_txt, T_img), n_in, n_out
+        self._grad = FP8_FORMATS[grad_format]
+        self._live = [i for i in (0, 1) if self.T[i] > 0]
+        self._tokens = tuple(B * t for t in self.T)
+        on = lambda make: tuple(torch.Size(make(t)) if t else None for t in self.T)  # noqa: E731
+        rows, srows = rlk_fp8_row_bytes, rlk_fp8_scale_row_bytes
+        code, byte = torch.float8_e4m3fn, torch.uint8
+        self._x = on(lambda t: (B, t, n_in))
+        self._y = on(lambda t: (B, t, n_out))
+        self._w = on(lambda t: (n_out, n_in))
+        self._b = on(lambda t: (n_out,))
+        self._kinds = {"y": (self._y, self.out_dtype), "dx": (self._x, bf16), "dw": (self._w, self.dw_dtype),
+                       "db": (self._b, f32), "xt": (on(lambda t: (n_in, rows(B * t))), code),
+                       "xt_scale": (on(lambda t: (n_in, srows(B * t))), byte)}
+        # weights as they are and turned, their scales
+        sizes = ((n_out, rows(n_in)), (n_out, srows(n_in)), (n_in, rows(n_out)), (n_in, srows(n_out)))
+        self._codes = [None if not t else tuple(torch.empty(k, dtype=byte, device=self.device) for k in sizes) for t in self.T]
+        self._at = [None if c is None else tuple(k.data_ptr() for k in c) for c in self._codes]
+        self._set = False
+        # the workspace: codes and scales of x, or of dy as it is and turned and the sums of its columns
+        self._fwd, self._bwd, fwd, bwd = {}, {}, 0, 0
+
+        def place(at, sizes):
+            starts = []
+            for k in sizes:
+                starts.append(at)
+                at += -(-k // 256) * 256
+            return at, starts
+        for i in self._live:
+            t = self._tokens[i]
+            fwd, self._fwd[i] = place(fwd, (t * rows(n_in), t * srows(n_in)))
+            bwd, self._bwd[i] = place(bwd, (t * rows(n_out), t * srows(n_out), n_out * rows(t), n_out * srows(t),
+                                            rlk_fp8_quant_workspace_bytes(t, n_out)))
+        self._ws_bytes = max(fwd, bwd)
+        self.workspace, self._streams = None, set()
+
+    def set_weights(self, w, stream=None) -> None:
+        """Rounds a pair of weights, float32 or bfloat16 [n_out, n_in], to codes in blocks of 128 x 128."""
+        import torch
+        dtype = next((t.dtype for t in w if t is not None), None)
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("weights are bfloat16 or float32")
+        pw = self._need("w", w, dtype, self._w)
+        _require_current(self.device)
+        items = (Fp8Quant * len(self._live))(*[
+            Fp8Quant(pw[i], *self._at[i], None, None, self.n_out, self.n_in, self.n_in, int(dtype is torch.float32), 0, 1, 0)
+            for i in self._live])
+        handle = _raw_stream(stream, self._index)
+        if handle not in self._streams and self.device.type == "cuda":
+            self._record(stream, handle)
+        rlk_fp8_quantize(items, handle)
+        self._set = True
+
+    def _record(self, stream, handle):
+        """The weights' codes wait for every torch stream that uses them when the object goes."""
+        import torch
+        s = torch.cuda.current_stream(self.device) if stream is None else stream
+        if not isinstance(s, int):
+            for c in self._codes:
+                for t in c or ():
+                    t.record_stream(s)
+
+    def _ready(self, stream):
+        if not self._set:
+            raise ValueError("no weights given: set_weights comes first")
+        _require_current(self.device)
+        handle = _raw_stream(stream, self._index)
+        if handle not in self._streams:
+            self._record(stream, handle)
+        return handle, _workspace(self, self._ws_bytes, stream, handle).data_ptr()
+
+    def _vectors(self, name, pair, dtype, sizes):
+        if pair is None or all(t is None for t in pair):
+            return _NONE
+        return self._need(name, pair, dtype, tuple(None if t is None else k for t, k in zip(pair, sizes)))
+
+    def forward(self, x, bias=None, train: bool = False, out=None, stream=None):
+        """y, and with train what the backward needs of x: xt and xt_scale, its codes turned. bias is a pair of bf16
+        [n_out], either of them or both None (0)."""
+        import torch
+        bf16 = torch.bfloat16
+        px = self._need("x", x, bf16, self._x)
+        pb = self._vectors("bias", bias, bf16, self._b)
+        out, p = self._outputs(out, ("y", "xt", "xt_scale") if train else ("y",), stream)
+        handle, ws = self._ready(stream)
+        n_in, n_out = self.n_in, self.n_out
+        quant, product = [], []
+        for i in self._live:
+            q, s = ws + self._fwd[i][0], ws + self._fwd[i][1]
+            t = self._tokens[i]
+            w = self._at[i]
+            quant.append(Fp8Quant(px[i], q, s, p["xt"][i] if train else None, p["xt_scale"][i] if train else None, None, None,
+                                  t, n_in, n_in, 0, 0, 0, 0))
+            product.append(Fp8Product(q, s, w[0], w[1], pb[i], p["y"][i], t, n_out, n_in, n_out, 0, 0,
+                                      int(self.out_dtype is not bf16), 0))
+        rlk_fp8_quantize((Fp8Quant * len(quant))(*quant), handle)
+        rlk_fp8_gemm((Fp8Product * len(product))(*product), handle)
+        return out
+
+    def backward(self, dy, saved, want=("dx", "dw", "db"), accumulate: bool = False, out=None, stream=None):
+        """Gradients named in ``want``: dx (bf16), dw (float32 or the constructor's dw_dtype), db (float32). ``saved`` is
+        what forward(train=True) returned (dw only; else None may be given). With accumulate, dw is added to the one in
+        ``out`` (float32)."""
+        import torch
+        bf16, f32 = torch.bfloat16, torch.float32
+        want = tuple(k for k in ("dx", "dw", "db") if k in want)
+        if not want:
+            raise ValueError("want must name dx, dw or db")
+        pdy = self._need("dy", dy, bf16, self._y)
+        pxt = pxs = _NONE
+        if "dw" in want:
+            if saved is None or "xt" not in saved:
+                raise ValueError("dw needs what forward(train=True) returned")
+            pxt = self._need("xt", saved["xt"], *self._kinds["xt"][::-1])
+            pxs = self._need("xt_scale", saved["xt_scale"], *self._kinds["xt_scale"][::-1])
+        if accumulate and ("dw" not in want or out is None or self.dw_dtype is not f32):
+            raise ValueError("accumulate needs out with a float32 dw")
+        out, p = self._outputs(out, want, stream)
+        handle, ws = self._ready(stream)
+        n_in, n_out = self.n_in, self.n_out
+        quant, product, f = [], [], self._grad
+        dx, dw, db = ("dx" in want), ("dw" in want), ("db" in want)
+        for i in self._live:
+            q, s, qt, st, part = [ws + k for k in self._bwd[i]]
+            t, w = self._tokens[i], self._at[i]
+            turned = dw or not dx  # (db alone: the sums come with one of the two)
+            quant.append(Fp8Quant(pdy[i], q if dx else None, s if dx else None, qt if turned else None, st if turned else None,
+                                  p["db"][i] if db else None, part if db else None, t, n_out, n_out, 0, f, 0, 0))
+            if dx:
+                product.append(Fp8Product(q, s, w[2], w[3], None, p["dx"][i], t, n_in, n_out, n_in, f, 0, 0, 0))
+            if dw:
+                product.append(Fp8Product(qt, st, pxt[i], pxs[i], None, p["dw"][i], n_out, n_in, t, n_in, f, 0,
+                                          int(self.dw_dtype is f32), int(accumulate)))
+        rlk_fp8_quantize((Fp8Quant * len(quant))(*quant), handle)
+        if product:
+            rlk_fp8_gemm((Fp8Product * len(product))(*product), handle)
+        return out
+
+
+POLYNOMIAL = (3.4445, -4.7750, 2.0315)
+
+
+def _matrix(name, t, dtypes, device, shape=None):
+    if t.dim() != 2 or t.dtype not in dtypes or (shape is not None and t.shape != shape) or not t.is_contiguous() or \
+            t.device != device:
+        want = "2-D" if shape is None else tuple(shape)
+        raise ValueError(f"{name} must be a contiguous {want} tensor ({dtypes}) on {device}, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
+
+
+def orthogonalize(matrices, out=None, iterations: int = 5, coefficients=POLYNOMIAL, eps: float = 1e-7, stream=None):
+    """Newton-Schulz products X = a X + (b A + c A A) X, A = X X^T, on each of a list of matrices (bf16 or float32 on one
+    device, of any sizes), from X = x / (||x||_F + eps) on: singular values go towards 1. Returns bf16 matrices, those of
+    ``out`` if it is given. See rlk_orthogonalize in the header."""
+    import torch
+    bf16, f32 = torch.bfloat16, torch.float32
+    matrices = list(matrices)
+    if not matrices:
+        return []
+    device = matrices[0].device
+    for i, x in enumerate(matrices):
+        _matrix(f"matrix {i}", x, (bf16, f32), device)
+    _require_current(device)
+    if out is None:
+        out = [_empty(x.shape, bf16, device, stream) for x in matrices]
+    if len(out) != len(matrices):
+        raise ValueError(f"expected {len(matrices)} outputs, got {len(out)}")
+    for i, (x, o) in enumerate(zip(matrices, out)):
+        _matrix(f"output {i}", o, (bf16,), device, x.shape)
+    n = len(matrices)
+    a, b, c = (float(k) for k in coefficients)
+    items = (MuonMatrix * n)(*[MuonMatrix(o.data_ptr() or None, None, x.data_ptr() or None, None, x.shape[0], x.shape[1], 0.0, 0.0,
+                                          int(x.dtype is f32), 0) for x, o in zip(matrices, out)])
+    args = MuonArgs(a=a, b=b, c=c, eps=float(eps), iterations=int(iterations))
+    size = rlk_muon_workspace_bytes(items)
+    if size == 0:
+        raise RlkError(1, "orthogonalize: invalid sizes")
+    rlk_orthogonalize(items, args, _empty(size, torch.uint8, device, stream), _raw_stream(stream, device.index))
+    return out
+
+
+class Muon:
+    """Muon over a list of matrices (see rlk_muon_step in the header), for the projections' weights; vectors and gains go
+    to AdamW.
+
+    ``params`` are contiguous 2-D CUDA tensors, float32, or bfloat16 with a float32 master copy (taken from ``masters``,
+    or made from the parameter). The momentum ``m`` is float32 of the parameter's shape, zero unless given.
+    ``weight_decay`` and ``lr_scale`` are one number or one per parameter. An update has the root mean square lr *
+    update_rms (at full rank), so that AdamW's rates serve here too. ``grads``, bfloat16 or float32, may be held here or
+    given to each call. ``params``, ``masters`` and ``m`` hold the tensors in use: load values into them with ``copy_``. A
+    call refuses a list with a tensor whose ``data`` was replaced. ``lr`` may be set at any time. The calls share one
+    workspace: calls that may overlap on the GPU need an object each. An object outlives the graphs that captured its
+    calls, and its calls on a stream that is given as an address. What is made here is written on the current stream."""
+
+    def __init__(self, params, masters=None, lr: float = 1e-3, momentum: float = 0.95, nesterov: bool = True, weight_decay=0.01,
+                 lr_scale=1.0, update_rms: float = 0.2, iterations: int = 5, coefficients=POLYNOMIAL, eps: float = 1e-7,
+                 grads=None, m=None):
+        import torch
+        f32, bf16 = torch.float32, torch.bfloat16
+        n = len(params)
+        if n == 0:
+            raise ValueError("no parameters given")
+        self.params, self.lr = tuple(params), float(lr)
+        self.device = self.params[0].device
+        self._index = self.device.index
+        each = lambda x: list(x) if isinstance(x, (list, tuple)) else [x] * n  # noqa: E731
+        decay, share = each(weight_decay), each(lr_scale)
+        masters = [None] * n if masters is None else list(masters)
+        m = [None] * n if m is None else list(m)
+        if not len(decay) == len(share) == len(masters) == len(m) == n:
+            raise ValueError(f"expected one entry for each of the {n} parameters")
+        self._list = (MuonMatrix * n)()
+        for i, p in enumerate(self.params):
+            _matrix(f"parameter {i}", p, (f32, bf16), self.device)
+            if p.dtype == f32 and masters[i] is not None:
+                raise ValueError(f"parameter {i} is float32 and takes no master")
+            if p.dtype == bf16 and masters[i] is None:
+                masters[i] = p.detach().float()
+            if m[i] is None:
+                m[i] = torch.zeros(p.shape, dtype=f32, device=self.device)
+            if masters[i] is not None:
+                _matrix(f"master {i}", masters[i], (f32,), self.device, p.shape)
+            _matrix(f"m {i}", m[i], (f32,), self.device, p.shape)
+            e = self._list[i]
+            e.p, e.master, e.m = (None if t is None else t.data_ptr() or None for t in (p, masters[i], m[i]))
+            e.rows, e.cols, e.lr_scale, e.weight_decay = p.shape[0], p.shape[1], float(share[i]), float(decay[i])
+        self.masters, self.m = tuple(masters), tuple(m)
+        self._held = [t for t in (*self.params, *self.masters, *self.m) if t is not None]
+        self._held_at = [t.data_ptr() for t in self._held]
+        # (the list holds addresses: the storages behind them stay allocated)
+        self._storages = [t.untyped_storage() for t in self._held]
+        a, b, c = (float(k) for k in coefficients)
+        self._args = MuonArgs(lr=self.lr, momentum=float(momentum), update_rms=float(update_rms), a=a, b=b, c=c, eps=float(eps),
+                              iterations=int(iterations), nesterov=int(bool(nesterov)))
+        self.grads = None
+        if grads is not None:
+            self._take(grads)
+        self._ws_bytes = rlk_muon_workspace_bytes(self._list)
+        if self._ws_bytes == 0:
+            raise RlkError(1, "Muon: invalid sizes")
+        self.workspace, self._streams = None, set()
+
+    def _take(self, grads):
+        import torch
+        grads = tuple(grads)
+        if len(grads) != len(self.params):
+            raise ValueError(f"expected {len(self.params)} gradients, got {len(grads)}")
+        for i, (g, p) in enumerate(zip(grads, self.params)):
+            _matrix(f"gradient {i}", g, (torch.float32, torch.bfloat16), self.device, p.shape)
+        self._grads_at = [g.data_ptr() for g in grads]
+        for e, g, at in zip(self._list, grads, self._grads_at):
+            e.g, e.g_dtype = at or None, int(g.dtype is torch.float32)
+        self.grads, self._grad_storages = grads, [g.untyped_storage() for g in grads]
+
+    def step(self, lr=None, grad_scale=None, grads=None, stream=None):
+        """One update, in place. ``lr`` is the rate if not the constructor's, a number, or a float32 device tensor of one
+        value that is read when the kernels run, as a captured step needs. ``grad_scale`` is one float32 value on the
+        device, such as AdamW.grad_norm(...)[1:]; if it is not finite, nothing is changed."""
+        import torch
+        if grads is not None:
+            self._take(grads)
+        if self.grads is None:
+            raise ValueError("no gradients given")
+        if [t.data_ptr() for t in self._held] != self._held_at or [t.data_ptr() for t in self.grads] != self._grads_at:
+            raise ValueError("a tensor's data was replaced: copy_ into it, or make a new object (gradients: give them anew)")
+        _require_current(self.device)
+        a = self._args
+        a.lr_dev, a.grad_scale = None, None
+        if isinstance(lr, torch.Tensor):
+            a.lr_dev, a.lr = self._scalar("lr", lr), 0.0
+        else:
+            a.lr = self.lr if lr is None else float(lr)
+        if grad_scale is not None:
+            a.grad_scale = self._scalar("grad_scale", grad_scale)
+        handle = _raw_stream(stream, self._index)
+        rlk_muon_step(self._list, a, _workspace(self, self._ws_bytes, stream, handle), handle)
+
+    def _scalar(self, name, t):
+        import torch
+        if t.dtype != torch.float32 or t.numel() != 1 or t.device != self.device:
+            raise ValueError(f"{name} must be one float32 value on {self.device}")
+        return t.data_ptr()

@@ -1,0 +1,697 @@
+// Projections in 8-bit floating point: rows rounded to codes of 8 bits (e4m3
+// or e5m2) with one power-of-two scale for each 128 of them, and the product of
+// two such operands.
+//
+//   quantise   block of 128 along a row (or 128 x 128): scale 2^e, e the
+//              smallest (>= -126) with max |x| <= 448 * 2^e (57344 for e5m2);
+//              code = x * 2^-e rounded to nearest, ties to even. Powers of two
+//              lose nothing but the code's own rounding, and are what the tensor
+//              core's block scale takes (one byte, e + 127).
+//   product    d[t, f] = sum_k a[t, k] b[f, k] (+ bias[f]): K in chunks of 512
+//              (4 blocks), a chunk's sum in the tensor core's fp32 accumulator,
+//              the chunks added in ascending order in fp32, one rounding of d.
+//
+// fp8_quant_kernel: one CTA per 128 x 128 tile of x, read once; writes the codes
+// of its rows' blocks, of its columns' blocks (the transposed operand that a sum
+// over rows needs), or both, and the columns' sums (a bias gradient). Bound by
+// HBM.
+//
+// fp8_gemm_kernel: tcgen05.mma kind::mxf8f6f4 with block scales. The features
+// (b's rows) are the 128 rows of an accumulator, the tokens (a's rows) its
+// columns: a call with few tokens takes a narrow accumulator (N = 16 or 64)
+// and reads each weight once, with the same sums in the same order as a call
+// with many (N = 224), so that a token's result does not depend on how many
+// there are. Persistent CTAs; warps: 0 TMA producer, 1 MMA issuer and TMEM
+// owner, 2 scale loader (gathers four blocks' bytes a row into the 128 x 4
+// layout that tcgen05.cp spreads over TMEM), 4 .. 11 the sums of the chunks and
+// the output. TMEM: two accumulators of N columns, so that a chunk is read out
+// while the next one is computed, and two sets of scales. Every wait is bounded.
+#include "rlk_device.cuh"
+#include "rlk_internal.h"
+#include "rlk_sm100.cuh"
+#include "rlk_tmap.h"
+
+RLK_DEFINE_STRICT_PROBE(probe_fp8_tu)
+
+namespace rlk {
+namespace {
+
+using namespace sm100;
+
+// ------------------------------------------------------------------ quantise
+constexpr int kTile = 128;          // rows and columns of a quantise CTA
+constexpr int kQuantThreads = 256;  // 16 row groups of 8 x 16 column groups of 8
+
+struct QuantItem {
+    const void* x;
+    uint8_t *q, *q_scale, *qt, *qt_scale;
+    float* part;  // column sums of each row tile [row_tiles, cols], or null
+    long long x_stride;
+    int rows, cols, ldq, lds, ldqt, ldst;
+    int col_tiles, tile0;  // tiles of the item: tile0 + row tile * col_tiles + column tile
+    bool fp32, square, e5m2;
+};
+struct QuantArgs {
+    QuantItem item[kFp8MaxItems];
+    int n;
+};
+
+// Exponent of the block's scale: the smallest e >= -126 with top <= 1.75 * 2^(e + room).
+__device__ __forceinline__ int scale_exponent(float top, int room) {
+    const int e = (int)((__float_as_uint(top) + 0x1FFFFFu) >> 23) - 127 - room;
+    return max(e, -126);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+template <bool kE5m2>
+__device__ __forceinline__ uint32_t code2(float lo, float hi) {  // two codes, lo in the low byte
+    uint16_t r;
+    if (kE5m2)
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <bool kE5m2>
+__device__ __forceinline__ uint2 code8(const float (&v)[8]) {
+    return make_uint2(code2<kE5m2>(v[0], v[1]) | code2<kE5m2>(v[2], v[3]) << 16,
+                      code2<kE5m2>(v[4], v[5]) | code2<kE5m2>(v[6], v[7]) << 16);
+}
+
+struct QuantSmem {
+    float row_top[kTile];
+    float col[16][kTile];  // the row groups' column maxima, then their column sums
+    float col_top[kTile];
+    uint8_t t[kTile * kTile];  // codes of columns: 128 bytes a column, 8-byte chunk g at g ^ (column / 8)
+};
+
+template <bool kE5m2>
+__device__ void quant_tile(const QuantItem& it, int tile, QuantSmem& sm) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int cg = tid & 15, rg = tid >> 4;
+    const int r0 = (tile / it.col_tiles) * kTile, c0 = (tile % it.col_tiles) * kTile;
+    const int col = c0 + 8 * cg;
+    constexpr int kRoom = kE5m2 ? 15 : 8;
+    float v[8][8];
+    const bool col_live = col < it.cols;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = r0 + 8 * rg + i;
+        if (row < it.rows && col_live) {
+            const long long at = (long long)row * it.x_stride + col;
+            if (it.fp32) {
+                const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(it.x) + at);
+                const float4 a = __ldg(p), b = __ldg(p + 1);
+                v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
+                v[i][4] = b.x, v[i][5] = b.y, v[i][6] = b.z, v[i][7] = b.w;
+            } else {
+                const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(it.x) + at));
+                const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[i][2 * k] = bf16_lo(w[k]), v[i][2 * k + 1] = bf16_hi(w[k]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+        }
+    }
+    const bool sums = it.part != nullptr;
+    float sum[8];
+    if (sums) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            sum[j] = v[0][j];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) sum[j] += v[i][j];
+        }
+    }
+    // an infinity takes the code of NaN and no part in its block's scale (fmaxf passes over NaN)
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[i][j]));
+    if (top == INFINITY) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (fabsf(v[i][j]) == INFINITY) v[i][j] = __uint_as_float(0x7fffffffu);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[i][j]));
+#pragma unroll
+        for (int k = 8; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+        if ((lane & 15) == i) sm.row_top[8 * rg + i] = m;
+    }
+    if (it.qt != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i][j]));
+            sm.col[rg][8 * cg + j] = m;
+        }
+    }
+    __syncthreads();
+    if (it.square) {  // one scale for the tile
+        if (tid < 32) {
+            float m = fmaxf(fmaxf(sm.row_top[lane], sm.row_top[lane + 32]), fmaxf(sm.row_top[lane + 64], sm.row_top[lane + 96]));
+#pragma unroll
+            for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+            __syncwarp();
+            for (int k = 0; k < 4; ++k) sm.row_top[lane + 32 * k] = sm.col_top[lane + 32 * k] = m;
+        }
+    } else if (it.qt != nullptr && tid < kTile) {
+        float m = sm.col[0][tid];
+#pragma unroll
+        for (int k = 1; k < 16; ++k) m = fmaxf(m, sm.col[k][tid]);
+        sm.col_top[tid] = m;
+    }
+    __syncthreads();
+    if (sums) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sm.col[rg][8 * cg + j] = sum[j];
+    }
+    if (it.q != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = r0 + 8 * rg + i;
+            const float s = power_of_two(-scale_exponent(sm.row_top[8 * rg + i], kRoom));
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = v[i][j] * s;
+            if (row < it.rows && col_live) *reinterpret_cast<uint2*>(it.q + (long long)row * it.ldq + col) = code8<kE5m2>(y);
+        }
+        if (tid < kTile && r0 + tid < it.rows)
+            it.q_scale[(long long)(r0 + tid) * it.lds + c0 / kTile] = (uint8_t)(scale_exponent(sm.row_top[tid], kRoom) + 127);
+    }
+    if (it.qt != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float s = power_of_two(-scale_exponent(sm.col_top[8 * cg + j], kRoom));
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = v[i][j] * s;
+            *reinterpret_cast<uint2*>(sm.t + (8 * cg + j) * kTile + ((rg ^ cg) << 3)) = code8<kE5m2>(y);
+        }
+        if (tid < kTile && c0 + tid < it.cols)
+            it.qt_scale[(long long)(c0 + tid) * it.ldst + r0 / kTile] = (uint8_t)(scale_exponent(sm.col_top[tid], kRoom) + 127);
+    }
+    __syncthreads();
+    if (it.qt != nullptr) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = tid + k * kQuantThreads, c = i >> 3, g = i & 7, x = c >> 3;
+            uint4 w = *reinterpret_cast<const uint4*>(sm.t + c * kTile + (((2 * g) ^ (x & ~1)) << 3));
+            if (x & 1) w = make_uint4(w.z, w.w, w.x, w.y);
+            // (a row's codes past it.rows are zeros, up to the row's padded length)
+            if (c0 + c < it.cols && r0 + 16 * g < it.rows)
+                *reinterpret_cast<uint4*>(it.qt + (long long)(c0 + c) * it.ldqt + r0 + 16 * g) = w;
+        }
+    }
+    if (sums && tid < kTile && c0 + tid < it.cols) {
+        float a = sm.col[0][tid];
+#pragma unroll
+        for (int k = 1; k < 16; ++k) a += sm.col[k][tid];
+        it.part[(long long)(r0 / kTile) * it.cols + c0 + tid] = a;
+    }
+}
+
+__global__ void __launch_bounds__(kQuantThreads) fp8_quant_kernel(const __grid_constant__ QuantArgs a) {
+    __shared__ __align__(16) QuantSmem sm;
+    int i = 0;
+    while (i + 1 < a.n && (int)blockIdx.x >= a.item[i + 1].tile0) ++i;
+    const QuantItem& it = a.item[i];
+    if (it.e5m2)
+        quant_tile<true>(it, blockIdx.x - it.tile0, sm);
+    else
+        quant_tile<false>(it, blockIdx.x - it.tile0, sm);
+}
+
+struct FoldItem {
+    const float* part;
+    float* out;
+    int tiles, cols, block0;
+};
+struct FoldArgs {
+    FoldItem item[kFp8MaxItems];
+    int n;
+};
+constexpr int kFoldThreads = 128;
+
+// Column sums: the row tiles in ascending order.
+__global__ void __launch_bounds__(kFoldThreads) fp8_fold_kernel(const __grid_constant__ FoldArgs a) {
+    int i = 0;
+    while (i + 1 < a.n && (int)blockIdx.x >= a.item[i + 1].block0) ++i;
+    const FoldItem& it = a.item[i];
+    const int c = (blockIdx.x - it.block0) * kFoldThreads + threadIdx.x;
+    if (c >= it.cols) return;
+    const float* p = it.part + c;
+    float s = 0.0f;
+    int t = 0;
+    for (; t + 8 <= it.tiles; t += 8) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = p[(long long)(t + k) * it.cols];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += v[k];
+    }
+    for (; t < it.tiles; ++t) s += p[(long long)t * it.cols];
+    it.out[c] = s;
+}
+
+// ------------------------------------------------------------------ product
+constexpr int kBK = 128;        // bytes of a row in a stage: one scale block
+constexpr int kChunkBlocks = 4; // blocks whose products share an accumulator
+constexpr int kFBytes = 128 * kBK;
+constexpr int kThreads = 384;
+constexpr int kWarpTma = 0, kWarpMma = 1, kWarpScale = 2, kWarpEpilogue = 4;
+constexpr int kScaleRing = 3;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+
+__device__ int g_status_fp8;
+
+template <int NT>
+struct Cfg {
+    static constexpr int kAtoms = (NT + 127) / 128;           // 128-row scale atoms of the tokens
+    static constexpr int kStageBytes = kFBytes + NT * kBK;
+    static constexpr int kStages = NT >= 200 ? 4 : 8;
+    static constexpr int kScaleBytes = 512 * (1 + kAtoms);    // one chunk's scales
+    static constexpr int kSmemBytes = kStages * kStageBytes + kScaleRing * kScaleBytes + 1024;
+    static constexpr int kHalf = NT >= 32 ? NT / 2 : NT;      // columns of an epilogue warp
+    static constexpr int kAccCol = (NT + 31) / 32 * 32;       // column of the second accumulator
+    static constexpr int kScaleCol = 2 * kAccCol;             // two sets of 4 + 4 * kAtoms columns, 16 apart
+    static_assert(kStageBytes % 1024 == 0 && kScaleCol + 32 <= 512 && 4 * (1 + kAtoms) <= 16, "");
+};
+
+struct GemmItem {
+    CUtensorMap map_f, map_t;  // features [n, k], box 128 x 128; tokens [m, k], box 128 x NT
+    const uint8_t *sf, *st;
+    const uint16_t* bias;
+    void* d;
+    long long d_stride;
+    int ldsf, ldst, m, n, blocks, tiles_f, tile0;
+    uint32_t idesc;  // formats of the operands
+    bool fp32, accumulate;
+};
+struct GemmArgs {
+    GemmItem item[kFp8MaxItems];
+    int n, tiles;
+};
+
+// Instruction descriptor of kind::mxf8f6f4 with e8m0 scales, without the
+// formats and the scale bytes' places.
+constexpr uint32_t idesc_mx(int M, int N) {
+    return (1u << 23) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// D[tmem] (+)= (A * 2^sa)[smem] * (B * 2^sb)[smem]; A, B 8-bit, K = 32, one scale a row.
+__device__ __forceinline__ void mma_mx(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sa,
+                                       uint32_t sb, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+// 32 rows of 16 bytes from shared memory to 4 TMEM columns, repeated in every lane quarter.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t sdesc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void fail(volatile int* abort_flag) {
+    *abort_flag = 1;
+    atomicOr(&g_status_fp8, 1);
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, kWaitLimitNs));
+}
+
+struct TileAt {
+    int item, f0, t0;
+};
+template <int NT>
+__device__ __forceinline__ TileAt tile_at(const GemmArgs& a, int t) {
+    TileAt r;
+    r.item = 0;
+    while (r.item + 1 < a.n && t >= a.item[r.item + 1].tile0) ++r.item;
+    const int l = t - a.item[r.item].tile0;
+    r.f0 = (l % a.item[r.item].tiles_f) * 128;  // consecutive tiles share their tokens (L2 reuse)
+    r.t0 = (l / a.item[r.item].tiles_f) * NT;
+    return r;
+}
+
+// One thread's feature f over kHalf tokens from t on: + bias, rounded, stored. Two lanes trade values so that
+// each holds two neighbouring features of one token: 4-byte stores, 64 bytes a token and warp.
+template <int kHalf>
+__device__ __forceinline__ void store_tile(const GemmItem& it, const float (&acc)[kHalf], int f, int t) {
+    const bool live = f < it.n;
+    const float b = live && it.bias != nullptr ? __uint_as_float((uint32_t)it.bias[f] << 16) : 0.0f;
+    if (it.fp32) {
+        float* d = static_cast<float*>(it.d) + (long long)t * it.d_stride + f;
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) {
+            if (live && t + j < it.m) *d = it.accumulate ? *d + (acc[j] + b) : acc[j] + b;
+            d += it.d_stride;
+        }
+        return;
+    }
+    const bool odd = threadIdx.x & 1;
+    uint16_t* d = static_cast<uint16_t*>(it.d) + (long long)(t + odd) * it.d_stride + (f & ~1);
+#pragma unroll
+    for (int j = 0; j < kHalf; j += 2) {
+        const float v0 = acc[j] + b, v1 = acc[j + 1] + b;
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+        if (live && t + j + odd < it.m) *reinterpret_cast<uint32_t*>(d) = odd ? pack_bf16(got, v1) : pack_bf16(v0, got);
+        d += 2 * it.d_stride;
+    }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ GemmArgs a) {
+    using C = Cfg<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * C::kStages + 2 * kScaleRing + 5];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int abort_flag;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    auto stage_f = [&](int st) { return sbase + st * C::kStageBytes; };
+    auto stage_t = [&](int st) { return sbase + st * C::kStageBytes + kFBytes; };
+    auto scales = [&](int g) { return sbase + C::kStages * C::kStageBytes + g * C::kScaleBytes; };
+    const uint32_t bar_full = smem_u32(&bars[0]);                     // [kStages] stage loaded
+    const uint32_t bar_empty = bar_full + 8 * C::kStages;             // [kStages] stage consumed
+    const uint32_t bar_sfull = bar_empty + 8 * C::kStages;            // [kScaleRing] a chunk's scales written
+    const uint32_t bar_sempty = bar_sfull + 8 * kScaleRing;           // [kScaleRing] and consumed
+    const uint32_t bar_acc = bar_sempty + 8 * kScaleRing;             // [2] accumulator complete
+    const uint32_t bar_free = bar_acc + 16;                           // [2] accumulator read out
+    const uint32_t bar_drain = bar_free + 16;
+
+    if (tid == 0) {
+        abort_flag = 0;
+        for (int i = 0; i < C::kStages; ++i) mbar_init(bar_full + 8 * i, 1), mbar_init(bar_empty + 8 * i, 1);
+        for (int i = 0; i < kScaleRing; ++i) mbar_init(bar_sfull + 8 * i, 1), mbar_init(bar_sempty + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(bar_acc + 8 * i, 1), mbar_init(bar_free + 8 * i, 8);
+        mbar_init(bar_drain, 1);
+        fence_barrier_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp == kWarpTma) {
+        if (lane == 0) {
+            uint32_t it = 0;  // stage uses so far
+            bool ok = true;
+            for (int t = blockIdx.x; ok && t < a.tiles; t += gridDim.x) {
+                const TileAt at = tile_at<NT>(a, t);
+                const GemmItem& g = a.item[at.item];
+                for (int kb = 0; kb < g.blocks; ++kb, ++it) {
+                    const int st = it % C::kStages;
+                    const uint32_t use = it / C::kStages;
+                    if (use > 0 && !mbar_wait(bar_empty + 8 * st, (use - 1) & 1, &abort_flag, kWaitLimitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx(bar_full + 8 * st, C::kStageBytes);
+                    tma_load_2d(stage_f(st), &g.map_f, bar_full + 8 * st, kb * kBK, at.f0);
+                    tma_load_2d(stage_t(st), &g.map_t, bar_full + 8 * st, kb * kBK, at.t0);
+                }
+            }
+            if (!ok) fail(&abort_flag);
+            // drain: every issued stage has landed (the last kStages uses)
+            for (uint32_t u = it < C::kStages ? 0 : it - C::kStages; u < it; ++u)
+                mbar_wait_drain(bar_full + 8 * (u % C::kStages), (u / C::kStages) & 1, kWaitLimitNs);
+        }
+    } else if (warp == kWarpMma) {
+        if (lane == 0) {
+            uint32_t it = 0, chunk = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; ok && t < a.tiles; t += gridDim.x) {
+                const TileAt at = tile_at<NT>(a, t);
+                const int blocks = a.item[at.item].blocks;
+                const uint32_t idesc = a.item[at.item].idesc;
+                for (int kb = 0; ok && kb < blocks; ++chunk) {
+                    const int buf = chunk & 1, ring = chunk % kScaleRing;
+                    const uint32_t use = chunk >> 1;
+                    if ((use > 0 && !mbar_wait(bar_free + 8 * buf, (use - 1) & 1, &abort_flag, kWaitLimitNs)) ||
+                        !mbar_wait(bar_sfull + 8 * ring, (chunk / kScaleRing) & 1, &abort_flag, kWaitLimitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t acc = tmem + buf * C::kAccCol;
+                    const uint32_t sa = tmem + C::kScaleCol + buf * 16, sb = sa + 4;
+#pragma unroll
+                    for (int i = 0; i < 1 + C::kAtoms; ++i)
+                        tmem_copy_scales(sa + 4 * i, sdesc_noswizzle(scales(ring) + 512 * i, 0, 128));
+                    const int end = min(kb + kChunkBlocks, blocks);
+                    uint32_t id = idesc;
+                    for (uint32_t first = 0; kb < end; ++kb, ++it) {
+                        const int st = it % C::kStages;
+                        if (!mbar_wait(bar_full + 8 * st, (it / C::kStages) & 1, &abort_flag, kWaitLimitNs)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll
+                        for (int j = 0; j < kBK / 32; ++j) {
+                            mma_mx(acc, sdesc_sw128(stage_f(st) + 32 * j, 16, 1024), sdesc_sw128(stage_t(st) + 32 * j, 16, 1024),
+                                   id, sa, sb, first);
+                            first = 1;
+                        }
+                        mma_commit(bar_empty + 8 * st);
+                        id += (1u << 29) | (1u << 4);  // the next block's scale bytes
+                    }
+                    if (ok) {
+                        mma_commit(bar_sempty + 8 * ring);
+                        mma_commit(bar_acc + 8 * buf);
+                    }
+                }
+            }
+            if (!ok) fail(&abort_flag);
+            mma_commit(bar_drain);
+            mbar_wait_drain(bar_drain, 0, kWaitLimitNs);
+        }
+    } else if (warp == kWarpScale) {
+        // a chunk's scale bytes, 128 rows an atom: row r's four bytes at (r % 32) * 16 + (r / 32) * 4
+        uint32_t chunk = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < a.tiles; t += gridDim.x) {
+            const TileAt at = tile_at<NT>(a, t);
+            const GemmItem& g = a.item[at.item];
+            for (int kb = 0; kb < g.blocks; kb += kChunkBlocks, ++chunk) {
+                const int ring = chunk % kScaleRing;
+                const uint32_t use = chunk / kScaleRing;
+                uint32_t w[1 + C::kAtoms][4];
+#pragma unroll
+                for (int i = 0; i < 1 + C::kAtoms; ++i) {
+                    const int r0 = i == 0 ? at.f0 : at.t0 + 128 * (i - 1), rows = i == 0 ? g.n : g.m;
+                    const uint8_t* p = i == 0 ? g.sf : g.st;
+                    const int ld = i == 0 ? g.ldsf : g.ldst;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int r = r0 + 32 * c + lane;
+                        w[i][c] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(p + (long long)r * ld + kb)) : 0x7f7f7f7fu;
+                    }
+                }
+                if (use > 0 && !warp_wait(bar_sempty + 8 * ring, (use - 1) & 1, &abort_flag)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int i = 0; i < 1 + C::kAtoms; ++i)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(scales(ring) + 512 * i + 16 * lane),
+                                 "r"(w[i][0]), "r"(w[i][1]), "r"(w[i][2]), "r"(w[i][3])
+                                 : "memory");
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_sfull + 8 * ring);
+            }
+        }
+        if (!ok && lane == 0) fail(&abort_flag);
+    } else if (warp >= kWarpEpilogue) {
+        const int quarter = warp & 3, half = (warp - kWarpEpilogue) >> 2;
+        const bool idle = half * C::kHalf >= NT;  // (N = 16: the first four warps take all columns)
+        const uint32_t at0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * C::kHalf;
+        uint32_t chunk = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < a.tiles; t += gridDim.x) {
+            const TileAt at = tile_at<NT>(a, t);
+            const GemmItem& g = a.item[at.item];
+            float acc[C::kHalf];
+            for (int kb = 0; kb < g.blocks; kb += kChunkBlocks, ++chunk) {
+                const int buf = chunk & 1;
+                if (!warp_wait(bar_acc + 8 * buf, (chunk >> 1) & 1, &abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (!idle) {
+#pragma unroll
+                    for (int c = 0; c < C::kHalf; c += 16) {
+                        uint32_t r[16];
+                        tmem_ld16(at0 + buf * C::kAccCol + c, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            acc[c + i] = kb == 0 ? __uint_as_float(r[i]) : acc[c + i] + __uint_as_float(r[i]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_free + 8 * buf);
+            }
+            if (ok && !idle) store_tile<C::kHalf>(g, acc, at.f0 + 32 * quarter + lane, at.t0 + half * C::kHalf);
+        }
+        if (!ok && lane == 0) fail(&abort_flag);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int NT>
+cudaError_t launch_nt(GemmArgs& a, int sms, cudaStream_t s) {
+    a.tiles = 0;
+    for (int i = 0; i < a.n; ++i) {
+        GemmItem& g = a.item[i];
+        g.tiles_f = (g.n + 127) / 128;
+        g.tile0 = a.tiles;
+        g.idesc |= idesc_mx(128, NT);
+        a.tiles += g.tiles_f * ((g.m + NT - 1) / NT);
+    }
+    cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NT>::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    timing_begin(kKFp8Gemm, s);
+    fp8_gemm_kernel<NT><<<a.tiles < sms ? a.tiles : sms, kThreads, Cfg<NT>::kSmemBytes, s>>>(a);
+    timing_end(kKFp8Gemm, s);
+    return cudaGetLastError();
+}
+
+// codes [rows, k] with rows ld bytes apart, box 128 x box_rows
+bool codes_map(CUtensorMap* m, const void* base, long long rows, long long k, long long ld, int box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld};
+    const cuuint32_t box[2] = {kBK, (cuuint32_t)box_rows};
+    return tmap::encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box);
+}
+
+}  // namespace
+
+long long fp8_quant_tiles(long long rows, long long cols) { return ((rows + 127) / 128) * ((cols + 127) / 128); }
+
+cudaError_t launch_fp8_quant(const rlk_fp8_quant* q, int n, cudaStream_t s) {
+    QuantArgs a;
+    FoldArgs f;
+    a.n = f.n = 0;
+    int tiles = 0, blocks = 0;
+    for (int i = 0; i < n; ++i) {
+        const rlk_fp8_quant& e = q[i];
+        if (e.col_sum != nullptr) {
+            f.item[f.n++] = FoldItem{static_cast<const float*>(e.workspace), e.col_sum, (int)((e.rows + 127) / 128), (int)e.cols, blocks};
+            blocks += ((int)e.cols + kFoldThreads - 1) / kFoldThreads;
+        }
+        if (e.rows == 0) continue;
+        QuantItem& it = a.item[a.n++];
+        it.x = e.x;
+        it.q = static_cast<uint8_t*>(e.q);
+        it.q_scale = e.q_scale;
+        it.qt = static_cast<uint8_t*>(e.qt);
+        it.qt_scale = e.qt_scale;
+        it.part = e.col_sum != nullptr ? static_cast<float*>(e.workspace) : nullptr;
+        it.x_stride = e.x_stride;
+        it.rows = (int)e.rows;
+        it.cols = (int)e.cols;
+        it.ldq = (int)rlk_fp8_row_bytes(e.cols);
+        it.lds = (int)rlk_fp8_scale_row_bytes(e.cols);
+        it.ldqt = (int)rlk_fp8_row_bytes(e.rows);
+        it.ldst = (int)rlk_fp8_scale_row_bytes(e.rows);
+        it.col_tiles = (int)((e.cols + 127) / 128);
+        it.tile0 = tiles;
+        it.fp32 = e.x_dtype == RLK_FP32;
+        it.square = e.square != 0;
+        it.e5m2 = e.format == RLK_E5M2;
+        tiles += (int)fp8_quant_tiles(e.rows, e.cols);
+    }
+    cudaError_t e = cudaSuccess;
+    if (tiles > 0) {
+        timing_begin(kKFp8Quant, s);
+        fp8_quant_kernel<<<tiles, kQuantThreads, 0, s>>>(a);
+        timing_end(kKFp8Quant, s);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess || blocks == 0) return e;
+    timing_begin(kKFp8Fold, s);
+    fp8_fold_kernel<<<blocks, kFoldThreads, 0, s>>>(f);
+    timing_end(kKFp8Fold, s);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_fp8_gemm(const rlk_fp8_product* p, int n, cudaStream_t s) {
+    GemmArgs a;
+    a.n = 0;
+    long long most = 0;
+    for (int i = 0; i < n; ++i) most = most < p[i].m ? p[i].m : most;
+    // The accumulator's columns: the narrowest that takes every token, else 224.
+    const int nt = most <= 16 ? 16 : most <= 64 ? 64 : 224;
+    for (int i = 0; i < n; ++i) {
+        const rlk_fp8_product& e = p[i];
+        if (e.m == 0 || e.n == 0) continue;
+        GemmItem& g = a.item[a.n++];
+        const long long ld = rlk_fp8_row_bytes(e.k);
+        if (!codes_map(&g.map_f, e.b, e.n, e.k, ld, 128) || !codes_map(&g.map_t, e.a, e.m, e.k, ld, nt))
+            return cudaErrorInvalidValue;
+        g.sf = e.b_scale;
+        g.st = e.a_scale;
+        g.bias = static_cast<const uint16_t*>(e.bias);
+        g.d = e.d;
+        g.d_stride = e.d_stride;
+        g.ldsf = g.ldst = (int)rlk_fp8_scale_row_bytes(e.k);
+        g.m = (int)e.m;
+        g.n = (int)e.n;
+        g.blocks = (int)((e.k + 127) / 128);
+        // (the features are the instruction's A)
+        g.idesc = (e.b_format == RLK_E5M2 ? 1u << 7 : 0u) | (e.a_format == RLK_E5M2 ? 1u << 10 : 0u);
+        g.fp32 = e.d_dtype == RLK_FP32;
+        g.accumulate = e.accumulate != 0;
+    }
+    if (a.n == 0) return cudaSuccess;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    return nt == 16 ? launch_nt<16>(a, sms, s) : nt == 64 ? launch_nt<64>(a, sms, s) : launch_nt<224>(a, sms, s);
+}
+
+int read_and_clear_status_fp8(cudaStream_t s) {
+    int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbolAsync(&v, g_status_fp8, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess) return -1;
+    if (cudaMemcpyToSymbolAsync(g_status_fp8, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess) return -1;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return -1;
+    return v;
+}
+
+}  // namespace rlk

@@ -1,0 +1,694 @@
+// Muon: momentum, an update made orthogonal by Newton-Schulz products, and the
+// weights' step, over a list of matrices.
+//
+//   m = mu m + g';  u = g' + mu m (Nesterov) or m;  X = u / (|u|_F + eps), turned over if it is tall (r <= k)
+//   each iteration:  A = X X^T;  B = b A + c A A;  X = a X + B X
+//   p -= rate wd p + rate update_rms sqrt(max(rows, columns)) X
+//
+// The products run on tcgen05 with fp16 operands and fp32 accumulators: the
+// singular values lie in [0, 1.3], so that fp16's range is enough (X starts
+// multiplied by a power of two near sqrt(r), where its entries are about 1 /
+// sqrt(k) as they are at the end), and its 11 bits keep the update within 2^-9
+// of the formula's where bf16's 8 lose a percent: small singular values grow
+// 3.4 times an iteration, and the roundings with them. A and B are
+// symmetric: only tiles that meet the lower triangle are computed, and stored
+// on both sides.
+//
+// Matrices of one size lie one behind the other in the workspace (a group): one
+// tensor map with the matrix as its third coordinate serves them, and cuts
+// tiles off at a matrix's end. One launch of a product serves every group of
+// the list. Each output tile is one CTA's accumulator, K ascending: a
+// matrix's result does not depend on its list.
+#include "rlk_device.cuh"
+#include "rlk_internal.h"
+#include "rlk_sm100.cuh"
+#include "rlk_tmap.h"
+
+#include <cuda_fp16.h>
+#include <math.h>
+#include <new>
+#include <vector>
+
+RLK_DEFINE_STRICT_PROBE(probe_muon_tu)
+
+namespace rlk {
+namespace {
+
+using namespace sm100;
+
+// ------------------------------------------------------------------ elementwise passes
+constexpr int kItems = 40;          // matrices a launch of an elementwise pass takes (its argument: 4 KB)
+constexpr int kPassThreads = 256;
+constexpr int kMaxPartials = 1024;  // partial sums of squares of a matrix
+constexpr int kMinChunk = 8192;     // elements a partial sums, at least
+constexpr int kSide = 64;           // the passes' tiles
+
+struct Item {
+    void* p;          // step: fp32, or bf16 with master; orthogonalize: bf16 out
+    float* master;
+    const void* g;    // step: gradient; orthogonalize: the matrix
+    float* m;         // null: orthogonalize
+    __half* x;        // the matrix's X [r, ld]
+    double* part;     // its partial sums
+    long long n, chunk;
+    int rows, cols, ld, parts, block0;
+    float start;      // X's power of two at the start
+    float rate, decay;  // p -= decay p + rate X (lr_dev: times its value)
+    bool g32;
+};
+struct PassArgs {
+    Item item[kItems];
+    int n;
+    float mu, eps;
+    bool nesterov;
+    const float *grad_scale, *lr_dev;
+};
+
+__device__ __forceinline__ const Item& item_of(const PassArgs& a) {
+    int i = 0;
+    while (i + 1 < a.n && (int)blockIdx.x >= a.item[i + 1].block0) ++i;
+    return a.item[i];
+}
+__device__ __forceinline__ float element(const void* g, bool fp32, long long i) {
+    return fp32 ? static_cast<const float*>(g)[i] : __uint_as_float((uint32_t)static_cast<const uint16_t*>(g)[i] << 16);
+}
+// The factor of the gradients; false: it is not finite and the tensors stay as they are.
+__device__ __forceinline__ bool factor_of(const PassArgs& a, float& f) {
+    f = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
+    return fabsf(f) < INFINITY;
+}
+// The sum over the CTA's threads, in a fixed order.
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double s[kPassThreads / 32];
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0;
+    for (int i = 0; i < kPassThreads / 32; ++i) v += s[i];
+    return v;
+}
+
+// New momentum, and the partial sums of u's squares: a chunk of consecutive elements a CTA, a thread's squares in
+// fp32 (at most 32 + its share of a long chunk), then fp64.
+__global__ void __launch_bounds__(kPassThreads) muon_momentum_kernel(const __grid_constant__ PassArgs a) {
+    const Item& it = item_of(a);
+    float f;
+    if (!factor_of(a, f)) return;
+    const int chunk = blockIdx.x - it.block0;
+    const long long lo = chunk * it.chunk, hi = min(lo + it.chunk, it.n);
+    double sum = 0.0;
+    for (long long i0 = lo; i0 < hi; i0 += 4 * kPassThreads) {
+        float sq = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const long long i = i0 + j * kPassThreads + threadIdx.x;
+            if (i < hi) {
+                float u = element(it.g, it.g32, i);
+                if (it.m != nullptr) {
+                    const float g = u * f, m = fmaf(a.mu, it.m[i], g);
+                    it.m[i] = m;
+                    u = a.nesterov ? fmaf(a.mu, m, g) : m;
+                }
+                sq = fmaf(u, u, sq);
+            }
+        }
+        sum += (double)sq;
+    }
+    sum = block_sum(sum);
+    if (threadIdx.x == 0) it.part[chunk] = sum;
+}
+
+// X = u * start / (|u| + eps) in fp16, turned over where the matrix is tall. A 64 x 64 tile a CTA.
+__global__ void __launch_bounds__(kPassThreads) muon_start_kernel(const __grid_constant__ PassArgs a) {
+    __shared__ float tile[kSide][kSide + 1];
+    const Item& it = item_of(a);
+    float f;
+    const bool ok = factor_of(a, f);
+    double sq = 0.0;
+    for (int i = threadIdx.x; i < it.parts; i += kPassThreads) sq += it.part[i];
+    const float inv = (float)((double)it.start / (sqrt(block_sum(sq)) + (double)a.eps));
+    const int tiles_c = (it.cols + kSide - 1) / kSide, t = blockIdx.x - it.block0;
+    const int r0 = t / tiles_c * kSide, c0 = t % tiles_c * kSide;
+    const int c = threadIdx.x & 63;
+    const bool tall = it.rows > it.cols;
+#pragma unroll 4
+    for (int r = threadIdx.x >> 6; r < kSide; r += kPassThreads / kSide) {
+        float u = 0.0f;
+        if (ok && r0 + r < it.rows && c0 + c < it.cols) {
+            const long long i = (long long)(r0 + r) * it.cols + c0 + c;
+            u = element(it.g, it.g32, i);
+            if (it.m != nullptr) u = a.nesterov ? fmaf(a.mu, it.m[i], u * f) : it.m[i];
+            u *= inv;
+        }
+        if (tall)
+            tile[r][c] = u;
+        else if (r0 + r < it.rows && c0 + c < it.cols)
+            it.x[(long long)(r0 + r) * it.ld + c0 + c] = __float2half_rn(u);
+    }
+    if (!tall) return;
+    __syncthreads();
+    for (int r = threadIdx.x >> 6; r < kSide; r += kPassThreads / kSide)
+        if (c0 + r < it.cols && r0 + c < it.rows)
+            it.x[(long long)(c0 + r) * it.ld + r0 + c] = __float2half_rn(tile[c][r]);
+}
+
+// p -= decay p + rate X, or p = X (orthogonalize). A 64 x 64 tile a CTA.
+__global__ void __launch_bounds__(kPassThreads) muon_update_kernel(const __grid_constant__ PassArgs a) {
+    __shared__ float tile[kSide][kSide + 1];
+    const Item& it = item_of(a);
+    float f;
+    if (!factor_of(a, f)) return;
+    const int tiles_c = (it.cols + kSide - 1) / kSide, t = blockIdx.x - it.block0;
+    const int r0 = t / tiles_c * kSide, c0 = t % tiles_c * kSide;
+    const int c = threadIdx.x & 63;
+    const bool tall = it.rows > it.cols;
+    if (tall) {
+#pragma unroll 4
+        for (int r = threadIdx.x >> 6; r < kSide; r += kPassThreads / kSide)
+            tile[r][c] = c0 + r < it.cols && r0 + c < it.rows ? __half2float(it.x[(long long)(c0 + r) * it.ld + r0 + c]) : 0.0f;
+        __syncthreads();
+    }
+    const float lr = a.lr_dev != nullptr ? *a.lr_dev : 1.0f;
+    const float rate = it.rate * lr, decay = it.decay * lr;
+#pragma unroll 4
+    for (int r = threadIdx.x >> 6; r < kSide; r += kPassThreads / kSide) {
+        if (r0 + r >= it.rows || c0 + c >= it.cols) continue;
+        const long long i = (long long)(r0 + r) * it.cols + c0 + c;
+        const float x = tall ? tile[c][r] : __half2float(it.x[(long long)(r0 + r) * it.ld + c0 + c]);
+        float* w = it.master != nullptr ? it.master : static_cast<float*>(it.p);
+        float v = x;
+        if (it.m != nullptr) {
+            v = w[i] - fmaf(decay, w[i], rate * x);
+            w[i] = v;
+        }
+        if (it.m == nullptr || it.master != nullptr) static_cast<__nv_bfloat16*>(it.p)[i] = __float2bfloat16_rn(v);
+    }
+}
+
+// ------------------------------------------------------------------ products
+enum Mode { kGram = 0, kPoly = 1, kApply = 2 };
+constexpr int kGroups = 8;  // sizes a launch takes
+constexpr int kBM = 128, kBN = 256, kBK = 64, kStages = 4;
+constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2, kStageBytes = kABytes + kBBytes;
+constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+constexpr int kThreads = 384;
+constexpr int kWarpTma = 0, kWarpMma = 1, kWarpEpilogue = 4;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+
+__device__ int g_status_muon;
+
+struct Group {
+    CUtensorMap map_m;   // the operand of the 128 rows: [z][rows][K], box 64 x 128 x 1
+    CUtensorMap map_n;   // the operand of the 256 columns: gram, poly the same, box 64 x 128; apply X, box 64 x 64 (MN-major)
+    const __half* add;   // poly: A; apply: X: added times `add_by`
+    __half* out;
+    long long add_step, out_step;  // from matrix to matrix
+    int rows, cols;      // of the output (gram, poly: r x r)
+    int ld_add, ld_out, steps, per, tile0;  // k-steps; tiles of one matrix; first tile
+    float by, add_by;    // out = by * product + add_by * add
+};
+struct GemmArgs {
+    Group g[kGroups];
+    int n, tiles;
+};
+
+struct TileAt {
+    int g, z, m0, n0;
+};
+template <int kMode>
+__device__ __forceinline__ TileAt tile_at(const GemmArgs& a, int t) {
+    TileAt r;
+    r.g = 0;
+    while (r.g + 1 < a.n && t >= a.g[r.g + 1].tile0) ++r.g;
+    const Group& g = a.g[r.g];
+    int l = t - g.tile0;
+    r.z = l / g.per;
+    l -= r.z * g.per;
+    if (kMode == kApply) {
+        const int tn = (g.cols + kBN - 1) / kBN;
+        r.m0 = l / tn * kBM;
+        r.n0 = l % tn * kBN;
+    } else {
+        // block rows 2p and 2p + 1 have p + 1 tiles each: p (p + 1) tiles before them
+        int p = (int)((sqrtf(4.0f * l + 1.0f) - 1.0f) * 0.5f);
+        while (p * (p + 1) > l) --p;
+        while ((p + 1) * (p + 2) <= l) ++p;
+        l -= p * (p + 1);
+        r.m0 = (2 * p + (l > p)) * kBM;
+        r.n0 = (l > p ? l - p - 1 : l) * kBN;
+    }
+    return r;
+}
+
+__device__ __forceinline__ void fail(volatile int* abort_flag) {
+    *abort_flag = 1;
+    atomicOr(&g_status_muon, 1);
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, kWaitLimitNs));
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
+    return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// 32 columns from j on of row i (a warp: 32 rows from i - lane): out = by * v + add_by * add, and on the other
+// side of the diagonal.
+template <int kMode>
+__device__ __forceinline__ void store32(const Group& g, int z, float (&v)[32], int i, int j) {
+    const int lane = threadIdx.x & 31, i0 = i - lane;
+    if (kMode != kApply && j > i0) return;  // above the diagonal: stored from the other side
+    const bool live = i < g.rows;
+    if (kMode != kGram) {
+        const __half* add = g.add + z * g.add_step + (long long)i * g.ld_add + j;
+#pragma unroll
+        for (int c = 0; c < 32; c += 8) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (live && j + c < g.cols) w = __ldg(reinterpret_cast<const uint4*>(add + c));
+            const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&q[k]));
+                v[c + 2 * k] = fmaf(g.add_by, x.x, g.by * v[c + 2 * k]);
+                v[c + 2 * k + 1] = fmaf(g.add_by, x.y, g.by * v[c + 2 * k + 1]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c] *= g.by;
+    }
+    __half* out = g.out + z * g.out_step;
+    __half* row = out + (long long)i * g.ld_out + j;
+    if (kMode != kApply && j == i0) {  // on the diagonal: the lower triangle and its mirror image, value by value
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            if (live && c <= lane) {
+                const __half h = __float2half_rn(v[c]);
+                row[c] = h;
+                out[(long long)(j + c) * g.ld_out + i] = h;
+            }
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < 32; c += 8)  // (columns up to the padded row's end)
+        if (live && j + c < g.cols)
+            *reinterpret_cast<uint4*>(row + c) = make_uint4(pack_half(v[c], v[c + 1]), pack_half(v[c + 2], v[c + 3]),
+                                                            pack_half(v[c + 4], v[c + 5]), pack_half(v[c + 6], v[c + 7]));
+    if (kMode == kApply) return;
+    const bool odd = lane & 1;
+    __half* col = out + (long long)(j + odd) * g.ld_out + (i & ~1);
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? v[c] : v[c + 1], 1);
+        // (all columns here are below the warp's rows, so they exist; the pair may end in the row's padding)
+        if ((i & ~1) < g.rows) *reinterpret_cast<uint32_t*>(col) = odd ? pack_half(got, v[c + 1]) : pack_half(v[c], got);
+        col += 2 * g.ld_out;
+    }
+}
+
+template <int kMode>
+__global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_constant__ GemmArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int abort_flag;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    auto stage_a = [&](int st) { return sbase + st * kStageBytes; };
+    auto stage_b = [&](int st) { return sbase + st * kStageBytes + kABytes; };
+    const uint32_t bar_full = smem_u32(&bars[0]), bar_empty = bar_full + 8 * kStages;
+    const uint32_t bar_acc = bar_empty + 8 * kStages, bar_free = bar_acc + 16, bar_drain = bar_free + 16;
+
+    if (tid == 0) {
+        abort_flag = 0;
+        for (int i = 0; i < kStages; ++i) mbar_init(bar_full + 8 * i, 1), mbar_init(bar_empty + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(bar_acc + 8 * i, 1), mbar_init(bar_free + 8 * i, 8);
+        mbar_init(bar_drain, 1);
+        fence_barrier_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp == kWarpTma) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; ok && t < a.tiles; t += gridDim.x) {
+                const TileAt at = tile_at<kMode>(a, t);
+                const Group& g = a.g[at.g];
+                for (int kk = 0; kk < g.steps; ++kk, ++it) {
+                    const int st = it % kStages;
+                    const uint32_t use = it / kStages, bar = bar_full + 8 * st;
+                    if (use > 0 && !mbar_wait(bar_empty + 8 * st, (use - 1) & 1, &abort_flag, kWaitLimitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx(bar, kStageBytes);
+                    tma_load_3d(stage_a(st), &g.map_m, bar, kk * kBK, at.m0, at.z);
+                    if (kMode == kApply) {
+                        for (int q = 0; q < 4; ++q) tma_load_3d(stage_b(st) + q * 8192, &g.map_n, bar, at.n0 + 64 * q, kk * kBK, at.z);
+                    } else {
+                        for (int q = 0; q < 2; ++q) tma_load_3d(stage_b(st) + q * 16384, &g.map_n, bar, kk * kBK, at.n0 + 128 * q, at.z);
+                    }
+                }
+            }
+            if (!ok) fail(&abort_flag);
+            for (uint32_t u = it < kStages ? 0 : it - kStages; u < it; ++u)
+                mbar_wait_drain(bar_full + 8 * (u % kStages), (u / kStages) & 1, kWaitLimitNs);
+        }
+    } else if (warp == kWarpMma) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_f16(kBM, kBN, kMode == kApply);
+            uint32_t it = 0, local = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; ok && t < a.tiles; t += gridDim.x, ++local) {
+                const int buf = local & 1;
+                const uint32_t use = local >> 1;
+                if (use > 0 && !mbar_wait(bar_free + 8 * buf, (use - 1) & 1, &abort_flag, kWaitLimitNs)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t acc = tmem + buf * kBN;
+                const int steps = a.g[tile_at<kMode>(a, t).g].steps;
+                for (int kk = 0; kk < steps; ++kk, ++it) {
+                    const int st = it % kStages;
+                    if (!mbar_wait(bar_full + 8 * st, (it / kStages) & 1, &abort_flag, kWaitLimitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int j = 0; j < kBK / 16; ++j)
+                        mma_ss(acc, sdesc_sw128(stage_a(st) + 32 * j, 16, 1024),
+                               kMode == kApply ? sdesc_sw128(stage_b(st) + 2048 * j, 8192, 1024)
+                                               : sdesc_sw128(stage_b(st) + 32 * j, 16, 1024),
+                               idesc, (kk > 0 || j > 0) ? 1u : 0u);
+                    mma_commit(bar_empty + 8 * st);
+                }
+                if (ok) mma_commit(bar_acc + 8 * buf);
+            }
+            if (!ok) fail(&abort_flag);
+            mma_commit(bar_drain);
+            mbar_wait_drain(bar_drain, 0, kWaitLimitNs);
+        }
+    } else if (warp >= kWarpEpilogue) {
+        const int quarter = warp & 3, half = (warp - kWarpEpilogue) >> 2;
+        const uint32_t at0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
+        uint32_t local = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < a.tiles; t += gridDim.x, ++local) {
+            const int buf = local & 1;
+            if (!warp_wait(bar_acc + 8 * buf, (local >> 1) & 1, &abort_flag)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const TileAt at = tile_at<kMode>(a, t);
+            const Group& g = a.g[at.g];
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+                const int j = at.n0 + half * 128 + c;
+                if (j >= g.cols) break;
+                uint32_t r[32];
+                tmem_ld32(at0 + buf * kBN + c, r);
+                tmem_ld_wait();
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                store32<kMode>(g, at.z, v, at.m0 + 32 * quarter + lane, j);
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_free + 8 * buf);
+        }
+        if (!ok && lane == 0) fail(&abort_flag);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------ host
+size_t up(size_t x, size_t k) { return (x + k - 1) / k * k; }
+
+// Where a list's matrices lie in the workspace.
+struct Size {
+    int r, k, ld, ldr, count;          // r <= k; X rows of ld, A and B rows of ldr elements
+    size_t x[2], a, b;                 // byte offsets: X twice (read and written in turn), A, B
+};
+struct Plan {
+    std::vector<Size> sizes;
+    std::vector<int> of, z, parts;     // a matrix's size, its place among them, its partial sums
+    std::vector<long long> chunk;
+    std::vector<size_t> part;          // byte offset of its partial sums
+    size_t bytes = 0;
+};
+
+void plan_of(const rlk_muon_matrix* t, int n, Plan& p) {
+    p.of.assign(n, -1);
+    p.z.assign(n, 0);
+    p.parts.assign(n, 0);
+    p.chunk.assign(n, 0);
+    p.part.assign(n, 0);
+    for (int i = 0; i < n; ++i) {
+        if (t[i].rows == 0 || t[i].cols == 0) continue;
+        const int r = (int)(t[i].rows < t[i].cols ? t[i].rows : t[i].cols), k = (int)(t[i].rows < t[i].cols ? t[i].cols : t[i].rows);
+        int s = 0;
+        while (s < (int)p.sizes.size() && (p.sizes[s].r != r || p.sizes[s].k != k)) ++s;
+        if (s == (int)p.sizes.size()) p.sizes.push_back(Size{r, k, (int)up(k, 8), (int)up(r, 8), 0, {0, 0}, 0, 0});
+        p.of[i] = s;
+        p.z[i] = p.sizes[s].count++;
+        const long long e = t[i].rows * t[i].cols;
+        long long chunk = (e + kMaxPartials - 1) / kMaxPartials;
+        chunk = (long long)up(chunk < kMinChunk ? kMinChunk : chunk, 4 * kPassThreads);
+        p.chunk[i] = chunk;
+        p.parts[i] = (int)((e + chunk - 1) / chunk);
+        p.part[i] = p.bytes;
+        p.bytes += sizeof(double) * p.parts[i];
+    }
+    for (Size& s : p.sizes) {
+        auto take = [&](size_t bytes) {
+            p.bytes = up(p.bytes, 256);
+            const size_t at = p.bytes;
+            p.bytes += bytes;
+            return at;
+        };
+        for (size_t& x : s.x) x = take((size_t)s.count * s.r * s.ld * 2);
+        s.a = take((size_t)s.count * s.r * s.ldr * 2);
+        s.b = take((size_t)s.count * s.r * s.ldr * 2);
+    }
+}
+
+bool half_map(CUtensorMap* m, const void* base, int cols, int rows, int count, int ld, int box_rows) {
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)count};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)rows * ld * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+    return tmap::encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, box);
+}
+
+template <int kMode>
+cudaError_t launch_product(GemmArgs& a, int sms, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(muon_gemm_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    const int id = kMode == kGram ? kKMuonGram : kMode == kPoly ? kKMuonPoly : kKMuonApply;
+    timing_begin(id, s);
+    muon_gemm_kernel<kMode><<<a.tiles < sms ? a.tiles : sms, kThreads, kSmemBytes, s>>>(a);
+    timing_end(id, s);
+    return cudaGetLastError();
+}
+
+// One pass over the list: kItems matrices a launch.
+template <typename Blocks, typename Launch>
+cudaError_t pass(const std::vector<Item>& items, PassArgs& a, Blocks blocks_of, Launch launch) {
+    for (size_t i = 0; i < items.size(); i += kItems) {
+        a.n = (int)(items.size() - i < kItems ? items.size() - i : kItems);
+        int blocks = 0;
+        for (int j = 0; j < a.n; ++j) {
+            a.item[j] = items[i + j];
+            a.item[j].block0 = blocks;
+            blocks += blocks_of(items[i + j]);
+        }
+        launch(blocks);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool step, void* workspace, cudaStream_t s) {
+    Plan plan;
+    plan_of(t, n, plan);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    std::vector<Item> items;
+    std::vector<float> start(plan.sizes.size());
+    for (size_t i = 0; i < plan.sizes.size(); ++i) start[i] = (float)exp2(floor(0.5 * log2((double)plan.sizes[i].r)));
+    for (int i = 0; i < n; ++i) {
+        if (plan.of[i] < 0) continue;
+        const rlk_muon_matrix& d = t[i];
+        const Size& z = plan.sizes[plan.of[i]];
+        Item it{};
+        it.p = d.p;
+        it.master = step ? d.master : nullptr;
+        it.g = d.g;
+        it.m = step ? d.m : nullptr;
+        it.x = reinterpret_cast<__half*>(ws + z.x[0]) + (size_t)plan.z[i] * z.r * z.ld;
+        it.part = reinterpret_cast<double*>(ws + plan.part[i]);
+        it.n = d.rows * d.cols;
+        it.chunk = plan.chunk[i];
+        it.rows = (int)d.rows;
+        it.cols = (int)d.cols;
+        it.ld = z.ld;
+        it.parts = plan.parts[i];
+        it.start = start[plan.of[i]];
+        const double rate = (q.lr_dev != nullptr ? 1.0 : q.lr) * d.lr_scale;
+        it.rate = (float)(rate * q.update_rms * sqrt((double)(d.rows > d.cols ? d.rows : d.cols)));
+        it.decay = (float)(rate * d.weight_decay);
+        it.g32 = d.g_dtype == RLK_FP32;
+        items.push_back(it);
+    }
+    if (items.empty()) return cudaSuccess;
+    PassArgs a;
+    a.mu = (float)q.momentum;
+    a.eps = (float)q.eps;
+    a.nesterov = q.nesterov != 0;
+    a.grad_scale = step ? q.grad_scale : nullptr;
+    a.lr_dev = q.lr_dev;
+    auto tiles = [](const Item& it) { return ((it.rows + kSide - 1) / kSide) * ((it.cols + kSide - 1) / kSide); };
+    e = pass(items, a, [](const Item& it) { return it.parts; }, [&](int blocks) {
+        timing_begin(kKMuonMomentum, s);
+        muon_momentum_kernel<<<blocks, kPassThreads, 0, s>>>(a);
+        timing_end(kKMuonMomentum, s);
+    });
+    if (e == cudaSuccess) e = pass(items, a, tiles, [&](int blocks) {
+        timing_begin(kKMuonStart, s);
+        muon_start_kernel<<<blocks, kPassThreads, 0, s>>>(a);
+        timing_end(kKMuonStart, s);
+    });
+    if (e != cudaSuccess) return e;
+    for (size_t g0 = 0; g0 < plan.sizes.size(); g0 += kGroups) {
+        const int ng = (int)(plan.sizes.size() - g0 < kGroups ? plan.sizes.size() - g0 : kGroups);
+        // X as the operand of 128 rows (gram) and of 256 columns (apply), both buffers; A; B
+        CUtensorMap x_rows[kGroups][2], x_cols[kGroups][2], map_a[kGroups], map_b[kGroups];
+        for (int g = 0; g < ng; ++g) {
+            const Size& z = plan.sizes[g0 + g];
+            bool ok = half_map(&map_a[g], ws + z.a, z.r, z.r, z.count, z.ldr, 128) &&
+                      half_map(&map_b[g], ws + z.b, z.r, z.r, z.count, z.ldr, 128);
+            for (int i = 0; i < 2; ++i)
+                ok = ok && half_map(&x_rows[g][i], ws + z.x[i], z.k, z.r, z.count, z.ld, 128) &&
+                     half_map(&x_cols[g][i], ws + z.x[i], z.k, z.r, z.count, z.ld, 64);
+            if (!ok) return cudaErrorInvalidValue;
+        }
+        for (int i = 0; i < q.iterations; ++i) {
+            for (int mode = kGram; mode <= kApply; ++mode) {
+                GemmArgs ga;
+                ga.n = ng;
+                ga.tiles = 0;
+                for (int g = 0; g < ng; ++g) {
+                    const Size& z = plan.sizes[g0 + g];
+                    Group& d = ga.g[g];
+                    auto half = [&](size_t at) { return reinterpret_cast<__half*>(ws + at); };
+                    const float scale = i == 0 ? 1.0f / start[g0 + g] : 1.0f;  // of X, until the first apply
+                    const int blocks = (z.r + kBM - 1) / kBM, p = blocks / 2;
+                    d.rows = z.r;
+                    d.per = p * (p + 1) + (blocks % 2) * (p + 1);
+                    if (mode == kGram) {
+                        d.map_m = d.map_n = x_rows[g][i & 1];
+                        d.add = nullptr;
+                        d.out = half(z.a);
+                        d.by = scale * scale;
+                        d.add_by = 0.0f;
+                        d.steps = (z.k + kBK - 1) / kBK;
+                    } else if (mode == kPoly) {
+                        d.map_m = d.map_n = map_a[g];
+                        d.add = half(z.a);
+                        d.out = half(z.b);
+                        d.by = (float)q.c;
+                        d.add_by = (float)q.b;
+                        d.steps = (z.r + kBK - 1) / kBK;
+                    } else {
+                        d.map_m = map_b[g];
+                        d.map_n = x_cols[g][i & 1];
+                        d.add = half(z.x[i & 1]);
+                        d.out = half(z.x[(i + 1) & 1]);
+                        d.by = scale;
+                        d.add_by = (float)q.a * scale;
+                        d.steps = (z.r + kBK - 1) / kBK;
+                        d.per = blocks * ((z.k + kBN - 1) / kBN);
+                    }
+                    d.cols = mode == kApply ? z.k : z.r;
+                    d.ld_add = d.ld_out = mode == kApply ? z.ld : z.ldr;
+                    d.add_step = d.out_step = (long long)z.r * d.ld_out;
+                    d.tile0 = ga.tiles;
+                    ga.tiles += d.per * z.count;
+                }
+                e = mode == kGram ? launch_product<kGram>(ga, sms, s)
+                                  : mode == kPoly ? launch_product<kPoly>(ga, sms, s) : launch_product<kApply>(ga, sms, s);
+                if (e != cudaSuccess) return e;
+            }
+        }
+    }
+    if (q.iterations % 2 == 1) {
+        size_t k = 0;
+        for (int i = 0; i < n; ++i)
+            if (plan.of[i] >= 0) {
+                const Size& z = plan.sizes[plan.of[i]];
+                items[k++].x = reinterpret_cast<__half*>(ws + z.x[1]) + (size_t)plan.z[i] * z.r * z.ld;
+            }
+    }
+    return pass(items, a, tiles, [&](int blocks) {
+        timing_begin(kKMuonUpdate, s);
+        muon_update_kernel<<<blocks, kPassThreads, 0, s>>>(a);
+        timing_end(kKMuonUpdate, s);
+    });
+}
+
+}  // namespace
+
+// (the lists are vectors: without memory for them the calls fail like one without a device)
+size_t muon_workspace(const rlk_muon_matrix* t, int n) try {
+    Plan p;
+    plan_of(t, n, p);
+    return p.bytes < 256 ? 256 : p.bytes;
+} catch (const std::bad_alloc&) {
+    return 0;
+}
+
+cudaError_t launch_muon(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool step, void* workspace,
+                        cudaStream_t s) try {
+    return run(t, n, q, step, workspace, s);
+} catch (const std::bad_alloc&) {
+    return cudaErrorMemoryAllocation;
+}
+
+int read_and_clear_status_muon(cudaStream_t s) {
+    int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbolAsync(&v, g_status_muon, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess) return -1;
+    if (cudaMemcpyToSymbolAsync(g_status_muon, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess) return -1;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return -1;
+    return v;
+}
+
+}  // namespace rlk

@@ -135,8 +135,9 @@ std::mutex g_dev_mu;
 int g_dev_state[kMaxDevices];  // 0 unknown, 1 ok, 2 wrong arch, 3 fast math, 4 cuda error
 
 int strict_all_units() {
-    const int r[9] = {probe_host_tu(), probe_prologue_tu(), probe_fwd_tu(), probe_bwd_tu(), probe_unfused_tu(),
-                      probe_qkv_tu(), probe_unfused_bwd_tu(), probe_adaln_tu(), probe_adamw_tu()};
+    const int r[11] = {probe_host_tu(), probe_prologue_tu(), probe_fwd_tu(), probe_bwd_tu(), probe_unfused_tu(),
+                      probe_qkv_tu(), probe_unfused_bwd_tu(), probe_adaln_tu(), probe_adamw_tu(),
+                       probe_fp8_tu(), probe_muon_tu()};
     for (int v : r)
         if (v < 0) return -1;
     for (int v : r)
@@ -345,6 +346,21 @@ const OpInfo kOps[] = {
     {"gradient norm and clip factor", "rlk_grad_norm", "fp32 squares, fp64 sum of the chunks, IEEE div/sqrt",
      "16384 elements of a tensor: a thread's squares in order, xor 16..1, warps ascending; the list's chunks: each "
      "1024th in order, xor 16..1 twice"},
+    {"fp8 block quantise", "rlk_fp8_quantize",
+     "power-of-two scales per 128 (or 128 x 128), codes to nearest even, fp32 column sums; no fast math",
+     "column sums: 8 rows in order, 16 such runs ascending, 128-row tiles ascending"},
+    {"fp8 projection", "rlk_fp8_gemm",
+     "e4m3 / e5m2 operands with e8m0 scales per 128, fp32 TMEM accumulators, fp32 sums of the chunks, + bf16 bias, one "
+     "rounding of the output",
+     "K in chunks of 512 (32 per MMA), chunks ascending, for any number of rows"},
+    {"muon", "rlk_muon_step",
+     "fp32 momentum and weights, fp16 operands of the Newton-Schulz products, fp32 TMEM accumulators, symmetric products "
+     "from one triangle",
+     "norm: a thread's squares in order, xor 16..1, warps ascending, chunks each 256th; products: K ascending"},
+    {"newton-schulz orthogonalisation", "rlk_orthogonalize",
+     "fp16 operands of the Newton-Schulz products, fp32 TMEM accumulators, symmetric products from one triangle, one bf16 "
+     "rounding of the output",
+     "norm: a thread's squares in order, xor 16..1, warps ascending, chunks each 256th; products: K ascending"},
 };
 const char* const kKernelNames[kNumKernelIds] = {
     "rope_table_kernel", "prologue_kernel", "attn_fwd_tc_kernel", "bwd_pre_kernel",
@@ -352,7 +368,9 @@ const char* const kKernelNames[kNumKernelIds] = {
     "qk_gemm_kernel", "softmax_kernel", "av_gemm_kernel", "attn_fwd_tc_kernel<shard>", "qkv_gemm_kernel",
     "qkv_gemm_kernel<out_proj>", "qk_gemm_kernel<dp>", "softmax_bwd_kernel", "acc_gemm_kernel<key>",
     "acc_gemm_kernel<query>", "norm_rope_bwd_q_kernel", "adaln_fwd_kernel", "adaln_bwd_kernel", "adaln_fold_kernel",
-    "grad_norm_kernel", "grad_norm_fold_kernel", "adamw_kernel", "adaln_weight_kernel"};
+    "grad_norm_kernel", "grad_norm_fold_kernel", "adamw_kernel", "adaln_weight_kernel", "fp8_quant_kernel", "fp8_fold_kernel",
+    "fp8_gemm_kernel", "muon_momentum_kernel", "muon_start_kernel", "muon_gemm_kernel<gram>", "muon_gemm_kernel<poly>",
+    "muon_gemm_kernel<apply>", "muon_update_kernel"};
 
 struct OpLog {
     std::mutex mu;
@@ -1414,6 +1432,208 @@ rlk_status rlk_grad_norm(const rlk_adamw_tensor* tensors, int32_t n_tensors, flo
     return sc.finish(grad_norm_impl(tensors, n_tensors, pre_scale, max_norm, out, workspace, workspace_bytes, stream));
 }
 
+// ---- projections in 8 bits ----
+size_t rlk_fp8_row_bytes(int64_t k) { return k < 1 ? 0 : (size_t)((k + 15) / 16 * 16); }
+size_t rlk_fp8_scale_row_bytes(int64_t k) { return k < 1 ? 0 : (size_t)(((k + 127) / 128 + 3) / 4 * 4); }
+
+constexpr long long kMaxFp8Rows = (1LL << 31) - 256;
+
+static bool quant_size_ok(int64_t rows, int64_t cols) {
+    return rows >= 0 && rows < kMaxFp8Rows && cols >= 1 && cols <= (1 << 20) && cols % 8 == 0;
+}
+
+size_t rlk_fp8_quant_workspace_bytes(int64_t rows, int64_t cols) {
+    if (!quant_size_ok(rows, cols)) return 0;
+    return (size_t)std::max<int64_t>(1, (rows + 127) / 128) * cols * sizeof(float);
+}
+
+// A call's buffers: no written range may overlap another one.
+struct Ranges {
+    struct Range {
+        uintptr_t lo, hi;
+        bool written;
+    };
+    Range r[RLK_FP8_MAX_ITEMS * 7];
+    int n = 0;
+    void add(const void* p, size_t bytes, bool written) {
+        if (p == nullptr || bytes == 0) return;
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+        r[n++] = Range{lo, lo + bytes, written};
+    }
+    bool disjoint() const {
+        for (int i = 0; i < n; ++i)
+            for (int j = 0; j < i; ++j)
+                if ((r[i].written || r[j].written) && r[i].lo < r[j].hi && r[j].lo < r[i].hi) return false;
+        return true;
+    }
+};
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static rlk_status fp8_quantize_impl(const rlk_fp8_quant* q, int32_t n, void* stream) {
+    if (q == nullptr || n < 1 || n > RLK_FP8_MAX_ITEMS) return RLK_ERR_INVALID_ARG;
+    Ranges ranges;
+    long long tiles = 0;
+    for (int i = 0; i < n; ++i) {
+        const rlk_fp8_quant& e = q[i];
+        if (!quant_size_ok(e.rows, e.cols) || e.x_stride < e.cols || e.x_stride > (1LL << 40) ||
+            (e.x_dtype != RLK_BF16 && e.x_dtype != RLK_FP32) || (e.format != RLK_E4M3 && e.format != RLK_E5M2) ||
+            (e.square != 0 && e.square != 1) || e.reserved != 0 || (e.q == nullptr && e.qt == nullptr) ||
+            (e.q == nullptr) != (e.q_scale == nullptr) || (e.qt == nullptr) != (e.qt_scale == nullptr) ||
+            (e.col_sum == nullptr) != (e.workspace == nullptr))
+            return RLK_ERR_INVALID_ARG;
+        if (e.rows > 0 && e.x == nullptr) return RLK_ERR_INVALID_ARG;
+        const size_t es = e.x_dtype == RLK_FP32 ? 4 : 2;
+        if ((e.x_stride * es) % 16 != 0 || !aligned16(e.x) || !aligned16(e.q) || !aligned16(e.qt) || !aligned16(e.col_sum) ||
+            !aligned16(e.workspace) || !aligned4(e.q_scale) || !aligned4(e.qt_scale))
+            return RLK_ERR_ALIGNMENT;
+        tiles += (e.rows + 127) / 128 * ((e.cols + 127) / 128);
+        ranges.add(e.x, e.rows == 0 ? 0 : ((size_t)(e.rows - 1) * e.x_stride + e.cols) * es, false);
+        ranges.add(e.q, (size_t)e.rows * rlk_fp8_row_bytes(e.cols), true);
+        ranges.add(e.q_scale, (size_t)e.rows * rlk_fp8_scale_row_bytes(e.cols), true);
+        ranges.add(e.qt, (size_t)e.cols * rlk_fp8_row_bytes(e.rows), true);
+        ranges.add(e.qt_scale, (size_t)e.cols * rlk_fp8_scale_row_bytes(e.rows), true);
+        ranges.add(e.col_sum, (size_t)e.cols * 4, true);
+        if (e.col_sum != nullptr) ranges.add(e.workspace, rlk_fp8_quant_workspace_bytes(e.rows, e.cols), true);
+    }
+    if (tiles >= (1LL << 31) || !ranges.disjoint()) return RLK_ERR_INVALID_ARG;
+    const rlk_status st = device_ok(stream);
+    if (st != RLK_OK) return st;
+    return launch_fp8_quant(q, n, static_cast<cudaStream_t>(stream)) == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
+}
+
+rlk_status rlk_fp8_quantize(const rlk_fp8_quant* items, int32_t n_items, void* stream) {
+    OpScope sc(kOpFp8Quant, nullptr);
+    return sc.finish(fp8_quantize_impl(items, n_items, stream));
+}
+
+static rlk_status fp8_gemm_impl(const rlk_fp8_product* p, int32_t n, void* stream) {
+    if (p == nullptr || n < 1 || n > RLK_FP8_MAX_ITEMS) return RLK_ERR_INVALID_ARG;
+    auto format_ok = [](int f) { return f == RLK_E4M3 || f == RLK_E5M2; };
+    Ranges ranges;
+    long long tiles = 0;
+    for (int i = 0; i < n; ++i) {
+        const rlk_fp8_product& e = p[i];
+        if (e.m < 0 || e.m >= kMaxFp8Rows || e.n < 0 || e.n >= kMaxFp8Rows || e.n % 8 != 0 || e.k < 1 || e.k >= kMaxFp8Rows ||
+            e.d_stride < e.n || e.d_stride > (1LL << 40) || !format_ok(e.a_format) || !format_ok(e.b_format) ||
+            (e.d_dtype != RLK_BF16 && e.d_dtype != RLK_FP32) || (e.accumulate != 0 && e.accumulate != 1) ||
+            (e.accumulate == 1 && e.d_dtype != RLK_FP32))
+            return RLK_ERR_INVALID_ARG;
+        if (e.m == 0 || e.n == 0) continue;
+        const rlk_status st = check_ptrs({e.a, e.b, e.d}, {e.bias});
+        if (st != RLK_OK) return st;
+        if (e.a_scale == nullptr || e.b_scale == nullptr) return RLK_ERR_INVALID_ARG;
+        if (!aligned4(e.a_scale) || !aligned4(e.b_scale) || e.d_stride % 8 != 0) return RLK_ERR_ALIGNMENT;
+        tiles += (e.m + 15) / 16 * ((e.n + 127) / 128);
+        const size_t row = rlk_fp8_row_bytes(e.k), srow = rlk_fp8_scale_row_bytes(e.k), es = e.d_dtype == RLK_FP32 ? 4 : 2;
+        ranges.add(e.a, (size_t)e.m * row, false);
+        ranges.add(e.a_scale, (size_t)e.m * srow, false);
+        ranges.add(e.b, (size_t)e.n * row, false);
+        ranges.add(e.b_scale, (size_t)e.n * srow, false);
+        ranges.add(e.bias, (size_t)e.n * 2, false);
+        ranges.add(e.d, ((size_t)(e.m - 1) * e.d_stride + e.n) * es, true);
+    }
+    if (tiles >= (1LL << 31) || !ranges.disjoint()) return RLK_ERR_INVALID_ARG;
+    const rlk_status st = device_ok(stream);
+    if (st != RLK_OK) return st;
+    return launch_fp8_gemm(p, n, static_cast<cudaStream_t>(stream)) == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
+}
+
+rlk_status rlk_fp8_gemm(const rlk_fp8_product* items, int32_t n_items, void* stream) {
+    OpScope sc(kOpFp8Gemm, nullptr);
+    return sc.finish(fp8_gemm_impl(items, n_items, stream));
+}
+
+// ---- Muon ----
+constexpr int kMaxMuonMatrices = 1 << 16;
+constexpr long long kMaxMuonSide = 1 << 16;
+
+static bool muon_sizes_ok(const rlk_muon_matrix* t, int32_t n) {
+    if (n < 0 || n > kMaxMuonMatrices || (n > 0 && t == nullptr)) return false;
+    for (int i = 0; i < n; ++i)
+        if (t[i].rows < 0 || t[i].cols < 0 || t[i].rows > kMaxMuonSide || t[i].cols > kMaxMuonSide ||
+            t[i].rows * t[i].cols >= (1LL << 31))
+            return false;
+    return true;
+}
+
+size_t rlk_muon_workspace_bytes(const rlk_muon_matrix* matrices, int32_t n_matrices) {
+    return muon_sizes_ok(matrices, n_matrices) ? muon_workspace(matrices, n_matrices) : 0;
+}
+
+static rlk_status muon_impl(const rlk_muon_matrix* t, int32_t n, const rlk_muon_args* a, bool step, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    if (a == nullptr || !muon_sizes_ok(t, n)) return RLK_ERR_INVALID_ARG;
+    auto rate_ok = [](double x) { return x >= 0.0 && x < 3.4e38; };
+    if (a->iterations < 1 || a->iterations > 32 || !std::isfinite(a->a) || !std::isfinite(a->b) || !std::isfinite(a->c) ||
+        std::fabs(a->a) > 1e6 || std::fabs(a->b) > 1e6 || std::fabs(a->c) > 1e6 || !(a->eps >= 0x1p-126) || !(a->eps <= 1.0))
+        return RLK_ERR_INVALID_ARG;
+    if (step) {
+        if (!rate_ok(a->lr) || !(a->momentum >= 0.0 && a->momentum < 1.0) || !rate_ok(a->update_rms) ||
+            (a->nesterov != 0 && a->nesterov != 1))
+            return RLK_ERR_INVALID_ARG;
+        if (!aligned4(a->lr_dev) || !aligned4(a->grad_scale)) return RLK_ERR_ALIGNMENT;
+    }
+    struct Range {
+        uintptr_t lo, hi;
+        bool written;
+    };
+    std::unique_ptr<Range[]> r(new (std::nothrow) Range[(size_t)n * 4 + 1]);
+    if (!r) return RLK_ERR_CUDA;
+    size_t k = 0;
+    auto add = [&](const void* p, size_t bytes, bool written) {
+        if (p != nullptr) r[k++] = Range{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, written};
+    };
+    for (int i = 0; i < n; ++i) {
+        const rlk_muon_matrix& e = t[i];
+        if (e.reserved != 0 || (e.g_dtype != RLK_BF16 && e.g_dtype != RLK_FP32)) return RLK_ERR_INVALID_ARG;
+        if (step) {
+            const double rate = (a->lr_dev != nullptr ? 1.0 : a->lr) * e.lr_scale;
+            if (!rate_ok(e.lr_scale) || !rate_ok(e.weight_decay) || !rate_ok(rate) || !rate_ok(rate * e.weight_decay) ||
+                !rate_ok(rate * a->update_rms * 256.0))
+                return RLK_ERR_INVALID_ARG;
+        }
+        const size_t c = (size_t)(e.rows * e.cols);
+        if (c == 0) continue;
+        if (step ? e.m == nullptr : (e.m != nullptr || e.master != nullptr)) return RLK_ERR_INVALID_ARG;
+        const rlk_status st = check_ptrs({e.p, e.g}, {e.master, e.m});
+        if (st != RLK_OK) return st;
+        add(e.p, c * (!step || e.master != nullptr ? 2 : 4), true);
+        add(e.master, c * 4, true);
+        add(e.m, c * 4, true);
+        add(e.g, c * (e.g_dtype == RLK_FP32 ? 4 : 2), false);
+    }
+    if (k == 0) return RLK_OK;
+    rlk_status st = check_ptrs({workspace}, {});
+    if (st != RLK_OK) return st;
+    const size_t need = muon_workspace(t, n);
+    if (need == 0) return RLK_ERR_CUDA;
+    if (workspace_bytes < need) return RLK_ERR_WORKSPACE;
+    add(workspace, need, true);
+    std::sort(r.get(), r.get() + k, [](const Range& x, const Range& y) { return x.lo < y.lo; });
+    uintptr_t any = 0, written = 0;
+    for (size_t i = 0; i < k; ++i) {
+        if (r[i].lo < (r[i].written ? any : written)) return RLK_ERR_INVALID_ARG;
+        any = std::max(any, r[i].hi);
+        if (r[i].written) written = std::max(written, r[i].hi);
+    }
+    st = device_ok(stream);
+    if (st != RLK_OK) return st;
+    return launch_muon(t, n, *a, step, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
+}
+
+rlk_status rlk_muon_step(const rlk_muon_matrix* matrices, int32_t n_matrices, const rlk_muon_args* args, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    OpScope sc(kOpMuon, nullptr);
+    return sc.finish(muon_impl(matrices, n_matrices, args, true, workspace, workspace_bytes, stream));
+}
+
+rlk_status rlk_orthogonalize(const rlk_muon_matrix* matrices, int32_t n_matrices, const rlk_muon_args* args,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+    OpScope sc(kOpOrthogonalize, nullptr);
+    return sc.finish(muon_impl(matrices, n_matrices, args, false, workspace, workspace_bytes, stream));
+}
+
 rlk_status rlk_joint_attn_check_status(void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (cudaStreamSynchronize(s) != cudaSuccess) return RLK_ERR_CUDA;
@@ -1423,8 +1643,10 @@ rlk_status rlk_joint_attn_check_status(void* stream) {
     const int d = read_and_clear_status_qkv(s);
     const int e = read_and_clear_status_prologue(s);
     const int f = read_and_clear_status_unfused_bwd(s);
-    if (a < 0 || b < 0 || c < 0 || d < 0 || e < 0 || f < 0) return RLK_ERR_CUDA;
-    if (a != 0 || b != 0 || c != 0 || d != 0 || e != 0 || f != 0) return RLK_ERR_DEVICE_TIMEOUT;
+    const int g = read_and_clear_status_fp8(s);
+    const int h = read_and_clear_status_muon(s);
+    if (a < 0 || b < 0 || c < 0 || d < 0 || e < 0 || f < 0 || g < 0 || h < 0) return RLK_ERR_CUDA;
+    if (a != 0 || b != 0 || c != 0 || d != 0 || e != 0 || f != 0 || g != 0 || h != 0) return RLK_ERR_DEVICE_TIMEOUT;
     return RLK_OK;
 }
 

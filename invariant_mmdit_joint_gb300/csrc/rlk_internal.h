@@ -94,7 +94,9 @@ enum KernelId {
     kKQkGemm = 8, kKSoftmax = 9, kKAvGemm = 10, kKAttnFwdShard = 11, kKQkvGemm = 12, kKOutGemm = 13,
     kKDpGemm = 14, kKSoftmaxBwd = 15, kKKeyGemm = 16, kKQueryGemm = 17, kKNormRopeBwdQ = 18,
     kKAdalnFwd = 19, kKAdalnBwd = 20, kKAdalnFold = 21, kKGradNorm = 22, kKGradNormFold = 23, kKAdamw = 24,
-    kKAdalnWeight = 25, kNumKernelIds = 26
+    kKAdalnWeight = 25,
+    kKFp8Quant = 26, kKFp8Fold = 27, kKFp8Gemm = 28, kKMuonMomentum = 29, kKMuonStart = 30, kKMuonGram = 31,
+    kKMuonPoly = 32, kKMuonApply = 33, kKMuonUpdate = 34, kNumKernelIds = 35
 };
 
 // Launch timing hooks (rlk_host.cu): bracket one launch with events.
@@ -109,7 +111,8 @@ enum OpKind {
     kOpFwd = 0, kOpBwd, kOpFwdNoalloc, kOpNormRope, kOpQkGemm, kOpSoftmax, kOpAvGemm, kOpFwdShard,
     kOpFwdStreams, kOpBwdStreams, kOpQkvGemm, kOpFwdCtx, kOpOutGemm,
     kOpBwdStats, kOpSoftmaxBwd, kOpAvGemmBwd, kOpQkGemmBwd, kOpNormRopeBwd,
-    kOpAdalnModFwd, kOpAdalnModBwd, kOpAdalnGateFwd, kOpAdalnGateBwd, kOpAdamw, kOpGradNorm
+    kOpAdalnModFwd, kOpAdalnModBwd, kOpAdalnGateFwd, kOpAdalnGateBwd, kOpAdamw, kOpGradNorm,
+    kOpFp8Quant, kOpFp8Gemm, kOpMuon, kOpOrthogonalize
 };
 class OpScope {
    public:
@@ -281,6 +284,21 @@ cudaError_t launch_grad_norm(const rlk_adamw_tensor* t, int n, float pre, float 
                              cudaStream_t s);
 cudaError_t launch_adamw(const rlk_adamw_tensor* t, int n, const rlk_adamw_args& a, cudaStream_t s);
 int probe_adamw_tu(void);
+
+// k_fp8.cu: codes with block scales and their products (checked arguments)
+constexpr int kFp8MaxItems = RLK_FP8_MAX_ITEMS;
+cudaError_t launch_fp8_quant(const rlk_fp8_quant* q, int n, cudaStream_t s);
+cudaError_t launch_fp8_gemm(const rlk_fp8_product* p, int n, cudaStream_t s);
+int probe_fp8_tu(void);
+int read_and_clear_status_fp8(cudaStream_t s);
+
+// k_muon.cu: the optimiser step for matrices, or (step false) their orthogonal
+// factors alone (checked arguments)
+size_t muon_workspace(const rlk_muon_matrix* t, int n);
+cudaError_t launch_muon(const rlk_muon_matrix* t, int n, const rlk_muon_args& a, bool step, void* workspace,
+                        cudaStream_t s);
+int probe_muon_tu(void);
+int read_and_clear_status_muon(cudaStream_t s);
 
 // Tile geometry of the attention kernels (reported by the trace record).
 extern const int kFwdBlockQ, kFwdBlockKV;
