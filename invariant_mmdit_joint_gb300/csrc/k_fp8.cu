@@ -13,8 +13,8 @@
 //
 // fp8_quant_kernel: one CTA per 128 x 128 tile of x, read once; writes the codes
 // of its rows' blocks, of its columns' blocks (the transposed operand that a sum
-// over rows needs), or both, and the columns' sums (a bias gradient). Bound by
-// HBM.
+// over rows needs), or both, and the columns' sums (a bias gradient).
+// fp8_quant_rows_kernel: the rows' blocks alone. Both bound by HBM.
 //
 // fp8_gemm_kernel: tcgen05.mma kind::mxf8f6f4 with block scales. The features
 // (b's rows) are the 128 rows of an accumulator, the tokens (a's rows) its
@@ -31,6 +31,8 @@
 #include "rlk_sm100.cuh"
 #include "rlk_tmap.h"
 
+#include <atomic>
+
 RLK_DEFINE_STRICT_PROBE(probe_fp8_tu)
 
 namespace rlk {
@@ -40,7 +42,8 @@ using namespace sm100;
 
 // ------------------------------------------------------------------ quantise
 constexpr int kTile = 128;          // rows and columns of a quantise CTA
-constexpr int kQuantThreads = 256;  // 16 row groups of 8 x 16 column groups of 8
+constexpr int kQuantThreads = 256;  // 16 row groups x 16 column groups of 8
+constexpr int kRowsTile = 64;       // rows of a CTA of the kernel for blocks along rows alone
 
 struct QuantItem {
     const void* x;
@@ -49,7 +52,7 @@ struct QuantItem {
     long long x_stride;
     int rows, cols, ldq, lds, ldqt, ldst;
     int col_tiles, tile0;  // tiles of the item: tile0 + row tile * col_tiles + column tile
-    bool fp32, square, e5m2;
+    bool square;
 };
 struct QuantArgs {
     QuantItem item[kFp8MaxItems];
@@ -78,6 +81,114 @@ __device__ __forceinline__ uint2 code8(const float (&v)[8]) {
                       code2<kE5m2>(v[4], v[5]) | code2<kE5m2>(v[6], v[7]) << 16);
 }
 
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {  // of magnitudes; passes over NaN
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+// Eight neighbouring values of a row as they are stored: 16 bytes of bf16, 32 of fp32.
+template <bool kFp32>
+struct Eight {
+    uint32_t w[kFp32 ? 8 : 4];
+    __device__ __forceinline__ void load(const void* x, long long at) {
+        if (kFp32) {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(x) + at);
+            const uint4 a = __ldg(p), b = __ldg(p + 1);
+            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+            w[kFp32 ? 4 : 0] = b.x, w[kFp32 ? 5 : 1] = b.y, w[kFp32 ? 6 : 2] = b.z, w[kFp32 ? 7 : 3] = b.w;
+        } else {
+            const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at));
+            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (uint32_t& k : w) k = 0;
+    }
+    __device__ __forceinline__ float get(int j) const {
+        return kFp32 ? __uint_as_float(w[kFp32 ? j : 0]) : (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+    }
+    // Largest magnitude but for NaN. An infinity takes the code of NaN and no part in its block's scale: it is made
+    // a NaN here, before anything else looks at it.
+    __device__ __forceinline__ float top() {
+        float m = top_once();
+        if (m == INFINITY) {
+            if (kFp32) {
+#pragma unroll
+                for (uint32_t& k : w)
+                    if ((k & 0x7fffffffu) == 0x7f800000u) k = 0x7fffffffu;
+            } else {
+#pragma unroll
+                for (uint32_t& k : w) {
+                    if ((k & 0x7fffu) == 0x7f80u) k |= 0x7fffu;
+                    if ((k & 0x7fff0000u) == 0x7f800000u) k |= 0x7fff0000u;
+                }
+            }
+            m = top_once();
+        }
+        return m;
+    }
+
+   private:
+    __device__ __forceinline__ float top_once() const {
+        if (kFp32) {
+            float m = 0.0f;
+#pragma unroll
+            for (const uint32_t k : w) m = fmaxf(m, fabsf(__uint_as_float(k)));
+            return m;
+        }
+        uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+        for (int k = 1; k < 4; ++k) m = max_bf16x2(m, w[k] & 0x7fff7fffu);
+        return fmaxf(fmaxf(bf16_lo(m), bf16_hi(m)), 0.0f);
+    }
+};
+
+template <bool kFp32, bool kE5m2>
+__device__ __forceinline__ uint2 codes_of(const Eight<kFp32>& v, float s) {
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = v.get(j) * s;
+    return code8<kE5m2>(y);
+}
+
+__device__ __forceinline__ const QuantItem& item_of(const QuantArgs& a, int& tile) {
+    int i = 0;
+    while (i + 1 < a.n && (int)blockIdx.x >= a.item[i + 1].tile0) ++i;
+    tile = blockIdx.x - a.item[i].tile0;
+    return a.item[i];
+}
+
+// Blocks along the rows alone: 16 lanes a block, four rows a thread, no shared memory (8704 rows of 2560: FIGURE_ROWS).
+template <bool kFp32, bool kE5m2>
+__global__ void __launch_bounds__(kQuantThreads) fp8_quant_rows_kernel(const __grid_constant__ QuantArgs a) {
+    constexpr int kRoom = kE5m2 ? 15 : 8, kRows = kRowsTile / 16;
+    int tile;
+    const QuantItem& it = item_of(a, tile);
+    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
+    const int r0 = (tile / it.col_tiles) * kRowsTile + rg, block = tile % it.col_tiles, col = block * kTile + 8 * cg;
+    Eight<kFp32> v[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        if (r0 + 16 * i < it.rows && col < it.cols)
+            v[i].load(it.x, (long long)(r0 + 16 * i) * it.x_stride + col);
+        else
+            v[i].clear();
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        float m = v[i].top();
+#pragma unroll
+        for (int k = 8; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+        const int row = r0 + 16 * i, e = scale_exponent(m, kRoom);
+        if (row < it.rows) {
+            if (col < it.cols)
+                *reinterpret_cast<uint2*>(it.q + (long long)row * it.ldq + col) = codes_of<kFp32, kE5m2>(v[i], power_of_two(-e));
+            if (cg == 0) it.q_scale[(long long)row * it.lds + block] = (uint8_t)(e + 127);
+        }
+    }
+}
+
 struct QuantSmem {
     float row_top[kTile];
     float col[16][kTile];  // the row groups' column maxima, then their column sums
@@ -85,75 +196,77 @@ struct QuantSmem {
     uint8_t t[kTile * kTile];  // codes of columns: 128 bytes a column, 8-byte chunk g at g ^ (column / 8)
 };
 
-template <bool kE5m2>
-__device__ void quant_tile(const QuantItem& it, int tile, QuantSmem& sm) {
+// Blocks along the columns (and along the rows, or of 128 x 128), column sums: a 128 x 128 tile a CTA, eight rows of
+// eight columns a thread, kept as they were loaded (8704 x 2560 both ways: FIGURE_TILE).
+template <bool kFp32, bool kE5m2>
+__global__ void __launch_bounds__(kQuantThreads) fp8_quant_kernel(const __grid_constant__ QuantArgs a) {
+    __shared__ __align__(16) QuantSmem sm;
+    constexpr int kRoom = kE5m2 ? 15 : 8;
+    int tile;
+    const QuantItem& it = item_of(a, tile);
     const int tid = threadIdx.x, lane = tid & 31;
     const int cg = tid & 15, rg = tid >> 4;
     const int r0 = (tile / it.col_tiles) * kTile, c0 = (tile % it.col_tiles) * kTile;
     const int col = c0 + 8 * cg;
-    constexpr int kRoom = kE5m2 ? 15 : 8;
-    float v[8][8];
-    const bool col_live = col < it.cols;
+    const bool col_live = col < it.cols, sums = it.part != nullptr;
+    Eight<kFp32> v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int row = r0 + 8 * rg + i;
-        if (row < it.rows && col_live) {
-            const long long at = (long long)row * it.x_stride + col;
-            if (it.fp32) {
-                const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(it.x) + at);
-                const float4 a = __ldg(p), b = __ldg(p + 1);
-                v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
-                v[i][4] = b.x, v[i][5] = b.y, v[i][6] = b.z, v[i][7] = b.w;
-            } else {
-                const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(it.x) + at));
-                const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[i][2 * k] = bf16_lo(w[k]), v[i][2 * k + 1] = bf16_hi(w[k]);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-        }
+        if (row < it.rows && col_live)
+            v[i].load(it.x, (long long)row * it.x_stride + col);
+        else
+            v[i].clear();
     }
-    const bool sums = it.part != nullptr;
     float sum[8];
     if (sums) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            sum[j] = v[0][j];
+            sum[j] = v[0].get(j);
 #pragma unroll
-            for (int i = 1; i < 8; ++i) sum[j] += v[i][j];
+            for (int i = 1; i < 8; ++i) sum[j] += v[i].get(j);
         }
     }
-    // an infinity takes the code of NaN and no part in its block's scale (fmaxf passes over NaN)
-    float top = 0.0f;
+    float tops[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8; ++i) tops[i] = v[i].top();
+    // rows over their 16 lanes, halves traded: lane k of a group ends with row k / 2
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[i][j]));
-    if (top == INFINITY) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (fabsf(v[i][j]) == INFINITY) v[i][j] = __uint_as_float(0x7fffffffu);
+    for (int i = 0; i < 4; ++i) {
+        const bool up = lane & 8;
+        const float give = up ? tops[i] : tops[i + 4], keep = up ? tops[i + 4] : tops[i];
+        tops[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, 8));
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float m = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[i][j]));
-#pragma unroll
-        for (int k = 8; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-        if ((lane & 15) == i) sm.row_top[8 * rg + i] = m;
+    for (int i = 0; i < 2; ++i) {
+        const bool up = lane & 4;
+        const float give = up ? tops[i] : tops[i + 2], keep = up ? tops[i + 2] : tops[i];
+        tops[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, 4));
     }
-    if (it.qt != nullptr) {
+    {
+        const bool up = lane & 2;
+        const float give = up ? tops[0] : tops[1], keep = up ? tops[1] : tops[0];
+        tops[0] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, 2));
+        tops[0] = fmaxf(tops[0], __shfl_xor_sync(0xffffffffu, tops[0], 1));
+    }
+    if ((lane & 1) == 0) sm.row_top[8 * rg + ((lane & 15) >> 1)] = tops[0];
+    if (!it.square) {
+        if (kFp32) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float m = 0.0f;
+            for (int j = 0; j < 8; ++j) {
+                float m = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i][j]));
-            sm.col[rg][8 * cg + j] = m;
+                for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i].get(j)));
+                sm.col[rg][8 * cg + j] = m;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t m = 0;  // (zero magnitudes: NaN never stays)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m = max_bf16x2(m, v[i].w[k] & 0x7fff7fffu);
+                *reinterpret_cast<float2*>(&sm.col[rg][8 * cg + 2 * k]) = make_float2(bf16_lo(m), bf16_hi(m));
+            }
         }
     }
     __syncthreads();
@@ -165,7 +278,7 @@ __device__ void quant_tile(const QuantItem& it, int tile, QuantSmem& sm) {
             __syncwarp();
             for (int k = 0; k < 4; ++k) sm.row_top[lane + 32 * k] = sm.col_top[lane + 32 * k] = m;
         }
-    } else if (it.qt != nullptr && tid < kTile) {
+    } else if (tid < kTile) {
         float m = sm.col[0][tid];
 #pragma unroll
         for (int k = 1; k < 16; ++k) m = fmaxf(m, sm.col[k][tid]);
@@ -181,10 +294,8 @@ __device__ void quant_tile(const QuantItem& it, int tile, QuantSmem& sm) {
         for (int i = 0; i < 8; ++i) {
             const int row = r0 + 8 * rg + i;
             const float s = power_of_two(-scale_exponent(sm.row_top[8 * rg + i], kRoom));
-            float y[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = v[i][j] * s;
-            if (row < it.rows && col_live) *reinterpret_cast<uint2*>(it.q + (long long)row * it.ldq + col) = code8<kE5m2>(y);
+            if (row < it.rows && col_live)
+                *reinterpret_cast<uint2*>(it.q + (long long)row * it.ldq + col) = codes_of<kFp32, kE5m2>(v[i], s);
         }
         if (tid < kTile && r0 + tid < it.rows)
             it.q_scale[(long long)(r0 + tid) * it.lds + c0 / kTile] = (uint8_t)(scale_exponent(sm.row_top[tid], kRoom) + 127);
@@ -195,7 +306,7 @@ __device__ void quant_tile(const QuantItem& it, int tile, QuantSmem& sm) {
             const float s = power_of_two(-scale_exponent(sm.col_top[8 * cg + j], kRoom));
             float y[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = v[i][j] * s;
+            for (int i = 0; i < 8; ++i) y[i] = v[i].get(j) * s;
             *reinterpret_cast<uint2*>(sm.t + (8 * cg + j) * kTile + ((rg ^ cg) << 3)) = code8<kE5m2>(y);
         }
         if (tid < kTile && c0 + tid < it.cols)
@@ -219,17 +330,6 @@ __device__ void quant_tile(const QuantItem& it, int tile, QuantSmem& sm) {
         for (int k = 1; k < 16; ++k) a += sm.col[k][tid];
         it.part[(long long)(r0 / kTile) * it.cols + c0 + tid] = a;
     }
-}
-
-__global__ void __launch_bounds__(kQuantThreads) fp8_quant_kernel(const __grid_constant__ QuantArgs a) {
-    __shared__ __align__(16) QuantSmem sm;
-    int i = 0;
-    while (i + 1 < a.n && (int)blockIdx.x >= a.item[i + 1].tile0) ++i;
-    const QuantItem& it = a.item[i];
-    if (it.e5m2)
-        quant_tile<true>(it, blockIdx.x - it.tile0, sm);
-    else
-        quant_tile<false>(it, blockIdx.x - it.tile0, sm);
 }
 
 struct FoldItem {
@@ -280,7 +380,7 @@ template <int NT>
 struct Cfg {
     static constexpr int kAtoms = (NT + 127) / 128;           // 128-row scale atoms of the tokens
     static constexpr int kStageBytes = kFBytes + NT * kBK;
-    static constexpr int kStages = NT >= 200 ? 4 : 8;
+    static constexpr int kStages = 8;
     static constexpr int kScaleBytes = 512 * (1 + kAtoms);    // one chunk's scales
     static constexpr int kSmemBytes = kStages * kStageBytes + kScaleRing * kScaleBytes + 1024;
     static constexpr int kHalf = NT >= 32 ? NT / 2 : NT;      // columns of an epilogue warp
@@ -319,9 +419,21 @@ __device__ __forceinline__ void mma_mx(uint32_t d_tmem, uint64_t a_desc, uint64_
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
         : "memory");
 }
+__device__ __forceinline__ void mma_mx_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sa,
+                                            uint32_t sb, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
 // 32 rows of 16 bytes from shared memory to 4 TMEM columns, repeated in every lane quarter.
 __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t sdesc) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t sdesc) {  // in both CTAs
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -376,6 +488,33 @@ __device__ __forceinline__ void store_tile(const GemmItem& it, const float (&acc
         const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
         if (live && t + j + odd < it.m) *reinterpret_cast<uint32_t*>(d) = odd ? pack_bf16(got, v1) : pack_bf16(v0, got);
         d += 2 * it.d_stride;
+    }
+}
+
+// A lane's four rows' scale words of atom i (0 features, then tokens) from block kb on.
+__device__ __forceinline__ void gather_scales(uint32_t (&w)[4], const GemmItem& g, int i, const TileAt& at, int kb, int lane) {
+    const int r0 = i == 0 ? at.f0 : at.t0 + 128 * (i - 1), rows = i == 0 ? g.n : g.m;
+    const uint8_t* p = i == 0 ? g.sf : g.st;
+    const int ld = i == 0 ? g.ldsf : g.ldst;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int r = r0 + 32 * c + lane;
+        w[c] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(p + (long long)r * ld + kb)) : 0x7f7f7f7fu;
+    }
+}
+__device__ __forceinline__ void put_scales(uint32_t dst, const uint32_t (&w)[4]) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+}
+// A chunk's sums from TMEM, added to those of the chunks before.
+template <int kHalf>
+__device__ __forceinline__ void add_chunk(float (&acc)[kHalf], uint32_t taddr, bool first) {
+#pragma unroll
+    for (int c = 0; c < kHalf; c += 16) {
+        uint32_t r[16];
+        tmem_ld16(taddr + c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[c + i] = first ? __uint_as_float(r[i]) : acc[c + i] + __uint_as_float(r[i]);
     }
 }
 
@@ -503,25 +642,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                 const uint32_t use = chunk / kScaleRing;
                 uint32_t w[1 + C::kAtoms][4];
 #pragma unroll
-                for (int i = 0; i < 1 + C::kAtoms; ++i) {
-                    const int r0 = i == 0 ? at.f0 : at.t0 + 128 * (i - 1), rows = i == 0 ? g.n : g.m;
-                    const uint8_t* p = i == 0 ? g.sf : g.st;
-                    const int ld = i == 0 ? g.ldsf : g.ldst;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int r = r0 + 32 * c + lane;
-                        w[i][c] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(p + (long long)r * ld + kb)) : 0x7f7f7f7fu;
-                    }
-                }
+                for (int i = 0; i < 1 + C::kAtoms; ++i) gather_scales(w[i], g, i, at, kb, lane);
                 if (use > 0 && !warp_wait(bar_sempty + 8 * ring, (use - 1) & 1, &abort_flag)) {
                     ok = false;
                     break;
                 }
 #pragma unroll
-                for (int i = 0; i < 1 + C::kAtoms; ++i)
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(scales(ring) + 512 * i + 16 * lane),
-                                 "r"(w[i][0]), "r"(w[i][1]), "r"(w[i][2]), "r"(w[i][3])
-                                 : "memory");
+                for (int i = 0; i < 1 + C::kAtoms; ++i) put_scales(scales(ring) + 512 * i + 16 * lane, w[i]);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_sfull + 8 * ring);
@@ -545,17 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                     break;
                 }
                 tc_fence_after();
-                if (!idle) {
-#pragma unroll
-                    for (int c = 0; c < C::kHalf; c += 16) {
-                        uint32_t r[16];
-                        tmem_ld16(at0 + buf * C::kAccCol + c, r);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            acc[c + i] = kb == 0 ? __uint_as_float(r[i]) : acc[c + i] + __uint_as_float(r[i]);
-                    }
-                }
+                if (!idle) add_chunk<C::kHalf>(acc, at0 + buf * C::kAccCol, kb == 0);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_free + 8 * buf);
@@ -571,6 +688,236 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+}
+
+// ---- the wide product: CTA pairs ----
+constexpr int kPairTokens = 224;  // columns of the accumulator: two of them and the scales fill TMEM
+struct Pair {
+    static constexpr int kTBytes = kPairTokens / 2 * kBK;  // a CTA's half of the tokens
+    static constexpr int kStageBytes = kFBytes + kTBytes;
+    static constexpr int kStages = 6;
+    static constexpr int kAtoms = 2, kScaleBytes = 512 * (1 + kAtoms);
+    static constexpr int kSmemBytes = kStages * kStageBytes + kScaleRing * kScaleBytes + 1024;
+    static constexpr int kHalf = kPairTokens / 2, kScaleCol = 2 * kPairTokens;
+    static_assert(kStageBytes % 1024 == 0 && kTBytes % 1024 == 0 && kScaleCol + 32 <= 512, "");
+};
+
+// 256 features x 224 tokens a cluster of two CTAs: each has 128 features' codes and half of the tokens', so that a
+// product reads half the tokens' bytes from each SM's shared memory. The first CTA issues; both load, and both read
+// out their 128 features.
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gemm_pair_kernel(const __grid_constant__ GemmArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * Pair::kStages + 2 * kScaleRing + 5];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int abort_flag;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    auto stage_f = [&](int st) { return sbase + st * Pair::kStageBytes; };
+    auto stage_t = [&](int st) { return sbase + st * Pair::kStageBytes + kFBytes; };
+    auto scales = [&](int g) { return sbase + Pair::kStages * Pair::kStageBytes + g * Pair::kScaleBytes; };
+    // of these the first CTA waits on its own full, sfull and free, both on theirs of the others
+    const uint32_t bar_full = smem_u32(&bars[0]), bar_empty = bar_full + 8 * Pair::kStages;
+    const uint32_t bar_sfull = bar_empty + 8 * Pair::kStages, bar_sempty = bar_sfull + 8 * kScaleRing;
+    const uint32_t bar_acc = bar_sempty + 8 * kScaleRing, bar_free = bar_acc + 16, bar_drain = bar_free + 16;
+
+    if (tid == 0) {
+        abort_flag = 0;
+        for (int i = 0; i < Pair::kStages; ++i) mbar_init(bar_full + 8 * i, 1), mbar_init(bar_empty + 8 * i, 1);
+        for (int i = 0; i < kScaleRing; ++i) mbar_init(bar_sfull + 8 * i, 2), mbar_init(bar_sempty + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(bar_acc + 8 * i, 1), mbar_init(bar_free + 8 * i, 16);
+        mbar_init(bar_drain, 1);
+        fence_barrier_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc_pair(smem_u32(&tmem_slot), kTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    auto tile = [&](int t) {
+        TileAt r;
+        r.item = 0;
+        while (r.item + 1 < a.n && t >= a.item[r.item + 1].tile0) ++r.item;
+        const int l = t - a.item[r.item].tile0;
+        r.f0 = (l % a.item[r.item].tiles_f) * 256 + 128 * rank;
+        r.t0 = (l / a.item[r.item].tiles_f) * kPairTokens;
+        return r;
+    };
+
+    if (warp == kWarpTma) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = first; ok && t < a.tiles; t += step) {
+                const TileAt at = tile(t);
+                const GemmItem& g = a.item[at.item];
+                for (int kb = 0; kb < g.blocks; ++kb, ++it) {
+                    const int st = it % Pair::kStages;
+                    const uint32_t use = it / Pair::kStages;
+                    if (use > 0 && !mbar_wait(bar_empty + 8 * st, (use - 1) & 1, &abort_flag, kWaitLimitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    // (the bytes of both CTAs; the second one's may be counted before this)
+                    if (rank == 0) mbar_expect_tx(bar_full + 8 * st, 2 * Pair::kStageBytes);
+                    tma_load_2d_pair(stage_f(st), &g.map_f, bar_full + 8 * st, kb * kBK, at.f0);
+                    tma_load_2d_pair(stage_t(st), &g.map_t, bar_full + 8 * st, kb * kBK, at.t0 + Pair::kHalf * rank);
+                }
+            }
+            if (!ok) fail(&abort_flag);
+            // drain: every stage issued here has landed (counted on the first CTA's barriers) or been consumed
+            if (rank == 0) {
+                for (uint32_t u = it < Pair::kStages ? 0 : it - Pair::kStages; u < it; ++u)
+                    mbar_wait_drain(bar_full + 8 * (u % Pair::kStages), (u / Pair::kStages) & 1, kWaitLimitNs);
+            } else if (ok) {
+                for (uint32_t u = it < Pair::kStages ? 0 : it - Pair::kStages; u < it; ++u)
+                    mbar_wait_drain(bar_empty + 8 * (u % Pair::kStages), (u / Pair::kStages) & 1, kWaitLimitNs);
+            }
+        }
+    } else if (warp == kWarpMma) {
+        if (lane == 0 && rank == 0) {
+            uint32_t it = 0, chunk = 0;
+            bool ok = true;
+            for (int t = first; ok && t < a.tiles; t += step) {
+                const GemmItem& g = a.item[tile(t).item];
+                const int blocks = g.blocks;
+                for (int kb = 0; ok && kb < blocks; ++chunk) {
+                    const int buf = chunk & 1, ring = chunk % kScaleRing;
+                    const uint32_t use = chunk >> 1;
+                    if ((use > 0 && !mbar_wait_cluster(bar_free + 8 * buf, (use - 1) & 1, &abort_flag, kWaitLimitNs)) ||
+                        !mbar_wait_cluster(bar_sfull + 8 * ring, (chunk / kScaleRing) & 1, &abort_flag, kWaitLimitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t acc = tmem + buf * kPairTokens;
+                    const uint32_t sa = tmem + Pair::kScaleCol + buf * 16, sb = sa + 4;
+#pragma unroll
+                    for (int i = 0; i < 1 + Pair::kAtoms; ++i)
+                        tmem_copy_scales_pair(sa + 4 * i, sdesc_noswizzle(scales(ring) + 512 * i, 0, 128));
+                    const int end = min(kb + kChunkBlocks, blocks);
+                    uint32_t id = g.idesc;
+                    for (uint32_t more = 0; kb < end; ++kb, ++it) {
+                        const int st = it % Pair::kStages;
+                        if (!mbar_wait_cluster(bar_full + 8 * st, (it / Pair::kStages) & 1, &abort_flag, kWaitLimitNs)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll
+                        for (int j = 0; j < kBK / 32; ++j) {
+                            mma_mx_pair(acc, sdesc_sw128(stage_f(st) + 32 * j, 16, 1024), sdesc_sw128(stage_t(st) + 32 * j, 16, 1024),
+                                        id, sa, sb, more);
+                            more = 1;
+                        }
+                        mma_commit_pair(bar_empty + 8 * st);
+                        id += (1u << 29) | (1u << 4);
+                    }
+                    if (ok) {
+                        mma_commit_pair(bar_sempty + 8 * ring);
+                        mma_commit_pair(bar_acc + 8 * buf);
+                    }
+                }
+            }
+            if (!ok) fail(&abort_flag);
+            mma_commit_pair(bar_drain);
+        }
+        if (lane == 0) mbar_wait_drain(bar_drain, 0, kWaitLimitNs);  // (in both: the last thing that arrives here)
+    } else if (warp == kWarpScale) {
+        uint32_t chunk = 0;
+        bool ok = true;
+        for (int t = first; ok && t < a.tiles; t += step) {
+            const TileAt at = tile(t);
+            const GemmItem& g = a.item[at.item];
+            for (int kb = 0; kb < g.blocks; kb += kChunkBlocks, ++chunk) {
+                const int ring = chunk % kScaleRing;
+                const uint32_t use = chunk / kScaleRing;
+                uint32_t w[1 + Pair::kAtoms][4];
+#pragma unroll
+                for (int i = 0; i < 1 + Pair::kAtoms; ++i) gather_scales(w[i], g, i, at, kb, lane);
+                if (use > 0 && !warp_wait(bar_sempty + 8 * ring, (use - 1) & 1, &abort_flag)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int i = 0; i < 1 + Pair::kAtoms; ++i) put_scales(scales(ring) + 512 * i + 16 * lane, w[i]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_rank(bar_sfull + 8 * ring, 0));
+            }
+        }
+        if (!ok && lane == 0) fail(&abort_flag);
+    } else if (warp >= kWarpEpilogue) {
+        const int quarter = warp & 3, half = (warp - kWarpEpilogue) >> 2;
+        const uint32_t at0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * Pair::kHalf;
+        uint32_t chunk = 0;
+        bool ok = true;
+        for (int t = first; ok && t < a.tiles; t += step) {
+            const TileAt at = tile(t);
+            const GemmItem& g = a.item[at.item];
+            float acc[Pair::kHalf];
+            for (int kb = 0; kb < g.blocks; kb += kChunkBlocks, ++chunk) {
+                const int buf = chunk & 1;
+                if (!warp_wait(bar_acc + 8 * buf, (chunk >> 1) & 1, &abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                add_chunk<Pair::kHalf>(acc, at0 + buf * kPairTokens, kb == 0);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_rank(bar_free + 8 * buf, 0));
+            }
+            if (ok) store_tile<Pair::kHalf>(g, acc, at.f0 + 32 * quarter + lane, at.t0 + half * Pair::kHalf);
+        }
+        if (!ok && lane == 0) fail(&abort_flag);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // the other CTA's products, commits and arrivals reach this one's memory until here
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+cudaError_t launch_pair(GemmArgs& a, int sms, cudaStream_t s) {
+    a.tiles = 0;
+    for (int i = 0; i < a.n; ++i) {
+        GemmItem& g = a.item[i];
+        g.tiles_f = (g.n + 255) / 256;
+        g.tile0 = a.tiles;
+        g.idesc |= idesc_mx(256, kPairTokens);
+        a.tiles += g.tiles_f * ((g.m + kPairTokens - 1) / kPairTokens);
+    }
+    cudaError_t e = cudaFuncSetAttribute(fp8_gemm_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Pair::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    // clusters that fit at once: more would wait for the first to end
+    static std::atomic<int> fit[64];
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    int pairs = dev < 64 ? fit[dev].load() : 0;
+    if (pairs == 0) {
+        cudaLaunchConfig_t c{};
+        c.gridDim = dim3(2 * (sms / 2));
+        c.blockDim = dim3(kThreads);
+        c.dynamicSmemBytes = Pair::kSmemBytes;
+        if ((e = cudaOccupancyMaxActiveClusters(&pairs, fp8_gemm_pair_kernel, &c)) != cudaSuccess) return e;
+        if (pairs < 1) return cudaErrorLaunchOutOfResources;
+        if (dev < 64) fit[dev].store(pairs);
+    }
+    timing_begin(kKFp8Gemm, s);
+    fp8_gemm_pair_kernel<<<2 * (a.tiles < pairs ? a.tiles : pairs), kThreads, Pair::kSmemBytes, s>>>(a);
+    timing_end(kKFp8Gemm, s);
+    return cudaGetLastError();
 }
 
 template <int NT>
@@ -601,20 +948,21 @@ bool codes_map(CUtensorMap* m, const void* base, long long rows, long long k, lo
 
 }  // namespace
 
-long long fp8_quant_tiles(long long rows, long long cols) { return ((rows + 127) / 128) * ((cols + 127) / 128); }
+// fp32 input 1, e5m2 2, blocks along the rows alone 4
+static int quant_kind(const rlk_fp8_quant& e) {
+    return (e.x_dtype == RLK_FP32 ? 1 : 0) | (e.format == RLK_E5M2 ? 2 : 0) |
+           (e.qt == nullptr && e.square == 0 && e.col_sum == nullptr ? 4 : 0);
+}
 
-cudaError_t launch_fp8_quant(const rlk_fp8_quant* q, int n, cudaStream_t s) {
+// The items of one kind (input type, format, rows alone or a tile's work) in one launch.
+static cudaError_t launch_quant_kind(const rlk_fp8_quant* q, int n, int kind, cudaStream_t s) {
     QuantArgs a;
-    FoldArgs f;
-    a.n = f.n = 0;
-    int tiles = 0, blocks = 0;
+    a.n = 0;
+    int tiles = 0;
+    const bool fp32 = kind & 1, e5m2 = kind & 2, rows_alone = kind & 4;
     for (int i = 0; i < n; ++i) {
         const rlk_fp8_quant& e = q[i];
-        if (e.col_sum != nullptr) {
-            f.item[f.n++] = FoldItem{static_cast<const float*>(e.workspace), e.col_sum, (int)((e.rows + 127) / 128), (int)e.cols, blocks};
-            blocks += ((int)e.cols + kFoldThreads - 1) / kFoldThreads;
-        }
-        if (e.rows == 0) continue;
+        if (e.rows == 0 || kind != quant_kind(e)) continue;
         QuantItem& it = a.item[a.n++];
         it.x = e.x;
         it.q = static_cast<uint8_t*>(e.q);
@@ -631,18 +979,37 @@ cudaError_t launch_fp8_quant(const rlk_fp8_quant* q, int n, cudaStream_t s) {
         it.ldst = (int)rlk_fp8_scale_row_bytes(e.rows);
         it.col_tiles = (int)((e.cols + 127) / 128);
         it.tile0 = tiles;
-        it.fp32 = e.x_dtype == RLK_FP32;
         it.square = e.square != 0;
-        it.e5m2 = e.format == RLK_E5M2;
-        tiles += (int)fp8_quant_tiles(e.rows, e.cols);
+        const long long tall = rows_alone ? kRowsTile : kTile;
+        tiles += (int)((e.rows + tall - 1) / tall) * it.col_tiles;
+    }
+    if (tiles == 0) return cudaSuccess;
+    void (*const kernel)(QuantArgs) =
+        rows_alone ? (fp32 ? (e5m2 ? fp8_quant_rows_kernel<true, true> : fp8_quant_rows_kernel<true, false>)
+                           : (e5m2 ? fp8_quant_rows_kernel<false, true> : fp8_quant_rows_kernel<false, false>))
+                   : (fp32 ? (e5m2 ? fp8_quant_kernel<true, true> : fp8_quant_kernel<true, false>)
+                           : (e5m2 ? fp8_quant_kernel<false, true> : fp8_quant_kernel<false, false>));
+    timing_begin(kKFp8Quant, s);
+    kernel<<<tiles, kQuantThreads, 0, s>>>(a);
+    timing_end(kKFp8Quant, s);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_fp8_quant(const rlk_fp8_quant* q, int n, cudaStream_t s) {
+    FoldArgs f;
+    f.n = 0;
+    int blocks = 0;
+    unsigned kinds = 0;
+    for (int i = 0; i < n; ++i) {
+        const rlk_fp8_quant& e = q[i];
+        if (e.rows > 0) kinds |= 1u << quant_kind(e);
+        if (e.col_sum == nullptr) continue;
+        f.item[f.n++] = FoldItem{static_cast<const float*>(e.workspace), e.col_sum, (int)((e.rows + 127) / 128), (int)e.cols, blocks};
+        blocks += ((int)e.cols + kFoldThreads - 1) / kFoldThreads;
     }
     cudaError_t e = cudaSuccess;
-    if (tiles > 0) {
-        timing_begin(kKFp8Quant, s);
-        fp8_quant_kernel<<<tiles, kQuantThreads, 0, s>>>(a);
-        timing_end(kKFp8Quant, s);
-        e = cudaGetLastError();
-    }
+    for (int kind = 0; kind < 8 && e == cudaSuccess; ++kind)
+        if (kinds >> kind & 1) e = launch_quant_kind(q, n, kind, s);
     if (e != cudaSuccess || blocks == 0) return e;
     timing_begin(kKFp8Fold, s);
     fp8_fold_kernel<<<blocks, kFoldThreads, 0, s>>>(f);
@@ -656,13 +1023,13 @@ cudaError_t launch_fp8_gemm(const rlk_fp8_product* p, int n, cudaStream_t s) {
     long long most = 0;
     for (int i = 0; i < n; ++i) most = most < p[i].m ? p[i].m : most;
     // The accumulator's columns: the narrowest that takes every token, else 224.
-    const int nt = most <= 16 ? 16 : most <= 64 ? 64 : 224;
+    const int nt = most <= 16 ? 16 : most <= 64 ? 64 : kPairTokens;
     for (int i = 0; i < n; ++i) {
         const rlk_fp8_product& e = p[i];
         if (e.m == 0 || e.n == 0) continue;
         GemmItem& g = a.item[a.n++];
         const long long ld = rlk_fp8_row_bytes(e.k);
-        if (!codes_map(&g.map_f, e.b, e.n, e.k, ld, 128) || !codes_map(&g.map_t, e.a, e.m, e.k, ld, nt))
+        if (!codes_map(&g.map_f, e.b, e.n, e.k, ld, 128) || !codes_map(&g.map_t, e.a, e.m, e.k, ld, nt == kPairTokens ? nt / 2 : nt))
             return cudaErrorInvalidValue;
         g.sf = e.b_scale;
         g.st = e.a_scale;
@@ -683,7 +1050,7 @@ cudaError_t launch_fp8_gemm(const rlk_fp8_product* p, int n, cudaStream_t s) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    return nt == 16 ? launch_nt<16>(a, sms, s) : nt == 64 ? launch_nt<64>(a, sms, s) : launch_nt<224>(a, sms, s);
+    return nt == 16 ? launch_nt<16>(a, sms, s) : nt == 64 ? launch_nt<64>(a, sms, s) : launch_pair(a, sms, s);
 }
 
 int read_and_clear_status_fp8(cudaStream_t s) {

@@ -27,6 +27,7 @@
 #include <cuda_fp16.h>
 #include <math.h>
 #include <new>
+#include <type_traits>
 #include <vector>
 
 RLK_DEFINE_STRICT_PROBE(probe_muon_tu)
@@ -39,7 +40,7 @@ using namespace sm100;
 // ------------------------------------------------------------------ elementwise passes
 constexpr int kItems = 40;          // matrices a launch of an elementwise pass takes (its argument: 4 KB)
 constexpr int kPassThreads = 256;
-constexpr int kMaxPartials = 1024;  // partial sums of squares of a matrix
+constexpr int kMaxPartials = 256;   // partial sums of squares of a matrix (each CTA of the start adds them)
 constexpr int kMinChunk = 8192;     // elements a partial sums, at least
 constexpr int kSide = 64;           // the passes' tiles
 
@@ -69,8 +70,39 @@ __device__ __forceinline__ const Item& item_of(const PassArgs& a) {
     while (i + 1 < a.n && (int)blockIdx.x >= a.item[i + 1].block0) ++i;
     return a.item[i];
 }
-__device__ __forceinline__ float element(const void* g, bool fp32, long long i) {
-    return fp32 ? static_cast<const float*>(g)[i] : __uint_as_float((uint32_t)static_cast<const uint16_t*>(g)[i] << 16);
+// Eight neighbouring values from i on, those from `live` on zeros; kVec: all there and 16-byte aligned.
+template <bool kVec>
+__device__ __forceinline__ void load8(float (&v)[8], const void* g, bool fp32, long long i, int live) {
+    if (kVec) {
+        if (fp32) {
+            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(g) + i);
+            const float4 a = p[0], b = p[1];
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+            const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g) + i);
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[2 * k] = bf16_lo(w[k]), v[2 * k + 1] = bf16_hi(w[k]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        v[k] = k >= live ? 0.0f
+               : fp32    ? static_cast<const float*>(g)[i + k]
+                         : __uint_as_float((uint32_t)static_cast<const uint16_t*>(g)[i + k] << 16);
+}
+template <bool kVec>
+__device__ __forceinline__ void store8(float* p, long long i, const float (&v)[8], int live) {
+    if (kVec) {
+        float4* q = reinterpret_cast<float4*>(p + i);
+        q[0] = make_float4(v[0], v[1], v[2], v[3]);
+        q[1] = make_float4(v[4], v[5], v[6], v[7]);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (k < live) p[i + k] = v[k];
 }
 // The factor of the gradients; false: it is not finite and the tensors stay as they are.
 __device__ __forceinline__ bool factor_of(const PassArgs& a, float& f) {
@@ -90,8 +122,8 @@ __device__ __forceinline__ double block_sum(double v) {
     return v;
 }
 
-// New momentum, and the partial sums of u's squares: a chunk of consecutive elements a CTA, a thread's squares in
-// fp32 (at most 32 + its share of a long chunk), then fp64.
+// New momentum, and the partial sums of u's squares: a chunk of consecutive elements a CTA, eight neighbours a thread
+// and turn in fp32, the turns in fp64.
 __global__ void __launch_bounds__(kPassThreads) muon_momentum_kernel(const __grid_constant__ PassArgs a) {
     const Item& it = item_of(a);
     float f;
@@ -99,91 +131,169 @@ __global__ void __launch_bounds__(kPassThreads) muon_momentum_kernel(const __gri
     const int chunk = blockIdx.x - it.block0;
     const long long lo = chunk * it.chunk, hi = min(lo + it.chunk, it.n);
     double sum = 0.0;
-    for (long long i0 = lo; i0 < hi; i0 += 4 * kPassThreads) {
+    auto eight = [&](auto vec, long long i, int live) {
+        constexpr bool kVec = decltype(vec)::value;
+        float u[8];
+        load8<kVec>(u, it.g, it.g32, i, live);
+        if (it.m != nullptr) {
+            float m[8];
+            load8<kVec>(m, it.m, true, i, live);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float g = u[k] * f;
+                m[k] = fmaf(a.mu, m[k], g);
+                u[k] = a.nesterov ? fmaf(a.mu, m[k], g) : m[k];
+            }
+            store8<kVec>(it.m, i, m, live);
+        }
         float sq = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const long long i = i0 + j * kPassThreads + threadIdx.x;
-            if (i < hi) {
-                float u = element(it.g, it.g32, i);
-                if (it.m != nullptr) {
-                    const float g = u * f, m = fmaf(a.mu, it.m[i], g);
-                    it.m[i] = m;
-                    u = a.nesterov ? fmaf(a.mu, m, g) : m;
-                }
-                sq = fmaf(u, u, sq);
-            }
-        }
+        for (int k = 0; k < 8; ++k) sq = fmaf(u[k], u[k], sq);
         sum += (double)sq;
+    };
+    // (chunks start at multiples of 8 elements: 16-byte aligned)
+#pragma unroll 2
+    for (long long i = lo + 8 * threadIdx.x; i < hi; i += 8 * kPassThreads) {
+        if (i + 8 <= hi)
+            eight(std::true_type{}, i, 8);
+        else
+            eight(std::false_type{}, i, (int)(hi - i));
     }
     sum = block_sum(sum);
     if (threadIdx.x == 0) it.part[chunk] = sum;
 }
 
-// X = u * start / (|u| + eps) in fp16, turned over where the matrix is tall. A 64 x 64 tile a CTA.
+// A 64 x 64 tile of a matrix by 256 threads: thread t has the columns 8 (t % 8) .. of the rows t / 8 and t / 8 + 32.
+struct TileOf {
+    int r0, c0;
+    __device__ __forceinline__ TileOf(const Item& it) {
+        const int tiles_c = (it.cols + kSide - 1) / kSide, t = blockIdx.x - it.block0;
+        r0 = t / tiles_c * kSide;
+        c0 = t % tiles_c * kSide;
+    }
+};
+constexpr int kPitch = kSide + 8;  // halves of a row in shared memory: 16-byte rows of another bank each
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const __half2 h = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// X = u * start / (|u| + eps) in fp16, turned over where the matrix is tall.
 __global__ void __launch_bounds__(kPassThreads) muon_start_kernel(const __grid_constant__ PassArgs a) {
-    __shared__ float tile[kSide][kSide + 1];
+    __shared__ __align__(16) __half tile[kSide * kPitch];
     const Item& it = item_of(a);
     float f;
     const bool ok = factor_of(a, f);
+    const TileOf at(it);
+    const int cc = 8 * (threadIdx.x & 7), c = at.c0 + cc;
+    const bool tall = it.rows > it.cols, vec = it.cols % 8 == 0;
+    float u[2][8];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int r = at.r0 + (threadIdx.x >> 3) + 32 * k, live = !ok || r >= it.rows ? 0 : min(it.cols - c, 8);
+        const long long i = (long long)r * it.cols + c;
+        float m[8];
+        if (live == 8 && vec) {
+            load8<true>(u[k], it.g, it.g32, i, 8);
+            if (it.m != nullptr) load8<true>(m, it.m, true, i, 8);
+        } else {
+            load8<false>(u[k], it.g, it.g32, i, live);
+            if (it.m != nullptr) load8<false>(m, it.m, true, i, live);
+        }
+        if (it.m != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[k][j] = a.nesterov ? fmaf(a.mu, m[j], u[k][j] * f) : m[j];
+        }
+    }
     double sq = 0.0;
     for (int i = threadIdx.x; i < it.parts; i += kPassThreads) sq += it.part[i];
     const float inv = (float)((double)it.start / (sqrt(block_sum(sq)) + (double)a.eps));
-    const int tiles_c = (it.cols + kSide - 1) / kSide, t = blockIdx.x - it.block0;
-    const int r0 = t / tiles_c * kSide, c0 = t % tiles_c * kSide;
-    const int c = threadIdx.x & 63;
-    const bool tall = it.rows > it.cols;
-#pragma unroll 4
-    for (int r = threadIdx.x >> 6; r < kSide; r += kPassThreads / kSide) {
-        float u = 0.0f;
-        if (ok && r0 + r < it.rows && c0 + c < it.cols) {
-            const long long i = (long long)(r0 + r) * it.cols + c0 + c;
-            u = element(it.g, it.g32, i);
-            if (it.m != nullptr) u = a.nesterov ? fmaf(a.mu, it.m[i], u * f) : it.m[i];
-            u *= inv;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int rr = (threadIdx.x >> 3) + 32 * k, r = at.r0 + rr;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[k][j] *= inv;
+        if (tall) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) tile[(cc + j) * kPitch + rr] = __float2half_rn(u[k][j]);
+        } else if (r < it.rows && c < it.cols) {  // (a row's padding takes zeros)
+            *reinterpret_cast<uint4*>(it.x + (long long)r * it.ld + c) = pack8(u[k]);
         }
-        if (tall)
-            tile[r][c] = u;
-        else if (r0 + r < it.rows && c0 + c < it.cols)
-            it.x[(long long)(r0 + r) * it.ld + c0 + c] = __float2half_rn(u);
     }
     if (!tall) return;
     __syncthreads();
-    for (int r = threadIdx.x >> 6; r < kSide; r += kPassThreads / kSide)
-        if (c0 + r < it.cols && r0 + c < it.rows)
-            it.x[(long long)(c0 + r) * it.ld + r0 + c] = __float2half_rn(tile[c][r]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int rr = (threadIdx.x >> 3) + 32 * k, r = at.c0 + rr, col = at.r0 + cc;
+        if (r < it.cols && col < it.rows)
+            *reinterpret_cast<uint4*>(it.x + (long long)r * it.ld + col) = *reinterpret_cast<const uint4*>(tile + rr * kPitch + cc);
+    }
 }
 
-// p -= decay p + rate X, or p = X (orthogonalize). A 64 x 64 tile a CTA.
+// p -= decay p + rate X, or p = X (orthogonalize).
 __global__ void __launch_bounds__(kPassThreads) muon_update_kernel(const __grid_constant__ PassArgs a) {
-    __shared__ float tile[kSide][kSide + 1];
+    __shared__ __align__(16) __half tile[kSide * kPitch];
     const Item& it = item_of(a);
     float f;
     if (!factor_of(a, f)) return;
-    const int tiles_c = (it.cols + kSide - 1) / kSide, t = blockIdx.x - it.block0;
-    const int r0 = t / tiles_c * kSide, c0 = t % tiles_c * kSide;
-    const int c = threadIdx.x & 63;
-    const bool tall = it.rows > it.cols;
+    const TileOf at(it);
+    const int cc = 8 * (threadIdx.x & 7), c = at.c0 + cc;
+    const bool tall = it.rows > it.cols, vec = it.cols % 8 == 0;
     if (tall) {
-#pragma unroll 4
-        for (int r = threadIdx.x >> 6; r < kSide; r += kPassThreads / kSide)
-            tile[r][c] = c0 + r < it.cols && r0 + c < it.rows ? __half2float(it.x[(long long)(c0 + r) * it.ld + r0 + c]) : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int rr = (threadIdx.x >> 3) + 32 * k, r = at.c0 + rr, col = at.r0 + cc;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (r < it.cols && col < it.rows) w = __ldg(reinterpret_cast<const uint4*>(it.x + (long long)r * it.ld + col));
+            const __half* h = reinterpret_cast<const __half*>(&w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) tile[(cc + j) * kPitch + rr] = h[j];
+        }
         __syncthreads();
     }
     const float lr = a.lr_dev != nullptr ? *a.lr_dev : 1.0f;
     const float rate = it.rate * lr, decay = it.decay * lr;
-#pragma unroll 4
-    for (int r = threadIdx.x >> 6; r < kSide; r += kPassThreads / kSide) {
-        if (r0 + r >= it.rows || c0 + c >= it.cols) continue;
-        const long long i = (long long)(r0 + r) * it.cols + c0 + c;
-        const float x = tall ? tile[c][r] : __half2float(it.x[(long long)(r0 + r) * it.ld + c0 + c]);
-        float* w = it.master != nullptr ? it.master : static_cast<float*>(it.p);
-        float v = x;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int rr = (threadIdx.x >> 3) + 32 * k, r = at.r0 + rr, live = r >= it.rows ? 0 : min(it.cols - c, 8);
+        if (live <= 0) continue;
+        const long long i = (long long)r * it.cols + c;
+        const uint4 w = tall ? *reinterpret_cast<const uint4*>(tile + rr * kPitch + cc)
+                             : __ldg(reinterpret_cast<const uint4*>(it.x + (long long)r * it.ld + c));
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __half2float(reinterpret_cast<const __half*>(&w)[j]);
+        const bool all = live == 8 && vec;
         if (it.m != nullptr) {
-            v = w[i] - fmaf(decay, w[i], rate * x);
-            w[i] = v;
+            float* p = it.master != nullptr ? it.master : static_cast<float*>(it.p);
+            float q[8];
+            if (all)
+                load8<true>(q, p, true, i, 8);
+            else
+                load8<false>(q, p, true, i, live);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = q[j] - fmaf(decay, q[j], rate * v[j]);
+            if (all)
+                store8<true>(p, i, v, 8);
+            else
+                store8<false>(p, i, v, live);
         }
-        if (it.m == nullptr || it.master != nullptr) static_cast<__nv_bfloat16*>(it.p)[i] = __float2bfloat16_rn(v);
+        if (it.m != nullptr && it.master == nullptr) continue;
+        uint16_t* b = static_cast<uint16_t*>(it.p) + i;
+        if (all) {
+            *reinterpret_cast<uint4*>(b) =
+                make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < live) b[j] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j]));
+        }
     }
 }
 

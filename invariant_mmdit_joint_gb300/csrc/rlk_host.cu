@@ -1487,7 +1487,7 @@ static rlk_status fp8_quantize_impl(const rlk_fp8_quant* q, int32_t n, void* str
         if ((e.x_stride * es) % 16 != 0 || !aligned16(e.x) || !aligned16(e.q) || !aligned16(e.qt) || !aligned16(e.col_sum) ||
             !aligned16(e.workspace) || !aligned4(e.q_scale) || !aligned4(e.qt_scale))
             return RLK_ERR_ALIGNMENT;
-        tiles += (e.rows + 127) / 128 * ((e.cols + 127) / 128);
+        tiles += (e.rows + 63) / 64 * ((e.cols + 127) / 128);
         ranges.add(e.x, e.rows == 0 ? 0 : ((size_t)(e.rows - 1) * e.x_stride + e.cols) * es, false);
         ranges.add(e.q, (size_t)e.rows * rlk_fp8_row_bytes(e.cols), true);
         ranges.add(e.q_scale, (size_t)e.rows * rlk_fp8_scale_row_bytes(e.cols), true);
