@@ -370,7 +370,7 @@ constexpr int kChunkBlocks = 4; // blocks whose products share an accumulator
 constexpr int kFBytes = 128 * kBK;
 constexpr int kThreads = 384;
 constexpr int kWarpTma = 0, kWarpMma = 1, kWarpScale = 2, kWarpEpilogue = 4;
-constexpr int kScaleRing = 3;
+constexpr int kScaleRing = 6;  // chunks whose scales are at hand: gathering one takes longer than its products
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -505,11 +505,19 @@ __device__ __forceinline__ void gather_scales(uint32_t (&w)[4], const GemmItem& 
 __device__ __forceinline__ void put_scales(uint32_t dst, const uint32_t (&w)[4]) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
 }
-// A chunk's sums from TMEM, added to those of the chunks before.
+// A chunk's sums from TMEM, added to those of the chunks before: 32 columns a wait, the last 16 by themselves.
 template <int kHalf>
 __device__ __forceinline__ void add_chunk(float (&acc)[kHalf], uint32_t taddr, bool first) {
 #pragma unroll
-    for (int c = 0; c < kHalf; c += 16) {
+    for (int c = 0; c + 32 <= kHalf; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(taddr + c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[c + i] = first ? __uint_as_float(r[i]) : acc[c + i] + __uint_as_float(r[i]);
+    }
+    if (kHalf % 32 != 0) {
+        constexpr int c = kHalf / 32 * 32;
         uint32_t r[16];
         tmem_ld16(taddr + c, r);
         tmem_ld_wait();
@@ -783,45 +791,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gem
         }
     } else if (warp == kWarpMma) {
         if (lane == 0 && rank == 0) {
-            uint32_t it = 0, chunk = 0;
+            // (the issuing thread has about a hundred cycles a product: descriptors are sums of what is at hand)
+            const uint64_t f0 = sdesc_sw128(stage_f(0), 16, 1024), t0 = sdesc_sw128(stage_t(0), 16, 1024);
+            const uint64_t s0 = sdesc_noswizzle(scales(0), 0, 128);
+            uint32_t chunks = 0;  // of all tiles
+            for (int t = first; t < a.tiles; t += step) chunks += (a.item[tile(t).item].blocks + kChunkBlocks - 1) / kChunkBlocks;
+            uint32_t st = 0, phase = 0, chunk = 0;
             bool ok = true;
+            auto copy_scales = [&](uint32_t c) {  // a chunk's, one chunk ahead of its products
+                const uint32_t ring = c % kScaleRing;
+                if (!mbar_wait_cluster(bar_sfull + 8 * ring, (c / kScaleRing) & 1, &abort_flag, kWaitLimitNs)) return false;
+                tc_fence_after();
+                const uint32_t sa = tmem + Pair::kScaleCol + (c & 1) * 16;
+#pragma unroll
+                for (int i = 0; i < 1 + Pair::kAtoms; ++i)
+                    tmem_copy_scales_pair(sa + 4 * i, s0 + ((ring * Pair::kScaleBytes + 512 * i) >> 4));
+                return true;
+            };
+            if (chunks > 0) ok = copy_scales(0);
             for (int t = first; ok && t < a.tiles; t += step) {
                 const GemmItem& g = a.item[tile(t).item];
                 const int blocks = g.blocks;
                 for (int kb = 0; ok && kb < blocks; ++chunk) {
-                    const int buf = chunk & 1, ring = chunk % kScaleRing;
+                    const int buf = chunk & 1;
                     const uint32_t use = chunk >> 1;
-                    if ((use > 0 && !mbar_wait_cluster(bar_free + 8 * buf, (use - 1) & 1, &abort_flag, kWaitLimitNs)) ||
-                        !mbar_wait_cluster(bar_sfull + 8 * ring, (chunk / kScaleRing) & 1, &abort_flag, kWaitLimitNs)) {
+                    if (use > 0 && !mbar_wait_cluster(bar_free + 8 * buf, (use - 1) & 1, &abort_flag, kWaitLimitNs)) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
                     const uint32_t acc = tmem + buf * kPairTokens;
                     const uint32_t sa = tmem + Pair::kScaleCol + buf * 16, sb = sa + 4;
-#pragma unroll
-                    for (int i = 0; i < 1 + Pair::kAtoms; ++i)
-                        tmem_copy_scales_pair(sa + 4 * i, sdesc_noswizzle(scales(ring) + 512 * i, 0, 128));
-                    const int end = min(kb + kChunkBlocks, blocks);
+                    const int start = kb, end = min(kb + kChunkBlocks, blocks);
                     uint32_t id = g.idesc;
-                    for (uint32_t more = 0; kb < end; ++kb, ++it) {
-                        const int st = it % Pair::kStages;
-                        if (!mbar_wait_cluster(bar_full + 8 * st, (it / Pair::kStages) & 1, &abort_flag, kWaitLimitNs)) {
+                    for (; kb < end; ++kb) {
+                        if (!mbar_wait(bar_full + 8 * st, phase, &abort_flag, kWaitLimitNs)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
+                        const uint64_t f = f0 + st * (Pair::kStageBytes >> 4), tk = t0 + st * (Pair::kStageBytes >> 4);
 #pragma unroll
-                        for (int j = 0; j < kBK / 32; ++j) {
-                            mma_mx_pair(acc, sdesc_sw128(stage_f(st) + 32 * j, 16, 1024), sdesc_sw128(stage_t(st) + 32 * j, 16, 1024),
-                                        id, sa, sb, more);
-                            more = 1;
-                        }
+                        for (int j = 0; j < kBK / 32; ++j)
+                            mma_mx_pair(acc, f + 2 * j, tk + 2 * j, id, sa, sb, j > 0 || kb > start ? 1u : 0u);
                         mma_commit_pair(bar_empty + 8 * st);
-                        id += (1u << 29) | (1u << 4);
+                        if (++st == Pair::kStages) st = 0, phase ^= 1;
+                        id += (1u << 29) | (1u << 4);  // the next block's scale bytes
+                        if (kb == start && chunk + 1 < chunks && !copy_scales(chunk + 1)) {
+                            ok = false;
+                            break;
+                        }
                     }
                     if (ok) {
-                        mma_commit_pair(bar_sempty + 8 * ring);
+                        mma_commit_pair(bar_sempty + 8 * (chunk % kScaleRing));
                         mma_commit_pair(bar_acc + 8 * buf);
                     }
                 }
