@@ -702,12 +702,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
 constexpr int kPairTokens = 224;  // columns of the accumulator: two of them and the scales fill TMEM
 struct Pair {
     static constexpr int kTBytes = kPairTokens / 2 * kBK;  // a CTA's half of the tokens
-    static constexpr int kStageBytes = kFBytes + kTBytes;
-    static constexpr int kStages = 6;
+    static constexpr int kBlockBytes = kFBytes + kTBytes;
+    static constexpr int kStageBlocks = 2;  // scale blocks of a stage: a wait and a commit for eight products
+    static constexpr int kStageBytes = kStageBlocks * kBlockBytes;
+    static constexpr int kStages = 3;
     static constexpr int kAtoms = 2, kScaleBytes = 512 * (1 + kAtoms);
     static constexpr int kSmemBytes = kStages * kStageBytes + kScaleRing * kScaleBytes + 1024;
     static constexpr int kHalf = kPairTokens / 2, kScaleCol = 2 * kPairTokens;
-    static_assert(kStageBytes % 1024 == 0 && kTBytes % 1024 == 0 && kScaleCol + 32 <= 512, "");
+    static_assert(kBlockBytes % 1024 == 0 && kTBytes % 1024 == 0 && kScaleCol + 32 <= 512 && kChunkBlocks % kStageBlocks == 0, "");
 };
 
 // 256 features x 224 tokens a cluster of two CTAs: each has 128 features' codes and half of the tokens', so that a
@@ -766,7 +768,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gem
             for (int t = first; ok && t < a.tiles; t += step) {
                 const TileAt at = tile(t);
                 const GemmItem& g = a.item[at.item];
-                for (int kb = 0; kb < g.blocks; ++kb, ++it) {
+                for (int kb = 0; kb < g.blocks; kb += Pair::kStageBlocks, ++it) {
                     const int st = it % Pair::kStages;
                     const uint32_t use = it / Pair::kStages;
                     if (use > 0 && !mbar_wait(bar_empty + 8 * st, (use - 1) & 1, &abort_flag, kWaitLimitNs)) {
@@ -775,8 +777,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gem
                     }
                     // (the bytes of both CTAs; the second one's may be counted before this)
                     if (rank == 0) mbar_expect_tx(bar_full + 8 * st, 2 * Pair::kStageBytes);
-                    tma_load_2d_pair(stage_f(st), &g.map_f, bar_full + 8 * st, kb * kBK, at.f0);
-                    tma_load_2d_pair(stage_t(st), &g.map_t, bar_full + 8 * st, kb * kBK, at.t0 + Pair::kHalf * rank);
+#pragma unroll
+                    for (int b = 0; b < Pair::kStageBlocks; ++b) {  // (zeros past the row's end)
+                        tma_load_2d_pair(stage_f(st) + b * Pair::kBlockBytes, &g.map_f, bar_full + 8 * st, (kb + b) * kBK, at.f0);
+                        tma_load_2d_pair(stage_t(st) + b * Pair::kBlockBytes, &g.map_t, bar_full + 8 * st, (kb + b) * kBK,
+                                         at.t0 + Pair::kHalf * rank);
+                    }
                 }
             }
             if (!ok) fail(&abort_flag);
@@ -823,20 +829,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gem
                     const uint32_t sa = tmem + Pair::kScaleCol + buf * 16, sb = sa + 4;
                     const int start = kb, end = min(kb + kChunkBlocks, blocks);
                     uint32_t id = g.idesc;
-                    for (; kb < end; ++kb) {
+                    while (kb < end) {
                         if (!mbar_wait(bar_full + 8 * st, phase, &abort_flag, kWaitLimitNs)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
                         const uint64_t f = f0 + st * (Pair::kStageBytes >> 4), tk = t0 + st * (Pair::kStageBytes >> 4);
+                        const bool new_sum = kb == start;
 #pragma unroll
-                        for (int j = 0; j < kBK / 32; ++j)
-                            mma_mx_pair(acc, f + 2 * j, tk + 2 * j, id, sa, sb, j > 0 || kb > start ? 1u : 0u);
+                        for (int b = 0; b < Pair::kStageBlocks; ++b) {
+                            if (b > 0 && kb >= end) break;
+#pragma unroll
+                            for (int j = 0; j < kBK / 32; ++j)
+                                mma_mx_pair(acc, f + ((b * Pair::kBlockBytes) >> 4) + 2 * j, tk + ((b * Pair::kBlockBytes) >> 4) + 2 * j,
+                                            id, sa, sb, b > 0 || j > 0 || !new_sum ? 1u : 0u);
+                            id += (1u << 29) | (1u << 4);  // the next block's scale bytes
+                            ++kb;
+                        }
                         mma_commit_pair(bar_empty + 8 * st);
                         if (++st == Pair::kStages) st = 0, phase ^= 1;
-                        id += (1u << 29) | (1u << 4);  // the next block's scale bytes
-                        if (kb == start && chunk + 1 < chunks && !copy_scales(chunk + 1)) {
+                        if (new_sum && chunk + 1 < chunks && !copy_scales(chunk + 1)) {
                             ok = false;
                             break;
                         }
