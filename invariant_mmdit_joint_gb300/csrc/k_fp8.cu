@@ -451,6 +451,10 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, kWaitLimitNs));
 }
 
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort_flag, kWaitLimitNs));
+}
+
 struct TileAt {
     int item, f0, t0;
 };
@@ -721,7 +725,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gem
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t rank = cluster_rank();
     const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -796,8 +800,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gem
             }
         }
     } else if (warp == kWarpMma) {
-        if (lane == 0 && rank == 0) {
-            // (the issuing thread has about a hundred cycles a product: descriptors are sums of what is at hand)
+        if (rank == 0) {
+            // (the whole warp runs the loop, one lane issues; the issuing thread has about a hundred cycles a product: descriptors are sums of what is at hand)
             const uint64_t f0 = sdesc_sw128(stage_f(0), 16, 1024), t0 = sdesc_sw128(stage_t(0), 16, 1024);
             const uint64_t s0 = sdesc_noswizzle(scales(0), 0, 128);
             uint32_t chunks = 0;  // of all tiles
@@ -806,9 +810,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gem
             bool ok = true;
             auto copy_scales = [&](uint32_t c) {  // a chunk's, one chunk ahead of its products
                 const uint32_t ring = c % kScaleRing;
-                if (!mbar_wait_cluster(bar_sfull + 8 * ring, (c / kScaleRing) & 1, &abort_flag, kWaitLimitNs)) return false;
+                if (!warp_wait_cluster(bar_sfull + 8 * ring, (c / kScaleRing) & 1, &abort_flag)) return false;
                 tc_fence_after();
                 const uint32_t sa = tmem + Pair::kScaleCol + (c & 1) * 16;
+                if (elect_one())
 #pragma unroll
                 for (int i = 0; i < 1 + Pair::kAtoms; ++i)
                     tmem_copy_scales_pair(sa + 4 * i, s0 + ((ring * Pair::kScaleBytes + 512 * i) >> 4));
@@ -821,7 +826,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gem
                 for (int kb = 0; ok && kb < blocks; ++chunk) {
                     const int buf = chunk & 1;
                     const uint32_t use = chunk >> 1;
-                    if (use > 0 && !mbar_wait_cluster(bar_free + 8 * buf, (use - 1) & 1, &abort_flag, kWaitLimitNs)) {
+                    if (use > 0 && !warp_wait_cluster(bar_free + 8 * buf, (use - 1) & 1, &abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -830,38 +835,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gem
                     const int start = kb, end = min(kb + kChunkBlocks, blocks);
                     uint32_t id = g.idesc;
                     while (kb < end) {
-                        if (!mbar_wait(bar_full + 8 * st, phase, &abort_flag, kWaitLimitNs)) {
+                        if (!warp_wait(bar_full + 8 * st, phase, &abort_flag)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
                         const uint64_t f = f0 + st * (Pair::kStageBytes >> 4), tk = t0 + st * (Pair::kStageBytes >> 4);
-                        const bool new_sum = kb == start;
+                        const bool new_sum = kb == start, two = kb + 1 < end;
+                        if (elect_one()) {
 #pragma unroll
-                        for (int b = 0; b < Pair::kStageBlocks; ++b) {
-                            if (b > 0 && kb >= end) break;
+                            for (int b = 0; b < Pair::kStageBlocks; ++b) {
+                                if (b > 0 && !two) break;
 #pragma unroll
-                            for (int j = 0; j < kBK / 32; ++j)
-                                mma_mx_pair(acc, f + ((b * Pair::kBlockBytes) >> 4) + 2 * j, tk + ((b * Pair::kBlockBytes) >> 4) + 2 * j,
-                                            id, sa, sb, b > 0 || j > 0 || !new_sum ? 1u : 0u);
-                            id += (1u << 29) | (1u << 4);  // the next block's scale bytes
-                            ++kb;
+                                for (int j = 0; j < kBK / 32; ++j)  // (each block's scale bytes are one further)
+                                    mma_mx_pair(acc, f + ((b * Pair::kBlockBytes) >> 4) + 2 * j, tk + ((b * Pair::kBlockBytes) >> 4) + 2 * j,
+                                                id + b * ((1u << 29) | (1u << 4)), sa, sb, b > 0 || j > 0 || !new_sum ? 1u : 0u);
+                            }
+                            mma_commit_pair(bar_empty + 8 * st);
                         }
-                        mma_commit_pair(bar_empty + 8 * st);
+                        kb += two ? 2 : 1;
+                        id += 2 * ((1u << 29) | (1u << 4));
                         if (++st == Pair::kStages) st = 0, phase ^= 1;
                         if (new_sum && chunk + 1 < chunks && !copy_scales(chunk + 1)) {
                             ok = false;
                             break;
                         }
                     }
-                    if (ok) {
+                    if (ok && elect_one()) {
                         mma_commit_pair(bar_sempty + 8 * (chunk % kScaleRing));
                         mma_commit_pair(bar_acc + 8 * buf);
                     }
                 }
             }
-            if (!ok) fail(&abort_flag);
-            mma_commit_pair(bar_drain);
+            if (elect_one()) {
+                if (!ok) fail(&abort_flag);
+                mma_commit_pair(bar_drain);
+            }
         }
         if (lane == 0) mbar_wait_drain(bar_drain, 0, kWaitLimitNs);  // (in both: the last thing that arrives here)
     } else if (warp == kWarpScale) {

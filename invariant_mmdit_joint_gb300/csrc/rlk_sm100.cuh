@@ -112,6 +112,15 @@ __device__ __forceinline__ bool mbar_wait_backoff(uint32_t bar, uint32_t parity,
     }
 }
 
+// One lane of a converged warp. Where a whole warp runs an issuing loop and only the instructions themselves stand
+// behind this, the compiler keeps their operands in uniform registers; in a branch of one lane it moves each there
+// anew.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
+}
+
 // ------------------------------------------------------------------ CTA pairs
 // A cluster of two CTAs whose tensor cores work on one product (cta_group::2):
 // the first CTA (rank 0) issues, both have the operands and the accumulator's
