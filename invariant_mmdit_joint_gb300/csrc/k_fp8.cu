@@ -390,7 +390,8 @@ struct Cfg {
 };
 
 struct GemmItem {
-    CUtensorMap map_f, map_t;  // features [n, k], box 128 x 128; tokens [m, k], box 128 x NT
+    CUtensorMap map_f, map_t;  // features [n, k], box 128 x 128; tokens [m, k], box 128 x NT (a pair's CTA: half)
+    CUtensorMap map_d;         // pairs: d [m, n], box of 32 features
     const uint8_t *sf, *st;
     const uint16_t* bias;
     void* d;
@@ -711,10 +712,50 @@ struct Pair {
     static constexpr int kStageBytes = kStageBlocks * kBlockBytes;
     static constexpr int kStages = 3;
     static constexpr int kAtoms = 2, kScaleBytes = 512 * (1 + kAtoms);
-    static constexpr int kSmemBytes = kStages * kStageBytes + kScaleRing * kScaleBytes + 1024;
     static constexpr int kHalf = kPairTokens / 2, kScaleCol = 2 * kPairTokens;
+    static constexpr int kOutTokens = kHalf / 2;           // tokens an epilogue warp hands to TMA at once in bf16
+    static constexpr int kOutBytes = kOutTokens * 32 * 2;  // its buffer; half as many tokens in fp32
+    static constexpr int kSmemBytes = kStages * kStageBytes + kScaleRing * kScaleBytes + 8 * kOutBytes + 1024;
+    static_assert(kOutBytes % 128 == 0 && kOutTokens % 2 == 0 && kSmemBytes <= 227 * 1024, "");
     static_assert(kBlockBytes % 1024 == 0 && kTBytes % 1024 == 0 && kScaleCol + 32 <= 512 && kChunkBlocks % kStageBlocks == 0, "");
 };
+
+// A warp's 32 features (lane: f) over kHalf tokens from t on: + bias, rounded, by way of its buffer in shared memory to
+// TMA, which cuts off what is past the matrix. Each pass waits until the one before it has left the buffer.
+template <bool kFp32>
+__device__ __forceinline__ void store_pair(const GemmItem& g, const float (&acc)[Pair::kHalf], uint32_t buffer, int f, int t) {
+    constexpr int kTokens = kFp32 ? Pair::kOutTokens / 2 : Pair::kOutTokens;
+    const int lane = threadIdx.x & 31, f0 = f - lane;
+    if (f0 >= g.n) return;
+    const float b = f < g.n && g.bias != nullptr ? __uint_as_float((uint32_t)g.bias[f] << 16) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < Pair::kHalf; j += kTokens) {
+        if (t + j >= g.m) break;
+        bulk_wait_read_all();  // (the lane that stored; nothing to wait for in the others)
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kTokens; i += 2) {
+            const float v0 = acc[j + i] + b, v1 = acc[j + i + 1] + b;
+            if (kFp32) {
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(buffer + i * 128 + lane * 4), "f"(v0) : "memory");
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(buffer + i * 128 + 128 + lane * 4), "f"(v1) : "memory");
+            } else {
+                const uint32_t w = pack_bf16(v0, v1);
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(buffer + i * 64 + lane * 2), "h"((uint16_t)w) : "memory");
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(buffer + i * 64 + 64 + lane * 2), "h"((uint16_t)(w >> 16)) : "memory");
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (kFp32 && g.accumulate)
+                tma_add_2d(&g.map_d, buffer, f0, t + j);
+            else
+                tma_store_2d(&g.map_d, buffer, f0, t + j);
+            bulk_commit_group();
+        }
+    }
+}
 
 // 256 features x 224 tokens a cluster of two CTAs: each has 128 features' codes and half of the tokens', so that a
 // product reads half the tokens' bytes from each SM's shared memory. The first CTA issues; both load, and both read
@@ -900,6 +941,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gem
     } else if (warp >= kWarpEpilogue) {
         const int quarter = warp & 3, half = (warp - kWarpEpilogue) >> 2;
         const uint32_t at0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * Pair::kHalf;
+        const uint32_t buffer = scales(kScaleRing) + (warp - kWarpEpilogue) * Pair::kOutBytes;
         uint32_t chunk = 0;
         bool ok = true;
         for (int t = first; ok && t < a.tiles; t += step) {
@@ -918,8 +960,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gem
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(map_rank(bar_free + 8 * buf, 0));
             }
-            if (ok) store_tile<Pair::kHalf>(g, acc, at.f0 + 32 * quarter + lane, at.t0 + half * Pair::kHalf);
+            const int f = at.f0 + 32 * quarter + lane, tk = at.t0 + half * Pair::kHalf;
+            if (ok && g.fp32) store_pair<true>(g, acc, buffer, f, tk);
+            if (ok && !g.fp32) store_pair<false>(g, acc, buffer, f, tk);
         }
+        bulk_wait_all();
         if (!ok && lane == 0) fail(&abort_flag);
     }
 
@@ -1074,6 +1119,15 @@ cudaError_t launch_fp8_gemm(const rlk_fp8_product* p, int n, cudaStream_t s) {
         const long long ld = rlk_fp8_row_bytes(e.k);
         if (!codes_map(&g.map_f, e.b, e.n, e.k, ld, 128) || !codes_map(&g.map_t, e.a, e.m, e.k, ld, nt == kPairTokens ? nt / 2 : nt))
             return cudaErrorInvalidValue;
+        if (nt == kPairTokens) {
+            const bool fp32 = e.d_dtype == RLK_FP32;
+            const cuuint64_t dims[2] = {(cuuint64_t)e.n, (cuuint64_t)e.m};
+            const cuuint64_t strides[1] = {(cuuint64_t)e.d_stride * (fp32 ? 4 : 2)};
+            const cuuint32_t box[2] = {32, (cuuint32_t)(fp32 ? Pair::kOutTokens / 2 : Pair::kOutTokens)};
+            if (!tmap::encode(&g.map_d, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, e.d, dims,
+                              strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+                return cudaErrorInvalidValue;
+        }
         g.sf = e.b_scale;
         g.st = e.a_scale;
         g.bias = static_cast<const uint16_t*>(e.bias);

@@ -1,5 +1,5 @@
 // Host-side TMA tensor-map encoders shared by the attention kernels' launch
-// code. Every map uses the 128-byte swizzle: boxes are 128 rows of 128
+// code. Every map but for encode()'s last argument uses the 128-byte swizzle: boxes are 128 rows of 128
 // bytes, so a shared-memory tile is rows of 128 bytes whose 16-byte chunk c
 // sits at position c ^ (row % 8).
 #pragma once
@@ -28,12 +28,13 @@ inline PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
 }
 
 inline bool encode(CUtensorMap* m, CUtensorMapDataType type, cuuint32_t rank, const void* base,
-                   const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+                   const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                   CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     auto enc = get_encode();
     if (enc == nullptr) return false;
     const cuuint32_t es[5] = {1, 1, 1, 1, 1};
     return enc(m, type, rank, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
