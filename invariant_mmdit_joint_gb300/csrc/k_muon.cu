@@ -302,7 +302,8 @@ enum Mode { kGram = 0, kPoly = 1, kApply = 2 };
 constexpr int kGroups = 8;  // sizes a launch takes
 constexpr int kBM = 128, kBN = 256, kBK = 64, kStages = 4;
 constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2, kStageBytes = kABytes + kBBytes;
-constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+constexpr int kOutBytes = 32 * 32 * 2;  // an epilogue warp's buffer: 32 rows of 32 columns
+constexpr int kSmemBytes = kStages * kStageBytes + 8 * kOutBytes + 1024;
 constexpr int kThreads = 384;
 constexpr int kWarpTma = 0, kWarpMma = 1, kWarpEpilogue = 4;
 constexpr uint32_t kTmemCols = 512;
@@ -313,6 +314,7 @@ __device__ int g_status_muon;
 struct Group {
     CUtensorMap map_m;   // the operand of the 128 rows: [z][rows][K], box 64 x 128 x 1
     CUtensorMap map_n;   // the operand of the 256 columns: gram, poly the same, box 64 x 128; apply X, box 64 x 64 (MN-major)
+    CUtensorMap map_out; // out, box 32 x 32 x 1
     const __half* add;   // poly: A; apply: X: added times `add_by`
     __half* out;
     long long add_step, out_step;  // from matrix to matrix
@@ -371,7 +373,7 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
 // 32 columns from j on of row i (a warp: 32 rows from i - lane): out = by * v + add_by * add, and on the other
 // side of the diagonal.
 template <int kMode>
-__device__ __forceinline__ void store32(const Group& g, int z, float (&v)[32], int i, int j) {
+__device__ __forceinline__ void store32(const Group& g, int z, float (&v)[32], int i, int j, uint32_t buffer) {
     const int lane = threadIdx.x & 31, i0 = i - lane;
     if (kMode != kApply && j > i0) return;  // above the diagonal: stored from the other side
     const bool live = i < g.rows;
@@ -405,11 +407,22 @@ __device__ __forceinline__ void store32(const Group& g, int z, float (&v)[32], i
             }
         return;
     }
+    // the rows through the warp's buffer (64-byte rows, 16-byte chunk c at c ^ (row / 2) % 4) and TMA, which cuts off
+    // what is past the matrix
+    bulk_wait_read_all();
+    __syncwarp();
 #pragma unroll
-    for (int c = 0; c < 32; c += 8)  // (columns up to the padded row's end)
-        if (live && j + c < g.cols)
-            *reinterpret_cast<uint4*>(row + c) = make_uint4(pack_half(v[c], v[c + 1]), pack_half(v[c + 2], v[c + 3]),
-                                                            pack_half(v[c + 4], v[c + 5]), pack_half(v[c + 6], v[c + 7]));
+    for (int c = 0; c < 4; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buffer + 64 * lane + 16 * (c ^ ((lane >> 1) & 3))),
+                     "r"(pack_half(v[8 * c], v[8 * c + 1])), "r"(pack_half(v[8 * c + 2], v[8 * c + 3])),
+                     "r"(pack_half(v[8 * c + 4], v[8 * c + 5])), "r"(pack_half(v[8 * c + 6], v[8 * c + 7]))
+                     : "memory");
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && i0 < g.rows) {
+        tma_store_3d(&g.map_out, buffer, j, i0, z);
+        bulk_commit_group();
+    }
     if (kMode == kApply) return;
     const bool odd = lane & 1;
     __half* col = out + (long long)(j + odd) * g.ld_out + (i & ~1);
@@ -429,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
     auto stage_a = [&](int st) { return sbase + st * kStageBytes; };
     auto stage_b = [&](int st) { return sbase + st * kStageBytes + kABytes; };
@@ -480,41 +493,44 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
                 mbar_wait_drain(bar_full + 8 * (u % kStages), (u / kStages) & 1, kWaitLimitNs);
         }
     } else if (warp == kWarpMma) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_f16(kBM, kBN, kMode == kApply);
-            uint32_t it = 0, local = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; ok && t < a.tiles; t += gridDim.x, ++local) {
-                const int buf = local & 1;
-                const uint32_t use = local >> 1;
-                if (use > 0 && !mbar_wait(bar_free + 8 * buf, (use - 1) & 1, &abort_flag, kWaitLimitNs)) {
+        // the whole warp runs the loop, one lane issues
+        constexpr uint32_t idesc = idesc_f16(kBM, kBN, kMode == kApply);
+        const uint64_t a0 = sdesc_sw128(stage_a(0), 16, 1024);
+        const uint64_t b0 = kMode == kApply ? sdesc_sw128(stage_b(0), 8192, 1024) : sdesc_sw128(stage_b(0), 16, 1024);
+        constexpr int kStepB = (kMode == kApply ? 2048 : 32) >> 4;
+        uint32_t st = 0, phase = 0, local = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < a.tiles; t += gridDim.x, ++local) {
+            const int buf = local & 1;
+            const uint32_t use = local >> 1;
+            if (use > 0 && !warp_wait(bar_free + 8 * buf, (use - 1) & 1, &abort_flag)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t acc = tmem + buf * kBN;
+            const int steps = a.g[tile_at<kMode>(a, t).g].steps;
+            for (int kk = 0; kk < steps; ++kk) {
+                if (!warp_wait(bar_full + 8 * st, phase, &abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t acc = tmem + buf * kBN;
-                const int steps = a.g[tile_at<kMode>(a, t).g].steps;
-                for (int kk = 0; kk < steps; ++kk, ++it) {
-                    const int st = it % kStages;
-                    if (!mbar_wait(bar_full + 8 * st, (it / kStages) & 1, &abort_flag, kWaitLimitNs)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                const uint64_t da = a0 + st * (kStageBytes >> 4), db = b0 + st * (kStageBytes >> 4);
+                if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < kBK / 16; ++j)
-                        mma_ss(acc, sdesc_sw128(stage_a(st) + 32 * j, 16, 1024),
-                               kMode == kApply ? sdesc_sw128(stage_b(st) + 2048 * j, 8192, 1024)
-                                               : sdesc_sw128(stage_b(st) + 32 * j, 16, 1024),
-                               idesc, (kk > 0 || j > 0) ? 1u : 0u);
+                    for (int j = 0; j < kBK / 16; ++j) mma_ss(acc, da + 2 * j, db + kStepB * j, idesc, (kk > 0 || j > 0) ? 1u : 0u);
                     mma_commit(bar_empty + 8 * st);
                 }
-                if (ok) mma_commit(bar_acc + 8 * buf);
+                if (++st == kStages) st = 0, phase ^= 1;
             }
+            if (ok && elect_one()) mma_commit(bar_acc + 8 * buf);
+        }
+        if (elect_one()) {
             if (!ok) fail(&abort_flag);
             mma_commit(bar_drain);
-            mbar_wait_drain(bar_drain, 0, kWaitLimitNs);
         }
+        if (lane == 0) mbar_wait_drain(bar_drain, 0, kWaitLimitNs);
     } else if (warp >= kWarpEpilogue) {
         const int quarter = warp & 3, half = (warp - kWarpEpilogue) >> 2;
         const uint32_t at0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
@@ -539,13 +555,14 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
                 float v[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-                store32<kMode>(g, at.z, v, at.m0 + 32 * quarter + lane, j);
+                store32<kMode>(g, at.z, v, at.m0 + 32 * quarter + lane, j, sbase + kStages * kStageBytes + (warp - kWarpEpilogue) * kOutBytes);
                 __syncwarp();
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_free + 8 * buf);
         }
+        bulk_wait_all();
         if (!ok && lane == 0) fail(&abort_flag);
     }
 
@@ -608,11 +625,12 @@ void plan_of(const rlk_muon_matrix* t, int n, Plan& p) {
     }
 }
 
-bool half_map(CUtensorMap* m, const void* base, int cols, int rows, int count, int ld, int box_rows) {
+bool half_map(CUtensorMap* m, const void* base, int cols, int rows, int count, int ld, int box_rows, bool out = false) {
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)count};
     const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)rows * ld * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
-    return tmap::encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, box);
+    const cuuint32_t box[3] = {out ? 32u : 64u, (cuuint32_t)box_rows, 1};
+    return tmap::encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, box,
+                        out ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int kMode>
@@ -701,14 +719,17 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
     for (size_t g0 = 0; g0 < plan.sizes.size(); g0 += kGroups) {
         const int ng = (int)(plan.sizes.size() - g0 < kGroups ? plan.sizes.size() - g0 : kGroups);
         // X as the operand of 128 rows (gram) and of 256 columns (apply), both buffers; A; B
-        CUtensorMap x_rows[kGroups][2], x_cols[kGroups][2], map_a[kGroups], map_b[kGroups];
+        CUtensorMap x_rows[kGroups][2], x_cols[kGroups][2], x_out[kGroups][2], map_a[kGroups], map_b[kGroups], a_out[kGroups], b_out[kGroups];
         for (int g = 0; g < ng; ++g) {
             const Size& z = plan.sizes[g0 + g];
             bool ok = half_map(&map_a[g], ws + z.a, z.r, z.r, z.count, z.ldr, 128) &&
-                      half_map(&map_b[g], ws + z.b, z.r, z.r, z.count, z.ldr, 128);
+                      half_map(&map_b[g], ws + z.b, z.r, z.r, z.count, z.ldr, 128) &&
+                      half_map(&a_out[g], ws + z.a, z.r, z.r, z.count, z.ldr, 32, true) &&
+                      half_map(&b_out[g], ws + z.b, z.r, z.r, z.count, z.ldr, 32, true);
             for (int i = 0; i < 2; ++i)
                 ok = ok && half_map(&x_rows[g][i], ws + z.x[i], z.k, z.r, z.count, z.ld, 128) &&
-                     half_map(&x_cols[g][i], ws + z.x[i], z.k, z.r, z.count, z.ld, 64);
+                     half_map(&x_cols[g][i], ws + z.x[i], z.k, z.r, z.count, z.ld, 64) &&
+                     half_map(&x_out[g][i], ws + z.x[i], z.k, z.r, z.count, z.ld, 32, true);
             if (!ok) return cudaErrorInvalidValue;
         }
         for (int i = 0; i < q.iterations; ++i) {
@@ -726,6 +747,7 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
                     d.per = p * (p + 1) + (blocks % 2) * (p + 1);
                     if (mode == kGram) {
                         d.map_m = d.map_n = x_rows[g][i & 1];
+                        d.map_out = a_out[g];
                         d.add = nullptr;
                         d.out = half(z.a);
                         d.by = scale * scale;
@@ -733,6 +755,7 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
                         d.steps = (z.k + kBK - 1) / kBK;
                     } else if (mode == kPoly) {
                         d.map_m = d.map_n = map_a[g];
+                        d.map_out = b_out[g];
                         d.add = half(z.a);
                         d.out = half(z.b);
                         d.by = (float)q.c;
@@ -740,6 +763,7 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
                         d.steps = (z.r + kBK - 1) / kBK;
                     } else {
                         d.map_m = map_b[g];
+                        d.map_out = x_out[g][(i + 1) & 1];
                         d.map_n = x_cols[g][i & 1];
                         d.add = half(z.x[i & 1]);
                         d.out = half(z.x[(i + 1) & 1]);
