@@ -673,7 +673,7 @@ typedef struct rlk_fp8_quant {
     uint8_t* q_scale;   /* [rows, ceil(cols / 128)], NULL with q */
     void* qt;           /* [cols, rows] codes, or NULL (one of q and qt is required) */
     uint8_t* qt_scale;  /* [cols, ceil(rows / 128)], NULL with qt */
-    float* col_sum;     /* [cols] or NULL: sums over the rows, 128 rows' sums in ascending order */
+    float* col_sum;     /* [cols] or NULL: sums over the rows, in a fixed order */
     void* workspace;    /* rlk_fp8_quant_workspace_bytes() bytes with col_sum, else NULL */
     int64_t rows, cols, x_stride;
     int32_t x_dtype;    /* RLK_BF16 or RLK_FP32 */

@@ -341,26 +341,27 @@ struct FoldArgs {
     FoldItem item[kFp8MaxItems];
     int n;
 };
-constexpr int kFoldThreads = 128;
+constexpr int kFoldThreads = 256, kFoldCols = 32, kFoldRuns = kFoldThreads / kFoldCols;
 
-// Column sums: the row tiles in ascending order.
+// Column sums: every 8th row tile in ascending order, then these 8 runs.
 __global__ void __launch_bounds__(kFoldThreads) fp8_fold_kernel(const __grid_constant__ FoldArgs a) {
+    __shared__ float sm[kFoldRuns][kFoldCols];
     int i = 0;
     while (i + 1 < a.n && (int)blockIdx.x >= a.item[i + 1].block0) ++i;
     const FoldItem& it = a.item[i];
-    const int c = (blockIdx.x - it.block0) * kFoldThreads + threadIdx.x;
-    if (c >= it.cols) return;
-    const float* p = it.part + c;
+    const int cc = threadIdx.x % kFoldCols, run = threadIdx.x / kFoldCols;
+    const int c = (blockIdx.x - it.block0) * kFoldCols + cc;
     float s = 0.0f;
-    int t = 0;
-    for (; t + 8 <= it.tiles; t += 8) {
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = p[(long long)(t + k) * it.cols];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s += v[k];
+    if (c < it.cols) {
+        const float* p = it.part + c;
+#pragma unroll 4
+        for (int t = run; t < it.tiles; t += kFoldRuns) s += p[(long long)t * it.cols];
     }
-    for (; t < it.tiles; ++t) s += p[(long long)t * it.cols];
+    sm[run][cc] = s;
+    __syncthreads();
+    if (run > 0 || c >= it.cols) return;
+#pragma unroll
+    for (int k = 1; k < kFoldRuns; ++k) s += sm[k][cc];
     it.out[c] = s;
 }
 
@@ -1093,7 +1094,7 @@ cudaError_t launch_fp8_quant(const rlk_fp8_quant* q, int n, cudaStream_t s) {
         if (e.rows > 0) kinds |= 1u << quant_kind(e);
         if (e.col_sum == nullptr) continue;
         f.item[f.n++] = FoldItem{static_cast<const float*>(e.workspace), e.col_sum, (int)((e.rows + 127) / 128), (int)e.cols, blocks};
-        blocks += ((int)e.cols + kFoldThreads - 1) / kFoldThreads;
+        blocks += ((int)e.cols + kFoldCols - 1) / kFoldCols;
     }
     cudaError_t e = cudaSuccess;
     for (int kind = 0; kind < 8 && e == cudaSuccess; ++kind)

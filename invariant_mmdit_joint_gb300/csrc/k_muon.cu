@@ -172,7 +172,9 @@ struct TileOf {
         c0 = t % tiles_c * kSide;
     }
 };
-constexpr int kPitch = kSide + 8;  // halves of a row in shared memory: 16-byte rows of another bank each
+// Where column c (0 .. 63) of row r of a turned tile lies in shared memory: 16-byte chunks exchanged by the row's
+// group of 8, so that threads of eight neighbouring row groups meet other banks.
+__device__ __forceinline__ int turned(int r, int c) { return r * kSide + ((((c >> 3) ^ (r >> 3)) & 7) << 3) + (c & 7); }
 
 __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
     uint32_t w[4];
@@ -186,7 +188,7 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 
 // X = u * start / (|u| + eps) in fp16, turned over where the matrix is tall.
 __global__ void __launch_bounds__(kPassThreads) muon_start_kernel(const __grid_constant__ PassArgs a) {
-    __shared__ __align__(16) __half tile[kSide * kPitch];
+    __shared__ __align__(16) __half tile[kSide * kSide];
     const Item& it = item_of(a);
     float f;
     const bool ok = factor_of(a, f);
@@ -211,9 +213,17 @@ __global__ void __launch_bounds__(kPassThreads) muon_start_kernel(const __grid_c
             for (int j = 0; j < 8; ++j) u[k][j] = a.nesterov ? fmaf(a.mu, m[j], u[k][j] * f) : m[j];
         }
     }
-    double sq = 0.0;
-    for (int i = threadIdx.x; i < it.parts; i += kPassThreads) sq += it.part[i];
-    const float inv = (float)((double)it.start / (sqrt(block_sum(sq)) + (double)a.eps));
+    // (one warp adds: fp64 is slow here; root and quotient in fp32, one rounding each)
+    __shared__ float s_inv;
+    if (threadIdx.x < 32) {
+        double sq = 0.0;
+        for (int i = threadIdx.x; i < it.parts; i += 32) sq += it.part[i];
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, k);
+        if (threadIdx.x == 0) s_inv = it.start / (sqrtf((float)sq) + a.eps);
+    }
+    __syncthreads();
+    const float inv = s_inv;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int rr = (threadIdx.x >> 3) + 32 * k, r = at.r0 + rr;
@@ -221,7 +231,7 @@ __global__ void __launch_bounds__(kPassThreads) muon_start_kernel(const __grid_c
         for (int j = 0; j < 8; ++j) u[k][j] *= inv;
         if (tall) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) tile[(cc + j) * kPitch + rr] = __float2half_rn(u[k][j]);
+            for (int j = 0; j < 8; ++j) tile[turned(cc + j, rr)] = __float2half_rn(u[k][j]);
         } else if (r < it.rows && c < it.cols) {  // (a row's padding takes zeros)
             *reinterpret_cast<uint4*>(it.x + (long long)r * it.ld + c) = pack8(u[k]);
         }
@@ -232,13 +242,13 @@ __global__ void __launch_bounds__(kPassThreads) muon_start_kernel(const __grid_c
     for (int k = 0; k < 2; ++k) {
         const int rr = (threadIdx.x >> 3) + 32 * k, r = at.c0 + rr, col = at.r0 + cc;
         if (r < it.cols && col < it.rows)
-            *reinterpret_cast<uint4*>(it.x + (long long)r * it.ld + col) = *reinterpret_cast<const uint4*>(tile + rr * kPitch + cc);
+            *reinterpret_cast<uint4*>(it.x + (long long)r * it.ld + col) = *reinterpret_cast<const uint4*>(tile + turned(rr, cc));
     }
 }
 
 // p -= decay p + rate X, or p = X (orthogonalize).
 __global__ void __launch_bounds__(kPassThreads) muon_update_kernel(const __grid_constant__ PassArgs a) {
-    __shared__ __align__(16) __half tile[kSide * kPitch];
+    __shared__ __align__(16) __half tile[kSide * kSide];
     const Item& it = item_of(a);
     float f;
     if (!factor_of(a, f)) return;
@@ -253,7 +263,7 @@ __global__ void __launch_bounds__(kPassThreads) muon_update_kernel(const __grid_
             if (r < it.cols && col < it.rows) w = __ldg(reinterpret_cast<const uint4*>(it.x + (long long)r * it.ld + col));
             const __half* h = reinterpret_cast<const __half*>(&w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) tile[(cc + j) * kPitch + rr] = h[j];
+            for (int j = 0; j < 8; ++j) tile[turned(cc + j, rr)] = h[j];
         }
         __syncthreads();
     }
@@ -264,7 +274,7 @@ __global__ void __launch_bounds__(kPassThreads) muon_update_kernel(const __grid_
         const int rr = (threadIdx.x >> 3) + 32 * k, r = at.r0 + rr, live = r >= it.rows ? 0 : min(it.cols - c, 8);
         if (live <= 0) continue;
         const long long i = (long long)r * it.cols + c;
-        const uint4 w = tall ? *reinterpret_cast<const uint4*>(tile + rr * kPitch + cc)
+        const uint4 w = tall ? *reinterpret_cast<const uint4*>(tile + turned(rr, cc))
                              : __ldg(reinterpret_cast<const uint4*>(it.x + (long long)r * it.ld + c));
         float v[8];
 #pragma unroll

@@ -348,7 +348,7 @@ const OpInfo kOps[] = {
      "1024th in order, xor 16..1 twice"},
     {"fp8 block quantise", "rlk_fp8_quantize",
      "power-of-two scales per 128 (or 128 x 128), codes to nearest even, fp32 column sums; no fast math",
-     "column sums: 8 rows in order, 16 such runs ascending, 128-row tiles ascending"},
+     "column sums: 8 rows in order, 16 such runs ascending, every 8th 128-row tile ascending, these 8 runs"},
     {"fp8 projection", "rlk_fp8_gemm",
      "e4m3 / e5m2 operands with e8m0 scales per 128, fp32 TMEM accumulators, fp32 sums of the chunks, + bf16 bias, one "
      "rounding of the output",
@@ -356,11 +356,11 @@ const OpInfo kOps[] = {
     {"muon", "rlk_muon_step",
      "fp32 momentum and weights, fp16 operands of the Newton-Schulz products, fp32 TMEM accumulators, symmetric products "
      "from one triangle",
-     "norm: a thread's squares in order, xor 16..1, warps ascending, chunks each 256th; products: K ascending"},
+     "norm: a thread's squares in order, xor 16..1, warps ascending, chunks each 32nd, xor 16..1; products: K ascending"},
     {"newton-schulz orthogonalisation", "rlk_orthogonalize",
      "fp16 operands of the Newton-Schulz products, fp32 TMEM accumulators, symmetric products from one triangle, one bf16 "
      "rounding of the output",
-     "norm: a thread's squares in order, xor 16..1, warps ascending, chunks each 256th; products: K ascending"},
+     "norm: a thread's squares in order, xor 16..1, warps ascending, chunks each 32nd, xor 16..1; products: K ascending"},
 };
 const char* const kKernelNames[kNumKernelIds] = {
     "rope_table_kernel", "prologue_kernel", "attn_fwd_tc_kernel", "bwd_pre_kernel",
