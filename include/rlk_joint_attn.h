@@ -915,7 +915,7 @@ const char* rlk_strerror(int status);
  * 19 adaln forward, 20 adaln backward, 21 its fold, 22 gradient norm, 23 its
  * fold, 24 AdamW, 25 adaln's weight gradients, 26 fp8 quantise, 27 its column
  * sums' fold, 28 fp8 product, 29 Muon momentum, 30 its start, 31 .. 33 its products
- * (X X^T, the polynomial, B X), 34 its update (14 .. 18: the standalone backward
+ * (X X^T, the polynomial, B X), 34 its update, 35 a small matrix's whole step (14 .. 18: the standalone backward
  * operators).
  * rlk_kernel_timing(1) makes later calls record a CUDA event pair around
  * every launch (up to 4096 launches per kernel id); rlk_kernel_timing(0)

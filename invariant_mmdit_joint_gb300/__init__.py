@@ -59,7 +59,7 @@ KERNEL_IDS = {
     "dp_gemm": 14, "softmax_bwd": 15, "key_gemm": 16, "query_gemm": 17, "norm_rope_bwd_q": 18,
     "adaln_fwd": 19, "adaln_bwd": 20, "adaln_fold": 21, "grad_norm": 22, "grad_norm_fold": 23, "adamw": 24,
     "adaln_weight": 25, "fp8_quant": 26, "fp8_fold": 27, "fp8_gemm": 28, "muon_momentum": 29, "muon_start": 30,
-    "muon_gram": 31, "muon_poly": 32, "muon_apply": 33, "muon_update": 34,
+    "muon_gram": 31, "muon_poly": 32, "muon_apply": 33, "muon_update": 34, "muon_small": 35,
 }
 # which intermediate rlk_joint_attn_unfused_bytes() sizes
 UNFUSED = {"scores": 0, "p": 1, "alpha": 2, "rows": 3, "dp": 4, "ds": 5, "stats": 6, "dhat": 7, "gain_tiles": 8}

@@ -437,14 +437,6 @@ __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t sdesc)
 __device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t sdesc) {  // in both CTAs
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(sdesc) : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-
 __device__ __forceinline__ void fail(volatile int* abort_flag) {
     *abort_flag = 1;
     atomicOr(&g_status_fp8, 1);

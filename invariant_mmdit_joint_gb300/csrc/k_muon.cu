@@ -584,6 +584,389 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
     }
 }
 
+// ------------------------------------------------------------------ small matrices
+// Matrices with r <= 128 rows whose X fits the shared memory of up to eight CTAs: one kernel does the whole step. Each
+// CTA of a matrix's group holds a slice of X's columns ([64-column block][R rows][128 bytes], R = 64 or 128; the
+// 128-byte swizzle makes a block a K-major operand of the slice's X X^T and an MN-major one of B X), the CTAs add
+// their parts of A in rank order, compute B each for itself and turn their slices to the next X in place. What
+// bounds it: the passes over g, m and p at the start and end, then the five iterations' chain of products,
+// exchanges and barriers (about FIGURE us).
+constexpr int kSmallItems = 128, kSmallThreads = 1024;
+constexpr int kSmallSmem = 224 * 1024 + 1024;
+__host__ __device__ constexpr int small_side(int r) { return r <= 64 ? 64 : 128; }
+__host__ __device__ constexpr int small_blocks(int side) { return side == 64 ? 24 : 8; }  // 64-column blocks a CTA holds
+
+struct SmallItem {
+    void* p;
+    float* master;
+    const void* g;
+    float* m;
+    int rows, cols, cta0;  // cta0: the group's first CTA
+    int ctas, width;       // CTAs of the group (a power of two), columns of a slice (a multiple of 64)
+    float start, rate, decay;
+    bool g32;
+};
+struct SmallArgs {
+    SmallItem item[kSmallItems];
+    int n, ctas, iterations;
+    float a, b, c, mu, eps;
+    bool nesterov;
+    const float *grad_scale, *lr_dev;
+};
+
+__device__ __forceinline__ float4 load_cluster(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ double load_cluster_f64(uint32_t addr) {
+    double v;
+    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// One element's place: in memory, and as row i, column c of the CTA's slice of X.
+struct Place {
+    int div;      // of the running index: columns of the slice (wide), rows of X (tall)
+    float inv;
+    bool tall;
+    long long base, step;
+    __device__ __forceinline__ void at(int e, long long& index, int& i, int& c) const {
+        const int q = __float2int_rz(((float)e + 0.5f) * inv), rem = e - q * div;  // (exact below 2^22)
+        i = tall ? rem : q;
+        c = tall ? q : rem;
+        index = base + q * step + rem;
+    }
+};
+
+__global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __grid_constant__ SmallArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[4];  // products (two regions of TMEM take turns), the group
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    __shared__ float s_sums[kSmallThreads / 32], s_inv;
+    __shared__ __align__(8) double s_part;
+
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const float f = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
+    // (every CTA of a cluster takes the same way here; those past the last group have nothing to do and nobody waits for them)
+    if ((int)blockIdx.x >= a.ctas || !(fabsf(f) < INFINITY)) return;
+    int lo = 0, hi = a.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((int)blockIdx.x >= a.item[mid].cta0)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const SmallItem& it = a.item[lo];
+    const int ctas = it.ctas, rank = blockIdx.x - it.cta0;
+    const uint32_t first = cluster_rank() - rank;  // the group's first CTA in the cluster
+    const bool tall = it.rows > it.cols;
+    const int r = tall ? it.cols : it.rows, k = tall ? it.rows : it.cols;
+    const int R = small_side(r), col0 = rank * it.width, live = max(0, min(it.width, k - col0));
+    const int blocks = it.width / 64, block_bytes = R * 128;
+    const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t sx = sbase, sa = sbase + small_blocks(R) * block_bytes, sb = sa + (R / 64) * 16384, sp = sb;
+    uint8_t* const generic = smem_raw + (sbase - smem_u32(smem_raw));
+    const uint32_t bar_mma = smem_u32(&bars[0]), bar_group = smem_u32(&bars[2]);
+
+    if (tid == 0) {
+        abort_flag = 0;
+        mbar_init(bar_mma, 1);
+        mbar_init(bar_mma + 8, 1);
+        mbar_init(bar_group, ctas);
+        fence_barrier_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_u32(&tmem_slot), 512);
+        tmem_relinquish();
+    }
+    for (int i = tid; i < blocks * block_bytes / 16; i += kSmallThreads)
+        reinterpret_cast<uint4*>(generic)[i] = make_uint4(0, 0, 0, 0);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (ctas > 1) cluster_sync_all();  // (the barriers exist before anyone arrives on them; all of a cluster's groups are of more than one CTA, or none)
+    const uint32_t tmem = tmem_slot;
+
+    uint32_t group_phase = 0, mma_phase[2] = {0, 0};
+    auto bounded = [&](bool ok) {
+        if (!ok) fail(&abort_flag);
+    };
+    auto group_sync = [&]() {
+        __syncthreads();
+        if (ctas == 1) return;
+        if (tid < ctas)
+            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(map_rank(bar_group, first + tid)) : "memory");
+        bounded(mbar_wait_cluster(bar_group, group_phase, &abort_flag, kWaitLimitNs));
+        group_phase ^= 1;
+    };
+    auto mma_wait = [&](int w) {
+        bounded(mbar_wait(bar_mma + 8 * w, mma_phase[w], &abort_flag, kWaitLimitNs));
+        mma_phase[w] ^= 1;
+        tc_fence_after();
+    };
+    auto publish = [&]() {  // shared memory written by every thread, TMEM read by every thread: before the next products
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    };
+    // byte offset of row i, 16-byte chunk q of a swizzled block of 128-byte rows
+    auto chunk_at = [&](int i, int q) { return i * 128 + ((q ^ (i & 7)) << 4); };
+
+    // ---- momentum, norm, X
+    Place place;
+    place.tall = tall;
+    place.div = tall ? r : max(live, 1);
+    place.inv = 1.0f / (float)place.div;
+    place.base = tall ? (long long)col0 * r : col0;
+    place.step = tall ? r : k;
+    const int total = live * r;
+    constexpr int kDeep = 8;
+    float sq = 0.0f;
+    for (int e0 = tid; e0 < total; e0 += kDeep * kSmallThreads) {
+        float u[kDeep], m[kDeep];
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+            const int e = e0 + d * kSmallThreads;
+            u[d] = m[d] = 0.0f;
+            if (e < total) {
+                long long index;
+                int i, c;
+                place.at(e, index, i, c);
+                u[d] = it.g32 ? static_cast<const float*>(it.g)[index]
+                              : __uint_as_float((uint32_t)static_cast<const uint16_t*>(it.g)[index] << 16);
+                if (it.m != nullptr) m[d] = it.m[index];
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+            const int e = e0 + d * kSmallThreads;
+            if (e >= total) continue;
+            if (it.m != nullptr) {
+                long long index;
+                int i, c;
+                place.at(e, index, i, c);
+                const float g = u[d] * f, mm = fmaf(a.mu, m[d], g);
+                it.m[index] = mm;
+                u[d] = a.nesterov ? fmaf(a.mu, mm, g) : mm;
+            }
+            sq = fmaf(u[d], u[d], sq);
+        }
+    }
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, w);
+    if (lane == 0) s_sums[warp] = sq;
+    __syncthreads();
+    if (tid == 0) {
+        double s = 0.0;
+        for (int w = 0; w < kSmallThreads / 32; ++w) s += (double)s_sums[w];
+        s_part = s;
+    }
+    group_sync();
+    if (tid == 0) {
+        double s = 0.0;
+        for (int w = 0; w < ctas; ++w) s += ctas == 1 ? s_part : load_cluster_f64(map_rank(smem_u32(&s_part), first + w));
+        s_inv = it.start / (sqrtf((float)s) + a.eps);
+    }
+    __syncthreads();
+    const float inv = s_inv;
+    for (int e0 = tid; e0 < total; e0 += kDeep * kSmallThreads) {
+        float u[kDeep], m[kDeep];
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+            const int e = e0 + d * kSmallThreads;
+            u[d] = m[d] = 0.0f;
+            if (e < total) {
+                long long index;
+                int i, c;
+                place.at(e, index, i, c);
+                u[d] = it.g32 ? static_cast<const float*>(it.g)[index]
+                              : __uint_as_float((uint32_t)static_cast<const uint16_t*>(it.g)[index] << 16);
+                if (it.m != nullptr) m[d] = it.m[index];
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+            const int e = e0 + d * kSmallThreads;
+            if (e >= total) continue;
+            long long index;
+            int i, c;
+            place.at(e, index, i, c);
+            if (it.m != nullptr) u[d] = a.nesterov ? fmaf(a.mu, m[d], u[d] * f) : m[d];
+            *reinterpret_cast<__half*>(generic + (c >> 6) * block_bytes + chunk_at(i, (c & 63) >> 3) + (c & 7) * 2) =
+                __float2half_rn(u[d] * inv);
+        }
+    }
+    publish();
+
+    // ---- iterations
+    const int quarter = warp & 3, group = warp >> 2;  // a warp's 32 rows, and its 16 of 128 columns
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t idesc_r = idesc_f16(128, R, false);
+    float scale = 1.0f / it.start;  // of X, until the first iteration's end
+    for (int n = 0; n < a.iterations; ++n) {
+        if (warp == 0 && elect_one()) {  // the slice's part of X X^T
+            for (int j = 0; j < blocks; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint64_t d = sdesc_sw128(sx + j * block_bytes + 32 * q, 16, 1024);
+                    mma_ss(tmem, d, d, idesc_r, j > 0 || q > 0 ? 1u : 0u);
+                }
+            mma_commit(bar_mma);
+        }
+        mma_wait(0);
+        if (row < R && group * 16 < R) {
+            uint32_t v[16];
+            tmem_ld16(tmem + lanes + group * 16, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sp + row * R * 4 + (((group * 4 + q) ^ (row & 7)) << 4)),
+                             "r"(v[4 * q]), "r"(v[4 * q + 1]), "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
+                             : "memory");
+        }
+        tc_fence_before();
+        group_sync();
+        // this CTA's rows of A: the parts in rank order
+        const int share = R / ctas, row0 = rank * share;
+        for (int e = tid; e < share * (R / 4); e += kSmallThreads) {
+            const int i = row0 + e / (R / 4), q = e % (R / 4);
+            const uint32_t at = sp + i * R * 4 + ((q ^ (i & 7)) << 4);
+            float4 v = make_float4(0, 0, 0, 0);
+            for (int w = 0; w < ctas; ++w) {
+                const float4 t = load_cluster(map_rank(at, first + w));
+                v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
+            }
+            const float by = scale * scale;
+            const uint32_t to = sa + (q >> 4) * 16384 + chunk_at(i, (q & 15) >> 1) + (q & 1) * 8;
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(pack_half(v.x * by, v.y * by)), "r"(pack_half(v.z * by, v.w * by))
+                         : "memory");
+        }
+        group_sync();
+        if (ctas > 1) {  // the others' rows
+            for (int e = tid; e < R * (R / 8); e += kSmallThreads) {
+                const int i = e / (R / 8), q = e % (R / 8), owner = i / share;
+                if (owner == rank) continue;
+                const uint32_t at = sa + (q >> 3) * 16384 + chunk_at(i, q & 7);
+                const float4 v = load_cluster(map_rank(at, first + owner));
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+            }
+        }
+        publish();
+        if (warp == 0 && elect_one()) {  // A A
+            for (int q = 0; q < R / 16; ++q) {
+                const uint64_t d = sdesc_sw128(sa + (q >> 2) * 16384 + (q & 3) * 32, 16, 1024);
+                mma_ss(tmem + 128, d, d, idesc_r, q > 0 ? 1u : 0u);
+            }
+            mma_commit(bar_mma);
+        }
+        mma_wait(0);
+        if (row < R && group * 16 < R) {
+            uint32_t v[16];
+            tmem_ld16(tmem + 128 + lanes + group * 16, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int q = group * 2 + h, off = (q >> 3) * 16384 + chunk_at(row, q & 7);
+                const uint4 w = *reinterpret_cast<const uint4*>(generic + (sa - sbase) + off);
+                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
+                    o[j] = pack_half(fmaf(a.b, y.x, a.c * __uint_as_float(v[8 * h + 2 * j])),
+                                     fmaf(a.b, y.y, a.c * __uint_as_float(v[8 * h + 2 * j + 1])));
+                }
+                *reinterpret_cast<uint4*>(generic + (sb - sbase) + off) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+        publish();
+        // X = a X + B X, 128 columns at a time in two regions of TMEM
+        const int tiles = (blocks + 1) / 2;
+        auto issue = [&](int t) {
+            if (warp == 0 && elect_one()) {
+                const uint32_t idesc = idesc_f16(128, 2 * t + 1 < blocks ? 128 : 64, true);
+                for (int q = 0; q < R / 16; ++q)
+                    mma_ss(tmem + 256 + 128 * (t & 1), sdesc_sw128(sb + (q >> 2) * 16384 + (q & 3) * 32, 16, 1024),
+                           sdesc_sw128(sx + 2 * t * block_bytes + 2048 * q, block_bytes, 1024), idesc, q > 0 ? 1u : 0u);
+                mma_commit(bar_mma + 8 * (t & 1));
+            }
+        };
+        issue(0);
+        if (tiles > 1) issue(1);
+        for (int t = 0; t < tiles; ++t) {
+            mma_wait(t & 1);
+            const int block = 2 * t + (group >> 2);
+            if (row < R && block < blocks) {
+                uint32_t v[16];
+                tmem_ld16(tmem + 256 + 128 * (t & 1) + lanes + group * 16, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint4* const at = reinterpret_cast<uint4*>(generic + block * block_bytes + chunk_at(row, (group & 3) * 2 + h));
+                    const uint4 w = *at;
+                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
+                        o[j] = pack_half(fmaf(a.a * scale, y.x, scale * __uint_as_float(v[8 * h + 2 * j])),
+                                         fmaf(a.a * scale, y.y, scale * __uint_as_float(v[8 * h + 2 * j + 1])));
+                    }
+                    *at = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+            publish();
+            if (t + 2 < tiles) issue(t + 2);
+        }
+        scale = 1.0f;
+    }
+
+    // ---- the weights, or X itself
+    const float lr = a.lr_dev != nullptr ? *a.lr_dev : 1.0f;
+    const float rate = it.rate * lr, decay = it.decay * lr;
+    float* const w32 = it.master != nullptr ? it.master : static_cast<float*>(it.p);
+    for (int e0 = tid; e0 < total; e0 += kDeep * kSmallThreads) {
+        float w[kDeep];
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+            const int e = e0 + d * kSmallThreads;
+            w[d] = 0.0f;
+            if (e < total && it.m != nullptr) {
+                long long index;
+                int i, c;
+                place.at(e, index, i, c);
+                w[d] = w32[index];
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+            const int e = e0 + d * kSmallThreads;
+            if (e >= total) continue;
+            long long index;
+            int i, c;
+            place.at(e, index, i, c);
+            float v = __half2float(
+                *reinterpret_cast<const __half*>(generic + (c >> 6) * block_bytes + chunk_at(i, (c & 63) >> 3) + (c & 7) * 2));
+            if (it.m != nullptr) {
+                v = w[d] - fmaf(decay, w[d], rate * v);
+                w32[index] = v;
+            }
+            if (it.m == nullptr || it.master != nullptr) static_cast<__nv_bfloat16*>(it.p)[index] = __float2bfloat16_rn(v);
+        }
+    }
+    tc_fence_before();
+    group_sync();  // nobody leaves while another reads its memory
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
 // ------------------------------------------------------------------ host
 size_t up(size_t x, size_t k) { return (x + k - 1) / k * k; }
 
@@ -600,6 +983,17 @@ struct Plan {
     size_t bytes = 0;
 };
 
+// CTAs of a small matrix's group, 0 for one that takes the products of whole launches: the fewest (a power of two)
+// whose shared memory holds X. By its size alone, so that the sums over its columns have one order in every list.
+int small_ctas(const rlk_muon_matrix& t) {
+    const long long r = t.rows < t.cols ? t.rows : t.cols, k = t.rows < t.cols ? t.cols : t.rows;
+    if (r > 128) return 0;
+    const long long room = 64LL * small_blocks(small_side((int)r));
+    for (int n = 1; n <= 8; n *= 2)
+        if (k <= n * room) return n;
+    return 0;
+}
+
 void plan_of(const rlk_muon_matrix* t, int n, Plan& p) {
     p.of.assign(n, -1);
     p.z.assign(n, 0);
@@ -607,7 +1001,7 @@ void plan_of(const rlk_muon_matrix* t, int n, Plan& p) {
     p.chunk.assign(n, 0);
     p.part.assign(n, 0);
     for (int i = 0; i < n; ++i) {
-        if (t[i].rows == 0 || t[i].cols == 0) continue;
+        if (t[i].rows == 0 || t[i].cols == 0 || small_ctas(t[i]) > 0) continue;
         const int r = (int)(t[i].rows < t[i].cols ? t[i].rows : t[i].cols), k = (int)(t[i].rows < t[i].cols ? t[i].cols : t[i].rows);
         int s = 0;
         while (s < (int)p.sizes.size() && (p.sizes[s].r != r || p.sizes[s].k != k)) ++s;
@@ -672,7 +1066,79 @@ cudaError_t pass(const std::vector<Item>& items, PassArgs& a, Blocks blocks_of, 
     return cudaSuccess;
 }
 
+float start_of(long long r) { return (float)exp2(floor(0.5 * log2((double)r))); }
+
+// p -= decay p + rate X (lr_dev: times its value)
+void rates_of(const rlk_muon_matrix& d, const rlk_muon_args& q, float& rate, float& decay) {
+    const double lr = (q.lr_dev != nullptr ? 1.0 : q.lr) * d.lr_scale;
+    rate = (float)(lr * q.update_rms * sqrt((double)(d.rows > d.cols ? d.rows : d.cols)));
+    decay = (float)(lr * d.weight_decay);
+}
+
+// The small matrices: groups of more CTAs first, so that each lies within a cluster.
+cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool step, cudaStream_t s) {
+    std::vector<int> order;
+    for (int ctas = 8; ctas > 0; ctas /= 2)
+        for (int i = 0; i < n; ++i)
+            if (t[i].rows > 0 && t[i].cols > 0 && small_ctas(t[i]) == ctas) order.push_back(i);
+    if (order.empty()) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(muon_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
+    if (e != cudaSuccess) return e;
+    SmallArgs a;
+    a.iterations = q.iterations;
+    a.a = (float)q.a;
+    a.b = (float)q.b;
+    a.c = (float)q.c;
+    a.mu = (float)q.momentum;
+    a.eps = (float)q.eps;
+    a.nesterov = q.nesterov != 0;
+    a.grad_scale = step ? q.grad_scale : nullptr;
+    a.lr_dev = step ? q.lr_dev : nullptr;
+    for (size_t i = 0; i < order.size();) {
+        const int size = small_ctas(t[order[i]]);  // of the cluster
+        a.n = a.ctas = 0;
+        for (; i < order.size() && a.n < kSmallItems; ++i) {
+            const rlk_muon_matrix& d = t[order[i]];
+            const int ctas = small_ctas(d);
+            if ((ctas == 1) != (size == 1)) break;  // (single CTAs need no cluster)
+            SmallItem& it = a.item[a.n++];
+            it.p = d.p;
+            it.master = step ? d.master : nullptr;
+            it.g = d.g;
+            it.m = step ? d.m : nullptr;
+            it.rows = (int)d.rows;
+            it.cols = (int)d.cols;
+            it.cta0 = a.ctas;
+            it.ctas = ctas;
+            const long long r = d.rows < d.cols ? d.rows : d.cols, k = d.rows < d.cols ? d.cols : d.rows;
+            it.width = (int)up((k + ctas - 1) / ctas, 64);
+            it.start = start_of(r);
+            rates_of(d, q, it.rate, it.decay);
+            it.g32 = d.g_dtype == RLK_FP32;
+            a.ctas += ctas;
+        }
+        cudaLaunchConfig_t c{};
+        c.gridDim = dim3((unsigned)up(a.ctas, size));
+        c.blockDim = dim3(kSmallThreads);
+        c.dynamicSmemBytes = kSmallSmem;
+        c.stream = s;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = size;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        c.attrs = &attr;
+        c.numAttrs = 1;
+        timing_begin(kKMuonSmall, s);
+        e = cudaLaunchKernelEx(&c, muon_small_kernel, a);
+        timing_end(kKMuonSmall, s);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
 cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool step, void* workspace, cudaStream_t s) {
+    const cudaError_t small = run_small(t, n, q, step, s);
+    if (small != cudaSuccess) return small;
     Plan plan;
     plan_of(t, n, plan);
     int dev = 0, sms = 0;
@@ -682,7 +1148,7 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     std::vector<Item> items;
     std::vector<float> start(plan.sizes.size());
-    for (size_t i = 0; i < plan.sizes.size(); ++i) start[i] = (float)exp2(floor(0.5 * log2((double)plan.sizes[i].r)));
+    for (size_t i = 0; i < plan.sizes.size(); ++i) start[i] = start_of(plan.sizes[i].r);
     for (int i = 0; i < n; ++i) {
         if (plan.of[i] < 0) continue;
         const rlk_muon_matrix& d = t[i];
@@ -701,9 +1167,7 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
         it.ld = z.ld;
         it.parts = plan.parts[i];
         it.start = start[plan.of[i]];
-        const double rate = (q.lr_dev != nullptr ? 1.0 : q.lr) * d.lr_scale;
-        it.rate = (float)(rate * q.update_rms * sqrt((double)(d.rows > d.cols ? d.rows : d.cols)));
-        it.decay = (float)(rate * d.weight_decay);
+        rates_of(d, q, it.rate, it.decay);
         it.g32 = d.g_dtype == RLK_FP32;
         items.push_back(it);
     }

@@ -370,7 +370,7 @@ const char* const kKernelNames[kNumKernelIds] = {
     "acc_gemm_kernel<query>", "norm_rope_bwd_q_kernel", "adaln_fwd_kernel", "adaln_bwd_kernel", "adaln_fold_kernel",
     "grad_norm_kernel", "grad_norm_fold_kernel", "adamw_kernel", "adaln_weight_kernel", "fp8_quant_kernel", "fp8_fold_kernel",
     "fp8_gemm_kernel", "muon_momentum_kernel", "muon_start_kernel", "muon_gemm_kernel<gram>", "muon_gemm_kernel<poly>",
-    "muon_gemm_kernel<apply>", "muon_update_kernel"};
+    "muon_gemm_kernel<apply>", "muon_update_kernel", "muon_small_kernel"};
 
 struct OpLog {
     std::mutex mu;

@@ -96,7 +96,7 @@ enum KernelId {
     kKAdalnFwd = 19, kKAdalnBwd = 20, kKAdalnFold = 21, kKGradNorm = 22, kKGradNormFold = 23, kKAdamw = 24,
     kKAdalnWeight = 25,
     kKFp8Quant = 26, kKFp8Fold = 27, kKFp8Gemm = 28, kKMuonMomentum = 29, kKMuonStart = 30, kKMuonGram = 31,
-    kKMuonPoly = 32, kKMuonApply = 33, kKMuonUpdate = 34, kNumKernelIds = 35
+    kKMuonPoly = 32, kKMuonApply = 33, kKMuonUpdate = 34, kKMuonSmall = 35, kNumKernelIds = 36
 };
 
 // Launch timing hooks (rlk_host.cu): bracket one launch with events.
