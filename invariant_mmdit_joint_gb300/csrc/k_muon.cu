@@ -610,7 +610,7 @@ struct SmallArgs {
     SmallItem item[kSmallItems];
     int n, ctas, iterations;
     float a, b, c, mu, eps;
-    bool nesterov;
+    bool nesterov, clusters;  // clusters: of more than one CTA
     const float *grad_scale, *lr_dev;
 };
 
@@ -625,19 +625,29 @@ __device__ __forceinline__ double load_cluster_f64(uint32_t addr) {
     return v;
 }
 
-// One element's place: in memory, and as row i, column c of the CTA's slice of X.
-struct Place {
-    int div;      // of the running index: columns of the slice (wide), rows of X (tall)
-    float inv;
-    bool tall;
-    long long base, step;
-    __device__ __forceinline__ void at(int e, long long& index, int& i, int& c) const {
-        const int q = __float2int_rz(((float)e + 0.5f) * inv), rem = e - q * div;  // (exact below 2^22)
-        i = tall ? rem : q;
-        c = tall ? q : rem;
-        index = base + q * step + rem;
-    }
+// A warp's turn at the slice: up to 8 x 32 neighbouring elements in memory (of one row of X, or, where the matrix is
+// tall, anywhere in its columns).
+constexpr int kDeep = 8, kUnit = 32 * kDeep;
+struct Unit {
+    long long at;  // of lane 0's first element, plus the lane
+    int left;      // elements from there on
+    int i, c;      // place in X of lane 0's first element; tall: c alone counts, as an index
 };
+__device__ __forceinline__ Unit unit_of(int u, int per_row, int live, int r, int k, int col0, bool tall, int lane) {
+    Unit x;
+    if (tall) {
+        x.i = 0;
+        x.c = u * kUnit + lane;
+        x.at = (long long)col0 * r + x.c;
+        x.left = live * r - x.c;
+    } else {
+        x.i = u / per_row;
+        x.c = (u - x.i * per_row) * kUnit + lane;
+        x.at = (long long)x.i * k + col0 + x.c;
+        x.left = live - x.c;
+    }
+    return x;
+}
 
 __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __grid_constant__ SmallArgs a) {
     extern __shared__ uint8_t smem_raw[];
@@ -649,7 +659,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const float f = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
-    // (every CTA of a cluster takes the same way here; those past the last group have nothing to do and nobody waits for them)
+    // (CTAs past the last group have nothing to do, and nobody waits for them)
     if ((int)blockIdx.x >= a.ctas || !(fabsf(f) < INFINITY)) return;
     int lo = 0, hi = a.n - 1;
     while (lo < hi) {
@@ -687,7 +697,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (ctas > 1) cluster_sync_all();  // (the barriers exist before anyone arrives on them; all of a cluster's groups are of more than one CTA, or none)
+    if (a.clusters) cluster_sync_all();  // the barriers exist before anyone arrives on them
     const uint32_t tmem = tmem_slot;
 
     uint32_t group_phase = 0, mma_phase[2] = {0, 0};
@@ -717,40 +727,34 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
     auto chunk_at = [&](int i, int q) { return i * 128 + ((q ^ (i & 7)) << 4); };
 
     // ---- momentum, norm, X
-    Place place;
-    place.tall = tall;
-    place.div = tall ? r : max(live, 1);
-    place.inv = 1.0f / (float)place.div;
-    place.base = tall ? (long long)col0 * r : col0;
-    place.step = tall ? r : k;
-    const int total = live * r;
-    constexpr int kDeep = 8;
+    const int per_row = (live + kUnit - 1) / kUnit, units = tall ? (live * r + kUnit - 1) / kUnit : r * per_row;
+    const float inv_r = 1.0f / (float)r;
+    auto x_at = [&](const Unit& x, int d) {  // where X holds the unit's element d
+        int i = x.i, c = x.c + 32 * d;
+        if (tall) {
+            const int e = c;
+            c = __float2int_rz(((float)e + 0.5f) * inv_r);  // e / r, exact below 2^22
+            i = e - c * r;
+        }
+        return reinterpret_cast<__half*>(generic + (c >> 6) * block_bytes + chunk_at(i, (c & 63) >> 3) + (c & 7) * 2);
+    };
+    auto gradient = [&](long long at) {
+        return it.g32 ? static_cast<const float*>(it.g)[at] : __uint_as_float((uint32_t)static_cast<const uint16_t*>(it.g)[at] << 16);
+    };
     float sq = 0.0f;
-    for (int e0 = tid; e0 < total; e0 += kDeep * kSmallThreads) {
+    for (int n = warp; n < units; n += kSmallThreads / 32) {
+        const Unit x = unit_of(n, per_row, live, r, k, col0, tall, lane);
         float u[kDeep], m[kDeep];
 #pragma unroll
         for (int d = 0; d < kDeep; ++d) {
-            const int e = e0 + d * kSmallThreads;
-            u[d] = m[d] = 0.0f;
-            if (e < total) {
-                long long index;
-                int i, c;
-                place.at(e, index, i, c);
-                u[d] = it.g32 ? static_cast<const float*>(it.g)[index]
-                              : __uint_as_float((uint32_t)static_cast<const uint16_t*>(it.g)[index] << 16);
-                if (it.m != nullptr) m[d] = it.m[index];
-            }
+            u[d] = 32 * d < x.left ? gradient(x.at + 32 * d) : 0.0f;
+            m[d] = 32 * d < x.left && it.m != nullptr ? it.m[x.at + 32 * d] : 0.0f;
         }
 #pragma unroll
         for (int d = 0; d < kDeep; ++d) {
-            const int e = e0 + d * kSmallThreads;
-            if (e >= total) continue;
             if (it.m != nullptr) {
-                long long index;
-                int i, c;
-                place.at(e, index, i, c);
                 const float g = u[d] * f, mm = fmaf(a.mu, m[d], g);
-                it.m[index] = mm;
+                if (32 * d < x.left) it.m[x.at + 32 * d] = mm;
                 u[d] = a.nesterov ? fmaf(a.mu, mm, g) : mm;
             }
             sq = fmaf(u[d], u[d], sq);
@@ -773,31 +777,18 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
     }
     __syncthreads();
     const float inv = s_inv;
-    for (int e0 = tid; e0 < total; e0 += kDeep * kSmallThreads) {
+    for (int n = warp; n < units; n += kSmallThreads / 32) {
+        const Unit x = unit_of(n, per_row, live, r, k, col0, tall, lane);
         float u[kDeep], m[kDeep];
 #pragma unroll
         for (int d = 0; d < kDeep; ++d) {
-            const int e = e0 + d * kSmallThreads;
-            u[d] = m[d] = 0.0f;
-            if (e < total) {
-                long long index;
-                int i, c;
-                place.at(e, index, i, c);
-                u[d] = it.g32 ? static_cast<const float*>(it.g)[index]
-                              : __uint_as_float((uint32_t)static_cast<const uint16_t*>(it.g)[index] << 16);
-                if (it.m != nullptr) m[d] = it.m[index];
-            }
+            u[d] = 32 * d < x.left ? gradient(x.at + 32 * d) : 0.0f;
+            m[d] = 32 * d < x.left && it.m != nullptr ? it.m[x.at + 32 * d] : 0.0f;
         }
 #pragma unroll
         for (int d = 0; d < kDeep; ++d) {
-            const int e = e0 + d * kSmallThreads;
-            if (e >= total) continue;
-            long long index;
-            int i, c;
-            place.at(e, index, i, c);
             if (it.m != nullptr) u[d] = a.nesterov ? fmaf(a.mu, m[d], u[d] * f) : m[d];
-            *reinterpret_cast<__half*>(generic + (c >> 6) * block_bytes + chunk_at(i, (c & 63) >> 3) + (c & 7) * 2) =
-                __float2half_rn(u[d] * inv);
+            if (32 * d < x.left) *x_at(x, d) = __float2half_rn(u[d] * inv);
         }
     }
     publish();
@@ -809,17 +800,35 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
     const uint32_t idesc_r = idesc_f16(128, R, false);
     float scale = 1.0f / it.start;  // of X, until the first iteration's end
     for (int n = 0; n < a.iterations; ++n) {
-        if (warp == 0 && elect_one()) {  // the slice's part of X X^T
-            for (int j = 0; j < blocks; ++j)
+        if (warp == 0) {  // the slice's part of X X^T
+            const uint64_t x0 = sdesc_sw128(sx, 16, 1024);
+            for (int j = 0; j < blocks; ++j) {
+                const uint64_t d = x0 + j * (block_bytes >> 4);
+                if (elect_one())
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint64_t d = sdesc_sw128(sx + j * block_bytes + 32 * q, 16, 1024);
-                    mma_ss(tmem, d, d, idesc_r, j > 0 || q > 0 ? 1u : 0u);
-                }
-            mma_commit(bar_mma);
+                    for (int q = 0; q < 4; ++q) mma_ss(tmem, d + 2 * q, d + 2 * q, idesc_r, j > 0 || q > 0 ? 1u : 0u);
+            }
+            if (elect_one()) mma_commit(bar_mma);
         }
         mma_wait(0);
-        if (row < R && group * 16 < R) {
+        if (ctas == 1) {  // all of A
+            if (row < R && group * 16 < R) {
+                uint32_t v[16];
+                tmem_ld16(tmem + lanes + group * 16, v);
+                tmem_ld_wait();
+                const float by = scale * scale;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        o[j] = pack_half(__uint_as_float(v[8 * h + 2 * j]) * by, __uint_as_float(v[8 * h + 2 * j + 1]) * by);
+                    const int q = group * 2 + h;
+                    *reinterpret_cast<uint4*>(generic + (sa - sbase) + (q >> 3) * 16384 + chunk_at(row, q & 7)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+        } else if (row < R && group * 16 < R) {
             uint32_t v[16];
             tmem_ld16(tmem + lanes + group * 16, v);
             tmem_ld_wait();
@@ -829,25 +838,26 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
                              "r"(v[4 * q]), "r"(v[4 * q + 1]), "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
                              : "memory");
         }
-        tc_fence_before();
-        group_sync();
-        // this CTA's rows of A: the parts in rank order
-        const int share = R / ctas, row0 = rank * share;
-        for (int e = tid; e < share * (R / 4); e += kSmallThreads) {
-            const int i = row0 + e / (R / 4), q = e % (R / 4);
-            const uint32_t at = sp + i * R * 4 + ((q ^ (i & 7)) << 4);
-            float4 v = make_float4(0, 0, 0, 0);
-            for (int w = 0; w < ctas; ++w) {
-                const float4 t = load_cluster(map_rank(at, first + w));
-                v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
+        if (ctas > 1) {
+            tc_fence_before();
+            group_sync();
+            // this CTA's rows of A: the parts in rank order
+            const int share = R / ctas, row0 = rank * share;
+            for (int e = tid; e < share * (R / 4); e += kSmallThreads) {
+                const int i = row0 + e / (R / 4), q = e % (R / 4);
+                const uint32_t at = sp + i * R * 4 + ((q ^ (i & 7)) << 4);
+                float4 v = make_float4(0, 0, 0, 0);
+                for (int w = 0; w < ctas; ++w) {
+                    const float4 t = load_cluster(map_rank(at, first + w));
+                    v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
+                }
+                const float by = scale * scale;
+                const uint32_t to = sa + (q >> 4) * 16384 + chunk_at(i, (q & 15) >> 1) + (q & 1) * 8;
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(pack_half(v.x * by, v.y * by)), "r"(pack_half(v.z * by, v.w * by))
+                             : "memory");
             }
-            const float by = scale * scale;
-            const uint32_t to = sa + (q >> 4) * 16384 + chunk_at(i, (q & 15) >> 1) + (q & 1) * 8;
-            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(pack_half(v.x * by, v.y * by)), "r"(pack_half(v.z * by, v.w * by))
-                         : "memory");
-        }
-        group_sync();
-        if (ctas > 1) {  // the others' rows
+            group_sync();
+            // the others' rows
             for (int e = tid; e < R * (R / 8); e += kSmallThreads) {
                 const int i = e / (R / 8), q = e % (R / 8), owner = i / share;
                 if (owner == rank) continue;
@@ -885,42 +895,45 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
             }
         }
         publish();
-        // X = a X + B X, 128 columns at a time in two regions of TMEM
-        const int tiles = (blocks + 1) / 2;
+        // X = a X + B X, 256 columns at a time in the halves of TMEM
+        const int tiles = (blocks + 3) / 4;
         auto issue = [&](int t) {
-            if (warp == 0 && elect_one()) {
-                const uint32_t idesc = idesc_f16(128, 2 * t + 1 < blocks ? 128 : 64, true);
-                for (int q = 0; q < R / 16; ++q)
-                    mma_ss(tmem + 256 + 128 * (t & 1), sdesc_sw128(sb + (q >> 2) * 16384 + (q & 3) * 32, 16, 1024),
-                           sdesc_sw128(sx + 2 * t * block_bytes + 2048 * q, block_bytes, 1024), idesc, q > 0 ? 1u : 0u);
-                mma_commit(bar_mma + 8 * (t & 1));
-            }
+            if (warp != 0) return;
+            const uint32_t idesc = idesc_f16(128, 64 * min(4, blocks - 4 * t), true);
+            const uint64_t b0 = sdesc_sw128(sb, 16, 1024), x0 = sdesc_sw128(sx + 4 * t * block_bytes, block_bytes, 1024);
+            for (int q = 0; q < R / 16; ++q)
+                if (elect_one())
+                    mma_ss(tmem + 256 * (t & 1), b0 + (q >> 2) * (16384 >> 4) + (q & 3) * 2, x0 + q * (2048 >> 4), idesc, q > 0 ? 1u : 0u);
+            if (elect_one()) mma_commit(bar_mma + 8 * (t & 1));
         };
         issue(0);
         if (tiles > 1) issue(1);
         for (int t = 0; t < tiles; ++t) {
             mma_wait(t & 1);
-            const int block = 2 * t + (group >> 2);
+            const int block = 4 * t + (group >> 1);  // 32 columns a warp
             if (row < R && block < blocks) {
-                uint32_t v[16];
-                tmem_ld16(tmem + 256 + 128 * (t & 1) + lanes + group * 16, v);
-                tmem_ld_wait();
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint4* const at = reinterpret_cast<uint4*>(generic + block * block_bytes + chunk_at(row, (group & 3) * 2 + h));
-                    const uint4 w = *at;
-                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t o[4];
+                for (int p = 0; p < 2; ++p) {
+                    uint32_t v[16];
+                    tmem_ld16(tmem + 256 * (t & 1) + lanes + group * 32 + 16 * p, v);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
-                        o[j] = pack_half(fmaf(a.a * scale, y.x, scale * __uint_as_float(v[8 * h + 2 * j])),
-                                         fmaf(a.a * scale, y.y, scale * __uint_as_float(v[8 * h + 2 * j + 1])));
+                    for (int h = 0; h < 2; ++h) {
+                        uint4* const at = reinterpret_cast<uint4*>(generic + block * block_bytes + chunk_at(row, (group & 1) * 4 + 2 * p + h));
+                        const uint4 w = *at;
+                        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
+                            o[j] = pack_half(fmaf(a.a * scale, y.x, scale * __uint_as_float(v[8 * h + 2 * j])),
+                                             fmaf(a.a * scale, y.y, scale * __uint_as_float(v[8 * h + 2 * j + 1])));
+                        }
+                        *at = make_uint4(o[0], o[1], o[2], o[3]);
                     }
-                    *at = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
-            publish();
+            if (t + 2 < tiles || t + 1 == tiles) publish();  // (tiles that are read out, X whole)
             if (t + 2 < tiles) issue(t + 2);
         }
         scale = 1.0f;
@@ -930,33 +943,20 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
     const float lr = a.lr_dev != nullptr ? *a.lr_dev : 1.0f;
     const float rate = it.rate * lr, decay = it.decay * lr;
     float* const w32 = it.master != nullptr ? it.master : static_cast<float*>(it.p);
-    for (int e0 = tid; e0 < total; e0 += kDeep * kSmallThreads) {
+    for (int n = warp; n < units; n += kSmallThreads / 32) {
+        const Unit x = unit_of(n, per_row, live, r, k, col0, tall, lane);
         float w[kDeep];
 #pragma unroll
-        for (int d = 0; d < kDeep; ++d) {
-            const int e = e0 + d * kSmallThreads;
-            w[d] = 0.0f;
-            if (e < total && it.m != nullptr) {
-                long long index;
-                int i, c;
-                place.at(e, index, i, c);
-                w[d] = w32[index];
-            }
-        }
+        for (int d = 0; d < kDeep; ++d) w[d] = 32 * d < x.left && it.m != nullptr ? w32[x.at + 32 * d] : 0.0f;
 #pragma unroll
         for (int d = 0; d < kDeep; ++d) {
-            const int e = e0 + d * kSmallThreads;
-            if (e >= total) continue;
-            long long index;
-            int i, c;
-            place.at(e, index, i, c);
-            float v = __half2float(
-                *reinterpret_cast<const __half*>(generic + (c >> 6) * block_bytes + chunk_at(i, (c & 63) >> 3) + (c & 7) * 2));
+            if (32 * d >= x.left) continue;
+            float v = __half2float(*x_at(x, d));
             if (it.m != nullptr) {
                 v = w[d] - fmaf(decay, w[d], rate * v);
-                w32[index] = v;
+                w32[x.at + 32 * d] = v;
             }
-            if (it.m == nullptr || it.master != nullptr) static_cast<__nv_bfloat16*>(it.p)[index] = __float2bfloat16_rn(v);
+            if (it.m == nullptr || it.master != nullptr) static_cast<__nv_bfloat16*>(it.p)[x.at + 32 * d] = __float2bfloat16_rn(v);
         }
     }
     tc_fence_before();
@@ -1097,10 +1097,10 @@ cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, b
     for (size_t i = 0; i < order.size();) {
         const int size = small_ctas(t[order[i]]);  // of the cluster
         a.n = a.ctas = 0;
+        a.clusters = size > 1;
         for (; i < order.size() && a.n < kSmallItems; ++i) {
             const rlk_muon_matrix& d = t[order[i]];
             const int ctas = small_ctas(d);
-            if ((ctas == 1) != (size == 1)) break;  // (single CTAs need no cluster)
             SmallItem& it = a.item[a.n++];
             it.p = d.p;
             it.master = step ? d.master : nullptr;
