@@ -603,7 +603,7 @@ struct SmallItem {
     float* m;
     int rows, cols, cta0;  // cta0: the group's first CTA
     int ctas, width;       // CTAs of the group (a power of two), columns of a slice (a multiple of 64)
-    float start, rate, decay;
+    float rate, decay;
     bool g32;
 };
 struct SmallArgs {
@@ -625,28 +625,266 @@ __device__ __forceinline__ double load_cluster_f64(uint32_t addr) {
     return v;
 }
 
-// A warp's turn at the slice: up to 8 x 32 neighbouring elements in memory (of one row of X, or, where the matrix is
-// tall, anywhere in its columns).
+// A warp's turn at the slice: up to 256 neighbouring elements in memory (of one row of X, or, where the matrix is
+// tall, anywhere in its columns), 8 a lane: four neighbours twice where rows are 16-byte aligned, else eight 32 apart.
 constexpr int kDeep = 8, kUnit = 32 * kDeep;
+template <bool kVec>
+__device__ __forceinline__ int offset_of(int d, int lane) {
+    return kVec ? 4 * lane + (d & 3) + 128 * (d >> 2) : lane + 32 * d;
+}
+template <bool kVec>
+__device__ __forceinline__ void load_unit(float (&v)[kDeep], const void* g, bool fp32, long long at, int left, int lane) {
+    if (kVec) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int o = 4 * lane + 128 * h;
+            float4 x = make_float4(0, 0, 0, 0);
+            if (o + 4 <= left) {
+                if (fp32) {
+                    x = *reinterpret_cast<const float4*>(static_cast<const float*>(g) + at + o);
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(g) + at + o);
+                    x = make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+                }
+            } else if (o < left) {  // (the slice's last elements)
+                float* const y = &x.x;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (o + j < left)
+                        y[j] = fp32 ? static_cast<const float*>(g)[at + o + j]
+                                    : __uint_as_float((uint32_t)static_cast<const uint16_t*>(g)[at + o + j] << 16);
+            }
+            v[4 * h] = x.x, v[4 * h + 1] = x.y, v[4 * h + 2] = x.z, v[4 * h + 3] = x.w;
+        }
+        return;
+    }
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+        const int o = offset_of<kVec>(d, lane);
+        v[d] = o >= left ? 0.0f
+               : fp32    ? static_cast<const float*>(g)[at + o]
+                         : __uint_as_float((uint32_t)static_cast<const uint16_t*>(g)[at + o] << 16);
+    }
+}
+template <bool kVec>
+__device__ __forceinline__ void store_unit(float* p, long long at, const float (&v)[kDeep], int left, int lane) {
+    if (kVec) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int o = 4 * lane + 128 * h;
+            if (o + 4 <= left) {
+                *reinterpret_cast<float4*>(p + at + o) = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (o + j < left) p[at + o + j] = v[4 * h + j];
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+        const int o = offset_of<kVec>(d, lane);
+        if (o < left) p[at + o] = v[d];
+    }
+}
+template <bool kVec>
+__device__ __forceinline__ void store_unit_bf16(uint16_t* p, long long at, const float (&v)[kDeep], int left, int lane) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int o = 4 * lane + 128 * h;
+        if (kVec && o + 4 <= left) {
+            *reinterpret_cast<uint2*>(p + at + o) = make_uint2(pack_bf16(v[4 * h], v[4 * h + 1]), pack_bf16(v[4 * h + 2], v[4 * h + 3]));
+            continue;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int e = offset_of<kVec>(4 * h + j, lane);
+            if (e < left) p[at + e] = __bfloat16_as_ushort(__float2bfloat16_rn(v[4 * h + j]));
+        }
+    }
+}
+
+constexpr int kPiece = 2048;  // elements a prefetch takes
+// The 16-byte pieces that lie within [p, p + bytes).
+__device__ __forceinline__ void prefetch_l2(const void* p, long long bytes) {
+    const uint64_t lo = (reinterpret_cast<uint64_t>(p) + 15) & ~15ull, hi = (reinterpret_cast<uint64_t>(p) + bytes) & ~15ull;
+    if (hi > lo) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(lo), "r"((uint32_t)(hi - lo)) : "memory");
+}
+
 struct Unit {
-    long long at;  // of lane 0's first element, plus the lane
+    long long at;  // first element
     int left;      // elements from there on
-    int i, c;      // place in X of lane 0's first element; tall: c alone counts, as an index
+    int i, c;      // its place in X; tall: c alone counts, as an index
 };
-__device__ __forceinline__ Unit unit_of(int u, int per_row, int live, int r, int k, int col0, bool tall, int lane) {
+__device__ __forceinline__ Unit unit_of(int u, int per_row, int live, int r, int k, int col0, bool tall) {
     Unit x;
     if (tall) {
         x.i = 0;
-        x.c = u * kUnit + lane;
+        x.c = u * kUnit;
         x.at = (long long)col0 * r + x.c;
         x.left = live * r - x.c;
     } else {
         x.i = u / per_row;
-        x.c = (u - x.i * per_row) * kUnit + lane;
+        x.c = (u - x.i * per_row) * kUnit;
         x.at = (long long)x.i * k + col0 + x.c;
         x.left = live - x.c;
     }
     return x;
+}
+
+// What the passes over a slice need to know.
+struct Slice {
+    int per_row, units, live, r, k, col0, block_bytes;
+    float inv_r;
+    bool tall;
+    uint8_t* x;
+    __device__ __forceinline__ Unit unit(int u) const { return unit_of(u, per_row, live, r, k, col0, tall); }
+    // where X holds the element o of a tall matrix's unit
+    __device__ __forceinline__ __half* tall_at(const Unit& u, int o) const {
+        const int e = u.c + o, c = __float2int_rz(((float)e + 0.5f) * inv_r), i = e - c * r;  // (e / r, exact below 2^22)
+        return reinterpret_cast<__half*>(x + (c >> 6) * block_bytes + i * 128 + ((((c & 63) >> 3) ^ (i & 7)) << 4) + (c & 7) * 2);
+    }
+    // Where X holds the lane's four neighbours h (vectors), or its element d: a unit starts at a multiple of 256 columns.
+    __device__ __forceinline__ uint2* four_at(const Unit& u, int h, int lane) const {
+        return reinterpret_cast<uint2*>(x + ((u.c >> 6) + 2 * h + (lane >> 4)) * block_bytes + u.i * 128 +
+                                        ((((lane & 15) >> 1) ^ (u.i & 7)) << 4) + (lane & 1) * 8);
+    }
+    __device__ __forceinline__ __half* one_at(const Unit& u, int d, int lane) const {
+        return reinterpret_cast<__half*>(x + ((u.c >> 6) + (d >> 1)) * block_bytes + u.i * 128 +
+                                         ((((lane >> 3) + 4 * (d & 1)) ^ (u.i & 7)) << 4) + (lane & 7) * 2);
+    }
+    // (a row's slice ends at a multiple of 4 columns where there are vectors; X has room up to a multiple of 64)
+    template <bool kVec>
+    __device__ __forceinline__ void put(const Unit& u, const float (&v)[kDeep], float scale, int lane) const {
+#pragma unroll
+        for (int d = 0; d < kDeep; d += kVec ? 4 : 1) {
+            const int o = offset_of<kVec>(d, lane);
+            if (o >= u.left) continue;
+            if (tall) {
+#pragma unroll
+                for (int j = 0; j < (kVec ? 4 : 1); ++j)
+                    if (o + j < u.left) *tall_at(u, o + j) = __float2half_rn(v[d + j] * scale);
+            } else if (kVec) {
+                *four_at(u, d >> 2, lane) = make_uint2(pack_half(v[d] * scale, v[(d + 1) % kDeep] * scale),
+                                                       pack_half(v[(d + 2) % kDeep] * scale, v[(d + 3) % kDeep] * scale));
+            } else {
+                *one_at(u, d, lane) = __float2half_rn(v[d] * scale);
+            }
+        }
+    }
+    template <bool kVec>
+    __device__ __forceinline__ void get(const Unit& u, float (&v)[kDeep], int lane) const {
+#pragma unroll
+        for (int d = 0; d < kDeep; d += kVec ? 4 : 1) {
+            const int o = offset_of<kVec>(d, lane);
+#pragma unroll
+            for (int j = 0; j < (kVec ? 4 : 1); ++j) v[d + j] = 0.0f;
+            if (o >= u.left) continue;
+            if (tall) {
+#pragma unroll
+                for (int j = 0; j < (kVec ? 4 : 1); ++j)
+                    if (o + j < u.left) v[d + j] = __half2float(*tall_at(u, o + j));
+            } else if (kVec) {
+                const uint2 w = *four_at(u, d >> 2, lane);
+                const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w.x)), q = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+                v[d] = p.x, v[(d + 1) % kDeep] = p.y, v[(d + 2) % kDeep] = q.x, v[(d + 3) % kDeep] = q.y;
+            } else {
+                v[d] = __half2float(*one_at(u, d, lane));
+            }
+        }
+    }
+};
+
+// The power of two that brings `top` to 2^8 (fp16 then has 2^8 to spare above it, and 2^22 below it as normal
+// numbers); 0 and what is not finite: 1.
+__device__ __forceinline__ float x_scale(float top) {
+    const int e = (int)(__float_as_uint(top) >> 23);
+    return top > 0.0f && e < 255 ? __uint_as_float((uint32_t)min(max(127 + 8 - (e - 127), 1), 254) << 23) : 1.0f;
+}
+
+// u of one unit: the new momentum is written (kMomentum), or was and is read again.
+template <bool kVec, bool kMomentum>
+__device__ __forceinline__ void update_of(float (&u)[kDeep], const SmallItem& it, const SmallArgs& a, const Unit& x, float f, int lane) {
+    load_unit<kVec>(u, it.g, it.g32, x.at, x.left, lane);
+    if (it.m == nullptr) return;
+    float m[kDeep];
+    load_unit<kVec>(m, it.m, true, x.at, x.left, lane);
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+        const float g = u[d] * f;
+        if (kMomentum) m[d] = fmaf(a.mu, m[d], g);
+        u[d] = a.nesterov ? fmaf(a.mu, m[d], g) : m[d];
+    }
+    if (kMomentum) store_unit<kVec>(it.m, x.at, m, x.left, lane);
+}
+__device__ __forceinline__ float block_top(float top, float* sums) {  // over the CTA's threads
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = top;
+    __syncthreads();
+    top = sums[threadIdx.x & 31];
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+    return top;
+}
+
+// One read of the slice: momentum, sum of u's squares, X = u * scale. The scale comes from the warps' first units; if
+// some value does not fit it after all, X is written again with one that fits (from the momentum as it is now).
+template <bool kVec>
+__device__ __forceinline__ float read_slice(const SmallItem& it, const SmallArgs& a, const Slice& s, float f, float* sums, float& sq) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kWarps = kSmallThreads / 32;
+    float u[kDeep], top = 0.0f;
+    auto look = [&]() {
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+            sq = fmaf(u[d], u[d], sq);
+            top = fmaxf(top, fabsf(u[d]));
+        }
+    };
+    sq = 0.0f;
+    Unit x = s.unit(min(warp, s.units - 1));
+    if (warp < s.units) {
+        update_of<kVec, true>(u, it, a, x, f, lane);
+        look();
+    }
+    float scale = x_scale(block_top(top, sums));
+    if (warp < s.units) s.put<kVec>(x, u, scale, lane);
+    for (int n = warp + kWarps; n < s.units; n += kWarps) {
+        x = s.unit(n);
+        update_of<kVec, true>(u, it, a, x, f, lane);
+        look();
+        s.put<kVec>(x, u, scale, lane);
+    }
+    top = block_top(top, sums);
+    if (top * scale < 32768.0f && (top * scale >= 1.0f || top == 0.0f)) return scale;
+    scale = x_scale(top);
+    for (int n = warp; n < s.units; n += kWarps) {
+        x = s.unit(n);
+        update_of<kVec, false>(u, it, a, x, f, lane);
+        s.put<kVec>(x, u, scale, lane);
+    }
+    return scale;
+}
+
+// p -= decay p + rate X, or p = X
+template <bool kVec>
+__device__ __forceinline__ void write_slice(const SmallItem& it, const Slice& s, float rate, float decay) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float* const w32 = it.master != nullptr ? it.master : static_cast<float*>(it.p);
+    for (int n = warp; n < s.units; n += kSmallThreads / 32) {
+        const Unit x = s.unit(n);
+        float w[kDeep];
+        float v[kDeep];
+        if (it.m != nullptr) load_unit<kVec>(w, w32, true, x.at, x.left, lane);
+        s.get<kVec>(x, v, lane);
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) w[d] = it.m != nullptr ? w[d] - fmaf(decay, w[d], rate * v[d]) : v[d];
+        if (it.m != nullptr) store_unit<kVec>(w32, x.at, w, x.left, lane);
+        if (it.m == nullptr || it.master != nullptr) store_unit_bf16<kVec>(static_cast<uint16_t*>(it.p), x.at, w, x.left, lane);
+    }
 }
 
 __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __grid_constant__ SmallArgs a) {
@@ -727,39 +965,38 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
     auto chunk_at = [&](int i, int q) { return i * 128 + ((q ^ (i & 7)) << 4); };
 
     // ---- momentum, norm, X
-    const int per_row = (live + kUnit - 1) / kUnit, units = tall ? (live * r + kUnit - 1) / kUnit : r * per_row;
-    const float inv_r = 1.0f / (float)r;
-    auto x_at = [&](const Unit& x, int d) {  // where X holds the unit's element d
-        int i = x.i, c = x.c + 32 * d;
-        if (tall) {
-            const int e = c;
-            c = __float2int_rz(((float)e + 0.5f) * inv_r);  // e / r, exact below 2^22
-            i = e - c * r;
-        }
-        return reinterpret_cast<__half*>(generic + (c >> 6) * block_bytes + chunk_at(i, (c & 63) >> 3) + (c & 7) * 2);
-    };
-    auto gradient = [&](long long at) {
-        return it.g32 ? static_cast<const float*>(it.g)[at] : __uint_as_float((uint32_t)static_cast<const uint16_t*>(it.g)[at] << 16);
-    };
-    float sq = 0.0f;
-    for (int n = warp; n < units; n += kSmallThreads / 32) {
-        const Unit x = unit_of(n, per_row, live, r, k, col0, tall, lane);
-        float u[kDeep], m[kDeep];
-#pragma unroll
-        for (int d = 0; d < kDeep; ++d) {
-            u[d] = 32 * d < x.left ? gradient(x.at + 32 * d) : 0.0f;
-            m[d] = 32 * d < x.left && it.m != nullptr ? it.m[x.at + 32 * d] : 0.0f;
-        }
-#pragma unroll
-        for (int d = 0; d < kDeep; ++d) {
+    // What the passes read is fetched to L2 first, in a few instructions: X leaves little of the SM's memory to the
+    // cache that plain loads in flight need.
+    {
+        const int es = it.g32 ? 4 : 2;
+        const long long run = tall ? (long long)live * r : live, base = tall ? (long long)col0 * r : col0;
+        const int runs = tall ? 1 : r, pieces = (int)((run + kPiece - 1) / kPiece);
+        for (int e = tid; e < runs * pieces; e += kSmallThreads) {
+            const int i = e / pieces;
+            const long long from = base + (long long)i * k + (long long)(e - i * pieces) * kPiece;
+            const long long n = min((long long)kPiece, run - (long long)(e - i * pieces) * kPiece);
+            prefetch_l2(static_cast<const uint8_t*>(it.g) + from * es, n * es);
             if (it.m != nullptr) {
-                const float g = u[d] * f, mm = fmaf(a.mu, m[d], g);
-                if (32 * d < x.left) it.m[x.at + 32 * d] = mm;
-                u[d] = a.nesterov ? fmaf(a.mu, mm, g) : mm;
+                prefetch_l2(it.m + from, n * 4);
+                prefetch_l2((it.master != nullptr ? it.master : static_cast<const float*>(it.p)) + from, n * 4);
             }
-            sq = fmaf(u[d], u[d], sq);
         }
     }
+    Slice slice;
+    slice.per_row = max(1, (live + kUnit - 1) / kUnit);
+    slice.units = tall ? (live * r + kUnit - 1) / kUnit : live > 0 ? r * slice.per_row : 0;
+    slice.live = live;
+    slice.r = r;
+    slice.inv_r = 1.0f / (float)r;
+    slice.k = k;
+    slice.col0 = col0;
+    slice.block_bytes = block_bytes;
+    slice.tall = tall;
+    slice.x = generic;
+    const bool vec = tall || k % 4 == 0;  // (slices start at multiples of 64 columns)
+    float sq;
+    const float up = vec ? read_slice<true>(it, a, slice, f, s_sums, sq) : read_slice<false>(it, a, slice, f, s_sums, sq);
+    __syncthreads();
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, w);
     if (lane == 0) s_sums[warp] = sq;
@@ -773,23 +1010,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
     if (tid == 0) {
         double s = 0.0;
         for (int w = 0; w < ctas; ++w) s += ctas == 1 ? s_part : load_cluster_f64(map_rank(smem_u32(&s_part), first + w));
-        s_inv = it.start / (sqrtf((float)s) + a.eps);
-    }
-    __syncthreads();
-    const float inv = s_inv;
-    for (int n = warp; n < units; n += kSmallThreads / 32) {
-        const Unit x = unit_of(n, per_row, live, r, k, col0, tall, lane);
-        float u[kDeep], m[kDeep];
-#pragma unroll
-        for (int d = 0; d < kDeep; ++d) {
-            u[d] = 32 * d < x.left ? gradient(x.at + 32 * d) : 0.0f;
-            m[d] = 32 * d < x.left && it.m != nullptr ? it.m[x.at + 32 * d] : 0.0f;
-        }
-#pragma unroll
-        for (int d = 0; d < kDeep; ++d) {
-            if (it.m != nullptr) u[d] = a.nesterov ? fmaf(a.mu, m[d], u[d] * f) : m[d];
-            if (32 * d < x.left) *x_at(x, d) = __float2half_rn(u[d] * inv);
-        }
+        s_inv = 1.0f / (sqrtf((float)s) + a.eps);
     }
     publish();
 
@@ -798,7 +1019,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
     const int row = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t idesc_r = idesc_f16(128, R, false);
-    float scale = 1.0f / it.start;  // of X, until the first iteration's end
+    float scale = s_inv / up;  // X is what is stored times this, until the first iteration's end
     for (int n = 0; n < a.iterations; ++n) {
         if (warp == 0) {  // the slice's part of X X^T
             const uint64_t x0 = sdesc_sw128(sx, 16, 1024);
@@ -816,13 +1037,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
                 uint32_t v[16];
                 tmem_ld16(tmem + lanes + group * 16, v);
                 tmem_ld_wait();
-                const float by = scale * scale;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t o[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        o[j] = pack_half(__uint_as_float(v[8 * h + 2 * j]) * by, __uint_as_float(v[8 * h + 2 * j + 1]) * by);
+                        o[j] = pack_half(__uint_as_float(v[8 * h + 2 * j]) * scale * scale,
+                                         __uint_as_float(v[8 * h + 2 * j + 1]) * scale * scale);
                     const int q = group * 2 + h;
                     *reinterpret_cast<uint4*>(generic + (sa - sbase) + (q >> 3) * 16384 + chunk_at(row, q & 7)) =
                         make_uint4(o[0], o[1], o[2], o[3]);
@@ -832,10 +1053,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
             uint32_t v[16];
             tmem_ld16(tmem + lanes + group * 16, v);
             tmem_ld_wait();
+            const auto part = [&](int j) { return __uint_as_float(v[j]) * scale * scale; };
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sp + row * R * 4 + (((group * 4 + q) ^ (row & 7)) << 4)),
-                             "r"(v[4 * q]), "r"(v[4 * q + 1]), "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(sp + row * R * 4 + (((group * 4 + q) ^ (row & 7)) << 4)),
+                             "f"(part(4 * q)), "f"(part(4 * q + 1)), "f"(part(4 * q + 2)), "f"(part(4 * q + 3))
                              : "memory");
         }
         if (ctas > 1) {
@@ -851,9 +1073,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
                     const float4 t = load_cluster(map_rank(at, first + w));
                     v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
                 }
-                const float by = scale * scale;
                 const uint32_t to = sa + (q >> 4) * 16384 + chunk_at(i, (q & 15) >> 1) + (q & 1) * 8;
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(pack_half(v.x * by, v.y * by)), "r"(pack_half(v.z * by, v.w * by))
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(pack_half(v.x, v.y)), "r"(pack_half(v.z, v.w))
                              : "memory");
             }
             group_sync();
@@ -867,12 +1088,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
             }
         }
         publish();
-        if (warp == 0 && elect_one()) {  // A A
-            for (int q = 0; q < R / 16; ++q) {
-                const uint64_t d = sdesc_sw128(sa + (q >> 2) * 16384 + (q & 3) * 32, 16, 1024);
-                mma_ss(tmem + 128, d, d, idesc_r, q > 0 ? 1u : 0u);
+        if (warp == 0) {  // A A
+            const uint64_t a0 = sdesc_sw128(sa, 16, 1024);
+            for (int h = 0; h < R / 64; ++h) {
+                const uint64_t d = a0 + h * (16384 >> 4);
+                if (elect_one())
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) mma_ss(tmem + 128, d + 2 * q, d + 2 * q, idesc_r, h > 0 || q > 0 ? 1u : 0u);
             }
-            mma_commit(bar_mma);
+            if (elect_one()) mma_commit(bar_mma);
         }
         mma_wait(0);
         if (row < R && group * 16 < R) {
@@ -891,7 +1115,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
                     o[j] = pack_half(fmaf(a.b, y.x, a.c * __uint_as_float(v[8 * h + 2 * j])),
                                      fmaf(a.b, y.y, a.c * __uint_as_float(v[8 * h + 2 * j + 1])));
                 }
-                *reinterpret_cast<uint4*>(generic + (sb - sbase) + off) = make_uint4(o[0], o[1], o[2], o[3]);
+                const uint4 b = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(generic + (sb - sbase) + off) = b;
+                // (64 rows: once more in the rows from 64 on, so that the other half of TMEM's lanes holds B X too)
+                if (R == 64) *reinterpret_cast<uint4*>(generic + (sb - sbase) + off + 64 * 128) = b;
             }
         }
         publish();
@@ -901,25 +1128,29 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
             if (warp != 0) return;
             const uint32_t idesc = idesc_f16(128, 64 * min(4, blocks - 4 * t), true);
             const uint64_t b0 = sdesc_sw128(sb, 16, 1024), x0 = sdesc_sw128(sx + 4 * t * block_bytes, block_bytes, 1024);
-            for (int q = 0; q < R / 16; ++q)
+            for (int h = 0; h < R / 64; ++h)
                 if (elect_one())
-                    mma_ss(tmem + 256 * (t & 1), b0 + (q >> 2) * (16384 >> 4) + (q & 3) * 2, x0 + q * (2048 >> 4), idesc, q > 0 ? 1u : 0u);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        mma_ss(tmem + 256 * (t & 1), b0 + h * (16384 >> 4) + 2 * q, x0 + (4 * h + q) * (2048 >> 4), idesc,
+                               h > 0 || q > 0 ? 1u : 0u);
             if (elect_one()) mma_commit(bar_mma + 8 * (t & 1));
         };
         issue(0);
         if (tiles > 1) issue(1);
         for (int t = 0; t < tiles; ++t) {
             mma_wait(t & 1);
-            const int block = 4 * t + (group >> 1);  // 32 columns a warp
-            if (row < R && block < blocks) {
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
+            // 32 columns a warp; where the lanes from 64 on hold the same rows again, 16 each
+            const int block = 4 * t + (group >> 1), i = R == 64 ? row & 63 : row;
+            if (block < blocks) {
+#pragma unroll 1
+                for (int p = R == 64 ? quarter >> 1 : 0; p < (R == 64 ? (quarter >> 1) + 1 : 2); ++p) {
                     uint32_t v[16];
                     tmem_ld16(tmem + 256 * (t & 1) + lanes + group * 32 + 16 * p, v);
                     tmem_ld_wait();
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        uint4* const at = reinterpret_cast<uint4*>(generic + block * block_bytes + chunk_at(row, (group & 1) * 4 + 2 * p + h));
+                        uint4* const at = reinterpret_cast<uint4*>(generic + block * block_bytes + chunk_at(i, (group & 1) * 4 + 2 * p + h));
                         const uint4 w = *at;
                         const uint32_t x[4] = {w.x, w.y, w.z, w.w};
                         uint32_t o[4];
@@ -933,32 +1164,24 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
                     }
                 }
             }
-            if (t + 2 < tiles || t + 1 == tiles) publish();  // (tiles that are read out, X whole)
-            if (t + 2 < tiles) issue(t + 2);
+            if (t + 2 < tiles) {  // (the tile is read out)
+                tc_fence_before();
+                __syncthreads();
+                tc_fence_after();
+                issue(t + 2);
+            }
         }
+        publish();
         scale = 1.0f;
     }
 
     // ---- the weights, or X itself
     const float lr = a.lr_dev != nullptr ? *a.lr_dev : 1.0f;
     const float rate = it.rate * lr, decay = it.decay * lr;
-    float* const w32 = it.master != nullptr ? it.master : static_cast<float*>(it.p);
-    for (int n = warp; n < units; n += kSmallThreads / 32) {
-        const Unit x = unit_of(n, per_row, live, r, k, col0, tall, lane);
-        float w[kDeep];
-#pragma unroll
-        for (int d = 0; d < kDeep; ++d) w[d] = 32 * d < x.left && it.m != nullptr ? w32[x.at + 32 * d] : 0.0f;
-#pragma unroll
-        for (int d = 0; d < kDeep; ++d) {
-            if (32 * d >= x.left) continue;
-            float v = __half2float(*x_at(x, d));
-            if (it.m != nullptr) {
-                v = w[d] - fmaf(decay, w[d], rate * v);
-                w32[x.at + 32 * d] = v;
-            }
-            if (it.m == nullptr || it.master != nullptr) static_cast<__nv_bfloat16*>(it.p)[x.at + 32 * d] = __float2bfloat16_rn(v);
-        }
-    }
+    if (vec)
+        write_slice<true>(it, slice, rate, decay);
+    else
+        write_slice<false>(it, slice, rate, decay);
     tc_fence_before();
     group_sync();  // nobody leaves while another reads its memory
     if (warp == 0) {
@@ -1110,9 +1333,8 @@ cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, b
             it.cols = (int)d.cols;
             it.cta0 = a.ctas;
             it.ctas = ctas;
-            const long long r = d.rows < d.cols ? d.rows : d.cols, k = d.rows < d.cols ? d.cols : d.rows;
+            const long long k = d.rows < d.cols ? d.cols : d.rows;
             it.width = (int)up((k + ctas - 1) / ctas, 64);
-            it.start = start_of(r);
             rates_of(d, q, it.rate, it.decay);
             it.g32 = d.g_dtype == RLK_FP32;
             a.ctas += ctas;
