@@ -591,10 +591,25 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
 // their parts of A in rank order, compute B each for itself and turn their slices to the next X in place. What
 // bounds it: the passes over g, m and p at the start and end, then the five iterations' chain of products,
 // exchanges and barriers (about FIGURE us).
-constexpr int kSmallItems = 128, kSmallThreads = 1024;
-constexpr int kSmallSmem = 224 * 1024 + 1024;
-__host__ __device__ constexpr int small_side(int r) { return r <= 64 ? 64 : 128; }
-__host__ __device__ constexpr int small_blocks(int side) { return side == 64 ? 24 : 8; }  // 64-column blocks a CTA holds
+constexpr int kSmallItems = 128, kSmallThreads = 512;
+constexpr int kSliceBlocks = 8;  // 64-column blocks of a CTA's slice, as long as eight CTAs are enough
+template <int R>
+struct Small {  // R rows of X
+    static constexpr int kMostBlocks = R == 64 ? 24 : 8;  // that fit a CTA
+    static constexpr int kBlockBytes = R * 128;
+    static constexpr int kABytes = R / 64 * 16384;         // A: 128 rows of R halves
+    static constexpr int kPBytes = R == 64 ? 16384 : 65536;  // the CTA's part of A in fp32, then B
+    static constexpr int kTile = R == 64 ? 128 : 256;       // columns of B X at a time, two such regions in TMEM
+    static constexpr int kTmemCols = 2 * kTile;            // (64 rows: two CTAs an SM)
+    // Never so little that more CTAs would fit an SM than its TMEM serves: one of a group that waits for TMEM while the
+    // others wait for it in the cluster's barrier would wait forever.
+    static constexpr int kLeastSmem = (R == 64 ? 80 : 120) * 1024;
+    static constexpr int smem(int blocks) {
+        const int need = blocks * kBlockBytes + kABytes + kPBytes + 1024;
+        return need > kLeastSmem ? need : kLeastSmem;
+    }
+    static_assert(512 / kTmemCols * kLeastSmem + kLeastSmem > 228 * 1024, "");
+};
 
 struct SmallItem {
     void* p;
@@ -608,7 +623,7 @@ struct SmallItem {
 };
 struct SmallArgs {
     SmallItem item[kSmallItems];
-    int n, ctas, iterations;
+    int n, ctas, iterations, blocks;  // blocks: the widest slice's
     float a, b, c, mu, eps;
     bool nesterov, clusters;  // clusters: of more than one CTA
     const float *grad_scale, *lr_dev;
@@ -824,7 +839,7 @@ __device__ __forceinline__ float block_top(float top, float* sums) {  // over th
     __syncthreads();
     if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = top;
     __syncthreads();
-    top = sums[threadIdx.x & 31];
+    top = sums[threadIdx.x % (kSmallThreads / 32)];
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
     return top;
@@ -887,7 +902,8 @@ __device__ __forceinline__ void write_slice(const SmallItem& it, const Slice& s,
     }
 }
 
-__global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __grid_constant__ SmallArgs a) {
+template <int R>
+__global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __grid_constant__ SmallArgs a) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[4];  // products (two regions of TMEM take turns), the group
     __shared__ uint32_t tmem_slot;
@@ -912,10 +928,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
     const uint32_t first = cluster_rank() - rank;  // the group's first CTA in the cluster
     const bool tall = it.rows > it.cols;
     const int r = tall ? it.cols : it.rows, k = tall ? it.rows : it.cols;
-    const int R = small_side(r), col0 = rank * it.width, live = max(0, min(it.width, k - col0));
-    const int blocks = it.width / 64, block_bytes = R * 128;
+    const int col0 = rank * it.width, live = max(0, min(it.width, k - col0));
+    const int blocks = it.width / 64;
+    constexpr int block_bytes = Small<R>::kBlockBytes, kTile = Small<R>::kTile;
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t sx = sbase, sa = sbase + small_blocks(R) * block_bytes, sb = sa + (R / 64) * 16384, sp = sb;
+    const uint32_t sx = sbase, sa = sbase + a.blocks * block_bytes, sb = sa + Small<R>::kABytes, sp = sb;
     uint8_t* const generic = smem_raw + (sbase - smem_u32(smem_raw));
     const uint32_t bar_mma = smem_u32(&bars[0]), bar_group = smem_u32(&bars[2]);
 
@@ -927,7 +944,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
         fence_barrier_init();
     }
     if (warp == 0) {
-        tmem_alloc(smem_u32(&tmem_slot), 512);
+        tmem_alloc(smem_u32(&tmem_slot), Small<R>::kTmemCols);
         tmem_relinquish();
     }
     for (int i = tid; i < blocks * block_bytes / 16; i += kSmallThreads)
@@ -1015,10 +1032,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
     publish();
 
     // ---- iterations
-    const int quarter = warp & 3, group = warp >> 2;  // a warp's 32 rows, and its 16 of 128 columns
+    const int quarter = warp & 3, group = warp >> 2;  // a warp's 32 rows, and its quarter of the columns
     const int row = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    const uint32_t idesc_r = idesc_f16(128, R, false);
+    constexpr uint32_t idesc_r = idesc_f16(128, R, false);
+    constexpr int kOwn = R / 4;                      // columns of A and B a warp has
+    constexpr uint32_t kPolyCol = R;                 // (the regions of B X lie over A's and B's)
     float scale = s_inv / up;  // X is what is stored times this, until the first iteration's end
     for (int n = 0; n < a.iterations; ++n) {
         if (warp == 0) {  // the slice's part of X X^T
@@ -1032,38 +1051,34 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
             if (elect_one()) mma_commit(bar_mma);
         }
         mma_wait(0);
-        if (ctas == 1) {  // all of A
-            if (row < R && group * 16 < R) {
+        if (row < R) {
+#pragma unroll
+            for (int c = group * kOwn; c < group * kOwn + kOwn; c += 16) {
                 uint32_t v[16];
-                tmem_ld16(tmem + lanes + group * 16, v);
+                tmem_ld16(tmem + lanes + c, v);
                 tmem_ld_wait();
+                const auto part = [&](int j) { return __uint_as_float(v[j]) * scale * scale; };
+                if (ctas == 1) {  // all of A
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t o[4];
+                    for (int h = 0; h < 2; ++h) {
+                        const int q = c / 8 + h;
+                        *reinterpret_cast<uint4*>(generic + (sa - sbase) + (q >> 3) * 16384 + chunk_at(row, q & 7)) =
+                            make_uint4(pack_half(part(8 * h), part(8 * h + 1)), pack_half(part(8 * h + 2), part(8 * h + 3)),
+                                       pack_half(part(8 * h + 4), part(8 * h + 5)), pack_half(part(8 * h + 6), part(8 * h + 7)));
+                    }
+                } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        o[j] = pack_half(__uint_as_float(v[8 * h + 2 * j]) * scale * scale,
-                                         __uint_as_float(v[8 * h + 2 * j + 1]) * scale * scale);
-                    const int q = group * 2 + h;
-                    *reinterpret_cast<uint4*>(generic + (sa - sbase) + (q >> 3) * 16384 + chunk_at(row, q & 7)) =
-                        make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int q = 0; q < 4; ++q)
+                        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(sp + row * R * 4 + (((c / 4 + q) ^ (row & 7)) << 4)),
+                                     "f"(part(4 * q)), "f"(part(4 * q + 1)), "f"(part(4 * q + 2)), "f"(part(4 * q + 3))
+                                     : "memory");
                 }
             }
-        } else if (row < R && group * 16 < R) {
-            uint32_t v[16];
-            tmem_ld16(tmem + lanes + group * 16, v);
-            tmem_ld_wait();
-            const auto part = [&](int j) { return __uint_as_float(v[j]) * scale * scale; };
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(sp + row * R * 4 + (((group * 4 + q) ^ (row & 7)) << 4)),
-                             "f"(part(4 * q)), "f"(part(4 * q + 1)), "f"(part(4 * q + 2)), "f"(part(4 * q + 3))
-                             : "memory");
         }
         if (ctas > 1) {
             tc_fence_before();
             group_sync();
-            // this CTA's rows of A: the parts in rank order
+            // this CTA's rows of A, the parts in rank order, to every CTA of the group
             const int share = R / ctas, row0 = rank * share;
             for (int e = tid; e < share * (R / 4); e += kSmallThreads) {
                 const int i = row0 + e / (R / 4), q = e % (R / 4);
@@ -1074,94 +1089,93 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
                     v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
                 }
                 const uint32_t to = sa + (q >> 4) * 16384 + chunk_at(i, (q & 15) >> 1) + (q & 1) * 8;
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(pack_half(v.x, v.y)), "r"(pack_half(v.z, v.w))
-                             : "memory");
+                const uint32_t lo = pack_half(v.x, v.y), hi = pack_half(v.z, v.w);
+                for (int w = 0; w < ctas; ++w)
+                    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(map_rank(to, first + w)), "r"(lo), "r"(hi) : "memory");
             }
             group_sync();
-            // the others' rows
-            for (int e = tid; e < R * (R / 8); e += kSmallThreads) {
-                const int i = e / (R / 8), q = e % (R / 8), owner = i / share;
-                if (owner == rank) continue;
-                const uint32_t at = sa + (q >> 3) * 16384 + chunk_at(i, q & 7);
-                const float4 v = load_cluster(map_rank(at, first + owner));
-                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
-            }
         }
         publish();
         if (warp == 0) {  // A A
             const uint64_t a0 = sdesc_sw128(sa, 16, 1024);
+#pragma unroll
             for (int h = 0; h < R / 64; ++h) {
                 const uint64_t d = a0 + h * (16384 >> 4);
                 if (elect_one())
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) mma_ss(tmem + 128, d + 2 * q, d + 2 * q, idesc_r, h > 0 || q > 0 ? 1u : 0u);
+                    for (int q = 0; q < 4; ++q) mma_ss(tmem + kPolyCol, d + 2 * q, d + 2 * q, idesc_r, h > 0 || q > 0 ? 1u : 0u);
             }
             if (elect_one()) mma_commit(bar_mma);
         }
         mma_wait(0);
-        if (row < R && group * 16 < R) {
-            uint32_t v[16];
-            tmem_ld16(tmem + 128 + lanes + group * 16, v);
-            tmem_ld_wait();
+        if (row < R) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int q = group * 2 + h, off = (q >> 3) * 16384 + chunk_at(row, q & 7);
-                const uint4 w = *reinterpret_cast<const uint4*>(generic + (sa - sbase) + off);
-                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                uint32_t o[4];
+            for (int c = group * kOwn; c < group * kOwn + kOwn; c += 16) {
+                uint32_t v[16];
+                tmem_ld16(tmem + kPolyCol + lanes + c, v);
+                tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
-                    o[j] = pack_half(fmaf(a.b, y.x, a.c * __uint_as_float(v[8 * h + 2 * j])),
-                                     fmaf(a.b, y.y, a.c * __uint_as_float(v[8 * h + 2 * j + 1])));
+                for (int h = 0; h < 2; ++h) {
+                    const int q = c / 8 + h, off = (q >> 3) * 16384 + chunk_at(row, q & 7);
+                    const uint4 w = *reinterpret_cast<const uint4*>(generic + (sa - sbase) + off);
+                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
+                        o[j] = pack_half(fmaf(a.b, y.x, a.c * __uint_as_float(v[8 * h + 2 * j])),
+                                         fmaf(a.b, y.y, a.c * __uint_as_float(v[8 * h + 2 * j + 1])));
+                    }
+                    const uint4 b = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(generic + (sb - sbase) + off) = b;
+                    // (64 rows: once more in the rows from 64 on, so that the other half of TMEM's lanes holds B X too)
+                    if (R == 64) *reinterpret_cast<uint4*>(generic + (sb - sbase) + off + 64 * 128) = b;
                 }
-                const uint4 b = make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4*>(generic + (sb - sbase) + off) = b;
-                // (64 rows: once more in the rows from 64 on, so that the other half of TMEM's lanes holds B X too)
-                if (R == 64) *reinterpret_cast<uint4*>(generic + (sb - sbase) + off + 64 * 128) = b;
             }
         }
         publish();
-        // X = a X + B X, 256 columns at a time in the halves of TMEM
-        const int tiles = (blocks + 3) / 4;
+        // X = a X + B X, kTile columns at a time in two regions of TMEM
+        constexpr int kTileBlocks = kTile / 64;
+        const int tiles = (blocks + kTileBlocks - 1) / kTileBlocks;
         auto issue = [&](int t) {
             if (warp != 0) return;
-            const uint32_t idesc = idesc_f16(128, 64 * min(4, blocks - 4 * t), true);
-            const uint64_t b0 = sdesc_sw128(sb, 16, 1024), x0 = sdesc_sw128(sx + 4 * t * block_bytes, block_bytes, 1024);
+            const uint32_t idesc = idesc_f16(128, 64 * min(kTileBlocks, blocks - kTileBlocks * t), true);
+            const uint64_t b0 = sdesc_sw128(sb, 16, 1024), x0 = sdesc_sw128(sx + kTileBlocks * t * block_bytes, block_bytes, 1024);
+#pragma unroll
             for (int h = 0; h < R / 64; ++h)
                 if (elect_one())
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        mma_ss(tmem + 256 * (t & 1), b0 + h * (16384 >> 4) + 2 * q, x0 + (4 * h + q) * (2048 >> 4), idesc,
+                        mma_ss(tmem + kTile * (t & 1), b0 + h * (16384 >> 4) + 2 * q, x0 + (4 * h + q) * (2048 >> 4), idesc,
                                h > 0 || q > 0 ? 1u : 0u);
             if (elect_one()) mma_commit(bar_mma + 8 * (t & 1));
         };
         issue(0);
         if (tiles > 1) issue(1);
+        // a warp's columns of a tile: a quarter of it; where the lanes from 64 on hold the same rows again, half of that
+        const int i = R == 64 ? row & 63 : row, own0 = R == 64 ? group * 32 + (quarter >> 1) * 16 : group * 64;
         for (int t = 0; t < tiles; ++t) {
             mma_wait(t & 1);
-            // 32 columns a warp; where the lanes from 64 on hold the same rows again, 16 each
-            const int block = 4 * t + (group >> 1), i = R == 64 ? row & 63 : row;
-            if (block < blocks) {
-#pragma unroll 1
-                for (int p = R == 64 ? quarter >> 1 : 0; p < (R == 64 ? (quarter >> 1) + 1 : 2); ++p) {
-                    uint32_t v[16];
-                    tmem_ld16(tmem + 256 * (t & 1) + lanes + group * 32 + 16 * p, v);
-                    tmem_ld_wait();
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint4* const at = reinterpret_cast<uint4*>(generic + block * block_bytes + chunk_at(i, (group & 1) * 4 + 2 * p + h));
-                        const uint4 w = *at;
-                        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                        uint32_t o[4];
+            for (int c = own0; c < own0 + (R == 64 ? 16 : 64); c += 16) {
+                const int block = kTileBlocks * t + (c >> 6);
+                if (block >= blocks) break;
+                uint32_t v[16];
+                tmem_ld16(tmem + kTile * (t & 1) + lanes + c, v);
+                tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
-                            o[j] = pack_half(fmaf(a.a * scale, y.x, scale * __uint_as_float(v[8 * h + 2 * j])),
-                                             fmaf(a.a * scale, y.y, scale * __uint_as_float(v[8 * h + 2 * j + 1])));
-                        }
-                        *at = make_uint4(o[0], o[1], o[2], o[3]);
+                for (int h = 0; h < 2; ++h) {
+                    uint4* const at = reinterpret_cast<uint4*>(generic + block * block_bytes + chunk_at(i, ((c & 63) >> 3) + h));
+                    const uint4 w = *at;
+                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
+                        o[j] = pack_half(fmaf(a.a * scale, y.x, scale * __uint_as_float(v[8 * h + 2 * j])),
+                                         fmaf(a.a * scale, y.y, scale * __uint_as_float(v[8 * h + 2 * j + 1])));
                     }
+                    *at = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
             if (t + 2 < tiles) {  // (the tile is read out)
@@ -1186,7 +1200,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const __gr
     group_sync();  // nobody leaves while another reads its memory
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, Small<R>::kTmemCols);
     }
 }
 
@@ -1207,14 +1221,14 @@ struct Plan {
 };
 
 // CTAs of a small matrix's group, 0 for one that takes the products of whole launches: the fewest (a power of two)
-// whose shared memory holds X. By its size alone, so that the sums over its columns have one order in every list.
+// with slices of 512 columns at most, or eight whose shared memory holds X. By its size alone, so that the sums over
+// its columns have one order in every list.
 int small_ctas(const rlk_muon_matrix& t) {
     const long long r = t.rows < t.cols ? t.rows : t.cols, k = t.rows < t.cols ? t.cols : t.rows;
     if (r > 128) return 0;
-    const long long room = 64LL * small_blocks(small_side((int)r));
-    for (int n = 1; n <= 8; n *= 2)
-        if (k <= n * room) return n;
-    return 0;
+    int n = 1;
+    while (n < 8 && k > n * 64LL * kSliceBlocks) n *= 2;
+    return k <= n * 64LL * (r <= 64 ? Small<64>::kMostBlocks : Small<128>::kMostBlocks) ? n : 0;
 }
 
 void plan_of(const rlk_muon_matrix* t, int n, Plan& p) {
@@ -1298,14 +1312,19 @@ void rates_of(const rlk_muon_matrix& d, const rlk_muon_args& q, float& rate, flo
     decay = (float)(lr * d.weight_decay);
 }
 
-// The small matrices: groups of more CTAs first, so that each lies within a cluster.
+// The small matrices of up to R rows (and more than 64, if R is 128): groups of more CTAs first, so that each lies
+// within a cluster.
+template <int R>
 cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool step, cudaStream_t s) {
     std::vector<int> order;
     for (int ctas = 8; ctas > 0; ctas /= 2)
-        for (int i = 0; i < n; ++i)
-            if (t[i].rows > 0 && t[i].cols > 0 && small_ctas(t[i]) == ctas) order.push_back(i);
+        for (int i = 0; i < n; ++i) {
+            const long long r = t[i].rows < t[i].cols ? t[i].rows : t[i].cols;
+            if (r > 0 && (r <= 64) == (R == 64) && small_ctas(t[i]) == ctas) order.push_back(i);
+        }
     if (order.empty()) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(muon_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
+    cudaError_t e = cudaFuncSetAttribute(muon_small_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Small<R>::smem(Small<R>::kMostBlocks));
     if (e != cudaSuccess) return e;
     SmallArgs a;
     a.iterations = q.iterations;
@@ -1319,7 +1338,7 @@ cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, b
     a.lr_dev = step ? q.lr_dev : nullptr;
     for (size_t i = 0; i < order.size();) {
         const int size = small_ctas(t[order[i]]);  // of the cluster
-        a.n = a.ctas = 0;
+        a.n = a.ctas = a.blocks = 0;
         a.clusters = size > 1;
         for (; i < order.size() && a.n < kSmallItems; ++i) {
             const rlk_muon_matrix& d = t[order[i]];
@@ -1338,11 +1357,12 @@ cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, b
             rates_of(d, q, it.rate, it.decay);
             it.g32 = d.g_dtype == RLK_FP32;
             a.ctas += ctas;
+            if (it.width / 64 > a.blocks) a.blocks = it.width / 64;
         }
         cudaLaunchConfig_t c{};
         c.gridDim = dim3((unsigned)up(a.ctas, size));
         c.blockDim = dim3(kSmallThreads);
-        c.dynamicSmemBytes = kSmallSmem;
+        c.dynamicSmemBytes = Small<R>::smem(a.blocks);
         c.stream = s;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
@@ -1351,7 +1371,7 @@ cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, b
         c.attrs = &attr;
         c.numAttrs = 1;
         timing_begin(kKMuonSmall, s);
-        e = cudaLaunchKernelEx(&c, muon_small_kernel, a);
+        e = cudaLaunchKernelEx(&c, muon_small_kernel<R>, a);
         timing_end(kKMuonSmall, s);
         if (e != cudaSuccess) return e;
     }
@@ -1359,8 +1379,10 @@ cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, b
 }
 
 cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool step, void* workspace, cudaStream_t s) {
-    const cudaError_t small = run_small(t, n, q, step, s);
-    if (small != cudaSuccess) return small;
+    for (const auto small : {run_small<64>, run_small<128>}) {
+        const cudaError_t e = small(t, n, q, step, s);
+        if (e != cudaSuccess) return e;
+    }
     Plan plan;
     plan_of(t, n, plan);
     int dev = 0, sms = 0;
