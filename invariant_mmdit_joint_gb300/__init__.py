@@ -1537,6 +1537,7 @@ class Fp8Projection(_Pairs):
             bwd, self._bwd[i] = place(bwd, (t * rows(n_out), t * srows(n_out), n_out * rows(t), n_out * srows(t),
                                             rlk_fp8_quant_workspace_bytes(t, n_out)))
         self._ws_bytes = max(fwd, bwd)
+        self._calls = {}  # the C calls' arguments by kind of call, once there is a workspace
         self.workspace, self._streams = None, set()
 
     def set_weights(self, w, stream=None) -> None:
@@ -1588,19 +1589,34 @@ class Fp8Projection(_Pairs):
         pb = self._vectors("bias", bias, bf16, self._b)
         out, p = self._outputs(out, ("y", "xt", "xt_scale") if train else ("y",), stream)
         handle, ws = self._ready(stream)
-        n_in, n_out = self.n_in, self.n_out
+        quant, product = self._calls.get(train) or self._fwd_calls(train, ws)
+        py, xt, xs = p["y"], p.get("xt"), p.get("xt_scale")
+        for n, i in enumerate(self._live):  # (the rest of a call stays what it is)
+            e, f = quant[n], product[n]
+            e.x, f.bias, f.d = px[i], pb[i], py[i]
+            if train:
+                e.qt, e.qt_scale = xt[i], xs[i]
+        self._run(quant, product, handle)
+        return out
+
+    def _fwd_calls(self, train, ws):
+        n_in, n_out, bf16 = self.n_in, self.n_out, self.out_dtype.itemsize == 2
         quant, product = [], []
         for i in self._live:
-            q, s = ws + self._fwd[i][0], ws + self._fwd[i][1]
-            t = self._tokens[i]
-            w = self._at[i]
-            quant.append(Fp8Quant(px[i], q, s, p["xt"][i] if train else None, p["xt_scale"][i] if train else None, None, None,
-                                  t, n_in, n_in, 0, 0, 0, 0))
-            product.append(Fp8Product(q, s, w[0], w[1], pb[i], p["y"][i], t, n_out, n_in, n_out, 0, 0,
-                                      int(self.out_dtype is not bf16), 0))
-        rlk_fp8_quantize((Fp8Quant * len(quant))(*quant), handle)
-        rlk_fp8_gemm((Fp8Product * len(product))(*product), handle)
-        return out
+            q, s, t, w = ws + self._fwd[i][0], ws + self._fwd[i][1], self._tokens[i], self._at[i]
+            quant.append(Fp8Quant(None, q, s, None, None, None, None, t, n_in, n_in, 0, 0, 0, 0))
+            product.append(Fp8Product(q, s, w[0], w[1], None, None, t, n_out, n_in, n_out, 0, 0, 0 if bf16 else 1, 0))
+        self._calls[train] = (Fp8Quant * len(quant))(*quant), (Fp8Product * len(product))(*product)
+        return self._calls[train]
+
+    def _run(self, quant, product, handle):
+        rc = lib().rlk_fp8_quantize(quant, len(quant), handle)
+        if rc:
+            _check(rc, "rlk_fp8_quantize")
+        if product is not None:
+            rc = lib().rlk_fp8_gemm(product, len(product), handle)
+            if rc:
+                _check(rc, "rlk_fp8_gemm")
 
     def backward(self, dy, saved, want=("dx", "dw", "db"), accumulate: bool = False, out=None, stream=None):
         """Gradients named in ``want``: dx (bf16), dw (float32 or the constructor's dw_dtype), db (float32). ``saved`` is
@@ -1622,24 +1638,39 @@ class Fp8Projection(_Pairs):
             raise ValueError("accumulate needs out with a float32 dw")
         out, p = self._outputs(out, want, stream)
         handle, ws = self._ready(stream)
-        n_in, n_out = self.n_in, self.n_out
-        quant, product, f = [], [], self._grad
         dx, dw, db = ("dx" in want), ("dw" in want), ("db" in want)
+        quant, product = self._calls.get(want) or self._bwd_calls(want, ws)
+        k = 0
+        for n, i in enumerate(self._live):
+            quant[n].x = pdy[i]
+            if db:
+                quant[n].col_sum = p["db"][i]
+            if dx:
+                product[k].d = p["dx"][i]
+                k += 1
+            if dw:
+                e = product[k]
+                e.b, e.b_scale, e.d, e.accumulate = pxt[i], pxs[i], p["dw"][i], int(accumulate)
+                k += 1
+        self._run(quant, product, handle)
+        return out
+
+    def _bwd_calls(self, want, ws):
+        n_in, n_out, f, f32 = self.n_in, self.n_out, self._grad, self.dw_dtype.itemsize == 4
+        dx, dw, db = ("dx" in want), ("dw" in want), ("db" in want)
+        quant, product = [], []
         for i in self._live:
             q, s, qt, st, part = [ws + k for k in self._bwd[i]]
             t, w = self._tokens[i], self._at[i]
             turned = dw or not dx  # (db alone: the sums come with one of the two)
-            quant.append(Fp8Quant(pdy[i], q if dx else None, s if dx else None, qt if turned else None, st if turned else None,
-                                  p["db"][i] if db else None, part if db else None, t, n_out, n_out, 0, f, 0, 0))
+            quant.append(Fp8Quant(None, q if dx else None, s if dx else None, qt if turned else None, st if turned else None,
+                                  None, part if db else None, t, n_out, n_out, 0, f, 0, 0))
             if dx:
-                product.append(Fp8Product(q, s, w[2], w[3], None, p["dx"][i], t, n_in, n_out, n_in, f, 0, 0, 0))
+                product.append(Fp8Product(q, s, w[2], w[3], None, None, t, n_in, n_out, n_in, f, 0, 0, 0))
             if dw:
-                product.append(Fp8Product(qt, st, pxt[i], pxs[i], None, p["dw"][i], n_out, n_in, t, n_in, f, 0,
-                                          int(self.dw_dtype is f32), int(accumulate)))
-        rlk_fp8_quantize((Fp8Quant * len(quant))(*quant), handle)
-        if product:
-            rlk_fp8_gemm((Fp8Product * len(product))(*product), handle)
-        return out
+                product.append(Fp8Product(qt, st, None, None, None, None, n_out, n_in, t, n_in, f, 0, int(f32), 0))
+        self._calls[want] = (Fp8Quant * len(quant))(*quant), (Fp8Product * len(product))(*product) if product else None
+        return self._calls[want]
 
 
 POLYNOMIAL = (3.4445, -4.7750, 2.0315)

@@ -163,6 +163,7 @@ __device__ __forceinline__ const QuantItem& item_of(const QuantArgs& a, int& til
 template <bool kFp32, bool kE5m2>
 __global__ void __launch_bounds__(kQuantThreads) fp8_quant_rows_kernel(const __grid_constant__ QuantArgs a) {
     constexpr int kRoom = kE5m2 ? 15 : 8, kRows = kRowsTile / 16;
+    asm volatile("griddepcontrol.launch_dependents;");  // (the product of few tokens starts on its weights)
     int tile;
     const QuantItem& it = item_of(a, tile);
     const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
@@ -377,17 +378,19 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 __device__ int g_status_fp8;
 
+// A call with few tokens: NT columns (16 or 64) of an accumulator for each chunk of K, all at hand until the end.
 template <int NT>
-struct Cfg {
-    static constexpr int kAtoms = (NT + 127) / 128;           // 128-row scale atoms of the tokens
+struct Few {
     static constexpr int kStageBytes = kFBytes + NT * kBK;
-    static constexpr int kStages = 8;
-    static constexpr int kScaleBytes = 512 * (1 + kAtoms);    // one chunk's scales
-    static constexpr int kSmemBytes = kStages * kStageBytes + kScaleRing * kScaleBytes + 1024;
-    static constexpr int kHalf = NT >= 32 ? NT / 2 : NT;      // columns of an epilogue warp
-    static constexpr int kAccCol = (NT + 31) / 32 * 32;       // column of the second accumulator
-    static constexpr int kScaleCol = 2 * kAccCol;             // two sets of 4 + 4 * kAtoms columns, 16 apart
-    static_assert(kStageBytes % 1024 == 0 && kScaleCol + 32 <= 512 && 4 * (1 + kAtoms) <= 16, "");
+    static constexpr int kStages = NT == 16 ? 5 : 4;
+    static constexpr int kSlots = NT == 16 ? 11 : 3;            // chunks a CTA takes
+    static constexpr int kScaleCol = kSlots * NT;               // two sets of 8 columns, 16 apart
+    static constexpr uint32_t kTmemCols = 256;                  // two CTAs an SM
+    static constexpr int kSumBytes = 128 * NT * 4;              // a chunk's sums, in the stages' place when these are done
+    static constexpr int kSumsBytes = kSlots * kSumBytes > kStages * kStageBytes ? kSlots * kSumBytes : kStages * kStageBytes;
+    static constexpr int kSmemBytes = kSumsBytes + kSlots * 1024 + 1024;
+    // (a third CTA on an SM would wait for TMEM, perhaps while its cluster waits for it)
+    static_assert(kScaleCol + 32 <= (int)kTmemCols && 2 * kSmemBytes <= 226 * 1024 && 3 * kSmemBytes > 228 * 1024, "");
 };
 
 struct GemmItem {
@@ -403,7 +406,7 @@ struct GemmItem {
 };
 struct GemmArgs {
     GemmItem item[kFp8MaxItems];
-    int n, tiles;
+    int n, tiles, ctas;  // ctas: of a cluster that shares K out (few tokens)
 };
 
 // Instruction descriptor of kind::mxf8f6f4 with e8m0 scales, without the
@@ -452,43 +455,6 @@ __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity,
 struct TileAt {
     int item, f0, t0;
 };
-template <int NT>
-__device__ __forceinline__ TileAt tile_at(const GemmArgs& a, int t) {
-    TileAt r;
-    r.item = 0;
-    while (r.item + 1 < a.n && t >= a.item[r.item + 1].tile0) ++r.item;
-    const int l = t - a.item[r.item].tile0;
-    r.f0 = (l % a.item[r.item].tiles_f) * 128;  // consecutive tiles share their tokens (L2 reuse)
-    r.t0 = (l / a.item[r.item].tiles_f) * NT;
-    return r;
-}
-
-// One thread's feature f over kHalf tokens from t on: + bias, rounded, stored. Two lanes trade values so that
-// each holds two neighbouring features of one token: 4-byte stores, 64 bytes a token and warp.
-template <int kHalf>
-__device__ __forceinline__ void store_tile(const GemmItem& it, const float (&acc)[kHalf], int f, int t) {
-    const bool live = f < it.n;
-    const float b = live && it.bias != nullptr ? __uint_as_float((uint32_t)it.bias[f] << 16) : 0.0f;
-    if (it.fp32) {
-        float* d = static_cast<float*>(it.d) + (long long)t * it.d_stride + f;
-#pragma unroll
-        for (int j = 0; j < kHalf; ++j) {
-            if (live && t + j < it.m) *d = it.accumulate ? *d + (acc[j] + b) : acc[j] + b;
-            d += it.d_stride;
-        }
-        return;
-    }
-    const bool odd = threadIdx.x & 1;
-    uint16_t* d = static_cast<uint16_t*>(it.d) + (long long)(t + odd) * it.d_stride + (f & ~1);
-#pragma unroll
-    for (int j = 0; j < kHalf; j += 2) {
-        const float v0 = acc[j] + b, v1 = acc[j + 1] + b;
-        const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-        if (live && t + j + odd < it.m) *reinterpret_cast<uint32_t*>(d) = odd ? pack_bf16(got, v1) : pack_bf16(v0, got);
-        d += 2 * it.d_stride;
-    }
-}
-
 // A lane's four rows' scale words of atom i (0 features, then tokens) from block kb on.
 __device__ __forceinline__ void gather_scales(uint32_t (&w)[4], const GemmItem& g, int i, const TileAt& at, int kb, int lane) {
     const int r0 = i == 0 ? at.f0 : at.t0 + 128 * (i - 1), rows = i == 0 ? g.n : g.m;
@@ -524,39 +490,74 @@ __device__ __forceinline__ void add_chunk(float (&acc)[kHalf], uint32_t taddr, b
     }
 }
 
+// Allows a kernel its shared memory, at its first launch on a device.
+template <auto kKernel>
+cudaError_t smem_once(int bytes) {
+    static std::atomic<uint64_t> done;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load() >> dev & 1) != 0)) return e;
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done |= 1ull << dev;
+    return e;
+}
+
+// ---- few tokens ----
+__device__ __forceinline__ float load_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// 128 features x NT tokens a cluster, the chunks of K shared out over its CTAs (rank r: chunks r * share ..), so that a
+// few tokens' weights stream through many SMs. Each CTA leaves its chunks' sums in shared memory; then each adds up a
+// part of the features over all chunks in ascending order: the sums and bytes of any other number of CTAs or tokens.
+// Before it waits for the kernel that rounds the tokens, a CTA has its weights fetched to L2.
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ GemmArgs a) {
-    using C = Cfg<NT>;
+__global__ void __launch_bounds__(kThreads, 2) fp8_gemm_few_kernel(const __grid_constant__ GemmArgs a) {
+    using C = Few<NT>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * C::kStages + 2 * kScaleRing + 5];
+    __shared__ __align__(8) uint64_t bars[2 * C::kStages + C::kSlots + 1];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int ctas = a.ctas, rank = blockIdx.x % ctas, t = blockIdx.x / ctas;
+    int item = 0;
+    while (item + 1 < a.n && t >= a.item[item + 1].tile0) ++item;
+    const GemmItem& g = a.item[item];
+    TileAt at;
+    at.item = item;
+    at.f0 = (t - g.tile0) % g.tiles_f * 128;
+    at.t0 = (t - g.tile0) / g.tiles_f * NT;
+    const int chunks = (g.blocks + kChunkBlocks - 1) / kChunkBlocks, share = (chunks + ctas - 1) / ctas;
+    const int c0 = min(rank * share, chunks), n_chunks = min(share, chunks - c0);
+    const int b0 = c0 * kChunkBlocks, n_blocks = min(g.blocks - min(b0, g.blocks), n_chunks * kChunkBlocks);
+
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
     auto stage_f = [&](int st) { return sbase + st * C::kStageBytes; };
     auto stage_t = [&](int st) { return sbase + st * C::kStageBytes + kFBytes; };
-    auto scales = [&](int g) { return sbase + C::kStages * C::kStageBytes + g * C::kScaleBytes; };
-    const uint32_t bar_full = smem_u32(&bars[0]);                     // [kStages] stage loaded
-    const uint32_t bar_empty = bar_full + 8 * C::kStages;             // [kStages] stage consumed
-    const uint32_t bar_sfull = bar_empty + 8 * C::kStages;            // [kScaleRing] a chunk's scales written
-    const uint32_t bar_sempty = bar_sfull + 8 * kScaleRing;           // [kScaleRing] and consumed
-    const uint32_t bar_acc = bar_sempty + 8 * kScaleRing;             // [2] accumulator complete
-    const uint32_t bar_free = bar_acc + 16;                           // [2] accumulator read out
-    const uint32_t bar_drain = bar_free + 16;
+    const uint32_t scales = sbase + C::kSumsBytes;
+    const uint32_t bar_full = smem_u32(&bars[0]), bar_empty = bar_full + 8 * C::kStages;
+    const uint32_t bar_scale = bar_empty + 8 * C::kStages, bar_acc = bar_scale + 8 * C::kSlots;
 
     if (tid == 0) {
         abort_flag = 0;
         for (int i = 0; i < C::kStages; ++i) mbar_init(bar_full + 8 * i, 1), mbar_init(bar_empty + 8 * i, 1);
-        for (int i = 0; i < kScaleRing; ++i) mbar_init(bar_sfull + 8 * i, 1), mbar_init(bar_sempty + 8 * i, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(bar_acc + 8 * i, 1), mbar_init(bar_free + 8 * i, 8);
-        mbar_init(bar_drain, 1);
+        for (int i = 0; i < C::kSlots; ++i) mbar_init(bar_scale + 8 * i, 1);
+        mbar_init(bar_acc, 1);
         fence_barrier_init();
     }
     if (warp == kWarpMma) {
-        tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
+        tmem_alloc(smem_u32(&tmem_slot), C::kTmemCols);
         tmem_relinquish();
     }
+    if (warp == kWarpTma && lane == 0)
+        for (int kb = 0; kb < n_blocks; ++kb)
+            asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(&g.map_f)),
+                         "r"((b0 + kb) * kBK), "r"(at.f0)
+                         : "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -564,135 +565,128 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
 
     if (warp == kWarpTma) {
         if (lane == 0) {
-            uint32_t it = 0;  // stage uses so far
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < a.tiles; t += gridDim.x) {
-                const TileAt at = tile_at<NT>(a, t);
-                const GemmItem& g = a.item[at.item];
-                for (int kb = 0; kb < g.blocks; ++kb, ++it) {
-                    const int st = it % C::kStages;
-                    const uint32_t use = it / C::kStages;
-                    if (use > 0 && !mbar_wait(bar_empty + 8 * st, (use - 1) & 1, &abort_flag, kWaitLimitNs)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_expect_tx(bar_full + 8 * st, C::kStageBytes);
-                    tma_load_2d(stage_f(st), &g.map_f, bar_full + 8 * st, kb * kBK, at.f0);
-                    tma_load_2d(stage_t(st), &g.map_t, bar_full + 8 * st, kb * kBK, at.t0);
-                }
-            }
-            if (!ok) fail(&abort_flag);
-            // drain: every issued stage has landed (the last kStages uses)
-            for (uint32_t u = it < C::kStages ? 0 : it - C::kStages; u < it; ++u)
-                mbar_wait_drain(bar_full + 8 * (u % C::kStages), (u / C::kStages) & 1, kWaitLimitNs);
-        }
-    } else if (warp == kWarpMma) {
-        if (lane == 0) {
-            uint32_t it = 0, chunk = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; ok && t < a.tiles; t += gridDim.x) {
-                const TileAt at = tile_at<NT>(a, t);
-                const int blocks = a.item[at.item].blocks;
-                const uint32_t idesc = a.item[at.item].idesc;
-                for (int kb = 0; ok && kb < blocks; ++chunk) {
-                    const int buf = chunk & 1, ring = chunk % kScaleRing;
-                    const uint32_t use = chunk >> 1;
-                    if ((use > 0 && !mbar_wait(bar_free + 8 * buf, (use - 1) & 1, &abort_flag, kWaitLimitNs)) ||
-                        !mbar_wait(bar_sfull + 8 * ring, (chunk / kScaleRing) & 1, &abort_flag, kWaitLimitNs)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t acc = tmem + buf * C::kAccCol;
-                    const uint32_t sa = tmem + C::kScaleCol + buf * 16, sb = sa + 4;
-#pragma unroll
-                    for (int i = 0; i < 1 + C::kAtoms; ++i)
-                        tmem_copy_scales(sa + 4 * i, sdesc_noswizzle(scales(ring) + 512 * i, 0, 128));
-                    const int end = min(kb + kChunkBlocks, blocks);
-                    uint32_t id = idesc;
-                    for (uint32_t first = 0; kb < end; ++kb, ++it) {
-                        const int st = it % C::kStages;
-                        if (!mbar_wait(bar_full + 8 * st, (it / C::kStages) & 1, &abort_flag, kWaitLimitNs)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-#pragma unroll
-                        for (int j = 0; j < kBK / 32; ++j) {
-                            mma_mx(acc, sdesc_sw128(stage_f(st) + 32 * j, 16, 1024), sdesc_sw128(stage_t(st) + 32 * j, 16, 1024),
-                                   id, sa, sb, first);
-                            first = 1;
-                        }
-                        mma_commit(bar_empty + 8 * st);
-                        id += (1u << 29) | (1u << 4);  // the next block's scale bytes
-                    }
-                    if (ok) {
-                        mma_commit(bar_sempty + 8 * ring);
-                        mma_commit(bar_acc + 8 * buf);
-                    }
-                }
-            }
-            if (!ok) fail(&abort_flag);
-            mma_commit(bar_drain);
-            mbar_wait_drain(bar_drain, 0, kWaitLimitNs);
-        }
-    } else if (warp == kWarpScale) {
-        // a chunk's scale bytes, 128 rows an atom: row r's four bytes at (r % 32) * 16 + (r / 32) * 4
-        uint32_t chunk = 0;
-        bool ok = true;
-        for (int t = blockIdx.x; ok && t < a.tiles; t += gridDim.x) {
-            const TileAt at = tile_at<NT>(a, t);
-            const GemmItem& g = a.item[at.item];
-            for (int kb = 0; kb < g.blocks; kb += kChunkBlocks, ++chunk) {
-                const int ring = chunk % kScaleRing;
-                const uint32_t use = chunk / kScaleRing;
-                uint32_t w[1 + C::kAtoms][4];
-#pragma unroll
-                for (int i = 0; i < 1 + C::kAtoms; ++i) gather_scales(w[i], g, i, at, kb, lane);
-                if (use > 0 && !warp_wait(bar_sempty + 8 * ring, (use - 1) & 1, &abort_flag)) {
+            int it = 0;
+            for (; it < n_blocks; ++it) {
+                const int st = it % C::kStages;
+                const uint32_t use = it / C::kStages;
+                if (use > 0 && !mbar_wait(bar_empty + 8 * st, (use - 1) & 1, &abort_flag, kWaitLimitNs)) {
                     ok = false;
                     break;
                 }
-#pragma unroll
-                for (int i = 0; i < 1 + C::kAtoms; ++i) put_scales(scales(ring) + 512 * i + 16 * lane, w[i]);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_sfull + 8 * ring);
+                mbar_expect_tx(bar_full + 8 * st, C::kStageBytes);
+                tma_load_2d(stage_f(st), &g.map_f, bar_full + 8 * st, (b0 + it) * kBK, at.f0);
+                tma_load_2d(stage_t(st), &g.map_t, bar_full + 8 * st, (b0 + it) * kBK, at.t0);
             }
+            if (!ok) fail(&abort_flag);
+            for (int u = max(0, it - C::kStages); u < it; ++u)
+                mbar_wait_drain(bar_full + 8 * (u % C::kStages), (u / C::kStages) & 1, kWaitLimitNs);
         }
-        if (!ok && lane == 0) fail(&abort_flag);
-    } else if (warp >= kWarpEpilogue) {
-        const int quarter = warp & 3, half = (warp - kWarpEpilogue) >> 2;
-        const bool idle = half * C::kHalf >= NT;  // (N = 16: the first four warps take all columns)
-        const uint32_t at0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * C::kHalf;
-        uint32_t chunk = 0;
+    } else if (warp == kWarpMma) {
+        const uint64_t f0 = sdesc_sw128(stage_f(0), 16, 1024), t0 = sdesc_sw128(stage_t(0), 16, 1024);
+        const uint64_t s0 = sdesc_noswizzle(scales, 0, 128);
+        uint32_t st = 0, phase = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < a.tiles; t += gridDim.x) {
-            const TileAt at = tile_at<NT>(a, t);
-            const GemmItem& g = a.item[at.item];
-            float acc[C::kHalf];
-            for (int kb = 0; kb < g.blocks; kb += kChunkBlocks, ++chunk) {
-                const int buf = chunk & 1;
-                if (!warp_wait(bar_acc + 8 * buf, (chunk >> 1) & 1, &abort_flag)) {
+        for (int c = 0; ok && c < n_chunks; ++c) {
+            if (!warp_wait(bar_scale + 8 * c, 0, &abort_flag)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t sa = tmem + C::kScaleCol + (c & 1) * 16, sb = sa + 4, acc = tmem + c * NT;
+            if (elect_one()) {
+                tmem_copy_scales(sa, s0 + (c * 1024 >> 4));
+                tmem_copy_scales(sb, s0 + ((c * 1024 + 512) >> 4));
+            }
+            const int n = min(kChunkBlocks, n_blocks - c * kChunkBlocks);
+            uint32_t id = g.idesc;
+            for (int kb = 0; kb < n; ++kb) {
+                if (!warp_wait(bar_full + 8 * st, phase, &abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if (!idle) add_chunk<C::kHalf>(acc, at0 + buf * C::kAccCol, kb == 0);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_free + 8 * buf);
+                const uint64_t f = f0 + st * (C::kStageBytes >> 4), tk = t0 + st * (C::kStageBytes >> 4);
+                if (elect_one()) {
+#pragma unroll
+                    for (int j = 0; j < kBK / 32; ++j) mma_mx(acc, f + 2 * j, tk + 2 * j, id, sa, sb, j > 0 || kb > 0 ? 1u : 0u);
+                    mma_commit(bar_empty + 8 * st);
+                }
+                if (++st == C::kStages) st = 0, phase ^= 1;
+                id += (1u << 29) | (1u << 4);  // the next block's scale bytes
             }
-            if (ok && !idle) store_tile<C::kHalf>(g, acc, at.f0 + 32 * quarter + lane, at.t0 + half * C::kHalf);
         }
-        if (!ok && lane == 0) fail(&abort_flag);
+        if (elect_one()) {
+            if (!ok) fail(&abort_flag);
+            mma_commit(bar_acc);
+        }
+    } else if (warp == kWarpScale) {
+        for (int c = 0; c < n_chunks; ++c) {
+            uint32_t w[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) gather_scales(w[i], g, i, at, b0 + c * kChunkBlocks, lane);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) put_scales(scales + c * 1024 + 512 * i + 16 * lane, w[i]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_scale + 8 * c);
+        }
     }
-
-    tc_fence_before();
+    __syncwarp();
+    // every product done, every stage read: their place takes the sums, [chunk][token][feature]
+    if (!warp_wait(bar_acc, 0, &abort_flag) && lane == 0) fail(&abort_flag);
+    tc_fence_after();
     __syncthreads();
+    if (warp >= kWarpEpilogue) {
+        const int quarter = warp & 3, f = 32 * quarter + lane;
+        for (int c = (warp - kWarpEpilogue) >> 2; c < n_chunks * (NT / 16); c += 2) {  // 16 columns each
+            uint32_t r[16];
+            tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + 16 * c, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + ((16 * c + i) * 128 + f) * 4), "r"(r[i]) : "memory");
+        }
+    }
+    tc_fence_before();
+    if (ctas > 1)
+        cluster_sync_all();
+    else
+        __syncthreads();
+    const int rows = 128 / ctas, first = rank * rows, tokens = min(NT, g.m - at.t0);
+    for (int e = tid; e < rows * tokens; e += kThreads) {
+        const int i = first + e % rows, tk = e / rows, f = at.f0 + i;
+        if (f >= g.n) continue;
+        float sum = 0.0f;
+        int w = 0, l = 0;
+        for (int c = 0; c < chunks; c += 4) {
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (c + j >= chunks) break;
+                const uint32_t from = sbase + ((l * NT + tk) * 128 + i) * 4;
+                v[j] = load_cluster(ctas > 1 ? map_rank(from, w) : from);
+                if (++l == share) l = 0, ++w;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (c + j >= chunks) break;
+                sum = c + j == 0 ? v[j] : sum + v[j];
+            }
+        }
+        if (g.bias != nullptr) sum += __uint_as_float((uint32_t)g.bias[f] << 16);
+        const long long to = (long long)(at.t0 + tk) * g.d_stride + f;
+        if (g.fp32) {
+            float* d = static_cast<float*>(g.d) + to;
+            *d = g.accumulate ? *d + sum : sum;
+        } else {
+            static_cast<__nv_bfloat16*>(g.d)[to] = __float2bfloat16_rn(sum);
+        }
+    }
+    if (ctas > 1) cluster_sync_all();  // nobody leaves while another reads its sums
     if (warp == kWarpMma) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc(tmem, C::kTmemCols);
     }
 }
 
@@ -979,7 +973,7 @@ cudaError_t launch_pair(GemmArgs& a, int sms, cudaStream_t s) {
         g.idesc |= idesc_mx(256, kPairTokens);
         a.tiles += g.tiles_f * ((g.m + kPairTokens - 1) / kPairTokens);
     }
-    cudaError_t e = cudaFuncSetAttribute(fp8_gemm_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Pair::kSmemBytes);
+    cudaError_t e = smem_once<fp8_gemm_pair_kernel>(Pair::kSmemBytes);
     if (e != cudaSuccess) return e;
     // clusters that fit at once: more would wait for the first to end
     static std::atomic<int> fit[64];
@@ -1001,9 +995,26 @@ cudaError_t launch_pair(GemmArgs& a, int sms, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+// The CTAs that share a tile's K: enough for two an SM of all the tiles, at most one a chunk, and enough for each CTA's
+// TMEM (0: it is not).
 template <int NT>
-cudaError_t launch_nt(GemmArgs& a, int sms, cudaStream_t s) {
+int few_ctas(const rlk_fp8_product* p, int n, int sms) {
+    long long tiles = 0, chunks = 1;
+    for (int i = 0; i < n; ++i) {
+        if (p[i].m == 0 || p[i].n == 0) continue;
+        tiles += (p[i].n + 127) / 128 * ((p[i].m + NT - 1) / NT);
+        const long long c = (p[i].k + 128 * kChunkBlocks - 1) / (128 * kChunkBlocks);
+        chunks = c > chunks ? c : chunks;
+    }
+    int ctas = 1;
+    while (ctas < 8 && (chunks > (long long)ctas * Few<NT>::kSlots || (2 * ctas <= chunks && 2 * ctas * tiles <= 2 * sms))) ctas *= 2;
+    return chunks <= (long long)ctas * Few<NT>::kSlots ? ctas : 0;
+}
+
+template <int NT>
+cudaError_t launch_few(GemmArgs& a, int ctas, cudaStream_t s) {
     a.tiles = 0;
+    a.ctas = ctas;
     for (int i = 0; i < a.n; ++i) {
         GemmItem& g = a.item[i];
         g.tiles_f = (g.n + 127) / 128;
@@ -1011,12 +1022,25 @@ cudaError_t launch_nt(GemmArgs& a, int sms, cudaStream_t s) {
         g.idesc |= idesc_mx(128, NT);
         a.tiles += g.tiles_f * ((g.m + NT - 1) / NT);
     }
-    cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NT>::kSmemBytes);
+    cudaError_t e = smem_once<fp8_gemm_few_kernel<NT>>(Few<NT>::kSmemBytes);
     if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)(a.tiles * ctas));
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = Few<NT>::kSmemBytes;
+    c.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = attr;
+    c.numAttrs = 2;
     timing_begin(kKFp8Gemm, s);
-    fp8_gemm_kernel<NT><<<a.tiles < sms ? a.tiles : sms, kThreads, Cfg<NT>::kSmemBytes, s>>>(a);
+    e = cudaLaunchKernelEx(&c, fp8_gemm_few_kernel<NT>, a);
     timing_end(kKFp8Gemm, s);
-    return cudaGetLastError();
+    return e;
 }
 
 // codes [rows, k] with rows ld bytes apart, box 128 x box_rows
@@ -1103,8 +1127,17 @@ cudaError_t launch_fp8_gemm(const rlk_fp8_product* p, int n, cudaStream_t s) {
     a.n = 0;
     long long most = 0;
     for (int i = 0; i < n; ++i) most = most < p[i].m ? p[i].m : most;
-    // The accumulator's columns: the narrowest that takes every token, else 224.
-    const int nt = most <= 16 ? 16 : most <= 64 ? 64 : kPairTokens;
+    int dev = 0, sms = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err != cudaSuccess) return err;
+    // The accumulator's columns: the narrowest that takes every token, if K is not too long for it, else 224.
+    int nt = kPairTokens, ctas = 0;
+    if (most <= 64) {
+        nt = most <= 16 ? 16 : 64;
+        ctas = nt == 16 ? few_ctas<16>(p, n, sms) : few_ctas<64>(p, n, sms);
+        if (ctas == 0) nt = kPairTokens;
+    }
     for (int i = 0; i < n; ++i) {
         const rlk_fp8_product& e = p[i];
         if (e.m == 0 || e.n == 0) continue;
@@ -1136,11 +1169,7 @@ cudaError_t launch_fp8_gemm(const rlk_fp8_product* p, int n, cudaStream_t s) {
         g.accumulate = e.accumulate != 0;
     }
     if (a.n == 0) return cudaSuccess;
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    return nt == 16 ? launch_nt<16>(a, sms, s) : nt == 64 ? launch_nt<64>(a, sms, s) : launch_pair(a, sms, s);
+    return nt == 16 ? launch_few<16>(a, ctas, s) : nt == 64 ? launch_few<64>(a, ctas, s) : launch_pair(a, sms, s);
 }
 
 int read_and_clear_status_fp8(cudaStream_t s) {
