@@ -1537,6 +1537,8 @@ class Fp8Projection(_Pairs):
             bwd, self._bwd[i] = place(bwd, (t * rows(n_out), t * srows(n_out), n_out * rows(t), n_out * srows(t),
                                             rlk_fp8_quant_workspace_bytes(t, n_out)))
         self._ws_bytes = max(fwd, bwd)
+        self._weight_call = (Fp8Quant * len(self._live))(*[
+            Fp8Quant(None, *self._at[i], None, None, n_out, n_in, n_in, 0, 0, 1, 0) for i in self._live])
         self._calls = {}  # the C calls' arguments by kind of call, once there is a workspace
         self.workspace, self._streams = None, set()
 
@@ -1548,13 +1550,13 @@ class Fp8Projection(_Pairs):
             raise ValueError("weights are bfloat16 or float32")
         pw = self._need("w", w, dtype, self._w)
         _require_current(self.device)
-        items = (Fp8Quant * len(self._live))(*[
-            Fp8Quant(pw[i], *self._at[i], None, None, self.n_out, self.n_in, self.n_in, int(dtype is torch.float32), 0, 1, 0)
-            for i in self._live])
         handle = _raw_stream(stream, self._index)
-        if handle not in self._streams and self.device.type == "cuda":
+        if handle not in self._streams:
             self._record(stream, handle)
-        rlk_fp8_quantize(items, handle)
+        items = self._weight_call
+        for e, i in zip(items, self._live):
+            e.x, e.x_dtype = pw[i], int(dtype is torch.float32)
+        self._run(items, None, handle)
         self._set = True
 
     def _record(self, stream, handle):
@@ -1575,6 +1577,15 @@ class Fp8Projection(_Pairs):
             self._record(stream, handle)
         return handle, _workspace(self, self._ws_bytes, stream, handle).data_ptr()
 
+    def _out(self, out, names, stream):
+        """The outputs of these names and their pointers (new ones without what a reuse is checked by: that takes
+        longer than the smallest kernels, and most calls' outputs are not passed back)."""
+        if out is not None:
+            return self._outputs(out, names, stream)
+        device, kinds = self.device, self._kinds
+        out = {k: tuple(None if size is None else _empty(size, kinds[k][1], device, stream) for size in kinds[k][0]) for k in names}
+        return out, {k: tuple(None if x is None else x.data_ptr() for x in pair) for k, pair in out.items()}
+
     def _vectors(self, name, pair, dtype, sizes):
         if pair is None or all(t is None for t in pair):
             return _NONE
@@ -1587,7 +1598,7 @@ class Fp8Projection(_Pairs):
         bf16 = torch.bfloat16
         px = self._need("x", x, bf16, self._x)
         pb = self._vectors("bias", bias, bf16, self._b)
-        out, p = self._outputs(out, ("y", "xt", "xt_scale") if train else ("y",), stream)
+        out, p = self._out(out, ("y", "xt", "xt_scale") if train else ("y",), stream)
         handle, ws = self._ready(stream)
         quant, product = self._calls.get(train) or self._fwd_calls(train, ws)
         py, xt, xs = p["y"], p.get("xt"), p.get("xt_scale")
@@ -1636,7 +1647,7 @@ class Fp8Projection(_Pairs):
             pxs = self._need("xt_scale", saved["xt_scale"], *self._kinds["xt_scale"][::-1])
         if accumulate and ("dw" not in want or out is None or self.dw_dtype is not f32):
             raise ValueError("accumulate needs out with a float32 dw")
-        out, p = self._outputs(out, want, stream)
+        out, p = self._out(out, want, stream)
         handle, ws = self._ready(stream)
         dx, dw, db = ("dx" in want), ("dw" in want), ("db" in want)
         quant, product = self._calls.get(want) or self._bwd_calls(want, ws)

@@ -25,6 +25,7 @@
 #include "rlk_tmap.h"
 
 #include <cuda_fp16.h>
+#include <atomic>
 #include <math.h>
 #include <new>
 #include <type_traits>
@@ -310,11 +311,14 @@ __global__ void __launch_bounds__(kPassThreads) muon_update_kernel(const __grid_
 // ------------------------------------------------------------------ products
 enum Mode { kGram = 0, kPoly = 1, kApply = 2 };
 constexpr int kGroups = 8;  // sizes a launch takes
-constexpr int kBM = 128, kBN = 256, kBK = 64, kStages = 4;
-constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2, kStageBytes = kABytes + kBBytes;
+// A cluster of two CTAs computes a tile of 256 rows (128 each) x 256 columns; each holds its rows' operand and half of
+// the columns': the pair's products read half as much shared memory, and TMA brings 32 KB instead of 48 a k-step and
+// CTA (one CTA a tile was bound by that: FIGURE_PAIR).
+constexpr int kBM = 128, kBN = 256, kBK = 64, kStages = 6;
 constexpr int kOutBytes = 32 * 32 * 2;  // an epilogue warp's buffer: 32 rows of 32 columns
-constexpr int kSmemBytes = kStages * kStageBytes + 8 * kOutBytes + 1024;
 constexpr int kThreads = 384;
+constexpr int kABytes = kBM * kBK * 2, kStageBytes = kABytes + kBN / 2 * kBK * 2;
+constexpr int kSmemBytes = kStages * kStageBytes + 8 * kOutBytes + 1024;
 constexpr int kWarpTma = 0, kWarpMma = 1, kWarpEpilogue = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -323,13 +327,13 @@ __device__ int g_status_muon;
 
 struct Group {
     CUtensorMap map_m;   // the operand of the 128 rows: [z][rows][K], box 64 x 128 x 1
-    CUtensorMap map_n;   // the operand of the 256 columns: gram, poly the same, box 64 x 128; apply X, box 64 x 64 (MN-major)
+    CUtensorMap map_n;   // the operand of the kBN columns: gram, poly the same, box 64 x 128; apply X, box 64 x 64 (MN-major)
     CUtensorMap map_out; // out, box 32 x 32 x 1
     const __half* add;   // poly: A; apply: X: added times `add_by`
     __half* out;
     long long add_step, out_step;  // from matrix to matrix
     int rows, cols;      // of the output (gram, poly: r x r)
-    int ld_add, ld_out, steps, per, tile0;  // k-steps; tiles of one matrix; first tile
+    int ld_add, ld_out, count, steps, per, tile0;  // matrices; k-steps; tiles of one matrix; first tile
     float by, add_by;    // out = by * product + add_by * add
 };
 struct GemmArgs {
@@ -340,6 +344,7 @@ struct GemmArgs {
 struct TileAt {
     int g, z, m0, n0;
 };
+// Tile t of a launch: its first row (of both CTAs) and column.
 template <int kMode>
 __device__ __forceinline__ TileAt tile_at(const GemmArgs& a, int t) {
     TileAt r;
@@ -351,16 +356,15 @@ __device__ __forceinline__ TileAt tile_at(const GemmArgs& a, int t) {
     l -= r.z * g.per;
     if (kMode == kApply) {
         const int tn = (g.cols + kBN - 1) / kBN;
-        r.m0 = l / tn * kBM;
+        r.m0 = l / tn * (2 * kBM);
         r.n0 = l % tn * kBN;
     } else {
-        // block rows 2p and 2p + 1 have p + 1 tiles each: p (p + 1) tiles before them
-        int p = (int)((sqrtf(4.0f * l + 1.0f) - 1.0f) * 0.5f);
-        while (p * (p + 1) > l) --p;
-        while ((p + 1) * (p + 2) <= l) ++p;
-        l -= p * (p + 1);
-        r.m0 = (2 * p + (l > p)) * kBM;
-        r.n0 = (l > p ? l - p - 1 : l) * kBN;
+        // i (i + 1) / 2 tiles before block row i
+        int i = (int)((sqrtf(8.0f * l + 1.0f) - 1.0f) * 0.5f);
+        while (i * (i + 1) / 2 > l) --i;
+        while ((i + 1) * (i + 2) / 2 <= l) ++i;
+        r.m0 = i * (2 * kBM);
+        r.n0 = (l - i * (i + 1) / 2) * kBN;
     }
     return r;
 }
@@ -385,7 +389,6 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
 template <int kMode>
 __device__ __forceinline__ void store32(const Group& g, int z, float (&v)[32], int i, int j, uint32_t buffer) {
     const int lane = threadIdx.x & 31, i0 = i - lane;
-    if (kMode != kApply && j > i0) return;  // above the diagonal: stored from the other side
     const bool live = i < g.rows;
     if (kMode != kGram) {
         const __half* add = g.add + z * g.add_step + (long long)i * g.ld_add + j;
@@ -445,33 +448,47 @@ __device__ __forceinline__ void store32(const Group& g, int z, float (&v)[32], i
     }
 }
 
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 template <int kMode>
-__global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_constant__ GemmArgs a) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_constant__ GemmArgs a) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int rank = cluster_rank(), first = blockIdx.x >> 1, step = gridDim.x >> 1;
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
     auto stage_a = [&](int st) { return sbase + st * kStageBytes; };
     auto stage_b = [&](int st) { return sbase + st * kStageBytes + kABytes; };
+    // (full and free: the first CTA's count for both)
     const uint32_t bar_full = smem_u32(&bars[0]), bar_empty = bar_full + 8 * kStages;
     const uint32_t bar_acc = bar_empty + 8 * kStages, bar_free = bar_acc + 16, bar_drain = bar_free + 16;
 
     if (tid == 0) {
         abort_flag = 0;
         for (int i = 0; i < kStages; ++i) mbar_init(bar_full + 8 * i, 1), mbar_init(bar_empty + 8 * i, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(bar_acc + 8 * i, 1), mbar_init(bar_free + 8 * i, 8);
+        for (int i = 0; i < 2; ++i) mbar_init(bar_acc + 8 * i, 1), mbar_init(bar_free + 8 * i, 16);
         mbar_init(bar_drain, 1);
         fence_barrier_init();
     }
     if (warp == kWarpMma) {
-        tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
-        tmem_relinquish();
+        tmem_alloc_pair(smem_u32(&tmem_slot), kTmemCols);
+        tmem_relinquish_pair();
     }
+    // (the kernel before this one still writes what the loads read; the one after may set itself up)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
 
@@ -479,9 +496,10 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < a.tiles; t += gridDim.x) {
+            for (int t = first; ok && t < a.tiles; t += step) {
                 const TileAt at = tile_at<kMode>(a, t);
                 const Group& g = a.g[at.g];
+                const int m0 = at.m0 + kBM * rank, n0 = at.n0 + kBN / 2 * rank;
                 for (int kk = 0; kk < g.steps; ++kk, ++it) {
                     const int st = it % kStages;
                     const uint32_t use = it / kStages, bar = bar_full + 8 * st;
@@ -489,64 +507,70 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
                         ok = false;
                         break;
                     }
-                    mbar_expect_tx(bar, kStageBytes);
-                    tma_load_3d(stage_a(st), &g.map_m, bar, kk * kBK, at.m0, at.z);
+                    if (rank == 0) mbar_expect_tx(bar, 2 * kStageBytes);
+                    tma_load_3d_pair(stage_a(st), &g.map_m, bar, kk * kBK, m0, at.z);
                     if (kMode == kApply) {
-                        for (int q = 0; q < 4; ++q) tma_load_3d(stage_b(st) + q * 8192, &g.map_n, bar, at.n0 + 64 * q, kk * kBK, at.z);
+#pragma unroll
+                        for (int q = 0; q < kBN / 128; ++q)
+                            tma_load_3d_pair(stage_b(st) + q * 8192, &g.map_n, bar, n0 + 64 * q, kk * kBK, at.z);
                     } else {
-                        for (int q = 0; q < 2; ++q) tma_load_3d(stage_b(st) + q * 16384, &g.map_n, bar, kk * kBK, at.n0 + 128 * q, at.z);
+                        tma_load_3d_pair(stage_b(st), &g.map_n, bar, kk * kBK, n0, at.z);
                     }
                 }
             }
             if (!ok) fail(&abort_flag);
-            for (uint32_t u = it < kStages ? 0 : it - kStages; u < it; ++u)
-                mbar_wait_drain(bar_full + 8 * (u % kStages), (u / kStages) & 1, kWaitLimitNs);
+            // drain: what was issued here has landed (counted by the first CTA) or been consumed
+            for (uint32_t u = it < kStages ? 0 : it - kStages; (rank == 0 || ok) && u < it; ++u)
+                mbar_wait_drain((rank == 0 ? bar_full : bar_empty) + 8 * (u % kStages), (u / kStages) & 1, kWaitLimitNs);
         }
     } else if (warp == kWarpMma) {
-        // the whole warp runs the loop, one lane issues
-        constexpr uint32_t idesc = idesc_f16(kBM, kBN, kMode == kApply);
-        const uint64_t a0 = sdesc_sw128(stage_a(0), 16, 1024);
-        const uint64_t b0 = kMode == kApply ? sdesc_sw128(stage_b(0), 8192, 1024) : sdesc_sw128(stage_b(0), 16, 1024);
-        constexpr int kStepB = (kMode == kApply ? 2048 : 32) >> 4;
-        uint32_t st = 0, phase = 0, local = 0;
-        bool ok = true;
-        for (int t = blockIdx.x; ok && t < a.tiles; t += gridDim.x, ++local) {
-            const int buf = local & 1;
-            const uint32_t use = local >> 1;
-            if (use > 0 && !warp_wait(bar_free + 8 * buf, (use - 1) & 1, &abort_flag)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            const uint32_t acc = tmem + buf * kBN;
-            const int steps = a.g[tile_at<kMode>(a, t).g].steps;
-            for (int kk = 0; kk < steps; ++kk) {
-                if (!warp_wait(bar_full + 8 * st, phase, &abort_flag)) {
+        if (rank == 0) {
+            // the whole warp runs the loop, one lane issues
+            constexpr uint32_t idesc = idesc_f16(2 * kBM, kBN, kMode == kApply);
+            const uint64_t a0 = sdesc_sw128(stage_a(0), 16, 1024);
+            const uint64_t b0 = kMode == kApply ? sdesc_sw128(stage_b(0), 8192, 1024) : sdesc_sw128(stage_b(0), 16, 1024);
+            constexpr int kStepB = (kMode == kApply ? 2048 : 32) >> 4;
+            uint32_t st = 0, phase = 0, local = 0;
+            bool ok = true;
+            for (int t = first; ok && t < a.tiles; t += step, ++local) {
+                const int buf = local & 1;
+                const uint32_t use = local >> 1;
+                if (use > 0 && !__all_sync(0xffffffffu, mbar_wait_cluster(bar_free + 8 * buf, (use - 1) & 1, &abort_flag, kWaitLimitNs))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint64_t da = a0 + st * (kStageBytes >> 4), db = b0 + st * (kStageBytes >> 4);
-                if (elect_one()) {
+                const uint32_t acc = tmem + buf * kBN;
+                const int steps = a.g[tile_at<kMode>(a, t).g].steps;
+                for (int kk = 0; kk < steps; ++kk) {
+                    if (!warp_wait(bar_full + 8 * st, phase, &abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t da = a0 + st * (kStageBytes >> 4), db = b0 + st * (kStageBytes >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < kBK / 16; ++j) mma_ss(acc, da + 2 * j, db + kStepB * j, idesc, (kk > 0 || j > 0) ? 1u : 0u);
-                    mma_commit(bar_empty + 8 * st);
+                        for (int j = 0; j < kBK / 16; ++j) mma_pair(acc, da + 2 * j, db + kStepB * j, idesc, (kk > 0 || j > 0) ? 1u : 0u);
+                        mma_commit_pair(bar_empty + 8 * st);
+                    }
+                    if (++st == kStages) st = 0, phase ^= 1;
                 }
-                if (++st == kStages) st = 0, phase ^= 1;
+                if (ok && elect_one()) mma_commit_pair(bar_acc + 8 * buf);
             }
-            if (ok && elect_one()) mma_commit(bar_acc + 8 * buf);
+            if (elect_one()) {
+                if (!ok) fail(&abort_flag);
+                mma_commit_pair(bar_drain);
+            }
         }
-        if (elect_one()) {
-            if (!ok) fail(&abort_flag);
-            mma_commit(bar_drain);
-        }
-        if (lane == 0) mbar_wait_drain(bar_drain, 0, kWaitLimitNs);
+        if (lane == 0) mbar_wait_drain(bar_drain, 0, kWaitLimitNs);  // (in both: the last thing that arrives here)
     } else if (warp >= kWarpEpilogue) {
         const int quarter = warp & 3, half = (warp - kWarpEpilogue) >> 2;
-        const uint32_t at0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
+        const uint32_t at0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * (kBN / 2);
+        const uint32_t buffer = sbase + kStages * kStageBytes + (warp - kWarpEpilogue) * kOutBytes;
         uint32_t local = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < a.tiles; t += gridDim.x, ++local) {
+        for (int t = first; t < a.tiles; t += step, ++local) {
             const int buf = local & 1;
             if (!warp_wait(bar_acc + 8 * buf, (local >> 1) & 1, &abort_flag)) {
                 ok = false;
@@ -555,22 +579,23 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
             tc_fence_after();
             const TileAt at = tile_at<kMode>(a, t);
             const Group& g = a.g[at.g];
+            const int row = at.m0 + kBM * rank + 32 * quarter + lane;
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-                const int j = at.n0 + half * 128 + c;
-                if (j >= g.cols) break;
+            for (int c = 0; c < kBN / 2; c += 32) {
+                const int j = at.n0 + half * (kBN / 2) + c;
+                if (j >= g.cols || (kMode != kApply && j > row - lane)) break;
                 uint32_t r[32];
                 tmem_ld32(at0 + buf * kBN + c, r);
                 tmem_ld_wait();
                 float v[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-                store32<kMode>(g, at.z, v, at.m0 + 32 * quarter + lane, j, sbase + kStages * kStageBytes + (warp - kWarpEpilogue) * kOutBytes);
+                store32<kMode>(g, at.z, v, row, j, buffer);
                 __syncwarp();
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_free + 8 * buf);
+            if (lane == 0) mbar_arrive_cluster(map_rank(bar_free + 8 * buf, 0));
         }
         bulk_wait_all();
         if (!ok && lane == 0) fail(&abort_flag);
@@ -578,9 +603,10 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
 
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all();  // the other CTA's products, commits and arrivals reach this one's memory until here
     if (warp == kWarpMma) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc_pair(tmem, kTmemCols);
     }
 }
 
@@ -1275,14 +1301,53 @@ bool half_map(CUtensorMap* m, const void* base, int cols, int rows, int count, i
 }
 
 template <int kMode>
-cudaError_t launch_product(GemmArgs& a, int sms, cudaStream_t s) {
+cudaError_t launch_product(GemmArgs& a, int pairs, cudaStream_t s) {
+    a.tiles = 0;
+    for (int g = 0; g < a.n; ++g) {
+        Group& d = a.g[g];
+        const int blocks = (d.rows + 2 * kBM - 1) / (2 * kBM);
+        d.per = kMode == kApply ? blocks * ((d.cols + kBN - 1) / kBN) : blocks * (blocks + 1) / 2;
+        d.tile0 = a.tiles;
+        a.tiles += d.per * d.count;
+    }
     cudaError_t e = cudaFuncSetAttribute(muon_gemm_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(2u * (unsigned)(a.tiles < pairs ? a.tiles : pairs));
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = kSmemBytes;
+    c.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &attr;
+    c.numAttrs = 1;
     const int id = kMode == kGram ? kKMuonGram : kMode == kPoly ? kKMuonPoly : kKMuonApply;
     timing_begin(id, s);
-    muon_gemm_kernel<kMode><<<a.tiles < sms ? a.tiles : sms, kThreads, kSmemBytes, s>>>(a);
+    e = cudaLaunchKernelEx(&c, muon_gemm_kernel<kMode>, a);
     timing_end(id, s);
-    return cudaGetLastError();
+    return e;
+}
+
+// Clusters of two that fit the device at once: more would wait for the first to end.
+cudaError_t pairs_of(int* pairs) {
+    static std::atomic<int> fit[64];
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (*pairs = fit[dev].load()) > 0) return cudaSuccess;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(muon_gemm_kernel<kApply>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(2 * (sms / 2));
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = kSmemBytes;
+    e = cudaOccupancyMaxActiveClusters(pairs, muon_gemm_kernel<kApply>, &c);
+    if (e == cudaSuccess && *pairs < 1) e = cudaErrorLaunchOutOfResources;
+    if (e == cudaSuccess && dev < 64) fit[dev].store(*pairs);
+    return e;
 }
 
 // One pass over the list: kItems matrices a launch.
@@ -1385,9 +1450,9 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
     }
     Plan plan;
     plan_of(t, n, plan);
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (plan.sizes.empty()) return cudaSuccess;
+    int pairs = 0;
+    cudaError_t e = pairs_of(&pairs);
     if (e != cudaSuccess) return e;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     std::vector<Item> items;
@@ -1454,15 +1519,13 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
             for (int mode = kGram; mode <= kApply; ++mode) {
                 GemmArgs ga;
                 ga.n = ng;
-                ga.tiles = 0;
                 for (int g = 0; g < ng; ++g) {
                     const Size& z = plan.sizes[g0 + g];
                     Group& d = ga.g[g];
                     auto half = [&](size_t at) { return reinterpret_cast<__half*>(ws + at); };
                     const float scale = i == 0 ? 1.0f / start[g0 + g] : 1.0f;  // of X, until the first apply
-                    const int blocks = (z.r + kBM - 1) / kBM, p = blocks / 2;
                     d.rows = z.r;
-                    d.per = p * (p + 1) + (blocks % 2) * (p + 1);
+                    d.count = z.count;
                     if (mode == kGram) {
                         d.map_m = d.map_n = x_rows[g][i & 1];
                         d.map_out = a_out[g];
@@ -1488,16 +1551,13 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
                         d.by = scale;
                         d.add_by = (float)q.a * scale;
                         d.steps = (z.r + kBK - 1) / kBK;
-                        d.per = blocks * ((z.k + kBN - 1) / kBN);
                     }
                     d.cols = mode == kApply ? z.k : z.r;
                     d.ld_add = d.ld_out = mode == kApply ? z.ld : z.ldr;
                     d.add_step = d.out_step = (long long)z.r * d.ld_out;
-                    d.tile0 = ga.tiles;
-                    ga.tiles += d.per * z.count;
                 }
-                e = mode == kGram ? launch_product<kGram>(ga, sms, s)
-                                  : mode == kPoly ? launch_product<kPoly>(ga, sms, s) : launch_product<kApply>(ga, sms, s);
+                e = mode == kGram ? launch_product<kGram>(ga, pairs, s)
+                                  : mode == kPoly ? launch_product<kPoly>(ga, pairs, s) : launch_product<kApply>(ga, pairs, s);
                 if (e != cudaSuccess) return e;
             }
         }
