@@ -164,7 +164,9 @@ __global__ void __launch_bounds__(kPassThreads) muon_momentum_kernel(const __gri
     if (threadIdx.x == 0) it.part[chunk] = sum;
 }
 
-// A 64 x 64 tile of a matrix by 256 threads: thread t has the columns 8 (t % 8) .. of the rows t / 8 and t / 8 + 32.
+// A 64 x 64 tile of a matrix by 256 threads: thread t has eight columns of the rows t / 8 and t / 8 + 32, neighbours
+// where rows are 16-byte aligned (kVec), else every eighth from t % 8 on: a warp's accesses then meet 32 bytes of a
+// row at a time (4530 x 1875, update: FIGURE_ODD).
 struct TileOf {
     int r0, c0;
     __device__ __forceinline__ TileOf(const Item& it) {
@@ -173,6 +175,27 @@ struct TileOf {
         c0 = t % tiles_c * kSide;
     }
 };
+template <bool kVec>
+__device__ __forceinline__ int column_of(int k) {
+    return kVec ? 8 * (threadIdx.x & 7) + k : (threadIdx.x & 7) + 8 * k;
+}
+// The values at column_of(0 .. 7) of a row from i on, of which `live` exist (kVec: all eight or none).
+template <bool kVec>
+__device__ __forceinline__ void load_row(float (&v)[8], const void* g, bool fp32, long long i, int live) {
+    if (kVec) {
+#pragma unroll
+        for (float& x : v) x = 0.0f;
+        if (column_of<true>(0) < live) load8<true>(v, g, fp32, i + column_of<true>(0), 8);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int c = column_of<false>(k);
+        v[k] = c >= live ? 0.0f
+               : fp32    ? static_cast<const float*>(g)[i + c]
+                         : __uint_as_float((uint32_t)static_cast<const uint16_t*>(g)[i + c] << 16);
+    }
+}
 // Where column c (0 .. 63) of row r of a turned tile lies in shared memory: 16-byte chunks exchanged by the row's
 // group of 8, so that threads of eight neighbouring row groups meet other banks.
 __device__ __forceinline__ int turned(int r, int c) { return r * kSide + ((((c >> 3) ^ (r >> 3)) & 7) << 3) + (c & 7); }
@@ -188,34 +211,29 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 }
 
 // X = u * start / (|u| + eps) in fp16, turned over where the matrix is tall.
-__global__ void __launch_bounds__(kPassThreads) muon_start_kernel(const __grid_constant__ PassArgs a) {
+template <bool kVec>
+__global__ void __launch_bounds__(kPassThreads, 6) muon_start_kernel(const __grid_constant__ PassArgs a) {
     __shared__ __align__(16) __half tile[kSide * kSide];
+    __shared__ float s_inv;
     const Item& it = item_of(a);
     float f;
     const bool ok = factor_of(a, f);
     const TileOf at(it);
-    const int cc = 8 * (threadIdx.x & 7), c = at.c0 + cc;
-    const bool tall = it.rows > it.cols, vec = it.cols % 8 == 0;
+    const bool tall = it.rows > it.cols;
     float u[2][8];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int r = at.r0 + (threadIdx.x >> 3) + 32 * k, live = !ok || r >= it.rows ? 0 : min(it.cols - c, 8);
-        const long long i = (long long)r * it.cols + c;
-        float m[8];
-        if (live == 8 && vec) {
-            load8<true>(u[k], it.g, it.g32, i, 8);
-            if (it.m != nullptr) load8<true>(m, it.m, true, i, 8);
-        } else {
-            load8<false>(u[k], it.g, it.g32, i, live);
-            if (it.m != nullptr) load8<false>(m, it.m, true, i, live);
-        }
+        const int r = at.r0 + (threadIdx.x >> 3) + 32 * k, live = !ok || r >= it.rows ? 0 : min(it.cols - at.c0, kSide);
+        const long long i = (long long)r * it.cols + at.c0;
+        load_row<kVec>(u[k], it.g, it.g32, i, live);
         if (it.m != nullptr) {
+            float m[8];
+            load_row<kVec>(m, it.m, true, i, live);
 #pragma unroll
             for (int j = 0; j < 8; ++j) u[k][j] = a.nesterov ? fmaf(a.mu, m[j], u[k][j] * f) : m[j];
         }
     }
     // (one warp adds: fp64 is slow here; root and quotient in fp32, one rounding each)
-    __shared__ float s_inv;
     if (threadIdx.x < 32) {
         double sq = 0.0;
         for (int i = threadIdx.x; i < it.parts; i += 32) sq += it.part[i];
@@ -230,80 +248,91 @@ __global__ void __launch_bounds__(kPassThreads) muon_start_kernel(const __grid_c
         const int rr = (threadIdx.x >> 3) + 32 * k, r = at.r0 + rr;
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[k][j] *= inv;
-        if (tall) {
+        if (kVec && !tall) {
+            const int c = at.c0 + column_of<true>(0);
+            if (r < it.rows && c < it.cols) *reinterpret_cast<uint4*>(it.x + (long long)r * it.ld + c) = pack8(u[k]);
+            continue;
+        }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) tile[turned(cc + j, rr)] = __float2half_rn(u[k][j]);
-        } else if (r < it.rows && c < it.cols) {  // (a row's padding takes zeros)
-            *reinterpret_cast<uint4*>(it.x + (long long)r * it.ld + c) = pack8(u[k]);
+        for (int j = 0; j < 8; ++j) {
+            const int c = column_of<kVec>(j);
+            tile[tall ? turned(c, rr) : turned(rr, c)] = __float2half_rn(u[k][j]);
         }
     }
-    if (!tall) return;
+    if (kVec && !tall) return;
     __syncthreads();
+    const int rows = tall ? it.cols : it.rows, cols = tall ? it.rows : it.cols, r0 = tall ? at.c0 : at.r0, c0 = tall ? at.r0 : at.c0;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int rr = (threadIdx.x >> 3) + 32 * k, r = at.c0 + rr, col = at.r0 + cc;
-        if (r < it.cols && col < it.rows)
+    for (int k = 0; k < 2; ++k) {  // (a row's padding takes zeros)
+        const int rr = (threadIdx.x >> 3) + 32 * k, r = r0 + rr, cc = 8 * (threadIdx.x & 7), col = c0 + cc;
+        if (r < rows && col < cols)
             *reinterpret_cast<uint4*>(it.x + (long long)r * it.ld + col) = *reinterpret_cast<const uint4*>(tile + turned(rr, cc));
     }
 }
 
 // p -= decay p + rate X, or p = X (orthogonalize).
-__global__ void __launch_bounds__(kPassThreads) muon_update_kernel(const __grid_constant__ PassArgs a) {
+template <bool kVec>
+__global__ void __launch_bounds__(kPassThreads, 5) muon_update_kernel(const __grid_constant__ PassArgs a) {
     __shared__ __align__(16) __half tile[kSide * kSide];
     const Item& it = item_of(a);
     float f;
     if (!factor_of(a, f)) return;
     const TileOf at(it);
-    const int cc = 8 * (threadIdx.x & 7), c = at.c0 + cc;
-    const bool tall = it.rows > it.cols, vec = it.cols % 8 == 0;
-    if (tall) {
+    const bool tall = it.rows > it.cols;
+    float* const p = it.master != nullptr ? it.master : static_cast<float*>(it.p);
+    // everything that is read, before anything is written
+    uint4 x[2];
+    float q[2][8];
+    const int rows = tall ? it.cols : it.rows, cols = tall ? it.rows : it.cols, r0 = tall ? at.c0 : at.r0, c0 = tall ? at.r0 : at.c0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int rr = (threadIdx.x >> 3) + 32 * k, cc = 8 * (threadIdx.x & 7);
+        x[k] = make_uint4(0, 0, 0, 0);
+        if (r0 + rr < rows && c0 + cc < cols) x[k] = __ldg(reinterpret_cast<const uint4*>(it.x + (long long)(r0 + rr) * it.ld + c0 + cc));
+    }
+    if (it.m != nullptr) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int rr = (threadIdx.x >> 3) + 32 * k, r = at.c0 + rr, col = at.r0 + cc;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (r < it.cols && col < it.rows) w = __ldg(reinterpret_cast<const uint4*>(it.x + (long long)r * it.ld + col));
-            const __half* h = reinterpret_cast<const __half*>(&w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) tile[turned(cc + j, rr)] = h[j];
+            const int r = at.r0 + (threadIdx.x >> 3) + 32 * k;
+            load_row<kVec>(q[k], p, true, (long long)r * it.cols + at.c0, r >= it.rows ? 0 : min(it.cols - at.c0, kSide));
         }
+    }
+    if (tall || !kVec) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<uint4*>(tile + turned((threadIdx.x >> 3) + 32 * k, 8 * (threadIdx.x & 7))) = x[k];
         __syncthreads();
     }
     const float lr = a.lr_dev != nullptr ? *a.lr_dev : 1.0f;
     const float rate = it.rate * lr, decay = it.decay * lr;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int rr = (threadIdx.x >> 3) + 32 * k, r = at.r0 + rr, live = r >= it.rows ? 0 : min(it.cols - c, 8);
-        if (live <= 0) continue;
-        const long long i = (long long)r * it.cols + c;
-        const uint4 w = tall ? *reinterpret_cast<const uint4*>(tile + turned(rr, cc))
-                             : __ldg(reinterpret_cast<const uint4*>(it.x + (long long)r * it.ld + c));
+        const int rr = (threadIdx.x >> 3) + 32 * k, r = at.r0 + rr, live = r >= it.rows ? 0 : min(it.cols - at.c0, kSide);
+        const long long i = (long long)r * it.cols + at.c0;
         float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __half2float(reinterpret_cast<const __half*>(&w)[j]);
-        const bool all = live == 8 && vec;
-        if (it.m != nullptr) {
-            float* p = it.master != nullptr ? it.master : static_cast<float*>(it.p);
-            float q[8];
-            if (all)
-                load8<true>(q, p, true, i, 8);
-            else
-                load8<false>(q, p, true, i, live);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = q[j] - fmaf(decay, q[j], rate * v[j]);
-            if (all)
-                store8<true>(p, i, v, 8);
-            else
-                store8<false>(p, i, v, live);
+        for (int j = 0; j < 8; ++j) {
+            const int c = column_of<kVec>(j);
+            const float y = kVec && !tall ? __half2float(reinterpret_cast<const __half*>(&x[k])[j])
+                                          : __half2float(tile[tall ? turned(c, rr) : turned(rr, c)]);
+            v[j] = it.m != nullptr ? q[k][j] - fmaf(decay, q[k][j], rate * y) : y;
         }
-        if (it.m != nullptr && it.master == nullptr) continue;
-        uint16_t* b = static_cast<uint16_t*>(it.p) + i;
-        if (all) {
-            *reinterpret_cast<uint4*>(b) =
-                make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        const bool both = it.m == nullptr || it.master != nullptr;
+        uint16_t* const b = static_cast<uint16_t*>(it.p) + i;
+        if (kVec) {
+            if (column_of<true>(0) >= live) continue;
+            if (it.m != nullptr) store8<true>(p, i + column_of<true>(0), v, 8);
+            if (both)
+                *reinterpret_cast<uint4*>(b + column_of<true>(0)) =
+                    make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < live) b[j] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j]));
+            for (int j = 0; j < 8; ++j) {
+                const int c = column_of<false>(j);
+                if (c >= live) continue;
+                if (it.m != nullptr) p[i + c] = v[j];
+                if (both) b[c] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j]));
+            }
         }
     }
 }
@@ -1350,20 +1379,25 @@ cudaError_t pairs_of(int* pairs) {
     return e;
 }
 
-// One pass over the list: kItems matrices a launch.
+// One pass over the list: kItems matrices a launch, those with 16-byte aligned rows in launches of their own where the
+// pass makes a difference between them.
 template <typename Blocks, typename Launch>
-cudaError_t pass(const std::vector<Item>& items, PassArgs& a, Blocks blocks_of, Launch launch) {
-    for (size_t i = 0; i < items.size(); i += kItems) {
-        a.n = (int)(items.size() - i < kItems ? items.size() - i : kItems);
+cudaError_t pass(const std::vector<Item>& items, PassArgs& a, bool apart, Blocks blocks_of, Launch launch) {
+    for (int vec = apart ? 0 : 1; vec < 2; ++vec) {
+        a.n = 0;
         int blocks = 0;
-        for (int j = 0; j < a.n; ++j) {
-            a.item[j] = items[i + j];
-            a.item[j].block0 = blocks;
-            blocks += blocks_of(items[i + j]);
+        for (size_t i = 0; i <= items.size(); ++i) {
+            if (a.n > 0 && (a.n == kItems || i == items.size())) {
+                launch(blocks, vec == 1);
+                const cudaError_t e = cudaGetLastError();
+                if (e != cudaSuccess) return e;
+                a.n = blocks = 0;
+            }
+            if (i == items.size() || (apart && (items[i].cols % 8 == 0) != (vec == 1))) continue;
+            a.item[a.n] = items[i];
+            a.item[a.n++].block0 = blocks;
+            blocks += blocks_of(items[i]);
         }
-        launch(blocks);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
@@ -1488,14 +1522,14 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
     a.grad_scale = step ? q.grad_scale : nullptr;
     a.lr_dev = q.lr_dev;
     auto tiles = [](const Item& it) { return ((it.rows + kSide - 1) / kSide) * ((it.cols + kSide - 1) / kSide); };
-    e = pass(items, a, [](const Item& it) { return it.parts; }, [&](int blocks) {
+    e = pass(items, a, false, [](const Item& it) { return it.parts; }, [&](int blocks, bool) {
         timing_begin(kKMuonMomentum, s);
         muon_momentum_kernel<<<blocks, kPassThreads, 0, s>>>(a);
         timing_end(kKMuonMomentum, s);
     });
-    if (e == cudaSuccess) e = pass(items, a, tiles, [&](int blocks) {
+    if (e == cudaSuccess) e = pass(items, a, true, tiles, [&](int blocks, bool vec) {
         timing_begin(kKMuonStart, s);
-        muon_start_kernel<<<blocks, kPassThreads, 0, s>>>(a);
+        (vec ? muon_start_kernel<true> : muon_start_kernel<false>)<<<blocks, kPassThreads, 0, s>>>(a);
         timing_end(kKMuonStart, s);
     });
     if (e != cudaSuccess) return e;
@@ -1570,9 +1604,9 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
                 items[k++].x = reinterpret_cast<__half*>(ws + z.x[1]) + (size_t)plan.z[i] * z.r * z.ld;
             }
     }
-    return pass(items, a, tiles, [&](int blocks) {
+    return pass(items, a, true, tiles, [&](int blocks, bool vec) {
         timing_begin(kKMuonUpdate, s);
-        muon_update_kernel<<<blocks, kPassThreads, 0, s>>>(a);
+        (vec ? muon_update_kernel<true> : muon_update_kernel<false>)<<<blocks, kPassThreads, 0, s>>>(a);
         timing_end(kKMuonUpdate, s);
     });
 }
