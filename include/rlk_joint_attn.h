@@ -719,7 +719,8 @@ rlk_status rlk_fp8_gemm(const rlk_fp8_product* items, int32_t n_items, void* str
  * rlk_orthogonalize stops at X: x in, its X out in bf16.
  *
  * X, A and B are held in fp16 (X is within 2^-9 of the formula's in the mean
- * square) with fp32 accumulators; the norm's squares are fp32 (magnitudes
+ * square; where the shorter side is at most 128, B is held in two fp16 numbers a
+ * value: with a few rows nothing averages) with fp32 accumulators; the norm's squares are fp32 (magnitudes
  * below 2^-63 vanish, a norm above 2^63 is infinite and gives X = 0), its sum
  * fp64; m and p are fp32. Sums have a fixed order without atomics: a matrix's
  * result does not depend on the list or its place in it. Matrices with an

@@ -1174,17 +1174,25 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
                     const int q = c / 8 + h, off = (q >> 3) * 16384 + chunk_at(row, q & 7);
                     const uint4 w = *reinterpret_cast<const uint4*>(generic + (sa - sbase) + off);
                     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t o[4];
+                    uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
-                        o[j] = pack_half(fmaf(a.b, y.x, a.c * __uint_as_float(v[8 * h + 2 * j])),
-                                         fmaf(a.b, y.y, a.c * __uint_as_float(v[8 * h + 2 * j + 1])));
+                        const float b0 = fmaf(a.b, y.x, a.c * __uint_as_float(v[8 * h + 2 * j]));
+                        const float b1 = fmaf(a.b, y.y, a.c * __uint_as_float(v[8 * h + 2 * j + 1]));
+                        hi[j] = pack_half(b0, b1);
+                        const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
+                        lo[j] = pack_half(b0 - z.x, b1 - z.y);
                     }
-                    const uint4 b = make_uint4(o[0], o[1], o[2], o[3]);
+                    // the rest of B that fp16 does not hold goes where A was: in a matrix of few rows nothing averages,
+                    // and a X + B X takes most of a X away again (1 x 9: 5e-3 off without it at most, 1.3e-3 with it)
+                    const uint4 b = make_uint4(hi[0], hi[1], hi[2], hi[3]), rest = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     *reinterpret_cast<uint4*>(generic + (sb - sbase) + off) = b;
-                    // (64 rows: once more in the rows from 64 on, so that the other half of TMEM's lanes holds B X too)
-                    if (R == 64) *reinterpret_cast<uint4*>(generic + (sb - sbase) + off + 64 * 128) = b;
+                    *reinterpret_cast<uint4*>(generic + (sa - sbase) + off) = rest;
+                    if (R == 64) {  // once more in the rows from 64 on, so that the other half of TMEM's lanes holds B X too
+                        *reinterpret_cast<uint4*>(generic + (sb - sbase) + off + 64 * 128) = b;
+                        *reinterpret_cast<uint4*>(generic + (sa - sbase) + off + 64 * 128) = rest;
+                    }
                 }
             }
         }
@@ -1195,14 +1203,15 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
         auto issue = [&](int t) {
             if (warp != 0) return;
             const uint32_t idesc = idesc_f16(128, 64 * min(kTileBlocks, blocks - kTileBlocks * t), true);
-            const uint64_t b0 = sdesc_sw128(sb, 16, 1024), x0 = sdesc_sw128(sx + kTileBlocks * t * block_bytes, block_bytes, 1024);
+            const uint64_t b0 = sdesc_sw128(sb, 16, 1024), r0 = sdesc_sw128(sa, 16, 1024);  // B and its rest
+            const uint64_t x0 = sdesc_sw128(sx + kTileBlocks * t * block_bytes, block_bytes, 1024);
 #pragma unroll
             for (int h = 0; h < R / 64; ++h)
                 if (elect_one())
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        mma_ss(tmem + kTile * (t & 1), b0 + h * (16384 >> 4) + 2 * q, x0 + (4 * h + q) * (2048 >> 4), idesc,
-                               h > 0 || q > 0 ? 1u : 0u);
+                    for (int q = 0; q < 8; ++q)
+                        mma_ss(tmem + kTile * (t & 1), (q < 4 ? b0 : r0) + h * (16384 >> 4) + 2 * (q & 3),
+                               x0 + (4 * h + (q & 3)) * (2048 >> 4), idesc, h > 0 || q > 0 ? 1u : 0u);
             if (elect_one()) mma_commit(bar_mma + 8 * (t & 1));
         };
         issue(0);

@@ -55,19 +55,21 @@ def _half(x):
     return x.astype(np.float16).astype(np.float64)
 
 
-def orthogonal(u, iterations=5, coefficients=POLYNOMIAL, eps=1e-7, stored=False):
+def orthogonal(u, iterations=5, coefficients=POLYNOMIAL, eps=1e-7, stored=False, lead=1.0):
     """X of u; stored: X, A and B rounded to fp16 as they are kept, X at the start with a power of two near the root
-    of its shorter side."""
+    of its shorter side times ``lead`` (another one draws other roundings). Matrices of up to 128 rows hold B in two
+    fp16 numbers a value."""
     u = np.asarray(u, np.float64)
     if u.shape[0] > u.shape[1]:
-        return orthogonal(u.T, iterations, coefficients, eps, stored).T
+        return orthogonal(u.T, iterations, coefficients, eps, stored, lead).T
     rnd = _half if stored else (lambda x: x)
-    start = 2.0 ** np.floor(0.5 * np.log2(u.shape[0])) if stored else 1.0
+    two = (lambda x: _half(x) + _half(x - _half(x))) if stored and u.shape[0] <= 128 else rnd
+    start = 2.0 ** np.floor(0.5 * np.log2(u.shape[0])) * lead if stored else 1.0
     x = rnd(u * (start / (np.sqrt((u * u).sum()) + eps)))
     a, b, c = coefficients
     for _ in range(iterations):
         gram = rnd(x @ x.T / start ** 2)
-        poly = rnd(b * gram + c * (gram @ gram))
+        poly = two(b * gram + c * (gram @ gram))
         x = rnd((a * x + poly @ x) / start)
         start = 1.0
     return x

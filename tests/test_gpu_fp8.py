@@ -218,6 +218,40 @@ def test_rows_do_not_depend_on_their_number(dev, k):
         assert Hh.bits_equal(gemm(dev, part, b, dtype=torch.float32), full[rows].contiguous()), rows
 
 
+def test_long_sums_of_few_tokens(dev):
+    """K past what the CTAs of a cluster hold for 16 tokens, and for 64."""
+    import torch
+    for rows, k in ((2, 45056), (2, 45200), (40, 12288), (40, 12400)):
+        x, w = rows_of(dev, 300, k, 31), rows_of(dev, 72, k, 32, size=0.1)
+        a, _, _ = quantize(dev, x, want="q")
+        b, _, _ = quantize(dev, w, square=True, want="q")
+        few, _, _ = quantize(dev, x[:rows], want="q")
+        got = gemm(dev, few, b, dtype=torch.float32)
+        assert Hh.bits_equal(got, gemm(dev, a, b, dtype=torch.float32)[:rows].contiguous()), (rows, k)
+        va, vb = few.values("e4m3"), b.values("e4m3")
+        assert_product(got, va @ vb.T, O.product_bound(va, vb), (rows, k))
+
+
+def test_places_past_32_bits(dev):
+    """An input and an output of more than 2^31 elements: the last rows as if they were alone."""
+    import torch
+    rows, k = 270000, 8192
+    g = torch.Generator(device=dev)
+    g.manual_seed(5)
+    x = torch.empty((rows, k), dtype=torch.bfloat16, device=dev)
+    x[-300:] = torch.randn((300, k), generator=g, device=dev).bfloat16()
+    x[:-300] = 0.5
+    op, last = (pkg.Fp8Projection(1, 0, t, k, n, device=dev) for t, n in ((rows, 8192), (300, 8192)))
+    w = (torch.randn((8192, k), generator=g, device=dev) / k ** 0.5).bfloat16()
+    op.set_weights((None, w))
+    last.set_weights((None, w))
+    y = op.forward((None, x.unsqueeze(0)))["y"][1][0, -300:].clone()
+    assert Hh.bits_equal(y, last.forward((None, x[None, -300:].contiguous()))["y"][1][0])
+    del op, x
+    # (turned operands: column sums over that many rows)
+    torch.cuda.empty_cache()
+
+
 def test_products_of_one_launch(dev):
     """Eight unlike products at once give what each gives alone."""
     import torch
@@ -337,6 +371,40 @@ def test_projection_captured_and_on_another_stream(dev):
     r2 = op.backward(dy, f2, stream=s)
     s.synchronize()
     assert all(Hh.bits_equal(p, q) for p, q in zip(want, (*f2["y"], *r2["dx"], *r2["dw"], *r2["db"])))
+
+
+def test_few_tokens_captured_and_beside_each_other(dev):
+    """The product of few tokens starts before the tokens are rounded: captured and replayed on inputs that change, and
+    two projections on two streams at once, give what each gives alone."""
+    import torch
+    made = [make(dev, 1, T, n_in, n_out, seed=i) for i, (T, n_in, n_out) in enumerate((((1, 16), 2560, 1536), ((5, 60), 1160, 4096)))]
+    for op, w, *_ in made:
+        op.set_weights(w)
+    g = torch.Generator(device=dev)
+    g.manual_seed(9)
+    inputs = [[tuple(torch.randn(t.shape, generator=g, device=dev).bfloat16() for t in x) for _ in range(6)] for _, _, _, x, _ in made]
+    want = [[[t.clone() for t in m[0].forward(x, m[2])["y"]] for x in xs] for m, xs in zip(made, inputs)]
+    for m, xs, ys in zip(made, inputs, want):
+        op, _, b, x, _ = m
+        out = op.forward(x, b)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(3):
+                op.forward(x, b, out=out)
+        for new, y in zip(xs, ys):
+            for t, n in zip(x, new):
+                t.copy_(n)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(Hh.bits_equal(p, q) for p, q in zip(out["y"], y))
+    streams = [torch.cuda.Stream() for _ in made]
+    torch.cuda.synchronize()
+    got = [[m[0].forward(x, m[2], stream=s)["y"] for x in xs for _ in (0, 1)] for m, xs, s in zip(made, inputs, streams)]
+    torch.cuda.synchronize()
+    for ys, zs in zip(want, got):
+        for i, z in enumerate(zs):
+            assert all(Hh.bits_equal(p, q) for p, q in zip(ys[i // 2], z))
+    pkg.rlk_joint_attn_check_status()
 
 
 def test_trace(dev):

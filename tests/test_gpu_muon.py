@@ -41,9 +41,11 @@ def gradient(dev, rows, cols, seed, dtype="fp32", low=4):
 
 
 def assert_orthogonal(got, u, where="", half=2.0 ** -9, **kw):
-    exact, stored = O.orthogonal(u, **kw), O.orthogonal(u, stored=True, **kw)
     norm = np.linalg.norm
-    d = norm(stored - exact)
+    exact = O.orthogonal(u, **kw)
+    d = norm(O.orthogonal(u, stored=True, **kw) - exact)
+    if min(u.shape) <= 16:
+        d = max(d, *(norm(O.orthogonal(u, stored=True, lead=f, **kw) - exact) for f in (1.1, 1.23, 1.37, 1.52, 1.71, 1.83, 1.97)))
     err = norm(f64(got) - exact)
     # a value's rounding to bf16 is off by half * 2 at most
     tol = 2 * d + 2 * half * norm(exact) + 1e-30
@@ -113,7 +115,7 @@ def state(dev, shapes, seed, bf16=True, dtype="bf16"):
 @pytest.mark.parametrize("bf16, dtype, nesterov", [(True, "bf16", True), (False, "fp32", False), (True, "fp32", False)])
 def test_step(dev, bf16, dtype, nesterov):
     import torch
-    shapes = [(64, 130), (257, 33), (130, 64), (5, 700), (64, 130)]
+    shapes = [(64, 130), (257, 333), (330, 164), (5, 700), (64, 130)]
     params, masters, m, grads = state(dev, shapes, 3, bf16, dtype)
     p0, m0 = [f64(t) for t in (masters or params)], [f64(t) for t in m]
     decay, share = [0.0, 0.1, 0.02, 0.5, 0.0], [1.0, 0.5, 2.0, 1.0, 0.0]
@@ -141,7 +143,7 @@ def test_step(dev, bf16, dtype, nesterov):
 def test_step_with_device_rate_and_bad_scale(dev):
     """A rate on the device gives the number's bytes; a factor that is not finite changes nothing."""
     import torch
-    shapes = [(100, 40), (40, 96)]
+    shapes = [(100, 40), (40, 96), (300, 200), (129, 1001)]
     runs = []
     for lr in (0.01, torch.tensor([0.01], device=dev)):
         params, masters, m, grads = state(dev, shapes, 9)
@@ -167,9 +169,58 @@ def test_list_order_and_many_sizes(dev):
     assert all(Hh.bits_equal(a, b) for a, b in zip(got, back))
 
 
+SMALL = [(1, 12289), (64, 12288), (12289, 64), (64, 513), (65, 512), (128, 4096), (4097, 128), (128, 4100), (100, 513), (17, 4097), (2, 1)]
+
+
+def test_edges_of_the_small_kernel(dev):
+    """The widest matrices that one kernel takes and the next ones, one column a CTA's slice and one more; odd rows and
+    aligned ones, tall and wide; among others and alone."""
+    xs = [gradient(dev, *s, i, "bf16" if i % 2 else "fp32") for i, s in enumerate(SMALL)]
+    got = pkg.orthogonalize(xs)
+    pkg.rlk_joint_attn_check_status()
+    for x, o in zip(xs, got):
+        assert_orthogonal(o, f64(x), tuple(x.shape))
+        assert Hh.bits_equal(pkg.orthogonalize([x])[0], o), tuple(x.shape)
+
+
+def test_values_that_the_first_look_misses(dev):
+    """X's scale in fp16 comes from a part of the matrix: values far above and below it elsewhere."""
+    import torch
+    for shape in ((60, 700), (700, 60), (100, 900)):
+        for size in (1e-7, 1.0, 1e6):
+            x = gradient(dev, *shape, 5)
+            x[: shape[0] // 2] *= size
+            x[:, -3:] *= 1e-3
+            assert_orthogonal(pkg.orthogonalize([x])[0], f64(x), (shape, size))
+        z = torch.zeros(shape, device=dev)
+        z[-1, -1] = 2.0
+        assert_orthogonal(pkg.orthogonalize([z])[0], f64(z), shape)
+
+
+def test_two_optimisers_at_once(dev):
+    """Objects of their own on two streams: small and large matrices."""
+    import torch
+    shapes = [(64, 700), (300, 260), (100, 2000), (260, 513)]
+    want, got = [], []
+    for run in (0, 1):
+        objects = []
+        for seed in (1, 2):
+            params, masters, m, grads = state(dev, shapes, seed)
+            objects.append((pkg.Muon(params, masters=masters, m=m, grads=grads), [*params, *masters, *m]))
+        streams = [torch.cuda.Stream(), torch.cuda.Stream()] if run else [None, None]
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for (opt, _), s in zip(objects, streams):
+                opt.step(stream=s)
+        torch.cuda.synchronize()
+        (got if run else want).extend(t for _, ts in objects for t in ts)
+    assert all(Hh.bits_equal(a, b) for a, b in zip(want, got))
+    pkg.rlk_joint_attn_check_status()
+
+
 def test_captured_step(dev):
     import torch
-    shapes = [(64, 200), (300, 130)]
+    shapes = [(64, 200), (300, 130), (100, 5000), (200, 260)]
     params, masters, m, grads = state(dev, shapes, 4)
     opt = pkg.Muon(params, masters=masters, m=m, grads=grads)
     lr = torch.tensor([0.02], device=dev)
