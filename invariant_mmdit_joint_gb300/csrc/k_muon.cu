@@ -647,23 +647,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) muon_ge
 // bounds it: the passes over g, m and p at the start and end, then the five iterations' chain of products,
 // exchanges and barriers (about FIGURE us).
 constexpr int kSmallItems = 128, kSmallThreads = 512;
-constexpr int kSliceBlocks = 8;  // 64-column blocks of a CTA's slice, as long as eight CTAs are enough
 template <int R>
 struct Small {  // R rows of X
-    static constexpr int kMostBlocks = R == 64 ? 24 : 8;  // that fit a CTA
+    static constexpr int kMostBlocks = R == 64 ? 24 : 8;   // 64-column blocks of X that fit a CTA
+    static constexpr int kSliceBlocks = R == 64 ? 9 : 8;   // of a CTA's slice, as long as eight CTAs are enough: two CTAs fit an SM
     static constexpr int kBlockBytes = R * 128;
     static constexpr int kABytes = R / 64 * 16384;         // A: 128 rows of R halves
     static constexpr int kPBytes = R == 64 ? 16384 : 65536;  // the CTA's part of A in fp32, then B
     static constexpr int kTile = R == 64 ? 128 : 256;       // columns of B X at a time, two such regions in TMEM
     static constexpr int kTmemCols = 2 * kTile;            // (64 rows: two CTAs an SM)
-    // Never so little that more CTAs would fit an SM than its TMEM serves: one of a group that waits for TMEM while the
-    // others wait for it in the cluster's barrier would wait forever.
-    static constexpr int kLeastSmem = (R == 64 ? 80 : 120) * 1024;
+    // Never so little that CTAs of clusters would share an SM whose TMEM does not serve them all: one that waits for
+    // TMEM while its cluster waits for it could wait forever. Two CTAs of 256 columns share one (80 KB each at least: no
+    // third fits; the 8-bit product of few tokens likewise), one of 512 columns has it alone (beside 152 KB no 80 fit).
+    static constexpr int kLeastSmem = (R == 64 ? 80 : 152) * 1024;
     static constexpr int smem(int blocks) {
         const int need = blocks * kBlockBytes + kABytes + kPBytes + 1024;
         return need > kLeastSmem ? need : kLeastSmem;
     }
-    static_assert(512 / kTmemCols * kLeastSmem + kLeastSmem > 228 * 1024, "");
+    static_assert(512 / kTmemCols * kLeastSmem + 80 * 1024 > 228 * 1024 && (R == 128 || 2 * smem(kSliceBlocks) <= 225 * 1024), "");
 };
 
 struct SmallItem {
@@ -671,16 +672,15 @@ struct SmallItem {
     float* master;
     const void* g;
     float* m;
-    int rows, cols, cta0;  // cta0: the group's first CTA
-    int ctas, width;       // CTAs of the group (a power of two), columns of a slice (a multiple of 64)
+    int rows, cols, width;  // width: columns of a slice (a multiple of 64)
     float rate, decay;
     bool g32;
 };
 struct SmallArgs {
     SmallItem item[kSmallItems];
-    int n, ctas, iterations, blocks;  // blocks: the widest slice's
+    int n, ctas, iterations, blocks;  // ctas: of a matrix (a cluster); blocks: the widest slice's
     float a, b, c, mu, eps;
-    bool nesterov, clusters;  // clusters: of more than one CTA
+    bool nesterov;
     const float *grad_scale, *lr_dev;
 };
 
@@ -960,7 +960,7 @@ __device__ __forceinline__ void write_slice(const SmallItem& it, const Slice& s,
 template <int R>
 __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __grid_constant__ SmallArgs a) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[4];  // products (two regions of TMEM take turns), the group
+    __shared__ __align__(8) uint64_t bars[2];  // products: two regions of TMEM take turns
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ float s_sums[kSmallThreads / 32], s_inv;
@@ -968,19 +968,15 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const float f = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
-    // (CTAs past the last group have nothing to do, and nobody waits for them)
-    if ((int)blockIdx.x >= a.ctas || !(fabsf(f) < INFINITY)) return;
-    int lo = 0, hi = a.n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if ((int)blockIdx.x >= a.item[mid].cta0)
-            lo = mid;
-        else
-            hi = mid - 1;
+    // The step's other launches of small matrices may run beside this one: they share nothing. Each waits for the one
+    // before it at its end, so that the last one's end is the end of all.
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int ctas = a.ctas, rank = blockIdx.x % ctas;
+    const SmallItem& it = a.item[blockIdx.x / ctas];
+    if (!(fabsf(f) < INFINITY)) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
     }
-    const SmallItem& it = a.item[lo];
-    const int ctas = it.ctas, rank = blockIdx.x - it.cta0;
-    const uint32_t first = cluster_rank() - rank;  // the group's first CTA in the cluster
     const bool tall = it.rows > it.cols;
     const int r = tall ? it.cols : it.rows, k = tall ? it.rows : it.cols;
     const int col0 = rank * it.width, live = max(0, min(it.width, k - col0));
@@ -989,13 +985,12 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t sx = sbase, sa = sbase + a.blocks * block_bytes, sb = sa + Small<R>::kABytes, sp = sb;
     uint8_t* const generic = smem_raw + (sbase - smem_u32(smem_raw));
-    const uint32_t bar_mma = smem_u32(&bars[0]), bar_group = smem_u32(&bars[2]);
+    const uint32_t bar_mma = smem_u32(&bars[0]);
 
     if (tid == 0) {
         abort_flag = 0;
         mbar_init(bar_mma, 1);
         mbar_init(bar_mma + 8, 1);
-        mbar_init(bar_group, ctas);
         fence_barrier_init();
     }
     if (warp == 0) {
@@ -1007,20 +1002,17 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (a.clusters) cluster_sync_all();  // the barriers exist before anyone arrives on them
     const uint32_t tmem = tmem_slot;
 
-    uint32_t group_phase = 0, mma_phase[2] = {0, 0};
+    uint32_t mma_phase[2] = {0, 0};
     auto bounded = [&](bool ok) {
         if (!ok) fail(&abort_flag);
     };
     auto group_sync = [&]() {
-        __syncthreads();
-        if (ctas == 1) return;
-        if (tid < ctas)
-            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(map_rank(bar_group, first + tid)) : "memory");
-        bounded(mbar_wait_cluster(bar_group, group_phase, &abort_flag, kWaitLimitNs));
-        group_phase ^= 1;
+        if (ctas > 1)
+            cluster_sync_all();
+        else
+            __syncthreads();
     };
     auto mma_wait = [&](int w) {
         bounded(mbar_wait(bar_mma + 8 * w, mma_phase[w], &abort_flag, kWaitLimitNs));
@@ -1039,7 +1031,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
     // ---- momentum, norm, X
     // What the passes read is fetched to L2 first, in a few instructions: X leaves little of the SM's memory to the
     // cache that plain loads in flight need.
-    {
+    const float* const w32 = it.master != nullptr ? it.master : static_cast<const float*>(it.p);
+    auto fetch = [&](bool weights) {
         const int es = it.g32 ? 4 : 2;
         const long long run = tall ? (long long)live * r : live, base = tall ? (long long)col0 * r : col0;
         const int runs = tall ? 1 : r, pieces = (int)((run + kPiece - 1) / kPiece);
@@ -1047,13 +1040,11 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
             const int i = e / pieces;
             const long long from = base + (long long)i * k + (long long)(e - i * pieces) * kPiece;
             const long long n = min((long long)kPiece, run - (long long)(e - i * pieces) * kPiece);
-            prefetch_l2(static_cast<const uint8_t*>(it.g) + from * es, n * es);
-            if (it.m != nullptr) {
-                prefetch_l2(it.m + from, n * 4);
-                prefetch_l2((it.master != nullptr ? it.master : static_cast<const float*>(it.p)) + from, n * 4);
-            }
+            if (!weights) prefetch_l2(static_cast<const uint8_t*>(it.g) + from * es, n * es);
+            if (it.m != nullptr) prefetch_l2(weights ? w32 + from : it.m + from, n * 4);
         }
-    }
+    };
+    fetch(false);
     Slice slice;
     slice.per_row = max(1, (live + kUnit - 1) / kUnit);
     slice.units = tall ? (live * r + kUnit - 1) / kUnit : live > 0 ? r * slice.per_row : 0;
@@ -1078,10 +1069,11 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
         for (int w = 0; w < kSmallThreads / 32; ++w) s += (double)s_sums[w];
         s_part = s;
     }
+    if (it.m != nullptr) fetch(true);  // (what the last pass reads)
     group_sync();
     if (tid == 0) {
         double s = 0.0;
-        for (int w = 0; w < ctas; ++w) s += ctas == 1 ? s_part : load_cluster_f64(map_rank(smem_u32(&s_part), first + w));
+        for (int w = 0; w < ctas; ++w) s += ctas == 1 ? s_part : load_cluster_f64(map_rank(smem_u32(&s_part), w));
         s_inv = 1.0f / (sqrtf((float)s) + a.eps);
     }
     publish();
@@ -1140,13 +1132,13 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
                 const uint32_t at = sp + i * R * 4 + ((q ^ (i & 7)) << 4);
                 float4 v = make_float4(0, 0, 0, 0);
                 for (int w = 0; w < ctas; ++w) {
-                    const float4 t = load_cluster(map_rank(at, first + w));
+                    const float4 t = load_cluster(map_rank(at, w));
                     v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
                 }
                 const uint32_t to = sa + (q >> 4) * 16384 + chunk_at(i, (q & 15) >> 1) + (q & 1) * 8;
                 const uint32_t lo = pack_half(v.x, v.y), hi = pack_half(v.z, v.w);
                 for (int w = 0; w < ctas; ++w)
-                    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(map_rank(to, first + w)), "r"(lo), "r"(hi) : "memory");
+                    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(map_rank(to, w)), "r"(lo), "r"(hi) : "memory");
             }
             group_sync();
         }
@@ -1266,6 +1258,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
         tc_fence_after();
         tmem_dealloc(tmem, Small<R>::kTmemCols);
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ host
@@ -1285,13 +1278,13 @@ struct Plan {
 };
 
 // CTAs of a small matrix's group, 0 for one that takes the products of whole launches: the fewest (a power of two)
-// with slices of 512 columns at most, or eight whose shared memory holds X. By its size alone, so that the sums over
+// with slices of 576 (above 64 rows: 512) columns at most, or eight whose shared memory holds X. By its size alone, so that the sums over
 // its columns have one order in every list.
 int small_ctas(const rlk_muon_matrix& t) {
     const long long r = t.rows < t.cols ? t.rows : t.cols, k = t.rows < t.cols ? t.cols : t.rows;
     if (r > 128) return 0;
     int n = 1;
-    while (n < 8 && k > n * 64LL * kSliceBlocks) n *= 2;
+    while (n < 8 && k > n * 64LL * (r <= 64 ? Small<64>::kSliceBlocks : Small<128>::kSliceBlocks)) n *= 2;
     return k <= n * 64LL * (r <= 64 ? Small<64>::kMostBlocks : Small<128>::kMostBlocks) ? n : 0;
 }
 
@@ -1420,20 +1413,10 @@ void rates_of(const rlk_muon_matrix& d, const rlk_muon_args& q, float& rate, flo
     decay = (float)(lr * d.weight_decay);
 }
 
-// The small matrices of up to R rows (and more than 64, if R is 128): groups of more CTAs first, so that each lies
-// within a cluster.
+// The small matrices of up to R rows (and more than 64, if R is 128), those of one number of CTAs a launch; `more`: a
+// launch of them came before, and this one may run beside it.
 template <int R>
-cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool step, cudaStream_t s) {
-    std::vector<int> order;
-    for (int ctas = 8; ctas > 0; ctas /= 2)
-        for (int i = 0; i < n; ++i) {
-            const long long r = t[i].rows < t[i].cols ? t[i].rows : t[i].cols;
-            if (r > 0 && (r <= 64) == (R == 64) && small_ctas(t[i]) == ctas) order.push_back(i);
-        }
-    if (order.empty()) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(muon_small_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Small<R>::smem(Small<R>::kMostBlocks));
-    if (e != cudaSuccess) return e;
+cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool step, bool& more, cudaStream_t s) {
     SmallArgs a;
     a.iterations = q.iterations;
     a.a = (float)q.a;
@@ -1444,13 +1427,43 @@ cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, b
     a.nesterov = q.nesterov != 0;
     a.grad_scale = step ? q.grad_scale : nullptr;
     a.lr_dev = step ? q.lr_dev : nullptr;
-    for (size_t i = 0; i < order.size();) {
-        const int size = small_ctas(t[order[i]]);  // of the cluster
-        a.n = a.ctas = a.blocks = 0;
-        a.clusters = size > 1;
-        for (; i < order.size() && a.n < kSmallItems; ++i) {
-            const rlk_muon_matrix& d = t[order[i]];
-            const int ctas = small_ctas(d);
+    auto launch = [&]() {
+        cudaError_t e = cudaFuncSetAttribute(muon_small_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             Small<R>::smem(Small<R>::kMostBlocks));
+        // (all of it for shared memory: two CTAs an SM)
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(muon_small_kernel<R>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t c{};
+        c.gridDim = dim3((unsigned)(a.n * a.ctas));
+        c.blockDim = dim3(kSmallThreads);
+        c.dynamicSmemBytes = Small<R>::smem(a.blocks);
+        c.stream = s;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = a.ctas;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        c.attrs = attr;
+        c.numAttrs = more ? 2 : 1;
+        timing_begin(kKMuonSmall, s);
+        e = cudaLaunchKernelEx(&c, muon_small_kernel<R>, a);
+        timing_end(kKMuonSmall, s);
+        more = true;
+        return e;
+    };
+    for (a.ctas = 8; a.ctas > 0; a.ctas /= 2) {
+        a.n = a.blocks = 0;
+        for (int i = 0; i <= n; ++i) {
+            if (a.n > 0 && (i == n || a.n == kSmallItems)) {
+                const cudaError_t e = launch();
+                if (e != cudaSuccess) return e;
+                a.n = a.blocks = 0;
+            }
+            if (i == n) break;
+            const rlk_muon_matrix& d = t[i];
+            const long long r = d.rows < d.cols ? d.rows : d.cols, k = d.rows < d.cols ? d.cols : d.rows;
+            if (r == 0 || (r <= 64) != (R == 64) || small_ctas(d) != a.ctas) continue;
             SmallItem& it = a.item[a.n++];
             it.p = d.p;
             it.master = step ? d.master : nullptr;
@@ -1458,37 +1471,19 @@ cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, b
             it.m = step ? d.m : nullptr;
             it.rows = (int)d.rows;
             it.cols = (int)d.cols;
-            it.cta0 = a.ctas;
-            it.ctas = ctas;
-            const long long k = d.rows < d.cols ? d.cols : d.rows;
-            it.width = (int)up((k + ctas - 1) / ctas, 64);
+            it.width = (int)up((k + a.ctas - 1) / a.ctas, 64);
             rates_of(d, q, it.rate, it.decay);
             it.g32 = d.g_dtype == RLK_FP32;
-            a.ctas += ctas;
             if (it.width / 64 > a.blocks) a.blocks = it.width / 64;
         }
-        cudaLaunchConfig_t c{};
-        c.gridDim = dim3((unsigned)up(a.ctas, size));
-        c.blockDim = dim3(kSmallThreads);
-        c.dynamicSmemBytes = Small<R>::smem(a.blocks);
-        c.stream = s;
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = size;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        c.attrs = &attr;
-        c.numAttrs = 1;
-        timing_begin(kKMuonSmall, s);
-        e = cudaLaunchKernelEx(&c, muon_small_kernel<R>, a);
-        timing_end(kKMuonSmall, s);
-        if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
 
 cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool step, void* workspace, cudaStream_t s) {
+    bool more = false;
     for (const auto small : {run_small<64>, run_small<128>}) {
-        const cudaError_t e = small(t, n, q, step, s);
+        const cudaError_t e = small(t, n, q, step, more, s);
         if (e != cudaSuccess) return e;
     }
     Plan plan;
