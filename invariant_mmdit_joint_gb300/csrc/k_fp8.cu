@@ -214,6 +214,7 @@ template <bool kFp32, bool kE5m2>
 __global__ void __launch_bounds__(kQuantThreads) fp8_quant_kernel(const __grid_constant__ QuantArgs a) {
     __shared__ __align__(16) QuantSmem sm;
     constexpr int kRoom = kE5m2 ? 15 : 8;
+    asm volatile("griddepcontrol.launch_dependents;");
     int tile;
     const QuantItem& it = item_of(a, tile);
     const int tid = threadIdx.x, lane = tid & 31;
@@ -359,6 +360,8 @@ constexpr int kFoldThreads = 256, kFoldCols = 32, kFoldRuns = kFoldThreads / kFo
 // Column sums: every 8th row tile in ascending order, then these 8 runs.
 __global__ void __launch_bounds__(kFoldThreads) fp8_fold_kernel(const __grid_constant__ FoldArgs a) {
     __shared__ float sm[kFoldRuns][kFoldCols];
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     int i = 0;
     while (i + 1 < a.n && (int)blockIdx.x >= a.item[i + 1].block0) ++i;
     const FoldItem& it = a.item[i];
@@ -513,6 +516,22 @@ cudaError_t smem_once(int bytes) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kKernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e == cudaSuccess && dev < 64) done |= 1ull << dev;
     return e;
+}
+
+// A launch that may set itself up while the one before it ends: its kernel waits (griddepcontrol.wait) before it reads.
+template <typename Args>
+cudaError_t launch_after(void (*kernel)(Args), int grid, int threads, int smem, cudaStream_t s, const Args& a) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)grid);
+    c.blockDim = dim3((unsigned)threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &attr;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, a);
 }
 
 // ---- few tokens ----
@@ -790,6 +809,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gem
         tmem_alloc_pair(smem_u32(&tmem_slot), kTmemCols);
         tmem_relinquish_pair();
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // (the kernels before it round what it reads)
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
@@ -1003,9 +1023,9 @@ cudaError_t launch_pair(GemmArgs& a, int sms, cudaStream_t s) {
         if (dev < 64) fit[dev].store(pairs);
     }
     timing_begin(kKFp8Gemm, s);
-    fp8_gemm_pair_kernel<<<2 * (a.tiles < pairs ? a.tiles : pairs), kThreads, Pair::kSmemBytes, s>>>(a);
+    e = launch_after(fp8_gemm_pair_kernel, 2 * (a.tiles < pairs ? a.tiles : pairs), kThreads, Pair::kSmemBytes, s, a);
     timing_end(kKFp8Gemm, s);
-    return cudaGetLastError();
+    return e;
 }
 
 // The CTAs that share a tile's K: enough for two an SM of all the tiles, at most one a chunk, and enough for each CTA's
@@ -1130,9 +1150,9 @@ cudaError_t launch_fp8_quant(const rlk_fp8_quant* q, int n, cudaStream_t s) {
         if (kinds >> kind & 1) e = launch_quant_kind(q, n, kind, s);
     if (e != cudaSuccess || blocks == 0) return e;
     timing_begin(kKFp8Fold, s);
-    fp8_fold_kernel<<<blocks, kFoldThreads, 0, s>>>(f);
+    e = launch_after(fp8_fold_kernel, blocks, kFoldThreads, 0, s, f);
     timing_end(kKFp8Fold, s);
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_fp8_gemm(const rlk_fp8_product* p, int n, cudaStream_t s) {
