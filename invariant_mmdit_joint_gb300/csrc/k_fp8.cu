@@ -31,6 +31,7 @@
 #include "rlk_sm100.cuh"
 #include "rlk_tmap.h"
 
+#include <algorithm>
 #include <atomic>
 
 RLK_DEFINE_STRICT_PROBE(probe_fp8_tu)
@@ -830,7 +831,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gem
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (int t = first; ok && t < a.tiles; t += step) {
+            for (int n = 0, t; ok && (t = tile_of_turn(n, first, step)) < a.tiles; ++n) {
                 const TileAt at = tile(t);
                 const GemmItem& g = a.item[at.item];
                 for (int kb = 0; kb < g.blocks; kb += Pair::kStageBlocks, ++it) {
@@ -866,7 +867,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gem
             const uint64_t f0 = sdesc_sw128(stage_f(0), 16, 1024), t0 = sdesc_sw128(stage_t(0), 16, 1024);
             const uint64_t s0 = sdesc_noswizzle(scales(0), 0, 128);
             uint32_t chunks = 0;  // of all tiles
-            for (int t = first; t < a.tiles; t += step) chunks += (a.item[tile(t).item].blocks + kChunkBlocks - 1) / kChunkBlocks;
+            for (int n = 0, t; (t = tile_of_turn(n, first, step)) < a.tiles; ++n) chunks += (a.item[tile(t).item].blocks + kChunkBlocks - 1) / kChunkBlocks;
             uint32_t st = 0, phase = 0, chunk = 0;
             bool ok = true;
             auto copy_scales = [&](uint32_t c) {  // a chunk's, one chunk ahead of its products
@@ -881,7 +882,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gem
                 return true;
             };
             if (chunks > 0) ok = copy_scales(0);
-            for (int t = first; ok && t < a.tiles; t += step) {
+            for (int n = 0, t; ok && (t = tile_of_turn(n, first, step)) < a.tiles; ++n) {
                 const GemmItem& g = a.item[tile(t).item];
                 const int blocks = g.blocks;
                 for (int kb = 0; ok && kb < blocks; ++chunk) {
@@ -937,7 +938,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gem
     } else if (warp == kWarpScale) {
         uint32_t chunk = 0;
         bool ok = true;
-        for (int t = first; ok && t < a.tiles; t += step) {
+        for (int n = 0, t; ok && (t = tile_of_turn(n, first, step)) < a.tiles; ++n) {
             const TileAt at = tile(t);
             const GemmItem& g = a.item[at.item];
             for (int kb = 0; kb < g.blocks; kb += kChunkBlocks, ++chunk) {
@@ -964,7 +965,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gem
         const uint32_t buffer = scales(kScaleRing) + (warp - kWarpEpilogue) * Pair::kOutBytes;
         uint32_t chunk = 0;
         bool ok = true;
-        for (int t = first; ok && t < a.tiles; t += step) {
+        for (int n = 0, t; ok && (t = tile_of_turn(n, first, step)) < a.tiles; ++n) {
             const TileAt at = tile(t);
             const GemmItem& g = a.item[at.item];
             float acc[Pair::kHalf];
@@ -998,6 +999,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) fp8_gem
 }
 
 cudaError_t launch_pair(GemmArgs& a, int sms, cudaStream_t s) {
+    std::stable_sort(a.item, a.item + a.n, [](const GemmItem& x, const GemmItem& y) { return x.blocks > y.blocks; });
     a.tiles = 0;
     for (int i = 0; i < a.n; ++i) {
         GemmItem& g = a.item[i];

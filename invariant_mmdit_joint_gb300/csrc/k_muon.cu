@@ -26,6 +26,7 @@
 
 #include <cuda_fp16.h>
 #include <atomic>
+#include <algorithm>
 #include <math.h>
 #include <new>
 #include <type_traits>
@@ -525,7 +526,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) muon_ge
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (int t = first; ok && t < a.tiles; t += step) {
+            for (int n = 0, t; ok && (t = tile_of_turn(n, first, step)) < a.tiles; ++n) {
                 const TileAt at = tile_at<kMode>(a, t);
                 const Group& g = a.g[at.g];
                 const int m0 = at.m0 + kBM * rank, n0 = at.n0 + kBN / 2 * rank;
@@ -561,7 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) muon_ge
             constexpr int kStepB = (kMode == kApply ? 2048 : 32) >> 4;
             uint32_t st = 0, phase = 0, local = 0;
             bool ok = true;
-            for (int t = first; ok && t < a.tiles; t += step, ++local) {
+            for (int n = 0, t; ok && (t = tile_of_turn(n, first, step)) < a.tiles; ++n, ++local) {
                 const int buf = local & 1;
                 const uint32_t use = local >> 1;
                 if (use > 0 && !__all_sync(0xffffffffu, mbar_wait_cluster(bar_free + 8 * buf, (use - 1) & 1, &abort_flag, kWaitLimitNs))) {
@@ -599,7 +600,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) muon_ge
         const uint32_t buffer = sbase + kStages * kStageBytes + (warp - kWarpEpilogue) * kOutBytes;
         uint32_t local = 0;
         bool ok = true;
-        for (int t = first; t < a.tiles; t += step, ++local) {
+        for (int n = 0, t; (t = tile_of_turn(n, first, step)) < a.tiles; ++n, ++local) {
             const int buf = local & 1;
             if (!warp_wait(bar_acc + 8 * buf, (local >> 1) & 1, &abort_flag)) {
                 ok = false;
@@ -1557,9 +1558,14 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
             for (int mode = kGram; mode <= kApply; ++mode) {
                 GemmArgs ga;
                 ga.n = ng;
-                for (int g = 0; g < ng; ++g) {
+                int order[kGroups];  // the longest sums first
+                for (int g = 0; g < ng; ++g) order[g] = g;
+                auto length = [&](int g) { return mode == kGram ? plan.sizes[g0 + g].k : plan.sizes[g0 + g].r; };
+                std::stable_sort(order, order + ng, [&](int x, int y) { return length(x) > length(y); });
+                for (int n_g = 0; n_g < ng; ++n_g) {
+                    const int g = order[n_g];
                     const Size& z = plan.sizes[g0 + g];
-                    Group& d = ga.g[g];
+                    Group& d = ga.g[n_g];
                     auto half = [&](size_t at) { return reinterpret_cast<__half*>(ws + at); };
                     const float scale = i == 0 ? 1.0f / start[g0 + g] : 1.0f;  // of X, until the first apply
                     d.rows = z.r;

@@ -167,6 +167,10 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
         }
     }
 }
+// The n-th tile of worker w of `workers`, to and fro: the tiles with the longest sums come first, and who has the longest
+// of one turn has the shortest of the next.
+__device__ __forceinline__ int tile_of_turn(int n, int w, int workers) { return n * workers + (n & 1 ? workers - 1 - w : w); }
+
 // TMA load into this CTA whose bytes are counted on the first CTA's barrier (the pair's CTAs differ in bit 24 of a
 // shared::cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
