@@ -125,15 +125,14 @@ __device__ __forceinline__ double block_sum(double v) {
 }
 
 // New momentum, and the partial sums of u's squares: a chunk of consecutive elements a CTA, eight neighbours a thread
-// and turn in fp32, the turns in fp64.
+// and turn, four turns in fp32 (32 squares), then fp64, which is slow here.
 __global__ void __launch_bounds__(kPassThreads) muon_momentum_kernel(const __grid_constant__ PassArgs a) {
     const Item& it = item_of(a);
     float f;
     if (!factor_of(a, f)) return;
     const int chunk = blockIdx.x - it.block0;
     const long long lo = chunk * it.chunk, hi = min(lo + it.chunk, it.n);
-    double sum = 0.0;
-    auto eight = [&](auto vec, long long i, int live) {
+    auto eight = [&](auto vec, long long i, int live, float& sq) {
         constexpr bool kVec = decltype(vec)::value;
         float u[8];
         load8<kVec>(u, it.g, it.g32, i, live);
@@ -148,18 +147,22 @@ __global__ void __launch_bounds__(kPassThreads) muon_momentum_kernel(const __gri
             }
             store8<kVec>(it.m, i, m, live);
         }
-        float sq = 0.0f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) sq = fmaf(u[k], u[k], sq);
-        sum += (double)sq;
     };
+    double sum = 0.0;
     // (chunks start at multiples of 8 elements: 16-byte aligned)
-#pragma unroll 2
-    for (long long i = lo + 8 * threadIdx.x; i < hi; i += 8 * kPassThreads) {
-        if (i + 8 <= hi)
-            eight(std::true_type{}, i, 8);
-        else
-            eight(std::false_type{}, i, (int)(hi - i));
+    for (long long i0 = lo + 8 * threadIdx.x; i0 < hi; i0 += 4 * 8 * kPassThreads) {
+        float sq = 0.0f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const long long i = i0 + t * 8 * kPassThreads;
+            if (i + 8 <= hi)
+                eight(std::true_type{}, i, 8, sq);
+            else if (i < hi)
+                eight(std::false_type{}, i, (int)(hi - i), sq);
+        }
+        sum += (double)sq;
     }
     sum = block_sum(sum);
     if (threadIdx.x == 0) it.part[chunk] = sum;
