@@ -665,7 +665,8 @@ size_t rlk_fp8_scale_row_bytes(int64_t k);  /* 0 for k < 1 */
 
 /* Limits: 0 <= rows < 2^31 - 128, 1 <= cols <= 2^20 a multiple of 8, x_stride
  * >= cols (elements) with every row 16-byte aligned (else RLK_ERR_ALIGNMENT).
- * Written buffers must not overlap another of the call. rows 0 writes nothing
+ * Written buffers must not overlap another of the call (a buffer reaches from its
+ * first row's start to its last one's end). rows 0 writes nothing
  * (but zeros to col_sum). */
 typedef struct rlk_fp8_quant {
     const void* x;      /* [rows, cols] */
@@ -684,7 +685,8 @@ typedef struct rlk_fp8_quant {
 
 /* Limits: 0 <= m, n < 2^31 - 256, n a multiple of 8, 1 <= k < 2^31 - 128,
  * d_stride >= n a multiple of 8 elements. m or n 0 computes nothing. d must
- * not overlap another buffer of the call. */
+ * not overlap another buffer of the call (from its first row's start to its last
+ * one's end: column slices of one tensor go into calls of their own). */
 typedef struct rlk_fp8_product {
     const void* a;          /* [m, k] codes */
     const uint8_t* a_scale; /* [m, ceil(k / 128)] */

@@ -16,16 +16,22 @@
 // over rows needs), or both, and the columns' sums (a bias gradient).
 // fp8_quant_rows_kernel: the rows' blocks alone. Both bound by HBM.
 //
-// fp8_gemm_kernel: tcgen05.mma kind::mxf8f6f4 with block scales. The features
-// (b's rows) are the 128 rows of an accumulator, the tokens (a's rows) its
-// columns: a call with few tokens takes a narrow accumulator (N = 16 or 64)
-// and reads each weight once, with the same sums in the same order as a call
-// with many (N = 224), so that a token's result does not depend on how many
-// there are. Persistent CTAs; warps: 0 TMA producer, 1 MMA issuer and TMEM
-// owner, 2 scale loader (gathers four blocks' bytes a row into the 128 x 4
-// layout that tcgen05.cp spreads over TMEM), 4 .. 11 the sums of the chunks and
-// the output. TMEM: two accumulators of N columns, so that a chunk is read out
-// while the next one is computed, and two sets of scales. Every wait is bounded.
+// The products: tcgen05.mma kind::mxf8f6f4 with block scales. The features (b's
+// rows) are the rows of an accumulator, the tokens (a's rows) its columns, so
+// that a call with few tokens takes a narrow accumulator and reads each weight
+// once. Warps: 0 TMA producer, 1 MMA issuer and TMEM owner (the whole warp runs
+// the loop, one elected lane issues: in a loop of one lane the operands are moved
+// to uniform registers one by one, which took as long as the products), 2 scale
+// loader (gathers four blocks' bytes a row into the 128 x 4 layout that tcgen05.cp
+// spreads over TMEM), 4 .. 11 the sums of the chunks and the output. Every
+// accumulator starts a chunk anew; the chunks meet in fp32 registers or shared
+// memory, always in ascending order: a token's bytes do not depend on the kernel
+// that computed them. Every wait is bounded.
+//   fp8_gemm_pair_kernel  CTA pairs, 256 features x 224 tokens: 3.1 PFLOP/s (8704
+//       tokens, 2560 -> 7680: 110 us); without the output 3.9. Bound by the tensor
+//       pipe (76% active), and by shared memory's port while the output passes.
+//   fp8_gemm_few_kernel   up to 64 tokens, 128 features x 16 or 64 tokens, the chunks
+//       shared out over a cluster. Bound by latency: launch, first loads, join.
 #include "rlk_device.cuh"
 #include "rlk_internal.h"
 #include "rlk_sm100.cuh"
@@ -163,7 +169,7 @@ __device__ __forceinline__ const QuantItem& item_of(const QuantArgs& a, int& til
 
 // Blocks along the rows alone: 8 lanes a block, each with two runs of eight columns; two rows a thread, no shared memory
 // (bound by instructions: 16 lanes with one run each and the same work beside it took 13.5 of them a value and 14.0 us
-// for 8704 rows of 2560, FIGURE_ROWS).
+// // for 8704 rows of 2560; 12.0 so, HBM's floor 9.9).
 template <bool kFp32, bool kE5m2>
 __global__ void __launch_bounds__(kQuantThreads) fp8_quant_rows_kernel(const __grid_constant__ QuantArgs a) {
     constexpr int kRoom = kE5m2 ? 15 : 8, kRows = kRowsTile / 32;
@@ -210,7 +216,8 @@ struct QuantSmem {
 };
 
 // Blocks along the columns (and along the rows, or of 128 x 128), column sums: a 128 x 128 tile a CTA, eight rows of
-// eight columns a thread, kept as they were loaded (8704 x 2560 both ways: FIGURE_TILE).
+// eight columns a thread, kept as they were loaded (8704 x 2560 both ways: 18.8 us cold, HBM's floor
+// 13.2; 65% of the issue slots).
 template <bool kFp32, bool kE5m2>
 __global__ void __launch_bounds__(kQuantThreads) fp8_quant_kernel(const __grid_constant__ QuantArgs a) {
     __shared__ __align__(16) QuantSmem sm;

