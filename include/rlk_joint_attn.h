@@ -639,7 +639,7 @@ rlk_status rlk_grad_norm(const rlk_adamw_tensor* tensors, int32_t n_tensors, flo
  * Layout: row r's codes start at r * rlk_fp8_row_bytes(K) (K rounded up to a
  * multiple of 16), its scales at r * rlk_fp8_scale_row_bytes(K) (the number of
  * blocks rounded up to a multiple of 4). What lies behind a row's last scale
- * is neither read nor written; codes behind a row's end are not read, and in
+ * is not written and takes no part; codes behind a row's end take none, and in
  * qt they may be written as zeros.
  *
  * The three products of a projection y = x W^T + b sum over different axes, so
@@ -659,6 +659,8 @@ rlk_status rlk_grad_norm(const rlk_adamw_tensor* tensors, int32_t n_tensors, flo
 #define RLK_E4M3 0
 #define RLK_E5M2 1
 #define RLK_FP8_MAX_ITEMS 8
+#define RLK_FP8_FEW_ROWS 16
+#define RLK_FP8_FEW_K 12288
 
 size_t rlk_fp8_row_bytes(int64_t k);        /* 0 for k < 1 */
 size_t rlk_fp8_scale_row_bytes(int64_t k);  /* 0 for k < 1 */
@@ -688,8 +690,8 @@ typedef struct rlk_fp8_quant {
  * not overlap another buffer of the call (from its first row's start to its last
  * one's end: column slices of one tensor go into calls of their own). */
 typedef struct rlk_fp8_product {
-    const void* a;          /* [m, k] codes */
-    const uint8_t* a_scale; /* [m, ceil(k / 128)] */
+    const void* a;          /* [m, k] codes, or bf16 rows (a_rows) */
+    const uint8_t* a_scale; /* [m, ceil(k / 128)]; NULL with a_rows */
     const void* b;          /* [n, k] codes */
     const uint8_t* b_scale; /* [n, ceil(k / 128)] */
     const void* bias;       /* bf16 [n] or NULL */
@@ -698,6 +700,10 @@ typedef struct rlk_fp8_product {
     int32_t a_format, b_format; /* RLK_E4M3 or RLK_E5M2 */
     int32_t d_dtype;        /* RLK_BF16 or RLK_FP32 */
     int32_t accumulate;     /* 1: d += the product (fp32 d only) */
+    int32_t a_rows;         /* 1: a is dense bf16 [m, k], rounded to a_format on the way: the bytes of rlk_fp8_quantize
+                               and this call after it, in one launch. For a few tokens: m <= RLK_FP8_FEW_ROWS, k a
+                               multiple of 8 up to RLK_FP8_FEW_K, and in every product of the call or in none */
+    int32_t reserved;       /* 0 */
 } rlk_fp8_product;
 
 /* Bytes of the column sums' workspace (128 rows' sums); 0 for an invalid size.

@@ -153,7 +153,7 @@ class AdamwArgs(ctypes.Structure):
 
 
 FP8_FORMATS = {"e4m3": 0, "e5m2": 1}
-FP8_MAX_ITEMS = 8
+FP8_MAX_ITEMS, FP8_FEW_ROWS, FP8_FEW_K = 8, 16, 12288
 
 
 class Fp8Quant(ctypes.Structure):
@@ -167,7 +167,7 @@ class Fp8Product(ctypes.Structure):
     """rlk_fp8_product: one product of two operands in codes."""
     _fields_ = [(n, ctypes.c_void_p) for n in ("a", "a_scale", "b", "b_scale", "bias", "d")] + \
                [(n, ctypes.c_int64) for n in ("m", "n", "k", "d_stride")] + \
-               [(n, ctypes.c_int32) for n in ("a_format", "b_format", "d_dtype", "accumulate")]
+               [(n, ctypes.c_int32) for n in ("a_format", "b_format", "d_dtype", "accumulate", "a_rows", "reserved")]
 
 
 class MuonMatrix(ctypes.Structure):
@@ -1603,8 +1603,13 @@ class Fp8Projection(_Pairs):
         quant, product = self._calls.get(train) or self._fwd_calls(train, ws)
         py, xt, xs = p["y"], p.get("xt"), p.get("xt_scale")
         for n, i in enumerate(self._live):  # (the rest of a call stays what it is)
-            e, f = quant[n], product[n]
-            e.x, f.bias, f.d = px[i], pb[i], py[i]
+            f = product[n]
+            f.bias, f.d = pb[i], py[i]
+            if quant is None:
+                f.a = px[i]
+                continue
+            e = quant[n]
+            e.x = px[i]
             if train:
                 e.qt, e.qt_scale = xt[i], xs[i]
         self._run(quant, product, handle)
@@ -1613,6 +1618,12 @@ class Fp8Projection(_Pairs):
     def _fwd_calls(self, train, ws):
         n_in, n_out, bf16 = self.n_in, self.n_out, self.out_dtype.itemsize == 2
         quant, product = [], []
+        if not train and max(self._tokens) <= FP8_FEW_ROWS and n_in <= FP8_FEW_K:  # a few tokens: rounded by the product
+            for i in self._live:
+                t, w = self._tokens[i], self._at[i]
+                product.append(Fp8Product(None, None, w[0], w[1], None, None, t, n_out, n_in, n_out, 0, 0, 0 if bf16 else 1, 0, 1, 0))
+            self._calls[train] = None, (Fp8Product * len(product))(*product)
+            return self._calls[train]
         for i in self._live:
             q, s, t, w = ws + self._fwd[i][0], ws + self._fwd[i][1], self._tokens[i], self._at[i]
             quant.append(Fp8Quant(None, q, s, None, None, None, None, t, n_in, n_in, 0, 0, 0, 0))
@@ -1621,9 +1632,10 @@ class Fp8Projection(_Pairs):
         return self._calls[train]
 
     def _run(self, quant, product, handle):
-        rc = lib().rlk_fp8_quantize(quant, len(quant), handle)
-        if rc:
-            _check(rc, "rlk_fp8_quantize")
+        if quant is not None:
+            rc = lib().rlk_fp8_quantize(quant, len(quant), handle)
+            if rc:
+                _check(rc, "rlk_fp8_quantize")
         if product is not None:
             rc = lib().rlk_fp8_gemm(product, len(product), handle)
             if rc:

@@ -401,17 +401,19 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 __device__ int g_status_fp8;
 
-// A call with few tokens: NT columns (16 or 64) of an accumulator for each chunk of K, all at hand until the end.
-template <int NT>
+// A call with few tokens: NT columns (16 or 64) of an accumulator for each chunk of K, all at hand until the end. kRaw:
+// the tokens come as bf16 rows and are rounded here, by the warps that have nothing to do until then.
+template <int NT, bool kRaw>
 struct Few {
-    static constexpr int kStageBytes = kFBytes + NT * kBK;
+    static constexpr int kStageBytes = kFBytes + (kRaw ? 0 : NT * kBK);
     static constexpr int kStages = NT == 16 ? 5 : 4;
-    static constexpr int kSlots = NT == 16 ? 11 : 3;            // chunks a CTA takes
+    static constexpr int kSlots = kRaw ? 3 : NT == 16 ? 11 : 3;  // chunks a CTA takes
     static constexpr int kScaleCol = kSlots * NT;               // two sets of 8 columns, 16 apart
     static constexpr uint32_t kTmemCols = 256;                  // two CTAs an SM
     static constexpr int kSumBytes = 128 * NT * 4;              // a chunk's sums, in the stages' place when these are done
     static constexpr int kSumsBytes = kSlots * kSumBytes > kStages * kStageBytes ? kSlots * kSumBytes : kStages * kStageBytes;
-    static constexpr int kSmemBytes = kSumsBytes + kSlots * 1024 + 1024;
+    static constexpr int kTokenBytes = kRaw ? kSlots * kChunkBlocks * NT * kBK : 0;  // their codes, for all of the CTA's K
+    static constexpr int kSmemBytes = kSumsBytes + kTokenBytes + kSlots * 1024 + 1024;
     // (a third CTA on an SM would wait for TMEM, perhaps while its cluster waits for it)
     static_assert(kScaleCol + 32 <= (int)kTmemCols && 2 * kSmemBytes <= 226 * 1024 && 3 * kSmemBytes > 228 * 1024, "");
 };
@@ -421,9 +423,10 @@ struct GemmItem {
     CUtensorMap map_d;         // pairs: d [m, n], box of 32 features
     const uint8_t *sf, *st;
     const uint16_t* bias;
+    const void* rows;  // bf16 tokens [m, k] to be rounded (few tokens), or null
     void* d;
     long long d_stride;
-    int ldsf, ldst, m, n, blocks, tiles_f, tile0;
+    int k, ldsf, ldst, m, n, blocks, tiles_f, tile0;
     uint32_t idesc;  // formats of the operands
     bool fp32, accumulate;
 };
@@ -553,9 +556,10 @@ __device__ __forceinline__ float load_cluster(uint32_t addr) {
 // few tokens' weights stream through many SMs. Each CTA leaves its chunks' sums in shared memory; then each adds up a
 // part of the features over all chunks in ascending order: the sums and bytes of any other number of CTAs or tokens.
 // Before it waits for the kernel that rounds the tokens, a CTA has its weights fetched to L2.
-template <int NT>
+// (16 bf16 tokens rounded here: one launch for two.)
+template <int NT, bool kRaw>
 __global__ void __launch_bounds__(kThreads, 2) fp8_gemm_few_kernel(const __grid_constant__ GemmArgs a) {
-    using C = Few<NT>;
+    using C = Few<NT, kRaw>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * C::kStages + C::kSlots + 1];
     __shared__ uint32_t tmem_slot;
@@ -577,14 +581,14 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_gemm_few_kernel(const __grid_
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
     auto stage_f = [&](int st) { return sbase + st * C::kStageBytes; };
     auto stage_t = [&](int st) { return sbase + st * C::kStageBytes + kFBytes; };
-    const uint32_t scales = sbase + C::kSumsBytes;
+    const uint32_t tokens = sbase + C::kSumsBytes, scales = tokens + C::kTokenBytes;
     const uint32_t bar_full = smem_u32(&bars[0]), bar_empty = bar_full + 8 * C::kStages;
     const uint32_t bar_scale = bar_empty + 8 * C::kStages, bar_acc = bar_scale + 8 * C::kSlots;
 
     if (tid == 0) {
         abort_flag = 0;
         for (int i = 0; i < C::kStages; ++i) mbar_init(bar_full + 8 * i, 1), mbar_init(bar_empty + 8 * i, 1);
-        for (int i = 0; i < C::kSlots; ++i) mbar_init(bar_scale + 8 * i, 1);
+        for (int i = 0; i < C::kSlots; ++i) mbar_init(bar_scale + 8 * i, kRaw ? 9 : 1);
         mbar_init(bar_acc, 1);
         fence_barrier_init();
     }
@@ -616,14 +620,14 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_gemm_few_kernel(const __grid_
                 }
                 mbar_expect_tx(bar_full + 8 * st, C::kStageBytes);
                 tma_load_2d(stage_f(st), &g.map_f, bar_full + 8 * st, (b0 + it) * kBK, at.f0);
-                tma_load_2d(stage_t(st), &g.map_t, bar_full + 8 * st, (b0 + it) * kBK, at.t0);
+                if (!kRaw) tma_load_2d(stage_t(st), &g.map_t, bar_full + 8 * st, (b0 + it) * kBK, at.t0);
             }
             if (!ok) fail(&abort_flag);
             for (int u = max(0, it - C::kStages); u < it; ++u)
                 mbar_wait_drain(bar_full + 8 * (u % C::kStages), (u / C::kStages) & 1, kWaitLimitNs);
         }
     } else if (warp == kWarpMma) {
-        const uint64_t f0 = sdesc_sw128(stage_f(0), 16, 1024), t0 = sdesc_sw128(stage_t(0), 16, 1024);
+        const uint64_t f0 = sdesc_sw128(stage_f(0), 16, 1024), t0 = sdesc_sw128(kRaw ? tokens : stage_t(0), 16, 1024);
         const uint64_t s0 = sdesc_noswizzle(scales, 0, 128);
         uint32_t st = 0, phase = 0;
         bool ok = true;
@@ -646,7 +650,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_gemm_few_kernel(const __grid_
                     break;
                 }
                 tc_fence_after();
-                const uint64_t f = f0 + st * (C::kStageBytes >> 4), tk = t0 + st * (C::kStageBytes >> 4);
+                const uint64_t f = f0 + st * (C::kStageBytes >> 4);
+                const uint64_t tk = t0 + (kRaw ? (c * kChunkBlocks + kb) * (NT * kBK >> 4) : st * (C::kStageBytes >> 4));
                 if (elect_one()) {
 #pragma unroll
                     for (int j = 0; j < kBK / 32; ++j) mma_mx(acc, f + 2 * j, tk + 2 * j, id, sa, sb, j > 0 || kb > 0 ? 1u : 0u);
@@ -664,9 +669,42 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_gemm_few_kernel(const __grid_
         for (int c = 0; c < n_chunks; ++c) {
             uint32_t w[2][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) gather_scales(w[i], g, i, at, b0 + c * kChunkBlocks, lane);
+            for (int i = 0; i < (kRaw ? 1 : 2); ++i) gather_scales(w[i], g, i, at, b0 + c * kChunkBlocks, lane);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) put_scales(scales + c * 1024 + 512 * i + 16 * lane, w[i]);
+            for (int i = 0; i < (kRaw ? 1 : 2); ++i) put_scales(scales + c * 1024 + 512 * i + 16 * lane, w[i]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_scale + 8 * c);
+        }
+    } else if (kRaw && warp >= kWarpEpilogue) {
+        // two tokens a warp, 16 lanes each: a block's 128 values to codes at once, a chunk's four loaded together
+        const bool e5m2 = g.idesc >> 10 & 1;
+        const int row = 2 * (warp - kWarpEpilogue) + (lane >> 4), cg = lane & 15;
+        for (int c = 0; c < n_chunks; ++c) {
+            Eight<false> v[kChunkBlocks];
+#pragma unroll
+            for (int b = 0; b < kChunkBlocks; ++b) {
+                const int col = (b0 + c * kChunkBlocks + b) * kBK + 8 * cg;
+                if (row < g.m && col < g.k)
+                    v[b].load(g.rows, (long long)row * g.k + col);
+                else
+                    v[b].clear();
+            }
+#pragma unroll
+            for (int b = 0; b < kChunkBlocks; ++b) {
+                float m = v[b].top();
+#pragma unroll
+                for (int k = 8; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+                const int e = scale_exponent(m, e5m2 ? 15 : 8);
+                const float s = power_of_two(-e);
+                const uint2 q = e5m2 ? codes_of<false, true>(v[b], s) : codes_of<false, false>(v[b], s);
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(tokens + (c * kChunkBlocks + b) * (NT * kBK) + row * kBK +
+                                                                      (((cg >> 1) ^ (row & 7)) << 4) + (cg & 1) * 8),
+                             "r"(q.x), "r"(q.y)
+                             : "memory");
+                if (cg == 0)
+                    asm volatile("st.shared.u8 [%0], %1;" ::"r"(scales + c * 1024 + 512 + row * 16 + b), "r"(e + 127) : "memory");
+            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_scale + 8 * c);
@@ -693,8 +731,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_gemm_few_kernel(const __grid_
         cluster_sync_all();
     else
         __syncthreads();
-    const int rows = 128 / ctas, first = rank * rows, tokens = min(NT, g.m - at.t0);
-    for (int e = tid; e < rows * tokens; e += kThreads) {
+    const int rows = 128 / ctas, first = rank * rows, count = min(NT, g.m - at.t0);
+    for (int e = tid; e < rows * count; e += kThreads) {
         const int i = first + e % rows, tk = e / rows, f = at.f0 + i;
         if (f >= g.n) continue;
         float sum = 0.0f;
@@ -1039,8 +1077,9 @@ cudaError_t launch_pair(GemmArgs& a, int sms, cudaStream_t s) {
 
 // The CTAs that share a tile's K: enough for two an SM of all the tiles, at most one a chunk, and enough for each CTA's
 // TMEM (0: it is not).
-template <int NT>
+template <int NT, bool kRaw>
 int few_ctas(const rlk_fp8_product* p, int n, int sms) {
+    constexpr int kSlots = Few<NT, kRaw>::kSlots;
     long long tiles = 0, chunks = 1;
     for (int i = 0; i < n; ++i) {
         if (p[i].m == 0 || p[i].n == 0) continue;
@@ -1049,11 +1088,11 @@ int few_ctas(const rlk_fp8_product* p, int n, int sms) {
         chunks = c > chunks ? c : chunks;
     }
     int ctas = 1;
-    while (ctas < 8 && (chunks > (long long)ctas * Few<NT>::kSlots || (2 * ctas <= chunks && 2 * ctas * tiles <= 2 * sms))) ctas *= 2;
-    return chunks <= (long long)ctas * Few<NT>::kSlots ? ctas : 0;
+    while (ctas < 8 && (chunks > (long long)ctas * kSlots || (2 * ctas <= chunks && 2 * ctas * tiles <= 2 * sms))) ctas *= 2;
+    return chunks <= (long long)ctas * kSlots ? ctas : 0;
 }
 
-template <int NT>
+template <int NT, bool kRaw>
 cudaError_t launch_few(GemmArgs& a, int ctas, cudaStream_t s) {
     a.tiles = 0;
     a.ctas = ctas;
@@ -1064,12 +1103,12 @@ cudaError_t launch_few(GemmArgs& a, int ctas, cudaStream_t s) {
         g.idesc |= idesc_mx(128, NT);
         a.tiles += g.tiles_f * ((g.m + NT - 1) / NT);
     }
-    cudaError_t e = smem_once<fp8_gemm_few_kernel<NT>>(Few<NT>::kSmemBytes);
+    cudaError_t e = smem_once<fp8_gemm_few_kernel<NT, kRaw>>(Few<NT, kRaw>::kSmemBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t c{};
     c.gridDim = dim3((unsigned)(a.tiles * ctas));
     c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = Few<NT>::kSmemBytes;
+    c.dynamicSmemBytes = Few<NT, kRaw>::kSmemBytes;
     c.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1080,7 +1119,7 @@ cudaError_t launch_few(GemmArgs& a, int ctas, cudaStream_t s) {
     c.attrs = attr;
     c.numAttrs = 2;
     timing_begin(kKFp8Gemm, s);
-    e = cudaLaunchKernelEx(&c, fp8_gemm_few_kernel<NT>, a);
+    e = cudaLaunchKernelEx(&c, fp8_gemm_few_kernel<NT, kRaw>, a);
     timing_end(kKFp8Gemm, s);
     return e;
 }
@@ -1175,17 +1214,19 @@ cudaError_t launch_fp8_gemm(const rlk_fp8_product* p, int n, cudaStream_t s) {
     if (err != cudaSuccess) return err;
     // The accumulator's columns: the narrowest that takes every token, if K is not too long for it, else 224.
     int nt = kPairTokens, ctas = 0;
+    const bool raw = p[0].a_rows != 0;  // (16 tokens at most, of 12288 values at most)
     if (most <= 64) {
         nt = most <= 16 ? 16 : 64;
-        ctas = nt == 16 ? few_ctas<16>(p, n, sms) : few_ctas<64>(p, n, sms);
+        ctas = raw ? few_ctas<16, true>(p, n, sms) : nt == 16 ? few_ctas<16, false>(p, n, sms) : few_ctas<64, false>(p, n, sms);
         if (ctas == 0) nt = kPairTokens;
     }
+    if (raw && nt != 16) return cudaErrorInvalidValue;
     for (int i = 0; i < n; ++i) {
         const rlk_fp8_product& e = p[i];
         if (e.m == 0 || e.n == 0) continue;
         GemmItem& g = a.item[a.n++];
         const long long ld = rlk_fp8_row_bytes(e.k);
-        if (!codes_map(&g.map_f, e.b, e.n, e.k, ld, 128) || !codes_map(&g.map_t, e.a, e.m, e.k, ld, nt == kPairTokens ? nt / 2 : nt))
+        if (!codes_map(&g.map_f, e.b, e.n, e.k, ld, 128) || (!raw && !codes_map(&g.map_t, e.a, e.m, e.k, ld, nt == kPairTokens ? nt / 2 : nt)))
             return cudaErrorInvalidValue;
         if (nt == kPairTokens) {
             const bool fp32 = e.d_dtype == RLK_FP32;
@@ -1199,6 +1240,8 @@ cudaError_t launch_fp8_gemm(const rlk_fp8_product* p, int n, cudaStream_t s) {
         g.sf = e.b_scale;
         g.st = e.a_scale;
         g.bias = static_cast<const uint16_t*>(e.bias);
+        g.rows = raw ? e.a : nullptr;
+        g.k = (int)e.k;
         g.d = e.d;
         g.d_stride = e.d_stride;
         g.ldsf = g.ldst = (int)rlk_fp8_scale_row_bytes(e.k);
@@ -1211,7 +1254,10 @@ cudaError_t launch_fp8_gemm(const rlk_fp8_product* p, int n, cudaStream_t s) {
         g.accumulate = e.accumulate != 0;
     }
     if (a.n == 0) return cudaSuccess;
-    return nt == 16 ? launch_few<16>(a, ctas, s) : nt == 64 ? launch_few<64>(a, ctas, s) : launch_pair(a, sms, s);
+    return raw        ? launch_few<16, true>(a, ctas, s)
+           : nt == 16 ? launch_few<16, false>(a, ctas, s)
+           : nt == 64 ? launch_few<64, false>(a, ctas, s)
+                      : launch_pair(a, sms, s);
 }
 
 int read_and_clear_status_fp8(cudaStream_t s) {

@@ -1517,16 +1517,18 @@ static rlk_status fp8_gemm_impl(const rlk_fp8_product* p, int32_t n, void* strea
         if (e.m < 0 || e.m >= kMaxFp8Rows || e.n < 0 || e.n >= kMaxFp8Rows || e.n % 8 != 0 || e.k < 1 || e.k >= kMaxFp8Rows ||
             e.d_stride < e.n || e.d_stride > (1LL << 40) || !format_ok(e.a_format) || !format_ok(e.b_format) ||
             (e.d_dtype != RLK_BF16 && e.d_dtype != RLK_FP32) || (e.accumulate != 0 && e.accumulate != 1) ||
-            (e.accumulate == 1 && e.d_dtype != RLK_FP32))
+            (e.accumulate == 1 && e.d_dtype != RLK_FP32) || (e.a_rows != 0 && e.a_rows != 1) || e.a_rows != p[0].a_rows ||
+            e.reserved != 0 ||
+            (e.a_rows == 1 && (e.m > RLK_FP8_FEW_ROWS || e.k > RLK_FP8_FEW_K || e.k % 8 != 0 || e.a_scale != nullptr)))
             return RLK_ERR_INVALID_ARG;
         if (e.m == 0 || e.n == 0) continue;
         const rlk_status st = check_ptrs({e.a, e.b, e.d}, {e.bias});
         if (st != RLK_OK) return st;
-        if (e.a_scale == nullptr || e.b_scale == nullptr) return RLK_ERR_INVALID_ARG;
+        if ((e.a_scale == nullptr && e.a_rows == 0) || e.b_scale == nullptr) return RLK_ERR_INVALID_ARG;
         if (!aligned4(e.a_scale) || !aligned4(e.b_scale) || e.d_stride % 8 != 0) return RLK_ERR_ALIGNMENT;
         tiles += (e.m + 15) / 16 * ((e.n + 127) / 128);
         const size_t row = rlk_fp8_row_bytes(e.k), srow = rlk_fp8_scale_row_bytes(e.k), es = e.d_dtype == RLK_FP32 ? 4 : 2;
-        ranges.add(e.a, (size_t)e.m * row, false);
+        ranges.add(e.a, e.a_rows == 1 ? (size_t)e.m * e.k * 2 : (size_t)e.m * row, false);
         ranges.add(e.a_scale, (size_t)e.m * srow, false);
         ranges.add(e.b, (size_t)e.n * row, false);
         ranges.add(e.b_scale, (size_t)e.n * srow, false);

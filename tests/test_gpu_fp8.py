@@ -232,6 +232,28 @@ def test_long_sums_of_few_tokens(dev):
         assert_product(got, va @ vb.T, O.product_bound(va, vb), (rows, k))
 
 
+@pytest.mark.parametrize("m, n, k", [(1, 8, 8), (1, 15360, 2560), (16, 136, 12288), (13, 2560, 10240), (5, 264, 1160), (16, 128, 128),
+                                     (2, 200, 4104)])
+@pytest.mark.parametrize("fa", ["e4m3", "e5m2"])
+def test_few_rows_rounded_on_the_way(dev, m, n, k, fa):
+    """bf16 rows as the operand: the bytes of rounding them first."""
+    import torch
+    x = rows_of(dev, m, k, m + k)
+    if m > 2:
+        x[1, 3], x[2, k - 1] = float("nan"), float("-inf")
+    a, _, _ = quantize(dev, x, fa, want="q")
+    b, _, _ = quantize(dev, rows_of(dev, n, k, 7, size=0.1), square=True, want="q")
+    bias = torch.randn(n, device=dev).bfloat16()
+    for dtype in (torch.bfloat16, torch.float32):
+        want = gemm(dev, a, b, fa, bias=bias, dtype=dtype)
+        got = torch.full((m, n), 7.0, dtype=dtype, device=dev)
+        item = pkg.Fp8Product(x.data_ptr(), None, b.q.data_ptr(), b.s.data_ptr(), bias.data_ptr(), got.data_ptr(), m, n, k, n,
+                              pkg.FP8_FORMATS[fa], 0, int(dtype == torch.float32), 0, 1, 0)
+        pkg.rlk_fp8_gemm((pkg.Fp8Product * 1)(item))
+        pkg.rlk_joint_attn_check_status()
+        assert Hh.bits_equal(torch.nan_to_num(got), torch.nan_to_num(want)) and bool((got.isnan() == want.isnan()).all())
+
+
 def test_places_past_32_bits(dev):
     """An input and an output of more than 2^31 elements: the last rows as if they were alone."""
     import torch

@@ -114,7 +114,10 @@ def gemm(L, *items, n=None):
     (dict(accumulate=2, d_dtype=1), 1), (dict(a=None), 1), (dict(a_scale=None), 1), (dict(b=None), 1), (dict(b_scale=None), 1),
     (dict(d=None), 1), (dict(d_stride=268), 3), (dict(a=P + 8), 3), (dict(b=P + 2 * STEP + 8), 3), (dict(d=P + 5 * STEP + 8), 3),
     (dict(bias=P + 4 * STEP + 2), 3), (dict(a_scale=P + STEP + 2), 3), (dict(b_scale=P + 3 * STEP + 1), 3),
-    (dict(d=P), 1), (dict(d=P + 3 * STEP - 1024), 1), (dict(d=P + 4 * STEP), 1)])
+    (dict(d=P), 1), (dict(d=P + 3 * STEP - 1024), 1), (dict(d=P + 4 * STEP), 1), (dict(reserved=1), 1), (dict(a_rows=2), 1),
+    (dict(a_rows=1, m=17, a_scale=None), 1), (dict(a_rows=1, m=16, k=12296, a_scale=None), 1),
+    (dict(a_rows=1, m=16, k=100, a_scale=None), 1), (dict(a_rows=1, m=16), 1),
+    (dict(a_rows=1, m=16, a_scale=None, d=P + 16 * 1000 * 2 - 16), 1)])
 def test_product_fails_closed(L, over, code):
     assert gemm(L, product(**over)) == code
 
@@ -126,6 +129,9 @@ def test_product_lists(L):
         assert gemm(L, product()) == 5 and gemm(L, product(bias=None, d_dtype=1, accumulate=1)) == 5
         assert gemm(L, product(), product(d=P + 6 * STEP)) == 5  # operands may be shared
         assert gemm(L, product(m=0, a=None, d=None)) == 5
+        few = dict(a_rows=1, m=16, a_scale=None)
+        assert gemm(L, product(**few)) == 5 and gemm(L, product(**few, k=12288), product(**few, d=P + 6 * STEP)) == 5
+    assert gemm(L, product(a_rows=1, m=16, a_scale=None), product(d=P + 6 * STEP)) == 1  # in every product or in none
 
 
 # ------------------------------------------------------------------ Muon
