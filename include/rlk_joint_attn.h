@@ -747,7 +747,8 @@ typedef struct rlk_muon_matrix {
 
 typedef struct rlk_muon_args {
     double lr, momentum, update_rms; /* >= 0, momentum < 1; the rates' products in fp32's range */
-    double a, b, c;          /* the polynomial: finite */
+    double a, b, c;          /* the polynomial: magnitudes up to 1e6; where it takes X, A or B past
+                                fp16's range (65504), the results are not finite */
     double eps;              /* 2^-126 .. 1 */
     const float* lr_dev;     /* device, or NULL: read instead of lr */
     const float* grad_scale; /* device, or NULL (1). Not finite: every tensor is left as it was */
