@@ -349,7 +349,7 @@ enum Mode { kGram = 0, kPoly = 1, kApply = 2 };
 constexpr int kGroups = 8;  // sizes a launch takes
 // A cluster of two CTAs computes a tile of 256 rows (128 each) x 256 columns; each holds its rows' operand and half of
 // the columns': the pair's products read half as much shared memory, and TMA brings 32 KB instead of 48 a k-step and
-// CTA (one CTA a tile was bound by that: X X^T of four projections 136 -> 113 us, B X 206 -> 174, 2.3 PFLOP/s).
+// CTA (one CTA a tile was bound by that: X X^T of four projections 136 -> 113 us, B X 206 -> 174, 1.5 PFLOP/s).
 constexpr int kBM = 128, kBN = 256, kBK = 64, kStages = 6;
 constexpr int kOutBytes = 32 * 32 * 2;  // an epilogue warp's buffer: 32 rows of 32 columns
 constexpr int kThreads = 384;
