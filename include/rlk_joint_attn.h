@@ -726,11 +726,11 @@ rlk_status rlk_fp8_gemm(const rlk_fp8_product* items, int32_t n_items, void* str
  *        at full rank: update_rms is then the update's root mean square)
  * rlk_orthogonalize stops at X: x in, its X out in bf16.
  *
- * X, A and B are held in fp16 (X is within 2^-9 of the formula's in the mean
- * square; where the shorter side is at most 128, B is held in two fp16 numbers a
- * value: with a few rows nothing averages) with fp32 accumulators; the norm's squares are fp32 (magnitudes
- * below 2^-63 vanish, a norm above 2^63 is infinite and gives X = 0), its sum
- * fp64; m and p are fp32. Sums have a fixed order without atomics: a matrix's
+ * X, A less a multiple of the identity, and the polynomial's part that goes with
+ * it are held in fp16, with fp32 accumulators (X is within 2^-9 of the formula's
+ * in the mean square, within 2^-10 where singular values are much alike); the
+ * norm's squares are fp32 (magnitudes below 2^-63 vanish, a norm above 2^63 is
+ * infinite and gives X = 0), its sum fp64; m and p are fp32. Sums have a fixed order without atomics: a matrix's
  * result does not depend on the list or its place in it. Matrices with an
  * infinity or NaN become NaN, as their formulas do. */
 typedef struct rlk_muon_matrix {
@@ -747,8 +747,8 @@ typedef struct rlk_muon_matrix {
 
 typedef struct rlk_muon_args {
     double lr, momentum, update_rms; /* >= 0, momentum < 1; the rates' products in fp32's range */
-    double a, b, c;          /* the polynomial: magnitudes up to 1e6; where it takes X, A or B past
-                                fp16's range (65504), the results are not finite */
+    double a, b, c;          /* the polynomial: magnitudes up to 1e6; where it takes X, A or a part of
+                                itself past fp16's range (65504), the results are not finite */
     double eps;              /* 2^-126 .. 1 */
     const float* lr_dev;     /* device, or NULL: read instead of lr */
     const float* grad_scale; /* device, or NULL (1). Not finite: every tensor is left as it was */

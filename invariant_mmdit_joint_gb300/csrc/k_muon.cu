@@ -10,7 +10,8 @@
 // multiplied by a power of two near sqrt(r), where its entries are about 1 /
 // sqrt(k) as they are at the end), and its 11 bits keep the update within 2^-9
 // of the formula's where bf16's 8 lose a percent: small singular values grow
-// 3.4 times an iteration, and the roundings with them. A and B are
+// 3.4 times an iteration, and the roundings with them. A is kept less a multiple
+// of the identity (Poly). A and B are
 // symmetric: only tiles that meet the lower triangle are computed, and stored
 // on both sides.
 //
@@ -365,7 +366,7 @@ struct Group {
     CUtensorMap map_m;   // the operand of the 128 rows: [z][rows][K], box 64 x 128 x 1
     CUtensorMap map_n;   // the operand of the kBN columns: gram, poly the same, box 64 x 128; apply X, box 64 x 64 (MN-major)
     CUtensorMap map_out; // out, box 32 x 32 x 1
-    const __half* add;   // poly: A; apply: X: added times `add_by`
+    const __half* add;   // gram: the identity (not read); poly: D; apply: X: added times `add_by`
     __half* out;
     long long add_step, out_step;  // from matrix to matrix
     int rows, cols;      // of the output (gram, poly: r x r)
@@ -412,6 +413,23 @@ __device__ __forceinline__ void fail(volatile int* abort_flag) {
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, kWaitLimitNs));
 }
+// One iteration's polynomial in D = A - shift I, an identity for any shift:
+//   a X + (b A + c A A) X = (a + b shift + c shift^2) X + ((b + 2 c shift) D + c D D) X
+// A's diagonal, which holds most of it, is near the square of X's singular values. With their expected square taken off
+// it, little is rounded to fp16: near 1, where A's roundings were multiplied by b = -4.8 and B's were 2^-11 of 2.7, the
+// two coefficients are 0.7 (X off by 6e-4 to 8e-4 of its norm, 1.4e-3 to 3e-3 without). What is expected is what the
+// polynomial makes of r equal singular values, 1 at most: a rule on r alone, so that a matrix's result depends on
+// nothing else (its own trace gains 5 percent more, and takes a pass over A before it is rounded).
+struct Poly {
+    float a, b, c, square;
+    __host__ __device__ float shift() const { return fminf(square, 1.0f); }  // (1 for a NaN)
+    __host__ __device__ float of_x() const { return fmaf(fmaf(c, shift(), b), shift(), a); }
+    __host__ __device__ float of_d() const { return fmaf(2.0f * c, shift(), b); }
+    __host__ __device__ void next() {
+        const float p = fmaf(fmaf(c, square, b), square, a);
+        square *= p * p;
+    }
+};
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -420,8 +438,8 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
     return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// 32 columns from j on of row i (a warp: 32 rows from i - lane): out = by * v + add_by * add, and on the other
-// side of the diagonal.
+// 32 columns from j on of row i (a warp: 32 rows from i - lane): out = by * v + add_by * add (gram: the identity), and
+// on the other side of the diagonal.
 template <int kMode>
 __device__ __forceinline__ void store32(const Group& g, int z, float (&v)[32], int i, int j, uint32_t buffer) {
     const int lane = threadIdx.x & 31, i0 = i - lane;
@@ -450,7 +468,7 @@ __device__ __forceinline__ void store32(const Group& g, int z, float (&v)[32], i
 #pragma unroll
         for (int c = 0; c < 32; ++c)
             if (live && c <= lane) {
-                const __half h = __float2half_rn(v[c]);
+                const __half h = __float2half_rn(kMode == kGram && c == lane ? v[c] + g.add_by : v[c]);
                 row[c] = h;
                 out[(long long)(j + c) * g.ld_out + i] = h;
             }
@@ -652,7 +670,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) muon_ge
 // 128-byte swizzle makes a block a K-major operand of the slice's X X^T and an MN-major one of B X), the CTAs add
 // their parts of A in rank order, compute B each for itself and turn their slices to the next X in place. What
 // bounds it: the passes over g, m and p at the start and end, then the five iterations' chain of products,
-// exchanges and barriers (about 5 us each; one 16 x 1160 takes 32 us, 64 adapters of up to 64 x 2567 75).
+// exchanges and barriers (about 5 us each; one 16 x 1160 takes 30 us, 64 adapters of up to 64 x 2567 70).
 constexpr int kSmallItems = 128, kSmallThreads = 512;
 template <int R>
 struct Small {  // R rows of X
@@ -1093,7 +1111,9 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
     constexpr int kOwn = R / 4;                      // columns of A and B a warp has
     constexpr uint32_t kPolyCol = R;                 // (the regions of B X lie over A's and B's)
     float scale = s_inv / up;  // X is what is stored times this, until the first iteration's end
-    for (int n = 0; n < a.iterations; ++n) {
+    Poly poly{a.a, a.b, a.c, 1.0f / (float)r};
+    for (int n = 0; n < a.iterations; ++n, poly.next()) {
+        const float shift = poly.shift();
         if (warp == 0) {  // the slice's part of X X^T
             const uint64_t x0 = sdesc_sw128(sx, 16, 1024);
             for (int j = 0; j < blocks; ++j) {
@@ -1111,8 +1131,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
                 uint32_t v[16];
                 tmem_ld16(tmem + lanes + c, v);
                 tmem_ld_wait();
-                const auto part = [&](int j) { return __uint_as_float(v[j]) * scale * scale; };
-                if (ctas == 1) {  // all of A
+                const auto part = [&](int j) { return __uint_as_float(v[j]) * scale * scale - (ctas == 1 && c + j == row ? shift : 0.0f); };
+                if (ctas == 1) {  // all of D
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int q = c / 8 + h;
@@ -1132,7 +1152,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
         if (ctas > 1) {
             tc_fence_before();
             group_sync();
-            // this CTA's rows of A, the parts in rank order, to every CTA of the group
+            // this CTA's rows of D, the parts in rank order, to every CTA of the group
             const int share = R / ctas, row0 = rank * share;
             for (int e = tid; e < share * (R / 4); e += kSmallThreads) {
                 const int i = row0 + e / (R / 4), q = e % (R / 4);
@@ -1142,6 +1162,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
                     const float4 t = load_cluster(map_rank(at, w));
                     v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
                 }
+                if (i >> 2 == q) (i & 2 ? i & 1 ? v.w : v.z : i & 1 ? v.y : v.x) -= shift;
                 const uint32_t to = sa + (q >> 4) * 16384 + chunk_at(i, (q & 15) >> 1) + (q & 1) * 8;
                 const uint32_t lo = pack_half(v.x, v.y), hi = pack_half(v.z, v.w);
                 for (int w = 0; w < ctas; ++w)
@@ -1150,7 +1171,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
             group_sync();
         }
         publish();
-        if (warp == 0) {  // A A
+        if (warp == 0) {  // D D
             const uint64_t a0 = sdesc_sw128(sa, 16, 1024);
 #pragma unroll
             for (int h = 0; h < R / 64; ++h) {
@@ -1173,48 +1194,41 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
                     const int q = c / 8 + h, off = (q >> 3) * 16384 + chunk_at(row, q & 7);
                     const uint4 w = *reinterpret_cast<const uint4*>(generic + (sa - sbase) + off);
                     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t hi[4], lo[4];
+                    uint32_t y[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
-                        const float b0 = fmaf(a.b, y.x, a.c * __uint_as_float(v[8 * h + 2 * j]));
-                        const float b1 = fmaf(a.b, y.y, a.c * __uint_as_float(v[8 * h + 2 * j + 1]));
-                        hi[j] = pack_half(b0, b1);
-                        const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
-                        lo[j] = pack_half(b0 - z.x, b1 - z.y);
+                        const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
+                        y[j] = pack_half(fmaf(poly.of_d(), d.x, a.c * __uint_as_float(v[8 * h + 2 * j])),
+                                         fmaf(poly.of_d(), d.y, a.c * __uint_as_float(v[8 * h + 2 * j + 1])));
                     }
-                    // the rest of B that fp16 does not hold goes where A was: in a matrix of few rows nothing averages,
-                    // and a X + B X takes most of a X away again (1 x 9: 5e-3 off without it at most, 1.3e-3 with it)
-                    const uint4 b = make_uint4(hi[0], hi[1], hi[2], hi[3]), rest = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    const uint4 b = make_uint4(y[0], y[1], y[2], y[3]);
                     *reinterpret_cast<uint4*>(generic + (sb - sbase) + off) = b;
-                    *reinterpret_cast<uint4*>(generic + (sa - sbase) + off) = rest;
-                    if (R == 64) {  // once more in the rows from 64 on, so that the other half of TMEM's lanes holds B X too
+                    if (R == 64)  // once more in the rows from 64 on, so that the other half of TMEM's lanes holds B X too
                         *reinterpret_cast<uint4*>(generic + (sb - sbase) + off + 64 * 128) = b;
-                        *reinterpret_cast<uint4*>(generic + (sa - sbase) + off + 64 * 128) = rest;
-                    }
                 }
             }
         }
         publish();
-        // X = a X + B X, kTile columns at a time in two regions of TMEM
+        // X = a X + B X (the coefficients of D's polynomial), kTile columns at a time in two regions of TMEM
         constexpr int kTileBlocks = kTile / 64;
         const int tiles = (blocks + kTileBlocks - 1) / kTileBlocks;
         auto issue = [&](int t) {
             if (warp != 0) return;
             const uint32_t idesc = idesc_f16(128, 64 * min(kTileBlocks, blocks - kTileBlocks * t), true);
-            const uint64_t b0 = sdesc_sw128(sb, 16, 1024), r0 = sdesc_sw128(sa, 16, 1024);  // B and its rest
+            const uint64_t b0 = sdesc_sw128(sb, 16, 1024);
             const uint64_t x0 = sdesc_sw128(sx + kTileBlocks * t * block_bytes, block_bytes, 1024);
 #pragma unroll
             for (int h = 0; h < R / 64; ++h)
                 if (elect_one())
 #pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        mma_ss(tmem + kTile * (t & 1), (q < 4 ? b0 : r0) + h * (16384 >> 4) + 2 * (q & 3),
-                               x0 + (4 * h + (q & 3)) * (2048 >> 4), idesc, h > 0 || q > 0 ? 1u : 0u);
+                    for (int q = 0; q < 4; ++q)
+                        mma_ss(tmem + kTile * (t & 1), b0 + h * (16384 >> 4) + 2 * q, x0 + (4 * h + q) * (2048 >> 4), idesc,
+                               h > 0 || q > 0 ? 1u : 0u);
             if (elect_one()) mma_commit(bar_mma + 8 * (t & 1));
         };
         issue(0);
         if (tiles > 1) issue(1);
+        const float of_x = poly.of_x() * scale;
         // a warp's columns of a tile: a quarter of it; where the lanes from 64 on hold the same rows again, half of that
         const int i = R == 64 ? row & 63 : row, own0 = R == 64 ? group * 32 + (quarter >> 1) * 16 : group * 64;
         for (int t = 0; t < tiles; ++t) {
@@ -1235,8 +1249,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
-                        o[j] = pack_half(fmaf(a.a * scale, y.x, scale * __uint_as_float(v[8 * h + 2 * j])),
-                                         fmaf(a.a * scale, y.y, scale * __uint_as_float(v[8 * h + 2 * j + 1])));
+                        o[j] = pack_half(fmaf(of_x, y.x, scale * __uint_as_float(v[8 * h + 2 * j])),
+                                         fmaf(of_x, y.y, scale * __uint_as_float(v[8 * h + 2 * j + 1])));
                     }
                     *at = make_uint4(o[0], o[1], o[2], o[3]);
                 }
@@ -1560,6 +1574,8 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
                      half_map(&x_out[g][i], ws + z.x[i], z.k, z.r, z.count, z.ld, 32, true);
             if (!ok) return cudaErrorInvalidValue;
         }
+        Poly poly[kGroups];
+        for (int g = 0; g < ng; ++g) poly[g] = Poly{(float)q.a, (float)q.b, (float)q.c, 1.0f / (float)plan.sizes[g0 + g].r};
         for (int i = 0; i < q.iterations; ++i) {
             for (int mode = kGram; mode <= kApply; ++mode) {
                 GemmArgs ga;
@@ -1582,15 +1598,15 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
                         d.add = nullptr;
                         d.out = half(z.a);
                         d.by = scale * scale;
-                        d.add_by = 0.0f;
+                        d.add_by = -poly[g].shift();
                         d.steps = (z.k + kBK - 1) / kBK;
                     } else if (mode == kPoly) {
                         d.map_m = d.map_n = map_a[g];
                         d.map_out = b_out[g];
                         d.add = half(z.a);
                         d.out = half(z.b);
-                        d.by = (float)q.c;
-                        d.add_by = (float)q.b;
+                        d.by = poly[g].c;
+                        d.add_by = poly[g].of_d();
                         d.steps = (z.r + kBK - 1) / kBK;
                     } else {
                         d.map_m = map_b[g];
@@ -1599,7 +1615,7 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
                         d.add = half(z.x[i & 1]);
                         d.out = half(z.x[(i + 1) & 1]);
                         d.by = scale;
-                        d.add_by = (float)q.a * scale;
+                        d.add_by = poly[g].of_x() * scale;
                         d.steps = (z.r + kBK - 1) / kBK;
                     }
                     d.cols = mode == kApply ? z.k : z.r;
@@ -1610,6 +1626,7 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
                                   : mode == kPoly ? launch_product<kPoly>(ga, pairs, s) : launch_product<kApply>(ga, pairs, s);
                 if (e != cudaSuccess) return e;
             }
+            for (int g = 0; g < ng; ++g) poly[g].next();
         }
     }
     if (q.iterations % 2 == 1) {

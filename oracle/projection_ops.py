@@ -56,9 +56,9 @@ def _half(x):
 
 
 def orthogonal(u, iterations=5, coefficients=POLYNOMIAL, eps=1e-7, stored=False, lead=1.0):
-    """X of u; stored: X, A and B rounded to fp16 as they are kept, X at the start with a power of two near the root
-    of its shorter side times ``lead`` (another one draws other roundings). Matrices of up to 128 rows hold B in two
-    fp16 numbers a value."""
+    """X of u; stored: X, A and B rounded to fp16, X at the start with a power of two near the root of its shorter side
+    times ``lead`` (another one draws other roundings), for matrices of up to 128 rows B in two fp16 numbers a value.
+    The kernels' own form, A less a multiple of the identity, rounds no more than that."""
     u = np.asarray(u, np.float64)
     if u.shape[0] > u.shape[1]:
         return orthogonal(u.T, iterations, coefficients, eps, stored, lead).T

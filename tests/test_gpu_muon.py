@@ -286,3 +286,26 @@ def test_projection_trained_by_muon(dev):
     y = op.forward(x, bias)["y"]
     op.set_weights(w)
     assert not Hh.bits_equal(op.forward(x, bias)["y"][1], y[1])  # the new weights' codes
+
+
+@pytest.mark.parametrize("rows, cols", [(16, 1160), (1000, 33), (64, 2567), (128, 1000), (130, 845), (300, 1000), (768, 400)])
+def test_what_fp16_leaves_of_independent_entries(dev, rows, cols):
+    """X is rounded to fp16 six times, each by 2^-11 of a value at most, 2^-11 / sqrt(3) of it in the mean square: 6.9e-4
+    in all. The roundings of A's and B's parts are fewer bits of less than that, as much again at most: sqrt(2) 6.9e-4
+    < 2^-10. (A and B rounded whole leave 1.3e-3 and more.)"""
+    import torch
+    g = torch.Generator(device=dev)
+    g.manual_seed(rows)
+    x = torch.randn((rows, cols), generator=g, device=dev)
+    p = torch.zeros_like(x)
+    pkg.Muon([p], lr=1.0, momentum=0.0, nesterov=False, weight_decay=0.0, update_rms=1.0, grads=[x]).step()
+    pkg.rlk_joint_attn_check_status()
+    got, exact = -f64(p) / np.sqrt(max(rows, cols)), O.orthogonal(f64(x))
+    assert np.linalg.norm(got - exact) <= 2.0 ** -10 * np.linalg.norm(exact)
+
+
+@pytest.mark.parametrize("poly", [(2.0, -1.5, 0.5), (1.875, -1.25, 0.375), (1.5, -0.5, 0.0), (1.0, 0.0, 0.0), (3.0, -3.2, 1.2)])
+@pytest.mark.parametrize("rows, cols", [(1, 9), (40, 50), (100, 700), (257, 300)])
+def test_other_polynomials(dev, poly, rows, cols):
+    x = gradient(dev, rows, cols, 11)
+    assert_orthogonal(pkg.orthogonalize([x], coefficients=poly)[0], f64(x), (poly, rows, cols), coefficients=poly)
