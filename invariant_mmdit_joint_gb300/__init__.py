@@ -1475,6 +1475,9 @@ def _cuda_device(device):
     return device
 
 
+_GRADS = ("dx", "dw", "db")
+
+
 class Fp8Projection(_Pairs):
     """Buffers + calls of one projection y = x W^T + b of both streams in 8-bit floating point (rlk_fp8_quantize,
     rlk_fp8_gemm), each stream with weights of its own.
@@ -1573,23 +1576,31 @@ class Fp8Projection(_Pairs):
             raise ValueError("no weights given: set_weights comes first")
         _require_current(self.device)
         handle = _raw_stream(stream, self._index)
-        if handle not in self._streams:
+        if handle not in self._streams:  # (those have a workspace)
             self._record(stream, handle)
-        return handle, _workspace(self, self._ws_bytes, stream, handle).data_ptr()
+            _workspace(self, self._ws_bytes, stream, handle)
+        return handle
 
     def _out(self, out, names, stream):
         """The outputs of these names and their pointers (new ones without what a reuse is checked by: that takes
         longer than the smallest kernels, and most calls' outputs are not passed back)."""
         if out is not None:
             return self._outputs(out, names, stream)
-        device, kinds = self.device, self._kinds
-        out = {k: tuple(None if size is None else _empty(size, kinds[k][1], device, stream) for size in kinds[k][0]) for k in names}
-        return out, {k: tuple(None if x is None else x.data_ptr() for x in pair) for k, pair in out.items()}
+        device, kinds, out, p = self.device, self._kinds, {}, {}
+        for k in names:
+            (t, i), dtype = kinds[k]
+            t = None if t is None else _empty(t, dtype, device, stream)
+            i = None if i is None else _empty(i, dtype, device, stream)
+            out[k], p[k] = (t, i), (None if t is None else t.data_ptr(), None if i is None else i.data_ptr())
+        return out, p
 
     def _vectors(self, name, pair, dtype, sizes):
-        if pair is None or all(t is None for t in pair):
+        if pair is None:
             return _NONE
-        return self._need(name, pair, dtype, tuple(None if t is None else k for t, k in zip(pair, sizes)))
+        if len(pair) != 2:
+            raise ValueError(f"{name} must be a (text, image) pair")
+        t, i = pair
+        return self._need(name, pair, dtype, (None if t is None else sizes[0], None if i is None else sizes[1]))
 
     def forward(self, x, bias=None, train: bool = False, out=None, stream=None):
         """y, and with train what the backward needs of x: xt and xt_scale, its codes turned. bias is a pair of bf16
@@ -1599,8 +1610,8 @@ class Fp8Projection(_Pairs):
         px = self._need("x", x, bf16, self._x)
         pb = self._vectors("bias", bias, bf16, self._b)
         out, p = self._out(out, ("y", "xt", "xt_scale") if train else ("y",), stream)
-        handle, ws = self._ready(stream)
-        quant, product = self._calls.get(train) or self._fwd_calls(train, ws)
+        handle = self._ready(stream)
+        quant, product = self._calls.get(train) or self._fwd_calls(train, self.workspace.data_ptr())
         py, xt, xs = p["y"], p.get("xt"), p.get("xt_scale")
         for n, i in enumerate(self._live):  # (the rest of a call stays what it is)
             f = product[n]
@@ -1647,22 +1658,24 @@ class Fp8Projection(_Pairs):
         ``out`` (float32)."""
         import torch
         bf16, f32 = torch.bfloat16, torch.float32
-        want = tuple(k for k in ("dx", "dw", "db") if k in want)
-        if not want:
-            raise ValueError("want must name dx, dw or db")
+        if want != _GRADS:
+            want = tuple(k for k in _GRADS if k in want)
+            if not want:
+                raise ValueError("want must name dx, dw or db")
         pdy = self._need("dy", dy, bf16, self._y)
         pxt = pxs = _NONE
         if "dw" in want:
             if saved is None or "xt" not in saved:
                 raise ValueError("dw needs what forward(train=True) returned")
-            pxt = self._need("xt", saved["xt"], *self._kinds["xt"][::-1])
-            pxs = self._need("xt_scale", saved["xt_scale"], *self._kinds["xt_scale"][::-1])
+            (sizes, dtype), (scale_sizes, scale_dtype) = self._kinds["xt"], self._kinds["xt_scale"]
+            pxt = self._need("xt", saved["xt"], dtype, sizes)
+            pxs = self._need("xt_scale", saved["xt_scale"], scale_dtype, scale_sizes)
         if accumulate and ("dw" not in want or out is None or self.dw_dtype is not f32):
             raise ValueError("accumulate needs out with a float32 dw")
         out, p = self._out(out, want, stream)
-        handle, ws = self._ready(stream)
+        handle = self._ready(stream)
         dx, dw, db = ("dx" in want), ("dw" in want), ("db" in want)
-        quant, product = self._calls.get(want) or self._bwd_calls(want, ws)
+        quant, product = self._calls.get(want) or self._bwd_calls(want, self.workspace.data_ptr())
         k = 0
         for n, i in enumerate(self._live):
             quant[n].x = pdy[i]
