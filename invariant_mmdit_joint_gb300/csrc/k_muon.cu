@@ -415,20 +415,18 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 }
 // One iteration's polynomial in D = A - shift I, an identity for any shift:
 //   a X + (b A + c A A) X = (a + b shift + c shift^2) X + ((b + 2 c shift) D + c D D) X
-// A's diagonal, which holds most of it, is near the square of X's singular values. With their expected square taken off
-// it, little is rounded to fp16: near 1, where A's roundings were multiplied by b = -4.8 and B's were 2^-11 of 2.7, the
-// two coefficients are 0.7 (X off by 6e-4 to 8e-4 of its norm, 1.4e-3 to 3e-3 without). What is expected is what the
-// polynomial makes of r equal singular values, 1 at most: a rule on r alone, so that a matrix's result depends on
-// nothing else (its own trace gains 5 percent more, and takes a pass over A before it is rounded).
+// A's diagonal, which holds most of it, is the squared norms of X's rows. With about their mean taken off it, little is
+// rounded to fp16: near 1, where A's roundings were multiplied by b = -4.8 and B's were 2^-11 of 2.7, the two
+// coefficients are 0.7 (X off by 5e-4 to 9e-4 of its norm, 1.2e-3 to 2.8e-3 without). Small matrices take the mean
+// itself, X's squares summed. The larger ones, where it would take a sum over many CTAs, take kSpread / r and what the
+// polynomial makes of it, 1 at most: a rule on r alone. 1 / r, the mean at the start, is too early where a few singular
+// values lead (300 x 1000 and 700 x 1500 with four of them: 0.35 8.3e-4 and 9.5e-4, 1 8.4e-4 and 1.1e-3, the mean 8.6e-4
+// and 9.2e-4).
+constexpr float kSpread = 0.35f;
 struct Poly {
-    float a, b, c, square;
-    __host__ __device__ float shift() const { return fminf(square, 1.0f); }  // (1 for a NaN)
-    __host__ __device__ float of_x() const { return fmaf(fmaf(c, shift(), b), shift(), a); }
-    __host__ __device__ float of_d() const { return fmaf(2.0f * c, shift(), b); }
-    __host__ __device__ void next() {
-        const float p = fmaf(fmaf(c, square, b), square, a);
-        square *= p * p;
-    }
+    float a, b, c;
+    __host__ __device__ float of_x(float shift) const { return fmaf(fmaf(c, shift, b), shift, a); }
+    __host__ __device__ float of_d(float shift) const { return fmaf(2.0f * c, shift, b); }
 };
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -670,7 +668,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) muon_ge
 // 128-byte swizzle makes a block a K-major operand of the slice's X X^T and an MN-major one of B X), the CTAs add
 // their parts of A in rank order, compute B each for itself and turn their slices to the next X in place. What
 // bounds it: the passes over g, m and p at the start and end, then the five iterations' chain of products,
-// exchanges and barriers (about 5 us each; one 16 x 1160 takes 30 us, 64 adapters of up to 64 x 2567 70).
+// exchanges and barriers (about 5 us each; one 16 x 1160 takes 31 us, 64 adapters of up to 64 x 2567 70).
 constexpr int kSmallItems = 128, kSmallThreads = 512;
 template <int R>
 struct Small {  // R rows of X
@@ -713,6 +711,9 @@ __device__ __forceinline__ float4 load_cluster(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
+}
+__device__ __forceinline__ void store_cluster(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 __device__ __forceinline__ double load_cluster_f64(uint32_t addr) {
     double v;
@@ -989,6 +990,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ float s_sums[kSmallThreads / 32], s_inv;
+    __shared__ __align__(16) float s_group[8];  // X's sum of squares, each CTA's
     __shared__ __align__(8) double s_part;
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -1014,6 +1016,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
 
     if (tid == 0) {
         abort_flag = 0;
+        for (int w = ctas; w < 8; ++w) s_group[w] = 0.0f;
         mbar_init(bar_mma, 1);
         mbar_init(bar_mma + 8, 1);
         fence_barrier_init();
@@ -1111,9 +1114,11 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
     constexpr int kOwn = R / 4;                      // columns of A and B a warp has
     constexpr uint32_t kPolyCol = R;                 // (the regions of B X lie over A's and B's)
     float scale = s_inv / up;  // X is what is stored times this, until the first iteration's end
-    Poly poly{a.a, a.b, a.c, 1.0f / (float)r};
-    for (int n = 0; n < a.iterations; ++n, poly.next()) {
-        const float shift = poly.shift();
+    // X's squares, a thread's part each, lie where nothing is read or written from an iteration's end to its next barrier
+    float* const squares = reinterpret_cast<float*>(generic + ((ctas == 1 ? sb : sa) - sbase));
+    const Poly poly{a.a, a.b, a.c};
+    float shift = 1.0f / (float)r;  // the mean of A's diagonal: X's sum of squares (1 at first) a row
+    for (int n = 0; n < a.iterations; ++n) {
         if (warp == 0) {  // the slice's part of X X^T
             const uint64_t x0 = sdesc_sw128(sx, 16, 1024);
             for (int j = 0; j < blocks; ++j) {
@@ -1123,6 +1128,17 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
                     for (int q = 0; q < 4; ++q) mma_ss(tmem, d + 2 * q, d + 2 * q, idesc_r, j > 0 || q > 0 ? 1u : 0u);
             }
             if (elect_one()) mma_commit(bar_mma);
+        }
+        if (n > 0 && (ctas == 1 || warp == 1)) {
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kSmallThreads; w += 32) s += squares[w + lane];
+#pragma unroll
+            for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+            if (ctas == 1)
+                shift = s * slice.inv_r;
+            else if (lane < ctas)  // (read between the iteration's two barriers, written after the last one's)
+                store_cluster(map_rank(smem_u32(&s_group[rank]), lane), s);
         }
         mma_wait(0);
         if (row < R) {
@@ -1152,6 +1168,10 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
         if (ctas > 1) {
             tc_fence_before();
             group_sync();
+            if (n > 0) {
+                const float4 p = *reinterpret_cast<const float4*>(s_group), q = *reinterpret_cast<const float4*>(s_group + 4);
+                shift = ((p.x + p.y) + (p.z + p.w) + ((q.x + q.y) + (q.z + q.w))) * slice.inv_r;
+            }
             // this CTA's rows of D, the parts in rank order, to every CTA of the group
             const int share = R / ctas, row0 = rank * share;
             for (int e = tid; e < share * (R / 4); e += kSmallThreads) {
@@ -1198,8 +1218,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
-                        y[j] = pack_half(fmaf(poly.of_d(), d.x, a.c * __uint_as_float(v[8 * h + 2 * j])),
-                                         fmaf(poly.of_d(), d.y, a.c * __uint_as_float(v[8 * h + 2 * j + 1])));
+                        y[j] = pack_half(fmaf(poly.of_d(shift), d.x, a.c * __uint_as_float(v[8 * h + 2 * j])),
+                                         fmaf(poly.of_d(shift), d.y, a.c * __uint_as_float(v[8 * h + 2 * j + 1])));
                     }
                     const uint4 b = make_uint4(y[0], y[1], y[2], y[3]);
                     *reinterpret_cast<uint4*>(generic + (sb - sbase) + off) = b;
@@ -1228,9 +1248,10 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
         };
         issue(0);
         if (tiles > 1) issue(1);
-        const float of_x = poly.of_x() * scale;
+        const float of_x = poly.of_x(shift) * scale;
         // a warp's columns of a tile: a quarter of it; where the lanes from 64 on hold the same rows again, half of that
         const int i = R == 64 ? row & 63 : row, own0 = R == 64 ? group * 32 + (quarter >> 1) * 16 : group * 64;
+        __half2 square = __float2half2_rn(0.0f);
         for (int t = 0; t < tiles; ++t) {
             mma_wait(t & 1);
 #pragma unroll
@@ -1249,8 +1270,11 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
-                        o[j] = pack_half(fmaf(of_x, y.x, scale * __uint_as_float(v[8 * h + 2 * j])),
-                                         fmaf(of_x, y.y, scale * __uint_as_float(v[8 * h + 2 * j + 1])));
+                        const float x0 = fmaf(of_x, y.x, scale * __uint_as_float(v[8 * h + 2 * j]));
+                        const float x1 = fmaf(of_x, y.y, scale * __uint_as_float(v[8 * h + 2 * j + 1]));
+                        const __half2 y2 = __floats2half2_rn(x0, x1);
+                        square = __hfma2(y2, y2, square);  // (fp16 is enough for where to shift)
+                        o[j] = *reinterpret_cast<const uint32_t*>(&y2);
                     }
                     *at = make_uint4(o[0], o[1], o[2], o[3]);
                 }
@@ -1262,6 +1286,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
                 issue(t + 2);
             }
         }
+        squares[tid] = __low2float(square) + __high2float(square);
         publish();
         scale = 1.0f;
     }
@@ -1574,9 +1599,15 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
                      half_map(&x_out[g][i], ws + z.x[i], z.k, z.r, z.count, z.ld, 32, true);
             if (!ok) return cudaErrorInvalidValue;
         }
-        Poly poly[kGroups];
-        for (int g = 0; g < ng; ++g) poly[g] = Poly{(float)q.a, (float)q.b, (float)q.c, 1.0f / (float)plan.sizes[g0 + g].r};
+        const Poly poly{(float)q.a, (float)q.b, (float)q.c};
+        float shift[kGroups], square[kGroups];
+        for (int g = 0; g < ng; ++g) square[g] = kSpread / (float)plan.sizes[g0 + g].r;
         for (int i = 0; i < q.iterations; ++i) {
+            for (int g = 0; g < ng; ++g) {
+                const float p = poly.of_x(square[g]);
+                shift[g] = fminf(square[g], 1.0f);  // (1 for a NaN)
+                square[g] *= p * p;
+            }
             for (int mode = kGram; mode <= kApply; ++mode) {
                 GemmArgs ga;
                 ga.n = ng;
@@ -1598,15 +1629,15 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
                         d.add = nullptr;
                         d.out = half(z.a);
                         d.by = scale * scale;
-                        d.add_by = -poly[g].shift();
+                        d.add_by = -shift[g];
                         d.steps = (z.k + kBK - 1) / kBK;
                     } else if (mode == kPoly) {
                         d.map_m = d.map_n = map_a[g];
                         d.map_out = b_out[g];
                         d.add = half(z.a);
                         d.out = half(z.b);
-                        d.by = poly[g].c;
-                        d.add_by = poly[g].of_d();
+                        d.by = poly.c;
+                        d.add_by = poly.of_d(shift[g]);
                         d.steps = (z.r + kBK - 1) / kBK;
                     } else {
                         d.map_m = map_b[g];
@@ -1615,7 +1646,7 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
                         d.add = half(z.x[i & 1]);
                         d.out = half(z.x[(i + 1) & 1]);
                         d.by = scale;
-                        d.add_by = poly[g].of_x() * scale;
+                        d.add_by = poly.of_x(shift[g]) * scale;
                         d.steps = (z.r + kBK - 1) / kBK;
                     }
                     d.cols = mode == kApply ? z.k : z.r;
@@ -1626,7 +1657,6 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
                                   : mode == kPoly ? launch_product<kPoly>(ga, pairs, s) : launch_product<kApply>(ga, pairs, s);
                 if (e != cudaSuccess) return e;
             }
-            for (int g = 0; g < ng; ++g) poly[g].next();
         }
     }
     if (q.iterations % 2 == 1) {
