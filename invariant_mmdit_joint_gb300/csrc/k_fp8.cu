@@ -26,7 +26,9 @@
 // spreads over TMEM), 4 .. 11 the sums of the chunks and the output. Every
 // accumulator starts a chunk anew; the chunks meet in fp32 registers or shared
 // memory, always in ascending order: a token's bytes do not depend on the kernel
-// that computed them. Every wait is bounded.
+// that computed them. Every wait is bounded. A kernel that starts early (griddepcontrol) is alive while the one before
+// it writes what it reads: its loads are ordinary ones, which the wait orders; read-only loads (ld.global.nc) are for
+// memory that nobody writes while the kernel lives.
 //   fp8_gemm_pair_kernel  CTA pairs, 256 features x 224 tokens: 3.1 PFLOP/s (8704
 //       tokens, 2560 -> 7680: 110 us); without the output 3.9. Bound by the tensor
 //       pipe (76% active), and by shared memory's port while the output passes.
@@ -100,11 +102,11 @@ struct Eight {
     __device__ __forceinline__ void load(const void* x, long long at) {
         if (kFp32) {
             const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(x) + at);
-            const uint4 a = __ldg(p), b = __ldg(p + 1);
+            const uint4 a = p[0], b = p[1];
             w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
             w[kFp32 ? 4 : 0] = b.x, w[kFp32 ? 5 : 1] = b.y, w[kFp32 ? 6 : 2] = b.z, w[kFp32 ? 7 : 3] = b.w;
         } else {
-            const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at));
+            const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
             w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
         }
     }
@@ -507,7 +509,7 @@ __device__ __forceinline__ void gather_scales(uint32_t (&w)[4], const GemmItem& 
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const int r = r0 + 32 * c + lane;
-        w[c] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(p + (long long)r * ld + kb)) : 0x7f7f7f7fu;
+        w[c] = r < rows ? *reinterpret_cast<const uint32_t*>(p + (long long)r * ld + kb) : 0x7f7f7f7fu;
     }
 }
 __device__ __forceinline__ void put_scales(uint32_t dst, const uint32_t (&w)[4]) {
@@ -757,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_gemm_few_kernel(const __grid_
             }
         }
         if (g.bias != nullptr) {
-            const uint2 b = __ldg(reinterpret_cast<const uint2*>(g.bias + f));
+            const uint2 b = *reinterpret_cast<const uint2*>(g.bias + f);
             sum = make_float4(sum.x + bf16_lo(b.x), sum.y + bf16_hi(b.x), sum.z + bf16_lo(b.y), sum.w + bf16_hi(b.y));
         }
         const long long to = (long long)(at.t0 + tk) * g.d_stride + f;

@@ -18,7 +18,9 @@
 // Matrices of one size lie one behind the other in the workspace (a group): one
 // tensor map with the matrix as its third coordinate serves them, and cuts
 // tiles off at a matrix's end. One launch of a product serves every group of
-// the list. Each output tile is one accumulator, K ascending: a matrix's result
+// the list, and starts while the one before it still writes what it reads: its
+// loads are ordinary ones, which the wait orders (read-only loads are for memory
+// that nobody writes while the kernel lives). Each output tile is one accumulator, K ascending: a matrix's result
 // does not depend on its list. Matrices of up to 128 rows whose X fits shared
 // memory take one kernel for the whole step instead (muon_small_kernel).
 #include "rlk_device.cuh"
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(kPassThreads, 5) muon_update_kernel(const __gr
     for (int k = 0; k < 2; ++k) {
         const int rr = (threadIdx.x >> 3) + 32 * k, cc = 8 * (threadIdx.x & 7);
         x[k] = make_uint4(0, 0, 0, 0);
-        if (r0 + rr < rows && c0 + cc < cols) x[k] = __ldg(reinterpret_cast<const uint4*>(it.x + (long long)(r0 + rr) * it.ld + c0 + cc));
+        if (r0 + rr < rows && c0 + cc < cols) x[k] = *reinterpret_cast<const uint4*>(it.x + (long long)(r0 + rr) * it.ld + c0 + cc);
     }
     if (it.m != nullptr) {
 #pragma unroll
@@ -447,7 +449,7 @@ __device__ __forceinline__ void store32(const Group& g, int z, float (&v)[32], i
 #pragma unroll
         for (int c = 0; c < 32; c += 8) {
             uint4 w = make_uint4(0, 0, 0, 0);
-            if (live && j + c < g.cols) w = __ldg(reinterpret_cast<const uint4*>(add + c));
+            if (live && j + c < g.cols) w = *reinterpret_cast<const uint4*>(add + c);
             const uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
