@@ -1572,7 +1572,7 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
     a.eps = (float)q.eps;
     a.nesterov = q.nesterov != 0;
     a.grad_scale = step ? q.grad_scale : nullptr;
-    a.lr_dev = q.lr_dev;
+    a.lr_dev = step ? q.lr_dev : nullptr;
     auto tiles = [](const Item& it) { return ((it.rows + kSide - 1) / kSide) * ((it.cols + kSide - 1) / kSide); };
     e = pass(items, a, false, [](const Item& it) { return it.parts; }, [&](int blocks, bool) {
         timing_begin(kKMuonMomentum, s);

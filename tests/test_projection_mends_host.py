@@ -1,8 +1,11 @@
 """CPU tests of the 8-bit projections and of Muon beside test_projection_host.py: what the header says of their limits
 and of what a call reads, held against the library and its sources."""
 
+import math
 import os
 import re
+
+from tests.test_projection_host import P, L, args, matrices, no_gpu, step  # noqa: F401
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "invariant_mmdit_joint_gb300", "csrc")
@@ -23,3 +26,18 @@ def test_kernels_that_start_early_read_by_ordinary_loads():
     for f in early:
         found = re.findall(r"__ldg\w*|ld\.global\.nc|__restrict__|__ldcs|__ldca", source(f))
         assert not found, (f, found)
+
+
+def test_orthogonalize_takes_no_argument_of_a_step(L):  # noqa: F811
+    """Rates, momentum and device scalars are not refused (a step refuses each), and every pointer that the kernels'
+    arguments take from args is a step's alone: one that the contract does not read may be no address at all."""
+    t = matrices(master=None, m=None)
+    t[0].master = t[0].m = None
+    for over in (dict(lr=-1.0), dict(lr=math.nan), dict(momentum=1.0), dict(update_rms=-1.0), dict(nesterov=2), dict(lr_dev=P + 2),
+                 dict(grad_scale=P + 1)):
+        assert step(L, a=args(**over)) != 0
+        if no_gpu():
+            assert step(L, t, name="rlk_orthogonalize", a=args(**over)) == 5, over
+    taken = re.findall(r"=\s*([^;=]*\bq\.(?:lr_dev|grad_scale))\b([^;]*);", source("k_muon.cu"))
+    taken = [(a, b) for a, b in taken if "!=" not in a + b]  # (the host's rate looks whether there is a pointer)
+    assert len(taken) == 4 and all(a.startswith("step ? ") and b == " : nullptr" for a, b in taken), taken
