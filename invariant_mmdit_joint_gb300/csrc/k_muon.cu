@@ -8,12 +8,12 @@
 // The products run on tcgen05 with fp16 operands and fp32 accumulators: the
 // singular values lie in [0, 1.3], so that fp16's range is enough (X starts
 // multiplied by a power of two near sqrt(r), where its entries are about 1 /
-// sqrt(k) as they are at the end), and its 11 bits keep the update within 2^-9
-// of the formula's where bf16's 8 lose a percent: small singular values grow
-// 3.4 times an iteration, and the roundings with them. A is kept less a multiple
-// of the identity (Poly). A and B are
-// symmetric: only tiles that meet the lower triangle are computed, and stored
-// on both sides.
+// sqrt(k) as they are at the end). Small singular values grow 3.4 times an
+// iteration, and what rounding X leaves in their directions grows with them: the
+// first kRests of the X's are kept with about five bits more (their rests), which
+// the sum a X + B X takes beside the product. A is kept less a multiple of the
+// identity (Poly). A and B are symmetric: only tiles that meet the lower triangle
+// are computed, and stored on both sides.
 //
 // Matrices of one size lie one behind the other in the workspace (a group): one
 // tensor map with the matrix as its third coordinate serves them, and cuts
@@ -58,9 +58,10 @@ struct Item {
     const void* g;    // step: gradient; orthogonalize: the matrix
     float* m;         // null: orthogonalize
     __half* x;        // the matrix's X [r, ld]
+    uint8_t* rest;    // what rounding it leaves [r, ld_rest]
     double* part;     // its partial sums
     long long n, chunk;
-    int rows, cols, ld, parts, block0;
+    int rows, cols, ld, ld_rest, parts, block0;
     float start;      // X's power of two at the start
     float rate, decay;  // p -= decay p + rate X (lr_dev: times its value)
     bool g32;
@@ -220,10 +221,48 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// X = u * start / (|u| + eps) in fp16, turned over where the matrix is tall.
+// What rounding X to fp16 leaves, as an e4m3 code of it times a power of two: five bits of it or so.
+//
+// The iteration takes a small singular value s to a s = 3.4 s, and a perturbation of X between two such directions
+// likewise; one that meets a direction whose value has grown is multiplied by that value's own growth alone, which ends
+// near 1. Rounding X spreads 2^-12 of its norm over all directions, so where a few of them lead, the others drown: X off
+// by 5e-3 of its norm with four leading by 10 times, 2e-2 with one by 100, 9e-2 with three alone, and it is the roundings
+// of the first X's that grow. B X and A do not pass them on (B is 0 but for directions that have grown), a X does. So
+// a X alone takes the rests: with a in the first two iterations, from the third on, where most values have grown, with
+// the coefficient that X itself has beside B (Poly). Three rests leave 4e-4 to 1.2e-3 of X up to 100 times (two 2e-3,
+// four no less), 3e-3 to 6e-3 beyond.
+constexpr int kRests = 3;
+// X's entries are 1 at most (times its power of two at the start): rests of 2^-12 and less, 448 and less times this, and
+// those of entries of 2^-14 and more keep their bits.
+constexpr float kRestScale = 1048576.0f;
+// Small matrices at the start: X's entries are below 2^12 and mostly below 2^9, rests below 2 and 1/4.
+constexpr float kRestScaleStart = 192.0f;
+__device__ __forceinline__ uint32_t rests2(uint64_t x, __half2 h, float scale) {  // of two x, the first one's in the low byte
+    const float2 f = __half22float2(h);
+    float lo, hi;
+    f2_unpack(mul_f2(sub_f2(x, f2_pack(f.x, f.y)), f2_pack(scale, scale)), lo, hi);
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t rests2(float x0, float x1, __half2 h, float scale) { return rests2(f2_pack(x0, x1), h, scale); }
+__device__ __forceinline__ float2 rest_values(uint32_t codes) {  // of the two low bytes
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ uint2 rests8(const float (&v)[8], float scale) {
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) w[k >> 2] |= rests2(v[k], v[k + 1], __floats2half2_rn(v[k], v[k + 1]), scale) << 8 * (k & 3);
+    return make_uint2(w[0], w[1]);
+}
+
+// X = u * start / (|u| + eps) in fp16 and its rest, turned over where the matrix is tall.
 template <bool kVec>
 __global__ void __launch_bounds__(kPassThreads, 6) muon_start_kernel(const __grid_constant__ PassArgs a) {
     __shared__ __align__(16) __half tile[kSide * kSide];
+    __shared__ __align__(8) uint8_t rests[kSide * kSide];
     __shared__ float s_inv;
     const Item& it = item_of(a);
     float f;
@@ -252,7 +291,7 @@ __global__ void __launch_bounds__(kPassThreads, 6) muon_start_kernel(const __gri
         if (threadIdx.x == 0) s_inv = it.start / (sqrtf((float)sq) + a.eps);
     }
     __syncthreads();
-    const float inv = s_inv;
+    const float inv = s_inv, rest_scale = kRestScale / it.start;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int rr = (threadIdx.x >> 3) + 32 * k, r = at.r0 + rr;
@@ -260,13 +299,18 @@ __global__ void __launch_bounds__(kPassThreads, 6) muon_start_kernel(const __gri
         for (int j = 0; j < 8; ++j) u[k][j] *= inv;
         if (kVec && !tall) {
             const int c = at.c0 + column_of<true>(0);
-            if (r < it.rows && c < it.cols) *reinterpret_cast<uint4*>(it.x + (long long)r * it.ld + c) = pack8(u[k]);
+            if (r < it.rows && c < it.cols) {
+                *reinterpret_cast<uint4*>(it.x + (long long)r * it.ld + c) = pack8(u[k]);
+                *reinterpret_cast<uint2*>(it.rest + (long long)r * it.ld_rest + c) = rests8(u[k], rest_scale);
+            }
             continue;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int c = column_of<kVec>(j);
-            tile[tall ? turned(c, rr) : turned(rr, c)] = __float2half_rn(u[k][j]);
+            const int c = column_of<kVec>(j), to = tall ? turned(c, rr) : turned(rr, c);
+            const __half h = __float2half_rn(u[k][j]);
+            tile[to] = h;
+            rests[to] = (uint8_t)rests2(u[k][j], 0.0f, __halves2half2(h, __float2half_rn(0.0f)), rest_scale);
         }
     }
     if (kVec && !tall) return;
@@ -275,8 +319,10 @@ __global__ void __launch_bounds__(kPassThreads, 6) muon_start_kernel(const __gri
 #pragma unroll
     for (int k = 0; k < 2; ++k) {  // (a row's padding takes zeros)
         const int rr = (threadIdx.x >> 3) + 32 * k, r = r0 + rr, cc = 8 * (threadIdx.x & 7), col = c0 + cc;
-        if (r < rows && col < cols)
+        if (r < rows && col < cols) {
             *reinterpret_cast<uint4*>(it.x + (long long)r * it.ld + col) = *reinterpret_cast<const uint4*>(tile + turned(rr, cc));
+            *reinterpret_cast<uint2*>(it.rest + (long long)r * it.ld_rest + col) = *reinterpret_cast<const uint2*>(rests + turned(rr, cc));
+        }
     }
 }
 
@@ -370,10 +416,12 @@ struct Group {
     CUtensorMap map_out; // out, box 32 x 32 x 1
     const __half* add;   // gram: the identity (not read); poly: D; apply: X: added times `add_by`
     __half* out;
-    long long add_step, out_step;  // from matrix to matrix
+    uint8_t* rest;       // apply: X's rests, or null; the new X's are written in their place (rest_out)
+    bool rest_out;
+    long long add_step, out_step, rest_step;  // from matrix to matrix
     int rows, cols;      // of the output (gram, poly: r x r)
-    int ld_add, ld_out, count, steps, per, tile0;  // matrices; k-steps; tiles of one matrix; first tile
-    float by, add_by;    // out = by * product + add_by * add
+    int ld_add, ld_out, ld_rest, count, steps, per, tile0;  // matrices; k-steps; tiles of one matrix; first tile
+    float by, add_by, rest_by;  // out = by * product + add_by * add + rest_by * rest (as its code has it)
 };
 struct GemmArgs {
     Group g[kGroups];
@@ -439,23 +487,54 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
 }
 
 // 32 columns from j on of row i (a warp: 32 rows from i - lane): out = by * v + add_by * add (gram: the identity), and
-// on the other side of the diagonal.
+// on the other side of the diagonal; apply: + rest_by * rest, and the rest of what is stored.
 template <int kMode>
 __device__ __forceinline__ void store32(const Group& g, int z, float (&v)[32], int i, int j, uint32_t buffer) {
     const int lane = threadIdx.x & 31, i0 = i - lane;
     const bool live = i < g.rows;
     if (kMode != kGram) {
         const __half* add = g.add + z * g.add_step + (long long)i * g.ld_add + j;
+        uint8_t* const rest = g.rest + z * g.rest_step + (long long)i * g.ld_rest + j;
+        const bool rests = kMode == kApply && g.rest != nullptr;
+        uint4 w[4], b[2];  // (everything that is read, before the rests are written)
 #pragma unroll
-        for (int c = 0; c < 32; c += 8) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (live && j + c < g.cols) w = *reinterpret_cast<const uint4*>(add + c);
-            const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+        for (int c = 0; c < 4; ++c) {
+            w[c] = make_uint4(0, 0, 0, 0);
+            if (live && j + 8 * c < g.cols) w[c] = *reinterpret_cast<const uint4*>(add + 8 * c);
+        }
+        if (rests) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&q[k]));
-                v[c + 2 * k] = fmaf(g.add_by, x.x, g.by * v[c + 2 * k]);
-                v[c + 2 * k + 1] = fmaf(g.add_by, x.y, g.by * v[c + 2 * k + 1]);
+            for (int c = 0; c < 2; ++c) {  // (rows of rests have room up to a multiple of 16)
+                b[c] = make_uint4(0, 0, 0, 0);
+                if (live && j + 16 * c < g.cols) b[c] = *reinterpret_cast<const uint4*>(rest + 16 * c);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+            const uint4& q = w[c >> 3];
+            const uint32_t word = (c >> 1 & 3) == 0 ? q.x : (c >> 1 & 3) == 1 ? q.y : (c >> 1 & 3) == 2 ? q.z : q.w;
+            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&word));
+            v[c] = fmaf(g.add_by, x.x, g.by * v[c]);
+            v[c + 1] = fmaf(g.add_by, x.y, g.by * v[c + 1]);
+        }
+        if (rests) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+                const uint4& q = b[c >> 4];
+                const uint32_t word = (c >> 2 & 3) == 0 ? q.x : (c >> 2 & 3) == 1 ? q.y : (c >> 2 & 3) == 2 ? q.z : q.w;
+                const float2 x = rest_values(word >> 8 * (c & 2));
+                v[c] = fmaf(g.rest_by, x.x, v[c]);
+                v[c + 1] = fmaf(g.rest_by, x.y, v[c + 1]);
+            }
+            if (g.rest_out) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t n[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2)
+                        n[k >> 2] |= rests2(v[16 * c + k], v[16 * c + k + 1], __floats2half2_rn(v[16 * c + k], v[16 * c + k + 1]), kRestScale) << 8 * (k & 2);
+                    if (live && j + 16 * c < g.cols) *reinterpret_cast<uint4*>(rest + 16 * c) = make_uint4(n[0], n[1], n[2], n[3]);
+                }
             }
         }
     } else {
@@ -671,7 +750,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) muon_ge
 // their parts of A in rank order, compute B each for itself and turn their slices to the next X in place. What
 // bounds it: the passes over g, m and p at the start and end, then the five iterations' chain of products,
 // exchanges and barriers (about 5 us each; one 16 x 1160 takes 31 us, 64 adapters of up to 64 x 2567 70).
-constexpr int kSmallItems = 128, kSmallThreads = 512;
+constexpr int kSmallItems = 128, kSmallThreads = 512, kMostSmallSmem = 225 * 1024;
 template <int R>
 struct Small {  // R rows of X
     static constexpr int kMostBlocks = R == 64 ? 24 : 8;   // 64-column blocks of X that fit a CTA
@@ -685,11 +764,15 @@ struct Small {  // R rows of X
     // TMEM while its cluster waits for it could wait forever. Two CTAs of 256 columns share one (80 KB each at least: no
     // third fits; the 8-bit product of few tokens likewise), one of 512 columns has it alone (beside 152 KB no 80 fit).
     static constexpr int kLeastSmem = (R == 64 ? 80 : 152) * 1024;
-    static constexpr int smem(int blocks) {
-        const int need = blocks * kBlockBytes + kABytes + kPBytes + 1024;
+    // X's rests, half as many bytes, lie beside it where that costs no CTA its place on the SM, else in the workspace.
+    __host__ __device__ static constexpr bool rests_fit(int blocks) { return R == 64 ? blocks <= 6 || (blocks > kSliceBlocks && blocks <= 16) : blocks <= 5; }
+    __host__ __device__ static constexpr int smem(int blocks) {
+        const int need = blocks * kBlockBytes / 2 * (rests_fit(blocks) ? 3 : 2) + kABytes + kPBytes + 1024;
         return need > kLeastSmem ? need : kLeastSmem;
     }
-    static_assert(512 / kTmemCols * kLeastSmem + 80 * 1024 > 228 * 1024 && (R == 128 || 2 * smem(kSliceBlocks) <= 225 * 1024), "");
+    static_assert(512 / kTmemCols * kLeastSmem + 80 * 1024 > 228 * 1024, "");
+    static_assert(R == 128 || (2 * smem(6) <= 225 * 1024 && 2 * smem(kSliceBlocks) <= 225 * 1024), "");
+    static_assert(smem(R == 64 ? 16 : 5) <= kMostSmallSmem && smem(kMostBlocks) <= kMostSmallSmem, "");
 };
 
 struct SmallItem {
@@ -697,13 +780,14 @@ struct SmallItem {
     float* master;
     const void* g;
     float* m;
+    uint8_t* rest;          // the slices' rests in the workspace, where shared memory has no room (Small::rests_fit)
     int rows, cols, width;  // width: columns of a slice (a multiple of 64)
     float rate, decay;
     bool g32;
 };
 struct SmallArgs {
     SmallItem item[kSmallItems];
-    int n, ctas, iterations, blocks;  // ctas: of a matrix (a cluster); blocks: the widest slice's
+    int n, ctas, iterations;  // ctas: of a matrix (a cluster)
     float a, b, c, mu, eps;
     bool nesterov;
     const float *grad_scale, *lr_dev;
@@ -836,12 +920,18 @@ struct Slice {
     int per_row, units, live, r, k, col0, block_bytes;
     float inv_r;
     bool tall;
-    uint8_t* x;
+    int rows;  // of the memory: 64 or 128
+    uint8_t *x, *rest;  // (rest: shared memory or the workspace)
     __device__ __forceinline__ Unit unit(int u) const { return unit_of(u, per_row, live, r, k, col0, tall); }
     // where X holds the element o of a tall matrix's unit
     __device__ __forceinline__ __half* tall_at(const Unit& u, int o) const {
         const int e = u.c + o, c = __float2int_rz(((float)e + 0.5f) * inv_r), i = e - c * r;  // (e / r, exact below 2^22)
         return reinterpret_cast<__half*>(x + (c >> 6) * block_bytes + i * 128 + ((((c & 63) >> 3) ^ (i & 7)) << 4) + (c & 7) * 2);
+    }
+    __device__ __forceinline__ void tall_put(const Unit& u, int o, __half h, uint8_t code) const {
+        const int e = u.c + o, c = __float2int_rz(((float)e + 0.5f) * inv_r), i = e - c * r;
+        *tall_at(u, o) = h;
+        rests_at(c >> 4, i)[c & 15] = code;
     }
     // Where X holds the lane's four neighbours h (vectors), or its element d: a unit starts at a multiple of 256 columns.
     __device__ __forceinline__ uint2* four_at(const Unit& u, int h, int lane) const {
@@ -852,22 +942,35 @@ struct Slice {
         return reinterpret_cast<__half*>(x + ((u.c >> 6) + (d >> 1)) * block_bytes + u.i * 128 +
                                          ((((lane >> 3) + 4 * (d & 1)) ^ (u.i & 7)) << 4) + (lane & 7) * 2);
     }
-    // (a row's slice ends at a multiple of 4 columns where there are vectors; X has room up to a multiple of 64)
+    // Where the rests of row i's 16 columns from 16 h on lie: a warp's 32 rows one behind the other.
+    __device__ __forceinline__ uint8_t* rests_at(int h, int i) const { return rest + (h * rows + i) * 16; }
+    // X = v * scale and its rests. (A row's slice ends at a multiple of 4 columns where there are vectors; X has room up to
+    // a multiple of 64.)
     template <bool kVec>
     __device__ __forceinline__ void put(const Unit& u, const float (&v)[kDeep], float scale, int lane) const {
 #pragma unroll
         for (int d = 0; d < kDeep; d += kVec ? 4 : 1) {
             const int o = offset_of<kVec>(d, lane);
             if (o >= u.left) continue;
+            constexpr int kWide = kVec ? 4 : 1;
+            __half2 h[kVec ? 2 : 1];
+            uint32_t codes = 0;
+#pragma unroll
+            for (int j = 0; j < kWide; j += 2) {
+                const float x0 = v[d + j] * scale, x1 = kVec ? v[(d + j + 1) % kDeep] * scale : 0.0f;
+                h[j / 2] = __floats2half2_rn(x0, x1);
+                codes |= rests2(x0, x1, h[j / 2], kRestScaleStart) << 8 * j;
+            }
             if (tall) {
 #pragma unroll
-                for (int j = 0; j < (kVec ? 4 : 1); ++j)
-                    if (o + j < u.left) *tall_at(u, o + j) = __float2half_rn(v[d + j] * scale);
+                for (int j = 0; j < kWide; ++j)
+                    if (o + j < u.left) tall_put(u, o + j, j & 1 ? __high2half(h[j / 2]) : __low2half(h[j / 2]), (uint8_t)(codes >> 8 * j));
             } else if (kVec) {
-                *four_at(u, d >> 2, lane) = make_uint2(pack_half(v[d] * scale, v[(d + 1) % kDeep] * scale),
-                                                       pack_half(v[(d + 2) % kDeep] * scale, v[(d + 3) % kDeep] * scale));
+                *four_at(u, d >> 2, lane) = make_uint2(*reinterpret_cast<const uint32_t*>(&h[0]), *reinterpret_cast<const uint32_t*>(&h[kVec ? 1 : 0]));
+                *reinterpret_cast<uint32_t*>(rests_at((u.c + o) >> 4, u.i) + ((u.c + o) & 15)) = codes;
             } else {
-                *one_at(u, d, lane) = __float2half_rn(v[d] * scale);
+                *one_at(u, d, lane) = __low2half(h[0]);
+                rests_at((u.c + o) >> 4, u.i)[(u.c + o) & 15] = (uint8_t)codes;
             }
         }
     }
@@ -894,8 +997,8 @@ struct Slice {
     }
 };
 
-// The power of two that brings `top` to 2^8 (fp16 then has 2^8 to spare above it, and 2^22 below it as normal
-// numbers); 0 and what is not finite: 1.
+// The power of two that brings `top` to 2^8 (fp16 then has 2^22 below it as normal numbers, and values up to 2^12 find
+// room for their rests); 0 and what is not finite: 1.
 __device__ __forceinline__ float x_scale(float top) {
     const int e = (int)(__float_as_uint(top) >> 23);
     return top > 0.0f && e < 255 ? __uint_as_float((uint32_t)min(max(127 + 8 - (e - 127), 1), 254) << 23) : 1.0f;
@@ -957,7 +1060,7 @@ __device__ __forceinline__ float read_slice(const SmallItem& it, const SmallArgs
         s.put<kVec>(x, u, scale, lane);
     }
     top = block_top(top, sums);
-    if (top * scale < 32768.0f && (top * scale >= 1.0f || top == 0.0f)) return scale;
+    if (top * scale < 4096.0f && (top * scale >= 1.0f || top == 0.0f)) return scale;
     scale = x_scale(top);
     for (int n = warp; n < s.units; n += kWarps) {
         x = s.unit(n);
@@ -986,7 +1089,7 @@ __device__ __forceinline__ void write_slice(const SmallItem& it, const Slice& s,
 }
 
 template <int R>
-__global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __grid_constant__ SmallArgs a) {
+__global__ void __launch_bounds__(kSmallThreads, R == 64 ? 2 : 1) muon_small_kernel(const __grid_constant__ SmallArgs a) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[2];  // products: two regions of TMEM take turns
     __shared__ uint32_t tmem_slot;
@@ -1012,8 +1115,10 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
     const int blocks = it.width / 64;
     constexpr int block_bytes = Small<R>::kBlockBytes, kTile = Small<R>::kTile;
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t sx = sbase, sa = sbase + a.blocks * block_bytes, sb = sa + Small<R>::kABytes, sp = sb;
+    const uint32_t sx = sbase, sa = sbase + blocks * block_bytes, sb = sa + Small<R>::kABytes, sp = sb;
     uint8_t* const generic = smem_raw + (sbase - smem_u32(smem_raw));
+    uint8_t* const rest = Small<R>::rests_fit(blocks) ? generic + (sb - sbase) + Small<R>::kPBytes
+                                                      : it.rest + (long long)rank * blocks * (block_bytes / 2);
     const uint32_t bar_mma = smem_u32(&bars[0]);
 
     if (tid == 0) {
@@ -1027,8 +1132,10 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
         tmem_alloc(smem_u32(&tmem_slot), Small<R>::kTmemCols);
         tmem_relinquish();
     }
-    for (int i = tid; i < blocks * block_bytes / 16; i += kSmallThreads)
+    for (int i = tid; i < blocks * block_bytes / 16; i += kSmallThreads) {
         reinterpret_cast<uint4*>(generic)[i] = make_uint4(0, 0, 0, 0);
+        if (i & 1) reinterpret_cast<uint4*>(rest)[i >> 1] = make_uint4(0, 0, 0, 0);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1086,6 +1193,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
     slice.block_bytes = block_bytes;
     slice.tall = tall;
     slice.x = generic;
+    slice.rows = R;
+    slice.rest = rest;
     const bool vec = tall || k % 4 == 0;  // (slices start at multiples of 64 columns)
     float sq;
     const float up = vec ? read_slice<true>(it, a, slice, f, s_sums, sq) : read_slice<false>(it, a, slice, f, s_sums, sq);
@@ -1253,41 +1362,74 @@ __global__ void __launch_bounds__(kSmallThreads, 2) muon_small_kernel(const __gr
         const float of_x = poly.of_x(shift) * scale;
         // a warp's columns of a tile: a quarter of it; where the lanes from 64 on hold the same rows again, half of that
         const int i = R == 64 ? row & 63 : row, own0 = R == 64 ? group * 32 + (quarter >> 1) * 16 : group * 64;
+        const float of_rest = (n + 1 < kRests ? a.a * scale : of_x) / (n == 0 ? kRestScaleStart : kRestScale);
+        const uint64_t of_x2 = f2_pack(of_x, of_x), scale2 = f2_pack(scale, scale), of_rest2 = f2_pack(of_rest, of_rest);
         __half2 square = __float2half2_rn(0.0f);
-        for (int t = 0; t < tiles; ++t) {
-            mma_wait(t & 1);
+        auto turn = [&](auto reads, auto writes) {  // (a form each: a branch within the loop costs every iteration)
+            constexpr bool kRead = decltype(reads)::value, kWrite = decltype(writes)::value;
+            for (int t = 0; t < tiles; ++t) {
+                mma_wait(t & 1);
 #pragma unroll
-            for (int c = own0; c < own0 + (R == 64 ? 16 : 64); c += 16) {
-                const int block = kTileBlocks * t + (c >> 6);
-                if (block >= blocks) break;
-                uint32_t v[16];
-                tmem_ld16(tmem + kTile * (t & 1) + lanes + c, v);
-                tmem_ld_wait();
+                for (int c = own0; c < own0 + (R == 64 ? 16 : 64); c += 16) {
+                    const int block = kTileBlocks * t + (c >> 6);
+                    if (block >= blocks) break;
+                    // (everything is read before anything is written)
+                    uint4* const low = reinterpret_cast<uint4*>(slice.rests_at((kTile * t + c) >> 4, i));
+                    uint4 rests = make_uint4(0, 0, 0, 0);
+                    if (kRead) rests = *low;
+                    uint4* const at0 = reinterpret_cast<uint4*>(generic + block * block_bytes + chunk_at(i, (c & 63) >> 3));
+                    uint4* const at1 = reinterpret_cast<uint4*>(generic + block * block_bytes + chunk_at(i, ((c & 63) >> 3) + 1));
+                    const uint4 w0 = *at0, w1 = *at1;
+                    uint32_t v[16];
+                    tmem_ld16(tmem + kTile * (t & 1) + lanes + c, v);
+                    tmem_ld_wait();
+                    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                    uint64_t x[8];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint4* const at = reinterpret_cast<uint4*>(generic + block * block_bytes + chunk_at(i, ((c & 63) >> 3) + h));
-                    const uint4 w = *at;
-                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t o[4];
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+                        x[j] = fma_f2(of_x2, f2_pack(y.x, y.y), mul_f2(scale2, f2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]))));
+                    }
+                    if (kRead) {
+                        const uint32_t l[4] = {rests.x, rests.y, rests.z, rests.w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
-                        const float x0 = fmaf(of_x, y.x, scale * __uint_as_float(v[8 * h + 2 * j]));
-                        const float x1 = fmaf(of_x, y.y, scale * __uint_as_float(v[8 * h + 2 * j + 1]));
+                        for (int j = 0; j < 8; ++j) {
+                            const float2 y = rest_values(l[j >> 1] >> 16 * (j & 1));
+                            x[j] = fma_f2(of_rest2, f2_pack(y.x, y.y), x[j]);
+                        }
+                    }
+                    uint32_t o[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float x0, x1;
+                        f2_unpack(x[j], x0, x1);
                         const __half2 y2 = __floats2half2_rn(x0, x1);
                         square = __hfma2(y2, y2, square);  // (fp16 is enough for where to shift)
                         o[j] = *reinterpret_cast<const uint32_t*>(&y2);
                     }
-                    *at = make_uint4(o[0], o[1], o[2], o[3]);
+                    *at0 = make_uint4(o[0], o[1], o[2], o[3]);
+                    *at1 = make_uint4(o[4], o[5], o[6], o[7]);
+                    if (kWrite) {
+                        uint32_t l[4] = {0, 0, 0, 0};
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) l[j >> 1] |= rests2(x[j], *reinterpret_cast<const __half2*>(&o[j]), kRestScale) << 16 * (j & 1);
+                        *low = make_uint4(l[0], l[1], l[2], l[3]);
+                    }
+                }
+                if (t + 2 < tiles) {  // (the tile is read out)
+                    tc_fence_before();
+                    __syncthreads();
+                    tc_fence_after();
+                    issue(t + 2);
                 }
             }
-            if (t + 2 < tiles) {  // (the tile is read out)
-                tc_fence_before();
-                __syncthreads();
-                tc_fence_after();
-                issue(t + 2);
-            }
-        }
+        };
+        if (n + 1 < kRests)
+            turn(std::true_type{}, std::true_type{});
+        else if (n < kRests)
+            turn(std::true_type{}, std::false_type{});
+        else
+            turn(std::false_type{}, std::false_type{});
         squares[tid] = __low2float(square) + __high2float(square);
         publish();
         scale = 1.0f;
@@ -1314,14 +1456,15 @@ size_t up(size_t x, size_t k) { return (x + k - 1) / k * k; }
 
 // Where a list's matrices lie in the workspace.
 struct Size {
-    int r, k, ld, ldr, count;          // r <= k; X rows of ld, A and B rows of ldr elements
-    size_t x[2], a, b;                 // byte offsets: X twice (read and written in turn), A, B
+    int r, k, ld, ldr, ld_rest, count;  // r <= k; rows of X, of A and B, of the rests: elements apart
+    size_t x[2], b, rest;              // byte offsets: X twice (read and written in turn; A lies in the one that is to be
+                                       // written next), B, the rests
 };
 struct Plan {
     std::vector<Size> sizes;
     std::vector<int> of, z, parts;     // a matrix's size, its place among them, its partial sums
     std::vector<long long> chunk;
-    std::vector<size_t> part;          // byte offset of its partial sums
+    std::vector<size_t> part;          // byte offset of its partial sums; small matrices: of their rests
     size_t bytes = 0;
 };
 
@@ -1336,6 +1479,17 @@ int small_ctas(const rlk_muon_matrix& t) {
     return k <= n * 64LL * (r <= 64 ? Small<64>::kMostBlocks : Small<128>::kMostBlocks) ? n : 0;
 }
 
+// Columns of a CTA's slice, and bytes of the rests that find no room in shared memory.
+int small_width(const rlk_muon_matrix& t, int ctas) {
+    const long long k = t.rows < t.cols ? t.cols : t.rows;
+    return (int)up((k + ctas - 1) / ctas, 64);
+}
+size_t small_rests(const rlk_muon_matrix& t, int ctas) {
+    const int r = (int)(t.rows < t.cols ? t.rows : t.cols), width = small_width(t, ctas);
+    if (r <= 64 ? Small<64>::rests_fit(width / 64) : Small<128>::rests_fit(width / 64)) return 0;
+    return (size_t)ctas * width * (r <= 64 ? 64 : 128);
+}
+
 void plan_of(const rlk_muon_matrix* t, int n, Plan& p) {
     p.of.assign(n, -1);
     p.z.assign(n, 0);
@@ -1344,10 +1498,16 @@ void plan_of(const rlk_muon_matrix* t, int n, Plan& p) {
     p.part.assign(n, 0);
     std::map<std::pair<int, int>, int> known;
     for (int i = 0; i < n; ++i) {
-        if (t[i].rows == 0 || t[i].cols == 0 || small_ctas(t[i]) > 0) continue;
+        if (t[i].rows == 0 || t[i].cols == 0) continue;
+        if (const int ctas = small_ctas(t[i])) {
+            p.bytes = up(p.bytes, 16);
+            p.part[i] = p.bytes;
+            p.bytes += small_rests(t[i], ctas);
+            continue;
+        }
         const int r = (int)(t[i].rows < t[i].cols ? t[i].rows : t[i].cols), k = (int)(t[i].rows < t[i].cols ? t[i].cols : t[i].rows);
         const int s = known.emplace(std::make_pair(r, k), (int)p.sizes.size()).first->second;
-        if (s == (int)p.sizes.size()) p.sizes.push_back(Size{r, k, (int)up(k, 8), (int)up(r, 8), 0, {0, 0}, 0, 0});
+        if (s == (int)p.sizes.size()) p.sizes.push_back(Size{r, k, (int)up(k, 8), (int)up(r, 8), (int)up(k, 16), 0, {0, 0}, 0, 0});
         p.of[i] = s;
         p.z[i] = p.sizes[s].count++;
         const long long e = t[i].rows * t[i].cols;
@@ -1355,6 +1515,7 @@ void plan_of(const rlk_muon_matrix* t, int n, Plan& p) {
         chunk = (long long)up(chunk < kMinChunk ? kMinChunk : chunk, 4 * kPassThreads);
         p.chunk[i] = chunk;
         p.parts[i] = (int)((e + chunk - 1) / chunk);
+        p.bytes = up(p.bytes, sizeof(double));
         p.part[i] = p.bytes;
         p.bytes += sizeof(double) * p.parts[i];
     }
@@ -1366,8 +1527,8 @@ void plan_of(const rlk_muon_matrix* t, int n, Plan& p) {
             return at;
         };
         for (size_t& x : s.x) x = take((size_t)s.count * s.r * s.ld * 2);
-        s.a = take((size_t)s.count * s.r * s.ldr * 2);
         s.b = take((size_t)s.count * s.r * s.ldr * 2);
+        s.rest = take((size_t)s.count * s.r * s.ld_rest);
     }
 }
 
@@ -1464,7 +1625,8 @@ void rates_of(const rlk_muon_matrix& d, const rlk_muon_args& q, float& rate, flo
 // The small matrices of up to R rows (and more than 64, if R is 128), those of one number of CTAs a launch; `more`: a
 // launch of them came before, and this one may run beside it.
 template <int R>
-cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool step, bool& more, cudaStream_t s) {
+cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool step, const Plan& plan, uint8_t* ws, bool& more,
+                      cudaStream_t s) {
     SmallArgs a;
     a.iterations = q.iterations;
     a.a = (float)q.a;
@@ -1475,16 +1637,17 @@ cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, b
     a.nesterov = q.nesterov != 0;
     a.grad_scale = step ? q.grad_scale : nullptr;
     a.lr_dev = step ? q.lr_dev : nullptr;
+    int smem = 0;  // what the matrix that needs most takes
     auto launch = [&]() {
         cudaError_t e = cudaFuncSetAttribute(muon_small_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             Small<R>::smem(Small<R>::kMostBlocks));
+                                             kMostSmallSmem);
         // (all of it for shared memory: two CTAs an SM)
         if (e == cudaSuccess) e = cudaFuncSetAttribute(muon_small_kernel<R>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t c{};
         c.gridDim = dim3((unsigned)(a.n * a.ctas));
         c.blockDim = dim3(kSmallThreads);
-        c.dynamicSmemBytes = Small<R>::smem(a.blocks);
+        c.dynamicSmemBytes = smem;
         c.stream = s;
         cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1501,16 +1664,16 @@ cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, b
         return e;
     };
     for (a.ctas = 8; a.ctas > 0; a.ctas /= 2) {
-        a.n = a.blocks = 0;
+        a.n = smem = 0;
         for (int i = 0; i <= n; ++i) {
             if (a.n > 0 && (i == n || a.n == kSmallItems)) {
                 const cudaError_t e = launch();
                 if (e != cudaSuccess) return e;
-                a.n = a.blocks = 0;
+                a.n = smem = 0;
             }
             if (i == n) break;
             const rlk_muon_matrix& d = t[i];
-            const long long r = d.rows < d.cols ? d.rows : d.cols, k = d.rows < d.cols ? d.cols : d.rows;
+            const long long r = d.rows < d.cols ? d.rows : d.cols;
             if (r == 0 || (r <= 64) != (R == 64) || small_ctas(d) != a.ctas) continue;
             SmallItem& it = a.item[a.n++];
             it.p = d.p;
@@ -1519,28 +1682,29 @@ cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, b
             it.m = step ? d.m : nullptr;
             it.rows = (int)d.rows;
             it.cols = (int)d.cols;
-            it.width = (int)up((k + a.ctas - 1) / a.ctas, 64);
+            it.width = small_width(d, a.ctas);
+            it.rest = ws + plan.part[i];
             rates_of(d, q, it.rate, it.decay);
             it.g32 = d.g_dtype == RLK_FP32;
-            if (it.width / 64 > a.blocks) a.blocks = it.width / 64;
+            if (Small<R>::smem(it.width / 64) > smem) smem = Small<R>::smem(it.width / 64);
         }
     }
     return cudaSuccess;
 }
 
 cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool step, void* workspace, cudaStream_t s) {
-    bool more = false;
-    for (const auto small : {run_small<64>, run_small<128>}) {
-        const cudaError_t e = small(t, n, q, step, more, s);
-        if (e != cudaSuccess) return e;
-    }
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
     Plan plan;
     plan_of(t, n, plan);
+    bool more = false;
+    for (const auto small : {run_small<64>, run_small<128>}) {
+        const cudaError_t e = small(t, n, q, step, plan, ws, more, s);
+        if (e != cudaSuccess) return e;
+    }
     if (plan.sizes.empty()) return cudaSuccess;
     int pairs = 0;
     cudaError_t e = pairs_of(&pairs);
     if (e != cudaSuccess) return e;
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
     std::vector<Item> items;
     std::vector<float> start(plan.sizes.size());
     for (size_t i = 0; i < plan.sizes.size(); ++i) start[i] = start_of(plan.sizes[i].r);
@@ -1554,6 +1718,8 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
         it.g = d.g;
         it.m = step ? d.m : nullptr;
         it.x = reinterpret_cast<__half*>(ws + z.x[0]) + (size_t)plan.z[i] * z.r * z.ld;
+        it.rest = ws + z.rest + (size_t)plan.z[i] * z.r * z.ld_rest;
+        it.ld_rest = z.ld_rest;
         it.part = reinterpret_cast<double*>(ws + plan.part[i]);
         it.n = d.rows * d.cols;
         it.chunk = plan.chunk[i];
@@ -1588,17 +1754,17 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
     for (size_t g0 = 0; g0 < plan.sizes.size(); g0 += kGroups) {
         const int ng = (int)(plan.sizes.size() - g0 < kGroups ? plan.sizes.size() - g0 : kGroups);
         // X as the operand of 128 rows (gram) and of 256 columns (apply), both buffers; A; B
-        CUtensorMap x_rows[kGroups][2], x_cols[kGroups][2], x_out[kGroups][2], map_a[kGroups], map_b[kGroups], a_out[kGroups], b_out[kGroups];
+        CUtensorMap x_rows[kGroups][2], x_cols[kGroups][2], x_out[kGroups][2], map_a[kGroups][2], a_out[kGroups][2], map_b[kGroups], b_out[kGroups];
         for (int g = 0; g < ng; ++g) {
             const Size& z = plan.sizes[g0 + g];
-            bool ok = half_map(&map_a[g], ws + z.a, z.r, z.r, z.count, z.ldr, 128) &&
-                      half_map(&map_b[g], ws + z.b, z.r, z.r, z.count, z.ldr, 128) &&
-                      half_map(&a_out[g], ws + z.a, z.r, z.r, z.count, z.ldr, 32, true) &&
+            bool ok = half_map(&map_b[g], ws + z.b, z.r, z.r, z.count, z.ldr, 128) &&
                       half_map(&b_out[g], ws + z.b, z.r, z.r, z.count, z.ldr, 32, true);
             for (int i = 0; i < 2; ++i)
                 ok = ok && half_map(&x_rows[g][i], ws + z.x[i], z.k, z.r, z.count, z.ld, 128) &&
                      half_map(&x_cols[g][i], ws + z.x[i], z.k, z.r, z.count, z.ld, 64) &&
-                     half_map(&x_out[g][i], ws + z.x[i], z.k, z.r, z.count, z.ld, 32, true);
+                     half_map(&x_out[g][i], ws + z.x[i], z.k, z.r, z.count, z.ld, 32, true) &&
+                     half_map(&map_a[g][i], ws + z.x[i], z.r, z.r, z.count, z.ldr, 128) &&
+                     half_map(&a_out[g][i], ws + z.x[i], z.r, z.r, z.count, z.ldr, 32, true);
             if (!ok) return cudaErrorInvalidValue;
         }
         const Poly poly{(float)q.a, (float)q.b, (float)q.c};
@@ -1623,32 +1789,43 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
                     Group& d = ga.g[n_g];
                     auto half = [&](size_t at) { return reinterpret_cast<__half*>(ws + at); };
                     const float scale = i == 0 ? 1.0f / start[g0 + g] : 1.0f;  // of X, until the first apply
+                    const int now = i & 1, next = now ^ 1;  // X is read from the one, A and then the new X lie in the other
                     d.rows = z.r;
                     d.count = z.count;
+                    d.rest = nullptr;
+                    d.rest_out = false;
                     if (mode == kGram) {
-                        d.map_m = d.map_n = x_rows[g][i & 1];
-                        d.map_out = a_out[g];
+                        d.map_m = d.map_n = x_rows[g][now];
+                        d.map_out = a_out[g][next];
                         d.add = nullptr;
-                        d.out = half(z.a);
+                        d.out = half(z.x[next]);
                         d.by = scale * scale;
                         d.add_by = -shift[g];
                         d.steps = (z.k + kBK - 1) / kBK;
                     } else if (mode == kPoly) {
-                        d.map_m = d.map_n = map_a[g];
+                        d.map_m = d.map_n = map_a[g][next];
                         d.map_out = b_out[g];
-                        d.add = half(z.a);
+                        d.add = half(z.x[next]);
                         d.out = half(z.b);
                         d.by = poly.c;
                         d.add_by = poly.of_d(shift[g]);
                         d.steps = (z.r + kBK - 1) / kBK;
                     } else {
                         d.map_m = map_b[g];
-                        d.map_out = x_out[g][(i + 1) & 1];
-                        d.map_n = x_cols[g][i & 1];
-                        d.add = half(z.x[i & 1]);
-                        d.out = half(z.x[(i + 1) & 1]);
+                        d.map_out = x_out[g][next];
+                        d.map_n = x_cols[g][now];
+                        d.add = half(z.x[now]);
+                        d.out = half(z.x[next]);
                         d.by = scale;
                         d.add_by = poly.of_x(shift[g]) * scale;
+                        if (i < kRests) {
+                            d.rest = ws + z.rest;
+                            d.rest_by = i + 1 < kRests ? poly.a * scale : d.add_by;
+                            d.rest_by *= (i == 0 ? start[g0 + g] : 1.0f) / kRestScale;
+                            d.ld_rest = z.ld_rest;
+                            d.rest_step = (long long)z.r * z.ld_rest;
+                            d.rest_out = i + 1 < kRests;
+                        }
                         d.steps = (z.r + kBK - 1) / kBK;
                     }
                     d.cols = mode == kApply ? z.k : z.r;

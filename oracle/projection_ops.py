@@ -80,3 +80,41 @@ def muon(p, m, g, lr, momentum, nesterov, weight_decay, update_rms, **kw):
     m = momentum * m + g
     x = orthogonal(g + momentum * m if nesterov else m, **kw)
     return p - lr * weight_decay * p - lr * update_rms * np.sqrt(max(p.shape)) * x, m, x
+
+
+def kept(x, scale):
+    """x as the kernels keep it: (fp16, and what that leaves as an e4m3 code of ``scale`` times it; scale 0: none)."""
+    h = _half(x)
+    if scale == 0:
+        return h, np.zeros_like(h)
+    y = np.clip((x - h) * scale, -448.0, 448.0)
+    _, e = np.frexp(y)
+    step = np.exp2(np.maximum(e - 1, -6) - 3)
+    return h, np.rint(y / step) * step / scale
+
+
+def orthogonal_as_kept(u, iterations=5, coefficients=POLYNOMIAL, eps=1e-7, rests=3, lead=1.0, alone=None):
+    """X of u with the kernels' own roundings and exact sums. A = D + s I is kept as D, so that X = of_x X + B X with
+    of_x = a + b s + c s^2 and B = (b + 2 c s) D + c D D; X, D and B are fp16, the first ``rests`` X's with codes of
+    their rests, which enter X alone: with a, the last of them with of_x. s is the mean of A's diagonal (1 / r at first) for the
+    matrices that one kernel takes (``alone``), else what the polynomial makes of 0.35 / r, 1 at most. ``lead``: another
+    factor at the start draws other roundings."""
+    u = np.asarray(u, np.float64)
+    if u.shape[0] > u.shape[1]:
+        return orthogonal_as_kept(u.T, iterations, coefficients, eps, rests, lead, alone).T
+    r, k = u.shape
+    if alone is None:
+        alone = r <= 128 and k <= (12288 if r <= 64 else 4096)
+    a, b, c = coefficients
+    start = 2.0 ** np.floor(0.5 * np.log2(r)) * lead
+    x, low = kept(u * (start / (np.sqrt((u * u).sum()) + eps)), 2.0 ** 20 / start if rests > 0 else 0)
+    scale, square = 1.0 / start, 0.35 / r
+    for n in range(iterations):
+        s = (1.0 / r if n == 0 else (x * x).sum() / r) if alone else min(square, 1.0)
+        square *= (a + b * square + c * square * square) ** 2
+        of_x = a + b * s + c * s * s
+        d = _half(x @ x.T * scale ** 2 - s * np.eye(r))
+        poly = _half((b + 2 * c * s) * d + c * (d @ d))
+        x, low = kept(scale * (of_x * x + (a if n + 1 < rests else of_x) * low + poly @ x), 2.0 ** 20 if n + 1 < rests else 0)
+        scale = 1.0
+    return x
