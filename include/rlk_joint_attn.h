@@ -727,15 +727,15 @@ rlk_status rlk_fp8_gemm(const rlk_fp8_product* items, int32_t n_items, void* str
  * rlk_orthogonalize stops at X: x in, its X out in bf16.
  *
  * X, A less a multiple of the identity, and the polynomial's part that goes with
- * it are held in fp16, the first three X's with codes of what that leaves, with fp32
- * accumulators. With the polynomial (3.4445, -4.775, 2.0315) and five iterations X
- * is within 2^-9 of the formula's in the norm, within 2^-10 for independent
- * entries, also where a few directions lead the others by 100 times; within 2^-7
- * where the others hold less than that or nothing. The
- * norm's squares are fp32 (magnitudes below 2^-63 vanish, a norm above 2^63 is
- * infinite and gives X = 0), its sum fp64; m and p are fp32. Sums have a fixed order without atomics: a matrix's
- * result does not depend on the list or its place in it. Matrices with an
- * infinity or NaN become NaN, as their formulas do. */
+ * it are held in fp16, the first three X's with codes of what that leaves, with
+ * fp32 accumulators. With the polynomial (3.4445, -4.775, 2.0315) and five
+ * iterations X is within 2^-9 of the formula's in the norm, also where a few
+ * directions lead the others by 100 times (independent entries: about half of
+ * that), within 2^-7 where the others hold less than that or nothing. The norm's
+ * squares are fp32, their sum fp64: a norm below 2^-56 counts as 2^-56, one above
+ * 2^63 is infinite and gives X = 0. m and p are fp32. Sums have a fixed order
+ * without atomics: a matrix's result does not depend on the list or its place in
+ * it. Matrices with an infinity or NaN become NaN, as their formulas do. */
 typedef struct rlk_muon_matrix {
     void* p;            /* [rows, cols] fp32, or bf16 when master is given; rlk_orthogonalize: bf16, written */
     float* master;      /* [rows, cols] or NULL; rlk_orthogonalize: NULL */

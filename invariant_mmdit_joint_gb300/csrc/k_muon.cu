@@ -118,6 +118,12 @@ __device__ __forceinline__ bool factor_of(const PassArgs& a, float& f) {
     f = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
     return fabsf(f) < INFINITY;
 }
+// |u| from the sum of its squares, at least 2^-56: fp32 squares of magnitudes below 2^-75 are 0, and as many of them as a
+// matrix has come to 2^-59. (A quotient by less would make X as large as it likes with a small eps.)
+__device__ __forceinline__ float norm_of(double squares) {
+    const float n = sqrtf((float)squares);
+    return n < 0x1p-56f ? 0x1p-56f : n;  // (a NaN stays)
+}
 // The sum over the CTA's threads, in a fixed order.
 __device__ __forceinline__ double block_sum(double v) {
     __shared__ double s[kPassThreads / 32];
@@ -288,7 +294,7 @@ __global__ void __launch_bounds__(kPassThreads, 6) muon_start_kernel(const __gri
         for (int i = threadIdx.x; i < it.parts; i += 32) sq += it.part[i];
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, k);
-        if (threadIdx.x == 0) s_inv = it.start / (sqrtf((float)sq) + a.eps);
+        if (threadIdx.x == 0) s_inv = it.start / (norm_of(sq) + a.eps);
     }
     __syncthreads();
     const float inv = s_inv, rest_scale = kRestScale / it.start;
@@ -1213,7 +1219,7 @@ __global__ void __launch_bounds__(kSmallThreads, R == 64 ? 2 : 1) muon_small_ker
     if (tid == 0) {
         double s = 0.0;
         for (int w = 0; w < ctas; ++w) s += ctas == 1 ? s_part : load_cluster_f64(map_rank(smem_u32(&s_part), w));
-        s_inv = 1.0f / (sqrtf((float)s) + a.eps);
+        s_inv = 1.0f / (norm_of(s) + a.eps);
     }
     publish();
 

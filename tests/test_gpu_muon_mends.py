@@ -4,7 +4,7 @@ import pytest
 
 import invariant_mmdit_joint_gb300 as pkg
 from tests import _helpers as Hh
-from tests.test_gpu_muon import gradient
+from tests.test_gpu_muon import assert_orthogonal, f64, gradient
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +34,23 @@ def test_orthogonalize_reads_no_argument_of_a_step(dev, rows, cols):
     pkg.rlk_orthogonalize(items, args, ws)
     pkg.rlk_joint_attn_check_status()
     assert Hh.bits_equal(want, got)
+
+
+@pytest.mark.parametrize("rows, cols", [(40, 50), (16, 1160), (300, 40), (200, 304), (301, 200)])
+def test_small_norms_with_any_eps(dev, rows, cols):
+    """Zero stays zero and nothing becomes infinite for the smallest eps; a norm above 2^-56 is the formula's, one below
+    counts as 2^-56: X is then no more than |u| 2^56 and its growth, 3.4445^5."""
+    import torch
+    x = gradient(dev, rows, cols, 2)
+    zero = torch.zeros_like(x)
+    for eps in (2.0 ** -126, 1e-30, 1e-7):
+        assert bool((pkg.orthogonalize([zero], eps=eps)[0] == 0).all()), eps
+        for size in (2.0 ** -60, 2.0 ** -70, 2.0 ** -90):  # (entries of about 2^-9 times this)
+            u = x * (size / float(x.double().norm()))
+            top = float(u.double().norm()) * 2.0 ** 56 * 3.45 ** 5
+            got = pkg.orthogonalize([u], eps=eps)[0]
+            assert bool(torch.isfinite(got).all()) and float(got.double().norm()) <= top + 2.0 ** -20, (eps, size)
+        u = x * (2.0 ** -50 / float(x.double().norm()))
+        if eps < 1e-7:
+            assert_orthogonal(pkg.orthogonalize([u], eps=eps)[0], f64(u), (rows, cols, eps), eps=eps)
+    pkg.rlk_joint_attn_check_status()
