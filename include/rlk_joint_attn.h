@@ -753,7 +753,7 @@ typedef struct rlk_muon_args {
     double a, b, c;          /* the polynomial: magnitudes up to 1e6; where it takes X, A or a part of
                                 itself past fp16's range (65504), the results are not finite */
     double eps;              /* 2^-126 .. 1 */
-    const float* lr_dev;     /* device, or NULL: read instead of lr */
+    const float* lr_dev;     /* device, or NULL: read instead of lr, with the bytes that the same number in lr gives */
     const float* grad_scale; /* device, or NULL (1). Not finite: every tensor is left as it was */
     int32_t iterations;      /* 1 .. 32 */
     int32_t nesterov;

@@ -46,11 +46,22 @@ namespace {
 using namespace sm100;
 
 // ------------------------------------------------------------------ elementwise passes
-constexpr int kItems = 40;          // matrices a launch of an elementwise pass takes (an argument of 4 KB)
+constexpr int kItems = 40;          // matrices a launch of an elementwise pass takes (an argument of 6 KB)
 constexpr int kPassThreads = 256;
 constexpr int kMaxPartials = 256;   // partial sums of squares of a matrix (each CTA of the start adds them)
 constexpr int kMinChunk = 8192;     // elements a partial sums, at least
 constexpr int kSide = 64;           // the passes' tiles
+
+// p -= decay p + rate X: fp64 and one rounding each, in one order, so that a rate on the device gives the bytes of the same
+// number from the host. One thread a matrix computes them: fp64 is slow here.
+struct Rates {
+    double lr_scale, weight_decay, update_rms, root;  // root: of the longer side
+    __device__ __forceinline__ void get(double lr, float& rate, float& decay) const {
+        lr *= lr_scale;
+        rate = (float)(lr * update_rms * root);
+        decay = (float)(lr * weight_decay);
+    }
+};
 
 struct Item {
     void* p;          // step: fp32, or bf16 with master; orthogonalize: bf16 out
@@ -63,7 +74,8 @@ struct Item {
     long long n, chunk;
     int rows, cols, ld, ld_rest, parts, block0;
     float start;      // X's power of two at the start
-    float rate, decay;  // p -= decay p + rate X (lr_dev: times its value)
+    float* rates;     // step: where the first pass leaves the last one's rate and decay
+    Rates rate;
     bool g32;
 };
 struct PassArgs {
@@ -71,7 +83,8 @@ struct PassArgs {
     int n;
     float mu, eps;
     bool nesterov;
-    const float *grad_scale, *lr_dev;
+    double lr;
+    const float *grad_scale, *lr_dev;  // lr_dev: read instead of lr
 };
 
 __device__ __forceinline__ const Item& item_of(const PassArgs& a) {
@@ -179,6 +192,8 @@ __global__ void __launch_bounds__(kPassThreads) muon_momentum_kernel(const __gri
     }
     sum = block_sum(sum);
     if (threadIdx.x == 0) it.part[chunk] = sum;
+    if (threadIdx.x == 32 && chunk == 0 && it.m != nullptr)
+        it.rate.get(a.lr_dev != nullptr ? (double)*a.lr_dev : a.lr, it.rates[0], it.rates[1]);
 }
 
 // A 64 x 64 tile of a matrix by 256 threads: thread t has eight columns of the rows t / 8 and t / 8 + 32, neighbours
@@ -365,8 +380,7 @@ __global__ void __launch_bounds__(kPassThreads, 5) muon_update_kernel(const __gr
             *reinterpret_cast<uint4*>(tile + turned((threadIdx.x >> 3) + 32 * k, 8 * (threadIdx.x & 7))) = x[k];
         __syncthreads();
     }
-    const float lr = a.lr_dev != nullptr ? *a.lr_dev : 1.0f;
-    const float rate = it.rate * lr, decay = it.decay * lr;
+    const float rate = it.m != nullptr ? it.rates[0] : 0.0f, decay = it.m != nullptr ? it.rates[1] : 0.0f;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int rr = (threadIdx.x >> 3) + 32 * k, r = at.r0 + rr, live = r >= it.rows ? 0 : min(it.cols - at.c0, kSide);
@@ -788,7 +802,7 @@ struct SmallItem {
     float* m;
     uint8_t* rest;          // the slices' rests in the workspace, where shared memory has no room (Small::rests_fit)
     int rows, cols, width;  // width: columns of a slice (a multiple of 64)
-    float rate, decay;
+    Rates rate;
     bool g32;
 };
 struct SmallArgs {
@@ -796,7 +810,8 @@ struct SmallArgs {
     int n, ctas, iterations;  // ctas: of a matrix (a cluster)
     float a, b, c, mu, eps;
     bool nesterov;
-    const float *grad_scale, *lr_dev;
+    double lr;
+    const float *grad_scale, *lr_dev;  // lr_dev: read instead of lr
 };
 
 __device__ __forceinline__ float4 load_cluster(uint32_t addr) {
@@ -1100,7 +1115,7 @@ __global__ void __launch_bounds__(kSmallThreads, R == 64 ? 2 : 1) muon_small_ker
     __shared__ __align__(8) uint64_t bars[2];  // products: two regions of TMEM take turns
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
-    __shared__ float s_sums[kSmallThreads / 32], s_inv;
+    __shared__ float s_sums[kSmallThreads / 32], s_inv, s_rates[2];
     __shared__ __align__(16) float s_group[8];  // X's sum of squares, each CTA's
     __shared__ __align__(8) double s_part;
 
@@ -1214,6 +1229,7 @@ __global__ void __launch_bounds__(kSmallThreads, R == 64 ? 2 : 1) muon_small_ker
         for (int w = 0; w < kSmallThreads / 32; ++w) s += (double)s_sums[w];
         s_part = s;
     }
+    if (tid == 32) it.rate.get(a.lr_dev != nullptr ? (double)*a.lr_dev : a.lr, s_rates[0], s_rates[1]);
     if (it.m != nullptr) fetch(true);  // (what the last pass reads)
     group_sync();
     if (tid == 0) {
@@ -1442,8 +1458,7 @@ __global__ void __launch_bounds__(kSmallThreads, R == 64 ? 2 : 1) muon_small_ker
     }
 
     // ---- the weights, or X itself
-    const float lr = a.lr_dev != nullptr ? *a.lr_dev : 1.0f;
-    const float rate = it.rate * lr, decay = it.decay * lr;
+    const float rate = s_rates[0], decay = s_rates[1];
     if (vec)
         write_slice<true>(it, slice, rate, decay);
     else
@@ -1523,7 +1538,7 @@ void plan_of(const rlk_muon_matrix* t, int n, Plan& p) {
         p.parts[i] = (int)((e + chunk - 1) / chunk);
         p.bytes = up(p.bytes, sizeof(double));
         p.part[i] = p.bytes;
-        p.bytes += sizeof(double) * p.parts[i];
+        p.bytes += sizeof(double) * (p.parts[i] + 1);  // (and its rates)
     }
     for (Size& s : p.sizes) {
         auto take = [&](size_t bytes) {
@@ -1621,11 +1636,8 @@ cudaError_t pass(const std::vector<Item>& items, PassArgs& a, bool apart, Blocks
 
 float start_of(long long r) { return (float)exp2(floor(0.5 * log2((double)r))); }
 
-// p -= decay p + rate X (lr_dev: times its value)
-void rates_of(const rlk_muon_matrix& d, const rlk_muon_args& q, float& rate, float& decay) {
-    const double lr = (q.lr_dev != nullptr ? 1.0 : q.lr) * d.lr_scale;
-    rate = (float)(lr * q.update_rms * sqrt((double)(d.rows > d.cols ? d.rows : d.cols)));
-    decay = (float)(lr * d.weight_decay);
+Rates rates_of(const rlk_muon_matrix& d, const rlk_muon_args& q) {
+    return Rates{d.lr_scale, d.weight_decay, q.update_rms, sqrt((double)(d.rows > d.cols ? d.rows : d.cols))};
 }
 
 // The small matrices of up to R rows (and more than 64, if R is 128), those of one number of CTAs a launch; `more`: a
@@ -1642,6 +1654,7 @@ cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, b
     a.eps = (float)q.eps;
     a.nesterov = q.nesterov != 0;
     a.grad_scale = step ? q.grad_scale : nullptr;
+    a.lr = step ? q.lr : 0.0;
     a.lr_dev = step ? q.lr_dev : nullptr;
     int smem = 0;  // what the matrix that needs most takes
     auto launch = [&]() {
@@ -1690,7 +1703,7 @@ cudaError_t run_small(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, b
             it.cols = (int)d.cols;
             it.width = small_width(d, a.ctas);
             it.rest = ws + plan.part[i];
-            rates_of(d, q, it.rate, it.decay);
+            it.rate = rates_of(d, q);
             it.g32 = d.g_dtype == RLK_FP32;
             if (Small<R>::smem(it.width / 64) > smem) smem = Small<R>::smem(it.width / 64);
         }
@@ -1734,7 +1747,8 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
         it.ld = z.ld;
         it.parts = plan.parts[i];
         it.start = start[plan.of[i]];
-        rates_of(d, q, it.rate, it.decay);
+        it.rate = rates_of(d, q);
+        it.rates = reinterpret_cast<float*>(ws + plan.part[i] + sizeof(double) * plan.parts[i]);
         it.g32 = d.g_dtype == RLK_FP32;
         items.push_back(it);
     }
@@ -1744,6 +1758,7 @@ cudaError_t run(const rlk_muon_matrix* t, int n, const rlk_muon_args& q, bool st
     a.eps = (float)q.eps;
     a.nesterov = q.nesterov != 0;
     a.grad_scale = step ? q.grad_scale : nullptr;
+    a.lr = step ? q.lr : 0.0;
     a.lr_dev = step ? q.lr_dev : nullptr;
     auto tiles = [](const Item& it) { return ((it.rows + kSide - 1) / kSide) * ((it.cols + kSide - 1) / kSide); };
     e = pass(items, a, false, [](const Item& it) { return it.parts; }, [&](int blocks, bool) {

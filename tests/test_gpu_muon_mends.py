@@ -1,10 +1,12 @@
 """Calls of Muon and of the orthogonal update that the operators' first tests do not make."""
 
+import numpy as np
 import pytest
 
 import invariant_mmdit_joint_gb300 as pkg
+from oracle import projection_ops as O
 from tests import _helpers as Hh
-from tests.test_gpu_muon import assert_orthogonal, f64, gradient
+from tests.test_gpu_muon import assert_orthogonal, f64, gradient, state
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +56,41 @@ def test_small_norms_with_any_eps(dev, rows, cols):
         if eps < 1e-7:
             assert_orthogonal(pkg.orthogonalize([u], eps=eps)[0], f64(u), (rows, cols, eps), eps=eps)
     pkg.rlk_joint_attn_check_status()
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("lr", [0.01, 2.0 ** -9, 1e-4])
+def test_device_rate_gives_the_numbers_bytes(dev, bf16, lr):
+    """One step from a rate on the device and from the same number: every byte of p, its master and m. The rates' products
+    with unlike scales and decays are no powers of two, so that another order or rounding of them shows; and both are the
+    formula's: p's error is X's, three roundings of the step, two of the decay and one of p."""
+    import torch
+    shapes = [(100, 40), (40, 96), (300, 200), (129, 1001), (700, 20), (150, 150)]
+    decay, share = [0.1, 0.3, 0.7, 0.9, 0.0, 1.1], [0.3, 1.0, 1.7, 0.9, 1.3, 0.7]
+    on_device = torch.tensor([lr], device=dev)
+    number, runs = float(on_device), []
+    for rate in (number, on_device):
+        params, masters, m, grads = state(dev, shapes, 9, bf16)
+        p0, m0 = [f64(t) for t in (masters or params)], [f64(t) for t in m]
+        opt = pkg.Muon(params, masters=masters, m=m, grads=grads, weight_decay=decay, lr_scale=share, lr=5.0, momentum=0.9)
+        opt.step(lr=rate)
+        pkg.rlk_joint_attn_check_status()
+        runs.append([*params, *(masters or ()), *m])
+        for i, (s, w) in enumerate(zip(shapes, masters or params)):
+            want, _, x = O.muon(p0[i], m0[i], f64(grads[i]), number * share[i], 0.9, True, decay[i], 0.2)
+            step, norm = number * share[i] * 0.2 * np.sqrt(max(s)), np.linalg.norm
+            tol = step * (2.0 ** -9 + 3 * 2.0 ** -24) * norm(x) + 2.0 ** -24 * (2 + 2 * number * share[i] * decay[i]) * norm(p0[i])
+            assert norm(f64(w) - want) <= tol, (i, s)
+    assert all(Hh.bits_equal(a, b) for a, b in zip(*runs))
+
+
+def test_device_rate_scales_the_decay(dev):
+    """A zero update: p -= rate decay p alone, which a decay without the rate, or twice the rate, misses."""
+    import torch
+    for shape in ((30, 70), (200, 304), (301, 150)):
+        for rate in (0.25, torch.tensor([0.25], device=dev)):
+            p = torch.randn(shape, device=dev)
+            want = p.double() * (1 - 0.25 * 0.5 * 0.125)
+            zero = torch.zeros_like(p)
+            pkg.Muon([p], lr=9.0, lr_scale=0.5, weight_decay=0.125, grads=[zero]).step(lr=rate)
+            assert bool(((p.double() - want).abs() <= 2.0 ** -23 * want.abs()).all()), shape
