@@ -665,7 +665,7 @@ rlk_status rlk_grad_norm(const rlk_adamw_tensor* tensors, int32_t n_tensors, flo
 size_t rlk_fp8_row_bytes(int64_t k);        /* 0 for k < 1 */
 size_t rlk_fp8_scale_row_bytes(int64_t k);  /* 0 for k < 1 */
 
-/* Limits: 0 <= rows < 2^31 - 128, 1 <= cols <= 2^20 a multiple of 8, x_stride
+/* Limits: 0 <= rows < 2^31 - 256, 1 <= cols <= 2^20 a multiple of 8, x_stride
  * >= cols (elements) with every row 16-byte aligned (else RLK_ERR_ALIGNMENT).
  * Written buffers must not overlap another of the call (a buffer reaches from its
  * first row's start to its last one's end). rows 0 writes nothing
@@ -685,7 +685,7 @@ typedef struct rlk_fp8_quant {
     int32_t reserved;   /* 0 */
 } rlk_fp8_quant;
 
-/* Limits: 0 <= m, n < 2^31 - 256, n a multiple of 8, 1 <= k < 2^31 - 128,
+/* Limits: 0 <= m, n < 2^31 - 256, n a multiple of 8, 1 <= k < 2^31 - 256,
  * d_stride >= n a multiple of 8 elements. m or n 0 computes nothing. d must
  * not overlap another buffer of the call (from its first row's start to its last
  * one's end: column slices of one tensor go into calls of their own). */

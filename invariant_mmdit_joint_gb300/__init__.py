@@ -1502,7 +1502,7 @@ class Fp8Projection(_Pairs):
         if grad_format not in FP8_FORMATS:
             raise ValueError(f"grad_format must be one of {sorted(FP8_FORMATS)}")
         if B < 1 or T_txt < 0 or T_img < 0 or T_txt + T_img == 0 or not all(
-                8 <= k <= 1 << 20 and k % 8 == 0 for k in (n_in, n_out)) or B * max(T_txt, T_img) >= 1 << 31:
+                8 <= k <= 1 << 20 and k % 8 == 0 for k in (n_in, n_out)) or B * max(T_txt, T_img) >= (1 << 31) - 256:
             raise RlkError(1, "Fp8Projection: invalid shape")
         self.device = _cuda_device(device)
         self._index = -1 if self.device.index is None else self.device.index

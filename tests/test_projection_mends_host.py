@@ -5,7 +5,10 @@ import math
 import os
 import re
 
-from tests.test_projection_host import P, L, args, matrices, no_gpu, step  # noqa: F401
+import pytest
+
+import invariant_mmdit_joint_gb300 as pkg
+from tests.test_projection_host import P, L, args, gemm, matrices, no_gpu, product, quant, quantize, step  # noqa: F401
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "invariant_mmdit_joint_gb300", "csrc")
@@ -41,3 +44,29 @@ def test_orthogonalize_takes_no_argument_of_a_step(L):  # noqa: F811
     taken = re.findall(r"=\s*([^;=]*\bq\.(?:lr_dev|grad_scale))\b([^;]*);", source("k_muon.cu"))
     taken = [(a, b) for a, b in taken if "!=" not in a + b]  # (the host's rate looks whether there is a pointer)
     assert len(taken) == 4 and all(a.startswith("step ? ") and b == " : nullptr" for a, b in taken), taken
+
+
+def test_the_headers_limits_are_the_librarys(L):  # noqa: F811
+    """Rows, tokens and sums of the 8-bit calls: the last size that the header allows passes, the next one is refused."""
+    with open(os.path.join(ROOT, "include", "rlk_joint_attn.h")) as f:
+        text = f.read()
+    rows = (1 << 31) - int(re.search(r"0 <= rows < 2\^31 - (\d+)", text).group(1))
+    both = (1 << 31) - int(re.search(r"0 <= m, n < 2\^31 - (\d+)", text).group(1))
+    k = (1 << 31) - int(re.search(r"1 <= k < 2\^31 - (\d+)", text).group(1))
+    assert both % 8 == 0  # (n's last multiple of 8 is 8 below)
+    far = lambda i: P + i * (1 << 44)  # noqa: E731
+    assert pkg.rlk_fp8_quant_workspace_bytes(rows - 1, 8) > 0 and pkg.rlk_fp8_quant_workspace_bytes(rows, 8) == 0
+    q = dict(x=far(0), q=far(1), q_scale=far(2), qt=far(3), qt_scale=far(4), col_sum=far(5), workspace=far(6), cols=8, x_stride=8)
+    p = dict(a=far(0), a_scale=far(1), b=far(2), b_scale=far(3), bias=far(4), d=far(5), m=8, n=8, k=128, d_stride=8)
+    assert quantize(L, quant(**q, rows=rows)) == 1
+    for over in (dict(m=both), dict(n=both, d_stride=both), dict(k=k)):
+        assert gemm(L, product(**{**p, **over})) == 1, over
+    if no_gpu():  # (what is right goes on to the device)
+        assert quantize(L, quant(**q, rows=rows - 1)) == 5
+        for over in (dict(m=both - 1), dict(n=both - 8, d_stride=both - 8), dict(k=k - 1)):
+            assert gemm(L, product(**{**p, **over})) == 5, over
+    torch = pytest.importorskip("torch")
+    make = lambda t: pkg.Fp8Projection(1, 0, t, 8, 8, device="cpu", dw_dtype=torch.float32)  # noqa: E731
+    make(rows - 1)
+    with pytest.raises(pkg.RlkError):
+        make(rows)
