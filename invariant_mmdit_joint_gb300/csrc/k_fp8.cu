@@ -171,7 +171,7 @@ __device__ __forceinline__ const QuantItem& item_of(const QuantArgs& a, int& til
 
 // Blocks along the rows alone: 8 lanes a block, each with two runs of eight columns; two rows a thread, no shared memory
 // (bound by instructions: 16 lanes with one run each and the same work beside it took 13.5 of them a value and 14.0 us
-// // for 8704 rows of 2560; 12.0 so, HBM's floor 9.9).
+// for 8704 rows of 2560; 12.0 so, HBM's floor 9.9).
 template <bool kFp32, bool kE5m2>
 __global__ void __launch_bounds__(kQuantThreads) fp8_quant_rows_kernel(const __grid_constant__ QuantArgs a) {
     constexpr int kRoom = kE5m2 ? 15 : 8, kRows = kRowsTile / 32;
