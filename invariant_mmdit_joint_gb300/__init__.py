@@ -1826,8 +1826,9 @@ class Muon:
 
     def step(self, lr=None, grad_scale=None, grads=None, stream=None):
         """One update, in place. ``lr`` is the rate if not the constructor's, a number, or a float32 device tensor of one
-        value that is read when the kernels run, as a captured step needs, and gives the bytes of the same number. ``grad_scale`` is one float32 value on the
-        device, such as AdamW.grad_norm(...)[1:]; if it is not finite, nothing is changed."""
+        value that is read when the kernels run, as a captured step needs, and gives the bytes of the same number.
+        ``grad_scale`` is one float32 value on the device, such as AdamW.grad_norm(...)[1:]; if it is not finite, nothing
+        is changed."""
         import torch
         if grads is not None:
             self._take(grads)

@@ -487,11 +487,12 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 //   a X + (b A + c A A) X = (a + b shift + c shift^2) X + ((b + 2 c shift) D + c D D) X
 // A's diagonal, which holds most of it, is the squared norms of X's rows. With about their mean taken off it, little is
 // rounded to fp16: near 1, where A's roundings were multiplied by b = -4.8 and B's were 2^-11 of 2.7, the two
-// coefficients are 0.7 (X off by 5e-4 to 9e-4 of its norm, 1.2e-3 to 2.8e-3 without). Small matrices take the mean
+// coefficients are 0.7 (X off by 4e-4 to 8e-4 of its norm, 1.0e-3 to 2.1e-3 without). Small matrices take the mean
 // itself, X's squares summed. The larger ones, where it would take a sum over many CTAs, take kSpread / r and what the
 // polynomial makes of it, 1 at most: a rule on r alone. 1 / r, the mean at the start, is too early where a few singular
-// values lead (300 x 1000 and 700 x 1500 with four of them: 0.35 8.3e-4 and 9.5e-4, 1 8.4e-4 and 1.1e-3, the mean 8.6e-4
-// and 9.2e-4).
+// values lead (300 x 1000 and 700 x 1500 with four of them: 0.35 5.1e-4 and 5.9e-4, 1 5.2e-4 and 8.3e-4, 0.2 4.7e-4 and
+// 5.1e-4, the mean the same; independent entries: 0.35 8.0e-4 and 6.6e-4, 1 and the mean 6.3e-4 and 6.1e-4, 0.2 9.4e-4
+// and 7.5e-4).
 constexpr float kSpread = 0.35f;
 struct Poly {
     float a, b, c;
@@ -769,7 +770,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) muon_ge
 // 128-byte swizzle makes a block a K-major operand of the slice's X X^T and an MN-major one of B X), the CTAs add
 // their parts of A in rank order, compute B each for itself and turn their slices to the next X in place. What
 // bounds it: the passes over g, m and p at the start and end, then the five iterations' chain of products,
-// exchanges and barriers (about 5 us each; one 16 x 1160 takes 31 us, 64 adapters of up to 64 x 2567 70).
+// exchanges and barriers (about 5 us each; one 16 x 1160 takes 34 us, 64 adapters of up to 64 x 2567 82).
 constexpr int kSmallItems = 128, kSmallThreads = 512, kMostSmallSmem = 225 * 1024;
 template <int R>
 struct Small {  // R rows of X

@@ -2,8 +2,8 @@
 (numpy), which the tests compare the kernels with.
 
 ``quantize`` rounds to codes with a power-of-two scale a block; ``orthogonal``
-runs the Newton-Schulz products, exactly or with X, A and B rounded to fp16 where
-the kernels store them."""
+runs the Newton-Schulz products, exactly or with X, A and B rounded whole to fp16;
+``orthogonal_as_kept`` has the kernels' own form and roundings."""
 
 from __future__ import annotations
 
@@ -58,7 +58,7 @@ def _half(x):
 def orthogonal(u, iterations=5, coefficients=POLYNOMIAL, eps=1e-7, stored=False, lead=1.0):
     """X of u; stored: X, A and B rounded to fp16, X at the start with a power of two near the root of its shorter side
     times ``lead`` (another one draws other roundings), for matrices of up to 128 rows B in two fp16 numbers a value.
-    The kernels' own form, A less a multiple of the identity, rounds no more than that."""
+    The kernels' own form (orthogonal_as_kept) rounds no more than that."""
     u = np.asarray(u, np.float64)
     if u.shape[0] > u.shape[1]:
         return orthogonal(u.T, iterations, coefficients, eps, stored, lead).T

@@ -4,13 +4,13 @@ others hold less than that or nothing.
 
 X is read without a rounding of its own: a Muon step with momentum 0, update_rms 1 and rate 1 on weights of 0 leaves
 -sqrt(max(rows, columns)) X in fp32, off by 2^-23 at most. Where the figures come from: the kernels keep X in fp16, the
-first three with codes of what that leaves, five bits more. A rounding to fp16 is off by 2^-11 / sqrt(12) of a power of two above the value in the
-mean square, 1.4e-4 to 2e-4 of X's norm in all directions alike, and two iterations on from the first X without more
-bits a small singular value has grown 3.4445^2 = 11.9 times: 2.4e-3 of the norm for what is lost in
-the small directions; where these hold a hundredth of the norm and more, they stop growing before the end, since their
-values come near 1: half of it. A and B add 3e-4 to 8e-4 (less than 2^-10, as the tests of independent entries hold),
-and the third X's rest, which B X does not take, is off by no more than b s of 4.775 / 3.4445 where s is A's mean: twice
-that rounding once more for a few rows. 2^-7 = 7.8e-3 holds all of it."""
+first three with codes of what that leaves, about five bits more. A rounding to fp16 is off by 2^-11 / sqrt(12) of a
+power of two above the value in the mean square, 1.4e-4 to 2e-4 of X's norm in all directions alike, and two iterations
+on from the first X without more bits a small singular value has grown 3.4445^2 = 11.9 times: 2.4e-3 of the norm for
+what is lost in the small directions; where these hold a hundredth of the norm and more, they stop growing before the
+end, since their values come near 1: half of it. A and B add 3e-4 to 8e-4 (less than 2^-10, as the tests of independent
+entries hold), and the third X's rest, which B X does not take, is off by no more than b s of 4.775 / 3.4445 where s is
+A's mean: twice that rounding once more for a few rows. 2^-7 = 7.8e-3 holds all of it."""
 
 import numpy as np
 import pytest
@@ -59,8 +59,8 @@ def update_of(x):
 
 
 # one kernel's (one CTA, a few, eight; 64 and 128 rows; odd and aligned rows, tall and wide), and the large ones
-SIZES = [(16, 1160), (1160, 16), (64, 700), (701, 63), (64, 2567), (32, 33), (128, 1000), (1000, 127), (100, 4001), (130, 300),
-         (300, 1000), (1000, 300), (301, 999), (999, 301), (512, 512), (768, 1536)]
+SIZES = [(16, 1160), (1160, 16), (64, 700), (701, 63), (64, 2567), (64, 4000), (4001, 50), (33, 9000), (32, 33), (128, 1000),
+         (1000, 127), (100, 4001), (130, 300), (300, 1000), (1000, 300), (301, 999), (999, 301), (512, 512), (768, 1536)]
 KINDS = [(0, 0), (4, 1), (4, 10), (4, 30), (1, 100), "1/i"]
 
 

@@ -94,3 +94,47 @@ def test_device_rate_scales_the_decay(dev):
             zero = torch.zeros_like(p)
             pkg.Muon([p], lr=9.0, lr_scale=0.5, weight_decay=0.125, grads=[zero]).step(lr=rate)
             assert bool(((p.double() - want).abs() <= 2.0 ** -23 * want.abs()).all()), shape
+
+
+def test_codes_in_the_workspace(dev):
+    """Sizes whose codes of X's rounding lie in the workspace beside ones whose do not: steps on two streams at once, a
+    captured step and a list turned over give the bytes of steps one by one, whatever the workspace held; a factor that is
+    not finite changes nothing."""
+    import torch
+    shapes = [(64, 4000), (4001, 50), (100, 4001), (33, 9000), (64, 2567), (300, 130), (128, 2600), (20, 30)]
+
+    def make(seed, order=1):
+        params, masters, m, grads = state(dev, shapes, seed)
+        opt = pkg.Muon(params[::order], masters=masters[::order], m=m[::order], grads=grads[::order], lr=0.02)
+        return opt, [*params, *masters, *m]
+    want = []
+    for seed in (1, 2):
+        opt, tensors = make(seed)
+        for _ in range(2):
+            opt.step()
+        want.append([t.clone() for t in tensors])
+    both, streams = [make(1), make(2)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(2):
+        for (opt, _), s in zip(both, streams):
+            opt.step(stream=s)
+    torch.cuda.synchronize()
+    for (_, tensors), w in zip(both, want):
+        assert all(Hh.bits_equal(a, b) for a, b in zip(tensors, w))
+    for order in (1, -1):
+        opt, tensors = make(1, order)
+        first = [t.clone() for t in tensors]
+        opt.step()
+        opt.workspace.fill_(0xff)  # (NaN codes)
+        for t, k in zip(tensors, first):
+            t.copy_(k)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            opt.step()
+        for _ in range(2):
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(Hh.bits_equal(a, b) for a, b in zip(tensors, want[0]))
+        opt.step(grad_scale=torch.tensor([float("nan")], device=dev))
+        assert all(Hh.bits_equal(a, b) for a, b in zip(tensors, want[0]))
+    pkg.rlk_joint_attn_check_status()
