@@ -729,9 +729,10 @@ rlk_status rlk_fp8_gemm(const rlk_fp8_product* items, int32_t n_items, void* str
  * X, A less a multiple of the identity, and the polynomial's part that goes with
  * it are held in fp16, the first three X's with codes of what that leaves, with
  * fp32 accumulators. With the polynomial (3.4445, -4.775, 2.0315) and five
- * iterations X is within 2^-9 of the formula's in the norm, also where a few
- * directions lead the others by 100 times (independent entries: about half of
- * that), within 2^-7 where the others hold less than that or nothing. The norm's
+ * iterations X is within 2^-9 of the formula's in the norm for dense matrices of
+ * 16 rows and columns or more, also where a few directions lead the others by 100
+ * times (independent entries: about half of that), and within 2^-6 for any other
+ * (directions that lead by more or alone, fewer rows, a few entries). The norm's
  * squares are fp32, their sum fp64: a norm below 2^-56 counts as 2^-56, one above
  * 2^63 is infinite and gives X = 0. m and p are fp32. Sums have a fixed order
  * without atomics: a matrix's result does not depend on the list or its place in
