@@ -251,8 +251,11 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 // by 5e-3 of its norm with four leading by 10 times, 2e-2 with one by 100, 9e-2 with three alone, and it is the roundings
 // of the first X's that grow. B X and A do not pass them on (B is 0 but for directions that have grown), a X does. So
 // a X alone takes the rests: with a in the first two iterations, from the third on, where most values have grown, with
-// the coefficient that X itself has beside B (Poly). Three rests leave 4e-4 to 1.4e-3 of X up to 100 times (two 2e-3,
-// four no less), 3e-3 to 7e-3 beyond; few rows or entries, whose roundings do not average out, up to 9e-3.
+// the coefficient that X itself has beside B (Poly). What a direction of eigenvalue t of A needs is a + b t + c t^2: with
+// few rows much alike a is too much, so small matrices take t as a quarter of the mean (4 to 15 rows: 6.6e-4 of X for
+// independent entries where a leaves 8e-4 to 1e-3 and no rests 5.8e-4; four leading by 30 times 1.3e-3, 1.1e-3, 9e-3), none of it
+// for 2 and 3 rows (where one leads by 10^4 a quarter leaves 2e-2), all of it for one, whose eigenvalue it is. Three rests leave 4e-4 to 1.4e-3 of X up to 100 times (two 2e-3,
+// four no less), 3e-3 to 7e-3 beyond; few rows or entries, whose roundings do not average out, up to 1.3e-2.
 constexpr int kRests = 3;
 // X's entries are 1 at most (times its power of two at the start): rests of 2^-12 and less, 448 and less times this, and
 // those of entries of 2^-14 and more keep their bits.
@@ -1255,6 +1258,7 @@ __global__ void __launch_bounds__(kSmallThreads, R == 64 ? 2 : 1) muon_small_ker
     // X's squares, a thread's part each, lie where nothing is read or written from an iteration's end to its next barrier
     float* const squares = reinterpret_cast<float*>(generic + ((ctas == 1 ? sb : sa) - sbase));
     const Poly poly{a.a, a.b, a.c};
+    const float rest_share = r == 1 ? 1.0f : r < 4 ? 0.0f : 0.25f;
     float shift = 1.0f / (float)r;  // the mean of A's diagonal: X's sum of squares (1 at first) a row
     for (int n = 0; n < a.iterations; ++n) {
         if (warp == 0) {  // the slice's part of X X^T
@@ -1389,8 +1393,7 @@ __global__ void __launch_bounds__(kSmallThreads, R == 64 ? 2 : 1) muon_small_ker
         const float of_x = poly.of_x(shift) * scale;
         // a warp's columns of a tile: a quarter of it; where the lanes from 64 on hold the same rows again, half of that
         const int i = R == 64 ? row & 63 : row, own0 = R == 64 ? group * 32 + (quarter >> 1) * 16 : group * 64;
-        // (one row: the shift is the square of its only singular value, and X's coefficient is the right one)
-        const float of_rest = (n + 1 < kRests && r > 1 ? a.a * scale : of_x) / (n == 0 ? kRestScaleStart : kRestScale);
+        const float of_rest = (n + 1 < kRests ? poly.of_x(shift * rest_share) * scale : of_x) / (n == 0 ? kRestScaleStart : kRestScale);
         const uint64_t of_x2 = f2_pack(of_x, of_x), scale2 = f2_pack(scale, scale), of_rest2 = f2_pack(of_rest, of_rest);
         __half2 square = __float2half2_rn(0.0f);
         auto turn = [&](auto reads, auto writes) {  // (a form each: a branch within the loop costs every iteration)

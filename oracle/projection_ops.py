@@ -96,8 +96,8 @@ def kept(x, scale):
 def orthogonal_as_kept(u, iterations=5, coefficients=POLYNOMIAL, eps=1e-7, rests=3, lead=1.0, alone=None):
     """X of u with the kernels' own roundings and exact sums. A = D + s I is kept as D, so that X = of_x X + B X with
     of_x = a + b s + c s^2 and B = (b + 2 c s) D + c D D; X, D and B are fp16, the first ``rests`` X's with codes of
-    their rests, which enter X alone: with a, the last of them (one row: all)
-    with of_x. s is the mean of A's diagonal (1 / r at first) for the
+    their rests, which enter X alone: with a (``alone``: a + b t + c t^2, t a
+    quarter of s; 2 or 3 rows none, one row all of it), the last of them with of_x. s is the mean of A's diagonal (1 / r at first) for the
     matrices that one kernel takes (``alone``), else what the polynomial makes of 0.35 / r, 1 at most. ``lead``: another
     factor at the start draws other roundings."""
     u = np.asarray(u, np.float64)
@@ -116,6 +116,8 @@ def orthogonal_as_kept(u, iterations=5, coefficients=POLYNOMIAL, eps=1e-7, rests
         of_x = a + b * s + c * s * s
         d = _half(x @ x.T * scale ** 2 - s * np.eye(r))
         poly = _half((b + 2 * c * s) * d + c * (d @ d))
-        x, low = kept(scale * (of_x * x + (a if n + 1 < rests and r > 1 else of_x) * low + poly @ x), 2.0 ** 20 if n + 1 < rests else 0)
+        t = s * (1.0 if r == 1 else 0.0 if r < 4 else 0.25) if alone else 0.0
+        of_rest = a + b * t + c * t * t if n + 1 < rests else of_x
+        x, low = kept(scale * (of_x * x + of_rest * low + poly @ x), 2.0 ** 20 if n + 1 < rests else 0)
         scale = 1.0
     return x

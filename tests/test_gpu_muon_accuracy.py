@@ -9,8 +9,8 @@ power of two above the value in the mean square, 1.4e-4 to 2e-4 of X's norm in a
 on from the first X without more bits a small singular value has grown 3.4445^2 = 11.9 times: 2.4e-3 of the norm for
 what is lost in the small directions; where these hold a hundredth of the norm and more, they stop growing before the
 end, since their values come near 1: half of it. A and B add 3e-4 to 8e-4 (less than 2^-10, as the tests of independent
-entries hold), and the third X's rest, which B X does not take, is off by no more than b s of 4.775 / 3.4445 where s is
-A's mean: twice that rounding once more for a few rows. 2^-7 = 7.8e-3 holds all of it
+entries hold), and the rests, which B X does not take, are taken with a coefficient that is off by no more than b s of 4.775 / 3.4445
+where s is A's mean: twice that rounding once more for a few rows. 2^-7 = 7.8e-3 holds all of it
 where there are enough entries for the roundings' mean square; a few of them may all be half a place off, 2^-11 for
 2^-11 / sqrt(12) of a power of two: 2^-6."""
 
